@@ -118,6 +118,7 @@ def lib() -> ctypes.CDLL:
             L.mxg_query_status.restype = i
             L.mxg_status_string.argtypes = [i]
             L.mxg_status_string.restype = ctypes.c_char_p
+            attention.bind(L)
             _lib = L
     return _lib
 
@@ -446,3 +447,9 @@ def mxg_mma_peak(kind: int, n: int = 256, iters: int = 20000, stream=None) -> fl
 def mxg_query_status(dev_status: torch.Tensor | None, stream=None) -> int:
     """Synchronise the stream, read and clear the device status word."""
     return int(lib().mxg_query_status(_ptr(dev_status), _stream(stream)))
+
+
+# ---------------------------------------------------------------- attention
+from . import attention  # noqa: E402  (it uses the helpers above)
+from .attention import (KVCache, attn_prompt, attn_tree, kv_append,  # noqa: E402,F401
+                        mxg_attn_tree_workspace_bytes, qk_norm_rope)
