@@ -1,100 +1,992 @@
-// attn.cu -- attention of packed prompts and of drafted token trees.
+// attn.cu -- attention of packed prompts (attn_prompt) and of drafted token
+// trees over a paged cache (attn_tree) on tcgen05 tensor cores.
+//
+// What is computed, per query row (a token or node and one of its heads):
+//   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q.k_j - m)
+// over the keys j the row sees, in one pass over the keys with a running
+// reference m (a running maximum, moved only when it falls behind by more
+// than 2^8: the weights then stay below 2^8, and fp32 sums and bf16 weights
+// lose nothing by it).
+//
+// Tiles.  The G = Hq / Hkv query heads that share a kv head are rows of one
+// tile: 128 / G tokens x G heads (so a decode step fills rows with heads, and
+// k and v are read once for all of them), against 128 keys.  Two row tiles,
+// or for a single row tile two alternating key tiles, are in flight as two
+// streams, so that the tensor core multiplies for one while the other takes
+// its exponentials.
+//
+// Warps of a CTA: 0-3 and 4-7 the softmax of stream 0 and 1 (a thread is a
+// row: its 128 scores come from TMEM into registers), 8 issues the MMAs, 9
+// loads by TMA, 10 guards the v tiles that not every row sees in full.
+// TMEM: scores of a stream 128 columns, the bf16 weights over the first 64 of
+// them once they are read, accumulators D columns a stream.
+// Hand-offs are mbarriers; every wait is bounded.
 #include <cstdint>
+#include <cstring>
+#include <mutex>
+#include <cudaTypedefs.h>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "attn.h"
+#include "attn_ptx.cuh"
 #include "kernels.h"
-#include "ptx.cuh"
 
 namespace mxg {
 namespace {
 
-constexpr int kBadIndex = 0x2;  // MXG_DEV_BAD_INDEX
+constexpr int kBadIndex = 0x2;    // MXG_DEV_BAD_INDEX
+constexpr int kSmemLayout = 0x4;  // MXG_DEV_SMEM_LAYOUT
+constexpr int kThreads = 384;
+constexpr int kKeys = 128;  // keys of a tile
+constexpr int kRowsT = 128; // rows of a tile
+constexpr int kHead = 3072; // shared memory before the tiles
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kFallBehind = 8.0f;  // log2 of how far the reference may lag the maximum
 
-// One warp per (token, query head): the plainest right form.  The lanes hold
-// D / 32 channels each; a key costs one warp sum.
-template <int D, bool TREE>
-__global__ void __launch_bounds__(128) attn_rows_kernel(const AttnParams p) {
-  constexpr int E = D / 32;
-  pdl_trigger();
-  pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (row >= (long long)p.T * p.Hq) return;
-  const int t = (int)(row / p.Hq), h = (int)(row % p.Hq), hk = h / (p.Hq / p.Hkv);
-  int b = -1, a0 = 0, a1 = 0;  // the sequence whose clamped range holds t
-  for (int s = 0, prev = 0; s < p.B && b < 0; ++s) {
-    const int x0 = max(min(max(p.cu[s], 0), p.T), prev), x1 = max(min(max(p.cu[s + 1], 0), p.T), x0);
-    if (t >= x0 && t < x1) b = s, a0 = x0, a1 = x1;
-    prev = x0;
-  }
-  if (b < 0) return;
-  float q[E], o[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = __uint_as_float((uint32_t)p.q.ptr[t * p.q.tok + h * p.q.head + lane * E + e] << 16) * p.scale;
-    o[e] = 0.0f;
-  }
-  float m = -INFINITY, l = 0.0f;
-  auto key = [&](const uint16_t *k, const uint16_t *v) {
-    float s = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(q[e], k ? __uint_as_float((uint32_t)k[lane * E + e] << 16) : 0.0f, s);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, x);
-    const float mn = fmaxf(m, s);
-    const float f = m == mn ? 1.0f : __expf(m - mn), w = __expf(s - mn);
-    l = l * f + w;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * f + w * (v ? __uint_as_float((uint32_t)v[lane * E + e] << 16) : 0.0f);
-    m = mn;
-  };
-  bool any = true;
-  if (!TREE) {
-    for (int j = a0; j <= t; ++j) key(p.k.ptr + j * p.k.tok + hk * p.k.head, p.v.ptr + j * p.v.tok + hk * p.v.head);
-  } else {
-    if (t - a0 >= kAttnMaxNodes) {
-      if (p.status && lane == 0) atomicOr(p.status, kBadIndex);
-      return;
-    }
-    const long long room = (long long)p.table_cols * p.cache.page_size;
-    int ctx = p.ctx[b];
-    if ((ctx < 0 || ctx > room) && p.status && lane == 0) atomicOr(p.status, kBadIndex);
-    ctx = (int)min((long long)max(ctx, 0), room);
-    for (int j = 0; j < ctx; ++j) {
-      const int pg = p.table[(long long)b * p.ld_table + j / p.cache.page_size];
-      const bool ok = pg >= 0 && pg < p.cache.pages;
-      if (!ok && p.status && lane == 0) atomicOr(p.status, kBadIndex);
-      const long long at = pg * p.cache.page + (j % p.cache.page_size) * p.cache.slot + hk * p.cache.head;
-      key(ok ? p.cache.k + at : nullptr, ok ? p.cache.v + at : nullptr);
-    }
-    const int n = min(a1 - a0, kAttnMaxNodes);
-    const unsigned long long word = p.mask[t] & (n >= 64 ? ~0ull : (1ull << n) - 1ull);
-    for (int j = 0; j < n; ++j)
-      if (word >> j & 1ull)
-        key(p.k.ptr + (a0 + j) * p.k.tok + hk * p.k.head, p.v.ptr + (a0 + j) * p.v.tok + hk * p.v.head);
-    any = ctx > 0 || word != 0ull;
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e)
-    p.out.ptr[t * p.out.tok + h * p.out.head + lane * E + e] =
-        (uint16_t)(pack_bf16x2(any ? o[e] / l : 0.0f, 0.0f) & 0xFFFFu);
-}
+template <int D>
+struct Cfg {
+  static constexpr int kHalves = D / 64;  // 128-byte columns of a row
+  static constexpr int kTile = kKeys * D * 2;
+  static constexpr int kSlots = D == 128 ? 5 : 8;
+  static constexpr int kSmem = kHead + (2 + kSlots) * kTile;
+  static constexpr long long kSlotFloats = 2LL * kRowsT * (D + 2);  // a CTA's partial result of an item
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+
+// ------------------------------------------------------------ work of a call
+// Sequences in order; of each its kv heads, its row groups (pairs of row
+// tiles), and -- tree -- its key tiles, all units numbered through.  The
+// coarse prefix holds the number of units before every block of sequences and
+// the offset the block's first sequence may not start below.
+constexpr int kBlocks = 64;
+constexpr int kBlocksLane = kBlocks / 32;
+struct Prefix {
+  long long units[kBlocks + 1];
+  int start[kBlocks];
+};
+
+struct Seq {
+  int a0, n;       // first token (node), tokens (nodes)
+  int ctx, nct;    // tree: cached tokens and their tiles
+  int tq, groups;  // tokens of a row tile, row groups
+  long long units;
+};
 
 template <bool TREE>
-cudaError_t launch_rows(const AttnParams &p, cudaStream_t stream) {
-  const long long rows = (long long)p.T * p.Hq;
-  cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, stream);
+__device__ __forceinline__ Seq seq_of(const AttnParams &p, int b, int &running, bool *bad) {
+  Seq s;
+  const int c0 = p.cu[b], c1 = p.cu[b + 1];
+  s.a0 = max(min(max(c0, 0), p.T), running);
+  const int a1 = max(min(max(c1, 0), p.T), s.a0);
+  if (bad && (c0 != s.a0 || c1 != a1)) *bad = true;
+  running = s.a0;
+  s.n = a1 - s.a0;
+  s.tq = kRowsT / (p.Hq / p.Hkv);
+  if (TREE) {
+    if (s.n > kAttnMaxNodes) {
+      s.n = kAttnMaxNodes;
+      if (bad) *bad = true;
+    }
+    const long long room = (long long)p.table_cols * p.cache.page_size;
+    const int c = p.ctx[b];
+    s.ctx = (int)min((long long)max(c, 0), room);
+    if (bad && c != s.ctx) *bad = true;
+    s.nct = (s.ctx + kKeys - 1) / kKeys;
+  } else {
+    s.ctx = s.nct = 0;
+  }
+  s.groups = (s.n + 2 * s.tq - 1) / (2 * s.tq);
+  s.units = (long long)s.groups * p.Hkv * (TREE ? s.nct + 1 : 1);
+  return s;
+}
+
+// One warp fills the prefix.
+template <bool TREE>
+__device__ __forceinline__ void fill_prefix(const AttnParams &p, Prefix &pre, int lane, bool report) {
+  constexpr unsigned kFull = 0xFFFFFFFFu;
+  const int per = (p.B + kBlocks - 1) / kBlocks;
+  const int own = kBlocksLane * per, b0 = min(lane * own, p.B), b1 = min(b0 + own, p.B);
+  int top = 0;  // largest clamped offset of this lane's sequences, then of those before
+  for (int b = b0; b < b1; ++b) top = max(top, min(max(p.cu[b], 0), p.T));
+  int incl = top;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl = max(incl, x);
+  }
+  int running = __shfl_up_sync(kFull, incl, 1);
+  if (lane == 0) running = 0;
+  bool bad = false;
+  long long mine = 0, part[kBlocksLane];
+#pragma unroll
+  for (int k = 0; k < kBlocksLane; ++k) {
+    const int s0 = min(b0 + k * per, p.B), s1 = min(s0 + per, p.B);
+    pre.start[lane * kBlocksLane + k] = running;
+    part[k] = mine;
+    for (int b = s0; b < s1; ++b) mine += seq_of<TREE>(p, b, running, &bad).units;
+  }
+  long long sum = mine;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(kFull, sum, o);
+    if (lane >= o) sum += x;
+  }
+#pragma unroll
+  for (int k = 0; k < kBlocksLane; ++k) pre.units[lane * kBlocksLane + k] = sum - mine + part[k];
+  if (lane == 31) pre.units[kBlocks] = sum;
+  if (bad && report && p.status) atomicOr(p.status, kBadIndex);
+}
+
+// The sequence that unit u is of, and u's number in it.
+template <bool TREE>
+__device__ __forceinline__ Seq find_seq(const AttnParams &p, const Prefix &pre, long long &u, int &b) {
+  int lo = 0, hi = kBlocks - 1;
+  while (lo < hi) {  // the last block that starts at or before u
+    const int mid = (lo + hi + 1) >> 1;
+    if (pre.units[mid] <= u) lo = mid;
+    else hi = mid - 1;
+  }
+  u -= pre.units[lo];
+  const int per = (p.B + kBlocks - 1) / kBlocks;
+  int running = pre.start[lo];
+  b = lo * per;
+  Seq s = seq_of<TREE>(p, b, running, nullptr);
+  while (u >= s.units && b + 1 < p.B) {
+    u -= s.units;
+    s = seq_of<TREE>(p, ++b, running, nullptr);
+  }
+  return s;
+}
+
+struct Item {
+  int b, hk;
+  int a0, n;     // the sequence's first token (node) and count
+  int r0;        // first token (node) of the first row tile, in the sequence
+  int cnt[2];    // tokens (nodes) of the two row tiles
+  int t0, t1;    // key tiles [t0, t1)
+  int end[2];    // dual: a stream's tiles are [t0, end)
+  int ctx, nct;
+  bool split;    // one row tile: the streams take alternate key tiles
+  int part;      // -1 = the whole item, else the CTA's partial slot (0: the item began before, 1: it goes on)
+};
+
+// Walks the items of one CTA.  Prompt: row groups from the last (its keys are
+// the most) to the first, strided over the grid.  Tree: the units are cut into
+// equal ranges over the grid, an item is the part of one row group's key tiles
+// that lies in this CTA's range.
+template <bool TREE>
+struct Walk {
+  long long cur, end;
+  __device__ __forceinline__ Walk(const Prefix &pre) {
+    const long long U = pre.units[kBlocks];
+    if (TREE) {
+      cur = U * blockIdx.x / gridDim.x;
+      end = U * (blockIdx.x + 1) / gridDim.x;
+    } else {
+      cur = blockIdx.x;
+      end = U;
+    }
+  }
+  __device__ __forceinline__ bool next(const AttnParams &p, const Prefix &pre, Item &it) {
+    if (cur >= end) return false;
+    long long u = TREE ? cur : end - 1 - cur;
+    const Seq s = find_seq<TREE>(p, pre, u, it.b);
+    it.a0 = s.a0;
+    it.n = s.n;
+    it.ctx = s.ctx;
+    it.nct = s.nct;
+    int g, last;
+    if (TREE) {
+      const int per = s.nct + 1;
+      const int gh = (int)(u / per);
+      it.t0 = (int)(u - (long long)gh * per);
+      it.hk = gh % p.Hkv;
+      g = gh / p.Hkv;
+      it.t1 = (int)min((long long)per, it.t0 + (end - cur));
+      cur += it.t1 - it.t0;
+      it.part = it.t0 > 0 ? 0 : it.t1 < per ? 1 : -1;
+      last = it.t1;
+    } else {
+      it.hk = (int)(u % p.Hkv);
+      g = (int)(u / p.Hkv);
+      it.t0 = 0;
+      it.part = -1;
+      cur += gridDim.x;
+      last = 0;
+    }
+    it.r0 = g * 2 * s.tq;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      it.cnt[k] = min(max(s.n - it.r0 - k * s.tq, 0), s.tq);
+      it.end[k] = it.cnt[k] == 0 ? it.t0 : TREE ? last : (it.r0 + k * s.tq + it.cnt[k] + kKeys - 1) / kKeys;
+    }
+    it.split = TREE && s.n <= s.tq;
+    if (!TREE) it.t1 = max(it.end[0], it.end[1]);
+    return true;
+  }
+};
+
+// V rows of key tile j that some row of the item sees, and the first of them
+// that not every row does.
+template <bool TREE>
+__device__ __forceinline__ int v_valid(const Item &it, int j) {
+  if (TREE) return j < it.nct ? min(kKeys, it.ctx - j * kKeys) : it.n;
+  return min(kKeys, it.r0 + it.cnt[0] + it.cnt[1] - j * kKeys);
+}
+template <bool TREE>
+__device__ __forceinline__ int v_shared(const Item &it, int j) {
+  if (TREE) return j < it.nct ? kKeys : 0;
+  return min(max(it.r0 + 1 - j * kKeys, 0), kKeys);
+}
+template <bool TREE>
+__device__ __forceinline__ bool guarded(const Item &it, int j) {
+  return min(v_valid<TREE>(it, j), v_shared<TREE>(it, j)) < kKeys;
+}
+// The first guarded tile at or after t0 (they are the item's last ones).
+template <bool TREE>
+__device__ __forceinline__ int first_guarded(const Item &it) {
+  const int j = TREE ? it.ctx / kKeys : (it.r0 + 1) / kKeys;
+  return max(j, it.t0);
+}
+
+template <int D>
+struct Smem {
+  using C = Cfg<D>;
+  // (8-byte barriers first)
+  uint64_t q_full[2], q_empty[2], kv_full[C::kSlots], kv_empty[C::kSlots];
+  uint64_t v_issued[C::kSlots], kv_clean[C::kSlots];  // the guard's
+  uint64_t s_full[2], p_ready[2], pv_done[2], o_free[2];
+  uint64_t guard_item[2], item_done[2], x_ready, x_free, mma_done, stall;
+  uint32_t tmem;
+  int abort_flag;
+  uint32_t poison[2][3][4];  // rows of the guarded tiles that hold a NaN or an infinity, by item parity
+  float xm[kRowsT], xl[kRowsT];
+  Prefix pre;
+};
+
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const WaitCtl &ctl) {
+  const bool ok = mbar_wait(smem_addr(bar), parity, ctl);
+  return __all_sync(0xFFFFFFFFu, ok);
+}
+// Bounded wait that ignores the abort flag: lets what is in flight land.
+__device__ __forceinline__ void drain(uint64_t *bar, uint32_t parity, uint64_t timeout_ns) {
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(smem_addr(bar), parity))
+    if (global_timer_ns() - t0 > timeout_ns) return;
+}
+__device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(smem_addr(bar));
+}
+
+__device__ __forceinline__ bool not_finite2(uint32_t w) {
+  return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+}
+
+template <int D, bool TREE>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKC,
+                const __grid_constant__ CUtensorMap tmVC, const AttnParams p) {
+  using C = Cfg<D>;
+  constexpr int S = C::kSlots;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  static_assert(sizeof(Smem<D>) <= kHead, "shared memory head");
+  Smem<D> &sm = *reinterpret_cast<Smem<D> *>(smem_raw);
+  const uint32_t base = smem_addr(smem_raw);
+  if (base & 1023u) {  // the swizzled tiles need it (uniform over the grid)
+    if (threadIdx.x == 0 && p.status) atomicOr(p.status, kSmemLayout);
+    return;
+  }
+  const uint32_t q_smem = base + kHead, kv_smem = q_smem + 2 * C::kTile;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = p.Hq / p.Hkv, TQ = kRowsT / G;
+  pdl_trigger();
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&sm.q_full[i]), 1);
+      mbar_init(smem_addr(&sm.q_empty[i]), 4);
+      mbar_init(smem_addr(&sm.s_full[i]), 1);
+      mbar_init(smem_addr(&sm.p_ready[i]), 4);
+      mbar_init(smem_addr(&sm.pv_done[i]), 1);
+      mbar_init(smem_addr(&sm.o_free[i]), 4);
+      mbar_init(smem_addr(&sm.guard_item[i]), 1);
+      mbar_init(smem_addr(&sm.item_done[i]), 8);
+    }
+    for (int i = 0; i < S; ++i) {
+      mbar_init(smem_addr(&sm.kv_full[i]), 1);
+      mbar_init(smem_addr(&sm.kv_empty[i]), 1);
+      mbar_init(smem_addr(&sm.v_issued[i]), 1);
+      mbar_init(smem_addr(&sm.kv_clean[i]), 1);
+    }
+    mbar_init(smem_addr(&sm.x_ready), 4);
+    mbar_init(smem_addr(&sm.x_free), 4);
+    mbar_init(smem_addr(&sm.mma_done), 1);
+    mbar_init(smem_addr(&sm.stall), 1);
+    sm.abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(smem_addr(&sm.tmem), 512);
+    tmem_relinquish();
+  }
+  if (warp == 9 && lane == 0) {
+    prefetch_tmap(&tmQ);
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
+    if (TREE) {
+      prefetch_tmap(&tmKC);
+      prefetch_tmap(&tmVC);
+    }
+  }
+  pdl_wait();
+  if (warp == 0) fill_prefix<TREE>(p, sm.pre, lane, blockIdx.x == 0);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&sm.tmem);
+  const WaitCtl ctl{&sm.abort_flag, p.status, p.timeout_ns};
+  Walk<TREE> walk(sm.pre);
+  Item it;
+
+  if (warp == 9) {
+    // ------------------------------------------------------------- loads
+    uint32_t n = 0, nq[2] = {0, 0}, ql[2] = {0, 0};
+    bool ok = true;
+    auto load_kv = [&](const Item &i, int j, bool is_v) {
+      const uint32_t slot = n % S;
+      if (n >= S && !warp_wait(&sm.kv_empty[slot], (n / S - 1) & 1, ctl)) return false;
+      const uint32_t bar = smem_addr(&sm.kv_full[slot]), dst = kv_smem + slot * C::kTile;
+      if (TREE && j < i.nct) {
+        // pages of up to 128 keys, one lane a page; those past the context stay out
+        const int box = min(p.cache.page_size, kKeys);
+        const int first = j * kKeys, boxes = (min(kKeys, i.ctx - first) + box - 1) / box;
+        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box * 128 * C::kHalves));
+        __syncwarp();
+        if (lane < boxes) {
+          const int key = first + lane * box, col = key / p.cache.page_size;
+          int pg = p.table[(long long)i.b * p.ld_table + col];
+          if (pg < 0 || pg >= p.cache.pages) {
+            pg = p.cache.pages;  // out of the map's bounds: zeros
+            if (p.status) atomicOr(p.status, kBadIndex);
+          }
+          const CUtensorMap *tm = is_v ? &tmVC : &tmKC;
+#pragma unroll
+          for (int h = 0; h < C::kHalves; ++h)
+            tma_load_4d(dst + h * 16384 + lane * box * 128, tm, h * 64, i.hk, key - col * p.cache.page_size, pg, bar);
+        }
+        __syncwarp();
+      } else if (lane == 0) {
+        // keys of the packed tensors: a prompt's tile, or the nodes (64 rows)
+        const int rows = TREE ? kAttnMaxNodes : kKeys;
+        mbar_arrive_expect_tx(bar, (uint32_t)(rows * 128 * C::kHalves));
+        const CUtensorMap *tm = is_v ? &tmV : &tmK;
+#pragma unroll
+        for (int h = 0; h < C::kHalves; ++h)
+          tma_load_3d(dst + h * 16384, tm, h * 64, i.hk, i.a0 + (TREE ? 0 : j * kKeys), bar);
+      }
+      if (is_v && guarded<TREE>(i, j)) warp_arrive(&sm.v_issued[slot], lane);
+      ++n;
+      return true;
+    };
+    while (ok && walk.next(p, sm.pre, it)) {
+      ok = load_kv(it, it.t0, false);
+      for (int s = 0; ok && s < 2; ++s) {
+        const bool load = it.split ? s == 0 : it.end[s] > it.t0;
+        if (!load && !it.split) continue;
+        if (nq[s] > 0) ok = warp_wait(&sm.q_empty[s], (nq[s] - 1) & 1, ctl);
+        ++nq[s];  // (a split item's second tile is the streams' exchange space)
+        if (ok && load) ++ql[s];
+        if (ok && load && lane == 0) {
+          const uint32_t bar = smem_addr(&sm.q_full[s]);
+          mbar_arrive_expect_tx(bar, (uint32_t)(TQ * G * 128 * C::kHalves));
+#pragma unroll
+          for (int h = 0; h < C::kHalves; ++h)
+            tma_load_3d(q_smem + s * C::kTile + h * 16384, &tmQ, h * 64, it.hk * G, it.a0 + it.r0 + s * TQ, bar);
+        }
+      }
+      const int lead = it.split ? 2 : 1;
+      if (ok && lead == 2 && it.t0 + 1 < it.t1) ok = load_kv(it, it.t0 + 1, false);
+      for (int j = it.t0; ok && j < it.t1; ++j) {
+        ok = load_kv(it, j, true);
+        if (ok && j + lead < it.t1) ok = load_kv(it, j + lead, false);
+      }
+    }
+    // nothing may land in shared memory once the CTA is gone (a timeout)
+    for (uint32_t k = n > S ? n - S : 0; k < n; ++k) drain(&sm.kv_full[k % S], (k / S) & 1, p.timeout_ns);
+    for (int s = 0; s < 2; ++s)
+      if (ql[s] > 0) drain(&sm.q_full[s], (ql[s] - 1) & 1, p.timeout_ns);
+  } else if (warp == 8) {
+    // --------------------------------------------------------------- MMAs
+    uint32_t rn = 0, qn[2] = {0, 0}, pn[2] = {0, 0}, on[2] = {0, 0}, clean = 0;
+    constexpr uint32_t kIdQK = idesc_bf16(128, kKeys, false), kIdPV = idesc_bf16(128, D, true);
+    const uint32_t s_t[2] = {tmem, tmem + 128}, o_t[2] = {tmem + 256, tmem + 384};
+    auto ring = [&](uint32_t k) { return warp_wait(&sm.kv_full[k % S], (k / S) & 1, ctl); };
+    auto ring_v = [&](uint32_t k, const Item &i, int j) {
+      if (!ring(k)) return false;
+      if (guarded<TREE>(i, j)) {
+        const uint32_t slot = k % S;
+        if (!warp_wait(&sm.kv_clean[slot], (clean >> slot) & 1, ctl)) return false;
+        clean ^= 1u << slot;
+      }
+      return true;
+    };
+    auto qk = [&](int s, int qs, uint32_t k) {  // scores of stream s = Q tile qs . K^T
+      tc_fence_after();
+      if (lane == 0) {
+        const uint64_t a = sdesc_kmajor_sw128(q_smem + qs * C::kTile);
+        const uint64_t b = sdesc_kmajor_sw128(kv_smem + (k % S) * C::kTile);
+#pragma unroll
+        for (int h = 0; h < C::kHalves; ++h)
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            mma_bf16_ss(s_t[s], a + h * 1024 + x * 2, b + h * 1024 + x * 2, kIdQK, (h | x) != 0);
+        tc_commit(smem_addr(&sm.s_full[s]));
+      }
+      __syncwarp();
+    };
+    auto pv = [&](int s, uint32_t k, bool acc) {  // accumulator of stream s (+)= P . V
+      tc_fence_after();
+      if (lane == 0) {
+        const uint64_t b = sdesc_mnmajor_sw128(kv_smem + (k % S) * C::kTile, 16384);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) mma_bf16_ts(o_t[s], s_t[s] + 8 * x, b + x * 128, kIdPV, acc || x > 0);
+        tc_commit(smem_addr(&sm.pv_done[s]));
+      }
+      __syncwarp();
+    };
+    auto release = [&](uint32_t k) {
+      if (lane == 0) tc_commit(smem_addr(&sm.kv_empty[k % S]));
+      __syncwarp();
+    };
+    // the weights of stream s are in TMEM, and (first product of an item) its accumulator has been read
+    auto weights = [&](int s, bool first) {
+      if (!warp_wait(&sm.p_ready[s], pn[s]++ & 1, ctl)) return false;
+      if (first) {
+        if (on[s] > 0 && !warp_wait(&sm.o_free[s], (on[s] - 1) & 1, ctl)) return false;
+        ++on[s];
+      }
+      return true;
+    };
+    bool ok = true;
+    while (ok && walk.next(p, sm.pre, it)) {
+      if (it.split) {
+        const int nt = it.t1 - it.t0;
+        for (int l = 0; ok && l < min(2, nt); ++l) {
+          ok = ring(rn) && (l > 0 || warp_wait(&sm.q_full[0], qn[0]++ & 1, ctl));
+          if (!ok) break;
+          qk(l, 0, rn);
+          release(rn++);
+        }
+        for (int i = 0; ok && i < nt; ++i) {
+          const int s = i & 1;
+          const uint32_t vk = rn++;
+          ok = weights(s, i < 2) && ring_v(vk, it, it.t0 + i);
+          if (!ok) break;
+          pv(s, vk, i >= 2);
+          release(vk);
+          if (i + 2 < nt) {
+            ok = ring(rn);
+            if (!ok) break;
+            qk(s, 0, rn);
+            release(rn++);
+          }
+        }
+      } else {
+        ok = ring(rn);
+        for (int s = 0; ok && s < 2; ++s) {
+          if (it.end[s] <= it.t0) continue;
+          ok = warp_wait(&sm.q_full[s], qn[s]++ & 1, ctl);
+          if (ok) qk(s, s, rn);
+        }
+        if (ok) release(rn++);
+        for (int j = it.t0; ok && j < it.t1; ++j) {
+          const uint32_t vk = rn++, kk = rn;
+          const bool more = j + 1 < it.t1;
+          if (more) ++rn;
+          bool have_v = false, have_k = false;
+          for (int s = 0; ok && s < 2; ++s) {
+            if (j >= it.end[s]) continue;
+            ok = weights(s, j == it.t0) && (have_v || ring_v(vk, it, j));
+            have_v = true;
+            if (!ok) break;
+            pv(s, vk, j > it.t0);
+            if (j + 1 < it.end[s]) {
+              ok = have_k || ring(kk);
+              have_k = true;
+              if (ok) qk(s, s, kk);
+            }
+          }
+          if (!ok) break;
+          release(vk);
+          if (more) release(kk);
+        }
+      }
+    }
+    // every MMA has completed before the CTA leaves its shared memory and TMEM
+    if (lane == 0) {
+      tc_commit(smem_addr(&sm.mma_done));
+      drain(&sm.mma_done, 0, p.timeout_ns);
+    }
+    __syncwarp();
+  } else if (warp == 10) {
+    // -------------------------------------------------------------- guard
+    // A weight of zero times a NaN is a NaN: before a v tile that not every
+    // row sees in full is multiplied, its rows that no row sees are zeroed,
+    // and a row that only some see is replaced by zeros if it holds a NaN or
+    // an infinity, and noted: who sees it adds it at the end.
+    uint32_t n = 0, issued = 0;
+    int k = 0;
+    bool ok = true;
+    while (ok && walk.next(p, sm.pre, it)) {
+      if (k >= 2) ok = warp_wait(&sm.item_done[k & 1], ((k >> 1) - 1) & 1, ctl);
+      if (!ok) break;
+      if (lane < 12) (&sm.poison[k & 1][0][0])[lane] = 0;
+      __syncwarp();
+      const int nt = it.t1 - it.t0, lead = min(it.split ? 2 : 1, nt);
+      const int g0 = first_guarded<TREE>(it);
+      for (int j = g0; ok && j < it.t1; ++j) {
+        if (!guarded<TREE>(it, j)) continue;
+        const int i = j - it.t0;
+        const uint32_t at = n + lead + i + min(i, nt - lead), slot = at % S;  // the v tile's place in the ring
+        // (once the load is issued, the slot's earlier phases are over)
+        ok = warp_wait(&sm.v_issued[slot], (issued >> slot) & 1, ctl) &&
+             warp_wait(&sm.kv_full[slot], (at / S) & 1, ctl);
+        if (!ok) break;
+        issued ^= 1u << slot;
+        const uint32_t tile = kv_smem + slot * C::kTile;
+        const int valid = v_valid<TREE>(it, j), shared = v_shared<TREE>(it, j);
+        for (int r = shared + lane; r < kKeys; r += 32) {
+          bool wipe = r >= valid;
+          if (!wipe) {
+            bool bad = false;
+#pragma unroll
+            for (int h = 0; h < C::kHalves; ++h)
+#pragma unroll
+              for (int x = 0; x < 8; ++x) {
+                const uint4 w = ld_shared_v4(tile + h * 16384 + r * 128 + ((x + lane) & 7) * 16);
+                bad |= not_finite2(w.x) || not_finite2(w.y) || not_finite2(w.z) || not_finite2(w.w);
+              }
+            if (bad) atomicOr(&sm.poison[k & 1][j - g0][r >> 5], 1u << (r & 31));
+            wipe = bad;
+          }
+          if (wipe) {
+#pragma unroll
+            for (int h = 0; h < C::kHalves; ++h)
+#pragma unroll
+              for (int x = 0; x < 8; ++x) st_shared_v4(tile + h * 16384 + r * 128 + ((x + lane) & 7) * 16, 0, 0, 0, 0);
+          }
+        }
+        // (a tile that all rows see as far as it goes: only its tail)
+        for (int r = max(valid, 0) + lane; r < min(shared, kKeys); r += 32)
+#pragma unroll
+          for (int h = 0; h < C::kHalves; ++h)
+#pragma unroll
+            for (int x = 0; x < 8; ++x) st_shared_v4(tile + h * 16384 + r * 128 + ((x + lane) & 7) * 16, 0, 0, 0, 0);
+        fence_proxy_async_smem();
+        warp_arrive(&sm.kv_clean[slot], lane);
+      }
+      n += 2 * nt;
+      if (ok) warp_arrive(&sm.guard_item[k & 1], lane);
+      ++k;
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ softmax
+    const int st = warp >> 2;                       // stream
+    const int row = (warp & 3) * 32 + lane;         // row of the tile
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_t = tmem + lanes + st * 128, o_t = tmem + lanes + 256 + st * 128;
+    const float c = p.scale * kLog2e;
+    const int rt = row / G, rg = row - rt * G;      // token of the tile, head of the group
+    uint32_t cnt = 0, xn = 0;
+    int k = 0;
+    bool ok = true;
+    if (p.debug_stall) ok = warp_wait(&sm.stall, 0, ctl);
+    while (ok && walk.next(p, sm.pre, it)) {
+      const int tile0 = it.split ? 0 : st;          // which row tile
+      const int tok = it.r0 + tile0 * TQ + rt;      // in the sequence
+      const bool valid_row = rt < it.cnt[tile0];
+      const bool warp_rows = __any_sync(0xFFFFFFFFu, valid_row);
+      const int first = it.split ? it.t0 + st : it.t0, step = it.split ? 2 : 1;
+      const int last = it.split ? it.t1 : it.end[st];
+      unsigned long long word = 0;
+      bool any = true;
+      if (TREE) {
+        if (valid_row) word = p.mask[it.a0 + tok] & (it.n >= 64 ? ~0ull : (1ull << it.n) - 1ull);
+        any = it.ctx > 0 || word != 0ull;
+      }
+      float m = -INFINITY, l = 0.0f;
+      for (int j = first; j < last; j += step) {
+        ok = warp_wait(&sm.s_full[st], cnt & 1, ctl);
+        if (!ok) break;
+        if (warp_rows) {
+          tc_fence_after();
+          uint32_t s[4][32];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) tmem_ld32(s_t + x * 32, s[x]);
+          tmem_ld_wait();
+          // what the row does not see
+          if (TREE ? j >= it.ctx / kKeys : (j + 1) * kKeys > it.r0 + tile0 * TQ + 1) {
+            if (TREE && j >= it.nct) {
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (x >= 2 || !((uint32_t)(word >> (x * 32)) >> e & 1u)) s[x][e] = 0xFF800000u;
+            } else {
+              const int see = (TREE ? it.ctx : tok + 1) - j * kKeys;
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (x * 32 + e >= see) s[x][e] = 0xFF800000u;
+            }
+          }
+          float mx = -INFINITY;
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(s[x][e]));
+          if (j == first) {
+            m = mx;
+          } else if (__any_sync(0xFFFFFFFFu, valid_row && (mx - m) * c > kFallBehind)) {
+            // the reference has fallen behind: move it, and with it the sum and the accumulator
+            const float mn = fmaxf(m, mx);
+            const float f = mn == -INFINITY ? 1.0f : ex2((m - mn) * c);
+            l *= f;
+            m = mn;
+            ok = warp_wait(&sm.pv_done[st], (cnt - 1) & 1, ctl);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int x = 0; x < D / 32; ++x) {
+              uint32_t o[32];
+              tmem_ld32(o_t + x * 32, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st32(o_t + x * 32, o);
+            }
+          }
+          const float ref = m == -INFINITY ? 0.0f : m * c;
+          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            uint32_t w[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float a = ex2(fmaf(__uint_as_float(s[2 * x + e / 16][2 * e % 32]), c, -ref));
+              const float b = ex2(fmaf(__uint_as_float(s[2 * x + e / 16][2 * e % 32 + 1]), c, -ref));
+              sum[e & 3] += a + b;
+              w[e] = pack_bf16x2(a, b);
+            }
+            tmem_st32(s_t + x * 32, w);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_st_wait();
+          tc_fence_before();
+        }
+        warp_arrive(&sm.p_ready[st], lane);
+        ++cnt;
+      }
+      if (!ok) break;
+      const int nt = it.t1 - it.t0;
+      const bool active = first < last, both = it.split && nt > 1;
+      // the q tile has been multiplied for the last time
+      if (it.split ? st == ((nt - 1) & 1) : active) warp_arrive(&sm.q_empty[it.split ? 0 : st], lane);
+      ok = warp_wait(&sm.guard_item[k & 1], (k >> 1) & 1, ctl);
+      if (!ok) break;
+      if (active) {
+        ok = warp_wait(&sm.pv_done[st], (cnt - 1) & 1, ctl);
+        if (!ok) break;
+        tc_fence_after();
+        // v rows that the guard has replaced, added by those who see them
+        const int g0 = first_guarded<TREE>(it);
+        uint32_t anyp = 0;
+        for (int x = 0; x < 12; ++x) anyp |= (&sm.poison[k & 1][0][0])[x];
+        auto poisoned = [&](uint32_t (&o)[32], int c0) {
+          for (int x = 0; x < 12; ++x) {
+            uint32_t bits = (&sm.poison[k & 1][0][0])[x];
+            const int j = g0 + x / 4;
+            if (it.split && ((j - first) & 1)) continue;  // the other stream's tile
+            while (bits) {
+              const int r = (x & 3) * 32 + __ffs(bits) - 1;
+              bits &= bits - 1;
+              const int key = TREE ? r : j * kKeys + r;
+              if (!valid_row || !(TREE ? (bool)(word >> key & 1ull) : key <= tok)) continue;
+              const uint16_t *v = p.v.ptr + (long long)(it.a0 + key) * p.v.tok + it.hk * p.v.head + c0;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const uint32_t y = v[e];
+                if ((y & 0x7F80u) == 0x7F80u) o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(y << 16));
+              }
+            }
+          }
+        };
+        float fo = 1.0f, fx = 0.0f;  // this stream's and the other's factor
+        if (both && st == 1) {
+          // hand the second stream's part of the result to the first, through
+          // the unused q tile, D / 2 columns at a time
+#pragma unroll 1
+          for (int h = 0; ok && h < 2; ++h, ++xn) {
+            if (xn > 0) ok = warp_wait(&sm.x_free, (xn - 1) & 1, ctl);
+            if (!ok) break;
+            if (h == 0) sm.xm[row] = m, sm.xl[row] = l;
+            if (warp_rows) {
+#pragma unroll 1
+              for (int x = 0; x < D / 64; ++x) {
+                const int c0 = h * (D / 2) + x * 32;
+                uint32_t o[32];
+                tmem_ld32(o_t + c0, o);
+                tmem_ld_wait();
+                if (anyp) poisoned(o, c0);
+                const uint32_t at = q_smem + C::kTile + (x * 32 * kRowsT + row) * 4;
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + e * kRowsT * 4), "r"(o[e]) : "memory");
+              }
+            }
+            warp_arrive(&sm.x_ready, lane);
+          }
+        } else {
+          const int tokg = it.a0 + tok, head = it.hk * G + rg;
+          float *part = nullptr;
+          if (TREE && it.part >= 0)
+            part = p.ws + ((long long)blockIdx.x * 2 + it.part) * C::kSlotFloats + tile0 * (kRowsT * (D + 2));
+          float inv = 0.0f;
+#pragma unroll 1
+          for (int h = 0; ok && h < 2; ++h) {
+            if (both) {
+              ok = warp_wait(&sm.x_ready, xn & 1, ctl);
+              if (!ok) break;
+              if (h == 0) {
+                const float m1 = sm.xm[row], l1 = sm.xl[row], mn = fmaxf(m, m1);
+                fo = m == -INFINITY ? 0.0f : ex2((m - mn) * c);
+                fx = m1 == -INFINITY ? 0.0f : ex2((m1 - mn) * c);
+                l = l * fo + l1 * fx;
+                m = mn;
+              }
+            }
+            if (h == 0) inv = any ? 1.0f / l : 0.0f;
+            if (warp_rows) {
+#pragma unroll 1
+              for (int x = 0; x < D / 64; ++x) {
+                const int c0 = h * (D / 2) + x * 32;
+                uint32_t o[32];
+                tmem_ld32(o_t + c0, o);
+                tmem_ld_wait();
+                if (anyp) poisoned(o, c0);
+                if (both) {
+                  const uint32_t at = q_smem + C::kTile + (x * 32 * kRowsT + row) * 4;
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) {
+                    float y;
+                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(y) : "r"(at + e * kRowsT * 4));
+                    o[e] = __float_as_uint(__uint_as_float(o[e]) * fo + y * fx);
+                  }
+                }
+                if (part) {
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) part[(c0 + e) * kRowsT + row] = __uint_as_float(o[e]);
+                } else if (valid_row) {
+                  uint16_t *out = p.out.ptr + (long long)tokg * p.out.tok + head * p.out.head + c0;
+#pragma unroll
+                  for (int e = 0; e < 32; e += 8) {
+                    float y[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[i] = any ? __uint_as_float(o[e + i]) * inv : 0.0f;
+                    *reinterpret_cast<uint4 *>(out + e) =
+                        make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                                   pack_bf16x2(y[6], y[7]));
+                  }
+                }
+              }
+            }
+            if (both) {
+              warp_arrive(&sm.x_free, lane);
+              ++xn;
+            }
+          }
+          if (part) {
+            part[D * kRowsT + row] = m;
+            part[(D + 1) * kRowsT + row] = l;
+          }
+        }
+        if (!ok) break;
+        tc_fence_before();
+        warp_arrive(&sm.o_free[st], lane);
+      }
+      if (it.split && st == 0) {
+        fence_proxy_async_smem();  // the exchange space is a TMA target again
+        warp_arrive(&sm.q_empty[1], lane);
+      }
+      warp_arrive(&sm.item_done[k & 1], lane);
+      ++k;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the parts of the items that several CTAs shared: CTA c (x) takes the
+// item that starts in its range and goes on, with its parts in the order of
+// the keys; y = 16-column slices.
+template <int D>
+__global__ void __launch_bounds__(128) attn_join_kernel(const AttnParams p, int ctas) {
+  using C = Cfg<D>;
+  __shared__ Prefix pre;
+  pdl_trigger();
+  pdl_wait();
+  if (threadIdx.x < 32) fill_prefix<true>(p, pre, threadIdx.x, false);
+  __syncthreads();
+  const long long U = pre.units[kBlocks];
+  const int c0 = blockIdx.x;
+  const long long u0 = U * c0 / ctas, u1 = U * (c0 + 1) / ctas;
+  if (u1 <= u0 || u1 >= U) return;
+  long long u = u1 - 1;  // the CTA's last unit
+  int b;
+  const Seq s = find_seq<true>(p, pre, u, b);
+  const int per = s.nct + 1, gh = (int)(u / per), hk = gh % p.Hkv, g = gh / p.Hkv;
+  const int t = (int)(u - (long long)gh * per);
+  if (t == per - 1 || t >= u1 - u0) return;  // it ends here, or began in a CTA before
+  const long long stop = u1 + (per - 1 - t);   // one past the item's last unit
+  const int row = threadIdx.x, G = p.Hq / p.Hkv, rt = row / G, rg = row - rt * G;
+  const float c = p.scale * kLog2e;
+  for (int tile = 0; tile < 2; ++tile) {
+    const int node = (2 * g + tile) * s.tq + rt;
+    if (rt >= s.tq || node >= s.n) continue;
+    auto slot = [&](int cta) {
+      return p.ws + ((long long)cta * 2 + (cta == c0 ? 1 : 0)) * C::kSlotFloats + tile * (kRowsT * (D + 2)) + row;
+    };
+    // (fewer units than CTAs: some ranges are empty)
+    auto holds = [&](int cta) { return U * (cta + 1) / ctas > U * cta / ctas; };
+    float m = -INFINITY;
+    for (int cta = c0; U * cta / ctas < stop; ++cta)
+      if (holds(cta)) m = fmaxf(m, __ldcg(slot(cta) + D * kRowsT));
+    float l = 0.0f, o[16] = {};
+    for (int cta = c0; U * cta / ctas < stop; ++cta) {
+      if (!holds(cta)) continue;
+      const float *q = slot(cta);
+      const float mi = __ldcg(q + D * kRowsT);
+      const float f = mi == -INFINITY ? 0.0f : ex2((mi - m) * c);
+      l += f * __ldcg(q + (D + 1) * kRowsT);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[e] += f * __ldcg(q + (blockIdx.y * 16 + e) * kRowsT);
+    }
+    const unsigned long long word = p.mask[s.a0 + node] & (s.n >= 64 ? ~0ull : (1ull << s.n) - 1ull);
+    const bool any = s.ctx > 0 || word != 0ull;
+    const float inv = 1.0f / l;
+    uint16_t *out = p.out.ptr + (long long)(s.a0 + node) * p.out.tok + (hk * G + rg) * p.out.head + blockIdx.y * 16;
+#pragma unroll
+    for (int e = 0; e < 16; e += 8) {
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = any ? o[e + i] * inv : 0.0f;
+      *reinterpret_cast<uint4 *>(out + e) = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
+                                                       pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+    }
+  }
+}
+
+// ------------------------------------------------------------------- host
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static std::once_flag once;
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  std::call_once(once, [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+// bf16, 128-byte swizzle; dims[0] = D, strides (bytes) of the others; a
+// dimension of one entry gets a stride the encoder accepts whatever the
+// caller's is.
+bool make_map(CUtensorMap *m, const void *ptr, int rank, const cuuint64_t *dims, const long long *elem_strides,
+              const cuuint32_t *box) {
+  auto enc = encoder();
+  if (!enc) return false;
+  cuuint64_t strides[4];
+  for (int i = 0; i < rank - 1; ++i)
+    strides[i] = dims[i + 1] == 1 ? dims[0] * 2 : (cuuint64_t)elem_strides[i] * 2;
+  const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void *>(ptr), dims, strides, box, ones,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool heads_map(CUtensorMap *m, const Heads &h, int heads, int T, int D, int box_heads, int box_toks) {
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)T};
+  const long long st[2] = {h.head, h.tok};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_toks};
+  return make_map(m, h.ptr, 3, dims, st, box);
+}
+
+template <int D, bool TREE>
+cudaError_t launch_t(const AttnParams &p, int sm_count, cudaStream_t stream) {
+  using C = Cfg<D>;
+  auto kern = attn_kernel<D, TREE>;
+  static DeviceOnce once;
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!once.done(dev)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    once.set(dev);
+  }
+  const int G = p.Hq / p.Hkv, TQ = kRowsT / G;
+  CUtensorMap q, k, v, kc, vc;
+  std::memset(&kc, 0, sizeof(kc));
+  std::memset(&vc, 0, sizeof(vc));
+  const int rows = TREE ? kAttnMaxNodes : kKeys;
+  if (!heads_map(&q, p.q, p.Hq, p.T, D, G, TQ) || !heads_map(&k, p.k, p.Hkv, p.T, D, 1, rows) ||
+      !heads_map(&v, p.v, p.Hkv, p.T, D, 1, rows))
+    return cudaErrorInvalidValue;
+  long long ctas = sm_count;
+  if (TREE) {
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)p.Hkv, (cuuint64_t)p.cache.page_size,
+                                (cuuint64_t)p.cache.pages};
+    const long long st[3] = {p.cache.head, p.cache.slot, p.cache.page};
+    const cuuint32_t box[4] = {64, 1, (cuuint32_t)(p.cache.page_size < kKeys ? p.cache.page_size : kKeys), 1};
+    if (!make_map(&kc, p.cache.k, 4, dims, st, box) || !make_map(&vc, p.cache.v, 4, dims, st, box))
+      return cudaErrorInvalidValue;
+  } else {
+    // a CTA an item: at most this many row groups (each sequence rounds up)
+    ctas = ((long long)p.T / (2 * TQ) + p.B) * p.Hkv;
+    if (ctas > 0x7fffffffLL) ctas = 0x7fffffffLL;  // (the kernel strides over the rest)
+  }
+  cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)ctas), dim3(kThreads), C::kSmem, stream);
   cudaLaunchAttribute attr[1];
   attach_pdl(cfg, attr);
-  return p.D == 64 ? cudaLaunchKernelEx(&cfg, attn_rows_kernel<64, TREE>, p)
-                   : cudaLaunchKernelEx(&cfg, attn_rows_kernel<128, TREE>, p);
+  e = cudaLaunchKernelEx(&cfg, kern, q, k, v, kc, vc, p);
+  if (TREE && e == cudaSuccess) {
+    cudaLaunchConfig_t jc = pdl_config(dim3((unsigned)ctas, D / 16), dim3(128), 0, stream);
+    attach_pdl(jc, attr);
+    e = cudaLaunchKernelEx(&jc, attn_join_kernel<D>, p, (int)ctas);
+  }
+  return e;
 }
 
 }  // namespace
 
-cudaError_t launch_attn_prompt(const AttnParams &p, int, cudaStream_t stream) { return launch_rows<false>(p, stream); }
-cudaError_t launch_attn_tree(const AttnParams &p, int, cudaStream_t stream) { return launch_rows<true>(p, stream); }
-size_t attn_tree_ws_bytes(int, int) { return 256; }
+cudaError_t launch_attn_prompt(const AttnParams &p, int sm_count, cudaStream_t stream) {
+  return p.D == 64 ? launch_t<64, false>(p, sm_count, stream) : launch_t<128, false>(p, sm_count, stream);
+}
+cudaError_t launch_attn_tree(const AttnParams &p, int sm_count, cudaStream_t stream) {
+  return p.D == 64 ? launch_t<64, true>(p, sm_count, stream) : launch_t<128, true>(p, sm_count, stream);
+}
+size_t attn_tree_ws_bytes(int D, int sm_count) {
+  const long long f = D == 64 ? Cfg<64>::kSlotFloats : Cfg<128>::kSlotFloats;
+  return (size_t)(2 * f * sm_count) * sizeof(float);
+}
 
 }  // namespace mxg

@@ -63,7 +63,7 @@ mxg::Cache cache_of(const mxg_kv_cache *c) {
 // What attn_prompt and attn_tree check alike.
 mxg_status check_attn(const mxg_heads *q, const mxg_heads *k, const mxg_heads *v, const int *cu, int B, int T,
                       int Hq, int Hkv, int D, float scale, const mxg_heads *out, const mxg_attn_opts *opts) {
-  if (!cu || B < 1 || T < 0 || Hq < 1 || Hkv < 1 || !std::isfinite(scale)) return MXG_ERR_INVALID_ARG;
+  if (!cu || B < 1 || T < 0 || Hq < 1 || Hkv < 1 || !std::isfinite(scale) || !(scale > 0.0f)) return MXG_ERR_INVALID_ARG;
   if ((D != 64 && D != 128) || Hq % Hkv != 0 || Hq / Hkv > 128 || B > mxg::kAttnMaxSeqs)
     return MXG_ERR_UNSUPPORTED_SHAPE;
   if (opts && (opts->debug_stall < 0 || opts->debug_stall > 1)) return MXG_ERR_INVALID_ARG;

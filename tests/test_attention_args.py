@@ -43,7 +43,7 @@ PROMPT = dict(q=H(), k=H(), v=H(), cu=P, B=2, T=10, Hq=8, Hkv=2, D=128, scale=0.
 
 
 @pytest.mark.parametrize("kw,want", [
-    (dict(B=0), 1), (dict(T=-1), 1), (dict(Hq=0), 1), (dict(Hkv=0), 1), (dict(cu=None), 1), (dict(scale=float("inf")), 1),
+    (dict(B=0), 1), (dict(T=-1), 1), (dict(Hq=0), 1), (dict(Hkv=0), 1), (dict(cu=None), 1), (dict(scale=float("inf")), 1), (dict(scale=0.0), 1), (dict(scale=-1.0), 1),
     (dict(Hkv=3), 2), (dict(D=96), 2), (dict(Hq=258, Hkv=2), 2), (dict(B=4097), 2), (dict(q=None), 1), (dict(out=H(ptr=None)), 1),
     (dict(v=H(ptr=P + 8)), 3), (dict(k=H(tok=4)), 3), (dict(cu=P + 1), 3), (dict(opts=AttnOpts(debug_stall=2)), 1),
     (dict(opts=AttnOpts(dev_status=P + 2)), 3),
