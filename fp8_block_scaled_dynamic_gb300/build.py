@@ -1,5 +1,6 @@
 """Build libmxgemm.so in-tree: nvcc for sm_103a only, one object per source
-compiled in parallel, then a shared link against the CUDA runtime."""
+compiled in parallel, then a shared link against the CUDA runtime; beside it
+_attn_bind.so, the CPython module that calls the attention entry points."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -14,6 +15,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmxgemm.so")
 SOURCES = ["api.cu", "quant.cu", "gemm.cu", "attn_api.cu", "attn.cu", "rope.cu"]
+BIND = os.path.join(PKG, "_attn_bind.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -33,6 +35,22 @@ def _stale(out: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _bind_flags() -> tuple[list[str], list[str]]:
+    """Compile and link flags of the CPython module (torch's headers and libraries)."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           os.path.join(os.path.dirname(_cuda_lib_dir()), "include"), sysconfig.get_paths()["include"], INCLUDE]
+    cc = ["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"] + ["-I" + i for i in inc]
+    lib = os.path.join(root, "lib")
+    ld = ["-L" + lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath," + lib,
+          "-L" + PKG, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + _cuda_lib_dir()]
+    return cc, ld
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
@@ -50,13 +68,18 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if force or _stale(o, [s] + headers):
             jobs.append([nvcc(), *flags, "-c", s, "-o", o])
 
+    bind_src, bind_obj = os.path.join(CSRC, "bind.cpp"), os.path.join(BUILD, "bind.o")
+    bind_cc, bind_ld = _bind_flags()
+    if force or _stale(bind_obj, [bind_src] + headers):
+        jobs.append(["g++", *bind_cc, "-c", bind_src, "-o", bind_obj])
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"{os.path.basename(cmd[0])} failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         return r.stdout + r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         for out in ex.map(run, jobs):
             if verbose and out:
                 print(out)
@@ -65,6 +88,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "shared",
              "-Xlinker", "-rpath," + _cuda_lib_dir()])
         os.replace(tmp, LIB)
+    if force or _stale(BIND, [bind_obj]):
+        tmp = BIND + f".tmp{os.getpid()}"
+        run(["g++", "-shared", "-o", tmp, bind_obj, *bind_ld])
+        os.replace(tmp, BIND)
     return LIB
 
 

@@ -17,7 +17,8 @@
 //
 // Warps of a CTA: 0-3 and 4-7 the softmax of stream 0 and 1 (a thread is a
 // row: its 128 scores come from TMEM into registers), 8 issues the MMAs, 9
-// loads by TMA, 10 guards the v tiles that not every row sees in full.
+// loads by TMA, 10 guards the v tiles that not every row sees in full, 11
+// works out the CTA's items and hands them to the others.
 // TMEM: scores of a stream 128 columns, the bf16 weights over the first 64 of
 // them once they are read, accumulators D columns a stream.
 // Hand-offs are mbarriers; every wait is bounded.
@@ -41,8 +42,15 @@ constexpr int kThreads = 384;
 constexpr int kKeys = 128;  // keys of a tile
 constexpr int kRowsT = 128; // rows of a tile
 constexpr int kHead = 3072; // shared memory before the tiles
+// Registers a thread: a softmax thread holds a row of 128 scores; the two
+// softmax warpgroups take what the third gives up.  The three shares are the
+// 168 a thread that the kernel is launched with.
+constexpr int kRegs = 168, kRegsSoftmax = 208, kRegsRest = 88;
+static_assert(2 * kRegsSoftmax + kRegsRest == 3 * kRegs, "register split");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kFallBehind = 8.0f;  // log2 of how far the reference may lag the maximum
+
+constexpr long long kJoinFloats = 256 * 8;  // JoinItem of each CTA at the workspace's start
 
 template <int D>
 struct Cfg {
@@ -50,65 +58,73 @@ struct Cfg {
   static constexpr int kTile = kKeys * D * 2;
   static constexpr int kSlots = D == 128 ? 5 : 8;
   static constexpr int kSmem = kHead + (2 + kSlots) * kTile;
-  static constexpr long long kSlotFloats = 2LL * kRowsT * (D + 2);  // a CTA's partial result of an item
+  // a CTA's partial result of an item: two row tiles of [row][D] sums, then
+  // their references and weight sums
+  static constexpr long long kSlotFloats = 2LL * kRowsT * (D + 2);
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
 // ------------------------------------------------------------ work of a call
 // Sequences in order; of each its kv heads, its row groups (pairs of row
-// tiles), and -- tree -- its key tiles, all units numbered through.  The
-// coarse prefix holds the number of units before every block of sequences and
-// the offset the block's first sequence may not start below.
+// tiles), and -- tree -- its key tiles, all units numbered through (the host
+// has checked that their number fits 31 bits).  The coarse prefix holds the
+// number of units before every block of sequences and the offset that the
+// block's first sequence may not start below.
 constexpr int kBlocks = 64;
 constexpr int kBlocksLane = kBlocks / 32;
 struct Prefix {
-  long long units[kBlocks + 1];
+  int units[kBlocks + 1];
   int start[kBlocks];
 };
 
 struct Seq {
-  int a0, n;       // first token (node), tokens (nodes)
-  int ctx, nct;    // tree: cached tokens and their tiles
-  int tq, groups;  // tokens of a row tile, row groups
-  long long units;
+  int a0, n;    // first token (node), tokens (nodes)
+  int ctx;      // tree: cached tokens
+  int per;      // key tiles of a row group that count as units (prompt: 1)
+  int units;
 };
 
+struct Raw {
+  int c0, c1, ctx;
+};
 template <bool TREE>
-__device__ __forceinline__ Seq seq_of(const AttnParams &p, int b, int &running, bool *bad) {
+__device__ __forceinline__ Raw raw_seq(const AttnParams &p, int b) {
+  return {__ldg(p.cu + b), __ldg(p.cu + b + 1), TREE ? __ldg(p.ctx + b) : 0};
+}
+
+template <bool TREE>
+__device__ __forceinline__ Seq seq_of(const AttnParams &p, const Raw &r, int tq2, int &running, bool *bad) {
   Seq s;
-  const int c0 = p.cu[b], c1 = p.cu[b + 1];
-  s.a0 = max(min(max(c0, 0), p.T), running);
-  const int a1 = max(min(max(c1, 0), p.T), s.a0);
-  if (bad && (c0 != s.a0 || c1 != a1)) *bad = true;
+  s.a0 = max(min(max(r.c0, 0), p.T), running);
+  const int a1 = max(min(max(r.c1, 0), p.T), s.a0);
+  if (bad && (r.c0 != s.a0 || r.c1 != a1)) *bad = true;
   running = s.a0;
   s.n = a1 - s.a0;
-  s.tq = kRowsT / (p.Hq / p.Hkv);
+  s.ctx = 0;
+  s.per = 1;
   if (TREE) {
     if (s.n > kAttnMaxNodes) {
       s.n = kAttnMaxNodes;
       if (bad) *bad = true;
     }
-    const long long room = (long long)p.table_cols * p.cache.page_size;
-    const int c = p.ctx[b];
-    s.ctx = (int)min((long long)max(c, 0), room);
-    if (bad && c != s.ctx) *bad = true;
-    s.nct = (s.ctx + kKeys - 1) / kKeys;
-  } else {
-    s.ctx = s.nct = 0;
+    s.ctx = min(max(r.ctx, 0), p.table_cols * p.cache.page_size);
+    if (bad && r.ctx != s.ctx) *bad = true;
+    s.per = (s.ctx + kKeys - 1) / kKeys + 1;
   }
-  s.groups = (s.n + 2 * s.tq - 1) / (2 * s.tq);
-  s.units = (long long)s.groups * p.Hkv * (TREE ? s.nct + 1 : 1);
+  s.units = (s.n + tq2 - 1) / tq2 * p.Hkv * s.per;
   return s;
 }
 
-// One warp fills the prefix.
+// One warp fills the prefix.  tq2: tokens of a row group.
 template <bool TREE>
-__device__ __forceinline__ void fill_prefix(const AttnParams &p, Prefix &pre, int lane, bool report) {
+__device__ __forceinline__ void fill_prefix(const AttnParams &p, Prefix &pre, int tq2, int lane, bool report) {
   constexpr unsigned kFull = 0xFFFFFFFFu;
   const int per = (p.B + kBlocks - 1) / kBlocks;
   const int own = kBlocksLane * per, b0 = min(lane * own, p.B), b1 = min(b0 + own, p.B);
-  int top = 0;  // largest clamped offset of this lane's sequences, then of those before
-  for (int b = b0; b < b1; ++b) top = max(top, min(max(p.cu[b], 0), p.T));
+  Raw first = {0, 0, 0};  // (a small batch is read once)
+  if (b0 < b1) first = raw_seq<TREE>(p, b0);
+  int top = min(max(first.c0, 0), p.T);  // largest offset of this lane's sequences, then of those before
+  for (int b = b0 + 1; b < b1; ++b) top = max(top, min(max(__ldg(p.cu + b), 0), p.T));
   int incl = top;
   for (int o = 1; o < 32; o <<= 1) {
     const int x = __shfl_up_sync(kFull, incl, o);
@@ -117,28 +133,30 @@ __device__ __forceinline__ void fill_prefix(const AttnParams &p, Prefix &pre, in
   int running = __shfl_up_sync(kFull, incl, 1);
   if (lane == 0) running = 0;
   bool bad = false;
-  long long mine = 0, part[kBlocksLane];
+  int mine = 0, part[kBlocksLane];
 #pragma unroll
   for (int k = 0; k < kBlocksLane; ++k) {
     const int s0 = min(b0 + k * per, p.B), s1 = min(s0 + per, p.B);
     pre.start[lane * kBlocksLane + k] = running;
     part[k] = mine;
-    for (int b = s0; b < s1; ++b) mine += seq_of<TREE>(p, b, running, &bad).units;
+    for (int b = s0; b < s1; ++b)
+      mine += seq_of<TREE>(p, b == b0 ? first : raw_seq<TREE>(p, b), tq2, running, &bad).units;
   }
-  long long sum = mine;
+  int sum = mine;
   for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(kFull, sum, o);
+    const int x = __shfl_up_sync(kFull, sum, o);
     if (lane >= o) sum += x;
   }
 #pragma unroll
   for (int k = 0; k < kBlocksLane; ++k) pre.units[lane * kBlocksLane + k] = sum - mine + part[k];
   if (lane == 31) pre.units[kBlocks] = sum;
   if (bad && report && p.status) atomicOr(p.status, kBadIndex);
+  __syncwarp();
 }
 
 // The sequence that unit u is of, and u's number in it.
 template <bool TREE>
-__device__ __forceinline__ Seq find_seq(const AttnParams &p, const Prefix &pre, long long &u, int &b) {
+__device__ __forceinline__ Seq find_seq(const AttnParams &p, const Prefix &pre, int tq2, int &u, int &b) {
   int lo = 0, hi = kBlocks - 1;
   while (lo < hi) {  // the last block that starts at or before u
     const int mid = (lo + hi + 1) >> 1;
@@ -149,25 +167,42 @@ __device__ __forceinline__ Seq find_seq(const AttnParams &p, const Prefix &pre, 
   const int per = (p.B + kBlocks - 1) / kBlocks;
   int running = pre.start[lo];
   b = lo * per;
-  Seq s = seq_of<TREE>(p, b, running, nullptr);
+  Seq s = seq_of<TREE>(p, raw_seq<TREE>(p, b), tq2, running, nullptr);
   while (u >= s.units && b + 1 < p.B) {
     u -= s.units;
-    s = seq_of<TREE>(p, ++b, running, nullptr);
+    s = seq_of<TREE>(p, raw_seq<TREE>(p, ++b), tq2, running, nullptr);
   }
   return s;
 }
 
 struct Item {
   int b, hk;
-  int a0, n;     // the sequence's first token (node) and count
-  int r0;        // first token (node) of the first row tile, in the sequence
-  int cnt[2];    // tokens (nodes) of the two row tiles
-  int t0, t1;    // key tiles [t0, t1)
-  int end[2];    // dual: a stream's tiles are [t0, end)
+  int a0, n;   // the sequence's first token (node) and count
+  int r0;      // first token (node) of the first row tile, in the sequence
+  int cnt[2];  // tokens (nodes) of the two row tiles
+  int t0, t1;  // key tiles [t0, t1); t1 == t0: there is no item any more
+  int end[2];  // dual: a stream's tiles are [t0, end)
   int ctx, nct;
-  bool split;    // one row tile: the streams take alternate key tiles
-  int part;      // -1 = the whole item, else the CTA's partial slot (0: the item began before, 1: it goes on)
+  int split;   // one row tile: the streams take alternate key tiles
+  int part;    // -1 = the whole item, else the CTA's partial slot (0: the item began before, 1: it goes on)
 };
+
+// What attn_join_kernel reads of a CTA's item that goes on in the next ones.
+struct JoinItem {
+  int rows0, rows;  // valid rows of the first row tile, of both (0: no such item)
+  int tok, cnt0;    // first token of the rows, tokens of the first row tile
+  int head;         // first query head
+  int last;         // last CTA that holds a part
+  int word, ctx;    // bits of a mask word that count, cached tokens
+};
+
+static_assert(sizeof(JoinItem) == 32, "workspace header");
+
+// The CTAs' shares of U units: CTA c has [c q + min(c, r), ...), q = U / G, r = U % G.
+__device__ __forceinline__ int share_begin(int c, int q, int r) { return c * q + min(c, r); }
+__device__ __forceinline__ int share_owner(int u, int q, int r) {
+  return u < r * (q + 1) ? u / (q + 1) : r + (u - r * (q + 1)) / q;
+}
 
 // Walks the items of one CTA.  Prompt: row groups from the last (its keys are
 // the most) to the first, strided over the grid.  Tree: the units are cut into
@@ -175,53 +210,51 @@ struct Item {
 // that lies in this CTA's range.
 template <bool TREE>
 struct Walk {
-  long long cur, end;
+  int cur, end, q, r;
   __device__ __forceinline__ Walk(const Prefix &pre) {
-    const long long U = pre.units[kBlocks];
+    const int U = pre.units[kBlocks];
     if (TREE) {
-      cur = U * blockIdx.x / gridDim.x;
-      end = U * (blockIdx.x + 1) / gridDim.x;
+      q = U / (int)gridDim.x;
+      r = U - q * (int)gridDim.x;
+      cur = share_begin(blockIdx.x, q, r);
+      end = share_begin(blockIdx.x + 1, q, r);
     } else {
       cur = blockIdx.x;
       end = U;
     }
   }
-  __device__ __forceinline__ bool next(const AttnParams &p, const Prefix &pre, Item &it) {
-    if (cur >= end) return false;
-    long long u = TREE ? cur : end - 1 - cur;
-    const Seq s = find_seq<TREE>(p, pre, u, it.b);
+  __device__ __forceinline__ void next(const AttnParams &p, const Prefix &pre, int tq, Item &it) {
+    it.t0 = it.t1 = 0;
+    if (cur >= end) return;
+    int u = TREE ? cur : end - 1 - cur;
+    const Seq s = find_seq<TREE>(p, pre, 2 * tq, u, it.b);
     it.a0 = s.a0;
     it.n = s.n;
     it.ctx = s.ctx;
-    it.nct = s.nct;
-    int g, last;
+    it.nct = s.per - 1;
+    int g, last = 0;
     if (TREE) {
-      const int per = s.nct + 1;
-      const int gh = (int)(u / per);
-      it.t0 = (int)(u - (long long)gh * per);
-      it.hk = gh % p.Hkv;
+      const int gh = u / s.per;
+      it.t0 = u - gh * s.per;
       g = gh / p.Hkv;
-      it.t1 = (int)min((long long)per, it.t0 + (end - cur));
+      it.hk = gh - g * p.Hkv;
+      last = it.t1 = min(s.per, it.t0 + (end - cur));
       cur += it.t1 - it.t0;
-      it.part = it.t0 > 0 ? 0 : it.t1 < per ? 1 : -1;
-      last = it.t1;
+      it.part = it.t0 > 0 ? 0 : it.t1 < s.per ? 1 : -1;
     } else {
-      it.hk = (int)(u % p.Hkv);
-      g = (int)(u / p.Hkv);
-      it.t0 = 0;
+      g = u / p.Hkv;
+      it.hk = u - g * p.Hkv;
       it.part = -1;
       cur += gridDim.x;
-      last = 0;
     }
-    it.r0 = g * 2 * s.tq;
+    it.r0 = g * 2 * tq;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      it.cnt[k] = min(max(s.n - it.r0 - k * s.tq, 0), s.tq);
-      it.end[k] = it.cnt[k] == 0 ? it.t0 : TREE ? last : (it.r0 + k * s.tq + it.cnt[k] + kKeys - 1) / kKeys;
+      it.cnt[k] = min(max(s.n - it.r0 - k * tq, 0), tq);
+      it.end[k] = it.cnt[k] == 0 ? it.t0 : TREE ? last : (it.r0 + k * tq + it.cnt[k] + kKeys - 1) / kKeys;
     }
-    it.split = TREE && s.n <= s.tq;
+    it.split = TREE && s.n <= tq;
     if (!TREE) it.t1 = max(it.end[0], it.end[1]);
-    return true;
   }
 };
 
@@ -248,17 +281,20 @@ __device__ __forceinline__ int first_guarded(const Item &it) {
   return max(j, it.t0);
 }
 
+constexpr int kItemReaders = 11;  // warps 0 to 10
+
 template <int D>
 struct Smem {
   using C = Cfg<D>;
   // (8-byte barriers first)
   uint64_t q_full[2], q_empty[2], kv_full[C::kSlots], kv_empty[C::kSlots];
   uint64_t v_issued[C::kSlots], kv_clean[C::kSlots];  // the guard's
-  uint64_t s_full[2], p_ready[2], pv_done[2], o_free[2];
-  uint64_t guard_item[2], item_done[2], x_ready, x_free, mma_done, stall;
+  uint64_t s_full[2], p_half[2], p_ready[2], pv_done[2], o_free[2];
+  uint64_t item_full[2], item_free[2], guard_item[2], x_ready, x_free, mma_done, stall;
   uint32_t tmem;
   int abort_flag;
   uint32_t poison[2][3][4];  // rows of the guarded tiles that hold a NaN or an infinity, by item parity
+  Item items[2];
   float xm[kRowsT], xl[kRowsT];
   Prefix pre;
 };
@@ -307,11 +343,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_addr(&sm.q_full[i]), 1);
       mbar_init(smem_addr(&sm.q_empty[i]), 4);
       mbar_init(smem_addr(&sm.s_full[i]), 1);
+      mbar_init(smem_addr(&sm.p_half[i]), 4);
       mbar_init(smem_addr(&sm.p_ready[i]), 4);
       mbar_init(smem_addr(&sm.pv_done[i]), 1);
       mbar_init(smem_addr(&sm.o_free[i]), 4);
       mbar_init(smem_addr(&sm.guard_item[i]), 1);
-      mbar_init(smem_addr(&sm.item_done[i]), 8);
+      mbar_init(smem_addr(&sm.item_full[i]), 1);
+      mbar_init(smem_addr(&sm.item_free[i]), kItemReaders);
     }
     for (int i = 0; i < S; ++i) {
       mbar_init(smem_addr(&sm.kv_full[i]), 1);
@@ -339,258 +377,306 @@ __global__ void __launch_bounds__(kThreads, 1)
       prefetch_tmap(&tmVC);
     }
   }
-  pdl_wait();
-  if (warp == 0) fill_prefix<TREE>(p, sm.pre, lane, blockIdx.x == 0);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&sm.tmem);
   const WaitCtl ctl{&sm.abort_flag, p.status, p.timeout_ns};
-  Walk<TREE> walk(sm.pre);
+  pdl_wait();
   Item it;
+  // item k of the CTA; false when there is none (or a wait ran out)
+  auto next_item = [&](int k) {
+    if (!warp_wait(&sm.item_full[k & 1], (k >> 1) & 1, ctl)) return false;
+    it = sm.items[k & 1];
+    return it.t1 > it.t0;
+  };
+  auto done_item = [&](int k) { warp_arrive(&sm.item_free[k & 1], lane); };
 
-  if (warp == 9) {
-    // ------------------------------------------------------------- loads
-    uint32_t n = 0, nq[2] = {0, 0}, ql[2] = {0, 0};
-    bool ok = true;
-    auto load_kv = [&](const Item &i, int j, bool is_v) {
-      const uint32_t slot = n % S;
-      if (n >= S && !warp_wait(&sm.kv_empty[slot], (n / S - 1) & 1, ctl)) return false;
-      const uint32_t bar = smem_addr(&sm.kv_full[slot]), dst = kv_smem + slot * C::kTile;
-      if (TREE && j < i.nct) {
-        // pages of up to 128 keys, one lane a page; those past the context stay out
-        const int box = min(p.cache.page_size, kKeys);
-        const int first = j * kKeys, boxes = (min(kKeys, i.ctx - first) + box - 1) / box;
-        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box * 128 * C::kHalves));
-        __syncwarp();
-        if (lane < boxes) {
-          const int key = first + lane * box, col = key / p.cache.page_size;
-          int pg = p.table[(long long)i.b * p.ld_table + col];
-          if (pg < 0 || pg >= p.cache.pages) {
-            pg = p.cache.pages;  // out of the map's bounds: zeros
-            if (p.status) atomicOr(p.status, kBadIndex);
+  if (warp >= 8) {
+    regs_less<kRegsRest>();
+    if (warp == 9) {
+      // ------------------------------------------------------------- loads
+      uint32_t n = 0, nq[2] = {0, 0}, ql[2] = {0, 0};
+      bool ok = true;
+      auto load_kv = [&](const Item &i, int j, bool is_v) {
+        const uint32_t slot = n % S;
+        if (n >= S && !warp_wait(&sm.kv_empty[slot], (n / S - 1) & 1, ctl)) return false;
+        const uint32_t bar = smem_addr(&sm.kv_full[slot]), dst = kv_smem + slot * C::kTile;
+        if (TREE && j < i.nct) {
+          // pages of up to 128 keys, one lane a page; those past the context stay out
+          const int box = min(p.cache.page_size, kKeys);
+          const int first = j * kKeys, boxes = (min(kKeys, i.ctx - first) + box - 1) / box;
+          if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box * 128 * C::kHalves));
+          __syncwarp();
+          if (lane < boxes) {
+            const int key = first + lane * box, col = key / p.cache.page_size;
+            int pg = p.table[(long long)i.b * p.ld_table + col];
+            if (pg < 0 || pg >= p.cache.pages) {
+              pg = p.cache.pages;  // out of the map's bounds: zeros
+              if (p.status) atomicOr(p.status, kBadIndex);
+            }
+            const CUtensorMap *tm = is_v ? &tmVC : &tmKC;
+  #pragma unroll
+            for (int h = 0; h < C::kHalves; ++h)
+              tma_load_4d(dst + h * 16384 + lane * box * 128, tm, h * 64, i.hk, key - col * p.cache.page_size, pg, bar);
           }
-          const CUtensorMap *tm = is_v ? &tmVC : &tmKC;
-#pragma unroll
+          __syncwarp();
+        } else if (lane == 0) {
+          // keys of the packed tensors: a prompt's tile, or the nodes (64 rows)
+          const int rows = TREE ? kAttnMaxNodes : kKeys;
+          mbar_arrive_expect_tx(bar, (uint32_t)(rows * 128 * C::kHalves));
+          const CUtensorMap *tm = is_v ? &tmV : &tmK;
+  #pragma unroll
           for (int h = 0; h < C::kHalves; ++h)
-            tma_load_4d(dst + h * 16384 + lane * box * 128, tm, h * 64, i.hk, key - col * p.cache.page_size, pg, bar);
+            tma_load_3d(dst + h * 16384, tm, h * 64, i.hk, i.a0 + (TREE ? 0 : j * kKeys), bar);
+        }
+        if (is_v && guarded<TREE>(i, j)) warp_arrive(&sm.v_issued[slot], lane);
+        ++n;
+        return true;
+      };
+      for (int k = 0; ok && next_item(k); ++k) {
+        ok = load_kv(it, it.t0, false);
+        for (int s = 0; ok && s < 2; ++s) {
+          const bool load = it.split ? s == 0 : it.end[s] > it.t0;
+          if (!load && !it.split) continue;
+          if (nq[s] > 0) ok = warp_wait(&sm.q_empty[s], (nq[s] - 1) & 1, ctl);
+          ++nq[s];  // (a split item's second tile is the streams' exchange space)
+          if (ok && load) ++ql[s];
+          if (ok && load && lane == 0) {
+            const uint32_t bar = smem_addr(&sm.q_full[s]);
+            mbar_arrive_expect_tx(bar, (uint32_t)(TQ * G * 128 * C::kHalves));
+  #pragma unroll
+            for (int h = 0; h < C::kHalves; ++h)
+              tma_load_3d(q_smem + s * C::kTile + h * 16384, &tmQ, h * 64, it.hk * G, it.a0 + it.r0 + s * TQ, bar);
+          }
+        }
+        const int lead = it.split ? 2 : 1;
+        if (ok && lead == 2 && it.t0 + 1 < it.t1) ok = load_kv(it, it.t0 + 1, false);
+        for (int j = it.t0; ok && j < it.t1; ++j) {
+          ok = load_kv(it, j, true);
+          if (ok && j + lead < it.t1) ok = load_kv(it, j + lead, false);
+        }
+        done_item(k);
+      }
+      // nothing may land in shared memory once the CTA is gone (a timeout)
+      for (uint32_t k = n > S ? n - S : 0; k < n; ++k) drain(&sm.kv_full[k % S], (k / S) & 1, p.timeout_ns);
+      for (int s = 0; s < 2; ++s)
+        if (ql[s] > 0) drain(&sm.q_full[s], (ql[s] - 1) & 1, p.timeout_ns);
+    } else if (warp == 8) {
+      // --------------------------------------------------------------- MMAs
+      uint32_t rn = 0, qn[2] = {0, 0}, pn[2] = {0, 0}, on[2] = {0, 0}, clean = 0;
+      constexpr uint32_t kIdQK = idesc_bf16(128, kKeys, false), kIdPV = idesc_bf16(128, D, true);
+      const uint32_t s_t[2] = {tmem, tmem + 128}, o_t[2] = {tmem + 256, tmem + 384};
+      auto ring = [&](uint32_t k) { return warp_wait(&sm.kv_full[k % S], (k / S) & 1, ctl); };
+      auto ring_v = [&](uint32_t k, const Item &i, int j) {
+        if (!ring(k)) return false;
+        if (guarded<TREE>(i, j)) {
+          const uint32_t slot = k % S;
+          if (!warp_wait(&sm.kv_clean[slot], (clean >> slot) & 1, ctl)) return false;
+          clean ^= 1u << slot;
+        }
+        return true;
+      };
+      auto qk = [&](int s, int qs, uint32_t k) {  // scores of stream s = Q tile qs . K^T
+        tc_fence_after();
+        if (lane == 0) {
+          const uint64_t a = sdesc_kmajor_sw128(q_smem + qs * C::kTile);
+          const uint64_t b = sdesc_kmajor_sw128(kv_smem + (k % S) * C::kTile);
+  #pragma unroll
+          for (int h = 0; h < C::kHalves; ++h)
+  #pragma unroll
+            for (int x = 0; x < 4; ++x)
+              mma_bf16_ss(s_t[s], a + h * 1024 + x * 2, b + h * 1024 + x * 2, kIdQK, (h | x) != 0);
+          tc_commit(smem_addr(&sm.s_full[s]));
         }
         __syncwarp();
-      } else if (lane == 0) {
-        // keys of the packed tensors: a prompt's tile, or the nodes (64 rows)
-        const int rows = TREE ? kAttnMaxNodes : kKeys;
-        mbar_arrive_expect_tx(bar, (uint32_t)(rows * 128 * C::kHalves));
-        const CUtensorMap *tm = is_v ? &tmV : &tmK;
-#pragma unroll
-        for (int h = 0; h < C::kHalves; ++h)
-          tma_load_3d(dst + h * 16384, tm, h * 64, i.hk, i.a0 + (TREE ? 0 : j * kKeys), bar);
-      }
-      if (is_v && guarded<TREE>(i, j)) warp_arrive(&sm.v_issued[slot], lane);
-      ++n;
-      return true;
-    };
-    while (ok && walk.next(p, sm.pre, it)) {
-      ok = load_kv(it, it.t0, false);
-      for (int s = 0; ok && s < 2; ++s) {
-        const bool load = it.split ? s == 0 : it.end[s] > it.t0;
-        if (!load && !it.split) continue;
-        if (nq[s] > 0) ok = warp_wait(&sm.q_empty[s], (nq[s] - 1) & 1, ctl);
-        ++nq[s];  // (a split item's second tile is the streams' exchange space)
-        if (ok && load) ++ql[s];
-        if (ok && load && lane == 0) {
-          const uint32_t bar = smem_addr(&sm.q_full[s]);
-          mbar_arrive_expect_tx(bar, (uint32_t)(TQ * G * 128 * C::kHalves));
-#pragma unroll
-          for (int h = 0; h < C::kHalves; ++h)
-            tma_load_3d(q_smem + s * C::kTile + h * 16384, &tmQ, h * 64, it.hk * G, it.a0 + it.r0 + s * TQ, bar);
-        }
-      }
-      const int lead = it.split ? 2 : 1;
-      if (ok && lead == 2 && it.t0 + 1 < it.t1) ok = load_kv(it, it.t0 + 1, false);
-      for (int j = it.t0; ok && j < it.t1; ++j) {
-        ok = load_kv(it, j, true);
-        if (ok && j + lead < it.t1) ok = load_kv(it, j + lead, false);
-      }
-    }
-    // nothing may land in shared memory once the CTA is gone (a timeout)
-    for (uint32_t k = n > S ? n - S : 0; k < n; ++k) drain(&sm.kv_full[k % S], (k / S) & 1, p.timeout_ns);
-    for (int s = 0; s < 2; ++s)
-      if (ql[s] > 0) drain(&sm.q_full[s], (ql[s] - 1) & 1, p.timeout_ns);
-  } else if (warp == 8) {
-    // --------------------------------------------------------------- MMAs
-    uint32_t rn = 0, qn[2] = {0, 0}, pn[2] = {0, 0}, on[2] = {0, 0}, clean = 0;
-    constexpr uint32_t kIdQK = idesc_bf16(128, kKeys, false), kIdPV = idesc_bf16(128, D, true);
-    const uint32_t s_t[2] = {tmem, tmem + 128}, o_t[2] = {tmem + 256, tmem + 384};
-    auto ring = [&](uint32_t k) { return warp_wait(&sm.kv_full[k % S], (k / S) & 1, ctl); };
-    auto ring_v = [&](uint32_t k, const Item &i, int j) {
-      if (!ring(k)) return false;
-      if (guarded<TREE>(i, j)) {
-        const uint32_t slot = k % S;
-        if (!warp_wait(&sm.kv_clean[slot], (clean >> slot) & 1, ctl)) return false;
-        clean ^= 1u << slot;
-      }
-      return true;
-    };
-    auto qk = [&](int s, int qs, uint32_t k) {  // scores of stream s = Q tile qs . K^T
-      tc_fence_after();
-      if (lane == 0) {
-        const uint64_t a = sdesc_kmajor_sw128(q_smem + qs * C::kTile);
-        const uint64_t b = sdesc_kmajor_sw128(kv_smem + (k % S) * C::kTile);
-#pragma unroll
-        for (int h = 0; h < C::kHalves; ++h)
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            mma_bf16_ss(s_t[s], a + h * 1024 + x * 2, b + h * 1024 + x * 2, kIdQK, (h | x) != 0);
-        tc_commit(smem_addr(&sm.s_full[s]));
-      }
-      __syncwarp();
-    };
-    auto pv = [&](int s, uint32_t k, bool acc) {  // accumulator of stream s (+)= P . V
-      tc_fence_after();
-      if (lane == 0) {
+      };
+      // accumulator of stream s (+)= P . V, for the first half of the keys as
+      // soon as their weights are there
+      auto pv = [&](int s, uint32_t k, bool acc) {
         const uint64_t b = sdesc_mnmajor_sw128(kv_smem + (k % S) * C::kTile, 16384);
-#pragma unroll
-        for (int x = 0; x < 8; ++x) mma_bf16_ts(o_t[s], s_t[s] + 8 * x, b + x * 128, kIdPV, acc || x > 0);
-        tc_commit(smem_addr(&sm.pv_done[s]));
-      }
-      __syncwarp();
-    };
-    auto release = [&](uint32_t k) {
-      if (lane == 0) tc_commit(smem_addr(&sm.kv_empty[k % S]));
-      __syncwarp();
-    };
-    // the weights of stream s are in TMEM, and (first product of an item) its accumulator has been read
-    auto weights = [&](int s, bool first) {
-      if (!warp_wait(&sm.p_ready[s], pn[s]++ & 1, ctl)) return false;
-      if (first) {
-        if (on[s] > 0 && !warp_wait(&sm.o_free[s], (on[s] - 1) & 1, ctl)) return false;
-        ++on[s];
-      }
-      return true;
-    };
-    bool ok = true;
-    while (ok && walk.next(p, sm.pre, it)) {
-      if (it.split) {
-        const int nt = it.t1 - it.t0;
-        for (int l = 0; ok && l < min(2, nt); ++l) {
-          ok = ring(rn) && (l > 0 || warp_wait(&sm.q_full[0], qn[0]++ & 1, ctl));
-          if (!ok) break;
-          qk(l, 0, rn);
-          release(rn++);
+        tc_fence_after();
+        if (lane == 0) {
+  #pragma unroll
+          for (int x = 0; x < 4; ++x) mma_bf16_ts(o_t[s], s_t[s] + 8 * x, b + x * 128, kIdPV, acc || x > 0);
         }
-        for (int i = 0; ok && i < nt; ++i) {
-          const int s = i & 1;
-          const uint32_t vk = rn++;
-          ok = weights(s, i < 2) && ring_v(vk, it, it.t0 + i);
-          if (!ok) break;
-          pv(s, vk, i >= 2);
-          release(vk);
-          if (i + 2 < nt) {
-            ok = ring(rn);
+        __syncwarp();
+        if (!warp_wait(&sm.p_ready[s], (pn[s] - 1) & 1, ctl)) return false;
+        tc_fence_after();
+        if (lane == 0) {
+  #pragma unroll
+          for (int x = 4; x < 8; ++x) mma_bf16_ts(o_t[s], s_t[s] + 8 * x, b + x * 128, kIdPV, 1u);
+          tc_commit(smem_addr(&sm.pv_done[s]));
+        }
+        __syncwarp();
+        return true;
+      };
+      auto release = [&](uint32_t k) {
+        if (lane == 0) tc_commit(smem_addr(&sm.kv_empty[k % S]));
+        __syncwarp();
+      };
+      // half of the weights of stream s are in TMEM, and (first product of an item) its accumulator has been read
+      auto weights = [&](int s, bool first) {
+        if (!warp_wait(&sm.p_half[s], pn[s]++ & 1, ctl)) return false;
+        if (first) {
+          if (on[s] > 0 && !warp_wait(&sm.o_free[s], (on[s] - 1) & 1, ctl)) return false;
+          ++on[s];
+        }
+        return true;
+      };
+      bool ok = true;
+      for (int k = 0; ok && next_item(k); ++k) {
+        if (it.split) {
+          const int nt = it.t1 - it.t0;
+          for (int l = 0; ok && l < min(2, nt); ++l) {
+            ok = ring(rn) && (l > 0 || warp_wait(&sm.q_full[0], qn[0]++ & 1, ctl));
             if (!ok) break;
-            qk(s, 0, rn);
+            qk(l, 0, rn);
             release(rn++);
           }
-        }
-      } else {
-        ok = ring(rn);
-        for (int s = 0; ok && s < 2; ++s) {
-          if (it.end[s] <= it.t0) continue;
-          ok = warp_wait(&sm.q_full[s], qn[s]++ & 1, ctl);
-          if (ok) qk(s, s, rn);
-        }
-        if (ok) release(rn++);
-        for (int j = it.t0; ok && j < it.t1; ++j) {
-          const uint32_t vk = rn++, kk = rn;
-          const bool more = j + 1 < it.t1;
-          if (more) ++rn;
-          bool have_v = false, have_k = false;
-          for (int s = 0; ok && s < 2; ++s) {
-            if (j >= it.end[s]) continue;
-            ok = weights(s, j == it.t0) && (have_v || ring_v(vk, it, j));
-            have_v = true;
+          for (int i = 0; ok && i < nt; ++i) {
+            const int s = i & 1;
+            const uint32_t vk = rn++;
+            ok = weights(s, i < 2) && ring_v(vk, it, it.t0 + i) && pv(s, vk, i >= 2);
             if (!ok) break;
-            pv(s, vk, j > it.t0);
-            if (j + 1 < it.end[s]) {
-              ok = have_k || ring(kk);
-              have_k = true;
-              if (ok) qk(s, s, kk);
+            release(vk);
+            if (i + 2 < nt) {
+              ok = ring(rn);
+              if (!ok) break;
+              qk(s, 0, rn);
+              release(rn++);
             }
           }
-          if (!ok) break;
-          release(vk);
-          if (more) release(kk);
-        }
-      }
-    }
-    // every MMA has completed before the CTA leaves its shared memory and TMEM
-    if (lane == 0) {
-      tc_commit(smem_addr(&sm.mma_done));
-      drain(&sm.mma_done, 0, p.timeout_ns);
-    }
-    __syncwarp();
-  } else if (warp == 10) {
-    // -------------------------------------------------------------- guard
-    // A weight of zero times a NaN is a NaN: before a v tile that not every
-    // row sees in full is multiplied, its rows that no row sees are zeroed,
-    // and a row that only some see is replaced by zeros if it holds a NaN or
-    // an infinity, and noted: who sees it adds it at the end.
-    uint32_t n = 0, issued = 0;
-    int k = 0;
-    bool ok = true;
-    while (ok && walk.next(p, sm.pre, it)) {
-      if (k >= 2) ok = warp_wait(&sm.item_done[k & 1], ((k >> 1) - 1) & 1, ctl);
-      if (!ok) break;
-      if (lane < 12) (&sm.poison[k & 1][0][0])[lane] = 0;
-      __syncwarp();
-      const int nt = it.t1 - it.t0, lead = min(it.split ? 2 : 1, nt);
-      const int g0 = first_guarded<TREE>(it);
-      for (int j = g0; ok && j < it.t1; ++j) {
-        if (!guarded<TREE>(it, j)) continue;
-        const int i = j - it.t0;
-        const uint32_t at = n + lead + i + min(i, nt - lead), slot = at % S;  // the v tile's place in the ring
-        // (once the load is issued, the slot's earlier phases are over)
-        ok = warp_wait(&sm.v_issued[slot], (issued >> slot) & 1, ctl) &&
-             warp_wait(&sm.kv_full[slot], (at / S) & 1, ctl);
-        if (!ok) break;
-        issued ^= 1u << slot;
-        const uint32_t tile = kv_smem + slot * C::kTile;
-        const int valid = v_valid<TREE>(it, j), shared = v_shared<TREE>(it, j);
-        for (int r = shared + lane; r < kKeys; r += 32) {
-          bool wipe = r >= valid;
-          if (!wipe) {
-            bool bad = false;
-#pragma unroll
-            for (int h = 0; h < C::kHalves; ++h)
-#pragma unroll
-              for (int x = 0; x < 8; ++x) {
-                const uint4 w = ld_shared_v4(tile + h * 16384 + r * 128 + ((x + lane) & 7) * 16);
-                bad |= not_finite2(w.x) || not_finite2(w.y) || not_finite2(w.z) || not_finite2(w.w);
+        } else {
+          ok = ring(rn);
+          for (int s = 0; ok && s < 2; ++s) {
+            if (it.end[s] <= it.t0) continue;
+            ok = warp_wait(&sm.q_full[s], qn[s]++ & 1, ctl);
+            if (ok) qk(s, s, rn);
+          }
+          if (ok) release(rn++);
+          for (int j = it.t0; ok && j < it.t1; ++j) {
+            const uint32_t vk = rn++, kk = rn;
+            const bool more = j + 1 < it.t1;
+            if (more) ++rn;
+            bool have_v = false, have_k = false;
+            for (int s = 0; ok && s < 2; ++s) {
+              if (j >= it.end[s]) continue;
+              ok = weights(s, j == it.t0) && (have_v || ring_v(vk, it, j));
+              have_v = true;
+              ok = ok && pv(s, vk, j > it.t0);
+              if (!ok) break;
+              if (j + 1 < it.end[s]) {
+                ok = have_k || ring(kk);
+                have_k = true;
+                if (ok) qk(s, s, kk);
               }
-            if (bad) atomicOr(&sm.poison[k & 1][j - g0][r >> 5], 1u << (r & 31));
-            wipe = bad;
-          }
-          if (wipe) {
-#pragma unroll
-            for (int h = 0; h < C::kHalves; ++h)
-#pragma unroll
-              for (int x = 0; x < 8; ++x) st_shared_v4(tile + h * 16384 + r * 128 + ((x + lane) & 7) * 16, 0, 0, 0, 0);
+            }
+            if (!ok) break;
+            release(vk);
+            if (more) release(kk);
           }
         }
-        // (a tile that all rows see as far as it goes: only its tail)
-        for (int r = max(valid, 0) + lane; r < min(shared, kKeys); r += 32)
-#pragma unroll
-          for (int h = 0; h < C::kHalves; ++h)
-#pragma unroll
-            for (int x = 0; x < 8; ++x) st_shared_v4(tile + h * 16384 + r * 128 + ((x + lane) & 7) * 16, 0, 0, 0, 0);
-        fence_proxy_async_smem();
-        warp_arrive(&sm.kv_clean[slot], lane);
+        done_item(k);
       }
-      n += 2 * nt;
-      if (ok) warp_arrive(&sm.guard_item[k & 1], lane);
-      ++k;
+      // every MMA has completed before the CTA leaves its shared memory and TMEM
+      if (lane == 0) {
+        tc_commit(smem_addr(&sm.mma_done));
+        drain(&sm.mma_done, 0, p.timeout_ns);
+      }
+      __syncwarp();
+    } else if (warp == 10) {
+      // -------------------------------------------------------------- guard
+      // A weight of zero times a NaN is a NaN: before a v tile that not every
+      // row sees in full is multiplied, its rows that no row sees are zeroed,
+      // and a row that only some see is replaced by zeros if it holds a NaN or
+      // an infinity, and noted: who sees it adds it at the end.
+      // (item k + 2 is only handed out when the softmax is through with item k
+      // and with what is noted of it)
+      uint32_t n = 0, issued = 0;
+      bool ok = true;
+      for (int k = 0; ok && next_item(k); ++k) {
+        if (lane < 12) (&sm.poison[k & 1][0][0])[lane] = 0;
+        __syncwarp();
+        const int nt = it.t1 - it.t0, lead = min(it.split ? 2 : 1, nt);
+        const int g0 = first_guarded<TREE>(it);
+        for (int j = g0; ok && j < it.t1; ++j) {
+          if (!guarded<TREE>(it, j)) continue;
+          const int i = j - it.t0;
+          const uint32_t at = n + lead + i + min(i, nt - lead), slot = at % S;  // the v tile's place in the ring
+          // (once the load is issued, the slot's earlier phases are over)
+          ok = warp_wait(&sm.v_issued[slot], (issued >> slot) & 1, ctl) &&
+               warp_wait(&sm.kv_full[slot], (at / S) & 1, ctl);
+          if (!ok) break;
+          issued ^= 1u << slot;
+          const uint32_t tile = kv_smem + slot * C::kTile;
+          const int valid = v_valid<TREE>(it, j), shared = v_shared<TREE>(it, j);
+          for (int r = shared + lane; r < kKeys; r += 32) {
+            bool wipe = r >= valid;
+            if (!wipe) {
+              bool bad = false;
+  #pragma unroll
+              for (int h = 0; h < C::kHalves; ++h)
+  #pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                  const uint4 w = ld_shared_v4(tile + h * 16384 + r * 128 + ((x + lane) & 7) * 16);
+                  bad |= not_finite2(w.x) || not_finite2(w.y) || not_finite2(w.z) || not_finite2(w.w);
+                }
+              if (bad) atomicOr(&sm.poison[k & 1][j - g0][r >> 5], 1u << (r & 31));
+              wipe = bad;
+            }
+            if (wipe) {
+  #pragma unroll
+              for (int h = 0; h < C::kHalves; ++h)
+  #pragma unroll
+                for (int x = 0; x < 8; ++x) st_shared_v4(tile + h * 16384 + r * 128 + ((x + lane) & 7) * 16, 0, 0, 0, 0);
+            }
+          }
+          // (a tile that all rows see as far as it goes: only its tail)
+          for (int r = max(valid, 0) + lane; r < min(shared, kKeys); r += 32)
+  #pragma unroll
+            for (int h = 0; h < C::kHalves; ++h)
+  #pragma unroll
+              for (int x = 0; x < 8; ++x) st_shared_v4(tile + h * 16384 + r * 128 + ((x + lane) & 7) * 16, 0, 0, 0, 0);
+          fence_proxy_async_smem();
+          warp_arrive(&sm.kv_clean[slot], lane);
+        }
+        n += 2 * nt;
+        if (ok) warp_arrive(&sm.guard_item[k & 1], lane);
+        done_item(k);
+      }
+    } else if (warp == 11) {
+      // -------------------------------------------------------------- items
+      fill_prefix<TREE>(p, sm.pre, 2 * TQ, lane, blockIdx.x == 0);
+      Walk<TREE> walk(sm.pre);
+      bool going_on = false;
+      for (int k = 0;; ++k) {
+        Item w;
+        walk.next(p, sm.pre, TQ, w);
+        if (k >= 2 && !warp_wait(&sm.item_free[k & 1], ((k >> 1) - 1) & 1, ctl)) break;
+        if (lane == 0) sm.items[k & 1] = w;
+        warp_arrive(&sm.item_full[k & 1], lane);
+        if (w.t1 == w.t0) break;
+        if (TREE && w.part == 1) {
+          going_on = true;
+          if (lane == 0) {
+            JoinItem j;
+            j.rows0 = w.cnt[0] * G;
+            j.rows = j.rows0 + w.cnt[1] * G;
+            j.tok = w.a0 + w.r0;
+            j.cnt0 = w.cnt[0];
+            j.head = w.hk * G;
+            j.last = share_owner(share_begin(blockIdx.x + 1, walk.q, walk.r) + w.nct - w.t1, walk.q, walk.r);
+            j.word = w.n;
+            j.ctx = w.ctx;
+            reinterpret_cast<JoinItem *>(p.ws)[blockIdx.x] = j;
+          }
+        }
+      }
+      if (TREE && !going_on && lane == 0) reinterpret_cast<JoinItem *>(p.ws)[blockIdx.x].rows = 0;
     }
-  } else if (warp < 8) {
+  } else {
+    regs_more<kRegsSoftmax>();
     // ------------------------------------------------------------ softmax
     const int st = warp >> 2;                       // stream
     const int row = (warp & 3) * 32 + lane;         // row of the tile
@@ -599,16 +685,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c = p.scale * kLog2e;
     const int rt = row / G, rg = row - rt * G;      // token of the tile, head of the group
     uint32_t cnt = 0, xn = 0;
-    int k = 0;
     bool ok = true;
     if (p.debug_stall) ok = warp_wait(&sm.stall, 0, ctl);
-    while (ok && walk.next(p, sm.pre, it)) {
+    for (int k = 0; ok && next_item(k); ++k) {
       const int tile0 = it.split ? 0 : st;          // which row tile
       const int tok = it.r0 + tile0 * TQ + rt;      // in the sequence
       const bool valid_row = rt < it.cnt[tile0];
       const bool warp_rows = __any_sync(0xFFFFFFFFu, valid_row);
       const int first = it.split ? it.t0 + st : it.t0, step = it.split ? 2 : 1;
       const int last = it.split ? it.t1 : it.end[st];
+      // tiles from here on are not seen in full
+      const int ragged = TREE ? it.ctx / kKeys : (it.r0 + tile0 * TQ + 1) / kKeys;
       unsigned long long word = 0;
       bool any = true;
       if (TREE) {
@@ -622,36 +709,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp_rows) {
           tc_fence_after();
           uint32_t s[4][32];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) tmem_ld32(s_t + x * 32, s[x]);
+          tmem_ld32(s_t, s[0]);
+          tmem_ld32(s_t + 32, s[1]);
           tmem_ld_wait();
-          // what the row does not see
-          if (TREE ? j >= it.ctx / kKeys : (j + 1) * kKeys > it.r0 + tile0 * TQ + 1) {
-            if (TREE && j >= it.nct) {
+          tmem_landed(s[0]);
+          tmem_landed(s[1]);
+          tmem_ld32(s_t + 64, s[2]);
+          tmem_ld32(s_t + 96, s[3]);
+          if (j >= ragged) {
+            // what the row does not see is -inf
+            uint32_t see[4];
+            const int n = TREE ? (j < it.nct ? it.ctx - j * kKeys : 0) : tok + 1 - j * kKeys;
 #pragma unroll
-              for (int x = 0; x < 4; ++x)
+            for (int x = 0; x < 4; ++x)
+              see[x] = n >= 32 * x + 32 ? 0xFFFFFFFFu : n > 32 * x ? (1u << (n - 32 * x)) - 1u : 0u;
+            if (TREE && j >= it.nct) see[0] = (uint32_t)word, see[1] = (uint32_t)(word >> 32);
+            tmem_ld_wait();
+            tmem_landed(s[2]);
+            tmem_landed(s[3]);
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (x >= 2 || !((uint32_t)(word >> (x * 32)) >> e & 1u)) s[x][e] = 0xFF800000u;
-            } else {
-              const int see = (TREE ? it.ctx : tok + 1) - j * kKeys;
+            for (int x = 0; x < 4; ++x)
 #pragma unroll
-              for (int x = 0; x < 4; ++x)
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (x * 32 + e >= see) s[x][e] = 0xFF800000u;
-            }
+              for (int e = 0; e < 32; ++e)
+                if (!(see[x] >> e & 1u)) s[x][e] = 0xFF800000u;
           }
-          float mx = -INFINITY;
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
+          for (int x = 0; x < 4; ++x) {
+            if (x == 2) {
+              tmem_ld_wait();
+              tmem_landed(s[2]);
+              tmem_landed(s[3]);
+            }
 #pragma unroll
-            for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(s[x][e]));
+            for (int e = 0; e < 32; e += 2)
+              mx[e / 2 & 3] = max3(mx[e / 2 & 3], __uint_as_float(s[x][e]), __uint_as_float(s[x][e + 1]));
+          }
+          const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
           if (j == first) {
-            m = mx;
-          } else if (__any_sync(0xFFFFFFFFu, valid_row && (mx - m) * c > kFallBehind)) {
+            m = top;
+          } else if (__any_sync(0xFFFFFFFFu, valid_row && (top - m) * c > kFallBehind)) {
             // the reference has fallen behind: move it, and with it the sum and the accumulator
-            const float mn = fmaxf(m, mx);
+            const float mn = fmaxf(m, top);
             const float f = mn == -INFINITY ? 1.0f : ex2((m - mn) * c);
             l *= f;
             m = mn;
@@ -659,34 +758,53 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             tc_fence_after();
 #pragma unroll 1
-            for (int x = 0; x < D / 32; ++x) {
-              uint32_t o[32];
-              tmem_ld32(o_t + x * 32, o);
+            for (int x = 0; x < D / 16; ++x) {
+              uint32_t o[16];
+              tmem_ld16(o_t + x * 16, o);
               tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st32(o_t + x * 32, o);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st16(o_t + x * 16, o);
             }
           }
-          const float ref = m == -INFINITY ? 0.0f : m * c;
-          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          const float ref = m == -INFINITY ? 0.0f : -m * c;
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            uint32_t w[32];
+          for (int x = 0; x < 4; ++x) {
+            uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float a = ex2(fmaf(__uint_as_float(s[2 * x + e / 16][2 * e % 32]), c, -ref));
-              const float b = ex2(fmaf(__uint_as_float(s[2 * x + e / 16][2 * e % 32 + 1]), c, -ref));
-              sum[e & 3] += a + b;
-              w[e] = pack_bf16x2(a, b);
+            for (int e = 0; e < 32; e += 2) {
+              float a, b;
+              fma2(a, b, __uint_as_float(s[x][e]), __uint_as_float(s[x][e + 1]), c, ref);
+              a = ex2(a);
+              b = ex2(b);
+              w[e / 2] = pack_bf16x2(a, b);
+              s[x][e] = __float_as_uint(a);
+              s[x][e + 1] = __float_as_uint(b);
             }
-            tmem_st32(s_t + x * 32, w);
+            tmem_st16(s_t + x * 16, w);
+            if (x == 1) {
+              tmem_st_wait();
+              tc_fence_before();
+              warp_arrive(&sm.p_half[st], lane);
+            }
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tmem_st_wait();
           tc_fence_before();
+          warp_arrive(&sm.p_ready[st], lane);
+          // the sum, while the weights are multiplied
+          float sum[4] = {l, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              add2(sum[0], sum[1], __uint_as_float(s[x][e]), __uint_as_float(s[x][e + 1]));
+              add2(sum[2], sum[3], __uint_as_float(s[x][e + 2]), __uint_as_float(s[x][e + 3]));
+            }
+          l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        } else {
+          warp_arrive(&sm.p_half[st], lane);
+          warp_arrive(&sm.p_ready[st], lane);
         }
-        warp_arrive(&sm.p_ready[st], lane);
         ++cnt;
       }
       if (!ok) break;
@@ -752,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int tokg = it.a0 + tok, head = it.hk * G + rg;
           float *part = nullptr;
           if (TREE && it.part >= 0)
-            part = p.ws + ((long long)blockIdx.x * 2 + it.part) * C::kSlotFloats + tile0 * (kRowsT * (D + 2));
+            part = p.ws + kJoinFloats + ((long long)blockIdx.x * 2 + it.part) * C::kSlotFloats + tile0 * (kRowsT * (D + 2));
           float inv = 0.0f;
 #pragma unroll 1
           for (int h = 0; ok && h < 2; ++h) {
@@ -785,10 +903,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     o[e] = __float_as_uint(__uint_as_float(o[e]) * fo + y * fx);
                   }
                 }
-                if (part) {
+                if (!valid_row) {
+                } else if (part) {
 #pragma unroll
-                  for (int e = 0; e < 32; ++e) part[(c0 + e) * kRowsT + row] = __uint_as_float(o[e]);
-                } else if (valid_row) {
+                  for (int e = 0; e < 32; e += 4)
+                    *reinterpret_cast<uint4 *>(part + row * D + c0 + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                } else {
                   uint16_t *out = p.out.ptr + (long long)tokg * p.out.tok + head * p.out.head + c0;
 #pragma unroll
                   for (int e = 0; e < 32; e += 8) {
@@ -807,7 +927,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               ++xn;
             }
           }
-          if (part) {
+          if (part && valid_row) {
             part[D * kRowsT + row] = m;
             part[(D + 1) * kRowsT + row] = l;
           }
@@ -820,8 +940,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();  // the exchange space is a TMA target again
         warp_arrive(&sm.q_empty[1], lane);
       }
-      warp_arrive(&sm.item_done[k & 1], lane);
-      ++k;
+      done_item(k);
     }
   }
 
@@ -833,63 +952,64 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the parts of the items that several CTAs shared: CTA c (x) takes the
-// item that starts in its range and goes on, with its parts in the order of
-// the keys; y = 16-column slices.
+// Joins the parts of the items that several CTAs shared, in the order of the
+// keys: block (c, y) takes 16 rows of the item that began in CTA c and went
+// on, a warp a row at a time.
+constexpr int kJoinRows = 16;
 template <int D>
-__global__ void __launch_bounds__(128) attn_join_kernel(const AttnParams p, int ctas) {
+__global__ void __launch_bounds__(128) attn_join_kernel(const AttnParams p) {
   using C = Cfg<D>;
-  __shared__ Prefix pre;
+  constexpr int V = D / 32;  // columns a lane
+  constexpr unsigned kFull = 0xFFFFFFFFu;
   pdl_trigger();
   pdl_wait();
-  if (threadIdx.x < 32) fill_prefix<true>(p, pre, threadIdx.x, false);
-  __syncthreads();
-  const long long U = pre.units[kBlocks];
-  const int c0 = blockIdx.x;
-  const long long u0 = U * c0 / ctas, u1 = U * (c0 + 1) / ctas;
-  if (u1 <= u0 || u1 >= U) return;
-  long long u = u1 - 1;  // the CTA's last unit
-  int b;
-  const Seq s = find_seq<true>(p, pre, u, b);
-  const int per = s.nct + 1, gh = (int)(u / per), hk = gh % p.Hkv, g = gh / p.Hkv;
-  const int t = (int)(u - (long long)gh * per);
-  if (t == per - 1 || t >= u1 - u0) return;  // it ends here, or began in a CTA before
-  const long long stop = u1 + (per - 1 - t);   // one past the item's last unit
-  const int row = threadIdx.x, G = p.Hq / p.Hkv, rt = row / G, rg = row - rt * G;
+  const int c0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const JoinItem it = reinterpret_cast<const JoinItem *>(p.ws)[c0];
+  const int G = p.Hq / p.Hkv, parts = it.last - c0 + 1;
   const float c = p.scale * kLog2e;
-  for (int tile = 0; tile < 2; ++tile) {
-    const int node = (2 * g + tile) * s.tq + rt;
-    if (rt >= s.tq || node >= s.n) continue;
-    auto slot = [&](int cta) {
-      return p.ws + ((long long)cta * 2 + (cta == c0 ? 1 : 0)) * C::kSlotFloats + tile * (kRowsT * (D + 2)) + row;
+  for (int i = warp; i < kJoinRows; i += 4) {
+    const int r = blockIdx.y * kJoinRows + i;
+    if (r >= it.rows) return;
+    const int tile = r >= it.rows0, row = r - tile * it.rows0;
+    const int rt = row / G, node = it.tok + tile * it.cnt0 + rt, head = it.head + row - rt * G;
+    auto slot = [&](int k) {
+      return p.ws + kJoinFloats + ((long long)(c0 + k) * 2 + (k == 0 ? 1 : 0)) * C::kSlotFloats + tile * (kRowsT * (D + 2));
     };
-    // (fewer units than CTAs: some ranges are empty)
-    auto holds = [&](int cta) { return U * (cta + 1) / ctas > U * cta / ctas; };
     float m = -INFINITY;
-    for (int cta = c0; U * cta / ctas < stop; ++cta)
-      if (holds(cta)) m = fmaxf(m, __ldcg(slot(cta) + D * kRowsT));
-    float l = 0.0f, o[16] = {};
-    for (int cta = c0; U * cta / ctas < stop; ++cta) {
-      if (!holds(cta)) continue;
-      const float *q = slot(cta);
-      const float mi = __ldcg(q + D * kRowsT);
-      const float f = mi == -INFINITY ? 0.0f : ex2((mi - m) * c);
-      l += f * __ldcg(q + (D + 1) * kRowsT);
+    for (int k = lane; k < parts; k += 32) m = fmaxf(m, __ldcg(slot(k) + D * kRowsT + row));
 #pragma unroll
-      for (int e = 0; e < 16; ++e) o[e] += f * __ldcg(q + (blockIdx.y * 16 + e) * kRowsT);
+    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, x));
+    float l = 0.0f, o[V] = {};
+    for (int k0 = 0; k0 < parts; k0 += 32) {
+      const int n = min(32, parts - k0);
+      float f = 0.0f, lk = 0.0f;
+      if (lane < n) {
+        const float *q = slot(k0 + lane) + D * kRowsT + row;
+        const float mk = __ldcg(q);
+        f = mk == -INFINITY ? 0.0f : ex2((mk - m) * c);
+        lk = f * __ldcg(q + kRowsT);
+      }
+#pragma unroll 8
+      for (int k = 0; k < n; ++k) {
+        const float fk = __shfl_sync(kFull, f, k);
+        l += __shfl_sync(kFull, lk, k);
+        const float *q = slot(k0 + k) + row * D + lane * V;
+        if (V == 4) {
+          const float4 y = __ldcg(reinterpret_cast<const float4 *>(q));
+          o[0] += fk * y.x, o[1] += fk * y.y, o[2 % V] += fk * y.z, o[3 % V] += fk * y.w;
+        } else {
+          const float2 y = __ldcg(reinterpret_cast<const float2 *>(q));
+          o[0] += fk * y.x, o[1] += fk * y.y;
+        }
+      }
     }
-    const unsigned long long word = p.mask[s.a0 + node] & (s.n >= 64 ? ~0ull : (1ull << s.n) - 1ull);
-    const bool any = s.ctx > 0 || word != 0ull;
+    const unsigned long long word = p.mask[node] & (it.word >= 64 ? ~0ull : (1ull << it.word) - 1ull);
+    const bool any = it.ctx > 0 || word != 0ull;
     const float inv = 1.0f / l;
-    uint16_t *out = p.out.ptr + (long long)(s.a0 + node) * p.out.tok + (hk * G + rg) * p.out.head + blockIdx.y * 16;
+    uint16_t *out = p.out.ptr + (long long)node * p.out.tok + head * p.out.head + lane * V;
 #pragma unroll
-    for (int e = 0; e < 16; e += 8) {
-      float y[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = any ? o[e + i] * inv : 0.0f;
-      *reinterpret_cast<uint4 *>(out + e) = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
-                                                       pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
-    }
+    for (int e = 0; e < V; e += 2)
+      reinterpret_cast<uint32_t *>(out)[e / 2] = any ? pack_bf16x2(o[e] * inv, o[e + 1] * inv) : 0u;
   }
 }
 
@@ -941,6 +1061,10 @@ cudaError_t launch_t(const AttnParams &p, int sm_count, cudaStream_t stream) {
   if (!once.done(dev)) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
+    // the warpgroups' register shares must be what the launch brings
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
+    if (fa.numRegs != kRegs) return cudaErrorInvalidConfiguration;
     once.set(dev);
   }
   const int G = p.Hq / p.Hkv, TQ = kRowsT / G;
@@ -951,7 +1075,7 @@ cudaError_t launch_t(const AttnParams &p, int sm_count, cudaStream_t stream) {
   if (!heads_map(&q, p.q, p.Hq, p.T, D, G, TQ) || !heads_map(&k, p.k, p.Hkv, p.T, D, 1, rows) ||
       !heads_map(&v, p.v, p.Hkv, p.T, D, 1, rows))
     return cudaErrorInvalidValue;
-  long long ctas = sm_count;
+  long long ctas = sm_count < 256 ? sm_count : 256;
   if (TREE) {
     const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)p.Hkv, (cuuint64_t)p.cache.page_size,
                                 (cuuint64_t)p.cache.pages};
@@ -969,9 +1093,9 @@ cudaError_t launch_t(const AttnParams &p, int sm_count, cudaStream_t stream) {
   attach_pdl(cfg, attr);
   e = cudaLaunchKernelEx(&cfg, kern, q, k, v, kc, vc, p);
   if (TREE && e == cudaSuccess) {
-    cudaLaunchConfig_t jc = pdl_config(dim3((unsigned)ctas, D / 16), dim3(128), 0, stream);
+    cudaLaunchConfig_t jc = pdl_config(dim3((unsigned)ctas, 2 * kRowsT / kJoinRows), dim3(128), 0, stream);
     attach_pdl(jc, attr);
-    e = cudaLaunchKernelEx(&jc, attn_join_kernel<D>, p, (int)ctas);
+    e = cudaLaunchKernelEx(&jc, attn_join_kernel<D>, p);
   }
   return e;
 }
@@ -986,7 +1110,7 @@ cudaError_t launch_attn_tree(const AttnParams &p, int sm_count, cudaStream_t str
 }
 size_t attn_tree_ws_bytes(int D, int sm_count) {
   const long long f = D == 64 ? Cfg<64>::kSlotFloats : Cfg<128>::kSlotFloats;
-  return (size_t)(2 * f * sm_count) * sizeof(float);
+  return (size_t)(kJoinFloats + 2 * f * (sm_count < 256 ? sm_count : 256)) * sizeof(float);
 }
 
 }  // namespace mxg
