@@ -281,7 +281,7 @@ __device__ __forceinline__ int first_guarded(const Item &it) {
   return max(j, it.t0);
 }
 
-constexpr int kItemReaders = 11;  // warps 0 to 10
+constexpr int kItemReaders = 11;  // warps 0 to 10, an arrival each
 
 template <int D>
 struct Smem {
@@ -436,7 +436,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       for (int k = 0; ok && next_item(k); ++k) {
         ok = load_kv(it, it.t0, false);
-        for (int s = 0; ok && s < 2; ++s) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (!ok) break;
           const bool load = it.split ? s == 0 : it.end[s] > it.t0;
           if (!load && !it.split) continue;
           if (nq[s] > 0) ok = warp_wait(&sm.q_empty[s], (nq[s] - 1) & 1, ctl);
@@ -463,110 +465,136 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int s = 0; s < 2; ++s)
         if (ql[s] > 0) drain(&sm.q_full[s], (ql[s] - 1) & 1, p.timeout_ns);
     } else if (warp == 8) {
-      // --------------------------------------------------------------- MMAs
-      uint32_t rn = 0, qn[2] = {0, 0}, pn[2] = {0, 0}, on[2] = {0, 0}, clean = 0;
+      // ------------------------------------------------------------- MMAs
+      // One elected lane issues them, but the whole warp takes every turn and
+      // the operands are warp-uniform values: they then live in uniform
+      // registers.  Held in ordinary ones, as in a single-lane loop, each MMA
+      // cost a dozen instructions that compete with the softmax warps for
+      // issue slots: 102 cycles an MMA of 128 x 128 x 16 instead of 64.
+      const bool el = elect_one();
+      const uint32_t tm = uniform(tmem), qb = uniform(q_smem), kb = uniform(kv_smem);
+      uint32_t rn = 0;                                   // tiles of the ring used so far
+      uint32_t q_ph = 0, p_ph = 0, o_ph = 0, clean = 0;  // phases, a bit for each stream (slot)
+      uint32_t started = 0;
       constexpr uint32_t kIdQK = idesc_bf16(128, kKeys, false), kIdPV = idesc_bf16(128, D, true);
-      const uint32_t s_t[2] = {tmem, tmem + 128}, o_t[2] = {tmem + 256, tmem + 384};
-      auto ring = [&](uint32_t k) { return warp_wait(&sm.kv_full[k % S], (k / S) & 1, ctl); };
-      auto ring_v = [&](uint32_t k, const Item &i, int j) {
+      auto wait = [&](uint64_t *bar, uint32_t parity) { return warp_wait(bar, parity, ctl); };
+      auto ring = [&](uint32_t k) { return wait(&sm.kv_full[k % S], (k / S) & 1); };
+      auto ring_v = [&](uint32_t k, int j) {
         if (!ring(k)) return false;
-        if (guarded<TREE>(i, j)) {
+        if (guarded<TREE>(it, j)) {
           const uint32_t slot = k % S;
-          if (!warp_wait(&sm.kv_clean[slot], (clean >> slot) & 1, ctl)) return false;
+          if (!wait(&sm.kv_clean[slot], (clean >> slot) & 1)) return false;
           clean ^= 1u << slot;
         }
         return true;
       };
+      auto q_loaded = [&](int s) {
+        const bool r = wait(&sm.q_full[s], (q_ph >> s) & 1);
+        q_ph ^= 1u << s;
+        return r;
+      };
       auto qk = [&](int s, int qs, uint32_t k) {  // scores of stream s = Q tile qs . K^T
+        const uint64_t a = sdesc_kmajor_sw128(qb + qs * C::kTile);
+        const uint64_t b = sdesc_kmajor_sw128(kb + uniform(k % S) * C::kTile);
         tc_fence_after();
-        if (lane == 0) {
-          const uint64_t a = sdesc_kmajor_sw128(q_smem + qs * C::kTile);
-          const uint64_t b = sdesc_kmajor_sw128(kv_smem + (k % S) * C::kTile);
-  #pragma unroll
+        if (el) {
+#pragma unroll
           for (int h = 0; h < C::kHalves; ++h)
-  #pragma unroll
+#pragma unroll
             for (int x = 0; x < 4; ++x)
-              mma_bf16_ss(s_t[s], a + h * 1024 + x * 2, b + h * 1024 + x * 2, kIdQK, (h | x) != 0);
+              mma_bf16_ss(tm + s * 128, a + h * 1024 + x * 2, b + h * 1024 + x * 2, kIdQK, (h | x) != 0);
           tc_commit(smem_addr(&sm.s_full[s]));
         }
         __syncwarp();
       };
       // accumulator of stream s (+)= P . V, for the first half of the keys as
-      // soon as their weights are there
-      auto pv = [&](int s, uint32_t k, bool acc) {
-        const uint64_t b = sdesc_mnmajor_sw128(kv_smem + (k % S) * C::kTile, 16384);
+      // soon as their weights are there; before an item's first product the
+      // accumulator has been read
+      auto pv = [&](int s, uint32_t k, int j, bool have_v, bool acc) {
+        const uint32_t ph = (p_ph >> s) & 1;
+        p_ph ^= 1u << s;
+        if (!wait(&sm.p_half[s], ph)) return false;
+        if (!acc && (started >> s & 1)) {
+          if (!wait(&sm.o_free[s], (o_ph >> s) & 1)) return false;
+          o_ph ^= 1u << s;
+        }
+        started |= 1u << s;
+        if (!have_v && !ring_v(k, j)) return false;
+        const uint64_t b = sdesc_mnmajor_sw128(kb + uniform(k % S) * C::kTile, 16384);
+        const uint32_t o = tm + 256 + s * 128, w = tm + s * 128, first = uniform(acc ? 1u : 0u);
         tc_fence_after();
-        if (lane == 0) {
-  #pragma unroll
-          for (int x = 0; x < 4; ++x) mma_bf16_ts(o_t[s], s_t[s] + 8 * x, b + x * 128, kIdPV, acc || x > 0);
+        if (el) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) mma_bf16_ts(o, w + 8 * x, b + x * 128, kIdPV, x > 0 ? 1u : first);
         }
         __syncwarp();
-        if (!warp_wait(&sm.p_ready[s], (pn[s] - 1) & 1, ctl)) return false;
+        if (!wait(&sm.p_ready[s], ph)) return false;
         tc_fence_after();
-        if (lane == 0) {
-  #pragma unroll
-          for (int x = 4; x < 8; ++x) mma_bf16_ts(o_t[s], s_t[s] + 8 * x, b + x * 128, kIdPV, 1u);
+        if (el) {
+#pragma unroll
+          for (int x = 4; x < 8; ++x) mma_bf16_ts(o, w + 8 * x, b + x * 128, kIdPV, 1u);
           tc_commit(smem_addr(&sm.pv_done[s]));
         }
         __syncwarp();
         return true;
       };
       auto release = [&](uint32_t k) {
-        if (lane == 0) tc_commit(smem_addr(&sm.kv_empty[k % S]));
+        if (el) tc_commit(smem_addr(&sm.kv_empty[k % S]));
         __syncwarp();
-      };
-      // half of the weights of stream s are in TMEM, and (first product of an item) its accumulator has been read
-      auto weights = [&](int s, bool first) {
-        if (!warp_wait(&sm.p_half[s], pn[s]++ & 1, ctl)) return false;
-        if (first) {
-          if (on[s] > 0 && !warp_wait(&sm.o_free[s], (on[s] - 1) & 1, ctl)) return false;
-          ++on[s];
-        }
-        return true;
       };
       bool ok = true;
       for (int k = 0; ok && next_item(k); ++k) {
-        if (it.split) {
-          const int nt = it.t1 - it.t0;
-          for (int l = 0; ok && l < min(2, nt); ++l) {
-            ok = ring(rn) && (l > 0 || warp_wait(&sm.q_full[0], qn[0]++ & 1, ctl));
+        const int t0 = (int)uniform(it.t0), t1 = (int)uniform(it.t1);
+        const int end[2] = {(int)uniform(it.end[0]), (int)uniform(it.end[1])};
+        done_item(k);
+        if (uniform(it.split)) {
+          const int nt = t1 - t0;
+          ok = ring(rn) && q_loaded(0);
+          if (!ok) break;
+          qk(0, 0, rn);
+          release(rn++);
+          if (nt > 1) {
+            ok = ring(rn);
             if (!ok) break;
-            qk(l, 0, rn);
+            qk(1, 0, rn);
             release(rn++);
           }
-          for (int i = 0; ok && i < nt; ++i) {
-            const int s = i & 1;
-            const uint32_t vk = rn++;
-            ok = weights(s, i < 2) && ring_v(vk, it, it.t0 + i) && pv(s, vk, i >= 2);
-            if (!ok) break;
-            release(vk);
-            if (i + 2 < nt) {
-              ok = ring(rn);
+          for (int i = 0; ok && i < nt; i += 2) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+              if (!ok || i + s >= nt) break;
+              const uint32_t vk = rn++;
+              ok = pv(s, vk, t0 + i + s, false, i > 0);
               if (!ok) break;
-              qk(s, 0, rn);
-              release(rn++);
+              if (i + s + 2 < nt) {
+                ok = ring(rn);
+                if (!ok) break;
+                qk(s, 0, rn);
+                release(rn++);
+              }
+              release(vk);
             }
           }
         } else {
           ok = ring(rn);
-          for (int s = 0; ok && s < 2; ++s) {
-            if (it.end[s] <= it.t0) continue;
-            ok = warp_wait(&sm.q_full[s], qn[s]++ & 1, ctl);
-            if (ok) qk(s, s, rn);
-          }
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+            if (ok && end[s] > t0) {
+              ok = q_loaded(s);
+              if (ok) qk(s, s, rn);
+            }
           if (ok) release(rn++);
-          for (int j = it.t0; ok && j < it.t1; ++j) {
+          for (int j = t0; ok && j < t1; ++j) {
             const uint32_t vk = rn++, kk = rn;
-            const bool more = j + 1 < it.t1;
+            const bool more = j + 1 < t1;
             if (more) ++rn;
             bool have_v = false, have_k = false;
-            for (int s = 0; ok && s < 2; ++s) {
-              if (j >= it.end[s]) continue;
-              ok = weights(s, j == it.t0) && (have_v || ring_v(vk, it, j));
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+              if (!ok || j >= end[s]) continue;
+              ok = pv(s, vk, j, have_v, j > t0);
               have_v = true;
-              ok = ok && pv(s, vk, j > it.t0);
-              if (!ok) break;
-              if (j + 1 < it.end[s]) {
+              if (ok && j + 1 < end[s]) {
                 ok = have_k || ring(kk);
                 have_k = true;
                 if (ok) qk(s, s, kk);
@@ -577,10 +605,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (more) release(kk);
           }
         }
-        done_item(k);
       }
       // every MMA has completed before the CTA leaves its shared memory and TMEM
-      if (lane == 0) {
+      if (el) {
         tc_commit(smem_addr(&sm.mma_done));
         drain(&sm.mma_done, 0, p.timeout_ns);
       }
@@ -690,10 +717,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; ok && next_item(k); ++k) {
       const int tile0 = it.split ? 0 : st;          // which row tile
       const int tok = it.r0 + tile0 * TQ + rt;      // in the sequence
-      const bool valid_row = rt < it.cnt[tile0];
+      const bool valid_row = rt < (tile0 ? it.cnt[1] : it.cnt[0]);
       const bool warp_rows = __any_sync(0xFFFFFFFFu, valid_row);
       const int first = it.split ? it.t0 + st : it.t0, step = it.split ? 2 : 1;
-      const int last = it.split ? it.t1 : it.end[st];
+      const int last = it.split ? it.t1 : st ? it.end[1] : it.end[0];
       // tiles from here on are not seen in full
       const int ragged = TREE ? it.ctx / kKeys : (it.r0 + tile0 * TQ + 1) / kKeys;
       unsigned long long word = 0;

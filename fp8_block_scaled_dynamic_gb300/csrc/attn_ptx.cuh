@@ -93,6 +93,16 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return y;
 }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
+}
+// A value that all lanes hold, in a form the compiler knows to be the same in
+// all of them (it then keeps it in a uniform register).
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
+
 // Registers of the calling warpgroup: all its warps execute the same one.
 template <int N>
 __device__ __forceinline__ void regs_more() {
