@@ -300,7 +300,7 @@ struct Smem {
 };
 
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const WaitCtl &ctl) {
-  const bool ok = mbar_wait(smem_addr(bar), parity, ctl);
+  const bool ok = mbar_wait_quick(smem_addr(bar), parity, ctl);
   return __all_sync(0xFFFFFFFFu, ok);
 }
 // Bounded wait that ignores the abort flag: lets what is in flight land.
@@ -466,143 +466,151 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ql[s] > 0) drain(&sm.q_full[s], (ql[s] - 1) & 1, p.timeout_ns);
     } else if (warp == 8) {
       // ------------------------------------------------------------- MMAs
-      // One elected lane issues them, but the whole warp takes every turn and
-      // the operands are warp-uniform values: they then live in uniform
-      // registers.  Held in ordinary ones, as in a single-lane loop, each MMA
-      // cost a dozen instructions that compete with the softmax warps for
-      // issue slots: 102 cycles an MMA of 128 x 128 x 16 instead of 64.
+      // One elected lane waits and issues, with operands that are warp-uniform
+      // values made by the whole warp: they then live in uniform registers.
+      // Held in ordinary ones, as in a single-lane loop, each MMA cost a dozen
+      // instructions that compete with the softmax warps for issue slots: 102
+      // cycles an MMA of 128 x 128 x 16 instead of 64.
       const bool el = elect_one();
       const uint32_t tm = uniform(tmem), qb = uniform(q_smem), kb = uniform(kv_smem);
       uint32_t rn = 0;                                   // tiles of the ring used so far
       uint32_t q_ph = 0, p_ph = 0, o_ph = 0, clean = 0;  // phases, a bit for each stream (slot)
       uint32_t started = 0;
       constexpr uint32_t kIdQK = idesc_bf16(128, kKeys, false), kIdPV = idesc_bf16(128, D, true);
-      auto wait = [&](uint64_t *bar, uint32_t parity) { return warp_wait(bar, parity, ctl); };
+      auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait_quick(smem_addr(bar), parity, ctl); };
+      // (what follows runs in the elected lane alone)
       auto ring = [&](uint32_t k) { return wait(&sm.kv_full[k % S], (k / S) & 1); };
-      auto ring_v = [&](uint32_t k, int j) {
-        if (!ring(k)) return false;
-        if (guarded<TREE>(it, j)) {
-          const uint32_t slot = k % S;
-          if (!wait(&sm.kv_clean[slot], (clean >> slot) & 1)) return false;
-          clean ^= 1u << slot;
-        }
-        return true;
+      auto ring_v = [&](uint32_t k, bool guard) {
+        return ring(k) && (!guard || wait(&sm.kv_clean[k % S], (clean >> k % S) & 1));
       };
-      auto q_loaded = [&](int s) {
-        const bool r = wait(&sm.q_full[s], (q_ph >> s) & 1);
-        q_ph ^= 1u << s;
-        return r;
-      };
-      auto qk = [&](int s, int qs, uint32_t k) {  // scores of stream s = Q tile qs . K^T
-        const uint64_t a = sdesc_kmajor_sw128(qb + qs * C::kTile);
-        const uint64_t b = sdesc_kmajor_sw128(kb + uniform(k % S) * C::kTile);
+      auto qk = [&](int s, uint64_t a, uint64_t b) {  // scores of stream s = Q . K^T
         tc_fence_after();
-        if (el) {
 #pragma unroll
-          for (int h = 0; h < C::kHalves; ++h)
+        for (int h = 0; h < C::kHalves; ++h)
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-              mma_bf16_ss(tm + s * 128, a + h * 1024 + x * 2, b + h * 1024 + x * 2, kIdQK, (h | x) != 0);
-          tc_commit(smem_addr(&sm.s_full[s]));
-        }
-        __syncwarp();
+          for (int x = 0; x < 4; ++x)
+            mma_bf16_ss(tm + s * 128, a + h * 1024 + x * 2, b + h * 1024 + x * 2, kIdQK, (h | x) != 0);
+        tc_commit(smem_addr(&sm.s_full[s]));
       };
       // accumulator of stream s (+)= P . V, for the first half of the keys as
-      // soon as their weights are there; before an item's first product the
-      // accumulator has been read
-      auto pv = [&](int s, uint32_t k, int j, bool have_v, bool acc) {
-        const uint32_t ph = (p_ph >> s) & 1;
-        p_ph ^= 1u << s;
+      // soon as their weights are there
+      auto pv = [&](int s, uint64_t b, uint32_t acc) {
+        const uint32_t ph = (p_ph >> s) & 1, o = tm + 256 + s * 128, w = tm + s * 128;
         if (!wait(&sm.p_half[s], ph)) return false;
-        if (!acc && (started >> s & 1)) {
-          if (!wait(&sm.o_free[s], (o_ph >> s) & 1)) return false;
-          o_ph ^= 1u << s;
-        }
-        started |= 1u << s;
-        if (!have_v && !ring_v(k, j)) return false;
-        const uint64_t b = sdesc_mnmajor_sw128(kb + uniform(k % S) * C::kTile, 16384);
-        const uint32_t o = tm + 256 + s * 128, w = tm + s * 128, first = uniform(acc ? 1u : 0u);
         tc_fence_after();
-        if (el) {
 #pragma unroll
-          for (int x = 0; x < 4; ++x) mma_bf16_ts(o, w + 8 * x, b + x * 128, kIdPV, x > 0 ? 1u : first);
-        }
-        __syncwarp();
+        for (int x = 0; x < 4; ++x) mma_bf16_ts(o, w + 8 * x, b + x * 128, kIdPV, x > 0 ? 1u : acc);
         if (!wait(&sm.p_ready[s], ph)) return false;
         tc_fence_after();
-        if (el) {
 #pragma unroll
-          for (int x = 4; x < 8; ++x) mma_bf16_ts(o, w + 8 * x, b + x * 128, kIdPV, 1u);
-          tc_commit(smem_addr(&sm.pv_done[s]));
-        }
-        __syncwarp();
+        for (int x = 4; x < 8; ++x) mma_bf16_ts(o, w + 8 * x, b + x * 128, kIdPV, 1u);
+        tc_commit(smem_addr(&sm.pv_done[s]));
         return true;
       };
-      auto release = [&](uint32_t k) {
-        if (el) tc_commit(smem_addr(&sm.kv_empty[k % S]));
-        __syncwarp();
+      auto release = [&](uint32_t k) { tc_commit(smem_addr(&sm.kv_empty[k % S])); };
+      // (the whole warp)
+      auto kdesc = [&](uint32_t k) { return sdesc_kmajor_sw128(kb + uniform(k % S) * C::kTile); };
+      auto vdesc = [&](uint32_t k) { return sdesc_mnmajor_sw128(kb + uniform(k % S) * C::kTile, 16384); };
+      auto all_ok = [&](bool ok) { return __all_sync(0xFFFFFFFFu, ok) != 0; };
+      // before an item's first product into a stream's accumulator the last item's has been read
+      auto o_read = [&](int s) { return !(started >> s & 1) || wait(&sm.o_free[s], (o_ph >> s) & 1); };
+      auto o_took = [&](int s) {
+        o_ph ^= started & (1u << s);
+        started |= 1u << s;
       };
       bool ok = true;
       for (int k = 0; ok && next_item(k); ++k) {
         const int t0 = (int)uniform(it.t0), t1 = (int)uniform(it.t1);
         const int end[2] = {(int)uniform(it.end[0]), (int)uniform(it.end[1])};
+        const uint64_t q[2] = {sdesc_kmajor_sw128(qb), sdesc_kmajor_sw128(qb + C::kTile)};
         done_item(k);
         if (uniform(it.split)) {
+          // tile i of the item is stream i & 1's; K runs two tiles ahead of V
           const int nt = t1 - t0;
-          ok = ring(rn) && q_loaded(0);
-          if (!ok) break;
-          qk(0, 0, rn);
-          release(rn++);
-          if (nt > 1) {
-            ok = ring(rn);
-            if (!ok) break;
-            qk(1, 0, rn);
-            release(rn++);
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            if (!ok || s >= nt) continue;
+            const uint64_t kd = kdesc(rn);
+            if (el) {
+              ok = ring(rn) && (s > 0 || wait(&sm.q_full[0], q_ph & 1));
+              if (ok) {
+                qk(s, q[0], kd);
+                release(rn);
+              }
+            }
+            ok = all_ok(ok);
+            if (s == 0) q_ph ^= 1;
+            ++rn;
           }
           for (int i = 0; ok && i < nt; i += 2) {
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-              if (!ok || i + s >= nt) break;
-              const uint32_t vk = rn++;
-              ok = pv(s, vk, t0 + i + s, false, i > 0);
-              if (!ok) break;
-              if (i + s + 2 < nt) {
-                ok = ring(rn);
-                if (!ok) break;
-                qk(s, 0, rn);
-                release(rn++);
+              if (!ok || i + s >= nt) continue;
+              const bool more = i + s + 2 < nt, guard = guarded<TREE>(it, t0 + i + s);
+              const uint64_t vd = vdesc(rn), kd = kdesc(rn + 1);
+              const uint32_t acc = uniform(i > 0);
+              if (el) {
+                ok = ring_v(rn, guard) && (i > 0 || o_read(s)) && pv(s, vd, acc);
+                if (ok) release(rn);
+                if (ok && more) {
+                  ok = ring(rn + 1);
+                  if (ok) {
+                    qk(s, q[0], kd);
+                    release(rn + 1);
+                  }
+                }
               }
-              release(vk);
+              ok = all_ok(ok);
+              p_ph ^= 1u << s;
+              if (i == 0) o_took(s);
+              if (guard) clean ^= 1u << rn % S;
+              rn += more ? 2 : 1;
             }
           }
         } else {
-          ok = ring(rn);
+          const uint64_t kd0 = kdesc(rn);
+          if (el) {
+            ok = ring(rn);
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+              if (ok && end[s] > t0) {
+                ok = wait(&sm.q_full[s], (q_ph >> s) & 1);
+                if (ok) qk(s, q[s], kd0);
+              }
+            if (ok) release(rn);
+          }
+          ok = all_ok(ok);
 #pragma unroll
           for (int s = 0; s < 2; ++s)
-            if (ok && end[s] > t0) {
-              ok = q_loaded(s);
-              if (ok) qk(s, s, rn);
-            }
-          if (ok) release(rn++);
+            if (end[s] > t0) q_ph ^= 1u << s;
+          ++rn;
           for (int j = t0; ok && j < t1; ++j) {
-            const uint32_t vk = rn++, kk = rn;
-            const bool more = j + 1 < t1;
-            if (more) ++rn;
-            bool have_v = false, have_k = false;
+            const bool more = j + 1 < t1, guard = guarded<TREE>(it, j);
+            const uint64_t vd = vdesc(rn), kd = kdesc(rn + 1);
+            const uint32_t acc = uniform(j > t0);
+            if (el) {
+              ok = ring_v(rn, guard);
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-              if (!ok || j >= end[s]) continue;
-              ok = pv(s, vk, j, have_v, j > t0);
-              have_v = true;
-              if (ok && j + 1 < end[s]) {
-                ok = have_k || ring(kk);
-                have_k = true;
-                if (ok) qk(s, s, kk);
+              for (int s = 0; s < 2; ++s) {
+                if (!ok || j >= end[s]) continue;
+                ok = (j > t0 || o_read(s)) && pv(s, vd, acc);
+                if (ok && j + 1 < end[s]) {
+                  ok = ring(rn + 1);
+                  if (ok) qk(s, q[s], kd);
+                }
               }
+              if (ok) release(rn);
+              if (ok && more) release(rn + 1);
             }
-            if (!ok) break;
-            release(vk);
-            if (more) release(kk);
+            ok = all_ok(ok);
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+              if (j < end[s]) {
+                p_ph ^= 1u << s;
+                if (j == t0) o_took(s);
+              }
+            if (guard) clean ^= 1u << rn % S;
+            rn += more ? 2 : 1;
           }
         }
       }

@@ -62,6 +62,26 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// mbar_wait with the clock read only after a number of failed tries: a read
+// of the global timer takes longer than most of the attention kernels' waits.
+__device__ __forceinline__ bool mbar_wait_quick(uint32_t bar, uint32_t parity, const WaitCtl &ctl) {
+  if (mbar_try_wait(bar, parity)) return true;
+  uint64_t t0 = 0;
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*ctl.abort_flag) return false;
+    const uint64_t t = global_timer_ns();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > ctl.timeout_ns) {
+      *ctl.abort_flag = 1;
+      if (ctl.status) atomicOr(ctl.status, 0x1 /* MXG_DEV_TIMEOUT */);
+      return false;
+    }
+  }
+}
+
 // Ties values a TMEM load has brought to the wait before it: arithmetic on them
 // stays behind it.
 __device__ __forceinline__ void tmem_landed(uint32_t (&r)[32]) {
