@@ -988,11 +988,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the parts of the items that several CTAs shared, in the order of the
-// keys: block (c, y) takes 16 rows of the item that began in CTA c and went
-// on, a warp a row at a time.
-constexpr int kJoinRows = 16;
+// keys: a warp takes one row of the item that began in CTA blockIdx.x and went
+// on.  Latency bounds it: the references and sums of 32 parts come in one load
+// a lane, the parts themselves in batches of 8 loads in flight.
+constexpr int kJoinRows = 8;
 template <int D>
-__global__ void __launch_bounds__(128) attn_join_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(32 * kJoinRows) attn_join_kernel(const AttnParams p) {
   using C = Cfg<D>;
   constexpr int V = D / 32;  // columns a lane
   constexpr unsigned kFull = 0xFFFFFFFFu;
@@ -1000,52 +1001,65 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnParams p) {
   pdl_wait();
   const int c0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const JoinItem it = reinterpret_cast<const JoinItem *>(p.ws)[c0];
+  const int r = blockIdx.y * kJoinRows + warp;
+  if (r >= it.rows) return;
   const int G = p.Hq / p.Hkv, parts = it.last - c0 + 1;
   const float c = p.scale * kLog2e;
-  for (int i = warp; i < kJoinRows; i += 4) {
-    const int r = blockIdx.y * kJoinRows + i;
-    if (r >= it.rows) return;
-    const int tile = r >= it.rows0, row = r - tile * it.rows0;
-    const int rt = row / G, node = it.tok + tile * it.cnt0 + rt, head = it.head + row - rt * G;
-    auto slot = [&](int k) {
-      return p.ws + kJoinFloats + ((long long)(c0 + k) * 2 + (k == 0 ? 1 : 0)) * C::kSlotFloats + tile * (kRowsT * (D + 2));
-    };
-    float m = -INFINITY;
-    for (int k = lane; k < parts; k += 32) m = fmaxf(m, __ldcg(slot(k) + D * kRowsT + row));
+  const int tile = r >= it.rows0, row = r - tile * it.rows0;
+  const int rt = row / G, node = it.tok + tile * it.cnt0 + rt, head = it.head + row - rt * G;
+  const unsigned long long word = p.mask[node] & (it.word >= 64 ? ~0ull : (1ull << it.word) - 1ull);
+  // CTA c0's part is in its second slot, the others' in their first
+  const float *base = p.ws + kJoinFloats + (long long)c0 * 2 * C::kSlotFloats + tile * (kRowsT * (D + 2));
+  auto slot = [&](int k) { return base + (long long)(k == 0 ? 1 : 2 * k) * C::kSlotFloats; };
+  float m = -INFINITY, l = 0.0f, o[V] = {};
+  for (int k0 = 0; k0 < parts; k0 += 32) {
+    const int n = min(32, parts - k0);
+    float mk = -INFINITY, lk = 0.0f;
+    if (lane < n) {
+      const float *q = slot(k0 + lane) + D * kRowsT + row;
+      mk = __ldcg(q);
+      lk = __ldcg(q + kRowsT);
+    }
+    float top = mk;
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, x));
-    float l = 0.0f, o[V] = {};
-    for (int k0 = 0; k0 < parts; k0 += 32) {
-      const int n = min(32, parts - k0);
-      float f = 0.0f, lk = 0.0f;
-      if (lane < n) {
-        const float *q = slot(k0 + lane) + D * kRowsT + row;
-        const float mk = __ldcg(q);
-        f = mk == -INFINITY ? 0.0f : ex2((mk - m) * c);
-        lk = f * __ldcg(q + kRowsT);
-      }
-#pragma unroll 8
-      for (int k = 0; k < n; ++k) {
-        const float fk = __shfl_sync(kFull, f, k);
-        l += __shfl_sync(kFull, lk, k);
-        const float *q = slot(k0 + k) + row * D + lane * V;
+    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
+    const float mn = fmaxf(m, top);
+    const float old = m == -INFINITY ? 0.0f : ex2((m - mn) * c);  // (more than 32 parts)
+    const float f = mk == -INFINITY ? 0.0f : ex2((mk - mn) * c);
+    m = mn;
+    l *= old;
+#pragma unroll
+    for (int e = 0; e < V; ++e) o[e] *= old;
+    lk *= f;
+    for (int k = 0; k < n; k += 8) {
+      float y[8][V];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float *q = slot(k0 + min(k + i, n - 1)) + row * D + lane * V;
         if (V == 4) {
-          const float4 y = __ldcg(reinterpret_cast<const float4 *>(q));
-          o[0] += fk * y.x, o[1] += fk * y.y, o[2 % V] += fk * y.z, o[3 % V] += fk * y.w;
+          const float4 v = __ldcg(reinterpret_cast<const float4 *>(q));
+          y[i][0] = v.x, y[i][1] = v.y, y[i][2 % V] = v.z, y[i][3 % V] = v.w;
         } else {
-          const float2 y = __ldcg(reinterpret_cast<const float2 *>(q));
-          o[0] += fk * y.x, o[1] += fk * y.y;
+          const float2 v = __ldcg(reinterpret_cast<const float2 *>(q));
+          y[i][0] = v.x, y[i][1] = v.y;
         }
       }
-    }
-    const unsigned long long word = p.mask[node] & (it.word >= 64 ? ~0ull : (1ull << it.word) - 1ull);
-    const bool any = it.ctx > 0 || word != 0ull;
-    const float inv = 1.0f / l;
-    uint16_t *out = p.out.ptr + (long long)node * p.out.tok + head * p.out.head + lane * V;
 #pragma unroll
-    for (int e = 0; e < V; e += 2)
-      reinterpret_cast<uint32_t *>(out)[e / 2] = any ? pack_bf16x2(o[e] * inv, o[e + 1] * inv) : 0u;
+      for (int i = 0; i < 8; ++i) {
+        const float fk = __shfl_sync(kFull, f, k + i), la = __shfl_sync(kFull, lk, k + i);
+        if (k + i >= n) break;
+        l += la;
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = fmaf(fk, y[i][e], o[e]);
+      }
+    }
   }
+  const bool any = it.ctx > 0 || word != 0ull;
+  const float inv = 1.0f / l;
+  uint16_t *out = p.out.ptr + (long long)node * p.out.tok + head * p.out.head + lane * V;
+#pragma unroll
+  for (int e = 0; e < V; e += 2)
+    reinterpret_cast<uint32_t *>(out)[e / 2] = any ? pack_bf16x2(o[e] * inv, o[e + 1] * inv) : 0u;
 }
 
 // ------------------------------------------------------------------- host
@@ -1128,7 +1142,11 @@ cudaError_t launch_t(const AttnParams &p, int sm_count, cudaStream_t stream) {
   attach_pdl(cfg, attr);
   e = cudaLaunchKernelEx(&cfg, kern, q, k, v, kc, vc, p);
   if (TREE && e == cudaSuccess) {
-    cudaLaunchConfig_t jc = pdl_config(dim3((unsigned)ctas, 2 * kRowsT / kJoinRows), dim3(128), 0, stream);
+    // rows that an item can have, 8 a block
+    int rows = (p.T < kAttnMaxNodes ? p.T : kAttnMaxNodes) * G;
+    if (rows > 2 * TQ * G) rows = 2 * TQ * G;
+    cudaLaunchConfig_t jc =
+        pdl_config(dim3((unsigned)ctas, (unsigned)((rows + kJoinRows - 1) / kJoinRows)), dim3(32 * kJoinRows), 0, stream);
     attach_pdl(jc, attr);
     e = cudaLaunchKernelEx(&jc, attn_join_kernel<D>, p);
   }
