@@ -10,10 +10,10 @@
 //
 // Tiles.  The G = Hq / Hkv query heads that share a kv head are rows of one
 // tile: 128 / G tokens x G heads (so a decode step fills rows with heads, and
-// k and v are read once for all of them), against 128 keys.  Two row tiles,
-// or for a single row tile two alternating key tiles, are in flight as two
-// streams, so that the tensor core multiplies for one while the other takes
-// its exponentials.
+// k and v are read once for all of them), against 128 keys.  Two row tiles
+// are in flight as two streams, so that the tensor core multiplies for one
+// while the other takes its exponentials.  A single row tile has its scores
+// doubly buffered instead: the next key tile's are there when one's are done.
 //
 // Warps of a CTA: 0-3 and 4-7 the softmax of stream 0 and 1 (a thread is a
 // row: its 128 scores come from TMEM into registers), 8 issues the MMAs, 9
@@ -181,9 +181,9 @@ struct Item {
   int r0;      // first token (node) of the first row tile, in the sequence
   int cnt[2];  // tokens (nodes) of the two row tiles
   int t0, t1;  // key tiles [t0, t1); t1 == t0: there is no item any more
-  int end[2];  // dual: a stream's tiles are [t0, end)
+  int end[2];  // a row tile's key tiles are [t0, end)
   int ctx, nct;
-  int split;   // one row tile: the streams take alternate key tiles
+  int single;  // one row tile, its scores doubly buffered
   int part;    // -1 = the whole item, else the CTA's partial slot (0: the item began before, 1: it goes on)
 };
 
@@ -253,7 +253,7 @@ struct Walk {
       it.cnt[k] = min(max(s.n - it.r0 - k * tq, 0), tq);
       it.end[k] = it.cnt[k] == 0 ? it.t0 : TREE ? last : (it.r0 + k * tq + it.cnt[k] + kKeys - 1) / kKeys;
     }
-    it.split = TREE && s.n <= tq;
+    it.single = it.cnt[1] == 0;
     if (!TREE) it.t1 = max(it.end[0], it.end[1]);
   }
 };
@@ -289,13 +289,15 @@ struct Smem {
   // (8-byte barriers first)
   uint64_t q_full[2], q_empty[2], kv_full[C::kSlots], kv_empty[C::kSlots];
   uint64_t v_issued[C::kSlots], kv_clean[C::kSlots];  // the guard's
-  uint64_t s_full[2], p_half[2], p_ready[2], pv_done[2], o_free[2];
-  uint64_t item_full[2], item_free[2], guard_item[2], x_ready, x_free, mma_done, stall;
+  // scores, weights and products: of the two streams, then of the two buffers
+  // of a single row tile (each has its own phases, since the second stream's
+  // warps have no part in a single tile)
+  uint64_t s_full[4], p_half[4], p_ready[4], pv_done[4], o_free[2];
+  uint64_t item_full[2], item_free[2], guard_item[2], mma_done, stall;
   uint32_t tmem;
   int abort_flag;
   uint32_t poison[2][3][4];  // rows of the guarded tiles that hold a NaN or an infinity, by item parity
   Item items[2];
-  float xm[kRowsT], xl[kRowsT];
   Prefix pre;
 };
 
@@ -342,14 +344,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&sm.q_full[i]), 1);
       mbar_init(smem_addr(&sm.q_empty[i]), 4);
-      mbar_init(smem_addr(&sm.s_full[i]), 1);
-      mbar_init(smem_addr(&sm.p_half[i]), 4);
-      mbar_init(smem_addr(&sm.p_ready[i]), 4);
-      mbar_init(smem_addr(&sm.pv_done[i]), 1);
       mbar_init(smem_addr(&sm.o_free[i]), 4);
       mbar_init(smem_addr(&sm.guard_item[i]), 1);
       mbar_init(smem_addr(&sm.item_full[i]), 1);
       mbar_init(smem_addr(&sm.item_free[i]), kItemReaders);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_addr(&sm.s_full[i]), 1);
+      mbar_init(smem_addr(&sm.p_half[i]), 4);
+      mbar_init(smem_addr(&sm.p_ready[i]), 4);
+      mbar_init(smem_addr(&sm.pv_done[i]), 1);
     }
     for (int i = 0; i < S; ++i) {
       mbar_init(smem_addr(&sm.kv_full[i]), 1);
@@ -357,8 +361,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_addr(&sm.v_issued[i]), 1);
       mbar_init(smem_addr(&sm.kv_clean[i]), 1);
     }
-    mbar_init(smem_addr(&sm.x_ready), 4);
-    mbar_init(smem_addr(&sm.x_free), 4);
     mbar_init(smem_addr(&sm.mma_done), 1);
     mbar_init(smem_addr(&sm.stall), 1);
     sm.abort_flag = 0;
@@ -396,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_less<kRegsRest>();
     if (warp == 9) {
       // ------------------------------------------------------------- loads
-      uint32_t n = 0, nq[2] = {0, 0}, ql[2] = {0, 0};
+      uint32_t n = 0, nq[2] = {0, 0};
       bool ok = true;
       auto load_kv = [&](const Item &i, int j, bool is_v) {
         const uint32_t slot = n % S;
@@ -438,21 +440,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = load_kv(it, it.t0, false);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          if (!ok) break;
-          const bool load = it.split ? s == 0 : it.end[s] > it.t0;
-          if (!load && !it.split) continue;
+          if (!ok || it.end[s] <= it.t0) continue;
           if (nq[s] > 0) ok = warp_wait(&sm.q_empty[s], (nq[s] - 1) & 1, ctl);
-          ++nq[s];  // (a split item's second tile is the streams' exchange space)
-          if (ok && load) ++ql[s];
-          if (ok && load && lane == 0) {
+          if (!ok) break;
+          ++nq[s];
+          if (lane == 0) {
             const uint32_t bar = smem_addr(&sm.q_full[s]);
             mbar_arrive_expect_tx(bar, (uint32_t)(TQ * G * 128 * C::kHalves));
-  #pragma unroll
+#pragma unroll
             for (int h = 0; h < C::kHalves; ++h)
               tma_load_3d(q_smem + s * C::kTile + h * 16384, &tmQ, h * 64, it.hk * G, it.a0 + it.r0 + s * TQ, bar);
           }
+          __syncwarp();
         }
-        const int lead = it.split ? 2 : 1;
+        const int lead = it.single ? 2 : 1;
         if (ok && lead == 2 && it.t0 + 1 < it.t1) ok = load_kv(it, it.t0 + 1, false);
         for (int j = it.t0; ok && j < it.t1; ++j) {
           ok = load_kv(it, j, true);
@@ -463,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // nothing may land in shared memory once the CTA is gone (a timeout)
       for (uint32_t k = n > S ? n - S : 0; k < n; ++k) drain(&sm.kv_full[k % S], (k / S) & 1, p.timeout_ns);
       for (int s = 0; s < 2; ++s)
-        if (ql[s] > 0) drain(&sm.q_full[s], (ql[s] - 1) & 1, p.timeout_ns);
+        if (nq[s] > 0) drain(&sm.q_full[s], (nq[s] - 1) & 1, p.timeout_ns);
     } else if (warp == 8) {
       // ------------------------------------------------------------- MMAs
       // One elected lane waits and issues, with operands that are warp-uniform
@@ -474,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool el = elect_one();
       const uint32_t tm = uniform(tmem), qb = uniform(q_smem), kb = uniform(kv_smem);
       uint32_t rn = 0;                                   // tiles of the ring used so far
-      uint32_t q_ph = 0, p_ph = 0, o_ph = 0, clean = 0;  // phases, a bit for each stream (slot)
+      uint32_t q_ph = 0, p_ph = 0, o_ph = 0, clean = 0;  // phases, a bit for each stream, buffer or slot
       uint32_t started = 0;
       constexpr uint32_t kIdQK = idesc_bf16(128, kKeys, false), kIdPV = idesc_bf16(128, D, true);
       auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait_quick(smem_addr(bar), parity, ctl); };
@@ -483,28 +484,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto ring_v = [&](uint32_t k, bool guard) {
         return ring(k) && (!guard || wait(&sm.kv_clean[k % S], (clean >> k % S) & 1));
       };
-      auto qk = [&](int s, uint64_t a, uint64_t b) {  // scores of stream s = Q . K^T
+      // scores = Q . K^T; x: the stream, or 2 + the buffer of a single row tile
+      auto qk = [&](int x4, uint64_t a, uint64_t b) {
+        const uint32_t d = tm + (x4 & 1) * 128;
         tc_fence_after();
 #pragma unroll
         for (int h = 0; h < C::kHalves; ++h)
 #pragma unroll
           for (int x = 0; x < 4; ++x)
-            mma_bf16_ss(tm + s * 128, a + h * 1024 + x * 2, b + h * 1024 + x * 2, kIdQK, (h | x) != 0);
-        tc_commit(smem_addr(&sm.s_full[s]));
+            mma_bf16_ss(d, a + h * 1024 + x * 2, b + h * 1024 + x * 2, kIdQK, (h | x) != 0);
+        tc_commit(smem_addr(&sm.s_full[x4]));
       };
-      // accumulator of stream s (+)= P . V, for the first half of the keys as
-      // soon as their weights are there
-      auto pv = [&](int s, uint64_t b, uint32_t acc) {
-        const uint32_t ph = (p_ph >> s) & 1, o = tm + 256 + s * 128, w = tm + s * 128;
-        if (!wait(&sm.p_half[s], ph)) return false;
+      // accumulator (+)= P . V, for the first half of the keys as soon as their
+      // weights are there
+      auto pv = [&](int x4, uint64_t b, uint32_t acc) {
+        const uint32_t ph = (p_ph >> x4) & 1, o = tm + 256 + (x4 == 1 ? 128 : 0), w = tm + (x4 & 1) * 128;
+        if (!wait(&sm.p_half[x4], ph)) return false;
         tc_fence_after();
 #pragma unroll
         for (int x = 0; x < 4; ++x) mma_bf16_ts(o, w + 8 * x, b + x * 128, kIdPV, x > 0 ? 1u : acc);
-        if (!wait(&sm.p_ready[s], ph)) return false;
+        if (!wait(&sm.p_ready[x4], ph)) return false;
         tc_fence_after();
 #pragma unroll
         for (int x = 4; x < 8; ++x) mma_bf16_ts(o, w + 8 * x, b + x * 128, kIdPV, 1u);
-        tc_commit(smem_addr(&sm.pv_done[s]));
+        tc_commit(smem_addr(&sm.pv_done[x4]));
         return true;
       };
       auto release = [&](uint32_t k) { tc_commit(smem_addr(&sm.kv_empty[k % S])); };
@@ -524,8 +527,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int end[2] = {(int)uniform(it.end[0]), (int)uniform(it.end[1])};
         const uint64_t q[2] = {sdesc_kmajor_sw128(qb), sdesc_kmajor_sw128(qb + C::kTile)};
         done_item(k);
-        if (uniform(it.split)) {
-          // tile i of the item is stream i & 1's; K runs two tiles ahead of V
+        if (uniform(it.single)) {
+          // K runs two tiles ahead of V
           const int nt = t1 - t0;
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
@@ -534,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (el) {
               ok = ring(rn) && (s > 0 || wait(&sm.q_full[0], q_ph & 1));
               if (ok) {
-                qk(s, q[0], kd);
+                qk(2 + s, q[0], kd);
                 release(rn);
               }
             }
@@ -548,21 +551,21 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!ok || i + s >= nt) continue;
               const bool more = i + s + 2 < nt, guard = guarded<TREE>(it, t0 + i + s);
               const uint64_t vd = vdesc(rn), kd = kdesc(rn + 1);
-              const uint32_t acc = uniform(i > 0);
+              const uint32_t acc = uniform(i + s > 0);
               if (el) {
-                ok = ring_v(rn, guard) && (i > 0 || o_read(s)) && pv(s, vd, acc);
+                ok = ring_v(rn, guard) && (i + s > 0 || o_read(0)) && pv(2 + s, vd, acc);
                 if (ok) release(rn);
                 if (ok && more) {
                   ok = ring(rn + 1);
                   if (ok) {
-                    qk(s, q[0], kd);
+                    qk(2 + s, q[0], kd);
                     release(rn + 1);
                   }
                 }
               }
               ok = all_ok(ok);
-              p_ph ^= 1u << s;
-              if (i == 0) o_took(s);
+              p_ph ^= 4u << s;
+              if (i + s == 0) o_took(0);
               if (guard) clean ^= 1u << rn % S;
               rn += more ? 2 : 1;
             }
@@ -633,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; ok && next_item(k); ++k) {
         if (lane < 12) (&sm.poison[k & 1][0][0])[lane] = 0;
         __syncwarp();
-        const int nt = it.t1 - it.t0, lead = min(it.split ? 2 : 1, nt);
+        const int nt = it.t1 - it.t0, lead = min(it.single ? 2 : 1, nt);
         const int g0 = first_guarded<TREE>(it);
         for (int j = g0; ok && j < it.t1; ++j) {
           if (!guarded<TREE>(it, j)) continue;
@@ -716,21 +719,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int st = warp >> 2;                       // stream
     const int row = (warp & 3) * 32 + lane;         // row of the tile
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_t = tmem + lanes + st * 128, o_t = tmem + lanes + 256 + st * 128;
+    const uint32_t o_t = tmem + lanes + 256 + st * 128;
     const float c = p.scale * kLog2e;
     const int rt = row / G, rg = row - rt * G;      // token of the tile, head of the group
-    uint32_t cnt = 0, xn = 0;
+    uint32_t ph = 0;  // phases of the streams and buffers, a bit each
     bool ok = true;
     if (p.debug_stall) ok = warp_wait(&sm.stall, 0, ctl);
     for (int k = 0; ok && next_item(k); ++k) {
-      const int tile0 = it.split ? 0 : st;          // which row tile
-      const int tok = it.r0 + tile0 * TQ + rt;      // in the sequence
-      const bool valid_row = rt < (tile0 ? it.cnt[1] : it.cnt[0]);
+      const int tok = it.r0 + st * TQ + rt;  // in the sequence
+      const bool valid_row = rt < (st ? it.cnt[1] : it.cnt[0]);
       const bool warp_rows = __any_sync(0xFFFFFFFFu, valid_row);
-      const int first = it.split ? it.t0 + st : it.t0, step = it.split ? 2 : 1;
-      const int last = it.split ? it.t1 : st ? it.end[1] : it.end[0];
+      const int last = st ? it.end[1] : it.end[0];
       // tiles from here on are not seen in full
-      const int ragged = TREE ? it.ctx / kKeys : (it.r0 + tile0 * TQ + 1) / kKeys;
+      const int ragged = TREE ? it.ctx / kKeys : (it.r0 + st * TQ + 1) / kKeys;
       unsigned long long word = 0;
       bool any = true;
       if (TREE) {
@@ -738,9 +739,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         any = it.ctx > 0 || word != 0ull;
       }
       float m = -INFINITY, l = 0.0f;
-      for (int j = first; j < last; j += step) {
-        ok = warp_wait(&sm.s_full[st], cnt & 1, ctl);
+      uint32_t x4 = it.single ? 3 : st;  // stream, or 2 + buffer
+      for (int j = it.t0; j < last; ++j) {
+        if (it.single) x4 ^= 1;
+        ok = warp_wait(&sm.s_full[x4], (ph >> x4) & 1, ctl);
         if (!ok) break;
+        const uint32_t s_t = tmem + lanes + (x4 & 1) * 128;
         if (warp_rows) {
           tc_fence_after();
           uint32_t s[4][32];
@@ -781,7 +785,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               mx[e / 2 & 3] = max3(mx[e / 2 & 3], __uint_as_float(s[x][e]), __uint_as_float(s[x][e + 1]));
           }
           const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-          if (j == first) {
+          if (j == it.t0) {
             m = top;
           } else if (__any_sync(0xFFFFFFFFu, valid_row && (top - m) * c > kFallBehind)) {
             // the reference has fallen behind: move it, and with it the sum and the accumulator
@@ -789,7 +793,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float f = mn == -INFINITY ? 1.0f : ex2((m - mn) * c);
             l *= f;
             m = mn;
-            ok = warp_wait(&sm.pv_done[st], (cnt - 1) & 1, ctl);
+            const uint32_t prev = it.single ? x4 ^ 1 : x4;  // the last product: one phase back
+            ok = warp_wait(&sm.pv_done[prev], (ph >> prev & 1) ^ 1, ctl);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll 1
@@ -820,12 +825,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (x == 1) {
               tmem_st_wait();
               tc_fence_before();
-              warp_arrive(&sm.p_half[st], lane);
+              warp_arrive(&sm.p_half[x4], lane);
             }
           }
           tmem_st_wait();
           tc_fence_before();
-          warp_arrive(&sm.p_ready[st], lane);
+          warp_arrive(&sm.p_ready[x4], lane);
           // the sum, while the weights are multiplied
           float sum[4] = {l, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -837,20 +842,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
         } else {
-          warp_arrive(&sm.p_half[st], lane);
-          warp_arrive(&sm.p_ready[st], lane);
+          warp_arrive(&sm.p_half[x4], lane);
+          warp_arrive(&sm.p_ready[x4], lane);
         }
-        ++cnt;
+        ph ^= 1u << x4;
       }
       if (!ok) break;
-      const int nt = it.t1 - it.t0;
-      const bool active = first < last, both = it.split && nt > 1;
+      const bool active = it.t0 < last;
       // the q tile has been multiplied for the last time
-      if (it.split ? st == ((nt - 1) & 1) : active) warp_arrive(&sm.q_empty[it.split ? 0 : st], lane);
+      if (active) warp_arrive(&sm.q_empty[st], lane);
       ok = warp_wait(&sm.guard_item[k & 1], (k >> 1) & 1, ctl);
       if (!ok) break;
       if (active) {
-        ok = warp_wait(&sm.pv_done[st], (cnt - 1) & 1, ctl);
+        ok = warp_wait(&sm.pv_done[x4], (ph >> x4 & 1) ^ 1, ctl);
         if (!ok) break;
         tc_fence_after();
         // v rows that the guard has replaced, added by those who see them
@@ -861,7 +865,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int x = 0; x < 12; ++x) {
             uint32_t bits = (&sm.poison[k & 1][0][0])[x];
             const int j = g0 + x / 4;
-            if (it.split && ((j - first) & 1)) continue;  // the other stream's tile
             while (bits) {
               const int r = (x & 3) * 32 + __ffs(bits) - 1;
               bits &= bits - 1;
@@ -876,104 +879,43 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         };
-        float fo = 1.0f, fx = 0.0f;  // this stream's and the other's factor
-        if (both && st == 1) {
-          // hand the second stream's part of the result to the first, through
-          // the unused q tile, D / 2 columns at a time
+        float *part = nullptr;
+        if (TREE && it.part >= 0)
+          part = p.ws + kJoinFloats + ((long long)blockIdx.x * 2 + it.part) * C::kSlotFloats + st * (kRowsT * (D + 2));
+        uint16_t *out = p.out.ptr + (long long)(it.a0 + tok) * p.out.tok + (it.hk * G + rg) * p.out.head;
+        const float inv = 1.0f / l;
+        if (warp_rows) {
 #pragma unroll 1
-          for (int h = 0; ok && h < 2; ++h, ++xn) {
-            if (xn > 0) ok = warp_wait(&sm.x_free, (xn - 1) & 1, ctl);
-            if (!ok) break;
-            if (h == 0) sm.xm[row] = m, sm.xl[row] = l;
-            if (warp_rows) {
-#pragma unroll 1
-              for (int x = 0; x < D / 64; ++x) {
-                const int c0 = h * (D / 2) + x * 32;
-                uint32_t o[32];
-                tmem_ld32(o_t + c0, o);
-                tmem_ld_wait();
-                if (anyp) poisoned(o, c0);
-                const uint32_t at = q_smem + C::kTile + (x * 32 * kRowsT + row) * 4;
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            uint32_t o[32];
+            tmem_ld32(o_t + c0, o);
+            tmem_ld_wait();
+            tmem_landed(o);
+            if (anyp) poisoned(o, c0);
+            if (!valid_row) continue;
+            if (part) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + e * kRowsT * 4), "r"(o[e]) : "memory");
+              for (int e = 0; e < 32; e += 4)
+                *reinterpret_cast<uint4 *>(part + row * D + c0 + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; e += 8) {
+                float y[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = any ? __uint_as_float(o[e + i]) * inv : 0.0f;
+                *reinterpret_cast<uint4 *>(out + c0 + e) =
+                    make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                               pack_bf16x2(y[6], y[7]));
               }
             }
-            warp_arrive(&sm.x_ready, lane);
-          }
-        } else {
-          const int tokg = it.a0 + tok, head = it.hk * G + rg;
-          float *part = nullptr;
-          if (TREE && it.part >= 0)
-            part = p.ws + kJoinFloats + ((long long)blockIdx.x * 2 + it.part) * C::kSlotFloats + tile0 * (kRowsT * (D + 2));
-          float inv = 0.0f;
-#pragma unroll 1
-          for (int h = 0; ok && h < 2; ++h) {
-            if (both) {
-              ok = warp_wait(&sm.x_ready, xn & 1, ctl);
-              if (!ok) break;
-              if (h == 0) {
-                const float m1 = sm.xm[row], l1 = sm.xl[row], mn = fmaxf(m, m1);
-                fo = m == -INFINITY ? 0.0f : ex2((m - mn) * c);
-                fx = m1 == -INFINITY ? 0.0f : ex2((m1 - mn) * c);
-                l = l * fo + l1 * fx;
-                m = mn;
-              }
-            }
-            if (h == 0) inv = any ? 1.0f / l : 0.0f;
-            if (warp_rows) {
-#pragma unroll 1
-              for (int x = 0; x < D / 64; ++x) {
-                const int c0 = h * (D / 2) + x * 32;
-                uint32_t o[32];
-                tmem_ld32(o_t + c0, o);
-                tmem_ld_wait();
-                if (anyp) poisoned(o, c0);
-                if (both) {
-                  const uint32_t at = q_smem + C::kTile + (x * 32 * kRowsT + row) * 4;
-#pragma unroll
-                  for (int e = 0; e < 32; ++e) {
-                    float y;
-                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(y) : "r"(at + e * kRowsT * 4));
-                    o[e] = __float_as_uint(__uint_as_float(o[e]) * fo + y * fx);
-                  }
-                }
-                if (!valid_row) {
-                } else if (part) {
-#pragma unroll
-                  for (int e = 0; e < 32; e += 4)
-                    *reinterpret_cast<uint4 *>(part + row * D + c0 + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                } else {
-                  uint16_t *out = p.out.ptr + (long long)tokg * p.out.tok + head * p.out.head + c0;
-#pragma unroll
-                  for (int e = 0; e < 32; e += 8) {
-                    float y[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) y[i] = any ? __uint_as_float(o[e + i]) * inv : 0.0f;
-                    *reinterpret_cast<uint4 *>(out + e) =
-                        make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                                   pack_bf16x2(y[6], y[7]));
-                  }
-                }
-              }
-            }
-            if (both) {
-              warp_arrive(&sm.x_free, lane);
-              ++xn;
-            }
-          }
-          if (part && valid_row) {
-            part[D * kRowsT + row] = m;
-            part[(D + 1) * kRowsT + row] = l;
           }
         }
-        if (!ok) break;
+        if (part && valid_row) {
+          part[D * kRowsT + row] = m;
+          part[(D + 1) * kRowsT + row] = l;
+        }
         tc_fence_before();
         warp_arrive(&sm.o_free[st], lane);
-      }
-      if (it.split && st == 0) {
-        fence_proxy_async_smem();  // the exchange space is a TMA target again
-        warp_arrive(&sm.q_empty[1], lane);
       }
       done_item(k);
     }
