@@ -204,6 +204,53 @@ __device__ __forceinline__ int share_owner(int u, int q, int r) {
   return u < r * (q + 1) ? u / (q + 1) : r + (u - r * (q + 1)) / q;
 }
 
+// A batch of at most 32 sequences in the registers of one warp, a sequence a
+// lane: no prefix in shared memory, no search (0.8 us less before the first
+// load of a decode step).
+template <bool TREE>
+struct Small {
+  Seq s;
+  int before, total;  // units before this lane's sequence, of all
+  __device__ __forceinline__ void read(const AttnParams &p, int tq2, int lane, bool report) {
+    constexpr unsigned kFull = 0xFFFFFFFFu;
+    Raw r = {0, 0, 0};
+    if (lane < p.B) r = raw_seq<TREE>(p, lane);
+    int running = min(max(r.c0, 0), p.T);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(kFull, running, o);
+      if (lane >= o) running = max(running, x);
+    }
+    running = __shfl_up_sync(kFull, running, 1);
+    if (lane == 0) running = 0;
+    bool bad = false;
+    s = seq_of<TREE>(p, r, tq2, running, &bad);
+    if (lane >= p.B) s.units = 0;
+    int sum = s.units;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(kFull, sum, o);
+      if (lane >= o) sum += x;
+    }
+    before = sum - s.units;
+    total = __shfl_sync(kFull, sum, 31);
+    if (bad && lane < p.B && report && p.status) atomicOr(p.status, kBadIndex);
+  }
+  // the sequence of unit u (u < total), and u's number in it
+  __device__ __forceinline__ Seq find(int &u, int &b) const {
+    constexpr unsigned kFull = 0xFFFFFFFFu;
+    b = __ffs(__ballot_sync(kFull, u >= before && u < before + s.units)) - 1;
+    Seq r;
+    r.a0 = __shfl_sync(kFull, s.a0, b);
+    r.n = __shfl_sync(kFull, s.n, b);
+    r.ctx = __shfl_sync(kFull, s.ctx, b);
+    r.per = __shfl_sync(kFull, s.per, b);
+    r.units = 0;
+    u -= __shfl_sync(kFull, before, b);
+    return r;
+  }
+};
+
 // Walks the items of one CTA.  Prompt: row groups from the last (its keys are
 // the most) to the first, strided over the grid.  Tree: the units are cut into
 // equal ranges over the grid, an item is the part of one row group's key tiles
@@ -211,8 +258,7 @@ __device__ __forceinline__ int share_owner(int u, int q, int r) {
 template <bool TREE>
 struct Walk {
   int cur, end, q, r;
-  __device__ __forceinline__ Walk(const Prefix &pre) {
-    const int U = pre.units[kBlocks];
+  __device__ __forceinline__ Walk(int U) {
     if (TREE) {
       q = U / (int)gridDim.x;
       r = U - q * (int)gridDim.x;
@@ -223,11 +269,12 @@ struct Walk {
       end = U;
     }
   }
-  __device__ __forceinline__ void next(const AttnParams &p, const Prefix &pre, int tq, Item &it) {
+  template <class Find>
+  __device__ __forceinline__ void next(const AttnParams &p, int tq, Item &it, Find find) {
     it.t0 = it.t1 = 0;
     if (cur >= end) return;
     int u = TREE ? cur : end - 1 - cur;
-    const Seq s = find_seq<TREE>(p, pre, 2 * tq, u, it.b);
+    const Seq s = find(u, it.b);
     it.a0 = s.a0;
     it.n = s.n;
     it.ctx = s.ctx;
@@ -685,12 +732,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 11) {
       // -------------------------------------------------------------- items
-      fill_prefix<TREE>(p, sm.pre, 2 * TQ, lane, blockIdx.x == 0);
-      Walk<TREE> walk(sm.pre);
+      const bool few = p.B <= 32;
+      Small<TREE> small;
+      if (few) small.read(p, 2 * TQ, lane, blockIdx.x == 0);
+      else fill_prefix<TREE>(p, sm.pre, 2 * TQ, lane, blockIdx.x == 0);
+      Walk<TREE> walk(few ? small.total : sm.pre.units[kBlocks]);
       bool going_on = false;
       for (int k = 0;; ++k) {
         Item w;
-        walk.next(p, sm.pre, TQ, w);
+        walk.next(p, TQ, w, [&](int &u, int &b) {
+          return few ? small.find(u, b) : find_seq<TREE>(p, sm.pre, 2 * TQ, u, b);
+        });
         if (k >= 2 && !warp_wait(&sm.item_free[k & 1], ((k >> 1) - 1) & 1, ctl)) break;
         if (lane == 0) sm.items[k & 1] = w;
         warp_arrive(&sm.item_full[k & 1], lane);
@@ -849,8 +901,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       const bool active = it.t0 < last;
-      // the q tile has been multiplied for the last time
-      if (active) warp_arrive(&sm.q_empty[st], lane);
       ok = warp_wait(&sm.guard_item[k & 1], (k >> 1) & 1, ctl);
       if (!ok) break;
       if (active) {
@@ -879,41 +929,80 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         };
+        // A thread holds a row, and rows are far apart in memory: the results
+        // go through the q tile (multiplied for the last time; each warp its
+        // own 32 rows, the 16-byte units of row r at unit ^ r), so that a store
+        // writes two whole rows of bf16 (half rows of fp32 parts).  Straight
+        // from the rows' threads, 32 lines a store, this took 5000 cycles.
         float *part = nullptr;
         if (TREE && it.part >= 0)
           part = p.ws + kJoinFloats + ((long long)blockIdx.x * 2 + it.part) * C::kSlotFloats + st * (kRowsT * (D + 2));
-        uint16_t *out = p.out.ptr + (long long)(it.a0 + tok) * p.out.tok + (it.hk * G + rg) * p.out.head;
-        const float inv = 1.0f / l;
+        const float inv = any ? 1.0f / l : 0.0f;
         if (warp_rows) {
+          constexpr int kUnits = D / 8;             // 16-byte units of a staged row
+          constexpr int kRowsStore = 32 / kUnits;   // rows a warp stores at once
+          const uint32_t stage = q_smem + st * C::kTile + (warp & 3) * 32 * kUnits * 16;
+          const uint32_t mine = stage + lane * kUnits * 16;
+          const int unit = lane % kUnits, sub = lane / kUnits;
+          const int rows = __popc(__ballot_sync(0xFFFFFFFFu, valid_row));  // (the first ones)
+          auto store = [&](uint8_t *base) {  // base: this row's first byte
+            __syncwarp();
+#pragma unroll 4
+            for (int r0 = 0; r0 < rows; r0 += kRowsStore) {
+              const int r = r0 + sub;
+              uint8_t *to = reinterpret_cast<uint8_t *>(
+                  __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(base), r));
+              const uint4 v = ld_shared_v4(stage + r * kUnits * 16 + ((unit ^ r) & (kUnits - 1)) * 16);
+              if (to) *reinterpret_cast<uint4 *>(to + unit * 16) = v;
+            }
+            __syncwarp();
+          };
+          if (part) {
 #pragma unroll 1
-          for (int c0 = 0; c0 < D; c0 += 32) {
-            uint32_t o[32];
-            tmem_ld32(o_t + c0, o);
-            tmem_ld_wait();
-            tmem_landed(o);
-            if (anyp) poisoned(o, c0);
-            if (!valid_row) continue;
-            if (part) {
+            for (int h = 0; h < 2; ++h) {
 #pragma unroll
-              for (int e = 0; e < 32; e += 4)
-                *reinterpret_cast<uint4 *>(part + row * D + c0 + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-            } else {
+              for (int x = 0; x < D / 64; ++x) {
+                uint32_t o[32];
+                tmem_ld32(o_t + h * (D / 2) + x * 32, o);
+                tmem_ld_wait();
+                tmem_landed(o);
+                if (anyp) poisoned(o, h * (D / 2) + x * 32);
 #pragma unroll
-              for (int e = 0; e < 32; e += 8) {
-                float y[8];
+                for (int e = 0; e < 8; ++e)
+                  st_shared_v4(mine + (((x * 8 + e) ^ lane) & (kUnits - 1)) * 16, o[4 * e], o[4 * e + 1], o[4 * e + 2],
+                               o[4 * e + 3]);
+              }
+              store(valid_row ? reinterpret_cast<uint8_t *>(part + row * D + h * (D / 2)) : nullptr);
+            }
+            if (valid_row) {
+              part[D * kRowsT + row] = m;
+              part[(D + 1) * kRowsT + row] = l;
+            }
+          } else {
+#pragma unroll 1
+            for (int x = 0; x < D / 32; ++x) {
+              uint32_t o[32];
+              tmem_ld32(o_t + x * 32, o);
+              tmem_ld_wait();
+              tmem_landed(o);
+              if (anyp) poisoned(o, x * 32);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = any ? __uint_as_float(o[e + i]) * inv : 0.0f;
-                *reinterpret_cast<uint4 *>(out + c0 + e) =
-                    make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                               pack_bf16x2(y[6], y[7]));
+              for (int e = 0; e < 4; ++e) {
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float a = __uint_as_float(o[8 * e + 2 * i]) * inv, b = __uint_as_float(o[8 * e + 2 * i + 1]) * inv;
+                  w[i] = any ? pack_bf16x2(a, b) : 0u;
+                }
+                st_shared_v4(mine + (((x * 4 + e) ^ lane) & (kUnits - 1)) * 16, w[0], w[1], w[2], w[3]);
               }
             }
+            uint16_t *out = p.out.ptr + (long long)(it.a0 + tok) * p.out.tok + (it.hk * G + rg) * p.out.head;
+            store(valid_row ? reinterpret_cast<uint8_t *>(out) : nullptr);
           }
         }
-        if (part && valid_row) {
-          part[D * kRowsT + row] = m;
-          part[(D + 1) * kRowsT + row] = l;
-        }
+        fence_proxy_async_smem();  // the q tile is a TMA target again
+        warp_arrive(&sm.q_empty[st], lane);
         tc_fence_before();
         warp_arrive(&sm.o_free[st], lane);
       }
