@@ -251,57 +251,123 @@ struct Small {
   }
 };
 
-// Walks the items of one CTA.  Prompt: row groups from the last (its keys are
-// the most) to the first, strided over the grid.  Tree: the units are cut into
-// equal ranges over the grid, an item is the part of one row group's key tiles
-// that lies in this CTA's range.
+// Walks the items of one CTA.
+// Prompt: row groups from the last (its keys are the most) to the first, dealt
+// over the CTAs there and back, so that who gets the heaviest of one round
+// gets the lightest of the next.
+// Tree: the units are cut into equal ranges over the CTAs, an item is the part
+// of one row group's key tiles that lies in this CTA's range -- or, where that
+// costs at most two tiles a CTA more, every row group's key tiles are cut into
+// equal chunks and a CTA takes one chunk: a second item costs a CTA more than
+// two tiles (its result, the next q).
 template <bool TREE>
 struct Walk {
-  int cur, end, q, r;
-  __device__ __forceinline__ Walk(int U) {
+  int cur, end, q, r;  // tree: this CTA's units, the shares; prompt: the round, the number of items
+  int chunk;           // tree: most key tiles of a chunk, 0: equal ranges
+  __device__ __forceinline__ explicit Walk(int U) : chunk(0) {
     if (TREE) {
       q = U / (int)gridDim.x;
       r = U - q * (int)gridDim.x;
       cur = share_begin(blockIdx.x, q, r);
       end = share_begin(blockIdx.x + 1, q, r);
     } else {
-      cur = blockIdx.x;
+      cur = 0;
       end = U;
+      q = r = 0;
     }
+  }
+  // the chunk length for which all chunks have a CTA, if there is a short one
+  __device__ __forceinline__ void choose_chunk(const Small<true> &b) {
+    const int least = q + (r > 0);
+    if (least == 0) return;
+#pragma unroll
+    for (int i = 2; i >= 0; --i) {
+      const int chunks = b.s.units > 0 ? b.s.units / b.s.per * ((b.s.per + least + i - 1) / (least + i)) : 0;
+      if (__reduce_add_sync(0xFFFFFFFFu, chunks) <= (int)gridDim.x) chunk = least + i;
+    }
+  }
+  // this CTA's only item, a chunk; returns the last CTA of the row group's chunks
+  __device__ __forceinline__ int one_chunk(const AttnParams &p, const Small<true> &b, int tq, Item &it) {
+    constexpr unsigned kFull = 0xFFFFFFFFu;
+    const int lane = threadIdx.x & 31, c = blockIdx.x;
+    const int pieces = (b.s.per + chunk - 1) / chunk;
+    const int mine = b.s.units > 0 ? b.s.units / b.s.per * pieces : 0;
+    int sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(kFull, sum, o);
+      if (lane >= o) sum += x;
+    }
+    const unsigned has = __ballot_sync(kFull, c >= sum - mine && c < sum);
+    it.t0 = it.t1 = 0;
+    cur = end;
+    if (!has) return 0;
+    it.b = __ffs(has) - 1;
+    it.a0 = __shfl_sync(kFull, b.s.a0, it.b);
+    it.n = __shfl_sync(kFull, b.s.n, it.b);
+    it.ctx = __shfl_sync(kFull, b.s.ctx, it.b);
+    const int per = __shfl_sync(kFull, b.s.per, it.b), k = __shfl_sync(kFull, pieces, it.b);
+    const int x = c - __shfl_sync(kFull, sum - mine, it.b), gh = x / k, piece = x - gh * k;
+    const int cut = per / k, rest = per - cut * k;
+    it.t0 = share_begin(piece, cut, rest);
+    it.t1 = share_begin(piece + 1, cut, rest);
+    rows_of(p, tq, gh, per, it);
+    return c + k - 1 - piece;
+  }
+  // tree: kv head and rows of row group x kv head gh, what its end is
+  __device__ __forceinline__ void rows_of(const AttnParams &p, int tq, int gh, int per, Item &it) {
+    const int g = gh / p.Hkv;
+    it.hk = gh - g * p.Hkv;
+    it.nct = per - 1;
+    it.part = it.t0 > 0 ? 0 : it.t1 < per ? 1 : -1;
+    it.r0 = g * 2 * tq;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      it.cnt[k] = min(max(it.n - it.r0 - k * tq, 0), tq);
+      it.end[k] = it.cnt[k] == 0 ? it.t0 : it.t1;
+    }
+    it.single = it.cnt[1] == 0;
   }
   template <class Find>
   __device__ __forceinline__ void next(const AttnParams &p, int tq, Item &it, Find find) {
     it.t0 = it.t1 = 0;
-    if (cur >= end) return;
-    int u = TREE ? cur : end - 1 - cur;
-    const Seq s = find(u, it.b);
-    it.a0 = s.a0;
-    it.n = s.n;
-    it.ctx = s.ctx;
-    it.nct = s.per - 1;
-    int g, last = 0;
     if (TREE) {
+      if (cur >= end) return;
+      int u = cur;
+      const Seq s = find(u, it.b);
+      it.a0 = s.a0;
+      it.n = s.n;
+      it.ctx = s.ctx;
       const int gh = u / s.per;
       it.t0 = u - gh * s.per;
-      g = gh / p.Hkv;
-      it.hk = gh - g * p.Hkv;
-      last = it.t1 = min(s.per, it.t0 + (end - cur));
+      it.t1 = min(s.per, it.t0 + (end - cur));
       cur += it.t1 - it.t0;
-      it.part = it.t0 > 0 ? 0 : it.t1 < s.per ? 1 : -1;
+      rows_of(p, tq, gh, s.per, it);
     } else {
-      g = u / p.Hkv;
+      const int G = gridDim.x, x = cur * G + (cur & 1 ? G - 1 - (int)blockIdx.x : (int)blockIdx.x);
+      if (cur * G >= end) return;
+      ++cur;
+      if (x >= end) {  // (the last round may be there or not)
+        it.t1 = -1;
+        return;
+      }
+      int u = end - 1 - x;
+      const Seq s = find(u, it.b);
+      it.a0 = s.a0;
+      it.n = s.n;
+      it.ctx = it.nct = 0;
+      const int g = u / p.Hkv;
       it.hk = u - g * p.Hkv;
       it.part = -1;
-      cur += gridDim.x;
-    }
-    it.r0 = g * 2 * tq;
+      it.r0 = g * 2 * tq;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      it.cnt[k] = min(max(s.n - it.r0 - k * tq, 0), tq);
-      it.end[k] = it.cnt[k] == 0 ? it.t0 : TREE ? last : (it.r0 + k * tq + it.cnt[k] + kKeys - 1) / kKeys;
+      for (int k = 0; k < 2; ++k) {
+        it.cnt[k] = min(max(s.n - it.r0 - k * tq, 0), tq);
+        it.end[k] = it.cnt[k] == 0 ? 0 : (it.r0 + k * tq + it.cnt[k] + kKeys - 1) / kKeys;
+      }
+      it.single = it.cnt[1] == 0;
+      it.t1 = max(it.end[0], it.end[1]);
     }
-    it.single = it.cnt[1] == 0;
-    if (!TREE) it.t1 = max(it.end[0], it.end[1]);
   }
 };
 
@@ -738,11 +804,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       else fill_prefix<TREE>(p, sm.pre, 2 * TQ, lane, blockIdx.x == 0);
       Walk<TREE> walk(few ? small.total : sm.pre.units[kBlocks]);
       bool going_on = false;
+      if constexpr (TREE) {
+        if (few) walk.choose_chunk(small);
+      }
       for (int k = 0;; ++k) {
         Item w;
-        walk.next(p, TQ, w, [&](int &u, int &b) {
-          return few ? small.find(u, b) : find_seq<TREE>(p, sm.pre, 2 * TQ, u, b);
-        });
+        int last = 0;  // the last CTA that has a part of the row group
+        if constexpr (TREE) {
+          if (walk.chunk > 0 && k == 0) {
+            last = walk.one_chunk(p, small, TQ, w);
+          } else {
+            walk.next(p, TQ, w, [&](int &u, int &b) {
+              return few ? small.find(u, b) : find_seq<TREE>(p, sm.pre, 2 * TQ, u, b);
+            });
+            if (w.t1 > w.t0 && w.part == 1)
+              last = share_owner(share_begin(blockIdx.x + 1, walk.q, walk.r) + w.nct - w.t1, walk.q, walk.r);
+          }
+        } else {
+          walk.next(p, TQ, w, [&](int &u, int &b) {
+            return few ? small.find(u, b) : find_seq<TREE>(p, sm.pre, 2 * TQ, u, b);
+          });
+          if (w.t1 < 0) w.t1 = 0;  // (no item in the last round, and none after it)
+        }
         if (k >= 2 && !warp_wait(&sm.item_free[k & 1], ((k >> 1) - 1) & 1, ctl)) break;
         if (lane == 0) sm.items[k & 1] = w;
         warp_arrive(&sm.item_full[k & 1], lane);
@@ -756,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             j.tok = w.a0 + w.r0;
             j.cnt0 = w.cnt[0];
             j.head = w.hk * G;
-            j.last = share_owner(share_begin(blockIdx.x + 1, walk.q, walk.r) + w.nct - w.t1, walk.q, walk.r);
+            j.last = last;
             j.word = w.n;
             j.ctx = w.ctx;
             reinterpret_cast<JoinItem *>(p.ws)[blockIdx.x] = j;
@@ -1164,9 +1247,9 @@ cudaError_t launch_t(const AttnParams &p, int sm_count, cudaStream_t stream) {
     if (!make_map(&kc, p.cache.k, 4, dims, st, box) || !make_map(&vc, p.cache.v, 4, dims, st, box))
       return cudaErrorInvalidValue;
   } else {
-    // a CTA an item: at most this many row groups (each sequence rounds up)
-    ctas = ((long long)p.T / (2 * TQ) + p.B) * p.Hkv;
-    if (ctas > 0x7fffffffLL) ctas = 0x7fffffffLL;  // (the kernel strides over the rest)
+    // no more than there can be row groups (each sequence rounds up)
+    const long long items = ((long long)p.T / (2 * TQ) + p.B) * p.Hkv;
+    if (items < ctas) ctas = items;
   }
   cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)ctas), dim3(kThreads), C::kSmem, stream);
   cudaLaunchAttribute attr[1];

@@ -24,135 +24,141 @@ __device__ __forceinline__ void unpack8(const uint4 &w, float (&x)[8]) {
 // ------------------------------------------------------------ qk_norm_rope
 // y = x * rsqrt(mean x^2 + eps) * w, then the rotation of the first rot
 // channels: every value is read once and written once, so HBM bounds a long
-// prompt and latency a decode step.  A head takes L lanes of 8 channels (one
-// 16-byte load each): the mean is a butterfly over them, the rotation partner
-// of a half-split pair is a shuffle away.  A CTA works on one token, so each
-// thread loads its 16 cosines and sines once and reuses them for every head it
-// takes; the loads of kU heads go out before the first is used.
-constexpr int kRopeThreads = 256;
+// prompt and latency a decode step.  A head takes L lanes of two 16-byte units
+// each, and a lane's two units are each other's rotation partners (half-split:
+// units c and c + rot/16; neighbouring pairs: two units in a row), so the
+// rotation needs no exchange between lanes and the mean log2 L shuffles.  A
+// CTA works on one token: each thread loads its 8 cosines and sines once for
+// all the heads it takes, behind the loads of the first kU heads.
+// 8192 tokens of 64 + 8 heads of 128, with the cache (353 MB): 62.9 us, 5.6
+// TB/s of 6.8 measured for a copy.  Threads of a CTA, heads in flight and CTAs
+// per SM were swept: 64, 3, 12 (the registers' limit); 256 threads take 79 us,
+// four heads in flight spill (81 us).
+constexpr int kRopeThreads = 64;
 constexpr int kU = 3;
 
 template <int L, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 12) rope_kernel(const RopeParams p) {
   constexpr unsigned kFull = 0xFFFFFFFFu;
   constexpr int kGroups = kRopeThreads / L;
   pdl_trigger();
   const int t = blockIdx.x;
   const int c = threadIdx.x % L, g = threadIdx.x / L;
-  const bool in = c * 8 < p.D;
-  const int heads = p.Hq + p.Hkv + (p.v.ptr ? p.Hkv : 0);
+  const int units = p.D >> 3, hc = p.rot >> 4;
+  // this lane's units of a head; past hc (half-split) they are not rotated
+  const bool turned = INTER ? 16 * c < p.rot : c < hc;
+  const int ua = INTER ? 2 * c : turned ? c : 2 * c, ub = INTER || !turned ? ua + 1 : c + hc;
+  const bool ina = ua < units, inb = ub < units;
+  const int heads_qk = p.Hq + p.Hkv, heads = heads_qk + (p.v.ptr ? p.Hkv : 0);
   const int step = gridDim.y * kGroups;
   pdl_wait();
 
-  // the cache place of this token; an out-of-range slot is not written
-  uint16_t *kc = nullptr, *vc = nullptr;
-  if (p.cache.k) {
-    const long long s = p.slots[t];
-    if (s >= 0) {
-      const long long pg = s / p.cache.page_size;
-      if (pg < p.cache.pages) {
-        const long long at = pg * p.cache.page + (s - pg * p.cache.page_size) * p.cache.slot;
-        kc = p.cache.k + at;
-        vc = p.cache.v + at;
-      } else if (p.status && threadIdx.x == 0) {
-        atomicOr(p.status, kBadIndex);
-      }
-    }
-  }
-  // this lane's cosines and sines (8 of each, or the 4 of its own pairs)
-  constexpr int kA = INTER ? 4 : 8;
-  float cs[kA], sn[kA];
-  bool bad = false;
-  const int half = p.rot >> 1;
-  const int hc = p.rot >> 4;  // 8-channel chunks in a half
-  const bool turned = c * 8 < p.rot;
-  if (p.rot > 0) {
-    const int pos = p.pos[t];
-    bad = pos < 0 || pos >= p.max_pos;
-    if (bad && p.status && threadIdx.x == 0) atomicOr(p.status, kBadIndex);
-    if (turned && !bad) {
-      const float *row = p.cos_sin + (size_t)pos * p.rot;
-      const int a = INTER ? c * 4 : (c < hc ? c : c - hc) * 8;
-#pragma unroll
-      for (int j = 0; j < kA; j += 4) {
-        const float4 x = __ldg(reinterpret_cast<const float4 *>(row + a + j));
-        const float4 y = __ldg(reinterpret_cast<const float4 *>(row + half + a + j));
-        cs[j] = x.x, cs[j + 1] = x.y, cs[j + 2] = x.z, cs[j + 3] = x.w;
-        sn[j] = y.x, sn[j + 1] = y.y, sn[j + 2] = y.z, sn[j + 3] = y.w;
-      }
-      if (!INTER && c < hc) {
-#pragma unroll
-        for (int j = 0; j < kA; ++j) sn[j] = -sn[j];  // the lower half subtracts
-      }
-    }
-  }
-  const int partner = !turned ? c : c < hc ? c + hc : c - hc;
-  const uint4 one = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
-  uint4 wq = one, wk = one;
-  if (in && p.wq) wq = __ldg(reinterpret_cast<const uint4 *>(p.wq) + c);
-  if (in && p.wk) wk = __ldg(reinterpret_cast<const uint4 *>(p.wk) + c);
-
-  // every lane of a warp takes the same number of turns (the shuffles need it)
-  for (int h0 = blockIdx.y * kGroups; h0 < heads; h0 += kU * step) {
-    uint4 x[kU];
+  const int pos = p.rot > 0 ? __ldg(p.pos + t) : 0;
+  const long long slot = p.cache.k ? __ldg(p.slots + t) : -1;
+  const uint16_t *q = p.q.ptr + t * p.q.tok, *k = p.k.ptr + t * p.k.tok, *v = p.v.ptr + t * p.v.tok;
+  uint4 xa[kU], xb[kU];
+  auto load = [&](int h0) {
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const int h = h0 + u * step + g;
-      x[u] = make_uint4(0, 0, 0, 0);
-      if (in && h < heads) {
-        const uint16_t *src = h < p.Hq          ? p.q.ptr + t * p.q.tok + h * p.q.head
-                              : h < p.Hq + p.Hkv ? p.k.ptr + t * p.k.tok + (h - p.Hq) * p.k.head
-                                                 : p.v.ptr + t * p.v.tok + (h - p.Hq - p.Hkv) * p.v.head;
-        x[u] = *reinterpret_cast<const uint4 *>(src + c * 8);
+      xa[u] = xb[u] = make_uint4(0, 0, 0, 0);
+      if (h < heads) {
+        const uint16_t *src = h < p.Hq       ? q + h * p.q.head
+                              : h < heads_qk ? k + (h - p.Hq) * p.k.head
+                                             : v + (h - heads_qk) * p.v.head;
+        if (ina) xa[u] = *reinterpret_cast<const uint4 *>(src + ua * 8);
+        if (inb) xb[u] = *reinterpret_cast<const uint4 *>(src + ub * 8);
       }
     }
+  };
+  load(blockIdx.y * kGroups);
+
+  // a position outside the table makes the token NaN
+  const bool bad = p.rot > 0 && (pos < 0 || pos >= p.max_pos);
+  float cs[8], sn[8];
+  if (turned && !bad) {
+    const float4 *row = reinterpret_cast<const float4 *>(p.cos_sin + (size_t)pos * p.rot) + c * 2;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float4 x = __ldg(row + i), y = __ldg(row + (p.rot >> 3) + i);
+      cs[4 * i] = x.x, cs[4 * i + 1] = x.y, cs[4 * i + 2] = x.z, cs[4 * i + 3] = x.w;
+      sn[4 * i] = y.x, sn[4 * i + 1] = y.y, sn[4 * i + 2] = y.z, sn[4 * i + 3] = y.w;
+    }
+  }
+  // the cache place of this token; an out-of-range slot is not written
+  long long at = -1;
+  if (slot >= 0) {
+    const long long pg = slot / p.cache.page_size;
+    if (pg < p.cache.pages) at = pg * p.cache.page + (slot - pg * p.cache.page_size) * p.cache.slot;
+  }
+  if (threadIdx.x == 0 && p.status && (bad || (slot >= 0 && at < 0))) atomicOr(p.status, kBadIndex);
+  const float inv_d = 1.0f / (float)p.D;
+
+  // every lane of a warp takes the same number of turns (the shuffles need it)
+  for (int h0 = blockIdx.y * kGroups; h0 < heads; h0 += kU * step) {
+    if (h0 != blockIdx.y * kGroups) load(h0);
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       if (h0 + u * step >= heads) break;  // uniform over the CTA
       const int h = h0 + u * step + g;
       const bool is_q = h < p.Hq;
-      float y[8], w[8];
-      unpack8(x[u], y);
-      if (is_q ? p.wq != nullptr : p.wk != nullptr) unpack8(is_q ? wq : wk, w);
-      else
+      const uint16_t *gain = is_q ? p.wq : p.wk;  // (read again for each head: it is in L1, registers are short)
+      uint4 wa = {}, wb = {};
+      if (gain && ina) wa = __ldg(reinterpret_cast<const uint4 *>(gain) + ua);
+      if (gain && inb) wb = __ldg(reinterpret_cast<const uint4 *>(gain) + ub);
+      float a[8], b[8], w[8], ss = 0.0f;
+      unpack8(xa[u], a);
+      unpack8(xb[u], b);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = 1.0f;
-      float ss = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(y[j], y[j], ss);
+      for (int j = 0; j < 8; ++j) ss = fmaf(b[j], b[j], fmaf(a[j], a[j], ss));
 #pragma unroll
       for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o, L);
-      const bool norm = is_q ? p.wq != nullptr : p.wk != nullptr;
-      const float r = norm ? rsqrtf(ss / (float)p.D + p.eps) : 1.0f;
+      if (gain) {
+        const float r = rsqrtf(fmaf(ss, inv_d, p.eps));
+        unpack8(wa, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = y[j] * r * w[j];
-      float z[8];
-      if (INTER) {
+        for (int j = 0; j < 8; ++j) a[j] = a[j] * r * w[j];
+        unpack8(wb, w);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          z[2 * j] = turned ? y[2 * j] * cs[j] - y[2 * j + 1] * sn[j] : y[2 * j];
-          z[2 * j + 1] = turned ? y[2 * j + 1] * cs[j] + y[2 * j] * sn[j] : y[2 * j + 1];
-        }
-      } else {
+        for (int j = 0; j < 8; ++j) b[j] = b[j] * r * w[j];
+      }
+      if (turned) {
+        if (INTER) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float o = __shfl_sync(kFull, y[j], partner, L);
-          z[j] = turned ? fmaf(y[j], cs[j % kA], o * sn[j % kA]) : y[j];
+          for (int j = 0; j < 4; ++j) {
+            const float x0 = a[2 * j], x1 = a[2 * j + 1], y0 = b[2 * j], y1 = b[2 * j + 1];
+            a[2 * j] = x0 * cs[j] - x1 * sn[j];
+            a[2 * j + 1] = x1 * cs[j] + x0 * sn[j];
+            b[2 * j] = y0 * cs[4 + j] - y1 * sn[4 + j];
+            b[2 * j + 1] = y1 * cs[4 + j] + y0 * sn[4 + j];
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float x = a[j], y = b[j];
+            a[j] = x * cs[j] - y * sn[j];
+            b[j] = y * cs[j] + x * sn[j];
+          }
         }
       }
-      uint4 out = make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]), pack_bf16x2(z[4], z[5]),
-                             pack_bf16x2(z[6], z[7]));
-      if (bad) out = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
-      if (!in || h >= heads) continue;
+      if (h >= heads) continue;
+      uint4 ra = make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]),
+                            pack_bf16x2(a[6], a[7]));
+      uint4 rb = make_uint4(pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]), pack_bf16x2(b[4], b[5]),
+                            pack_bf16x2(b[6], b[7]));
+      if (bad) ra = rb = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
+      auto put = [&](uint16_t *dst, const uint4 &x, const uint4 &y) {
+        if (ina) *reinterpret_cast<uint4 *>(dst + ua * 8) = x;
+        if (inb) *reinterpret_cast<uint4 *>(dst + ub * 8) = y;
+      };
       if (is_q) {
-        *reinterpret_cast<uint4 *>(p.q_out.ptr + t * p.q_out.tok + h * p.q_out.head + c * 8) = out;
-      } else if (h < p.Hq + p.Hkv) {
+        put(p.q_out.ptr + t * p.q_out.tok + h * p.q_out.head, ra, rb);
+      } else if (h < heads_qk) {
         const int hk = h - p.Hq;
-        if (p.k_out.ptr)
-          *reinterpret_cast<uint4 *>(p.k_out.ptr + t * p.k_out.tok + hk * p.k_out.head + c * 8) = out;
-        if (kc) *reinterpret_cast<uint4 *>(kc + hk * p.cache.head + c * 8) = out;
-      } else if (vc) {
-        *reinterpret_cast<uint4 *>(vc + (h - p.Hq - p.Hkv) * p.cache.head + c * 8) = x[u];
+        if (p.k_out.ptr) put(p.k_out.ptr + t * p.k_out.tok + hk * p.k_out.head, ra, rb);
+        if (at >= 0) put(p.cache.k + at + hk * p.cache.head, ra, rb);
+      } else if (at >= 0) {
+        put(p.cache.v + at + (h - heads_qk) * p.cache.head, xa[u], xb[u]);
       }
     }
   }
@@ -246,12 +252,14 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
 }  // namespace
 
 cudaError_t launch_qk_norm_rope(const RopeParams &p, bool interleaved, int sm_count, cudaStream_t stream) {
-  const int chunks = p.D / 8;
-  if (chunks <= 2) return rope_launch<2>(p, interleaved, sm_count, stream);
-  if (chunks <= 4) return rope_launch<4>(p, interleaved, sm_count, stream);
-  if (chunks <= 8) return rope_launch<8>(p, interleaved, sm_count, stream);
-  if (chunks <= 16) return rope_launch<16>(p, interleaved, sm_count, stream);
-  return rope_launch<32>(p, interleaved, sm_count, stream);
+  // lanes of a head: two units each; a half-split rotation pairs them first
+  const int units = p.D / 8, pairs = p.rot / 16;
+  const int lanes = pairs + (units - 2 * pairs + 1) / 2;
+  if (lanes <= 1) return rope_launch<1>(p, interleaved, sm_count, stream);
+  if (lanes <= 2) return rope_launch<2>(p, interleaved, sm_count, stream);
+  if (lanes <= 4) return rope_launch<4>(p, interleaved, sm_count, stream);
+  if (lanes <= 8) return rope_launch<8>(p, interleaved, sm_count, stream);
+  return rope_launch<16>(p, interleaved, sm_count, stream);
 }
 
 cudaError_t launch_kv_append(const AppendParams &p, cudaStream_t stream) {
