@@ -64,6 +64,14 @@ struct Cfg {
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
+// a / b for a >= 0, b > 0 and a quotient below 2^22, in fp32 and one correction
+// (the full integer division took a few hundred cycles of the item warp's way
+// to the first load).
+__device__ __forceinline__ int div_small(int a, int b) {
+  const int q = (int)__fdividef((float)a, (float)b), r = a - q * b;
+  return q + (r >= b) - (r < 0);
+}
+
 // ------------------------------------------------------------ work of a call
 // Sequences in order; of each its kv heads, its row groups (pairs of row
 // tiles), and -- tree -- its key tiles, all units numbered through (the host
@@ -111,7 +119,7 @@ __device__ __forceinline__ Seq seq_of(const AttnParams &p, const Raw &r, int tq2
     if (bad && r.ctx != s.ctx) *bad = true;
     s.per = (s.ctx + kKeys - 1) / kKeys + 1;
   }
-  s.units = (s.n + tq2 - 1) / tq2 * p.Hkv * s.per;
+  s.units = div_small(s.n + tq2 - 1, tq2) * p.Hkv * s.per;
   return s;
 }
 
@@ -280,9 +288,10 @@ struct Walk {
   __device__ __forceinline__ void choose_chunk(const Small<true> &b) {
     const int least = q + (r > 0);
     if (least == 0) return;
+    const int rows = div_small(b.s.units, b.s.per);
 #pragma unroll
     for (int i = 2; i >= 0; --i) {
-      const int chunks = b.s.units > 0 ? b.s.units / b.s.per * ((b.s.per + least + i - 1) / (least + i)) : 0;
+      const int chunks = b.s.units > 0 ? rows * div_small(b.s.per + least + i - 1, least + i) : 0;
       if (__reduce_add_sync(0xFFFFFFFFu, chunks) <= (int)gridDim.x) chunk = least + i;
     }
   }
@@ -290,8 +299,8 @@ struct Walk {
   __device__ __forceinline__ int one_chunk(const AttnParams &p, const Small<true> &b, int tq, Item &it) {
     constexpr unsigned kFull = 0xFFFFFFFFu;
     const int lane = threadIdx.x & 31, c = blockIdx.x;
-    const int pieces = (b.s.per + chunk - 1) / chunk;
-    const int mine = b.s.units > 0 ? b.s.units / b.s.per * pieces : 0;
+    const int pieces = div_small(b.s.per + chunk - 1, chunk);
+    const int mine = b.s.units > 0 ? div_small(b.s.units, b.s.per) * pieces : 0;
     int sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -307,8 +316,8 @@ struct Walk {
     it.n = __shfl_sync(kFull, b.s.n, it.b);
     it.ctx = __shfl_sync(kFull, b.s.ctx, it.b);
     const int per = __shfl_sync(kFull, b.s.per, it.b), k = __shfl_sync(kFull, pieces, it.b);
-    const int x = c - __shfl_sync(kFull, sum - mine, it.b), gh = x / k, piece = x - gh * k;
-    const int cut = per / k, rest = per - cut * k;
+    const int x = c - __shfl_sync(kFull, sum - mine, it.b), gh = div_small(x, k), piece = x - gh * k;
+    const int cut = div_small(per, k), rest = per - cut * k;
     it.t0 = share_begin(piece, cut, rest);
     it.t1 = share_begin(piece + 1, cut, rest);
     rows_of(p, tq, gh, per, it);
@@ -316,7 +325,7 @@ struct Walk {
   }
   // tree: kv head and rows of row group x kv head gh, what its end is
   __device__ __forceinline__ void rows_of(const AttnParams &p, int tq, int gh, int per, Item &it) {
-    const int g = gh / p.Hkv;
+    const int g = div_small(gh, p.Hkv);
     it.hk = gh - g * p.Hkv;
     it.nct = per - 1;
     it.part = it.t0 > 0 ? 0 : it.t1 < per ? 1 : -1;
@@ -338,7 +347,7 @@ struct Walk {
       it.a0 = s.a0;
       it.n = s.n;
       it.ctx = s.ctx;
-      const int gh = u / s.per;
+      const int gh = div_small(u, s.per);
       it.t0 = u - gh * s.per;
       it.t1 = min(s.per, it.t0 + (end - cur));
       cur += it.t1 - it.t0;
@@ -356,7 +365,7 @@ struct Walk {
       it.a0 = s.a0;
       it.n = s.n;
       it.ctx = it.nct = 0;
-      const int g = u / p.Hkv;
+      const int g = div_small(u, p.Hkv);
       it.hk = u - g * p.Hkv;
       it.part = -1;
       it.r0 = g * 2 * tq;
@@ -417,6 +426,19 @@ struct Smem {
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const WaitCtl &ctl) {
   const bool ok = mbar_wait_quick(smem_addr(bar), parity, ctl);
   return __all_sync(0xFFFFFFFFu, ok);
+}
+// The same for the warps that hold few registers, the loop out of line: some
+// forty copies of it would be a fifth of the code.
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *status,
+                                     unsigned long long timeout_ns) {
+  return mbar_wait_quick(bar, parity, WaitCtl{abort_flag, status, timeout_ns});
+}
+__device__ __forceinline__ bool lane_wait(uint64_t *bar, uint32_t parity, const WaitCtl &ctl) {
+  return mbar_try_wait(smem_addr(bar), parity) ||
+         wait_on(smem_addr(bar), parity, ctl.abort_flag, ctl.status, ctl.timeout_ns);
+}
+__device__ __forceinline__ bool warp_wait_far(uint64_t *bar, uint32_t parity, const WaitCtl &ctl) {
+  return __all_sync(0xFFFFFFFFu, lane_wait(bar, parity, ctl));
 }
 // Bounded wait that ignores the abort flag: lets what is in flight land.
 __device__ __forceinline__ void drain(uint64_t *bar, uint32_t parity, uint64_t timeout_ns) {
@@ -515,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       auto load_kv = [&](const Item &i, int j, bool is_v) {
         const uint32_t slot = n % S;
-        if (n >= S && !warp_wait(&sm.kv_empty[slot], (n / S - 1) & 1, ctl)) return false;
+        if (n >= S && !warp_wait_far(&sm.kv_empty[slot], (n / S - 1) & 1, ctl)) return false;
         const uint32_t bar = smem_addr(&sm.kv_full[slot]), dst = kv_smem + slot * C::kTile;
         if (TREE && j < i.nct) {
           // pages of up to 128 keys, one lane a page; those past the context stay out
@@ -554,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           if (!ok || it.end[s] <= it.t0) continue;
-          if (nq[s] > 0) ok = warp_wait(&sm.q_empty[s], (nq[s] - 1) & 1, ctl);
+          if (nq[s] > 0) ok = warp_wait_far(&sm.q_empty[s], (nq[s] - 1) & 1, ctl);
           if (!ok) break;
           ++nq[s];
           if (lane == 0) {
@@ -591,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t q_ph = 0, p_ph = 0, o_ph = 0, clean = 0;  // phases, a bit for each stream, buffer or slot
       uint32_t started = 0;
       constexpr uint32_t kIdQK = idesc_bf16(128, kKeys, false), kIdPV = idesc_bf16(128, D, true);
-      auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait_quick(smem_addr(bar), parity, ctl); };
+      auto wait = [&](uint64_t *bar, uint32_t parity) { return lane_wait(bar, parity, ctl); };
       // (what follows runs in the elected lane alone)
       auto ring = [&](uint32_t k) { return wait(&sm.kv_full[k % S], (k / S) & 1); };
       auto ring_v = [&](uint32_t k, bool guard) {
@@ -756,8 +778,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int i = j - it.t0;
           const uint32_t at = n + lead + i + min(i, nt - lead), slot = at % S;  // the v tile's place in the ring
           // (once the load is issued, the slot's earlier phases are over)
-          ok = warp_wait(&sm.v_issued[slot], (issued >> slot) & 1, ctl) &&
-               warp_wait(&sm.kv_full[slot], (at / S) & 1, ctl);
+          ok = warp_wait_far(&sm.v_issued[slot], (issued >> slot) & 1, ctl) &&
+               warp_wait_far(&sm.kv_full[slot], (at / S) & 1, ctl);
           if (!ok) break;
           issued ^= 1u << slot;
           const uint32_t tile = kv_smem + slot * C::kTile;
@@ -826,7 +848,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           });
           if (w.t1 < 0) w.t1 = 0;  // (no item in the last round, and none after it)
         }
-        if (k >= 2 && !warp_wait(&sm.item_free[k & 1], ((k >> 1) - 1) & 1, ctl)) break;
+        if (k >= 2 && !warp_wait_far(&sm.item_free[k & 1], ((k >> 1) - 1) & 1, ctl)) break;
         if (lane == 0) sm.items[k & 1] = w;
         warp_arrive(&sm.item_full[k & 1], lane);
         if (w.t1 == w.t0) break;
@@ -995,9 +1017,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t anyp = 0;
         for (int x = 0; x < 12; ++x) anyp |= (&sm.poison[k & 1][0][0])[x];
         auto poisoned = [&](uint32_t (&o)[32], int c0) {
+#pragma unroll 1
           for (int x = 0; x < 12; ++x) {
             uint32_t bits = (&sm.poison[k & 1][0][0])[x];
             const int j = g0 + x / 4;
+#pragma unroll 1
             while (bits) {
               const int r = (x & 3) * 32 + __ffs(bits) - 1;
               bits &= bits - 1;
@@ -1028,47 +1052,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t mine = stage + lane * kUnits * 16;
           const int unit = lane % kUnits, sub = lane / kUnits;
           const int rows = __popc(__ballot_sync(0xFFFFFFFFu, valid_row));  // (the first ones)
-          auto store = [&](uint8_t *base) {  // base: this row's first byte
-            __syncwarp();
-#pragma unroll 4
-            for (int r0 = 0; r0 < rows; r0 += kRowsStore) {
-              const int r = r0 + sub;
-              uint8_t *to = reinterpret_cast<uint8_t *>(
-                  __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(base), r));
-              const uint4 v = ld_shared_v4(stage + r * kUnits * 16 + ((unit ^ r) & (kUnits - 1)) * 16);
-              if (to) *reinterpret_cast<uint4 *>(to + unit * 16) = v;
-            }
-            __syncwarp();
-          };
-          if (part) {
+          uint16_t *out = p.out.ptr + (long long)(it.a0 + tok) * p.out.tok + (it.hk * G + rg) * p.out.head;
 #pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
+          for (int x = 0; x < D / 32; ++x) {
+            uint32_t o[32];
+            tmem_ld32(o_t + x * 32, o);
+            tmem_ld_wait();
+            tmem_landed(o);
+            if (anyp) poisoned(o, x * 32);
+            if (part) {  // half a row fills a staged row
+              const int u0 = x % (D / 64) * 8;
 #pragma unroll
-              for (int x = 0; x < D / 64; ++x) {
-                uint32_t o[32];
-                tmem_ld32(o_t + h * (D / 2) + x * 32, o);
-                tmem_ld_wait();
-                tmem_landed(o);
-                if (anyp) poisoned(o, h * (D / 2) + x * 32);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  st_shared_v4(mine + (((x * 8 + e) ^ lane) & (kUnits - 1)) * 16, o[4 * e], o[4 * e + 1], o[4 * e + 2],
-                               o[4 * e + 3]);
-              }
-              store(valid_row ? reinterpret_cast<uint8_t *>(part + row * D + h * (D / 2)) : nullptr);
-            }
-            if (valid_row) {
-              part[D * kRowsT + row] = m;
-              part[(D + 1) * kRowsT + row] = l;
-            }
-          } else {
-#pragma unroll 1
-            for (int x = 0; x < D / 32; ++x) {
-              uint32_t o[32];
-              tmem_ld32(o_t + x * 32, o);
-              tmem_ld_wait();
-              tmem_landed(o);
-              if (anyp) poisoned(o, x * 32);
+              for (int e = 0; e < 8; ++e)
+                st_shared_v4(mine + (((u0 + e) ^ lane) & (kUnits - 1)) * 16, o[4 * e], o[4 * e + 1], o[4 * e + 2],
+                             o[4 * e + 3]);
+            } else {
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 uint32_t w[4];
@@ -1080,8 +1078,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 st_shared_v4(mine + (((x * 4 + e) ^ lane) & (kUnits - 1)) * 16, w[0], w[1], w[2], w[3]);
               }
             }
-            uint16_t *out = p.out.ptr + (long long)(it.a0 + tok) * p.out.tok + (it.hk * G + rg) * p.out.head;
-            store(valid_row ? reinterpret_cast<uint8_t *>(out) : nullptr);
+            const bool half = part && (x + 1) % (D / 64) == 0;
+            if (!half && x + 1 < D / 32) continue;
+            uint8_t *row0 = part ? reinterpret_cast<uint8_t *>(part + row * D + (x + 1 - D / 64) * 32)
+                                 : reinterpret_cast<uint8_t *>(out);
+            if (!valid_row) row0 = nullptr;
+            __syncwarp();
+#pragma unroll 4
+            for (int r0 = 0; r0 < rows; r0 += kRowsStore) {
+              const int r = r0 + sub;
+              uint8_t *to = reinterpret_cast<uint8_t *>(
+                  __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(row0), r));
+              const uint4 v = ld_shared_v4(stage + r * kUnits * 16 + ((unit ^ r) & (kUnits - 1)) * 16);
+              if (to) *reinterpret_cast<uint4 *>(to + unit * 16) = v;
+            }
+            __syncwarp();
+          }
+          if (part && valid_row) {
+            part[D * kRowsT + row] = m;
+            part[(D + 1) * kRowsT + row] = l;
           }
         }
         fence_proxy_async_smem();  // the q tile is a TMA target again

@@ -159,7 +159,8 @@ mxg_status attn_prompt(const mxg_heads *q, const mxg_heads *k, const mxg_heads *
   if (T == 0) return MXG_OK;
   // row groups x kv heads, numbered in 32 bits
   const int tq = 128 / (Hq / Hkv);
-  if (((long long)T / (2 * tq) + B) * Hkv > 0x3fffffffLL) return MXG_ERR_UNSUPPORTED_SHAPE;
+  if (((long long)T / (2 * tq) + B) * Hkv > 0x3fffffffLL || T / (2 * tq) >= (1 << 22) || Hkv >= (1 << 16))
+    return MXG_ERR_UNSUPPORTED_SHAPE;
   const mxg::AttnParams p = attn_params(q, k, v, cu_seqlens, B, T, Hq, Hkv, D, scale, out, opts);
   const cudaError_t e = mxg::launch_attn_prompt(p, sm, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MXG_OK : MXG_ERR_CUDA;
@@ -189,7 +190,7 @@ mxg_status attn_tree(const mxg_heads *q, const mxg_heads *k, const mxg_heads *v,
   // row groups x kv heads x key tiles, numbered in 32 bits
   const int tq = 128 / (Hq / Hkv);
   const long long groups = N / (2 * tq) + (N < B ? N : B);
-  if (groups * Hkv * ((long long)table_cols * cache->page_size / 128 + 2) > 0x3fffffffLL)
+  if (groups * Hkv * ((long long)table_cols * cache->page_size / 128 + 2) > 0x3fffffffLL || Hkv >= (1 << 16))
     return MXG_ERR_UNSUPPORTED_SHAPE;
   if (N == 0) return MXG_OK;
   mxg::AttnParams p = attn_params(q, k, v, cu_nodes, B, N, Hq, Hkv, D, scale, out, opts);
