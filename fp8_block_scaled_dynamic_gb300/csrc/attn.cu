@@ -1120,7 +1120,36 @@ __global__ void __launch_bounds__(kThreads, 1)
 // keys: a warp takes one row of the item that began in CTA blockIdx.x and went
 // on.  Latency bounds it: the references and sums of 32 parts come in one load
 // a lane, the parts themselves in batches of 8 loads in flight.
-constexpr int kJoinRows = 8;
+constexpr int kJoinRows = 8, kJoinBlocks = 16;
+// Eight parts of a row at once, V values a lane.  One statement: left to
+// itself, the compiler put each part's sums before the next part's load, eight
+// round trips to L2 instead of one.
+__device__ __forceinline__ void load_parts(const float *const (&p)[8], uint32_t (&y)[8][4]) {
+  asm volatile(
+      "ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%32];\n\tld.global.cg.v4.u32 {%4, %5, %6, %7}, [%33];\n\t"
+      "ld.global.cg.v4.u32 {%8, %9, %10, %11}, [%34];\n\tld.global.cg.v4.u32 {%12, %13, %14, %15}, [%35];\n\t"
+      "ld.global.cg.v4.u32 {%16, %17, %18, %19}, [%36];\n\tld.global.cg.v4.u32 {%20, %21, %22, %23}, [%37];\n\t"
+      "ld.global.cg.v4.u32 {%24, %25, %26, %27}, [%38];\n\tld.global.cg.v4.u32 {%28, %29, %30, %31}, [%39];"
+      : "=&r"(y[0][0]), "=&r"(y[0][1]), "=&r"(y[0][2]), "=&r"(y[0][3]), "=&r"(y[1][0]), "=&r"(y[1][1]),
+        "=&r"(y[1][2]), "=&r"(y[1][3]), "=&r"(y[2][0]), "=&r"(y[2][1]), "=&r"(y[2][2]), "=&r"(y[2][3]),
+        "=&r"(y[3][0]), "=&r"(y[3][1]), "=&r"(y[3][2]), "=&r"(y[3][3]), "=&r"(y[4][0]), "=&r"(y[4][1]),
+        "=&r"(y[4][2]), "=&r"(y[4][3]), "=&r"(y[5][0]), "=&r"(y[5][1]), "=&r"(y[5][2]), "=&r"(y[5][3]),
+        "=&r"(y[6][0]), "=&r"(y[6][1]), "=&r"(y[6][2]), "=&r"(y[6][3]), "=&r"(y[7][0]), "=&r"(y[7][1]),
+        "=&r"(y[7][2]), "=&r"(y[7][3])
+      : "l"(p[0]), "l"(p[1]), "l"(p[2]), "l"(p[3]), "l"(p[4]), "l"(p[5]), "l"(p[6]), "l"(p[7]));
+}
+__device__ __forceinline__ void load_parts(const float *const (&p)[8], uint32_t (&y)[8][2]) {
+  asm volatile(
+      "ld.global.cg.v2.u32 {%0, %1}, [%16];\n\tld.global.cg.v2.u32 {%2, %3}, [%17];\n\t"
+      "ld.global.cg.v2.u32 {%4, %5}, [%18];\n\tld.global.cg.v2.u32 {%6, %7}, [%19];\n\t"
+      "ld.global.cg.v2.u32 {%8, %9}, [%20];\n\tld.global.cg.v2.u32 {%10, %11}, [%21];\n\t"
+      "ld.global.cg.v2.u32 {%12, %13}, [%22];\n\tld.global.cg.v2.u32 {%14, %15}, [%23];"
+      : "=&r"(y[0][0]), "=&r"(y[0][1]), "=&r"(y[1][0]), "=&r"(y[1][1]), "=&r"(y[2][0]), "=&r"(y[2][1]),
+        "=&r"(y[3][0]), "=&r"(y[3][1]), "=&r"(y[4][0]), "=&r"(y[4][1]), "=&r"(y[5][0]), "=&r"(y[5][1]),
+        "=&r"(y[6][0]), "=&r"(y[6][1]), "=&r"(y[7][0]), "=&r"(y[7][1])
+      : "l"(p[0]), "l"(p[1]), "l"(p[2]), "l"(p[3]), "l"(p[4]), "l"(p[5]), "l"(p[6]), "l"(p[7]));
+}
+
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinRows) attn_join_kernel(const AttnParams p) {
   using C = Cfg<D>;
@@ -1130,65 +1159,60 @@ __global__ void __launch_bounds__(32 * kJoinRows) attn_join_kernel(const AttnPar
   pdl_wait();
   const int c0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const JoinItem it = reinterpret_cast<const JoinItem *>(p.ws)[c0];
-  const int r = blockIdx.y * kJoinRows + warp;
-  if (r >= it.rows) return;
   const int G = p.Hq / p.Hkv, parts = it.last - c0 + 1;
   const float c = p.scale * kLog2e;
-  const int tile = r >= it.rows0, row = r - tile * it.rows0;
-  const int rt = row / G, node = it.tok + tile * it.cnt0 + rt, head = it.head + row - rt * G;
-  const unsigned long long word = p.mask[node] & (it.word >= 64 ? ~0ull : (1ull << it.word) - 1ull);
-  // CTA c0's part is in its second slot, the others' in their first
-  const float *base = p.ws + kJoinFloats + (long long)c0 * 2 * C::kSlotFloats + tile * (kRowsT * (D + 2));
-  auto slot = [&](int k) { return base + (long long)(k == 0 ? 1 : 2 * k) * C::kSlotFloats; };
-  float m = -INFINITY, l = 0.0f, o[V] = {};
-  for (int k0 = 0; k0 < parts; k0 += 32) {
-    const int n = min(32, parts - k0);
-    float mk = -INFINITY, lk = 0.0f;
-    if (lane < n) {
-      const float *q = slot(k0 + lane) + D * kRowsT + row;
-      mk = __ldcg(q);
-      lk = __ldcg(q + kRowsT);
-    }
-    float top = mk;
+  for (int r = blockIdx.y * kJoinRows + warp; r < it.rows; r += gridDim.y * kJoinRows) {
+    const int tile = r >= it.rows0, row = r - tile * it.rows0;
+    const int rt = row / G, node = it.tok + tile * it.cnt0 + rt, head = it.head + row - rt * G;
+    const unsigned long long word = p.mask[node] & (it.word >= 64 ? ~0ull : (1ull << it.word) - 1ull);
+    // CTA c0's part is in its second slot, the others' in their first
+    const float *base = p.ws + kJoinFloats + (long long)c0 * 2 * C::kSlotFloats + tile * (kRowsT * (D + 2));
+    auto slot = [&](int k) { return base + (long long)(k == 0 ? 1 : 2 * k) * C::kSlotFloats; };
+    float m = -INFINITY, l = 0.0f, o[V] = {};
+    for (int k0 = 0; k0 < parts; k0 += 32) {
+      const int n = min(32, parts - k0);
+      float mk = -INFINITY, lk = 0.0f, f = 0.0f;
+      if (lane < n) {
+        const float *q = slot(k0 + lane) + D * kRowsT + row;
+        mk = __ldcg(q);
+        lk = __ldcg(q + kRowsT);
+      }
+      for (int k = 0; k < n; k += 8) {
+        const float *at[8];
+        uint32_t y[8][V];
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
-    const float mn = fmaxf(m, top);
-    const float old = m == -INFINITY ? 0.0f : ex2((m - mn) * c);  // (more than 32 parts)
-    const float f = mk == -INFINITY ? 0.0f : ex2((mk - mn) * c);
-    m = mn;
-    l *= old;
+        for (int i = 0; i < 8; ++i) at[i] = slot(k0 + min(k + i, n - 1)) + row * D + lane * V;
+        load_parts(at, y);
+        if (k == 0) {  // (with the first parts under way)
+          float top = mk;
 #pragma unroll
-    for (int e = 0; e < V; ++e) o[e] *= old;
-    lk *= f;
-    for (int k = 0; k < n; k += 8) {
-      float y[8][V];
+          for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
+          const float mn = fmaxf(m, top);
+          const float old = m == -INFINITY ? 0.0f : ex2((m - mn) * c);  // (more than 32 parts)
+          f = mk == -INFINITY ? 0.0f : ex2((mk - mn) * c);
+          m = mn;
+          l *= old;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float *q = slot(k0 + min(k + i, n - 1)) + row * D + lane * V;
-        if (V == 4) {
-          const float4 v = __ldcg(reinterpret_cast<const float4 *>(q));
-          y[i][0] = v.x, y[i][1] = v.y, y[i][2 % V] = v.z, y[i][3 % V] = v.w;
-        } else {
-          const float2 v = __ldcg(reinterpret_cast<const float2 *>(q));
-          y[i][0] = v.x, y[i][1] = v.y;
+          for (int e = 0; e < V; ++e) o[e] *= old;
+          lk *= f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float fk = __shfl_sync(kFull, f, (k + i) & 31), la = __shfl_sync(kFull, lk, (k + i) & 31);
+          const bool in = k + i < n;
+          l += in ? la : 0.0f;
+#pragma unroll
+          for (int e = 0; e < V; ++e) o[e] = fmaf(in ? fk : 0.0f, in ? __uint_as_float(y[i][e]) : 0.0f, o[e]);
         }
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float fk = __shfl_sync(kFull, f, k + i), la = __shfl_sync(kFull, lk, k + i);
-        if (k + i >= n) break;
-        l += la;
-#pragma unroll
-        for (int e = 0; e < V; ++e) o[e] = fmaf(fk, y[i][e], o[e]);
-      }
     }
-  }
-  const bool any = it.ctx > 0 || word != 0ull;
-  const float inv = 1.0f / l;
-  uint16_t *out = p.out.ptr + (long long)node * p.out.tok + head * p.out.head + lane * V;
+    const bool any = it.ctx > 0 || word != 0ull;
+    const float inv = 1.0f / l;
+    uint16_t *out = p.out.ptr + (long long)node * p.out.tok + head * p.out.head + lane * V;
 #pragma unroll
-  for (int e = 0; e < V; e += 2)
-    reinterpret_cast<uint32_t *>(out)[e / 2] = any ? pack_bf16x2(o[e] * inv, o[e + 1] * inv) : 0u;
+    for (int e = 0; e < V; e += 2)
+      reinterpret_cast<uint32_t *>(out)[e / 2] = any ? pack_bf16x2(o[e] * inv, o[e + 1] * inv) : 0u;
+  }
 }
 
 // ------------------------------------------------------------------- host
@@ -1271,11 +1295,13 @@ cudaError_t launch_t(const AttnParams &p, int sm_count, cudaStream_t stream) {
   attach_pdl(cfg, attr);
   e = cudaLaunchKernelEx(&cfg, kern, q, k, v, kc, vc, p);
   if (TREE && e == cudaSuccess) {
-    // rows that an item can have, 8 a block
+    // rows that an item can have, 8 a block, in up to kJoinBlocks blocks an
+    // item (most are empty: the kernel's time grows with their number)
     int rows = (p.T < kAttnMaxNodes ? p.T : kAttnMaxNodes) * G;
     if (rows > 2 * TQ * G) rows = 2 * TQ * G;
-    cudaLaunchConfig_t jc =
-        pdl_config(dim3((unsigned)ctas, (unsigned)((rows + kJoinRows - 1) / kJoinRows)), dim3(32 * kJoinRows), 0, stream);
+    const int blocks = (rows + kJoinRows - 1) / kJoinRows;
+    cudaLaunchConfig_t jc = pdl_config(dim3((unsigned)ctas, (unsigned)(blocks < kJoinBlocks ? blocks : kJoinBlocks)),
+                                       dim3(32 * kJoinRows), 0, stream);
     attach_pdl(jc, attr);
     e = cudaLaunchKernelEx(&jc, attn_join_kernel<D>, p);
   }
