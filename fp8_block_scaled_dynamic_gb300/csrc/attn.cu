@@ -50,7 +50,8 @@ static_assert(2 * kRegsSoftmax + kRegsRest == 3 * kRegs, "register split");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kFallBehind = 8.0f;  // log2 of how far the reference may lag the maximum
 
-constexpr long long kJoinFloats = 256 * 8;  // JoinItem of each CTA at the workspace's start
+constexpr int kMaxCtas = 256;                       // of attn_tree
+constexpr long long kJoinFloats = kMaxCtas * 8;     // JoinItem of each CTA at the workspace's start
 
 template <int D>
 struct Cfg {
@@ -89,7 +90,8 @@ struct Seq {
   int a0, n;    // first token (node), tokens (nodes)
   int ctx;      // tree: cached tokens
   int per;      // key tiles of a row group that count as units (prompt: 1)
-  int units;
+  int rows;     // row groups x kv heads
+  int units;    // their product
 };
 
 struct Raw {
@@ -119,7 +121,8 @@ __device__ __forceinline__ Seq seq_of(const AttnParams &p, const Raw &r, int tq2
     if (bad && r.ctx != s.ctx) *bad = true;
     s.per = (s.ctx + kKeys - 1) / kKeys + 1;
   }
-  s.units = div_small(s.n + tq2 - 1, tq2) * p.Hkv * s.per;
+  s.rows = div_small(s.n + tq2 - 1, tq2) * p.Hkv;
+  s.units = s.rows * s.per;
   return s;
 }
 
@@ -233,7 +236,7 @@ struct Small {
     if (lane == 0) running = 0;
     bool bad = false;
     s = seq_of<TREE>(p, r, tq2, running, &bad);
-    if (lane >= p.B) s.units = 0;
+    if (lane >= p.B) s.rows = s.units = 0;
     int sum = s.units;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -253,7 +256,7 @@ struct Small {
     r.n = __shfl_sync(kFull, s.n, b);
     r.ctx = __shfl_sync(kFull, s.ctx, b);
     r.per = __shfl_sync(kFull, s.per, b);
-    r.units = 0;
+    r.rows = r.units = 0;
     u -= __shfl_sync(kFull, before, b);
     return r;
   }
@@ -288,19 +291,20 @@ struct Walk {
   __device__ __forceinline__ void choose_chunk(const Small<true> &b) {
     const int least = q + (r > 0);
     if (least == 0) return;
-    const int rows = div_small(b.s.units, b.s.per);
+    int chunks[3];
 #pragma unroll
-    for (int i = 2; i >= 0; --i) {
-      const int chunks = b.s.units > 0 ? rows * div_small(b.s.per + least + i - 1, least + i) : 0;
-      if (__reduce_add_sync(0xFFFFFFFFu, chunks) <= (int)gridDim.x) chunk = least + i;
-    }
+    for (int i = 0; i < 3; ++i)
+      chunks[i] = __reduce_add_sync(0xFFFFFFFFu, b.s.rows * div_small(b.s.per + least + i - 1, least + i));
+#pragma unroll
+    for (int i = 2; i >= 0; --i)
+      if (chunks[i] <= (int)gridDim.x) chunk = least + i;
   }
   // this CTA's only item, a chunk; returns the last CTA of the row group's chunks
   __device__ __forceinline__ int one_chunk(const AttnParams &p, const Small<true> &b, int tq, Item &it) {
     constexpr unsigned kFull = 0xFFFFFFFFu;
     const int lane = threadIdx.x & 31, c = blockIdx.x;
     const int pieces = div_small(b.s.per + chunk - 1, chunk);
-    const int mine = b.s.units > 0 ? div_small(b.s.units, b.s.per) * pieces : 0;
+    const int mine = b.s.rows * pieces;
     int sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -1039,8 +1043,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // A thread holds a row, and rows are far apart in memory: the results
         // go through the q tile (multiplied for the last time; each warp its
         // own 32 rows, the 16-byte units of row r at unit ^ r), so that a store
-        // writes two whole rows of bf16 (half rows of fp32 parts).  Straight
-        // from the rows' threads, 32 lines a store, this took 5000 cycles.
+        // writes whole rows.  Straight from the rows' threads, 32 lines a
+        // store, this took 5000 cycles.  (A part's rows are fp32, a whole line
+        // for every thread's 32 values, and often few.)
         float *part = nullptr;
         if (TREE && it.part >= 0)
           part = p.ws + kJoinFloats + ((long long)blockIdx.x * 2 + it.part) * C::kSlotFloats + st * (kRowsT * (D + 2));
@@ -1060,12 +1065,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld_wait();
             tmem_landed(o);
             if (anyp) poisoned(o, x * 32);
-            if (part) {  // half a row fills a staged row
-              const int u0 = x % (D / 64) * 8;
+            if (part) {
+              if (valid_row)
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                st_shared_v4(mine + (((u0 + e) ^ lane) & (kUnits - 1)) * 16, o[4 * e], o[4 * e + 1], o[4 * e + 2],
-                             o[4 * e + 3]);
+                for (int e = 0; e < 32; e += 8) st_global_v8(part + row * D + x * 32 + e, o + e);
             } else {
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
@@ -1078,17 +1081,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 st_shared_v4(mine + (((x * 4 + e) ^ lane) & (kUnits - 1)) * 16, w[0], w[1], w[2], w[3]);
               }
             }
-            const bool half = part && (x + 1) % (D / 64) == 0;
-            if (!half && x + 1 < D / 32) continue;
-            uint8_t *row0 = part ? reinterpret_cast<uint8_t *>(part + row * D + (x + 1 - D / 64) * 32)
-                                 : reinterpret_cast<uint8_t *>(out);
-            if (!valid_row) row0 = nullptr;
+          }
+          if (!part) {
+            const unsigned long long row0 = valid_row ? reinterpret_cast<unsigned long long>(out) : 0ull;
             __syncwarp();
 #pragma unroll 4
             for (int r0 = 0; r0 < rows; r0 += kRowsStore) {
               const int r = r0 + sub;
-              uint8_t *to = reinterpret_cast<uint8_t *>(
-                  __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(row0), r));
+              uint8_t *to = reinterpret_cast<uint8_t *>(__shfl_sync(0xFFFFFFFFu, row0, r));
               const uint4 v = ld_shared_v4(stage + r * kUnits * 16 + ((unit ^ r) & (kUnits - 1)) * 16);
               if (to) *reinterpret_cast<uint4 *>(to + unit * 16) = v;
             }
@@ -1117,10 +1117,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the parts of the items that several CTAs shared, in the order of the
-// keys: a warp takes one row of the item that began in CTA blockIdx.x and went
-// on.  Latency bounds it: the references and sums of 32 parts come in one load
-// a lane, the parts themselves in batches of 8 loads in flight.
-constexpr int kJoinRows = 8, kJoinBlocks = 16;
+// keys: a warp takes a row of an item that began in one CTA and went on.
+// Latency bounds it.  Every block reads the whole list of items and deals the
+// rows of all of them over the grid's warps (a block an item and 8 rows, most
+// of them empty, took 6.5 us for a verify step); the references and sums of 32
+// parts come in one load a lane, the parts themselves 8 in flight.
+constexpr int kJoinWarps = 8, kJoinBlocksSm = 3;
 // Eight parts of a row at once, V values a lane.  One statement: left to
 // itself, the compiler put each part's sums before the next part's load, eight
 // round trips to L2 instead of one.
@@ -1151,17 +1153,41 @@ __device__ __forceinline__ void load_parts(const float *const (&p)[8], uint32_t 
 }
 
 template <int D>
-__global__ void __launch_bounds__(32 * kJoinRows) attn_join_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(32 * kJoinWarps, kJoinBlocksSm) attn_join_kernel(const AttnParams p, int ctas) {
   using C = Cfg<D>;
   constexpr int V = D / 32;  // columns a lane
   constexpr unsigned kFull = 0xFFFFFFFFu;
+  static_assert(32 * kJoinWarps == kMaxCtas, "a thread reads an item");
+  __shared__ JoinItem s_item[kMaxCtas];
+  __shared__ int s_end[kMaxCtas], s_warp[kJoinWarps];  // rows of the items up to and with one
   pdl_trigger();
-  pdl_wait();
-  const int c0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const JoinItem it = reinterpret_cast<const JoinItem *>(p.ws)[c0];
-  const int G = p.Hq / p.Hkv, parts = it.last - c0 + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = p.Hq / p.Hkv;
   const float c = p.scale * kLog2e;
-  for (int r = blockIdx.y * kJoinRows + warp; r < it.rows; r += gridDim.y * kJoinRows) {
+  pdl_wait();
+  JoinItem mine = {};
+  if ((int)threadIdx.x < ctas) mine = reinterpret_cast<const JoinItem *>(p.ws)[threadIdx.x];
+  int sum = mine.rows;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(kFull, sum, o);
+    if (lane >= o) sum += x;
+  }
+  if (lane == 31) s_warp[warp] = sum;
+  s_item[threadIdx.x] = mine;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) sum += w < warp ? s_warp[w] : 0;
+  s_end[threadIdx.x] = sum;
+  __syncthreads();
+  const int total = s_end[kMaxCtas - 1];
+  for (int x = blockIdx.x + gridDim.x * warp; x < total; x += gridDim.x * kJoinWarps) {
+    int c0 = 0;  // the first item whose rows end after x
+#pragma unroll
+    for (int o = kMaxCtas / 2; o > 0; o >>= 1)
+      if (s_end[c0 + o - 1] <= x) c0 += o;
+    const JoinItem it = s_item[c0];
+    const int r = x - (s_end[c0] - it.rows), parts = it.last - c0 + 1;
     const int tile = r >= it.rows0, row = r - tile * it.rows0;
     const int rt = row / G, node = it.tok + tile * it.cnt0 + rt, head = it.head + row - rt * G;
     const unsigned long long word = p.mask[node] & (it.word >= 64 ? ~0ull : (1ull << it.word) - 1ull);
@@ -1277,7 +1303,7 @@ cudaError_t launch_t(const AttnParams &p, int sm_count, cudaStream_t stream) {
   if (!heads_map(&q, p.q, p.Hq, p.T, D, G, TQ) || !heads_map(&k, p.k, p.Hkv, p.T, D, 1, rows) ||
       !heads_map(&v, p.v, p.Hkv, p.T, D, 1, rows))
     return cudaErrorInvalidValue;
-  long long ctas = sm_count < 256 ? sm_count : 256;
+  long long ctas = sm_count < kMaxCtas ? sm_count : kMaxCtas;
   if (TREE) {
     const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)p.Hkv, (cuuint64_t)p.cache.page_size,
                                 (cuuint64_t)p.cache.pages};
@@ -1295,15 +1321,9 @@ cudaError_t launch_t(const AttnParams &p, int sm_count, cudaStream_t stream) {
   attach_pdl(cfg, attr);
   e = cudaLaunchKernelEx(&cfg, kern, q, k, v, kc, vc, p);
   if (TREE && e == cudaSuccess) {
-    // rows that an item can have, 8 a block, in up to kJoinBlocks blocks an
-    // item (most are empty: the kernel's time grows with their number)
-    int rows = (p.T < kAttnMaxNodes ? p.T : kAttnMaxNodes) * G;
-    if (rows > 2 * TQ * G) rows = 2 * TQ * G;
-    const int blocks = (rows + kJoinRows - 1) / kJoinRows;
-    cudaLaunchConfig_t jc = pdl_config(dim3((unsigned)ctas, (unsigned)(blocks < kJoinBlocks ? blocks : kJoinBlocks)),
-                                       dim3(32 * kJoinRows), 0, stream);
+    cudaLaunchConfig_t jc = pdl_config(dim3((unsigned)(kJoinBlocksSm * sm_count)), dim3(32 * kJoinWarps), 0, stream);
     attach_pdl(jc, attr);
-    e = cudaLaunchKernelEx(&jc, attn_join_kernel<D>, p);
+    e = cudaLaunchKernelEx(&jc, attn_join_kernel<D>, p, (int)ctas);
   }
   return e;
 }
@@ -1318,7 +1338,7 @@ cudaError_t launch_attn_tree(const AttnParams &p, int sm_count, cudaStream_t str
 }
 size_t attn_tree_ws_bytes(int D, int sm_count) {
   const long long f = D == 64 ? Cfg<64>::kSlotFloats : Cfg<128>::kSlotFloats;
-  return (size_t)(kJoinFloats + 2 * f * (sm_count < 256 ? sm_count : 256)) * sizeof(float);
+  return (size_t)(kJoinFloats + 2 * f * (sm_count < kMaxCtas ? sm_count : kMaxCtas)) * sizeof(float);
 }
 
 }  // namespace mxg

@@ -92,6 +92,13 @@ __device__ __forceinline__ void tmem_landed(uint32_t (&r)[32]) {
         "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
 }
 
+// A 32-byte store (p aligned to it).
+__device__ __forceinline__ void st_global_v8(float *p, const uint32_t *v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ void fma2(float &x, float &y, float a0, float a1, float b, float c) {
   asm("{\n\t.reg .b64 a, b, c, d;\n\t"
