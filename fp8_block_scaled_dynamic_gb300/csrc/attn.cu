@@ -1123,33 +1123,47 @@ __global__ void __launch_bounds__(kThreads, 1)
 // of them empty, took 6.5 us for a verify step); the references and sums of 32
 // parts come in one load a lane, the parts themselves 8 in flight.
 constexpr int kJoinWarps = 8, kJoinBlocksSm = 3;
-// Eight parts of a row at once, V values a lane.  One statement: left to
-// itself, the compiler put each part's sums before the next part's load, eight
-// round trips to L2 instead of one.
-__device__ __forceinline__ void load_parts(const float *const (&p)[8], uint32_t (&y)[8][4]) {
+// Up to eight parts of a row at once (zeros for those past n), V values a
+// lane.  One statement: left to itself, the compiler put each part's sums
+// before the next part's load, eight round trips to L2 instead of one.
+__device__ __forceinline__ void load_parts(const float *const (&p)[8], int n, uint32_t (&y)[8][4]) {
   asm volatile(
-      "ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%32];\n\tld.global.cg.v4.u32 {%4, %5, %6, %7}, [%33];\n\t"
-      "ld.global.cg.v4.u32 {%8, %9, %10, %11}, [%34];\n\tld.global.cg.v4.u32 {%12, %13, %14, %15}, [%35];\n\t"
-      "ld.global.cg.v4.u32 {%16, %17, %18, %19}, [%36];\n\tld.global.cg.v4.u32 {%20, %21, %22, %23}, [%37];\n\t"
-      "ld.global.cg.v4.u32 {%24, %25, %26, %27}, [%38];\n\tld.global.cg.v4.u32 {%28, %29, %30, %31}, [%39];"
-      : "=&r"(y[0][0]), "=&r"(y[0][1]), "=&r"(y[0][2]), "=&r"(y[0][3]), "=&r"(y[1][0]), "=&r"(y[1][1]),
-        "=&r"(y[1][2]), "=&r"(y[1][3]), "=&r"(y[2][0]), "=&r"(y[2][1]), "=&r"(y[2][2]), "=&r"(y[2][3]),
-        "=&r"(y[3][0]), "=&r"(y[3][1]), "=&r"(y[3][2]), "=&r"(y[3][3]), "=&r"(y[4][0]), "=&r"(y[4][1]),
-        "=&r"(y[4][2]), "=&r"(y[4][3]), "=&r"(y[5][0]), "=&r"(y[5][1]), "=&r"(y[5][2]), "=&r"(y[5][3]),
-        "=&r"(y[6][0]), "=&r"(y[6][1]), "=&r"(y[6][2]), "=&r"(y[6][3]), "=&r"(y[7][0]), "=&r"(y[7][1]),
+      "{\n\t.reg .pred q;\n\t"
+      "setp.gt.s32 q, %40, 0; mov.b32 %0, 0; mov.b32 %1, 0; mov.b32 %2, 0; mov.b32 %3, 0;\n\t@q ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%32];\n\t"
+      "setp.gt.s32 q, %40, 1; mov.b32 %4, 0; mov.b32 %5, 0; mov.b32 %6, 0; mov.b32 %7, 0;\n\t@q ld.global.cg.v4.u32 {%4, %5, %6, %7}, [%33];\n\t"
+      "setp.gt.s32 q, %40, 2; mov.b32 %8, 0; mov.b32 %9, 0; mov.b32 %10, 0; mov.b32 %11, 0;\n\t@q ld.global.cg.v4.u32 {%8, %9, %10, %11}, [%34];\n\t"
+      "setp.gt.s32 q, %40, 3; mov.b32 %12, 0; mov.b32 %13, 0; mov.b32 %14, 0; mov.b32 %15, 0;\n\t@q ld.global.cg.v4.u32 {%12, %13, %14, %15}, [%35];\n\t"
+      "setp.gt.s32 q, %40, 4; mov.b32 %16, 0; mov.b32 %17, 0; mov.b32 %18, 0; mov.b32 %19, 0;\n\t@q ld.global.cg.v4.u32 {%16, %17, %18, %19}, [%36];\n\t"
+      "setp.gt.s32 q, %40, 5; mov.b32 %20, 0; mov.b32 %21, 0; mov.b32 %22, 0; mov.b32 %23, 0;\n\t@q ld.global.cg.v4.u32 {%20, %21, %22, %23}, [%37];\n\t"
+      "setp.gt.s32 q, %40, 6; mov.b32 %24, 0; mov.b32 %25, 0; mov.b32 %26, 0; mov.b32 %27, 0;\n\t@q ld.global.cg.v4.u32 {%24, %25, %26, %27}, [%38];\n\t"
+      "setp.gt.s32 q, %40, 7; mov.b32 %28, 0; mov.b32 %29, 0; mov.b32 %30, 0; mov.b32 %31, 0;\n\t@q ld.global.cg.v4.u32 {%28, %29, %30, %31}, [%39];\n\t"
+      "}"
+      : "=&r"(y[0][0]), "=&r"(y[0][1]), "=&r"(y[0][2]), "=&r"(y[0][3]), "=&r"(y[1][0]),
+        "=&r"(y[1][1]), "=&r"(y[1][2]), "=&r"(y[1][3]), "=&r"(y[2][0]), "=&r"(y[2][1]),
+        "=&r"(y[2][2]), "=&r"(y[2][3]), "=&r"(y[3][0]), "=&r"(y[3][1]), "=&r"(y[3][2]),
+        "=&r"(y[3][3]), "=&r"(y[4][0]), "=&r"(y[4][1]), "=&r"(y[4][2]), "=&r"(y[4][3]),
+        "=&r"(y[5][0]), "=&r"(y[5][1]), "=&r"(y[5][2]), "=&r"(y[5][3]), "=&r"(y[6][0]),
+        "=&r"(y[6][1]), "=&r"(y[6][2]), "=&r"(y[6][3]), "=&r"(y[7][0]), "=&r"(y[7][1]),
         "=&r"(y[7][2]), "=&r"(y[7][3])
-      : "l"(p[0]), "l"(p[1]), "l"(p[2]), "l"(p[3]), "l"(p[4]), "l"(p[5]), "l"(p[6]), "l"(p[7]));
+      : "l"(p[0]), "l"(p[1]), "l"(p[2]), "l"(p[3]), "l"(p[4]), "l"(p[5]), "l"(p[6]), "l"(p[7]), "r"(n));
 }
-__device__ __forceinline__ void load_parts(const float *const (&p)[8], uint32_t (&y)[8][2]) {
+__device__ __forceinline__ void load_parts(const float *const (&p)[8], int n, uint32_t (&y)[8][2]) {
   asm volatile(
-      "ld.global.cg.v2.u32 {%0, %1}, [%16];\n\tld.global.cg.v2.u32 {%2, %3}, [%17];\n\t"
-      "ld.global.cg.v2.u32 {%4, %5}, [%18];\n\tld.global.cg.v2.u32 {%6, %7}, [%19];\n\t"
-      "ld.global.cg.v2.u32 {%8, %9}, [%20];\n\tld.global.cg.v2.u32 {%10, %11}, [%21];\n\t"
-      "ld.global.cg.v2.u32 {%12, %13}, [%22];\n\tld.global.cg.v2.u32 {%14, %15}, [%23];"
-      : "=&r"(y[0][0]), "=&r"(y[0][1]), "=&r"(y[1][0]), "=&r"(y[1][1]), "=&r"(y[2][0]), "=&r"(y[2][1]),
-        "=&r"(y[3][0]), "=&r"(y[3][1]), "=&r"(y[4][0]), "=&r"(y[4][1]), "=&r"(y[5][0]), "=&r"(y[5][1]),
-        "=&r"(y[6][0]), "=&r"(y[6][1]), "=&r"(y[7][0]), "=&r"(y[7][1])
-      : "l"(p[0]), "l"(p[1]), "l"(p[2]), "l"(p[3]), "l"(p[4]), "l"(p[5]), "l"(p[6]), "l"(p[7]));
+      "{\n\t.reg .pred q;\n\t"
+      "setp.gt.s32 q, %24, 0; mov.b32 %0, 0; mov.b32 %1, 0;\n\t@q ld.global.cg.v2.u32 {%0, %1}, [%16];\n\t"
+      "setp.gt.s32 q, %24, 1; mov.b32 %2, 0; mov.b32 %3, 0;\n\t@q ld.global.cg.v2.u32 {%2, %3}, [%17];\n\t"
+      "setp.gt.s32 q, %24, 2; mov.b32 %4, 0; mov.b32 %5, 0;\n\t@q ld.global.cg.v2.u32 {%4, %5}, [%18];\n\t"
+      "setp.gt.s32 q, %24, 3; mov.b32 %6, 0; mov.b32 %7, 0;\n\t@q ld.global.cg.v2.u32 {%6, %7}, [%19];\n\t"
+      "setp.gt.s32 q, %24, 4; mov.b32 %8, 0; mov.b32 %9, 0;\n\t@q ld.global.cg.v2.u32 {%8, %9}, [%20];\n\t"
+      "setp.gt.s32 q, %24, 5; mov.b32 %10, 0; mov.b32 %11, 0;\n\t@q ld.global.cg.v2.u32 {%10, %11}, [%21];\n\t"
+      "setp.gt.s32 q, %24, 6; mov.b32 %12, 0; mov.b32 %13, 0;\n\t@q ld.global.cg.v2.u32 {%12, %13}, [%22];\n\t"
+      "setp.gt.s32 q, %24, 7; mov.b32 %14, 0; mov.b32 %15, 0;\n\t@q ld.global.cg.v2.u32 {%14, %15}, [%23];\n\t"
+      "}"
+      : "=&r"(y[0][0]), "=&r"(y[0][1]), "=&r"(y[1][0]), "=&r"(y[1][1]), "=&r"(y[2][0]),
+        "=&r"(y[2][1]), "=&r"(y[3][0]), "=&r"(y[3][1]), "=&r"(y[4][0]), "=&r"(y[4][1]),
+        "=&r"(y[5][0]), "=&r"(y[5][1]), "=&r"(y[6][0]), "=&r"(y[6][1]), "=&r"(y[7][0]),
+        "=&r"(y[7][1])
+      : "l"(p[0]), "l"(p[1]), "l"(p[2]), "l"(p[3]), "l"(p[4]), "l"(p[5]), "l"(p[6]), "l"(p[7]), "r"(n));
 }
 
 template <int D>
@@ -1207,8 +1221,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps, kJoinBlocksSm) attn_join_kern
         const float *at[8];
         uint32_t y[8][V];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) at[i] = slot(k0 + min(k + i, n - 1)) + row * D + lane * V;
-        load_parts(at, y);
+        for (int i = 0; i < 8; ++i) at[i] = slot(k0 + k + i) + row * D + lane * V;
+        load_parts(at, n - k, y);
         if (k == 0) {  // (with the first parts under way)
           float top = mk;
 #pragma unroll
@@ -1225,10 +1239,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps, kJoinBlocksSm) attn_join_kern
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float fk = __shfl_sync(kFull, f, (k + i) & 31), la = __shfl_sync(kFull, lk, (k + i) & 31);
-          const bool in = k + i < n;
-          l += in ? la : 0.0f;
+          l += k + i < n ? la : 0.0f;  // (lanes past n hold a factor of 0)
 #pragma unroll
-          for (int e = 0; e < V; ++e) o[e] = fmaf(in ? fk : 0.0f, in ? __uint_as_float(y[i][e]) : 0.0f, o[e]);
+          for (int e = 0; e < V; ++e) o[e] = fmaf(fk, __uint_as_float(y[i][e]), o[e]);
         }
       }
     }
