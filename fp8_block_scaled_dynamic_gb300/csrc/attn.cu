@@ -53,12 +53,16 @@ constexpr float kFallBehind = 8.0f;  // log2 of how far the reference may lag th
 constexpr int kMaxCtas = 256;                       // of attn_tree
 constexpr long long kJoinFloats = kMaxCtas * 8;     // JoinItem of each CTA at the workspace's start
 
-template <int D>
+template <int D, bool TREE>
 struct Cfg {
   static constexpr int kHalves = D / 64;  // 128-byte columns of a row
   static constexpr int kTile = kKeys * D * 2;
-  static constexpr int kSlots = D == 128 ? 5 : 8;
-  static constexpr int kSmem = kHead + (2 + kSlots) * kTile;
+  // A result goes to memory through a tile of its own, so that the next item's
+  // q can come early -- or, where k and v are to be read at the memory's rate
+  // and a fifth slot of the ring counts for more, through the q tile.
+  static constexpr bool kOwnStage = !(TREE && D == 128);
+  static constexpr int kSlots = D == 64 ? 8 : TREE ? 5 : 4;
+  static constexpr int kSmem = kHead + (2 + kSlots + (kOwnStage ? 1 : 0)) * kTile;
   // a CTA's partial result of an item: two row tiles of [row][D] sums, then
   // their references and weight sums
   static constexpr long long kSlotFloats = 2LL * kRowsT * (D + 2);
@@ -289,8 +293,8 @@ struct Walk {
   }
   // the chunk length for which all chunks have a CTA, if there is a short one
   __device__ __forceinline__ void choose_chunk(const Small<true> &b) {
+    if (q == 0) return;  // fewer units than CTAs: the ranges are single units
     const int least = q + (r > 0);
-    if (least == 0) return;
     int chunks[3];
 #pragma unroll
     for (int i = 0; i < 3; ++i)
@@ -409,9 +413,9 @@ __device__ __forceinline__ int first_guarded(const Item &it) {
 
 constexpr int kItemReaders = 11;  // warps 0 to 10, an arrival each
 
-template <int D>
+template <int D, bool TREE>
 struct Smem {
-  using C = Cfg<D>;
+  using C = Cfg<D, TREE>;
   // (8-byte barriers first)
   uint64_t q_full[2], q_empty[2], kv_full[C::kSlots], kv_empty[C::kSlots];
   uint64_t v_issued[C::kSlots], kv_clean[C::kSlots];  // the guard's
@@ -464,11 +468,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKC,
                 const __grid_constant__ CUtensorMap tmVC, const AttnParams p) {
-  using C = Cfg<D>;
+  using C = Cfg<D, TREE>;
   constexpr int S = C::kSlots;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  static_assert(sizeof(Smem<D>) <= kHead, "shared memory head");
-  Smem<D> &sm = *reinterpret_cast<Smem<D> *>(smem_raw);
+  static_assert(sizeof(Smem<D, TREE>) <= kHead, "shared memory head");
+  Smem<D, TREE> &sm = *reinterpret_cast<Smem<D, TREE> *>(smem_raw);
   const uint32_t base = smem_addr(smem_raw);
   if (base & 1023u) {  // the swizzled tiles need it (uniform over the grid)
     if (threadIdx.x == 0 && p.status) atomicOr(p.status, kSmemLayout);
@@ -539,6 +543,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------------- loads
       uint32_t n = 0, nq[2] = {0, 0};
       bool ok = true;
+      const int page_shift = 31 - __clz(p.cache.page_size);
+      if (TREE) {
+        // a small batch's page table into L1, while the items are worked out
+        // (a line a lane: the first load then does not wait for L2 twice)
+        const long long ints = (long long)(p.B - 1) * p.ld_table + p.table_cols;
+        if (lane * 32LL < ints) prefetch_l1(p.table + lane * 32);
+      }
       auto load_kv = [&](const Item &i, int j, bool is_v) {
         const uint32_t slot = n % S;
         if (n >= S && !warp_wait_far(&sm.kv_empty[slot], (n / S - 1) & 1, ctl)) return false;
@@ -550,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box * 128 * C::kHalves));
           __syncwarp();
           if (lane < boxes) {
-            const int key = first + lane * box, col = key / p.cache.page_size;
+            const int key = first + lane * box, col = key >> page_shift;
             int pg = p.table[(long long)i.b * p.ld_table + col];
             if (pg < 0 || pg >= p.cache.pages) {
               pg = p.cache.pages;  // out of the map's bounds: zeros
@@ -1010,6 +1021,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       const bool active = it.t0 < last;
+      // the q tile has been multiplied for the last time
+      if (C::kOwnStage && active) warp_arrive(&sm.q_empty[st], lane);
       ok = warp_wait(&sm.guard_item[k & 1], (k >> 1) & 1, ctl);
       if (!ok) break;
       if (active) {
@@ -1041,9 +1054,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         };
         // A thread holds a row, and rows are far apart in memory: the results
-        // go through the q tile (multiplied for the last time; each warp its
-        // own 32 rows, the 16-byte units of row r at unit ^ r), so that a store
-        // writes whole rows.  Straight from the rows' threads, 32 lines a
+        // go through shared memory (a tile of the streams', or the q tile, which
+        // has been multiplied for the last time; each warp its own rows, the
+        // 16-byte units of row r at unit ^ r), so that a store writes whole
+        // rows.  Straight from the rows' threads, 32 lines a
         // store, this took 5000 cycles.  (A part's rows are fp32, a whole line
         // for every thread's 32 values, and often few.)
         float *part = nullptr;
@@ -1051,13 +1065,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           part = p.ws + kJoinFloats + ((long long)blockIdx.x * 2 + it.part) * C::kSlotFloats + st * (kRowsT * (D + 2));
         const float inv = any ? 1.0f / l : 0.0f;
         if (warp_rows) {
-          constexpr int kUnits = D / 8;             // 16-byte units of a staged row
+          // A stream's half of the own tile holds all rows of half the channels.
+          constexpr int kPasses = C::kOwnStage ? 2 : 1;
+          constexpr int kUnits = D / 8 / kPasses;   // 16-byte units of a staged row
           constexpr int kRowsStore = 32 / kUnits;   // rows a warp stores at once
-          const uint32_t stage = q_smem + st * C::kTile + (warp & 3) * 32 * kUnits * 16;
+          const uint32_t stage = (C::kOwnStage ? kv_smem + S * C::kTile + st * (C::kTile / 2) : q_smem + st * C::kTile) +
+                                 (warp & 3) * 32 * kUnits * 16;
           const uint32_t mine = stage + lane * kUnits * 16;
           const int unit = lane % kUnits, sub = lane / kUnits;
           const int rows = __popc(__ballot_sync(0xFFFFFFFFu, valid_row));  // (the first ones)
           uint16_t *out = p.out.ptr + (long long)(it.a0 + tok) * p.out.tok + (it.hk * G + rg) * p.out.head;
+          const unsigned long long row0 = valid_row ? reinterpret_cast<unsigned long long>(out) : 0ull;
 #pragma unroll 1
           for (int x = 0; x < D / 32; ++x) {
             uint32_t o[32];
@@ -1080,27 +1098,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 st_shared_v4(mine + (((x * 4 + e) ^ lane) & (kUnits - 1)) * 16, w[0], w[1], w[2], w[3]);
               }
-            }
-          }
-          if (!part) {
-            const unsigned long long row0 = valid_row ? reinterpret_cast<unsigned long long>(out) : 0ull;
-            __syncwarp();
+              if ((x + 1) % (D / 32 / kPasses)) continue;
+              __syncwarp();
 #pragma unroll 4
-            for (int r0 = 0; r0 < rows; r0 += kRowsStore) {
-              const int r = r0 + sub;
-              uint8_t *to = reinterpret_cast<uint8_t *>(__shfl_sync(0xFFFFFFFFu, row0, r));
-              const uint4 v = ld_shared_v4(stage + r * kUnits * 16 + ((unit ^ r) & (kUnits - 1)) * 16);
-              if (to) *reinterpret_cast<uint4 *>(to + unit * 16) = v;
+              for (int r0 = 0; r0 < rows; r0 += kRowsStore) {
+                const int r = r0 + sub;
+                uint8_t *to = reinterpret_cast<uint8_t *>(__shfl_sync(0xFFFFFFFFu, row0, r));
+                const uint4 v = ld_shared_v4(stage + r * kUnits * 16 + ((unit ^ r) & (kUnits - 1)) * 16);
+                if (to) *reinterpret_cast<uint4 *>(to + ((x * 4 + 4 - kUnits) + unit) * 16) = v;
+              }
+              __syncwarp();
             }
-            __syncwarp();
           }
           if (part && valid_row) {
             part[D * kRowsT + row] = m;
             part[(D + 1) * kRowsT + row] = l;
           }
         }
-        fence_proxy_async_smem();  // the q tile is a TMA target again
-        warp_arrive(&sm.q_empty[st], lane);
+        if (!C::kOwnStage) {
+          fence_proxy_async_smem();  // the q tile is a TMA target again
+          warp_arrive(&sm.q_empty[st], lane);
+        }
         tc_fence_before();
         warp_arrive(&sm.o_free[st], lane);
       }
@@ -1168,7 +1186,7 @@ __device__ __forceinline__ void load_parts(const float *const (&p)[8], int n, ui
 
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps, kJoinBlocksSm) attn_join_kernel(const AttnParams p, int ctas) {
-  using C = Cfg<D>;
+  using C = Cfg<D, true>;
   constexpr int V = D / 32;  // columns a lane
   constexpr unsigned kFull = 0xFFFFFFFFu;
   static_assert(32 * kJoinWarps == kMaxCtas, "a thread reads an item");
@@ -1293,7 +1311,7 @@ bool heads_map(CUtensorMap *m, const Heads &h, int heads, int T, int D, int box_
 
 template <int D, bool TREE>
 cudaError_t launch_t(const AttnParams &p, int sm_count, cudaStream_t stream) {
-  using C = Cfg<D>;
+  using C = Cfg<D, TREE>;
   auto kern = attn_kernel<D, TREE>;
   static DeviceOnce once;
   int dev = -1;
@@ -1350,7 +1368,7 @@ cudaError_t launch_attn_tree(const AttnParams &p, int sm_count, cudaStream_t str
   return p.D == 64 ? launch_t<64, true>(p, sm_count, stream) : launch_t<128, true>(p, sm_count, stream);
 }
 size_t attn_tree_ws_bytes(int D, int sm_count) {
-  const long long f = D == 64 ? Cfg<64>::kSlotFloats : Cfg<128>::kSlotFloats;
+  const long long f = D == 64 ? Cfg<64, true>::kSlotFloats : Cfg<128, true>::kSlotFloats;
   return (size_t)(kJoinFloats + 2 * f * (sm_count < kMaxCtas ? sm_count : kMaxCtas)) * sizeof(float);
 }
 

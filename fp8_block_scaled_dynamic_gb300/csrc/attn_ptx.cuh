@@ -92,6 +92,8 @@ __device__ __forceinline__ void tmem_landed(uint32_t (&r)[32]) {
         "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
 }
 
+__device__ __forceinline__ void prefetch_l1(const void *p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
+
 // A 32-byte store (p aligned to it).
 __device__ __forceinline__ void st_global_v8(float *p, const uint32_t *v) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
