@@ -541,73 +541,97 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_less<kRegsRest>();
     if (warp == 9) {
       // ------------------------------------------------------------- loads
-      uint32_t n = 0, nq[2] = {0, 0};
+      // The loader has to keep pace with 64 KB a key tile beside busy softmax
+      // warps (at pages of 16, 32 copies), so: no divisions, the ring's place
+      // and phase carried along, pages read from the table two to three tiles
+      // ahead, and the copies issued by one elected lane from warp-uniform
+      // operands.
+      uint32_t n = 0, nq[2] = {0, 0}, slot = 0, turn = 0;
       bool ok = true;
-      const int page_shift = 31 - __clz(p.cache.page_size);
+      const bool el = elect_one();
+      const uint32_t kvb = uniform(kv_smem), full0 = uniform(smem_addr(&sm.kv_full[0])), qb = uniform(q_smem);
+      const int page_shift = TREE ? 31 - __clz(p.cache.page_size) : 0, box_shift = TREE ? min(page_shift, 7) : 7;
       if (TREE) {
         // a small batch's page table into L1, while the items are worked out
         // (a line a lane: the first load then does not wait for L2 twice)
         const long long ints = (long long)(p.B - 1) * p.ld_table + p.table_cols;
         if (lane * 32LL < ints) prefetch_l1(p.table + lane * 32);
       }
-      auto load_kv = [&](const Item &i, int j, bool is_v) {
-        const uint32_t slot = n % S;
-        if (n >= S && !warp_wait_far(&sm.kv_empty[slot], (n / S - 1) & 1, ctl)) return false;
-        const uint32_t bar = smem_addr(&sm.kv_full[slot]), dst = kv_smem + slot * C::kTile;
-        if (TREE && j < i.nct) {
-          // pages of up to 128 keys, one lane a page; those past the context stay out
-          const int box = min(p.cache.page_size, kKeys);
-          const int first = j * kKeys, boxes = (min(kKeys, i.ctx - first) + box - 1) / box;
-          if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box * 128 * C::kHalves));
-          __syncwarp();
-          if (lane < boxes) {
-            const int key = first + lane * box, col = key >> page_shift;
-            int pg = p.table[(long long)i.b * p.ld_table + col];
-            if (pg < 0 || pg >= p.cache.pages) {
+      for (int k = 0; ok && next_item(k); ++k) {
+        const int t0 = (int)uniform(it.t0), t1 = (int)uniform(it.t1), nct = (int)uniform(it.nct);
+        const int hk = (int)uniform(it.hk), a0 = (int)uniform(it.a0), ctx = (int)uniform(it.ctx);
+        // lane b: the page of box b (a page of up to 128 keys) of tile j
+        const int *row = p.table + (long long)it.b * p.ld_table;
+        auto page_of = [&](int j) {
+          const int key = (j << 7) + (lane << box_shift);
+          if (!TREE || j >= nct || j >= t1 || (lane << box_shift) >= kKeys || key >= ctx) return 0;
+          return __ldg(row + (key >> page_shift));
+        };
+        auto load_kv = [&](int j, bool is_v, int pg) {
+          if (!warp_wait_far(&sm.kv_empty[slot], turn ^ 1, ctl)) return false;  // (free at first)
+          const uint32_t us = uniform(slot), bar = full0 + 8 * us, dst = kvb + us * C::kTile;
+          if (TREE && j < nct) {
+            const int boxes = (min(kKeys, ctx - (j << 7)) + (1 << box_shift) - 1) >> box_shift;
+            if ((uint32_t)pg >= (uint32_t)p.cache.pages) {
               pg = p.cache.pages;  // out of the map's bounds: zeros
               if (p.status) atomicOr(p.status, kBadIndex);
             }
-            const CUtensorMap *tm = is_v ? &tmVC : &tmKC;
-  #pragma unroll
+            int page[8];
+#pragma unroll
+            for (int b = 0; b < 8; ++b) page[b] = (int)__shfl_sync(0xFFFFFFFFu, pg, b);
+            if (el) {
+              mbar_arrive_expect_tx(bar, (uint32_t)boxes << (box_shift + 7) << (C::kHalves - 1));
+#pragma unroll
+              for (int b = 0; b < 8; ++b) {
+                if (b >= boxes) break;
+#pragma unroll
+                for (int h = 0; h < C::kHalves; ++h)
+                  tma_load_4d(dst + h * 16384 + (b << box_shift) * 128, is_v ? &tmVC : &tmKC, h * 64, hk,
+                              (j << 7) & ((1 << page_shift) - 1), page[b], bar);
+              }
+            }
+          } else if (el) {
+            // keys of the packed tensors: a prompt's tile, or the nodes (64 rows)
+            mbar_arrive_expect_tx(bar, (uint32_t)((TREE ? kAttnMaxNodes : kKeys) * 128 * C::kHalves));
+#pragma unroll
             for (int h = 0; h < C::kHalves; ++h)
-              tma_load_4d(dst + h * 16384 + lane * box * 128, tm, h * 64, i.hk, key - col * p.cache.page_size, pg, bar);
+              tma_load_3d(dst + h * 16384, is_v ? &tmV : &tmK, h * 64, hk, a0 + (TREE ? 0 : j * kKeys), bar);
           }
           __syncwarp();
-        } else if (lane == 0) {
-          // keys of the packed tensors: a prompt's tile, or the nodes (64 rows)
-          const int rows = TREE ? kAttnMaxNodes : kKeys;
-          mbar_arrive_expect_tx(bar, (uint32_t)(rows * 128 * C::kHalves));
-          const CUtensorMap *tm = is_v ? &tmV : &tmK;
-  #pragma unroll
-          for (int h = 0; h < C::kHalves; ++h)
-            tma_load_3d(dst + h * 16384, tm, h * 64, i.hk, i.a0 + (TREE ? 0 : j * kKeys), bar);
-        }
-        if (is_v && guarded<TREE>(i, j)) warp_arrive(&sm.v_issued[slot], lane);
-        ++n;
-        return true;
-      };
-      for (int k = 0; ok && next_item(k); ++k) {
-        ok = load_kv(it, it.t0, false);
+          if (is_v && guarded<TREE>(it, j)) warp_arrive(&sm.v_issued[slot], lane);
+          ++n;
+          if (++slot == S) slot = 0, turn ^= 1;
+          return true;
+        };
+        int pg[4];  // this lane's pages of tiles j .. j + 3
+#pragma unroll
+        for (int x = 0; x < 3; ++x) pg[x] = page_of(t0 + x);
+        ok = load_kv(t0, false, pg[0]);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          if (!ok || it.end[s] <= it.t0) continue;
+          if (!ok || it.end[s] <= t0) continue;
           if (nq[s] > 0) ok = warp_wait_far(&sm.q_empty[s], (nq[s] - 1) & 1, ctl);
           if (!ok) break;
           ++nq[s];
-          if (lane == 0) {
+          const int tok = (int)uniform(it.a0 + it.r0 + s * TQ);
+          if (el) {
             const uint32_t bar = smem_addr(&sm.q_full[s]);
             mbar_arrive_expect_tx(bar, (uint32_t)(TQ * G * 128 * C::kHalves));
 #pragma unroll
             for (int h = 0; h < C::kHalves; ++h)
-              tma_load_3d(q_smem + s * C::kTile + h * 16384, &tmQ, h * 64, it.hk * G, it.a0 + it.r0 + s * TQ, bar);
+              tma_load_3d(qb + s * C::kTile + h * 16384, &tmQ, h * 64, hk * G, tok, bar);
           }
           __syncwarp();
         }
-        const int lead = it.single ? 2 : 1;
-        if (ok && lead == 2 && it.t0 + 1 < it.t1) ok = load_kv(it, it.t0 + 1, false);
-        for (int j = it.t0; ok && j < it.t1; ++j) {
-          ok = load_kv(it, j, true);
-          if (ok && j + lead < it.t1) ok = load_kv(it, j + lead, false);
+        const bool two = it.single;  // K runs two tiles ahead of V
+        if (ok && two && t0 + 1 < t1) ok = load_kv(t0 + 1, false, pg[1]);
+        for (int j = t0; ok && j < t1; ++j) {
+          pg[3] = page_of(j + 3);
+          ok = load_kv(j, true, pg[0]);
+          const int jk = j + (two ? 2 : 1);
+          if (ok && jk < t1) ok = load_kv(jk, false, two ? pg[2] : pg[1]);
+#pragma unroll
+          for (int x = 0; x < 3; ++x) pg[x] = pg[x + 1];
         }
         done_item(k);
       }
