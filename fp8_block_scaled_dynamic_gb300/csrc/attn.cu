@@ -45,7 +45,7 @@ constexpr int kHead = 3072; // shared memory before the tiles
 // Registers a thread: a softmax thread holds a row of 128 scores; the two
 // softmax warpgroups take what the third gives up.  The three shares are the
 // 168 a thread that the kernel is launched with.
-constexpr int kRegs = 168, kRegsSoftmax = 208, kRegsRest = 88;
+constexpr int kRegs = 168, kRegsSoftmax = 200, kRegsRest = 104;
 static_assert(2 * kRegsSoftmax + kRegsRest == 3 * kRegs, "register split");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kFallBehind = 8.0f;  // log2 of how far the reference may lag the maximum
@@ -139,6 +139,7 @@ __device__ __forceinline__ void fill_prefix(const AttnParams &p, Prefix &pre, in
   Raw first = {0, 0, 0};  // (a small batch is read once)
   if (b0 < b1) first = raw_seq<TREE>(p, b0);
   int top = min(max(first.c0, 0), p.T);  // largest offset of this lane's sequences, then of those before
+#pragma unroll 8
   for (int b = b0 + 1; b < b1; ++b) top = max(top, min(max(__ldg(p.cu + b), 0), p.T));
   int incl = top;
   for (int o = 1; o < 32; o <<= 1) {
@@ -154,6 +155,7 @@ __device__ __forceinline__ void fill_prefix(const AttnParams &p, Prefix &pre, in
     const int s0 = min(b0 + k * per, p.B), s1 = min(s0 + per, p.B);
     pre.start[lane * kBlocksLane + k] = running;
     part[k] = mine;
+#pragma unroll 4
     for (int b = s0; b < s1; ++b)
       mine += seq_of<TREE>(p, b == b0 ? first : raw_seq<TREE>(p, b), tq2, running, &bad).units;
   }

@@ -72,6 +72,10 @@ mxg_status check_attn(const mxg_heads *q, const mxg_heads *k, const mxg_heads *v
   mxg_status st;
   for (const mxg_heads *h : {q, k, v, out})
     if ((st = check_heads(h)) != MXG_OK) return st;
+  // (a tensor map has no stride of zero)
+  if ((T > 1 && (!q->tok_stride || !k->tok_stride || !v->tok_stride || !out->tok_stride)) ||
+      (Hq > 1 && (!q->head_stride || !out->head_stride)) || (Hkv > 1 && (!k->head_stride || !v->head_stride)))
+    return MXG_ERR_UNSUPPORTED_SHAPE;
   return MXG_OK;
 }
 
@@ -181,6 +185,8 @@ mxg_status attn_tree(const mxg_heads *q, const mxg_heads *k, const mxg_heads *v,
   if ((N > 0 && !mask) || !ctx_len || table_cols < 0 || ld_table < table_cols || (table_cols > 0 && !block_table))
     return MXG_ERR_INVALID_ARG;
   if ((st = check_cache(cache)) != MXG_OK) return st;
+  if (!cache->slot_stride || (cache->pages > 1 && !cache->page_stride) || (Hkv > 1 && !cache->head_stride))
+    return MXG_ERR_UNSUPPORTED_SHAPE;
   if ((long long)table_cols * cache->page_size > 0x7fffff00LL) return MXG_ERR_UNSUPPORTED_SHAPE;
   if (!aligned(mask, 8) || !aligned(ctx_len, 4) || !aligned(block_table, 4)) return MXG_ERR_MISALIGNED;
   int sm = 0;

@@ -41,7 +41,8 @@ extern "C" {
 
 /* Heads of tokens: element (token t, head h, channel d) at
  * ptr[t * tok_stride + h * head_stride + d], strides in elements, multiples
- * of 8.  A slice of a packed qkv projection, or a tensor of its own. */
+ * of 8 (attn_prompt and attn_tree: not 0 where there is more than one token or
+ * head).  A slice of a packed qkv projection, or a tensor of its own. */
 typedef struct {
     void *ptr;
     int64_t tok_stride;

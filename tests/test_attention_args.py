@@ -46,7 +46,7 @@ PROMPT = dict(q=H(), k=H(), v=H(), cu=P, B=2, T=10, Hq=8, Hkv=2, D=128, scale=0.
     (dict(B=0), 1), (dict(T=-1), 1), (dict(Hq=0), 1), (dict(Hkv=0), 1), (dict(cu=None), 1), (dict(scale=float("inf")), 1), (dict(scale=0.0), 1), (dict(scale=-1.0), 1),
     (dict(Hkv=3), 2), (dict(D=96), 2), (dict(Hq=258, Hkv=2), 2), (dict(B=4097), 2), (dict(q=None), 1), (dict(out=H(ptr=None)), 1),
     (dict(v=H(ptr=P + 8)), 3), (dict(k=H(tok=4)), 3), (dict(cu=P + 1), 3), (dict(opts=AttnOpts(debug_stall=2)), 1),
-    (dict(opts=AttnOpts(dev_status=P + 2)), 3),
+    (dict(opts=AttnOpts(dev_status=P + 2)), 3), (dict(k=H(head=0)), 2), (dict(q=H(tok=0)), 2),
 ])
 def test_prompt_refusals(kw, want):
     assert mx.lib().attn_prompt(*{**PROMPT, **kw}.values()) == want
@@ -60,7 +60,7 @@ TREE = dict(q=H(), k=H(), v=H(), cu=P, mask=P, B=2, N=10, cache=C(), table=P, ld
     (dict(B=0), 1), (dict(N=-1), 1), (dict(mask=None), 1), (dict(ctx=None), 1), (dict(cache=None), 1), (dict(table=None), 1),
     (dict(ld=7), 1), (dict(cols=-1), 1), (dict(cache=C(page_size=8)), 2), (dict(cache=C(page_size=512)), 2), (dict(D=32), 2),
     (dict(Hkv=3), 2), (dict(cols=1 << 25, ld=1 << 25), 2), (dict(mask=P + 4), 3), (dict(cache=C(v=P + 8)), 3),
-    (dict(cache=C(head_stride=12)), 3), (dict(table=P + 2), 3),
+    (dict(cache=C(head_stride=12)), 3), (dict(table=P + 2), 3), (dict(cache=C(page_stride=0)), 2), (dict(cache=C(head_stride=0)), 2),
 ])
 def test_tree_refusals(kw, want):
     assert mx.lib().attn_tree(*{**TREE, **kw}.values()) == want
