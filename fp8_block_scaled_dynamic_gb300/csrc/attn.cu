@@ -171,9 +171,27 @@ __device__ __forceinline__ void fill_prefix(const AttnParams &p, Prefix &pre, in
   __syncwarp();
 }
 
-// The sequence that unit u is of, and u's number in it.
+// A sequence found, and the unit at which it begins.
+struct Found {
+  Seq s;
+  int b = -1, base = 0;
+};
+
+// The sequence that unit u is of, and u's number in it.  The units asked for
+// mostly follow one another (tree), so it goes on from the last one found.
 template <bool TREE>
-__device__ __forceinline__ Seq find_seq(const AttnParams &p, const Prefix &pre, int tq2, int &u, int &b) {
+__device__ __forceinline__ Seq find_seq(const AttnParams &p, const Prefix &pre, int tq2, int &u, int &b, Found &last) {
+  if (TREE && last.b >= 0 && u >= last.base) {
+    while (u >= last.base + last.s.units && last.b + 1 < p.B) {
+      int running = last.s.a0;
+      last.base += last.s.units;
+      last.s = seq_of<TREE>(p, raw_seq<TREE>(p, ++last.b), tq2, running, nullptr);
+    }
+    b = last.b;
+    u -= last.base;
+    return last.s;
+  }
+  const int u0 = u;
   int lo = 0, hi = kBlocks - 1;
   while (lo < hi) {  // the last block that starts at or before u
     const int mid = (lo + hi + 1) >> 1;
@@ -189,6 +207,9 @@ __device__ __forceinline__ Seq find_seq(const AttnParams &p, const Prefix &pre, 
     u -= s.units;
     s = seq_of<TREE>(p, raw_seq<TREE>(p, ++b), tq2, running, nullptr);
   }
+  last.s = s;
+  last.b = b;
+  last.base = u0 - u;
   return s;
 }
 
@@ -611,11 +632,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = load_kv(t0, false, pg[0]);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          if (!ok || it.end[s] <= t0) continue;
+          // (single row tiles take the two q tiles in turn)
+          if (!ok || (it.single ? s != (k & 1) : it.end[s] <= t0)) continue;
           if (nq[s] > 0) ok = warp_wait_far(&sm.q_empty[s], (nq[s] - 1) & 1, ctl);
           if (!ok) break;
           ++nq[s];
-          const int tok = (int)uniform(it.a0 + it.r0 + s * TQ);
+          const int tok = (int)uniform(it.a0 + it.r0 + (it.single ? 0 : s * TQ));
           if (el) {
             const uint32_t bar = smem_addr(&sm.q_full[s]);
             mbar_arrive_expect_tx(bar, (uint32_t)(TQ * G * 128 * C::kHalves));
@@ -701,7 +723,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; ok && next_item(k); ++k) {
         const int t0 = (int)uniform(it.t0), t1 = (int)uniform(it.t1);
         const int end[2] = {(int)uniform(it.end[0]), (int)uniform(it.end[1])};
-        const uint64_t q[2] = {sdesc_kmajor_sw128(qb), sdesc_kmajor_sw128(qb + C::kTile)};
+        const uint32_t q0 = qb + uniform(it.single ? (uint32_t)(k & 1) * C::kTile : 0u);
+        const uint64_t q[2] = {sdesc_kmajor_sw128(q0), sdesc_kmajor_sw128(qb + C::kTile)};
         done_item(k);
         if (uniform(it.single)) {
           // K runs two tiles ahead of V
@@ -711,14 +734,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok || s >= nt) continue;
             const uint64_t kd = kdesc(rn);
             if (el) {
-              ok = ring(rn) && (s > 0 || wait(&sm.q_full[0], q_ph & 1));
+              ok = ring(rn) && (s > 0 || wait(&sm.q_full[k & 1], (q_ph >> (k & 1)) & 1));
               if (ok) {
                 qk(2 + s, q[0], kd);
                 release(rn);
               }
             }
             ok = all_ok(ok);
-            if (s == 0) q_ph ^= 1;
+            if (s == 0) q_ph ^= 1u << (k & 1);
             ++rn;
           }
           for (int i = 0; ok && i < nt; i += 2) {
@@ -866,6 +889,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (few) small.read(p, 2 * TQ, lane, blockIdx.x == 0);
       else fill_prefix<TREE>(p, sm.pre, 2 * TQ, lane, blockIdx.x == 0);
       Walk<TREE> walk(few ? small.total : sm.pre.units[kBlocks]);
+      Found found;
       bool going_on = false;
       if constexpr (TREE) {
         if (few) walk.choose_chunk(small);
@@ -878,14 +902,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             last = walk.one_chunk(p, small, TQ, w);
           } else {
             walk.next(p, TQ, w, [&](int &u, int &b) {
-              return few ? small.find(u, b) : find_seq<TREE>(p, sm.pre, 2 * TQ, u, b);
+              return few ? small.find(u, b) : find_seq<TREE>(p, sm.pre, 2 * TQ, u, b, found);
             });
             if (w.t1 > w.t0 && w.part == 1)
               last = share_owner(share_begin(blockIdx.x + 1, walk.q, walk.r) + w.nct - w.t1, walk.q, walk.r);
           }
         } else {
           walk.next(p, TQ, w, [&](int &u, int &b) {
-            return few ? small.find(u, b) : find_seq<TREE>(p, sm.pre, 2 * TQ, u, b);
+            return few ? small.find(u, b) : find_seq<TREE>(p, sm.pre, 2 * TQ, u, b, found);
           });
           if (w.t1 < 0) w.t1 = 0;  // (no item in the last round, and none after it)
         }
@@ -1047,106 +1071,117 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       const bool active = it.t0 < last;
-      // the q tile has been multiplied for the last time
-      if (C::kOwnStage && active) warp_arrive(&sm.q_empty[st], lane);
+      const int qt = it.single ? k & 1 : st;  // the q tile, multiplied for the last time
+      if (C::kOwnStage && active) warp_arrive(&sm.q_empty[qt], lane);
       ok = warp_wait(&sm.guard_item[k & 1], (k >> 1) & 1, ctl);
       if (!ok) break;
       if (active) {
         ok = warp_wait(&sm.pv_done[x4], (ph >> x4 & 1) ^ 1, ctl);
         if (!ok) break;
         tc_fence_after();
-        // v rows that the guard has replaced, added by those who see them
         const int g0 = first_guarded<TREE>(it);
         uint32_t anyp = 0;
-        for (int x = 0; x < 12; ++x) anyp |= (&sm.poison[k & 1][0][0])[x];
-        auto poisoned = [&](uint32_t (&o)[32], int c0) {
-#pragma unroll 1
-          for (int x = 0; x < 12; ++x) {
-            uint32_t bits = (&sm.poison[k & 1][0][0])[x];
-            const int j = g0 + x / 4;
-#pragma unroll 1
-            while (bits) {
-              const int r = (x & 3) * 32 + __ffs(bits) - 1;
-              bits &= bits - 1;
-              const int key = TREE ? r : j * kKeys + r;
-              if (!valid_row || !(TREE ? (bool)(word >> key & 1ull) : key <= tok)) continue;
-              const uint16_t *v = p.v.ptr + (long long)(it.a0 + key) * p.v.tok + it.hk * p.v.head + c0;
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const uint32_t y = v[e];
-                if ((y & 0x7F80u) == 0x7F80u) o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(y << 16));
-              }
-            }
-          }
-        };
-        // A thread holds a row, and rows are far apart in memory: the results
-        // go through shared memory (a tile of the streams', or the q tile, which
-        // has been multiplied for the last time; each warp its own rows, the
-        // 16-byte units of row r at unit ^ r), so that a store writes whole
-        // rows.  Straight from the rows' threads, 32 lines a
-        // store, this took 5000 cycles.  (A part's rows are fp32, a whole line
-        // for every thread's 32 values, and often few.)
+        for (int x = 0; x < 12; ++x) anyp |= (&sm.poison[k & 1][0][0])[x];
         float *part = nullptr;
         if (TREE && it.part >= 0)
           part = p.ws + kJoinFloats + ((long long)blockIdx.x * 2 + it.part) * C::kSlotFloats + st * (kRowsT * (D + 2));
+        // A thread holds a row, and rows are far apart in memory: the result
+        // goes through shared memory (a tile of the streams', or the q tile,
+        // which has been multiplied for the last time; half the channels at a
+        // time, each warp its own rows, the 16-byte units of row r at unit ^
+        // r), so that a store writes whole halves of rows.  Straight from the
+        // rows' threads, 32 lines a store, this took 5000 cycles.
+        constexpr int kUnits = D / 16;           // 16-byte units of a staged half row
+        constexpr int kRowsStore = 32 / kUnits;  // rows a warp stores at once
+        const uint32_t stage = (C::kOwnStage ? kv_smem + S * C::kTile + st * (C::kTile / 2) : q_smem + qt * C::kTile) +
+                               (warp & 3) * 32 * kUnits * 16;
+        const uint32_t mine = stage + lane * kUnits * 16;
+        const int unit = lane % kUnits, sub = lane / kUnits;
+        const int rows = __popc(__ballot_sync(0xFFFFFFFFu, valid_row));  // (the first ones)
         const float inv = any ? 1.0f / l : 0.0f;
-        if (warp_rows) {
-          // A stream's half of the own tile holds all rows of half the channels.
-          constexpr int kPasses = C::kOwnStage ? 2 : 1;
-          constexpr int kUnits = D / 8 / kPasses;   // 16-byte units of a staged row
-          constexpr int kRowsStore = 32 / kUnits;   // rows a warp stores at once
-          const uint32_t stage = (C::kOwnStage ? kv_smem + S * C::kTile + st * (C::kTile / 2) : q_smem + st * C::kTile) +
-                                 (warp & 3) * 32 * kUnits * 16;
-          const uint32_t mine = stage + lane * kUnits * 16;
-          const int unit = lane % kUnits, sub = lane / kUnits;
-          const int rows = __popc(__ballot_sync(0xFFFFFFFFu, valid_row));  // (the first ones)
-          uint16_t *out = p.out.ptr + (long long)(it.a0 + tok) * p.out.tok + (it.hk * G + rg) * p.out.head;
-          const unsigned long long row0 = valid_row ? reinterpret_cast<unsigned long long>(out) : 0ull;
+        uint16_t *out = p.out.ptr + (long long)(it.a0 + tok) * p.out.tok + (it.hk * G + rg) * p.out.head;
+        const unsigned long long row0 = valid_row ? reinterpret_cast<unsigned long long>(out) : 0ull;
+        unsigned long long to[32 / kRowsStore];  // the rows that this lane stores a unit of
+#pragma unroll
+        for (int i = 0; i < 32 / kRowsStore; ++i) to[i] = __shfl_sync(0xFFFFFFFFu, row0, i * kRowsStore + sub);
+        if (!warp_rows) warp_arrive(&sm.o_free[st], lane);
 #pragma unroll 1
-          for (int x = 0; x < D / 32; ++x) {
-            uint32_t o[32];
-            tmem_ld32(o_t + x * 32, o);
-            tmem_ld_wait();
-            tmem_landed(o);
-            if (anyp) poisoned(o, x * 32);
-            if (part) {
-              if (valid_row)
+        for (int h = warp_rows ? 0 : 2; h < 2; ++h) {
+          uint32_t o[D / 64][32];
 #pragma unroll
-                for (int e = 0; e < 32; e += 8) st_global_v8(part + row * D + x * 32 + e, o + e);
-            } else {
+          for (int x = 0; x < D / 64; ++x) tmem_ld32(o_t + h * (D / 2) + x * 32, o[x]);
+          tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                uint32_t w[4];
+          for (int x = 0; x < D / 64; ++x) tmem_landed(o[x]);
+          if (h == 1) {
+            tc_fence_before();
+            warp_arrive(&sm.o_free[st], lane);  // (the next item's products may begin)
+          }
+          if (anyp) {
+            // v rows that the guard has replaced, added by those who see them
+#pragma unroll 1
+            for (int x = 0; x < 12; ++x) {
+              uint32_t bits = (&sm.poison[k & 1][0][0])[x];
+              const int j = g0 + x / 4;
+#pragma unroll 1
+              while (bits) {
+                const int r = (x & 3) * 32 + __ffs(bits) - 1;
+                bits &= bits - 1;
+                const int key = TREE ? r : j * kKeys + r;
+                if (!valid_row || !(TREE ? (bool)(word >> key & 1ull) : key <= tok)) continue;
+                const uint16_t *v = p.v.ptr + (long long)(it.a0 + key) * p.v.tok + it.hk * p.v.head + h * (D / 2);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const float a = __uint_as_float(o[8 * e + 2 * i]) * inv, b = __uint_as_float(o[8 * e + 2 * i + 1]) * inv;
-                  w[i] = any ? pack_bf16x2(a, b) : 0u;
-                }
-                st_shared_v4(mine + (((x * 4 + e) ^ lane) & (kUnits - 1)) * 16, w[0], w[1], w[2], w[3]);
+                for (int c0 = 0; c0 < D / 64; ++c0)
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) {
+                    const uint32_t y = v[c0 * 32 + e];
+                    if ((y & 0x7F80u) == 0x7F80u)
+                      o[c0][e] = __float_as_uint(__uint_as_float(o[c0][e]) + __uint_as_float(y << 16));
+                  }
               }
-              if ((x + 1) % (D / 32 / kPasses)) continue;
-              __syncwarp();
-#pragma unroll 4
-              for (int r0 = 0; r0 < rows; r0 += kRowsStore) {
-                const int r = r0 + sub;
-                uint8_t *to = reinterpret_cast<uint8_t *>(__shfl_sync(0xFFFFFFFFu, row0, r));
-                const uint4 v = ld_shared_v4(stage + r * kUnits * 16 + ((unit ^ r) & (kUnits - 1)) * 16);
-                if (to) *reinterpret_cast<uint4 *>(to + ((x * 4 + 4 - kUnits) + unit) * 16) = v;
-              }
-              __syncwarp();
             }
           }
-          if (part && valid_row) {
-            part[D * kRowsT + row] = m;
-            part[(D + 1) * kRowsT + row] = l;
+          if (part) {
+            // (a part's rows are fp32, a whole line for every 32 values of a
+            // thread, and often few: straight from the threads)
+            if (valid_row) {
+#pragma unroll
+              for (int x = 0; x < D / 64; ++x)
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) st_global_v8(part + row * D + h * (D / 2) + x * 32 + e, o[x] + e);
+            }
+            continue;
           }
+#pragma unroll
+          for (int u = 0; u < kUnits; ++u) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float a = __uint_as_float(o[u / 4][u % 4 * 8 + 2 * i]) * inv;
+              const float b = __uint_as_float(o[u / 4][u % 4 * 8 + 2 * i + 1]) * inv;
+              w[i] = any ? pack_bf16x2(a, b) : 0u;
+            }
+            st_shared_v4(mine + ((u ^ lane) & (kUnits - 1)) * 16, w[0], w[1], w[2], w[3]);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 32 / kRowsStore; ++i) {
+            if (i * kRowsStore >= rows) break;
+            const int r = i * kRowsStore + sub;
+            const uint4 v = ld_shared_v4(stage + r * kUnits * 16 + ((unit ^ r) & (kUnits - 1)) * 16);
+            if (to[i]) *reinterpret_cast<uint4 *>(to[i] + (h * kUnits + unit) * 16) = v;
+          }
+          __syncwarp();
+        }
+        if (part && valid_row) {
+          part[D * kRowsT + row] = m;
+          part[(D + 1) * kRowsT + row] = l;
         }
         if (!C::kOwnStage) {
           fence_proxy_async_smem();  // the q tile is a TMA target again
-          warp_arrive(&sm.q_empty[st], lane);
+          warp_arrive(&sm.q_empty[qt], lane);
         }
-        tc_fence_before();
-        warp_arrive(&sm.o_free[st], lane);
       }
       done_item(k);
     }
