@@ -600,8 +600,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (p.status) atomicOr(p.status, kBadIndex);
             }
             int page[8];
+            page[0] = (int)__shfl_sync(0xFFFFFFFFu, pg, 0);
+            if (box_shift < 7) page[1] = (int)__shfl_sync(0xFFFFFFFFu, pg, 1);
+            if (box_shift < 6) {
 #pragma unroll
-            for (int b = 0; b < 8; ++b) page[b] = (int)__shfl_sync(0xFFFFFFFFu, pg, b);
+              for (int b = 2; b < 8; ++b) page[b] = (int)__shfl_sync(0xFFFFFFFFu, pg, b);
+            }
             if (el) {
               mbar_arrive_expect_tx(bar, (uint32_t)boxes << (box_shift + 7) << (C::kHalves - 1));
 #pragma unroll
