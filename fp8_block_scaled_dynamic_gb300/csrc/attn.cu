@@ -1205,7 +1205,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // rows of all of them over the grid's warps (a block an item and 8 rows, most
 // of them empty, took 6.5 us for a verify step); the references and sums of 32
 // parts come in one load a lane, the parts themselves 8 in flight.
-constexpr int kJoinWarps = 8, kJoinBlocksSm = 3;
+constexpr int kJoinWarps = 8, kJoinBlocksSm = 2;
 // Up to eight parts of a row at once (zeros for those past n), V values a
 // lane.  One statement: left to itself, the compiler put each part's sums
 // before the next part's load, eight round trips to L2 instead of one.
