@@ -184,7 +184,7 @@ cudaError_t rope_launch(const RopeParams &p, bool inter, int sm_count, cudaStrea
 // A copy of (accepted rows) x (heads) x (k, v) in each layer: HBM bounds a
 // large batch, latency a step.  One CTA per (sequence, layer): its threads
 // work out where up to kRows accepted rows come from and go to, then copy them
-// as 16-byte units.
+// as 16-byte units, a thread the same place of every row it takes.
 constexpr int kAppendThreads = 256;
 constexpr int kRows = 64;
 
@@ -193,14 +193,15 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   __shared__ int s_src[kRows], s_end[2];
   pdl_trigger();
   const int b = blockIdx.x, layer = blockIdx.y;
-  pdl_wait();
-  const int ctx = p.ctx[b];
-  // the sequence's rows, clamped to the tensor
-  int n0 = p.cu[b], n1 = p.cu[b + 1];
-  n0 = min(max(n0, 0), p.N);
-  n1 = min(max(n1, n0), p.N);
-  const int *acc = p.accept + (size_t)b * p.ld_accept;
   const int unit = p.D / 8, per_row = p.Hkv * unit;
+  // rows that are copied side by side, and this thread's place: row lane, head, 16-byte unit
+  const int side = per_row < kAppendThreads ? kAppendThreads / per_row : 1;
+  const int rl = per_row < kAppendThreads ? (int)threadIdx.x / per_row : 0, u0 = (int)threadIdx.x - rl * per_row;
+  pdl_wait();
+  const int ctx = __ldg(p.ctx + b), c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1);
+  // the sequence's rows, clamped to the tensor
+  const int n0 = min(max(c0, 0), p.N), n1 = min(max(c1, n0), p.N);
+  const int *acc = p.accept + (size_t)b * p.ld_accept;
   int done = 0;
   bool more = true;
   while (more && done < p.max_accept) {
@@ -208,40 +209,37 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
     bool bad = false;
     if (threadIdx.x < kRows) {
       const int i = threadIdx.x;
-      const int a = i < n ? acc[done + i] : -1;
+      const int a = i < n ? __ldg(acc + done + i) : -1;
+      // (the page is read whatever the entry turns out to be)
+      const long long at = (long long)ctx + done + i;
+      const long long col = at / p.cache.page_size;
+      const bool in = i < n && ctx >= 0 && col < p.table_cols;
+      const int pg = in ? __ldg(p.table + (size_t)b * p.ld_table + col) : -1;
       const unsigned neg = __ballot_sync(0xFFFFFFFFu, a < 0);
       if ((i & 31) == 0) s_end[i >> 5] = neg ? __ffs(neg) - 1 : 32;
-      long long dst = -1;
-      if (a >= 0) {
-        const long long at = (long long)ctx + done + i;
-        const long long col = at / p.cache.page_size;
-        bad = a >= n1 - n0 || ctx < 0 || col >= p.table_cols;
-        if (!bad) {
-          const int pg = p.table[(size_t)b * p.ld_table + col];
-          bad = pg < 0 || pg >= p.cache.pages;
-          if (!bad) dst = pg * p.cache.page + (at - col * p.cache.page_size) * p.cache.slot;
-        }
-      }
+      bad = a >= n1 - n0 || pg < 0 || pg >= p.cache.pages;
       s_src[i] = n0 + a;
-      s_dst[i] = dst;
+      s_dst[i] = bad || a < 0 ? -1 : pg * p.cache.page + (at - col * p.cache.page_size) * p.cache.slot;
     }
     __syncthreads();
     const int rows = s_end[0] < 32 ? s_end[0] : 32 + s_end[1];
     more = rows == kRows;
     // (a bad entry past the end of the list is nobody's)
     if (bad && (int)threadIdx.x < rows && p.status && layer == 0) atomicOr(p.status, kBadIndex);
-    const int units = rows * per_row;
-    for (int u = threadIdx.x; u < units; u += kAppendThreads) {
-      const int i = u / per_row, r = u - i * per_row;
-      const int h = r / unit, c = r - h * unit;
-      if (s_dst[i] < 0) continue;
-      const long long at = layer * p.cache.layer + s_dst[i] + h * p.cache.head + c * 8;
-      const uint4 kv = *reinterpret_cast<const uint4 *>(p.k.ptr + layer * p.k_layer + s_src[i] * p.k.tok +
-                                                        h * p.k.head + c * 8);
-      const uint4 vv = *reinterpret_cast<const uint4 *>(p.v.ptr + layer * p.v_layer + s_src[i] * p.v.tok +
-                                                        h * p.v.head + c * 8);
-      *reinterpret_cast<uint4 *>(p.cache.k + at) = kv;
-      *reinterpret_cast<uint4 *>(p.cache.v + at) = vv;
+    for (int u = u0; u < per_row && rl < side; u += kAppendThreads) {
+      const int h = u / unit, c = u - h * unit;
+      const uint16_t *k = p.k.ptr + layer * p.k_layer + h * p.k.head + c * 8;
+      const uint16_t *v = p.v.ptr + layer * p.v_layer + h * p.v.head + c * 8;
+      const long long to = layer * p.cache.layer + h * p.cache.head + c * 8;
+#pragma unroll 4
+      for (int i = rl; i < rows; i += side) {
+        const long long dst = s_dst[i], src = s_src[i];
+        if (dst < 0) continue;
+        const uint4 kv = *reinterpret_cast<const uint4 *>(k + src * p.k.tok);
+        const uint4 vv = *reinterpret_cast<const uint4 *>(v + src * p.v.tok);
+        *reinterpret_cast<uint4 *>(p.cache.k + dst + to) = kv;
+        *reinterpret_cast<uint4 *>(p.cache.v + dst + to) = vv;
+      }
     }
     done += rows;
     __syncthreads();
