@@ -41,7 +41,7 @@ constexpr int kSmemLayout = 0x4;  // MXG_DEV_SMEM_LAYOUT
 constexpr int kThreads = 384;
 constexpr int kKeys = 128;  // keys of a tile
 constexpr int kRowsT = 128; // rows of a tile
-constexpr int kHead = 3072; // shared memory before the tiles
+constexpr int kHead = 3 * 1024;  // bytes of shared memory before the tiles
 // Registers a thread: a softmax thread holds a row of 128 scores; the two
 // softmax warpgroups take what the third gives up.  The three shares are the
 // 168 a thread that the kernel is launched with.
@@ -58,11 +58,11 @@ struct Cfg {
   static constexpr int kHalves = D / 64;  // 128-byte columns of a row
   static constexpr int kTile = kKeys * D * 2;
   // A result goes to memory through a tile of its own, so that the next item's
-  // q can come early -- or, where k and v are to be read at the memory's rate
-  // and a fifth slot of the ring counts for more, through the q tile.
-  static constexpr bool kOwnStage = !(TREE && D == 128);
-  static constexpr int kSlots = D == 64 ? 8 : TREE ? 5 : 4;
-  static constexpr int kSmem = kHead + (2 + kSlots + (kOwnStage ? 1 : 0)) * kTile;
+  // q can come early.  (A tree's through its q tile, with a fifth slot for k
+  // and v instead: 16 x 16384 cached tokens 166.5 us instead of 167.7, a
+  // verify step's 20.0 either way.)
+  static constexpr int kSlots = D == 64 ? 8 : 4;
+  static constexpr int kSmem = kHead + (2 + kSlots + 1) * kTile;
   // a CTA's partial result of an item: two row tiles of [row][D] sums, then
   // their references and weight sums
   static constexpr long long kSlotFloats = 2LL * kRowsT * (D + 2);
@@ -1076,7 +1076,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       const bool active = it.t0 < last;
       const int qt = it.single ? k & 1 : st;  // the q tile, multiplied for the last time
-      if (C::kOwnStage && active) warp_arrive(&sm.q_empty[qt], lane);
+      if (active) warp_arrive(&sm.q_empty[qt], lane);
       ok = warp_wait(&sm.guard_item[k & 1], (k >> 1) & 1, ctl);
       if (!ok) break;
       if (active) {
@@ -1091,15 +1091,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (TREE && it.part >= 0)
           part = p.ws + kJoinFloats + ((long long)blockIdx.x * 2 + it.part) * C::kSlotFloats + st * (kRowsT * (D + 2));
         // A thread holds a row, and rows are far apart in memory: the result
-        // goes through shared memory (a tile of the streams', or the q tile,
-        // which has been multiplied for the last time; half the channels at a
-        // time, each warp its own rows, the 16-byte units of row r at unit ^
-        // r), so that a store writes whole halves of rows.  Straight from the
-        // rows' threads, 32 lines a store, this took 5000 cycles.
+        // goes through shared memory (half the channels at a time, each warp
+        // its own rows, the 16-byte units of row r at unit ^ r), so that a store
+        // writes whole halves of rows.  Straight from the rows' threads, 32
+        // lines a store, this took 5000 cycles.
         constexpr int kUnits = D / 16;           // 16-byte units of a staged half row
         constexpr int kRowsStore = 32 / kUnits;  // rows a warp stores at once
-        const uint32_t stage = (C::kOwnStage ? kv_smem + S * C::kTile + st * (C::kTile / 2) : q_smem + qt * C::kTile) +
-                               (warp & 3) * 32 * kUnits * 16;
+        const uint32_t stage = kv_smem + S * C::kTile + st * (C::kTile / 2) + (warp & 3) * 32 * kUnits * 16;
         const uint32_t mine = stage + lane * kUnits * 16;
         const int unit = lane % kUnits, sub = lane / kUnits;
         const int rows = __popc(__ballot_sync(0xFFFFFFFFu, valid_row));  // (the first ones)
@@ -1181,10 +1179,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (part && valid_row) {
           part[D * kRowsT + row] = m;
           part[(D + 1) * kRowsT + row] = l;
-        }
-        if (!C::kOwnStage) {
-          fence_proxy_async_smem();  // the q tile is a TMA target again
-          warp_arrive(&sm.q_empty[qt], lane);
         }
       }
       done_item(k);
