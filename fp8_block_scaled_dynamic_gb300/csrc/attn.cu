@@ -22,6 +22,25 @@
 // TMEM: scores of a stream 128 columns, the bf16 weights over the first 64 of
 // them once they are read, accumulators D columns a stream.
 // Hand-offs are mbarriers; every wait is bounded.
+//
+// What bounds it, and what was measured (GB300; a copy runs at 6.8 TB/s, a
+// bf16 library product at 1.90 PFLOP/s):
+// - Long prompts of heads of 128: the tensor core (64 cycles for each 128 x 128
+//   x 16) and the power it draws: 8192 tokens of 64 / 8 heads 671 us, 1.64
+//   PFLOP/s; 16384 of 16 / 2 heads 1.69.
+// - Prompts of heads of 64: a stream's chain of scores, softmax and product
+//   (about 2500 cycles a tile of which the products are 512), which two streams
+//   cover to half: 8192 tokens of 64 / 8 heads 571 us, 0.96 PFLOP/s.  A tile's
+//   exponentials take 512 cycles of a scheduler, its tensor work as many.
+//   Tried and slower: the weights in TMEM columns of their own with the next
+//   scores under way during the softmax (585 us: the streams fall into step and
+//   want the exponential unit together), two threads a row in 16 warps (732 us).
+// - Trees over a long cache: HBM for one node a sequence (16 x 16384 cached
+//   tokens, 8 kv heads of 128: 167 us, 6.4 TB/s), the softmax beside it for
+//   many (32 nodes: 215 us, 1.28 PFLOP/s).
+// - Short calls: latency.  One token over 1500 cached ones takes 12 us with
+//   8 us in this kernel: reading the lists, the items, page table and first
+//   load, first scores, first softmax and the result are about 1 us each.
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -698,7 +717,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_commit(smem_addr(&sm.s_full[x4]));
       };
       // accumulator (+)= P . V, for the first half of the keys as soon as their
-      // weights are there
+      // weights are there (8192 tokens 671 us; at a quarter of them 675, at
+      // three quarters 693, when all are there 681)
       auto pv = [&](int x4, uint64_t b, uint32_t acc) {
         const uint32_t ph = (p_ph >> x4) & 1, o = tm + 256 + (x4 == 1 ? 128 : 0), w = tm + (x4 & 1) * 128;
         if (!wait(&sm.p_half[x4], ph)) return false;

@@ -167,7 +167,8 @@ __global__ void __launch_bounds__(kRopeThreads, 12) rope_kernel(const RopeParams
 template <int L>
 cudaError_t rope_launch(const RopeParams &p, bool inter, int sm_count, cudaStream_t stream) {
   // few tokens: a token's heads go to several CTAs, so that about two CTAs per
-  // SM share the work of a decode step
+  // SM share the work of a decode step (64 tokens of 64 + 8 heads: 3.2 us; one
+  // CTA a token 6.2, one or four an SM 3.2)
   const int groups = kRopeThreads / L;
   const int heads = p.Hq + p.Hkv + (p.v.ptr ? p.Hkv : 0);
   const int most = (heads + groups - 1) / groups;
@@ -185,6 +186,9 @@ cudaError_t rope_launch(const RopeParams &p, bool inter, int sm_count, cudaStrea
 // large batch, latency a step.  One CTA per (sequence, layer): its threads
 // work out where up to kRows accepted rows come from and go to, then copy them
 // as 16-byte units, a thread the same place of every row it takes.
+// 64 sequences of up to 8 rows x 32 layers (87 MB): 17.7 us, 4.9 TB/s (a page
+// of reading before the first row moves; two layers a CTA 17.2, four 18.4); a
+// step's 5 layers 3.0 us, of which 2.5 are a launch (128 threads 3.6).
 constexpr int kAppendThreads = 256;
 constexpr int kRows = 64;
 
