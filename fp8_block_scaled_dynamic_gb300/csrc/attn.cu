@@ -283,15 +283,49 @@ struct Small {
     bool bad = false;
     s = seq_of<TREE>(p, r, tq2, running, &bad);
     if (lane >= p.B) s.rows = s.units = 0;
-    int sum = s.units;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(kFull, sum, o);
-      if (lane >= o) sum += x;
-    }
-    before = sum - s.units;
-    total = __shfl_sync(kFull, sum, 31);
     if (bad && lane < p.B && report && p.status) atomicOr(p.status, kBadIndex);
+  }
+  // Trees in order, prompts with the longest last (whose last units are dealt
+  // first: six ragged prompts whose longest is the first of the batch 30.8 us
+  // -> 27.1, as if it were the fourth).
+  __device__ __forceinline__ void number(const AttnParams &p, int lane) {
+    constexpr unsigned kFull = 0xFFFFFFFFu;
+    total = __reduce_add_sync(kFull, s.units);
+    if (TREE) {
+      int sum = s.units;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(kFull, sum, o);
+        if (lane >= o) sum += x;
+      }
+      before = sum - s.units;
+    } else {
+      before = 0;
+#pragma unroll 4
+      for (int i = 0; i < p.B; ++i) {
+        const int n = __shfl_sync(kFull, s.n, i), units = __shfl_sync(kFull, s.units, i);
+        if (n < s.n || (n == s.n && i < lane)) before += units;
+      }
+    }
+  }
+  // Prompts: row groups of one row tile instead of two, where even then the
+  // longest has more key tiles than a CTA's share of all.  The longest row
+  // group's key tiles follow one another, and a lone row tile takes 0.6 to 0.7
+  // of a pair's time for each: 1024 tokens of 16 / 16 heads 22.8 us -> 16.1,
+  // 2048 of 16 / 2 heads 29.5 -> 23.5; but 512 of 64 / 8 heads, whose longest
+  // is no longer than the share, would go from 13.8 to 16.2.  Returns the tokens
+  // of a row group.
+  __device__ __forceinline__ int choose_span(const AttnParams &p, int tq, int lane) {
+    constexpr unsigned kFull = 0xFFFFFFFFu;
+    const int ctas = gridDim.x;
+    // (with two rounds of pairs the share is longer, and what follows fits 32 bits)
+    if (__reduce_add_sync(kFull, s.units) >= 2 * ctas) return 2 * tq;
+    const int tiles = lane < p.B ? min((s.n + kKeys - 1) / kKeys, 1 << 16) : 0;
+    // key tiles of all lone row tiles, on average half the last one's
+    const int work = __reduce_add_sync(kFull, s.rows * (tiles + 1));
+    if (__reduce_max_sync(kFull, tiles) * ctas <= work) return 2 * tq;
+    s.units = s.rows = lane < p.B ? div_small(s.n + tq - 1, tq) * p.Hkv : 0;
+    return tq;
   }
   // the sequence of unit u (u < total), and u's number in it
   __device__ __forceinline__ Seq find(int &u, int &b) const {
@@ -321,7 +355,8 @@ template <bool TREE>
 struct Walk {
   int cur, end, q, r;  // tree: this CTA's units, the shares; prompt: the round, the number of items
   int chunk;           // tree: most key tiles of a chunk, 0: equal ranges
-  __device__ __forceinline__ explicit Walk(int U) : chunk(0) {
+  int span;            // tokens (nodes) of a row group
+  __device__ __forceinline__ Walk(int U, int span) : chunk(0), span(span) {
     if (TREE) {
       q = U / (int)gridDim.x;
       r = U - q * (int)gridDim.x;
@@ -379,7 +414,7 @@ struct Walk {
     it.hk = gh - g * p.Hkv;
     it.nct = per - 1;
     it.part = it.t0 > 0 ? 0 : it.t1 < per ? 1 : -1;
-    it.r0 = g * 2 * tq;
+    it.r0 = g * span;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       it.cnt[k] = min(max(it.n - it.r0 - k * tq, 0), tq);
@@ -418,10 +453,11 @@ struct Walk {
       const int g = div_small(u, p.Hkv);
       it.hk = u - g * p.Hkv;
       it.part = -1;
-      it.r0 = g * 2 * tq;
+      it.r0 = g * span;
+      const int n = min(s.n, it.r0 + span);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        it.cnt[k] = min(max(s.n - it.r0 - k * tq, 0), tq);
+        it.cnt[k] = min(max(n - it.r0 - k * tq, 0), tq);
         it.end[k] = it.cnt[k] == 0 ? 0 : (it.r0 + k * tq + it.cnt[k] + kKeys - 1) / kKeys;
       }
       it.single = it.cnt[1] == 0;
@@ -912,7 +948,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       Small<TREE> small;
       if (few) small.read(p, 2 * TQ, lane, blockIdx.x == 0);
       else fill_prefix<TREE>(p, sm.pre, 2 * TQ, lane, blockIdx.x == 0);
-      Walk<TREE> walk(few ? small.total : sm.pre.units[kBlocks]);
+      const int span = !TREE && few ? small.choose_span(p, TQ, lane) : 2 * TQ;
+      if (few) small.number(p, lane);
+      Walk<TREE> walk(few ? small.total : sm.pre.units[kBlocks], span);
       Found found;
       bool going_on = false;
       if constexpr (TREE) {
@@ -1423,7 +1461,7 @@ cudaError_t launch_t(const AttnParams &p, int sm_count, cudaStream_t stream) {
       return cudaErrorInvalidValue;
   } else {
     // no more than there can be row groups (each sequence rounds up)
-    const long long items = ((long long)p.T / (2 * TQ) + p.B) * p.Hkv;
+    const long long items = ((long long)p.T / TQ + p.B) * p.Hkv;
     if (items < ctas) ctas = items;
   }
   cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)ctas), dim3(kThreads), C::kSmem, stream);
