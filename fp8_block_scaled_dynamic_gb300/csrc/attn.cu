@@ -541,6 +541,13 @@ __device__ __forceinline__ bool not_finite2(uint32_t w) {
   return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
 }
 
+// The same two values, zeros for what is not finite.
+__device__ __forceinline__ uint32_t finite2(uint32_t w) {
+  if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+  if ((w & 0x7F800000u) == 0x7F800000u) w &= 0xFFFFu;
+  return w;
+}
+
 template <int D, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -886,8 +893,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // -------------------------------------------------------------- guard
       // A weight of zero times a NaN is a NaN: before a v tile that not every
       // row sees in full is multiplied, its rows that no row sees are zeroed,
-      // and a row that only some see is replaced by zeros if it holds a NaN or
-      // an infinity, and noted: who sees it adds it at the end.
+      // and so are the NaN and infinities of a row that only some see, which is
+      // noted: who sees it adds them at the end.
       // (item k + 2 is only handed out when the softmax is through with item k
       // and with what is noted of it)
       uint32_t n = 0, issued = 0;
@@ -909,31 +916,38 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t tile = kv_smem + slot * C::kTile;
           const int valid = v_valid<TREE>(it, j), shared = v_shared<TREE>(it, j);
           for (int r = shared + lane; r < kKeys; r += 32) {
-            bool wipe = r >= valid;
+            const bool wipe = r >= valid;
             if (!wipe) {
               bool bad = false;
-  #pragma unroll
+#pragma unroll
               for (int h = 0; h < C::kHalves; ++h)
-  #pragma unroll
+#pragma unroll
                 for (int x = 0; x < 8; ++x) {
                   const uint4 w = ld_shared_v4(tile + h * 16384 + r * 128 + ((x + lane) & 7) * 16);
                   bad |= not_finite2(w.x) || not_finite2(w.y) || not_finite2(w.z) || not_finite2(w.w);
                 }
-              if (bad) atomicOr(&sm.poison[k & 1][j - g0][r >> 5], 1u << (r & 31));
-              wipe = bad;
+              if (bad) {
+                atomicOr(&sm.poison[k & 1][j - g0][r >> 5], 1u << (r & 31));
+#pragma unroll 1
+                for (int x = 0; x < 8 * C::kHalves; ++x) {
+                  const uint32_t to = tile + (x >> 3) * 16384 + r * 128 + (x & 7) * 16;
+                  const uint4 w = ld_shared_v4(to);
+                  st_shared_v4(to, finite2(w.x), finite2(w.y), finite2(w.z), finite2(w.w));
+                }
+              }
             }
             if (wipe) {
-  #pragma unroll
+#pragma unroll
               for (int h = 0; h < C::kHalves; ++h)
-  #pragma unroll
+#pragma unroll
                 for (int x = 0; x < 8; ++x) st_shared_v4(tile + h * 16384 + r * 128 + ((x + lane) & 7) * 16, 0, 0, 0, 0);
             }
           }
           // (a tile that all rows see as far as it goes: only its tail)
           for (int r = max(valid, 0) + lane; r < min(shared, kKeys); r += 32)
-  #pragma unroll
+#pragma unroll
             for (int h = 0; h < C::kHalves; ++h)
-  #pragma unroll
+#pragma unroll
               for (int x = 0; x < 8; ++x) st_shared_v4(tile + h * 16384 + r * 128 + ((x + lane) & 7) * 16, 0, 0, 0, 0);
           fence_proxy_async_smem();
           warp_arrive(&sm.kv_clean[slot], lane);
@@ -1179,7 +1193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             warp_arrive(&sm.o_free[st], lane);  // (the next item's products may begin)
           }
           if (anyp) {
-            // v rows that the guard has replaced, added by those who see them
+            // what the guard has taken out of v rows, added by those who see them
 #pragma unroll 1
             for (int x = 0; x < 12; ++x) {
               uint32_t bits = (&sm.poison[k & 1][0][0])[x];

@@ -157,3 +157,30 @@ def test_prompt_offsets_out_of_range_are_clamped():
     mx.attn_prompt(q, k, v, cu, out=out)
     assert bool(torch.isfinite(out).all())
     check(out, q[:30], k[:30], v[:30], [30], 1 / 8, "first")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,Hq,Hkv", [
+    ([1], 8, 1), ([300], 7, 1), ([0, 255, 256, 257, 0], 8, 8), ([700, 3, 130], 64, 8), ([513], 14, 2), ([90, 41], 71, 1),
+    ([1100, 600], 32, 16),
+])
+def test_prompt_is_the_same_in_a_larger_batch(D, lens, Hq, Hkv):
+    """However the rows are grouped (a batch of more than 32 sequences, a few
+    long or short ones), a row's result is the same, and within the bound; so
+    is what a NaN reaches."""
+    d = dev()
+    T = sum(lens)
+    q, k, v = inputs(20 + T, T, Hq, Hkv, D, d)
+    cu = offsets(lens, d)
+    many = torch.cat([torch.zeros(20, dtype=torch.int32, device=d), cu, cu[-1:].expand(20)])
+    out = mx.attn_prompt(q, k, v, many)
+    check(out, q, k, v, lens, 1 / math.sqrt(D), f"{lens} {Hq}/{Hkv} D={D}, 40 empty sequences more")
+    assert torch.equal(mx.attn_prompt(q, k, v, cu), out)
+    longest = max(range(len(lens)), key=lambda b: lens[b])
+    at = sum(lens[:longest]) + lens[longest] // 2
+    v[at, 0, 1] = float("nan")
+    a, b = mx.attn_prompt(q, k, v, many), mx.attn_prompt(q, k, v, cu)
+    assert torch.equal(a.isnan(), b.isnan()) and torch.equal(a.nan_to_num(), b.nan_to_num())
+    sees = torch.zeros(T, Hq, D, dtype=torch.bool, device=d)
+    sees[at:sum(lens[:longest + 1]), :Hq // Hkv, 1] = True
+    assert bool(a[sees].isnan().all()) and torch.equal(a[~sees], out[~sees])

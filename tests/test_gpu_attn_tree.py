@@ -232,3 +232,23 @@ def test_one_node_trees_are_decoding():
     for at, o, b in attn_ref.prompt(q, k, v, [n], 1 / math.sqrt(D), lambda m: torch.tensor([m - 1])):
         attn_ref.assert_within(out, o, b, "decode")
         attn_ref.assert_within(prompt[at], o, b, "prompt")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_tree_a_value_that_is_not_finite_leaves_its_row_s_others(D, bad):
+    """One channel of a node's v is NaN or infinite: the nodes that see it have
+    all other channels as if that one were finite."""
+    c = Case([150, 20, 0], [12, 8, 64], 8, 2, D, 16, seed=9)
+    ref = c.run()
+    for at, heads, ch in ((5, 0, 7), (13, 1, D - 1), (30, 0, 0)):
+        c.v[at, heads, ch] = bad
+    out = c.run()
+    hit = torch.zeros(out.shape, dtype=torch.bool, device=out.device)
+    first = [0, 12, 20]
+    for at, heads, ch in ((5, 0, 7), (13, 1, D - 1), (30, 0, 0)):
+        b = max(i for i in range(3) if first[i] <= at)
+        lo, hi = first[b], first[b] + c.nodes[b]
+        hit[lo:hi, heads * 4:heads * 4 + 4, ch] = ((c.mask[lo:hi] >> (at - lo)) & 1).bool()[:, None]
+    assert bool(hit.any()) and torch.equal(out[~hit], ref[~hit])
+    assert not bool(torch.isfinite(out[hit]).any())
