@@ -5,7 +5,8 @@ in C++ (``csrc/bind.cpp``), since these calls are short.
 
 Tensors of heads are (tokens, heads, D) bf16 with a unit inner stride; the
 other strides are free (multiples of 8 elements), so a slice of the packed qkv
-projection is passed as it is.  A paged cache is a `KVCache`.
+projection is passed as it is.  A paged cache is a `KVCache`.  A call runs on
+`stream` (None = the current one); what it allocates belongs to that stream.
 """
 from __future__ import annotations
 
@@ -13,7 +14,7 @@ import ctypes
 
 import torch
 
-from . import MxgError, lib, workspace
+from . import MxgError, lib
 
 MAX_SEQS, MAX_NODES = 4096, 64
 
@@ -112,9 +113,6 @@ def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: t
     return (_mod or _load()).attn_prompt(q, k, v, cu_seqlens, scale, out, dev_status, timeout_ms, debug_stall, stream)
 
 
-_tree_ws: dict = {}
-
-
 def mxg_attn_tree_workspace_bytes(D: int) -> int:
     """Workspace of attn_tree on the current device (it does not depend on the
     batch)."""
@@ -129,18 +127,10 @@ def attn_tree(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_nodes: torch
     k, v (N, Hkv, D), sequence b = nodes cu_nodes[b] .. cu_nodes[b+1] - 1 (at
     most 64), mask (N,) int64: bit j = node sees the sequence's node j; the
     cached tokens 0 .. ctx_len[b] - 1 of the pages block_table[b] (int32) are
-    seen by all.  ws None = the device's shared workspace (calls on several
-    streams need their own, mxg_attn_tree_workspace_bytes).  Returns out
-    (N, Hq, D)."""
-    m = _mod or _load()
-    if ws is None:
-        d, dev = q.shape[-1], q.device
-        n = _tree_ws.get(d)
-        if n is None:
-            n = _tree_ws[d] = max(mxg_attn_tree_workspace_bytes(d), 1)
-        ws = workspace(n, dev)
-    return m.attn_tree(q, k, v, cu_nodes, mask, cache.k, cache.v, block_table, ctx_len, scale, out, dev_status,
-                       timeout_ms, debug_stall, ws, stream)
+    seen by all.  ws None = mxg_attn_tree_workspace_bytes(D) bytes from torch's
+    allocator.  Returns out (N, Hq, D)."""
+    return (_mod or _load()).attn_tree(q, k, v, cu_nodes, mask, cache.k, cache.v, block_table, ctx_len, scale, out,
+                                       dev_status, timeout_ms, debug_stall, ws, stream)
 
 
 def kv_append(k: torch.Tensor, v: torch.Tensor, cu_nodes: torch.Tensor, accept: torch.Tensor, cache: KVCache,

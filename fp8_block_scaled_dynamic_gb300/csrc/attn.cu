@@ -560,7 +560,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   Smem<D, TREE> &sm = *reinterpret_cast<Smem<D, TREE> *>(smem_raw);
   const uint32_t base = smem_addr(smem_raw);
   if (base & 1023u) {  // the swizzled tiles need it (uniform over the grid)
-    if (threadIdx.x == 0 && p.status) atomicOr(p.status, kSmemLayout);
+    if (threadIdx.x == 0) {
+      pdl_wait();
+      if (TREE) reinterpret_cast<JoinItem *>(p.ws)[blockIdx.x].rows = 0;
+      if (p.status) atomicOr(p.status, kSmemLayout);
+    }
     return;
   }
   const uint32_t q_smem = base + kHead, kv_smem = q_smem + 2 * C::kTile;

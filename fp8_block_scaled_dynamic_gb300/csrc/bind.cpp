@@ -2,7 +2,7 @@
 //
 // The small calls of a decode step run for 3-10 us on the GPU; marshalling ten
 // tensors through ctypes took 17-27 us of host time a call, so these entry
-// points read the tensors in C++ (3 us a call, attn_tree 6).  Like the rest of the binding
+// points read the tensors in C++ (3 us a call, attn_tree 7).  Like the rest of the binding
 // it checks dtypes and shapes, allocates missing outputs with torch and calls
 // the C entry point of the same name.
 #define PY_SSIZE_T_CLEAN
@@ -12,10 +12,12 @@
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_like.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
+#include <optional>
 #include <stdexcept>
 #include <string>
 
@@ -91,15 +93,23 @@ mxg_kv_cache cache_of(PyObject *ko, PyObject *vo, int64_t Hkv, int64_t D) {
           as_int(k.size(-3), "slots of a page")};
 }
 
-mxg_stream_t stream_of(PyObject *o) {
-  if (!given(o)) return reinterpret_cast<mxg_stream_t>(c10::cuda::getCurrentCUDAStream().stream());
-  PyObject *a = PyObject_GetAttrString(o, "cuda_stream");
-  if (!a) throw Raised();
-  void *s = PyLong_AsVoidPtr(a);
-  Py_DECREF(a);
-  if (!s && PyErr_Occurred()) throw Raised();
-  return reinterpret_cast<mxg_stream_t>(s);
-}
+// The stream of a call, made torch's current one meanwhile, so that what is
+// allocated here belongs to the stream that writes it.
+struct Stream {
+  std::optional<c10::cuda::CUDAStreamGuard> on;
+  explicit Stream(PyObject *o) {
+    if (!given(o)) return;
+    PyObject *a = PyObject_GetAttrString(o, "cuda_stream");
+    if (!a) throw Raised();
+    void *x = PyLong_AsVoidPtr(a);
+    Py_DECREF(a);
+    if (!x && PyErr_Occurred()) throw Raised();
+    on.emplace(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(x), c10::cuda::current_device()));
+  }
+  mxg_stream_t handle() const {
+    return reinterpret_cast<mxg_stream_t>(c10::cuda::getCurrentCUDAStream().stream());
+  }
+};
 
 double number(PyObject *o) {
   const double x = PyFloat_AsDouble(o);
@@ -141,6 +151,7 @@ void count(Py_ssize_t n, Py_ssize_t want) { need(n == want, "wrong number of arg
 PyObject *py_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded([&]() -> PyObject * {
     count(n, 16);
+    const Stream stream(a[15]);
     const at::Tensor &q = heads_of(a[0], "q"), &k = heads_of(a[1], "k");
     const int64_t T = q.size(0), Hq = q.size(1), D = q.size(2), Hkv = k.size(1);
     need(k.size(0) == T && k.size(2) == D, "k must be (T, Hkv, D)");
@@ -178,7 +189,7 @@ PyObject *py_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
     check("qk_norm_rope",
           qk_norm_rope(&qh, &kh, as_int(T, "tokens"), as_int(Hq, "heads"), as_int(Hkv, "heads"), as_int(D, "channels"),
                        w[0], w[1], (float)number(a[6]), pos, cs, max_pos, rot, (int)integer(a[7]), &qoh, &koh,
-                       cached ? &vh : nullptr, cached ? &c : nullptr, slots, status_word(a[14]), stream_of(a[15])));
+                       cached ? &vh : nullptr, cached ? &c : nullptr, slots, status_word(a[14]), stream.handle()));
     PyObject *qp = THPVariable_Wrap(qo), *kp = THPVariable_Wrap(ko);
     return Py_BuildValue("NN", qp, kp);
   });
@@ -213,11 +224,12 @@ Attn attn_of(PyObject *const *a, int at_) {
 PyObject *py_prompt(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded([&]() -> PyObject * {
     count(n, 10);
+    const Stream stream(a[9]);
     const Attn r = attn_of(a, 4);
     const at::Tensor &cu = tensor(a[3], "cu_seqlens", at::kInt, 1);
     check("attn_prompt", attn_prompt(&r.q, &r.k, &r.v, static_cast<int *>(ptr(cu)), as_int(cu.numel() - 1, "sequences"),
                                      as_int(r.T, "tokens"), as_int(r.Hq, "heads"), as_int(r.Hkv, "heads"),
-                                     as_int(r.D, "channels"), r.scale, &r.out, &r.opts, stream_of(a[9])));
+                                     as_int(r.D, "channels"), r.scale, &r.out, &r.opts, stream.handle()));
     return THPVariable_Wrap(r.o);
   });
 }
@@ -226,8 +238,13 @@ PyObject *py_prompt(PyObject *, PyObject *const *a, Py_ssize_t n) {
 PyObject *py_tree(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded([&]() -> PyObject * {
     count(n, 16);
+    const Stream stream(a[15]);
     Attn r = attn_of(a, 9);
-    const at::Tensor &ctx = tensor(a[8], "ctx_len", at::kInt, 1), &ws = tensor(a[14], "ws", at::kByte, 1);
+    const at::Tensor &ctx = tensor(a[8], "ctx_len", at::kInt, 1);
+    // (back with the allocator on return, for what follows in the stream)
+    const at::Tensor ws = given(a[14]) ? tensor(a[14], "ws", at::kByte, 1)
+                                       : at::empty({(int64_t)mxg_attn_tree_workspace_bytes((int)r.D)},
+                                                   r.o.options().dtype(at::kByte));
     const int64_t B = ctx.numel();
     const int *cu = index<int>(a[3], "cu_nodes", at::kInt, B + 1);
     const uint64_t *mask = index<uint64_t>(a[4], "mask", at::kLong, r.T);
@@ -238,7 +255,7 @@ PyObject *py_tree(PyObject *, PyObject *const *a, Py_ssize_t n) {
     check("attn_tree",
           attn_tree(&r.q, &r.k, &r.v, cu, mask, as_int(B, "sequences"), as_int(r.T, "nodes"), &c, t.p, t.ld, t.cols,
                     static_cast<int *>(ptr(ctx)), as_int(r.Hq, "heads"), as_int(r.Hkv, "heads"),
-                    as_int(r.D, "channels"), r.scale, &r.out, &r.opts, stream_of(a[15])));
+                    as_int(r.D, "channels"), r.scale, &r.out, &r.opts, stream.handle()));
     return THPVariable_Wrap(r.o);
   });
 }
@@ -247,6 +264,7 @@ PyObject *py_tree(PyObject *, PyObject *const *a, Py_ssize_t n) {
 PyObject *py_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded([&]() -> PyObject * {
     count(n, 11);
+    const Stream stream(a[10]);
     if (!THPVariable_Check(a[0])) bad("k must be a tensor");
     const int dim = THPVariable_Unpack(a[0]).dim() == 4 ? 4 : 3;
     const at::Tensor &k = tensor(a[0], "k", at::kBFloat16, dim), &v = tensor(a[1], "v", at::kBFloat16, dim);
@@ -265,7 +283,7 @@ PyObject *py_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
           kv_append(&kh, dim == 4 ? k.stride(0) : 0, &vh, dim == 4 ? v.stride(0) : 0, cu, as_int(B, "sequences"),
                     as_int(N, "nodes"), acc.p, acc.ld, acc.cols, &c, t.p, t.ld, t.cols, static_cast<int *>(ptr(ctx)),
                     as_int(Hkv, "heads"), as_int(D, "channels"), static_cast<int *>(ptr(out)), status_word(a[9]),
-                    stream_of(a[10])));
+                    stream.handle()));
     return THPVariable_Wrap(out);
   });
 }

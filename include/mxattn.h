@@ -66,7 +66,8 @@ typedef struct {
                             overlap on the GPU need separate workspaces. */
     size_t ws_bytes;
     int *dev_status;     /* optional device int; kernels OR MXG_DEV_* bits into it */
-    uint32_t timeout_ms; /* limit of every device-side wait; 0 = 1000 ms */
+    uint32_t timeout_ms; /* limit of every device-side wait; 0 = 1000 ms.  The longest legitimate
+                            one lasts as long as a CTA's keys: about 2 us for 128 of them */
     int debug_stall;     /* test hook: 1 makes the first wait of every CTA one that nothing
                             satisfies, so that the timeout path runs (no fault, no hang) */
 } mxg_attn_opts;

@@ -252,3 +252,20 @@ def test_tree_a_value_that_is_not_finite_leaves_its_row_s_others(D, bad):
         hit[lo:hi, heads * 4:heads * 4 + 4, ch] = ((c.mask[lo:hi] >> (at - lo)) & 1).bool()[:, None]
     assert bool(hit.any()) and torch.equal(out[~hit], ref[~hit])
     assert not bool(torch.isfinite(out[hit]).any())
+
+
+def test_tree_streams_side_by_side():
+    """Calls on two streams at once, outputs and scratch from the allocator:
+    neither disturbs the other, nor what the current stream allocates next."""
+    a = Case([9000, 300, 2500], [8, 1, 30], 16, 2, 128, 64, seed=12)
+    b = Case([4000, 5000], [3, 17], 16, 2, 128, 64, seed=13)
+    want = [a.run(), b.run()]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[], []]
+    for _ in range(6):
+        for i, c in enumerate((a, b)):
+            outs[i].append(c.run(stream=streams[i]))
+        torch.full((24 << 20,), 1.0, device=a.q.device)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for got, w in zip(outs, want) for o in got)
