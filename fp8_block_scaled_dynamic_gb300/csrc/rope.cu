@@ -30,15 +30,37 @@ __device__ __forceinline__ void unpack8(const uint4 &w, float (&x)[8]) {
 // rotation needs no exchange between lanes and the mean log2 L shuffles.  A
 // CTA works on one token: each thread loads its 8 cosines and sines once for
 // all the heads it takes, behind the loads of the first kU heads.
-// 8192 tokens of 64 + 8 heads of 128, with the cache (353 MB): 62.9 us, 5.6
-// TB/s of 6.8 measured for a copy.  Threads of a CTA, heads in flight and CTAs
-// per SM were swept: 64, 3, 12 (the registers' limit); 256 threads take 79 us,
-// four heads in flight spill (81 us).
+// 8192 tokens of 64 + 8 heads of 128, with the cache (353 MB): 57.4 us, 6.1
+// TB/s of 6.8 measured for a copy.  Issue slots count beside the loads in
+// flight: two-value arithmetic, and no bounds of a head's units where it fills
+// its lanes (FULL), took 63.5 us to 59.3.  Threads of a CTA, heads in flight and
+// CTAs per SM were swept: 64, 2, 14; 3 heads and 12 CTAs take 59.3 us, 1 and 18
+// 60.8, 2 and 16 (fewer registers) 58.1; 32 threads 62.1, 128 threads 61.5.
 constexpr int kRopeThreads = 64;
-constexpr int kU = 3;
+constexpr int kU = 2;
 
-template <int L, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads, 12) rope_kernel(const RopeParams p) {
+// Two fp32 operations in one instruction: s += a * b, a *= b, a -= b.
+__device__ __forceinline__ void fma2(float &s0, float &s1, float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 a, b, s;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 s, {%0, %1};\n\t"
+      "fma.rn.f32x2 s, a, b, s;\n\tmov.b64 {%0, %1}, s;\n\t}"
+      : "+f"(s0), "+f"(s1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void mul2(float &a0, float &a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+      "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void sub2(float &a0, float &a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+      "sub.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1));
+}
+
+template <int L, bool INTER, bool FULL>
+__global__ void __launch_bounds__(kRopeThreads, 14) rope_kernel(const RopeParams p) {
   constexpr unsigned kFull = 0xFFFFFFFFu;
   constexpr int kGroups = kRopeThreads / L;
   pdl_trigger();
@@ -48,7 +70,7 @@ __global__ void __launch_bounds__(kRopeThreads, 12) rope_kernel(const RopeParams
   // this lane's units of a head; past hc (half-split) they are not rotated
   const bool turned = INTER ? 16 * c < p.rot : c < hc;
   const int ua = INTER ? 2 * c : turned ? c : 2 * c, ub = INTER || !turned ? ua + 1 : c + hc;
-  const bool ina = ua < units, inb = ub < units;
+  const bool ina = FULL || ua < units, inb = FULL || ub < units;
   const int heads_qk = p.Hq + p.Hkv, heads = heads_qk + (p.v.ptr ? p.Hkv : 0);
   const int step = gridDim.y * kGroups;
   pdl_wait();
@@ -61,7 +83,7 @@ __global__ void __launch_bounds__(kRopeThreads, 12) rope_kernel(const RopeParams
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const int h = h0 + u * step + g;
-      xa[u] = xb[u] = make_uint4(0, 0, 0, 0);
+      if (!FULL) xa[u] = xb[u] = make_uint4(0, 0, 0, 0);
       if (h < heads) {
         const uint16_t *src = h < p.Hq       ? q + h * p.q.head
                               : h < heads_qk ? k + (h - p.Hq) * p.k.head
@@ -109,18 +131,29 @@ __global__ void __launch_bounds__(kRopeThreads, 12) rope_kernel(const RopeParams
       float a[8], b[8], w[8], ss = 0.0f;
       unpack8(xa[u], a);
       unpack8(xb[u], b);
+      float s2 = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(b[j], b[j], fmaf(a[j], a[j], ss));
+      for (int j = 0; j < 8; j += 2) {
+        fma2(ss, s2, a[j], a[j + 1], a[j], a[j + 1]);
+        fma2(ss, s2, b[j], b[j + 1], b[j], b[j + 1]);
+      }
+      ss += s2;
 #pragma unroll
       for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o, L);
       if (gain) {
         const float r = rsqrtf(fmaf(ss, inv_d, p.eps));
         unpack8(wa, w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) a[j] = a[j] * r * w[j];
+        for (int j = 0; j < 8; j += 2) {
+          mul2(a[j], a[j + 1], r, r);
+          mul2(a[j], a[j + 1], w[j], w[j + 1]);
+        }
         unpack8(wb, w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) b[j] = b[j] * r * w[j];
+        for (int j = 0; j < 8; j += 2) {
+          mul2(b[j], b[j + 1], r, r);
+          mul2(b[j], b[j + 1], w[j], w[j + 1]);
+        }
       }
       if (turned) {
         if (INTER) {
@@ -134,10 +167,13 @@ __global__ void __launch_bounds__(kRopeThreads, 12) rope_kernel(const RopeParams
           }
         } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float x = a[j], y = b[j];
-            a[j] = x * cs[j] - y * sn[j];
-            b[j] = y * cs[j] + x * sn[j];
+          for (int j = 0; j < 8; j += 2) {
+            float x0 = a[j], x1 = a[j + 1], y0 = b[j], y1 = b[j + 1];
+            mul2(a[j], a[j + 1], cs[j], cs[j + 1]);
+            mul2(y0, y1, sn[j], sn[j + 1]);
+            sub2(a[j], a[j + 1], y0, y1);
+            mul2(b[j], b[j + 1], cs[j], cs[j + 1]);
+            fma2(b[j], b[j + 1], x0, x1, sn[j], sn[j + 1]);
           }
         }
       }
@@ -177,8 +213,11 @@ cudaError_t rope_launch(const RopeParams &p, bool inter, int sm_count, cudaStrea
   cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)p.T, (unsigned)split), dim3(kRopeThreads), 0, stream);
   cudaLaunchAttribute attr[1];
   attach_pdl(cfg, attr);
-  return inter ? cudaLaunchKernelEx(&cfg, rope_kernel<L, true>, p)
-               : cudaLaunchKernelEx(&cfg, rope_kernel<L, false>, p);
+  if (p.D == 16 * L)
+    return inter ? cudaLaunchKernelEx(&cfg, rope_kernel<L, true, true>, p)
+                 : cudaLaunchKernelEx(&cfg, rope_kernel<L, false, true>, p);
+  return inter ? cudaLaunchKernelEx(&cfg, rope_kernel<L, true, false>, p)
+               : cudaLaunchKernelEx(&cfg, rope_kernel<L, false, false>, p);
 }
 
 // --------------------------------------------------------------- kv_append
