@@ -642,7 +642,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int page_shift = TREE ? 31 - __clz(p.cache.page_size) : 0, box_shift = TREE ? min(page_shift, 7) : 7;
       if (TREE) {
         // a small batch's page table into L1, while the items are worked out
-        // (a line a lane: the first load then does not wait for L2 twice)
+        // (a line a lane: the first load then does not wait for L2 twice; a table
+        // of no columns has a row stride of 0, and nothing is prefetched)
         const long long ints = (long long)(p.B - 1) * p.ld_table + p.table_cols;
         if (lane * 32LL < ints) prefetch_l1(p.table + lane * 32);
       }

@@ -204,7 +204,7 @@ mxg_status attn_tree(const mxg_heads *q, const mxg_heads *k, const mxg_heads *v,
   p.mask = reinterpret_cast<const unsigned long long *>(mask);
   p.table = block_table;
   p.ctx = ctx_len;
-  p.ld_table = ld_table;
+  p.ld_table = table_cols > 0 ? ld_table : 0;  // (no columns: the table may be null, and nothing of it is touched)
   p.table_cols = table_cols;
   p.ws = static_cast<float *>(opts->workspace);
   const cudaError_t e = mxg::launch_attn_tree(p, sm, reinterpret_cast<cudaStream_t>(stream));
