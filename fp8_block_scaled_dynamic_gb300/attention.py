@@ -138,7 +138,8 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cu_nodes: torch.Tensor, accept: 
     """The accepted nodes into the cache, in every layer: k, v (layers, N, Hkv,
     D), or (N, Hkv, D) with a one-layer cache; accept (B, most) int32: the
     nodes, counted from the sequence's first, that become tokens ctx_len[b],
-    ctx_len[b] + 1, ... (the first negative entry ends the list).  Returns
-    ctx_out (B,) = ctx_len + accepted."""
+    ctx_len[b] + 1, ... (the first negative entry ends the list, and so does
+    one that cannot be written: no such node, or no page for the token).
+    Returns ctx_out (B,) = ctx_len + tokens written."""
     return (_mod or _load()).kv_append(k, v, cu_nodes, accept, cache.k, cache.v, block_table, ctx_len, ctx_out,
                                        dev_status, stream)

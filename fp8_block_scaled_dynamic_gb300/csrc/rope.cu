@@ -225,8 +225,8 @@ cudaError_t rope_launch(const RopeParams &p, bool inter, int sm_count, cudaStrea
 // large batch, latency a step.  One CTA per (sequence, layer): its threads
 // work out where up to kRows accepted rows come from and go to, then copy them
 // as 16-byte units, a thread the same place of every row it takes.
-// 64 sequences of up to 8 rows x 32 layers (87 MB): 17.7 us, 4.9 TB/s (a page
-// of reading before the first row moves; two layers a CTA 17.2, four 18.4); a
+// 64 sequences of up to 8 rows x 32 layers (87 MB): 17.1 us, 5.1 TB/s (list,
+// page and row are read one after another before the first row moves); a
 // step's 5 layers 3.0 us, of which 2.5 are a launch (128 threads 3.6).
 constexpr int kAppendThreads = 256;
 constexpr int kRows = 64;
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   bool more = true;
   while (more && done < p.max_accept) {
     const int n = min(kRows, p.max_accept - done);
-    bool bad = false;
+    bool refused = false;
     if (threadIdx.x < kRows) {
       const int i = threadIdx.x;
       const int a = i < n ? __ldg(acc + done + i) : -1;
@@ -258,26 +258,27 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
       const long long col = at / p.cache.page_size;
       const bool in = i < n && ctx >= 0 && col < p.table_cols;
       const int pg = in ? __ldg(p.table + (size_t)b * p.ld_table + col) : -1;
-      const unsigned neg = __ballot_sync(0xFFFFFFFFu, a < 0);
-      if ((i & 31) == 0) s_end[i >> 5] = neg ? __ffs(neg) - 1 : 32;
-      bad = a >= n1 - n0 || pg < 0 || pg >= p.cache.pages;
+      refused = a >= 0 && (a >= n1 - n0 || pg < 0 || pg >= p.cache.pages);
+      const unsigned stop = __ballot_sync(0xFFFFFFFFu, a < 0 || refused);
+      if ((i & 31) == 0) s_end[i >> 5] = stop ? __ffs(stop) - 1 : 32;
       s_src[i] = n0 + a;
-      s_dst[i] = bad || a < 0 ? -1 : pg * p.cache.page + (at - col * p.cache.page_size) * p.cache.slot;
+      s_dst[i] = pg * p.cache.page + (at - col * p.cache.page_size) * p.cache.slot;  // (used before the end alone)
     }
     __syncthreads();
+    // The list ends at its first negative entry and at the first one that
+    // cannot be written: a sequence never counts a token that is not there.
     const int rows = s_end[0] < 32 ? s_end[0] : 32 + s_end[1];
     more = rows == kRows;
     // (a bad entry past the end of the list is nobody's)
-    if (bad && (int)threadIdx.x < rows && p.status && layer == 0) atomicOr(p.status, kBadIndex);
+    if (refused && (int)threadIdx.x == rows && p.status && layer == 0) atomicOr(p.status, kBadIndex);
     for (int u = u0; u < per_row && rl < side; u += kAppendThreads) {
       const int h = u / unit, c = u - h * unit;
       const uint16_t *k = p.k.ptr + layer * p.k_layer + h * p.k.head + c * 8;
       const uint16_t *v = p.v.ptr + layer * p.v_layer + h * p.v.head + c * 8;
       const long long to = layer * p.cache.layer + h * p.cache.head + c * 8;
-#pragma unroll 4
+#pragma unroll 1  // (two rows at a time 18.3 us for the large batch)
       for (int i = rl; i < rows; i += side) {
         const long long dst = s_dst[i], src = s_src[i];
-        if (dst < 0) continue;
         const uint4 kv = *reinterpret_cast<const uint4 *>(k + src * p.k.tok);
         const uint4 vv = *reinterpret_cast<const uint4 *>(v + src * p.v.tok);
         *reinterpret_cast<uint4 *>(p.cache.k + dst + to) = kv;

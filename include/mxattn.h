@@ -146,12 +146,13 @@ mxg_status attn_tree(const mxg_heads *q, const mxg_heads *k, const mxg_heads *v,
  * ends the list) names the node that becomes token ctx_len[b] + i of the
  * sequence (counted from cu_nodes[b]); its k and v (layer l at
  * l * k_layer_stride / v_layer_stride elements) are copied to that token's
- * slot, and ctx_out[b] = ctx_len[b] + (accepted).  The page of every slot
+ * slot, and ctx_out[b] = ctx_len[b] + (tokens written).  The page of every slot
  * written must be in the block table, and no two sequences may write the same
  * page.  ctx_out (nullable) must not be ctx_len.
  * D % 8 == 0, 8 <= D <= 1024; cache->layers layers; max_accept >= 0.
  * Out of range: a node index at or past the sequence's nodes, or a token whose
- * page is not in the table or not in the cache, is not written. */
+ * page is not in the table or not in the cache, ends the list as a negative
+ * entry does: neither it nor what follows is written or counted. */
 mxg_status kv_append(const mxg_heads *k, int64_t k_layer_stride, const mxg_heads *v,
                      int64_t v_layer_stride, const int *cu_nodes, int B, int N, const int *accept,
                      int ld_accept, int max_accept, const mxg_kv_cache *cache,
