@@ -5,8 +5,11 @@
 //   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q.k_j - m)
 // over the keys j the row sees, in one pass over the keys with a running
 // reference m (a running maximum, moved only when it falls behind by more
-// than 2^8: the weights then stay below 2^8, and fp32 sums and bf16 weights
-// lose nothing by it).
+// than 2^8: the weights then stay below 2^8, and fp32 sums lose nothing by it).
+// The weights are rounded to bf16 for their product with v (the tensor core's
+// operand type).  Those roundings are independent of one another and weigh as
+// much as the result's own: a row of random values is off by 0.0020 to 0.0024
+// of its length, of which 0.0017 are the result's rounding.
 //
 // Tiles.  The G = Hq / Hkv query heads that share a kv head are rows of one
 // tile: 128 / G tokens x G heads (so a decode step fills rows with heads, and
@@ -1134,8 +1137,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st_wait();
           tc_fence_before();
           warp_arrive(&sm.p_ready[x4], lane);
-          // the sum, while the weights are multiplied
-          float sum[4] = {l, 0.0f, 0.0f, 0.0f};
+          // The sum, while the weights are multiplied: of the weights in fp32, but
+          // of the tile's largest as the product has it, rounded.  Where one key
+          // has most of a row, its rounding then cancels: with a reference 2^4.3
+          // behind, such a row's error falls from 0.0030 of its length to 0.0018.
+          // 8192 tokens take 672 us, 669 without this; the sum of all the rounded
+          // weights gains nothing more and takes 702.
+          const float most = ex2(fmaf(top, c, ref));
+          float sum[4] = {l + (__uint_as_float(pack_bf16x2(0.0f, most)) - most), 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int x = 0; x < 4; ++x)
 #pragma unroll

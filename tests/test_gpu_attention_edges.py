@@ -1,5 +1,5 @@
 """The attention operators at the edges of what they take: tables without
-columns, accepted nodes that cannot be written."""
+columns, accepted nodes that cannot be written, rows that one key has nearly all of."""
 import math
 
 import pytest
@@ -8,7 +8,7 @@ import torch
 import attn_ref
 import fp8_block_scaled_dynamic_gb300 as mx
 from gpu_util import dev
-from test_gpu_attn_tree import offsets, randn, tree_masks
+from test_gpu_attn_tree import Case, offsets, randn, tree_masks
 
 pytestmark = pytest.mark.gpu
 
@@ -74,3 +74,65 @@ def test_append_counts_only_what_it_writes(D, page):
                        torch.arange(6, dtype=torch.int32, device=d)[:, None], torch.zeros(6, dtype=torch.int32, device=d),
                        dev_status=status)
     assert mx.mxg_query_status(status) == 0 and got.tolist() == [1] * 6
+
+
+# One key has nearly all of a row, and comes after the running reference was
+# set by another: its weight is 2^x, x between 5 and 8, not 1, and is rounded to
+# bf16 for the product.  The values are alike over the keys, so the row's result
+# is that value: exactly, if the heavy weight's rounding is in the sum too.
+# What else there is: the first key's weight, 1, and a few hundred of at most
+# 2^-20, whose roundings move the result by 2^-25; the fp32 sums by 300 2^-23;
+# half a unit of bf16 is 2^-9.
+
+def heavy_key(T, H, D, first, heavy, seed):
+    """Keys (T, H, D) along one direction: 0 at `first`, 1 at `heavy`, else -4;
+    and queries' lengths along it for scores of 3.6 to 5.4 with the heavy one."""
+    k = torch.full((T, H, 1), -4.0)
+    k[first], k[heavy] = 0.0, 1.0
+    e = torch.zeros(D)
+    e[seed % D] = 1.0
+    return (k * e).bfloat16(), e
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,Hq,Hkv", [([600, 420], 8, 2), ([400] * 5, 8, 8), ([300] * 40, 2, 1)])
+def test_prompt_one_heavy_key(D, lens, Hq, Hkv):
+    d = dev()
+    T, at = sum(lens), 0
+    g = torch.Generator().manual_seed(T + D)
+    q = (3.6 + 1.8 * torch.rand(T, Hq, 1, generator=g)).bfloat16()
+    k = torch.empty(T, Hkv, D, dtype=torch.bfloat16)
+    rows = []
+    for n in lens:
+        j = 128 + int(torch.randint(0, n - 130, (1,), generator=g))
+        k[at:at + n], e = heavy_key(n, Hkv, D, 0, j, 3)
+        rows += range(at + j, at + n)
+        at += n
+    one = randn(33, 1, Hkv, D).to(d)
+    out = mx.attn_prompt((q * e).bfloat16().to(d), k.to(d), one.expand(T, -1, -1).contiguous(), offsets(lens, d), scale=1.0)
+    off = out[rows] != one.repeat_interleave(Hq // Hkv, 1)
+    assert not bool(off.any()), f"{int(off.sum())} of {off.numel()} values are not the value"
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,n,ctx", [(40, 3, 300), (100, 16, 130)])
+def test_tree_one_heavy_key(D, B, n, ctx):
+    """Every node sees the context and itself; its own key is the heavy one."""
+    Hq, Hkv, page = 16, 8, 32
+    c = Case([ctx] * B, [n] * B, Hq, Hkv, D, page, seed=36)
+    d = c.q.device
+    kc, e = heavy_key(ctx, Hkv, D, 0, 0, 5)
+    kc[0] = 0
+    j = torch.arange(ctx)
+    for b in range(B):
+        c.kc[c.tab[b].long()[(j // page).to(d)], (j % page).to(d)] = kc.to(d)
+    g = torch.Generator().manual_seed(D + B)
+    N = B * n
+    c.q = ((3.6 + 1.8 * torch.rand(N, Hq, 1, generator=g)).bfloat16() * e).bfloat16().to(d)
+    c.k = e.bfloat16().expand(N, Hkv, D).contiguous().to(d)
+    c.mask = torch.tensor([1 << i for i in range(n)] * B, dtype=torch.int64, device=d)
+    one = randn(35, 1, Hkv, D).to(d)
+    c.v = one.expand(N, -1, -1).contiguous()
+    c.vc = one[0].expand(c.vc.shape).contiguous()
+    off = c.run(scale=1.0) != one.repeat_interleave(Hq // Hkv, 1)
+    assert not bool(off.any()), f"{int(off.sum())} of {off.numel()} values are not the value"
