@@ -72,7 +72,8 @@ def _load():
 class KVCache:
     """A paged key/value cache: k and v of shape (pages, page_size, Hkv, D), or
     (layers, pages, page_size, Hkv, D), bf16, with equal strides.  It refers to
-    the two tensors and owns nothing else."""
+    the two tensors and owns nothing else.  kv_append takes all layers at once;
+    qk_norm_rope and attn_tree take one, and refuse a cache of several."""
 
     __slots__ = ("k", "v")
 
@@ -97,7 +98,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, pos: torch.Tensor | None = No
     (T, Hq, D) and k (T, Hkv, D); cos_sin (max_pos, rot) f32 with rows
     [cos | sin], pos (T,) int32.  With cache, k and v (T, Hkv, D) also go to
     the slots (T,) int64 (page * page_size + place; negative = not written) of
-    its (first) layer.  q_out=q and k_out=k work in place.  Returns
+    this one-layer cache (cache.layer(i)).  q_out=q and k_out=k work in place.  Returns
     (q_out, k_out)."""
     ck, cv = (None, None) if cache is None else (cache.k, cache.v)
     return (_mod or _load()).qk_norm_rope(q, k, pos, cos_sin, wq, wk, eps, interleaved, q_out, k_out, v, ck, cv, slots,
@@ -127,7 +128,7 @@ def attn_tree(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_nodes: torch
     k, v (N, Hkv, D), sequence b = nodes cu_nodes[b] .. cu_nodes[b+1] - 1 (at
     most 64), mask (N,) int64: bit j = node sees the sequence's node j; the
     cached tokens 0 .. ctx_len[b] - 1 of the pages block_table[b] (int32) are
-    seen by all.  ws None = mxg_attn_tree_workspace_bytes(D) bytes from torch's
+    seen by all.  cache: one layer (cache.layer(i)).  ws None = mxg_attn_tree_workspace_bytes(D) bytes from torch's
     allocator.  Returns out (N, Hq, D)."""
     return (_mod or _load()).attn_tree(q, k, v, cu_nodes, mask, cache.k, cache.v, block_table, ctx_len, scale, out,
                                        dev_status, timeout_ms, debug_stall, ws, stream)

@@ -78,13 +78,15 @@ int as_int(int64_t n, const char *what) {
   return (int)n;
 }
 
-// cache: a KVCache's k and v, (pages, page_size, Hkv, D) or with a leading layers dimension
-mxg_kv_cache cache_of(PyObject *ko, PyObject *vo, int64_t Hkv, int64_t D) {
+// cache: a KVCache's k and v, (pages, page_size, Hkv, D) or with a leading
+// layers dimension; one_layer: of a call that takes a single layer
+mxg_kv_cache cache_of(PyObject *ko, PyObject *vo, int64_t Hkv, int64_t D, bool one_layer) {
   if (!ko || !THPVariable_Check(ko)) bad("a cache holds two tensors");
   const int dim = THPVariable_Unpack(ko).dim() == 5 ? 5 : 4;
   const at::Tensor &k = tensor(ko, "cache.k", at::kBFloat16, dim), &v = tensor(vo, "cache.v", at::kBFloat16, dim);
   need(k.sizes() == v.sizes() && k.strides() == v.strides(), "k and v of a cache differ in shape or strides");
   need(k.size(-2) == Hkv && k.size(-1) == D, "the cache does not fit k");
+  need(!one_layer || dim == 4 || k.size(0) == 1, "the call takes one layer of the cache: cache.layer(i)");
   return {ptr(k),       ptr(v),
           dim == 5 ? k.stride(0) : 0,
           k.stride(-4), k.stride(-3), k.stride(-2),
@@ -183,7 +185,7 @@ PyObject *py_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
       const at::Tensor &v = heads_of(a[10], "v");
       need(v.sizes() == k.sizes(), "v must have k's shape");
       vh = heads(v);
-      c = cache_of(a[11], a[12], Hkv, D);
+      c = cache_of(a[11], a[12], Hkv, D, true);
       slots = index<int64_t>(a[13], "slots", at::kLong, T);
     }
     check("qk_norm_rope",
@@ -248,7 +250,7 @@ PyObject *py_tree(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const int64_t B = ctx.numel();
     const int *cu = index<int>(a[3], "cu_nodes", at::kInt, B + 1);
     const uint64_t *mask = index<uint64_t>(a[4], "mask", at::kLong, r.T);
-    const mxg_kv_cache c = cache_of(a[5], a[6], r.Hkv, r.D);
+    const mxg_kv_cache c = cache_of(a[5], a[6], r.Hkv, r.D, true);
     const Table t = table(a[7], "block_table", B);
     r.opts.workspace = ptr(ws);
     r.opts.ws_bytes = (size_t)ws.numel();
@@ -270,7 +272,7 @@ PyObject *py_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const at::Tensor &k = tensor(a[0], "k", at::kBFloat16, dim), &v = tensor(a[1], "v", at::kBFloat16, dim);
     need(k.sizes() == v.sizes(), "k and v must be ([layers,] N, Hkv, D)");
     const int64_t N = k.size(-3), Hkv = k.size(-2), D = k.size(-1);
-    const mxg_kv_cache c = cache_of(a[4], a[5], Hkv, D);
+    const mxg_kv_cache c = cache_of(a[4], a[5], Hkv, D, false);
     need((dim == 4 ? k.size(0) : 1) == c.layers, "k and the cache differ in layers");
     const at::Tensor &ctx = tensor(a[7], "ctx_len", at::kInt, 1);
     const int64_t B = ctx.numel();

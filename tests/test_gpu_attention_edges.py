@@ -1,5 +1,6 @@
 """The attention operators at the edges of what they take: tables without
-columns, accepted nodes that cannot be written, rows that one key has nearly all of."""
+columns, accepted nodes that cannot be written, rows that one key has nearly all of,
+caches of several layers."""
 import math
 
 import pytest
@@ -136,3 +137,26 @@ def test_tree_one_heavy_key(D, B, n, ctx):
     c.vc = one[0].expand(c.vc.shape).contiguous()
     off = c.run(scale=1.0) != one.repeat_interleave(Hq // Hkv, 1)
     assert not bool(off.any()), f"{int(off.sum())} of {off.numel()} values are not the value"
+
+
+def test_calls_of_one_layer_refuse_a_cache_of_several():
+    """attn_tree and qk_norm_rope work on one layer: given a cache of three they
+    do not silently take its first.  One layer of it, and a cache of one, are
+    taken."""
+    c = Case([40, 9], [3, 2], 4, 2, 64, 16, seed=37)
+    d = c.q.device
+    many = mx.KVCache(torch.stack([c.kc * 0, c.kc, c.kc * 0]), torch.stack([c.vc * 0, c.vc, c.vc * 0]))
+    one = mx.KVCache(c.kc[None], c.vc[None])
+    run = lambda cache: mx.attn_tree(c.q, c.k, c.v, c.cu, c.mask, cache, c.tab, c.len)  # noqa: E731
+    want = c.run()
+    assert torch.equal(run(many.layer(1)), want) and torch.equal(run(one), want)
+    with pytest.raises(ValueError, match="layer"):
+        run(many)
+    keep = many.k.clone()
+    slots = torch.arange(5, device=d)
+    with pytest.raises(ValueError, match="layer"):
+        mx.qk_norm_rope(c.q, c.k, v=c.v, cache=many, slots=slots)
+    torch.cuda.synchronize()
+    assert torch.equal(many.k.nan_to_num(7.0), keep.nan_to_num(7.0))
+    mx.qk_norm_rope(c.q, c.k, v=c.v, cache=many.layer(2), slots=slots)
+    assert torch.equal(many.k[2, 0, :5], c.k) and torch.equal(many.k[:2].nan_to_num(7.0), keep[:2].nan_to_num(7.0))
