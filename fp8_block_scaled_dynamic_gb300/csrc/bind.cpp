@@ -16,7 +16,9 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <climits>
 #include <cmath>
+#include <cstdint>
 #include <optional>
 #include <stdexcept>
 #include <string>
@@ -217,8 +219,11 @@ Attn attn_of(PyObject *const *a, int at_) {
   r.scale = given(a[at_]) ? (float)number(a[at_]) : (float)(1.0 / std::sqrt((double)(r.D > 0 ? r.D : 1)));
   r.opts = {};
   r.opts.dev_status = status_word(a[at_ + 2]);
-  r.opts.timeout_ms = (uint32_t)integer(a[at_ + 3]);
-  r.opts.debug_stall = (int)integer(a[at_ + 4]);
+  const long ms = integer(a[at_ + 3]), stall = integer(a[at_ + 4]);
+  need(ms >= 0 && ms <= (long)UINT32_MAX, "timeout_ms must be 0 (the default) or a number of milliseconds in 32 bits");
+  need(stall == 0 || stall == 1, "debug_stall must be 0 or 1");
+  r.opts.timeout_ms = (uint32_t)ms;
+  r.opts.debug_stall = (int)stall;
   return r;
 }
 

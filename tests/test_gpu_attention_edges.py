@@ -1,6 +1,6 @@
 """The attention operators at the edges of what they take: tables without
 columns, accepted nodes that cannot be written, rows that one key has nearly all of,
-caches of several layers."""
+caches of several layers, limits of the waits that are none."""
 import math
 
 import pytest
@@ -160,3 +160,15 @@ def test_calls_of_one_layer_refuse_a_cache_of_several():
     assert torch.equal(many.k.nan_to_num(7.0), keep.nan_to_num(7.0))
     mx.qk_norm_rope(c.q, c.k, v=c.v, cache=many.layer(2), slots=slots)
     assert torch.equal(many.k[2, 0, :5], c.k) and torch.equal(many.k[:2].nan_to_num(7.0), keep[:2].nan_to_num(7.0))
+
+
+@pytest.mark.parametrize("kw", [dict(timeout_ms=-1), dict(timeout_ms=1 << 32), dict(timeout_ms=(1 << 32) + 5),
+                                dict(debug_stall=-1), dict(debug_stall=2), dict(debug_stall=1 << 32)])
+def test_wait_limits_out_of_range_are_refused(kw):
+    """-1 ms is not a limit of 49 days, nor 2^32 + 5 one of 5 ms."""
+    c = Case([40, 9], [3, 2], 4, 2, 64, 16, seed=38)
+    with pytest.raises(ValueError, match=next(iter(kw))):
+        c.run(**kw)
+    with pytest.raises(ValueError, match=next(iter(kw))):
+        mx.attn_prompt(c.q, c.k, c.v, c.cu, **kw)
+    mx.attn_prompt(c.q, c.k, c.v, c.cu, timeout_ms=(1 << 32) - 1)
