@@ -1,6 +1,9 @@
 """Build libmxgemm.so in-tree: nvcc for sm_103a only, one object per source
 compiled in parallel, then a shared link against the CUDA runtime; beside it
-_attn_bind.so, the CPython module that calls the attention entry points."""
+_attn_bind.so, the CPython module that calls the attention entry points.  The
+library needs nvcc alone and is linked whatever becomes of the module, which
+needs torch's headers; where torch is not installed it is left out (the package,
+which loads it, needs torch too)."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -35,11 +38,15 @@ def _stale(out: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def _bind_flags() -> tuple[list[str], list[str]]:
-    """Compile and link flags of the CPython module (torch's headers and libraries)."""
+def _bind_flags() -> tuple[list[str], list[str], str] | None:
+    """Compile and link flags of the CPython module (torch's headers and
+    libraries) and what it is built for; None without torch."""
+    import sys
     import sysconfig
-
-    import torch
+    try:
+        import torch
+    except (ImportError, OSError):
+        return None
     root = os.path.dirname(os.path.abspath(torch.__file__))
     inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
            os.path.join(os.path.dirname(_cuda_lib_dir()), "include"), sysconfig.get_paths()["include"], INCLUDE]
@@ -48,7 +55,15 @@ def _bind_flags() -> tuple[list[str], list[str]]:
     lib = os.path.join(root, "lib")
     ld = ["-L" + lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath," + lib,
           "-L" + PKG, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + _cuda_lib_dir()]
-    return cc, ld
+    made_for = f"torch {torch.__version__}, Python {sys.version}\n" + "\n".join(cc + ld)
+    return cc, ld, made_for
+
+
+def _run(cmd: list[str]) -> str:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    return r.stdout + r.stderr
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -68,30 +83,35 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if force or _stale(o, [s] + headers):
             jobs.append([nvcc(), *flags, "-c", s, "-o", o])
 
+    # the module: also built anew for another torch or Python than its stamp names
     bind_src, bind_obj = os.path.join(CSRC, "bind.cpp"), os.path.join(BUILD, "bind.o")
-    bind_cc, bind_ld = _bind_flags()
-    if force or _stale(bind_obj, [bind_src] + headers):
-        jobs.append(["g++", *bind_cc, "-c", bind_src, "-o", bind_obj])
-
-    def run(cmd):
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"{os.path.basename(cmd[0])} failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
-        return r.stdout + r.stderr
+    stamp = os.path.join(BUILD, "bind.stamp")
+    flags_bind = _bind_flags()
+    made = None
+    if os.path.exists(stamp):
+        with open(stamp) as f:
+            made = f.read()
+    bind_new = flags_bind is not None and (force or made != flags_bind[2] or _stale(BIND, [bind_src] + headers))
 
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        for out in ex.map(run, jobs):
+        bind_job = ex.submit(_run, ["g++", *flags_bind[0], "-c", bind_src, "-o", bind_obj]) if bind_new else None
+        for out in ex.map(_run, jobs):
             if verbose and out:
                 print(out)
-    if force or _stale(LIB, objs):
-        tmp = LIB + f".tmp{os.getpid()}"
-        run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "shared",
-             "-Xlinker", "-rpath," + _cuda_lib_dir()])
-        os.replace(tmp, LIB)
-    if force or _stale(BIND, [bind_obj]):
+        if force or _stale(LIB, objs):
+            tmp = LIB + f".tmp{os.getpid()}"
+            _run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "shared",
+                  "-Xlinker", "-rpath," + _cuda_lib_dir()])
+            os.replace(tmp, LIB)
+    if bind_job is not None:
+        bind_job.result()
         tmp = BIND + f".tmp{os.getpid()}"
-        run(["g++", "-shared", "-o", tmp, bind_obj, *bind_ld])
+        _run(["g++", "-shared", "-o", tmp, bind_obj, *flags_bind[1]])
         os.replace(tmp, BIND)
+        with open(stamp, "w") as f:
+            f.write(flags_bind[2])
+    elif flags_bind is None:
+        print("torch is not installed: the library is built, its Python module for the attention entry points is not")
     return LIB
 
 
