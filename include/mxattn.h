@@ -111,6 +111,7 @@ mxg_status qk_norm_rope(const mxg_heads *q, const mxg_heads *k, int T, int Hq, i
  * allowed), cu_seqlens[B] <= T; tokens past cu_seqlens[B] are not written.
  * D in {64, 128}, Hq / Hkv <= 128, 1 <= B <= MXG_ATTN_MAX_SEQS, T >= 0,
  * scale > 0.
+ * out may be q itself; it must not overlap k or v, nor q in any other way.
  * v of a token that a query does not see has no influence on it, NaN and
  * infinities included.  opts may be NULL; no workspace is needed.
  * Out of range: offsets are clamped to [0, T] and to the offsets before. */
@@ -127,8 +128,9 @@ mxg_status attn_prompt(const mxg_heads *q, const mxg_heads *k, const mxg_heads *
  * global, j counted from the sequence's first node; bits at or past the
  * sequence's node count are ignored).  A node that sees nothing gets 0.
  * One node a sequence with mask 1 is plain decoding.
- * table_cols: columns of block_table that may be read.  D, Hq, Hkv, B, scale as
- * for attn_prompt; N >= 0.  v of what a node does not see has no influence on it.
+ * table_cols: columns of block_table that may be read.  D, Hq, Hkv, B, scale
+ * and out as for attn_prompt (nor may out overlap the cache); N >= 0.  v of
+ * what a node does not see has no influence on it.
  * opts with a workspace is required.  Results do not depend on timing: the
  * parts of a long context are joined in a fixed order.
  * Out of range: offsets are clamped as for attn_prompt, a tree's nodes past

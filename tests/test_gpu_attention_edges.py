@@ -1,6 +1,7 @@
 """The attention operators at the edges of what they take: tables without
 columns, accepted nodes that cannot be written, rows that one key has nearly all of,
-caches of several layers, limits of the waits that are none."""
+caches of several layers, limits of the waits that are none,
+results in place of q."""
 import math
 
 import pytest
@@ -172,3 +173,19 @@ def test_wait_limits_out_of_range_are_refused(kw):
     with pytest.raises(ValueError, match=next(iter(kw))):
         mx.attn_prompt(c.q, c.k, c.v, c.cu, **kw)
     mx.attn_prompt(c.q, c.k, c.v, c.cu, timeout_ms=(1 << 32) - 1)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_results_in_place_of_q(D):
+    """out may be q itself: a row group's q is read by those that make its
+    result, and written when all of them have it."""
+    c = Case([9000, 300, 0, 2500], [8, 1, 40, 30], 16, 2, D, 64, seed=39)
+    want, q = c.run(), c.q.clone()
+    assert c.run(out=c.q) is c.q and torch.equal(c.q, want)
+    lens = [1, 7, 1000, 300]
+    qkv = randn(40, sum(lens), 20, D).to(q.device)
+    q, k, v = qkv[:, :16], qkv[:, 16:18], qkv[:, 18:]
+    cu = offsets(lens, q.device)
+    want = mx.attn_prompt(q, k, v, cu)
+    mx.attn_prompt(q, k, v, cu, out=q)
+    assert torch.equal(q, want)
