@@ -28,19 +28,22 @@
 //
 // What bounds it, and what was measured (GB300; a copy runs at 6.8 TB/s, a
 // bf16 library product at 1.90 PFLOP/s):
-// - Long prompts of heads of 128: the tensor core (64 cycles for each 128 x 128
-//   x 16) and the power it draws: 8192 tokens of 64 / 8 heads 671 us, 1.64
-//   PFLOP/s; 16384 of 16 / 2 heads 1.69.
+// - Long prompts of heads of 128: the two streams' chains and power.  8192 tokens
+//   of 64 / 8 heads take 672-683 us at 2070 MHz (1.63 PFLOP/s): 1.53 us, 3200
+//   cycles, for each pair of row tiles and 128 keys, of which the products are
+//   2048 (64 for each 128 x 128 x 16; the tensor pipe is active 62 % of the time)
+//   and the exponentials, beside them, 1024.  In a run of seconds the power limit
+//   (1364 W) takes the clock to 1942 MHz and the time to 732 us.
 // - Prompts of heads of 64: a stream's chain of scores, softmax and product
 //   (about 2500 cycles a tile of which the products are 512), which two streams
-//   cover to half: 8192 tokens of 64 / 8 heads 571 us, 0.96 PFLOP/s.  A tile's
+//   cover to half: 8192 tokens of 64 / 8 heads 569 us, 0.97 PFLOP/s, at 2070 MHz.  A tile's
 //   exponentials take 512 cycles of a scheduler, its tensor work as many.
 //   Tried and slower: the weights in TMEM columns of their own with the next
 //   scores under way during the softmax (585 us: the streams fall into step and
 //   want the exponential unit together), two threads a row in 16 warps (732 us).
 // - Trees over a long cache: HBM for one node a sequence (16 x 16384 cached
-//   tokens, 8 kv heads of 128: 167 us, 6.4 TB/s), the softmax beside it for
-//   many (32 nodes: 215 us, 1.28 PFLOP/s).
+//   tokens, 8 kv heads of 128: 164-167 us, 6.4-6.5 TB/s), the softmax beside it
+//   for many (32 nodes: 218-222 us, 1.26 PFLOP/s).
 // - Short calls: latency.  One token over 1500 cached ones takes 12 us with
 //   8 us in this kernel: reading the lists, the items, page table and first
 //   load, first scores, first softmax and the result are about 1 us each.
@@ -346,9 +349,10 @@ struct Small {
 };
 
 // Walks the items of one CTA.
-// Prompt: row groups from the last (its keys are the most) to the first, dealt
-// over the CTAs there and back, so that who gets the heaviest of one round
-// gets the lightest of the next.
+// Prompt: row groups from the last number to the first, dealt over the CTAs there
+// and back.  A sequence's later row groups have more keys, so that within a long
+// sequence who gets a heavy one in one round gets a light one in the next; in a
+// small batch the longest sequence is numbered last and comes first (Small).
 // Tree: the units are cut into equal ranges over the CTAs, an item is the part
 // of one row group's key tiles that lies in this CTA's range -- or, where that
 // costs at most two tiles a CTA more, every row group's key tiles are cut into
