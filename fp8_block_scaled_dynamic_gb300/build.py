@@ -17,7 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmxgemm.so")
-SOURCES = ["api.cu", "quant.cu", "gemm.cu", "attn_api.cu", "attn.cu", "rope.cu"]
+SOURCES = ["api.cu", "quant.cu", "gemm.cu", "attn_api.cu", "attn.cu", "attn_long.cu", "rope.cu", "index.cu"]
 BIND = os.path.join(PKG, "_attn_bind.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

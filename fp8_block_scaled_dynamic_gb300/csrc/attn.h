@@ -53,13 +53,57 @@ struct AttnParams {
   int debug_stall;
 };
 
+struct SharedParams {  // attn_shared
+  AttnParams a;
+  const int *groups, *prefix;  // n_groups + 1 sequence offsets, n_groups lengths
+  int n_groups;
+};
+
+struct SparseParams {  // attn_sparse
+  AttnParams a;
+  const int *sel;  // (T, Hkv, n_sel)
+  int n_sel;
+};
+
+struct PageIndex {  // strides in bytes
+  int8_t *codes;
+  uint8_t *exps;
+  long long codes_layer, codes_page, codes_head, exps_layer, exps_page;
+  int layers, pages;
+};
+
+struct IndexParams {
+  Cache cache;
+  PageIndex index;
+  const int *table, *old, *now;  // old null: zeros
+  int *status;
+  int B, Hkv, D, ld_table, table_cols;
+};
+
+struct SelectParams {
+  Heads q;
+  PageIndex index;
+  const int *cu, *table, *ctx;
+  int *sel, *status;
+  float *ws;  // scores
+  int B, N, Hq, Hkv, D, page_size, ld_table, table_cols, n_sel, first, last;
+};
+
 constexpr int kAttnMaxSeqs = 4096;
 constexpr int kAttnMaxNodes = 64;
+constexpr int kAttnMaxSelect = 512;
 
 cudaError_t launch_qk_norm_rope(const RopeParams &p, bool interleaved, int sm_count, cudaStream_t stream);
 cudaError_t launch_kv_append(const AppendParams &p, cudaStream_t stream);
 cudaError_t launch_attn_prompt(const AttnParams &p, int sm_count, cudaStream_t stream);
 cudaError_t launch_attn_tree(const AttnParams &p, int sm_count, cudaStream_t stream);
 size_t attn_tree_ws_bytes(int D, int sm_count);
+cudaError_t launch_attn_shared(const SharedParams &p, int sm_count, cudaStream_t stream);
+size_t attn_shared_ws_bytes(long long N, int Hq, int D, int sm_count);
+cudaError_t launch_attn_sparse(const SparseParams &p, int sm_count, cudaStream_t stream);
+size_t attn_sparse_ws_bytes(long long N, int Hkv, int n_sel, int D, int sm_count);
+cudaError_t launch_kv_index(const IndexParams &p, int sm_count, cudaStream_t stream);
+cudaError_t launch_attn_select(const SelectParams &p, int sm_count, cudaStream_t stream);
+size_t attn_select_ws_bytes(long long N, int Hkv, int table_cols);
 
 }  // namespace mxg

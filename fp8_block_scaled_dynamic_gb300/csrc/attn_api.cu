@@ -10,7 +10,9 @@
 #include "attn.h"
 #include "mxattn.h"
 
-static_assert(mxg::kAttnMaxSeqs == MXG_ATTN_MAX_SEQS && mxg::kAttnMaxNodes == MXG_ATTN_MAX_NODES, "limits");
+static_assert(mxg::kAttnMaxSeqs == MXG_ATTN_MAX_SEQS && mxg::kAttnMaxNodes == MXG_ATTN_MAX_NODES &&
+                  mxg::kAttnMaxSelect == MXG_ATTN_MAX_SELECT,
+              "limits");
 
 namespace {
 
@@ -79,6 +81,53 @@ mxg_status check_attn(const mxg_heads *q, const mxg_heads *k, const mxg_heads *v
   return MXG_OK;
 }
 
+// What attn_tree, attn_shared and attn_sparse check alike of the cache side.
+mxg_status check_paged(int N, const uint64_t *mask, const mxg_kv_cache *cache, const int *block_table, int ld_table,
+                       int table_cols, const int *ctx_len, int Hkv) {
+  if ((N > 0 && !mask) || !ctx_len || table_cols < 0 || ld_table < table_cols || (table_cols > 0 && !block_table))
+    return MXG_ERR_INVALID_ARG;
+  mxg_status st;
+  if ((st = check_cache(cache)) != MXG_OK) return st;
+  if (!cache->slot_stride || (cache->pages > 1 && !cache->page_stride) || (Hkv > 1 && !cache->head_stride))
+    return MXG_ERR_UNSUPPORTED_SHAPE;
+  if ((long long)table_cols * cache->page_size > 0x7fffff00LL) return MXG_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned(mask, 8) || !aligned(ctx_len, 4) || !aligned(block_table, 4)) return MXG_ERR_MISALIGNED;
+  return MXG_OK;
+}
+
+// Row groups x kv heads x key tiles, numbered in 32 bits; starts: row groups that
+// begin anew, besides the full ones.
+mxg_status check_units(int N, int Hq, int Hkv, long long starts, int table_cols, int page_size) {
+  const int tq = 128 / (Hq / Hkv);
+  const long long groups = N / (2 * tq) + starts;
+  return groups * Hkv * ((long long)table_cols * page_size / 128 + 2) > 0x3fffffffLL || Hkv >= (1 << 16)
+             ? MXG_ERR_UNSUPPORTED_SHAPE
+             : MXG_OK;
+}
+
+mxg_status check_ws(const mxg_attn_opts *opts, size_t need) {
+  if (!opts || !opts->workspace || need == 0 || opts->ws_bytes < need) return MXG_ERR_WORKSPACE;
+  return aligned(opts->workspace, 256) ? MXG_OK : MXG_ERR_MISALIGNED;
+}
+
+// Bytes, a multiple of 16 of them, that no reachable entry's offset overflows.
+bool bytes_ok(int64_t s) { return s >= 0 && s % 16 == 0 && s < (1LL << 38); }
+
+mxg_status check_index(const mxg_page_index *x) {
+  if (!x || !x->codes || !x->exps || x->layers < 1 || x->pages < 1 || x->codes_layer < 0 || x->codes_page < 0 ||
+      x->codes_head < 0 || x->exps_layer < 0 || x->exps_page < 0)
+    return MXG_ERR_INVALID_ARG;
+  if (!aligned(x->codes, 16) || !bytes_ok(x->codes_layer) || !bytes_ok(x->codes_page) || !bytes_ok(x->codes_head) ||
+      x->exps_layer >= (1LL << 38) || x->exps_page >= (1LL << 38))
+    return MXG_ERR_MISALIGNED;
+  return MXG_OK;
+}
+
+mxg::PageIndex index_of(const mxg_page_index *x) {
+  return {x->codes,      x->exps,      x->codes_layer, x->codes_page, x->codes_head,
+          x->exps_layer, x->exps_page, x->layers,      x->pages};
+}
+
 mxg::AttnParams attn_params(const mxg_heads *q, const mxg_heads *k, const mxg_heads *v, const int *cu, int B, int T,
                             int Hq, int Hkv, int D, float scale, const mxg_heads *out, const mxg_attn_opts *opts) {
   mxg::AttnParams p = {};
@@ -97,6 +146,17 @@ mxg::AttnParams attn_params(const mxg_heads *q, const mxg_heads *k, const mxg_he
   p.timeout_ns = (unsigned long long)(opts && opts->timeout_ms ? opts->timeout_ms : 1000u) * 1000000ull;
   p.debug_stall = opts ? opts->debug_stall : 0;
   return p;
+}
+
+void paged(mxg::AttnParams &p, const uint64_t *mask, const mxg_kv_cache *cache, const int *block_table, int ld_table,
+           int table_cols, const int *ctx_len, const mxg_attn_opts *opts) {
+  p.cache = cache_of(cache);
+  p.mask = reinterpret_cast<const unsigned long long *>(mask);
+  p.table = block_table;
+  p.ctx = ctx_len;
+  p.ld_table = table_cols > 0 ? ld_table : 0;  // (no columns: the table may be null, and nothing of it is touched)
+  p.table_cols = table_cols;
+  p.ws = static_cast<float *>(opts->workspace);
 }
 
 }  // namespace
@@ -182,31 +242,14 @@ mxg_status attn_tree(const mxg_heads *q, const mxg_heads *k, const mxg_heads *v,
                      const mxg_heads *out, const mxg_attn_opts *opts, mxg_stream_t stream) {
   mxg_status st = check_attn(q, k, v, cu_nodes, B, N, Hq, Hkv, D, scale, out, opts);
   if (st != MXG_OK) return st;
-  if ((N > 0 && !mask) || !ctx_len || table_cols < 0 || ld_table < table_cols || (table_cols > 0 && !block_table))
-    return MXG_ERR_INVALID_ARG;
-  if ((st = check_cache(cache)) != MXG_OK) return st;
-  if (!cache->slot_stride || (cache->pages > 1 && !cache->page_stride) || (Hkv > 1 && !cache->head_stride))
-    return MXG_ERR_UNSUPPORTED_SHAPE;
-  if ((long long)table_cols * cache->page_size > 0x7fffff00LL) return MXG_ERR_UNSUPPORTED_SHAPE;
-  if (!aligned(mask, 8) || !aligned(ctx_len, 4) || !aligned(block_table, 4)) return MXG_ERR_MISALIGNED;
+  if ((st = check_paged(N, mask, cache, block_table, ld_table, table_cols, ctx_len, Hkv)) != MXG_OK) return st;
   int sm = 0;
   if ((st = device_sms(&sm)) != MXG_OK) return st;
-  if (!opts || !opts->workspace || opts->ws_bytes < mxg::attn_tree_ws_bytes(D, sm)) return MXG_ERR_WORKSPACE;
-  if (!aligned(opts->workspace, 256)) return MXG_ERR_MISALIGNED;
-  // row groups x kv heads x key tiles, numbered in 32 bits
-  const int tq = 128 / (Hq / Hkv);
-  const long long groups = N / (2 * tq) + (N < B ? N : B);
-  if (groups * Hkv * ((long long)table_cols * cache->page_size / 128 + 2) > 0x3fffffffLL || Hkv >= (1 << 16))
-    return MXG_ERR_UNSUPPORTED_SHAPE;
+  if ((st = check_ws(opts, mxg::attn_tree_ws_bytes(D, sm))) != MXG_OK) return st;
+  if ((st = check_units(N, Hq, Hkv, N < B ? N : B, table_cols, cache->page_size)) != MXG_OK) return st;
   if (N == 0) return MXG_OK;
   mxg::AttnParams p = attn_params(q, k, v, cu_nodes, B, N, Hq, Hkv, D, scale, out, opts);
-  p.cache = cache_of(cache);
-  p.mask = reinterpret_cast<const unsigned long long *>(mask);
-  p.table = block_table;
-  p.ctx = ctx_len;
-  p.ld_table = table_cols > 0 ? ld_table : 0;  // (no columns: the table may be null, and nothing of it is touched)
-  p.table_cols = table_cols;
-  p.ws = static_cast<float *>(opts->workspace);
+  paged(p, mask, cache, block_table, ld_table, table_cols, ctx_len, opts);
   const cudaError_t e = mxg::launch_attn_tree(p, sm, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MXG_OK : MXG_ERR_CUDA;
 }
@@ -251,6 +294,158 @@ mxg_status kv_append(const mxg_heads *k, int64_t k_layer_stride, const mxg_heads
   p.ld_table = ld_table;
   p.table_cols = table_cols;
   const cudaError_t e = mxg::launch_kv_append(p, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MXG_OK : MXG_ERR_CUDA;
+}
+
+size_t mxg_attn_shared_workspace_bytes(int N, int Hq, int D) {
+  int sm = 0;
+  if ((D != 64 && D != 128) || N < 0 || Hq < 1 || device_sms(&sm) != MXG_OK) return 0;
+  return mxg::attn_shared_ws_bytes(N, Hq, D, sm);
+}
+
+mxg_status attn_shared(const mxg_heads *q, const mxg_heads *k, const mxg_heads *v, const int *cu_nodes,
+                       const uint64_t *mask, int B, int N, const mxg_kv_cache *cache, const int *block_table,
+                       int ld_table, int table_cols, const int *ctx_len, const int *cu_groups, const int *prefix_len,
+                       int n_groups, int Hq, int Hkv, int D, float scale, const mxg_heads *out,
+                       const mxg_attn_opts *opts, mxg_stream_t stream) {
+  mxg_status st = check_attn(q, k, v, cu_nodes, B, N, Hq, Hkv, D, scale, out, opts);
+  if (st != MXG_OK) return st;
+  if (n_groups < 0 || n_groups > B || (n_groups > 0 && (!cu_groups || !prefix_len))) return MXG_ERR_INVALID_ARG;
+  if ((st = check_paged(N, mask, cache, block_table, ld_table, table_cols, ctx_len, Hkv)) != MXG_OK) return st;
+  if (!aligned(cu_groups, 4) || !aligned(prefix_len, 4)) return MXG_ERR_MISALIGNED;
+  int sm = 0;
+  if ((st = device_sms(&sm)) != MXG_OK) return st;
+  if ((st = check_ws(opts, mxg::attn_shared_ws_bytes(N, Hq, D, sm))) != MXG_OK) return st;
+  if ((st = check_units(N, Hq, Hkv, 2LL * (N < B ? N : B), table_cols, cache->page_size)) != MXG_OK) return st;
+  if (N == 0) return MXG_OK;
+  mxg::SharedParams p = {};
+  p.a = attn_params(q, k, v, cu_nodes, B, N, Hq, Hkv, D, scale, out, opts);
+  paged(p.a, mask, cache, block_table, ld_table, table_cols, ctx_len, opts);
+  p.groups = cu_groups;
+  p.prefix = prefix_len;
+  p.n_groups = n_groups;
+  const cudaError_t e = mxg::launch_attn_shared(p, sm, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MXG_OK : MXG_ERR_CUDA;
+}
+
+mxg_status kv_index(const mxg_kv_cache *cache, int Hkv, int D, const mxg_page_index *index, const int *block_table,
+                    int B, int ld_table, int table_cols, const int *ctx_old, const int *ctx_new, int *dev_status,
+                    mxg_stream_t stream) {
+  if (B < 1 || Hkv < 1 || D < 1 || !ctx_new || table_cols < 0 || ld_table < table_cols ||
+      (table_cols > 0 && !block_table))
+    return MXG_ERR_INVALID_ARG;
+  if ((D != 64 && D != 128) || B > mxg::kAttnMaxSeqs || Hkv > 65535) return MXG_ERR_UNSUPPORTED_SHAPE;
+  mxg_status st;
+  if ((st = check_cache(cache)) != MXG_OK || (st = check_index(index)) != MXG_OK) return st;
+  if (index->layers < cache->layers || index->pages < cache->pages) return MXG_ERR_INVALID_ARG;
+  // (pages of all sequences, numbered in 32 bits)
+  if ((long long)table_cols * cache->page_size > 0x7fffff00LL || (long long)table_cols * B > 0x7fffffffLL)
+    return MXG_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned(block_table, 4) || !aligned(ctx_old, 4) || !aligned(ctx_new, 4) || !aligned(dev_status, 4))
+    return MXG_ERR_MISALIGNED;
+  int sm = 0;
+  if ((st = device_sms(&sm)) != MXG_OK) return st;
+  if (table_cols == 0) return MXG_OK;
+  mxg::IndexParams p = {};
+  p.cache = cache_of(cache);
+  p.index = index_of(index);
+  p.table = block_table;
+  p.old = ctx_old;
+  p.now = ctx_new;
+  p.status = dev_status;
+  p.B = B;
+  p.Hkv = Hkv;
+  p.D = D;
+  p.ld_table = ld_table;
+  p.table_cols = table_cols;
+  const cudaError_t e = mxg::launch_kv_index(p, sm, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MXG_OK : MXG_ERR_CUDA;
+}
+
+size_t mxg_attn_select_workspace_bytes(int N, int Hkv, int table_cols) {
+  if (N < 0 || Hkv < 1 || table_cols < 0) return 0;
+  return mxg::attn_select_ws_bytes(N, Hkv, table_cols);
+}
+
+mxg_status attn_select(const mxg_heads *q, const int *cu_nodes, int B, int N, const mxg_page_index *index,
+                       int page_size, const int *block_table, int ld_table, int table_cols, const int *ctx_len, int Hq,
+                       int Hkv, int D, int n_sel, int first, int last, int *sel, const mxg_attn_opts *opts,
+                       mxg_stream_t stream) {
+  if (!cu_nodes || B < 1 || N < 0 || Hq < 1 || Hkv < 1 || !ctx_len || table_cols < 0 || ld_table < table_cols ||
+      (table_cols > 0 && !block_table) || (N > 0 && !sel) || first < 0 || last < 1 || n_sel < 1 || first > n_sel ||
+      last > n_sel - first || page_size < 1)
+    return MXG_ERR_INVALID_ARG;
+  if (opts && opts->debug_stall != 0) return MXG_ERR_INVALID_ARG;
+  if ((D != 64 && D != 128) || Hq % Hkv != 0 || Hq / Hkv > 128 || B > mxg::kAttnMaxSeqs ||
+      n_sel > mxg::kAttnMaxSelect ||
+      (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128 && page_size != 256) ||
+      (long long)table_cols * page_size > 0x7fffff00LL || (long long)N * Hkv > 0x7fffffffLL)
+    return MXG_ERR_UNSUPPORTED_SHAPE;
+  mxg_status st;
+  if ((st = check_index(index)) != MXG_OK) return st;
+  if (N > 0 && (st = check_heads(q)) != MXG_OK) return st;
+  if (!aligned(cu_nodes, 4) || !aligned(block_table, 4) || !aligned(ctx_len, 4) || !aligned(sel, 4) ||
+      (opts && opts->dev_status && !aligned(opts->dev_status, 4)))
+    return MXG_ERR_MISALIGNED;
+  int sm = 0;
+  if ((st = device_sms(&sm)) != MXG_OK) return st;
+  if ((st = check_ws(opts, mxg::attn_select_ws_bytes(N, Hkv, table_cols))) != MXG_OK) return st;
+  if (N == 0) return MXG_OK;
+  mxg::SelectParams p = {};
+  p.q = heads(q);
+  p.index = index_of(index);
+  p.cu = cu_nodes;
+  p.table = block_table;
+  p.ctx = ctx_len;
+  p.sel = sel;
+  p.status = opts->dev_status;
+  p.ws = static_cast<float *>(opts->workspace);
+  p.B = B;
+  p.N = N;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.D = D;
+  p.page_size = page_size;
+  p.ld_table = table_cols > 0 ? ld_table : 0;
+  p.table_cols = table_cols;
+  p.n_sel = n_sel;
+  p.first = first;
+  p.last = last;
+  const cudaError_t e = mxg::launch_attn_select(p, sm, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MXG_OK : MXG_ERR_CUDA;
+}
+
+size_t mxg_attn_sparse_workspace_bytes(int N, int Hkv, int n_sel, int D) {
+  int sm = 0;
+  if ((D != 64 && D != 128) || N < 0 || Hkv < 1 || n_sel < 1 || device_sms(&sm) != MXG_OK) return 0;
+  return mxg::attn_sparse_ws_bytes(N, Hkv, n_sel, D, sm);
+}
+
+mxg_status attn_sparse(const mxg_heads *q, const mxg_heads *k, const mxg_heads *v, const int *cu_nodes,
+                       const uint64_t *mask, int B, int N, const mxg_kv_cache *cache, const int *block_table,
+                       int ld_table, int table_cols, const int *ctx_len, const int *sel, int n_sel, int Hq, int Hkv,
+                       int D, float scale, const mxg_heads *out, const mxg_attn_opts *opts, mxg_stream_t stream) {
+  mxg_status st = check_attn(q, k, v, cu_nodes, B, N, Hq, Hkv, D, scale, out, opts);
+  if (st != MXG_OK) return st;
+  if (n_sel < 1 || (N > 0 && !sel)) return MXG_ERR_INVALID_ARG;
+  if (n_sel > mxg::kAttnMaxSelect) return MXG_ERR_UNSUPPORTED_SHAPE;
+  if ((st = check_paged(N, mask, cache, block_table, ld_table, table_cols, ctx_len, Hkv)) != MXG_OK) return st;
+  if (!aligned(sel, 4)) return MXG_ERR_MISALIGNED;
+  int sm = 0;
+  if ((st = device_sms(&sm)) != MXG_OK) return st;
+  if ((st = check_ws(opts, mxg::attn_sparse_ws_bytes(N, Hkv, n_sel, D, sm))) != MXG_OK) return st;
+  // (a sequence's nodes name no more pages than there are, nor than all their lists hold)
+  const long long named = (long long)mxg::kAttnMaxNodes * n_sel;
+  if ((st = check_units(N, Hq, Hkv, N < B ? N : B, named < table_cols ? (int)named : table_cols, cache->page_size)) !=
+      MXG_OK)
+    return st;
+  if (N == 0) return MXG_OK;
+  mxg::SparseParams p = {};
+  p.a = attn_params(q, k, v, cu_nodes, B, N, Hq, Hkv, D, scale, out, opts);
+  paged(p.a, mask, cache, block_table, ld_table, table_cols, ctx_len, opts);
+  p.sel = sel;
+  p.n_sel = n_sel;
+  const cudaError_t e = mxg::launch_attn_sparse(p, sm, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MXG_OK : MXG_ERR_CUDA;
 }
 

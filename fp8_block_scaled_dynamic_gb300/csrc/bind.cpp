@@ -267,6 +267,160 @@ PyObject *py_tree(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
+// What attn_tree, attn_shared and attn_sparse take alike, at a[0 ... 8]: q, k, v, cu_nodes, mask, cache k, cache v,
+// block_table, ctx_len; and at a[at ...] what attn_of takes there, then ws.
+struct Paged {
+  Attn r;
+  const int *cu, *ctx;
+  const uint64_t *mask;
+  mxg_kv_cache c;
+  Table t;
+  int64_t B;
+  at::Tensor ws;
+};
+
+template <class Bytes>
+Paged paged_of(PyObject *const *a, int at_, Bytes bytes) {
+  Paged p;
+  p.r = attn_of(a, at_);
+  const at::Tensor &ctx = tensor(a[8], "ctx_len", at::kInt, 1);
+  p.B = ctx.numel();
+  p.ctx = static_cast<int *>(ptr(ctx));
+  p.cu = index<int>(a[3], "cu_nodes", at::kInt, p.B + 1);
+  p.mask = index<uint64_t>(a[4], "mask", at::kLong, p.r.T);
+  p.c = cache_of(a[5], a[6], p.r.Hkv, p.r.D, true);
+  p.t = table(a[7], "block_table", p.B);
+  as_int(p.r.T, "nodes"), as_int(p.r.Hq, "heads"), as_int(p.r.D, "channels");
+  // (back with the allocator on return, for what follows in the stream)
+  p.ws = given(a[at_ + 5]) ? tensor(a[at_ + 5], "ws", at::kByte, 1)
+                           : at::empty({(int64_t)bytes(p.r)}, p.r.o.options().dtype(at::kByte));
+  p.r.opts.workspace = ptr(p.ws);
+  p.r.opts.ws_bytes = (size_t)p.ws.numel();
+  return p;
+}
+
+// (q, k, v, cu_nodes, mask, cache k, cache v, block_table, ctx_len, cu_groups, prefix_len, scale, out, dev_status,
+// timeout_ms, debug_stall, ws, stream)
+PyObject *py_shared(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    count(n, 18);
+    const Stream stream(a[17]);
+    const Paged p = paged_of(
+        a, 11, [](const Attn &r) { return mxg_attn_shared_workspace_bytes((int)r.T, (int)r.Hq, (int)r.D); });
+    const at::Tensor &prefix = tensor(a[10], "prefix_len", at::kInt, 1);
+    const int groups = as_int(prefix.numel(), "groups");
+    const int *cg = index<int>(a[9], "cu_groups", at::kInt, (int64_t)groups + 1);
+    check("attn_shared",
+          attn_shared(&p.r.q, &p.r.k, &p.r.v, p.cu, p.mask, as_int(p.B, "sequences"), (int)p.r.T, &p.c, p.t.p, p.t.ld,
+                      p.t.cols, p.ctx, cg, static_cast<int *>(ptr(prefix)), groups, (int)p.r.Hq, (int)p.r.Hkv,
+                      (int)p.r.D, p.r.scale, &p.r.out, &p.r.opts, stream.handle()));
+    return THPVariable_Wrap(p.r.o);
+  });
+}
+
+// (q, k, v, cu_nodes, mask, cache k, cache v, block_table, ctx_len, sel, scale, out, dev_status, timeout_ms,
+// debug_stall, ws, stream)
+PyObject *py_sparse(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    count(n, 17);
+    const Stream stream(a[16]);
+    const at::Tensor &sel = tensor(a[9], "sel", at::kInt, 3);
+    const int n_sel = as_int(sel.size(2), "pages");
+    const Paged p = paged_of(a, 10, [&](const Attn &r) {
+      return mxg_attn_sparse_workspace_bytes((int)r.T, as_int(r.Hkv, "heads"), n_sel, (int)r.D);
+    });
+    need(sel.size(0) == p.r.T && sel.size(1) == p.r.Hkv && sel.is_contiguous(), "sel must be contiguous (N, Hkv, n_sel)");
+    check("attn_sparse",
+          attn_sparse(&p.r.q, &p.r.k, &p.r.v, p.cu, p.mask, as_int(p.B, "sequences"), (int)p.r.T, &p.c, p.t.p, p.t.ld,
+                      p.t.cols, p.ctx, static_cast<int *>(ptr(sel)), n_sel, (int)p.r.Hq, (int)p.r.Hkv, (int)p.r.D,
+                      p.r.scale, &p.r.out, &p.r.opts, stream.handle()));
+    return THPVariable_Wrap(p.r.o);
+  });
+}
+
+// a PageIndex's codes and exps, (pages, Hkv, 2, D) and (pages, Hkv), or with a leading layers dimension
+mxg_page_index index_of(PyObject *co, PyObject *eo, int64_t Hkv, int64_t D, bool one_layer) {
+  if (!co || !THPVariable_Check(co)) bad("an index holds two tensors");
+  const int dim = THPVariable_Unpack(co).dim() == 5 ? 5 : 4;
+  const at::Tensor &c = tensor(co, "index.codes", at::kChar, dim), &e = tensor(eo, "index.exps", at::kByte, dim - 2);
+  need(c.size(-3) == Hkv && c.size(-2) == 2 && c.size(-1) == D, "the index does not fit the heads");
+  need(c.stride(-2) == D, "the two rows of an index entry must follow one another");
+  need(e.size(-1) == Hkv && e.size(-2) == c.size(-4) && (dim == 4 || e.size(0) == c.size(0)),
+       "codes and exps of an index differ in shape");
+  need(!one_layer || dim == 4 || c.size(0) == 1, "the call takes one layer of the index: index.layer(i)");
+  return {static_cast<int8_t *>(ptr(c)),
+          static_cast<uint8_t *>(ptr(e)),
+          dim == 5 ? c.stride(0) : 0,
+          c.stride(-4),
+          c.stride(-3),
+          dim == 5 ? e.stride(0) : 0,
+          e.stride(-2),
+          dim == 5 ? as_int(c.size(0), "layers") : 1,
+          as_int(c.size(-4), "pages")};
+}
+
+// (cache k, cache v, codes, exps, page_size, block_table, ctx_old, ctx_new, dev_status, stream)
+PyObject *py_index(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    count(n, 10);
+    const Stream stream(a[9]);
+    if (!THPVariable_Check(a[0])) bad("a cache holds two tensors");
+    const at::Tensor &kc = THPVariable_Unpack(a[0]);
+    need(kc.dim() == 4 || kc.dim() == 5, "a cache is ([layers,] pages, page_size, Hkv, D)");
+    const int64_t Hkv = kc.size(-2), D = kc.size(-1);
+    const mxg_kv_cache c = cache_of(a[0], a[1], Hkv, D, false);
+    const mxg_page_index x = index_of(a[2], a[3], Hkv, D, false);
+    need(integer(a[4]) == c.page_size, "the index and the cache differ in page size");
+    need(x.layers == c.layers, "the index and the cache differ in layers");
+    const at::Tensor &now = tensor(a[7], "ctx_new", at::kInt, 1);
+    const int64_t B = now.numel();
+    const Table t = table(a[5], "block_table", B);
+    const int *old = given(a[6]) ? index<int>(a[6], "ctx_old", at::kInt, B) : nullptr;
+    check("kv_index", kv_index(&c, as_int(Hkv, "heads"), as_int(D, "channels"), &x, t.p, as_int(B, "sequences"), t.ld,
+                               t.cols, old, static_cast<int *>(ptr(now)), status_word(a[8]), stream.handle()));
+    Py_RETURN_NONE;
+  });
+}
+
+// (q, cu_nodes, codes, exps, page_size, block_table, ctx_len, n_sel, first, last, out, dev_status, ws, stream)
+PyObject *py_select(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    count(n, 14);
+    const Stream stream(a[13]);
+    const at::Tensor &q = heads_of(a[0], "q");
+    if (!THPVariable_Check(a[2])) bad("an index holds two tensors");
+    const at::Tensor &codes = THPVariable_Unpack(a[2]);
+    need(codes.dim() == 4 || codes.dim() == 5, "index.codes is ([layers,] pages, Hkv, 2, D)");
+    const int64_t N = q.size(0), Hq = q.size(1), D = q.size(2), Hkv = codes.size(-3);
+    const mxg_page_index x = index_of(a[2], a[3], Hkv, D, true);
+    const at::Tensor &ctx = tensor(a[6], "ctx_len", at::kInt, 1);
+    const int64_t B = ctx.numel();
+    const int *cu = index<int>(a[1], "cu_nodes", at::kInt, B + 1);
+    const Table t = table(a[5], "block_table", B);
+    const long page = integer(a[4]), n_sel = integer(a[7]), first = integer(a[8]), last = integer(a[9]);
+    for (const long i : {page, n_sel, first, last}) need(i >= 0 && i <= INT_MAX, "a number of pages is out of range");
+    need(n_sel >= 1 && n_sel <= MXG_ATTN_MAX_SELECT, "n_sel must be 1 to 512");
+    const at::Tensor sel = given(a[10]) ? tensor(a[10], "out", at::kInt, 3)
+                                        : at::empty({N, Hkv, (int64_t)n_sel}, q.options().dtype(at::kInt));
+    need(sel.size(0) == N && sel.size(1) == Hkv && sel.size(2) == n_sel && sel.is_contiguous(),
+         "out must be contiguous (N, Hkv, n_sel)");
+    const at::Tensor ws =
+        given(a[12]) ? tensor(a[12], "ws", at::kByte, 1)
+                     : at::empty({(int64_t)mxg_attn_select_workspace_bytes(as_int(N, "nodes"), as_int(Hkv, "heads"), t.cols)},
+                                 q.options().dtype(at::kByte));
+    mxg_attn_opts o = {};
+    o.workspace = ptr(ws);
+    o.ws_bytes = (size_t)ws.numel();
+    o.dev_status = status_word(a[11]);
+    const mxg_heads qh = heads(q);
+    check("attn_select", attn_select(&qh, cu, as_int(B, "sequences"), as_int(N, "nodes"), &x, (int)page, t.p, t.ld, t.cols,
+                                     static_cast<int *>(ptr(ctx)), as_int(Hq, "heads"), as_int(Hkv, "heads"),
+                                     as_int(D, "channels"), (int)n_sel, (int)first, (int)last,
+                                     static_cast<int *>(ptr(sel)), &o, stream.handle()));
+    return THPVariable_Wrap(sel);
+  });
+}
+
 // (k, v, cu_nodes, accept, cache k, cache v, block_table, ctx_len, ctx_out, dev_status, stream)
 PyObject *py_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded([&]() -> PyObject * {
@@ -310,6 +464,10 @@ PyMethodDef g_methods[] = {
     {"qk_norm_rope", fast<py_rope>(), METH_FASTCALL, nullptr},
     {"attn_prompt", fast<py_prompt>(), METH_FASTCALL, nullptr},
     {"attn_tree", fast<py_tree>(), METH_FASTCALL, nullptr},
+    {"attn_shared", fast<py_shared>(), METH_FASTCALL, nullptr},
+    {"attn_sparse", fast<py_sparse>(), METH_FASTCALL, nullptr},
+    {"attn_select", fast<py_select>(), METH_FASTCALL, nullptr},
+    {"kv_index", fast<py_index>(), METH_FASTCALL, nullptr},
     {"kv_append", fast<py_append>(), METH_FASTCALL, nullptr},
     {"set_error", py_set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},

@@ -9,10 +9,19 @@
  *                  tokens) over a paged cache
  *   kv_append      accepted tokens' keys and values into the cache
  *
+ * and, for long contexts over the same cache:
+ *
+ *   attn_shared    attn_tree for sequences that share a prefix by groups
+ *   kv_index       8-bit bounds of the keys of each full page
+ *   attn_select    the pages whose bounds promise the largest scores
+ *   attn_sparse    attn_tree over selected pages
+ *
  * A prompt pass is qk_norm_rope (which also fills the cache), attn_prompt,
  * o_proj.  A verify step is qk_norm_rope, attn_tree, o_proj per layer, then
  * -- once the accepted path is known -- one kv_append for all layers: the
- * drafted tokens' keys and values stay out of the cache until they count.
+ * drafted tokens' keys and values stay out of the cache until they count.  Over
+ * selected pages a step is qk_norm_rope, attn_select, attn_sparse, o_proj per
+ * layer, then one kv_append and one kv_index for all layers.
  *
  * Conventions are those of mxgemm.h: DEVICE pointers owned by the caller,
  * 16-byte aligned (index arrays: aligned to their element); calls asynchronous
@@ -21,7 +30,9 @@
  * device waits bounded (mxg_attn_opts.timeout_ms); no memory allocated and no
  * pointer kept.  All tensors are bf16; norms, rotations, scores, softmax
  * statistics and accumulators are fp32, rounded to bf16 once at the end (the
- * softmax weights are rounded to bf16 before their product with v).
+ * softmax weights are rounded to bf16 before their product with v).  The bounds
+ * and scores of kv_index and attn_select are whole numbers times powers of two,
+ * computed without rounding: what is selected is the same on any machine.
  * These are inference operators: there are no gradients.
  *
  * What the host cannot see -- lengths, positions, page numbers, node indices
@@ -60,10 +71,23 @@ typedef struct {
     int layers, pages, page_size;
 } mxg_kv_cache;
 
+/* Bounds of the keys of a paged cache's full pages, by physical page: of (layer
+ * l, page p, head h) two rows of D codes -- the upper bounds, then the lower --
+ * at codes + l * codes_layer + p * codes_page + h * codes_head (strides in
+ * bytes, multiples of 16) and the power of two that they count, as an E8M0 code,
+ * at exps + l * exps_layer + p * exps_page + h. */
 typedef struct {
-    void *workspace;     /* attn_tree: device scratch of >= mxg_attn_tree_workspace_bytes(),
-                            256-byte aligned; its contents on entry do not matter.  Calls that
-                            overlap on the GPU need separate workspaces. */
+    int8_t *codes;
+    uint8_t *exps;
+    int64_t codes_layer, codes_page, codes_head, exps_layer, exps_page;
+    int layers, pages;
+} mxg_page_index;
+
+typedef struct {
+    void *workspace;     /* attn_tree, attn_shared, attn_select, attn_sparse: device scratch of >=
+                            mxg_<name>_workspace_bytes(), 256-byte aligned; its contents on
+                            entry do not matter.  Calls that overlap on the GPU need separate
+                            workspaces. */
     size_t ws_bytes;
     int *dev_status;     /* optional device int; kernels OR MXG_DEV_* bits into it */
     uint32_t timeout_ms; /* limit of every device-side wait; 0 = 1000 ms.  The longest legitimate
@@ -76,6 +100,8 @@ typedef struct {
  * nodes of one sequence's tree (the bits of a mask word). */
 #define MXG_ATTN_MAX_SEQS 4096
 #define MXG_ATTN_MAX_NODES 64
+/* Most pages that attn_select selects and attn_sparse takes. */
+#define MXG_ATTN_MAX_SELECT 512
 
 /* For every token t < T and every head of q (Hq heads) and k (Hkv heads):
  *   y = x * rsqrt(mean(x^2) + eps) * w     (w: wq or wk, D bf16 gains;
@@ -160,6 +186,84 @@ mxg_status kv_append(const mxg_heads *k, int64_t k_layer_stride, const mxg_heads
                      int ld_accept, int max_accept, const mxg_kv_cache *cache,
                      const int *block_table, int ld_table, int table_cols, const int *ctx_len,
                      int Hkv, int D, int *ctx_out, int *dev_status, mxg_stream_t stream);
+
+/* attn_tree for sequences that share the beginning of their contexts by groups,
+ * which is then read once for the group.  Group g is sequences cu_groups[g] ..
+ * cu_groups[g+1] - 1 (n_groups + 1 ints, cu_groups[0] = 0, non-decreasing,
+ * cu_groups[n_groups] <= B; sequences past it share nothing); the first
+ * prefix_len[g] cached tokens of each of them, a multiple of page_size, are read
+ * from the pages in the block table's row of the group's first sequence (where
+ * the others name the same pages, the result is attn_tree's).  ctx_len counts
+ * them: it is at least prefix_len[g] throughout the group.  Everything else is as
+ * for attn_tree.
+ * n_groups <= B; n_groups 0: cu_groups and prefix_len may be NULL.
+ * Out of range, besides attn_tree's: cu_groups is clamped as offsets are,
+ * prefix_len to [0, the group's smallest ctx_len] and then to whole pages. */
+size_t mxg_attn_shared_workspace_bytes(int N, int Hq, int D);
+mxg_status attn_shared(const mxg_heads *q, const mxg_heads *k, const mxg_heads *v,
+                       const int *cu_nodes, const uint64_t *mask, int B, int N,
+                       const mxg_kv_cache *cache, const int *block_table, int ld_table,
+                       int table_cols, const int *ctx_len, const int *cu_groups,
+                       const int *prefix_len, int n_groups, int Hq, int Hkv, int D, float scale,
+                       const mxg_heads *out, const mxg_attn_opts *opts, mxg_stream_t stream);
+
+/* Bounds of the pages that became full, in every layer: of each sequence b, the
+ * pages j with floor(ctx_old[b] / page_size) <= j < floor(ctx_new[b] / page_size)
+ * (ctx_old NULL: all zero), after their keys were written.  Of the page's keys of
+ * a layer and kv head:
+ *   e = the least whole number >= -100 with max |k| <= 127 * 2^e
+ *   upper[d] = ceil(max k[d] / 2^e), lower[d] = floor(min k[d] / 2^e)
+ *   E8M0 code e + 127;  255 and all bounds zero where a key is NaN or infinite.
+ * Sequences may share pages.  Other pages' entries are left as they were; v is
+ * not read (cache->v must be given all the same).  index: as many layers as the
+ * cache, entries for at least its pages.
+ * D in {64, 128}, B <= MXG_ATTN_MAX_SEQS.
+ * Out of range: ctx_old and ctx_new are clamped to [0, table_cols * page_size], a
+ * page outside [0, pages) is skipped. */
+mxg_status kv_index(const mxg_kv_cache *cache, int Hkv, int D, const mxg_page_index *index,
+                    const int *block_table, int B, int ld_table, int table_cols,
+                    const int *ctx_old, const int *ctx_new, int *dev_status, mxg_stream_t stream);
+
+/* The pages that each node attends to, for each kv head h: of the sequence's
+ * P = ceil(ctx_len / page_size) logical pages the first `first` and the last
+ * `last`, and of the others those with the highest scores, lower pages first
+ * among equals, until there are n_sel (all, if P <= n_sel).  With the bounds of
+ * the page (layer 0 of index) and the query heads g of kv head h:
+ *   e = the least whole number >= -100 with max |q| <= 127 * 2^e over g and d
+ *   x[g][d] = q[g][d] / 2^e rounded to the nearest whole number, ties to even
+ *   score = 2^(code - 127) * max_g sum_d max(x[g][d] upper[d], x[g][d] lower[d])
+ * which is an upper bound of q . k over the page's keys, up to the rounding of q
+ * and a factor that the node's scores have in common.  A page of code 255 comes
+ * before all others; a q that holds a NaN or an infinity counts as zero.
+ * sel: (N, Hkv, n_sel) ints: logical page numbers, ascending, then -1; rows of
+ * nodes past cu_nodes[B] are not written.  The last page, which may not be full, is
+ * always selected and needs no bounds: 1 <= last, 0 <= first, first + last <= n_sel
+ * <= MXG_ATTN_MAX_SELECT.
+ * D in {64, 128}, Hq % Hkv == 0, Hq / Hkv <= 128, B <= MXG_ATTN_MAX_SEQS.
+ * Out of range: offsets, nodes and ctx_len are clamped as for attn_tree; a page
+ * whose number is outside [0, index->pages) has the score zero. */
+size_t mxg_attn_select_workspace_bytes(int N, int Hkv, int table_cols);
+mxg_status attn_select(const mxg_heads *q, const int *cu_nodes, int B, int N,
+                       const mxg_page_index *index, int page_size, const int *block_table,
+                       int ld_table, int table_cols, const int *ctx_len, int Hq, int Hkv, int D,
+                       int n_sel, int first, int last, int *sel, const mxg_attn_opts *opts,
+                       mxg_stream_t stream);
+
+/* attn_tree where node i and the query heads of kv head h see, of the sequence's
+ * cached tokens, those in the logical pages sel[(i * Hkv + h) * n_sel ...]
+ * (negative entries name none; any order; a page named twice is seen once).  A
+ * page is read once for all nodes of its sequence that name it.  Everything else
+ * is as for attn_tree.
+ * 1 <= n_sel <= MXG_ATTN_MAX_SELECT.
+ * Out of range, besides attn_tree's: a logical page at or past the sequence's
+ * last one names none. */
+size_t mxg_attn_sparse_workspace_bytes(int N, int Hkv, int n_sel, int D);
+mxg_status attn_sparse(const mxg_heads *q, const mxg_heads *k, const mxg_heads *v,
+                       const int *cu_nodes, const uint64_t *mask, int B, int N,
+                       const mxg_kv_cache *cache, const int *block_table, int ld_table,
+                       int table_cols, const int *ctx_len, const int *sel, int n_sel, int Hq,
+                       int Hkv, int D, float scale, const mxg_heads *out,
+                       const mxg_attn_opts *opts, mxg_stream_t stream);
 
 #ifdef __cplusplus
 }
