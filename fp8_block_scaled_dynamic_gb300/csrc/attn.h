@@ -39,6 +39,24 @@ struct AppendParams {
   int B, N, Hkv, D, ld_accept, max_accept, ld_table, table_cols;
 };
 
+// A sequence as the kernels see it where a plan kernel has worked it out: its
+// nodes as queries (rows), the keys in a list of pages, and perhaps its nodes.
+struct PlanRec {
+  int a0, n, ctx, hk;  // first node, nodes, cached tokens in the list, kv head or -1 (all)
+  long long list;      // where its page numbers begin
+  int flags, pad;
+};
+static_assert(sizeof(PlanRec) == 32, "read as two 16-byte words");
+
+struct Plan {
+  const PlanRec *rec;
+  int n;                            // records
+  const int *list;                  // sparse: page numbers
+  const unsigned long long *names;  // sparse: the nodes that name a page, a bit each
+  const int *info;                  // shared: of each node, how its parts are joined
+  float *rows, *stats;              // shared: parts of whole rows (prefix, own): sums, references and weights
+};
+
 struct AttnParams {
   Heads q, k, v, out;
   Cache cache;              // tree only
@@ -48,9 +66,11 @@ struct AttnParams {
   int B, T, Hq, Hkv, D, ld_table, table_cols;
   float scale;
   float *ws;
+  long long slots;  // floats before the CTAs' parts
   int *status;
   unsigned long long timeout_ns;
   int debug_stall;
+  Plan plan;
 };
 
 struct SharedParams {  // attn_shared
@@ -92,6 +112,7 @@ struct SelectParams {
 constexpr int kAttnMaxSeqs = 4096;
 constexpr int kAttnMaxNodes = 64;
 constexpr int kAttnMaxSelect = 512;
+constexpr int kAttnMaxListed = 1 << 19;  // columns of attn_sparse's block table (a bit each in shared memory)
 
 cudaError_t launch_qk_norm_rope(const RopeParams &p, bool interleaved, int sm_count, cudaStream_t stream);
 cudaError_t launch_kv_append(const AppendParams &p, cudaStream_t stream);

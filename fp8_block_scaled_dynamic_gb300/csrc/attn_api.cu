@@ -311,6 +311,7 @@ mxg_status attn_shared(const mxg_heads *q, const mxg_heads *k, const mxg_heads *
   mxg_status st = check_attn(q, k, v, cu_nodes, B, N, Hq, Hkv, D, scale, out, opts);
   if (st != MXG_OK) return st;
   if (n_groups < 0 || n_groups > B || (n_groups > 0 && (!cu_groups || !prefix_len))) return MXG_ERR_INVALID_ARG;
+  if (N / (256 / (Hq / Hkv)) >= (1 << 22)) return MXG_ERR_UNSUPPORTED_SHAPE;  // (a group's row groups)
   if ((st = check_paged(N, mask, cache, block_table, ld_table, table_cols, ctx_len, Hkv)) != MXG_OK) return st;
   if (!aligned(cu_groups, 4) || !aligned(prefix_len, 4)) return MXG_ERR_MISALIGNED;
   int sm = 0;
@@ -428,7 +429,8 @@ mxg_status attn_sparse(const mxg_heads *q, const mxg_heads *k, const mxg_heads *
   mxg_status st = check_attn(q, k, v, cu_nodes, B, N, Hq, Hkv, D, scale, out, opts);
   if (st != MXG_OK) return st;
   if (n_sel < 1 || (N > 0 && !sel)) return MXG_ERR_INVALID_ARG;
-  if (n_sel > mxg::kAttnMaxSelect) return MXG_ERR_UNSUPPORTED_SHAPE;
+  if (n_sel > mxg::kAttnMaxSelect || table_cols > mxg::kAttnMaxListed)
+    return MXG_ERR_UNSUPPORTED_SHAPE;
   if ((st = check_paged(N, mask, cache, block_table, ld_table, table_cols, ctx_len, Hkv)) != MXG_OK) return st;
   if (!aligned(sel, 4)) return MXG_ERR_MISALIGNED;
   int sm = 0;

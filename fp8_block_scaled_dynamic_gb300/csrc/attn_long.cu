@@ -1,111 +1,303 @@
 // attn_long.cu -- attention of drafted trees whose sequences share a prefix by
 // groups (attn_shared) and over selected pages (attn_sparse).
-#include <cuda_runtime.h>
-#include <cstdint>
-
-#include "attn.h"
-#include "attn_ptx.cuh"
-#include "kernels.h"
+//
+// Both are attn_kernel.cuh's kernel over records that a plan kernel writes:
+// - shared: a record a group, the nodes of all its sequences as rows of the
+//   prefix's keys (so a prefix is read once for 256 rows of a kv head, not once a
+//   sequence), and a record a sequence, its nodes over its own keys.  A row that has
+//   parts of both is joined from them: softmax's sums over disjoint sets of keys add
+//   up once they have a common reference.
+// - sparse: a record a sequence and kv head, whose keys are the pages that any of
+//   its nodes names, in order, with a word a page that says which nodes do.  A page
+//   is then loaded once for all of them; the scores of those that do not name it are
+//   taken out by the word.
+#include "attn_kernel.cuh"
 
 namespace mxg {
 namespace {
 
-constexpr int kBadIndex = 0x2;  // MXG_DEV_BAD_INDEX
 constexpr unsigned kFull = 0xFFFFFFFFu;
 
-// One warp a node and query head, keys one after another with a running maximum.
-template <int D>
-__global__ void __launch_bounds__(32) simple_kernel(const AttnParams p, const int *groups, const int *prefix, int n_groups,
-                                                    const int *sel, int n_sel) {
-  constexpr int V = D / 32;
-  const int node = blockIdx.x, head = blockIdx.y, hk = head / (p.Hq / p.Hkv), lane = threadIdx.x, page = p.cache.page_size;
-  const int limit = p.table_cols * page;
-  int running = 0, b = -1, a0 = 0, n = 0;
+// Exclusive sum (or running maximum) over the block's threads of one value each.
+template <int THREADS, class Op>
+__device__ __forceinline__ int scan_block(int x, int none, int *s_warp, Op op, int *total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl = op(incl, y);
+  }
+  __syncthreads();  // (s_warp may be in use)
+  if (lane == 31) s_warp[warp] = incl;
+  int excl = __shfl_up_sync(kFull, incl, 1);
+  if (lane == 0) excl = none;
+  __syncthreads();
+  int all = none;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) excl = op(excl, s_warp[w]);
+    all = op(all, s_warp[w]);
+  }
+  if (total) *total = all;
+  return excl;
+}
+struct Max {
+  __device__ int operator()(int a, int b) const { return max(a, b); }
+};
+struct Sum {
+  __device__ int operator()(int a, int b) const { return a + b; }
+};
+
+// ------------------------------------------------------------------ shared
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanOwn = kAttnMaxSeqs / kPlanThreads;  // sequences (groups) of a thread, one after another
+
+// One block: the sequences' nodes and contexts, the groups' sequences and
+// prefixes, all within their bounds, as records.
+__global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedParams p, PlanRec *rec, int *info) {
+  __shared__ int s_a0[kAttnMaxSeqs + 1], s_len[kAttnMaxSeqs], s_warp[kPlanThreads / 32];
+  __shared__ uint16_t s_g[kAttnMaxSeqs + 1];
+  pdl_trigger();
+  pdl_wait();
+  const AttnParams &a = p.a;
+  const int B = a.B, page = a.cache.page_size, limit = a.table_cols * page, tid = threadIdx.x;
   bool bad = false;
-  for (int i = 0; i < p.B; ++i) {
-    const int c0 = p.cu[i], c1 = p.cu[i + 1], x0 = max(min(max(c0, 0), p.T), running);
-    int x1 = max(min(max(c1, 0), p.T), x0);
-    bad |= c0 != x0 || c1 != x1 || x1 - x0 > kAttnMaxNodes || p.ctx[i] < 0 || p.ctx[i] > limit;
-    x1 = min(x1, x0 + kAttnMaxNodes);
-    running = x0;
-    if (node >= x0 && node < x1) b = i, a0 = x0, n = x1 - x0;
-  }
-  int shared = 0, first = b;
-  running = 0;
-  for (int g = 0; g < n_groups; ++g) {
-    const int c0 = groups[g], c1 = groups[g + 1], g0 = max(min(max(c0, 0), p.B), running);
-    const int g1 = max(min(max(c1, 0), p.B), g0);
-    bad |= c0 != g0 || c1 != g1;
-    running = g0;
-    int least = limit;
-    for (int i = g0; i < g1; ++i) least = min(least, min(max(p.ctx[i], 0), limit));
-    const int len = min(max(prefix[g], 0), least) / page * page;
-    bad |= len != prefix[g];
-    if (b >= g0 && b < g1) shared = len, first = g0;
-  }
-  if (bad && p.status && lane == 0) atomicOr(p.status, kBadIndex);
-  if (b < 0) return;
-  const int ctx = min(max(p.ctx[b], 0), limit);
-  float q[V], o[V] = {}, m = -INFINITY, l = 0.0f;
-  bool any = false;
-  auto value = [](uint16_t x) { return __uint_as_float((uint32_t)x << 16); };
-  for (int i = 0; i < V; ++i) q[i] = value(p.q.ptr[node * p.q.tok + head * p.q.head + lane * V + i]);
-  auto take = [&](const uint16_t *k, const uint16_t *v) {
-    float s = 0.0f;
-    for (int i = 0; i < V; ++i) s += q[i] * (k ? value(k[lane * V + i]) : 0.0f);
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(kFull, s, x);
-    s *= p.scale * 1.4426950408889634f;
-    any = true;
-    const float mn = fmaxf(m, s), f = m == mn ? 1.0f : ex2(m - mn), w = ex2(s - mn);
-    l = l * f + w;
-    for (int i = 0; i < V; ++i) o[i] = o[i] * f + w * (v ? value(v[lane * V + i]) : 0.0f);
-    m = mn;
-  };
-  auto take_page = [&](int row, int j, int n_tok) {
-    const int pg = p.table[(long long)row * p.ld_table + j];
-    const bool in = (uint32_t)pg < (uint32_t)p.cache.pages;
-    if (!in && p.status && lane == 0) atomicOr(p.status, kBadIndex);
-    for (int t = 0; t < n_tok; ++t) {
-      const long long at = pg * p.cache.page + t * p.cache.slot + hk * p.cache.head;
-      take(in ? p.cache.k + at : nullptr, in ? p.cache.v + at : nullptr);
+  // offsets never fall: a thread's own ones, then what comes before them
+  auto clamp_offsets = [&](const int *at, int n, int most, auto put) {
+    const int per = (n + kPlanThreads - 1) / kPlanThreads, b0 = min(tid * per, n), b1 = min(b0 + per, n);
+    int top = 0;
+    for (int b = b0; b < b1; ++b) top = max(top, min(max(__ldg(at + b), 0), most));
+    int running = scan_block<kPlanThreads>(top, 0, s_warp, Max(), nullptr);
+    for (int b = b0; b < b1; ++b) {
+      const int raw = __ldg(at + b);
+      running = max(running, min(max(raw, 0), most));
+      bad |= raw != running;
+      put(b, running);
     }
   };
-  if (sel) {
-    const int *mine = sel + ((long long)node * p.Hkv + hk) * n_sel;
-    for (int i = 0; i < n_sel; ++i)
-      if (mine[i] >= 0 && (long long)mine[i] * page >= ctx && p.status && lane == 0) atomicOr(p.status, kBadIndex);
-    for (int j = 0; j * page < ctx; ++j) {
-      bool named = false;
-      for (int i = lane; i < n_sel; i += 32) named |= mine[i] == j;
-      if (__any_sync(kFull, named)) take_page(b, j, min(page, ctx - j * page));
+  clamp_offsets(a.cu, B + 1, a.T, [&](int b, int x) { s_a0[b] = x; });
+  const int ng = p.n_groups;
+  if (ng > 0) clamp_offsets(p.groups, ng + 1, B, [&](int g, int x) { s_g[g] = (uint16_t)x; });
+  for (int g = tid; g < ng; g += kPlanThreads) s_len[g] = limit;
+  __syncthreads();
+  // a sequence's group, or -1: the last group that begins at or before it and is not empty
+  auto group_of = [&](int b) {
+    if (ng == 0 || b < s_g[0] || b >= s_g[ng]) return -1;
+    int lo = 0, hi = ng - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_g[mid] <= b) lo = mid;
+      else hi = mid - 1;
     }
-  } else {
-    for (int j = 0; j * page < ctx; ++j) take_page(j * page < shared ? first : b, j, min(page, ctx - j * page));
+    return lo;
+  };
+  int ctx[kPlanOwn], of[kPlanOwn];
+#pragma unroll
+  for (int i = 0; i < kPlanOwn; ++i) {
+    const int b = tid + i * kPlanThreads;
+    of[i] = -1;
+    if (b >= B) continue;
+    const int raw = __ldg(a.ctx + b);
+    ctx[i] = min(max(raw, 0), limit);
+    bad |= raw != ctx[i] || s_a0[b + 1] - s_a0[b] > kAttnMaxNodes;
+    of[i] = group_of(b);
+    if (of[i] >= 0) atomicMin(&s_len[of[i]], ctx[i]);
   }
-  for (int i = 0; i < n; ++i)
-    if (p.mask[node] >> i & 1ull)
-      take(p.k.ptr + (a0 + i) * p.k.tok + hk * p.k.head, p.v.ptr + (a0 + i) * p.v.tok + hk * p.v.head);
-  uint16_t *out = p.out.ptr + node * p.out.tok + head * p.out.head;
-  for (int i = 0; i < V; ++i) out[lane * V + i] = any ? (uint16_t)pack_bf16x2(o[i] / l, 0.0f) : 0;
+  __syncthreads();
+  for (int g = tid; g < ng; g += kPlanThreads) {
+    const int g0 = s_g[g], g1 = s_g[g + 1], raw = __ldg(p.prefix + g);
+    const int len = g1 > g0 ? min(max(raw, 0), s_len[g]) / page * page : 0;
+    bad |= g1 > g0 && raw != len;
+    s_len[g] = len;
+    PlanRec r = {};
+    r.a0 = s_a0[g0];
+    r.n = s_a0[g1] - r.a0;
+    r.ctx = len;
+    r.hk = -1;
+    r.list = (long long)g0 * a.ld_table;
+    r.flags = kJoined;
+    rec[g] = r;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kPlanOwn; ++i) {
+    const int b = tid + i * kPlanThreads;
+    if (b >= B) continue;
+    const int len = of[i] >= 0 ? s_len[of[i]] : 0, a0 = s_a0[b], a1 = s_a0[b + 1];
+    PlanRec r = {};
+    r.a0 = a0;
+    r.n = min(a1 - a0, kAttnMaxNodes);
+    r.ctx = ctx[i] - len;
+    r.hk = -1;
+    r.list = (long long)b * a.ld_table + len / page;
+    r.flags = kHasNodes | (len > 0 ? kJoined : 0);
+    rec[ng + b] = r;
+    for (int x = a0; x < a1; ++x) info[x] = x - a0 < kAttnMaxNodes ? len > 0 : -1;
+  }
+  for (int x = tid; x < s_a0[0]; x += kPlanThreads) info[x] = -1;
+  for (int x = s_a0[B] + tid; x < a.T; x += kPlanThreads) info[x] = -1;
+  if (bad && a.status) atomicOr(a.status, kBadIndex);
 }
 
-cudaError_t launch(const AttnParams &p, const int *groups, const int *prefix, int n_groups, const int *sel, int n_sel,
-                   cudaStream_t stream) {
-  const dim3 grid((unsigned)p.T, (unsigned)p.Hq);
-  if (p.D == 64) simple_kernel<64><<<grid, 32, 0, stream>>>(p, groups, prefix, n_groups, sel, n_sel);
-  else simple_kernel<128><<<grid, 32, 0, stream>>>(p, groups, prefix, n_groups, sel, n_sel);
-  return cudaGetLastError();
+// ------------------------------------------------------------------ sparse
+constexpr int kListThreads = 128;
+
+// A block a sequence and kv head: the pages that any of its nodes names, in
+// order (a bit a logical page in shared memory, a page's place is the number of bits
+// below its own), and for several nodes the word of those that name it.
+__global__ void __launch_bounds__(kListThreads) sparse_plan_kernel(const SparseParams p, PlanRec *rec, int *list,
+                                                                   unsigned long long *names) {
+  extern __shared__ uint32_t s_bits[];  // words of bits, then the number of bits before each
+  __shared__ int s_warp[kListThreads / 32];
+  pdl_trigger();
+  const AttnParams &a = p.a;
+  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, page = a.cache.page_size;
+  pdl_wait();
+  int top = 0;
+  for (int i = tid; i <= b; i += kListThreads) top = max(top, min(max(__ldg(a.cu + i), 0), a.T));
+  int a0;
+  scan_block<kListThreads>(top, 0, s_warp, Max(), &a0);
+  const int c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1), a1 = max(min(max(c1, 0), a.T), a0);
+  const int n = min(a1 - a0, kAttnMaxNodes), raw = __ldg(a.ctx + b), ctx = min(max(raw, 0), a.table_cols * page);
+  bool bad = h == 0 && (c0 != a0 || c1 != a1 || a1 - a0 > kAttnMaxNodes || raw != ctx);
+  const int P = (ctx + page - 1) / page, W = (P + 31) / 32, total = n * p.n_sel;
+  uint32_t *s_before = s_bits + W;
+  for (int i = tid; i < W; i += kListThreads) s_bits[i] = 0;
+  __syncthreads();
+  // (a node's pages of this kv head follow one another, the next node's are Hkv lists on)
+  const int *sel = p.sel + ((long long)a0 * a.Hkv + h) * p.n_sel;
+  auto named = [&](int e, int &node) {
+    node = e / p.n_sel;
+    return __ldg(sel + (long long)node * a.Hkv * p.n_sel + (e - node * p.n_sel));
+  };
+  for (int e = tid; e < total; e += kListThreads) {
+    int node;
+    const int j = named(e, node);
+    bad |= j >= P;
+    if (j >= 0 && j < P) atomicOr(&s_bits[j >> 5], 1u << (j & 31));
+  }
+  __syncthreads();
+  const int per = (W + kListThreads - 1) / kListThreads, w0 = min(tid * per, W), w1 = min(w0 + per, W);
+  int sum = 0, count;
+  for (int i = w0; i < w1; ++i) sum += __popc(s_bits[i]);
+  int at = scan_block<kListThreads>(sum, 0, s_warp, Sum(), &count);
+  const long long base = ((long long)a0 * a.Hkv + (long long)h * n) * p.n_sel;
+  for (int i = w0; i < w1; ++i) {
+    s_before[i] = at;
+    for (uint32_t bits = s_bits[i]; bits; bits &= bits - 1) {
+      list[base + at] = __ldg(a.table + (long long)b * a.ld_table + i * 32 + __ffs(bits) - 1);
+      if (n > 1) names[base + at] = 0;
+      ++at;
+    }
+  }
+  __syncthreads();
+  if (n > 1)
+    for (int e = tid; e < total; e += kListThreads) {
+      int node;
+      const int j = named(e, node);
+      if (j >= 0 && j < P)
+        atomicOr(names + base + s_before[j >> 5] + __popc(s_bits[j >> 5] & ((1u << (j & 31)) - 1u)), 1ull << node);
+    }
+  if (tid == 0) {
+    const bool has_last = P > 0 && (s_bits[(P - 1) >> 5] >> ((P - 1) & 31) & 1u);
+    PlanRec r = {};
+    r.a0 = a0;
+    r.n = n;
+    r.ctx = count == 0 ? 0 : (count - 1) * page + (has_last ? ctx - (P - 1) * page : page);
+    r.hk = h;
+    r.list = base;
+    r.flags = kHasNodes | (n > 1 ? kLists : 0);
+    rec[b * a.Hkv + h] = r;
+  }
+  if (bad && a.status) atomicOr(a.status, kBadIndex);
 }
+
+// -------------------------------------------------------------- workspaces
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+size_t slots_bytes(int D, int sm_count) {
+  const long long f = D == 64 ? Cfg<64, kShared>::kSlotFloats : Cfg<128, kShared>::kSlotFloats;
+  return (size_t)(2 * f * (sm_count < kMaxCtas ? sm_count : kMaxCtas)) * sizeof(float);
+}
+
+// Byte offsets; the items that attn_join_kernel reads come first.
+struct SharedWs {
+  size_t rec, info, slots, rows, stats, end;
+  SharedWs(long long N, int Hq, int D, int sm_count) {
+    rec = kJoinFloats * sizeof(float);
+    info = rec + 2 * kAttnMaxSeqs * sizeof(PlanRec);
+    slots = round256(info + N * sizeof(int));
+    rows = slots + slots_bytes(D, sm_count);
+    stats = rows + (size_t)(2 * N * Hq) * D * sizeof(float);
+    end = round256(stats + (size_t)(2 * N * Hq) * 2 * sizeof(float));
+  }
+};
+struct SparseWs {
+  size_t rec, slots, names, list, end;
+  SparseWs(long long N, int Hkv, int n_sel, int D, int sm_count) {
+    rec = kJoinFloats * sizeof(float);
+    slots = rec + (size_t)kAttnMaxSeqs * Hkv * sizeof(PlanRec);
+    names = slots + slots_bytes(D, sm_count);
+    list = names + (size_t)(N * Hkv) * n_sel * sizeof(unsigned long long);
+    end = round256(list + (size_t)(N * Hkv) * n_sel * sizeof(int));
+  }
+};
 
 }  // namespace
 
-cudaError_t launch_attn_shared(const SharedParams &p, int, cudaStream_t stream) {
-  return launch(p.a, p.groups, p.prefix, p.n_groups, nullptr, 0, stream);
+size_t attn_shared_ws_bytes(long long N, int Hq, int D, int sm_count) { return SharedWs(N, Hq, D, sm_count).end; }
+size_t attn_sparse_ws_bytes(long long N, int Hkv, int n_sel, int D, int sm_count) {
+  return SparseWs(N, Hkv, n_sel, D, sm_count).end;
 }
-size_t attn_shared_ws_bytes(long long, int, int, int) { return 256; }
-cudaError_t launch_attn_sparse(const SparseParams &p, int, cudaStream_t stream) {
-  return launch(p.a, nullptr, nullptr, 0, p.sel, p.n_sel, stream);
+
+cudaError_t launch_attn_shared(const SharedParams &shared, int sm_count, cudaStream_t stream) {
+  SharedParams p = shared;
+  const SharedWs ws(p.a.T, p.a.Hq, p.a.D, sm_count);
+  char *w = reinterpret_cast<char *>(p.a.ws);
+  PlanRec *rec = reinterpret_cast<PlanRec *>(w + ws.rec);
+  int *info = reinterpret_cast<int *>(w + ws.info);
+  cudaLaunchConfig_t cfg = pdl_config(dim3(1), dim3(kPlanThreads), 0, stream);
+  cudaLaunchAttribute attr[1];
+  attach_pdl(cfg, attr);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, shared_plan_kernel, p, rec, info);
+  if (e != cudaSuccess) return e;
+  p.a.slots = (long long)(ws.slots / sizeof(float));
+  p.a.plan.rec = rec;
+  p.a.plan.n = p.n_groups + p.a.B;
+  p.a.plan.info = info;
+  p.a.plan.rows = reinterpret_cast<float *>(w + ws.rows);
+  p.a.plan.stats = reinterpret_cast<float *>(w + ws.stats);
+  return p.a.D == 64 ? launch_t<64, kShared>(p.a, sm_count, stream) : launch_t<128, kShared>(p.a, sm_count, stream);
 }
-size_t attn_sparse_ws_bytes(long long, int, int, int, int) { return 256; }
+
+cudaError_t launch_attn_sparse(const SparseParams &sparse, int sm_count, cudaStream_t stream) {
+  SparseParams p = sparse;
+  const SparseWs ws(p.a.T, p.a.Hkv, p.n_sel, p.a.D, sm_count);
+  char *w = reinterpret_cast<char *>(p.a.ws);
+  PlanRec *rec = reinterpret_cast<PlanRec *>(w + ws.rec);
+  int *list = reinterpret_cast<int *>(w + ws.list);
+  unsigned long long *names = reinterpret_cast<unsigned long long *>(w + ws.names);
+  static DeviceOnce once;
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!once.done(dev)) {
+    e = cudaFuncSetAttribute(sparse_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnMaxListed / 32 * 8);
+    if (e != cudaSuccess) return e;
+    once.set(dev);
+  }
+  const size_t smem = (size_t)((p.a.table_cols + 31) / 32) * 2 * sizeof(uint32_t);
+  cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)p.a.Hkv, (unsigned)p.a.B), dim3(kListThreads), smem, stream);
+  cudaLaunchAttribute attr[1];
+  attach_pdl(cfg, attr);
+  e = cudaLaunchKernelEx(&cfg, sparse_plan_kernel, p, rec, list, names);
+  if (e != cudaSuccess) return e;
+  p.a.slots = (long long)(ws.slots / sizeof(float));
+  p.a.plan.rec = rec;
+  p.a.plan.n = p.a.B * p.a.Hkv;
+  p.a.plan.list = list;
+  p.a.plan.names = names;
+  return p.a.D == 64 ? launch_t<64, kSparse>(p.a, sm_count, stream) : launch_t<128, kSparse>(p.a, sm_count, stream);
+}
 
 }  // namespace mxg

@@ -254,7 +254,7 @@ mxg_status attn_select(const mxg_heads *q, const int *cu_nodes, int B, int N,
  * (negative entries name none; any order; a page named twice is seen once).  A
  * page is read once for all nodes of its sequence that name it.  Everything else
  * is as for attn_tree.
- * 1 <= n_sel <= MXG_ATTN_MAX_SELECT.
+ * 1 <= n_sel <= MXG_ATTN_MAX_SELECT, table_cols <= 524288.
  * Out of range, besides attn_tree's: a logical page at or past the sequence's
  * last one names none. */
 size_t mxg_attn_sparse_workspace_bytes(int N, int Hkv, int n_sel, int D);

@@ -37,7 +37,7 @@ SPARSE = dict(q=H(), k=H(), v=H(), cu=P, mask=P, B=2, N=10, cache=C(), table=P, 
 
 
 @pytest.mark.parametrize("kw,want", PAGED + [
-    (dict(sel=None), 1), (dict(n_sel=0), 1), (dict(n_sel=513), 2), (dict(sel=P + 2), 3),
+    (dict(sel=None), 1), (dict(n_sel=0), 1), (dict(n_sel=513), 2), (dict(sel=P + 2), 3), (dict(cols=1 << 20, ld=1 << 20), 2),
 ])
 def test_sparse_refusals(kw, want):
     assert mx.lib().attn_sparse(*{**SPARSE, **kw}.values()) == want
