@@ -231,7 +231,7 @@ mxg_status kv_index(const mxg_kv_cache *cache, int Hkv, int D, const mxg_page_in
  * the page (layer 0 of index) and the query heads g of kv head h:
  *   e = the least whole number >= -100 with max |q| <= 127 * 2^e over g and d
  *   x[g][d] = q[g][d] / 2^e rounded to the nearest whole number, ties to even
- *   score = 2^(code - 127) * max_g sum_d max(x[g][d] upper[d], x[g][d] lower[d])
+ *   score = 2^(code - 127) * max_g sum_d x[g][d] * (x[g][d] > 0 ? upper[d] : lower[d])
  * which is an upper bound of q . k over the page's keys, up to the rounding of q
  * and a factor that the node's scores have in common.  A page of code 255 comes
  * before all others; a q that holds a NaN or an infinity counts as zero.

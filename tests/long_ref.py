@@ -117,7 +117,7 @@ def select(q, nodes, codes, exps, table, ctx, page, n_sel, first, last, N):
                             s = math.inf
                         else:
                             up, down = codes[pg, h]
-                            s = int(torch.maximum(x * up, x * down).sum(1).max()) * 2.0 ** (exps[pg][h] - 127)
+                            s = int((x.clamp_min(0) * up + x.clamp_max(0) * down).sum(1).max()) * 2.0 ** (exps[pg][h] - 127)
                         rest.append((-s, j))
                 pick = sorted(always + [j for _, j in sorted(rest)[:max(n_sel - len(always), 0)]]) if P > n_sel else list(range(P))
                 out[i, h] = torch.tensor(pick + [-1] * (n_sel - len(pick)), dtype=torch.int32)
