@@ -164,32 +164,40 @@ __global__ void __launch_bounds__(kIndexThreads) index_kernel(const IndexParams 
 // for the query heads of up to eight groups of eight columns, by
 //   sum_d x (x > 0 ? u : l) = [max(x, 0) | min(x, 0)] . [u | l],
 // a product of 2 D whole numbers below 2^7 that m16n8k16 in fp16 with fp32 sums has
-// exactly.  (A page's codes are read straight into the order in which the product
-// wants them: which 16 of the 2 D positions a step takes does not matter as long as
-// both operands agree.)  A score goes, as a 32-bit key of the same order, to the
-// shared memory of the block that chooses for its node; then the warps of a node
-// find the key of the last page that is taken, bit by bit from the top, and write
-// the pages out in order.
-constexpr int kSelectThreads = 256, kSelectWarps = kSelectThreads / 32;
-constexpr int kSelectGroups = 8;       // of eight columns (query heads) in a pass, or one node's
-constexpr int kSelectKeys = 16 * 1024; // keys of a block in shared memory, where one node's are no more
-constexpr int kSelectMostKeys = 38 * 1024;  // beyond that they are in the workspace
+// exactly (the 8-bit form of the instruction, without the codes' conversion, is far
+// slower on this part: a batch of 64 x 1024 pages 102 us where this one took 72).  A
+// page's codes are kept in the order in which the product wants them: which 16 of the
+// 2 D positions a step takes does not matter as long as both operands agree.  With one
+// group a tile's registers are filled again for the next tile as they are used; with
+// several (MANY) its codes are converted once.  A score goes, as a 32-bit key of the
+// same order, to the shared memory of the block that chooses for its node; there the
+// warps of a node find the key of the last page that is taken, bit by bit from the top,
+// and write the pages out in order.
+constexpr int kSelectWarps = 8;  // most warps of a block
+template <bool MANY>
+constexpr int kWarps = MANY ? 8 : 4;
+constexpr int kSelectGroups = 8;            // most groups of eight columns (query heads) in a pass, or one node's
+constexpr int kSelectKeys = 12 * 1024;      // most keys of a block in shared memory, where one node's are no more
+constexpr int kSelectMostKeys = 32 * 1024;  // beyond that they are in the workspace
 constexpr int kSelectMostCluster = 8;
 
 struct SelectPlan {
-  int cluster;   // blocks of a sequence and kv head
-  int cols;      // keys of a node: the table's columns, rounded up to 128
-  int slots;     // nodes that a block chooses for in a pass
-  int gp;        // columns of a node: Hq / Hkv rounded up to 1, 2, 4 or a multiple of 8
-  int groups;    // of eight columns in a pass
-  bool spill;    // keys in the workspace
+  int cluster;  // blocks of a sequence and kv head, a power of two
+  int shift;    // its logarithm
+  int cols;     // keys of a node: the table's columns, rounded up to blocks (key_at)
+  int slots;    // nodes that a block chooses for in a pass
+  int gp;       // columns of a node: Hq / Hkv rounded up to 1, 2, 4 or a multiple of 8
+  int gp_inv;   // 2^16 / gp, rounded up: c / gp = c * gp_inv >> 16 for the columns of a pass (a division took 25 instructions)
+  int groups;   // of eight columns in a pass
+  bool spill;   // keys in the workspace
 };
 
-__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 // Four signed bytes as fp16: 0x6400 + (x + 128) is 1152 + x.
 __device__ __forceinline__ void bytes_to_half(uint32_t w, uint32_t &h01, uint32_t &h23) {
@@ -219,140 +227,159 @@ __device__ __forceinline__ void st_cluster(uint32_t saddr, uint32_t rank, uint32
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
+// Keys are kept in blocks of 32 lanes x 2^lg: a lane's are consecutive pages, four
+// of them side by side, so that it reads its own ones 16 bytes at a time.
+__host__ __device__ __forceinline__ int lane_shift(int pages) { return pages <= 256 ? 3 : 5; }
+__device__ __forceinline__ int key_at(int j, int lg) {
+  const int in = j & ((1 << lg) - 1), lane = (j >> lg) & 31;
+  return (j & ~((32 << lg) - 1)) + (in >> 2) * 128 + lane * 4 + (in & 3);
+}
 
 // The choice for one node by `warps` warps (this one is the w-th) of a named
 // barrier: candidates are the pages with a key above 0.
 struct Choice {
   uint32_t (*box)[kSelectWarps][2];  // two of them, in turn
   int w, warps, bar, turn;
-  // both sums over the warps, and over those before this one
-  __device__ __forceinline__ void sums(int &a, int &b, int &a_before, int &b_before) {
-    a = __reduce_add_sync(kFull, a);
-    b = __reduce_add_sync(kFull, b);
-    a_before = b_before = 0;
-    if (warps == 1) return;
-    if ((threadIdx.x & 31) == 0) box[turn][w][0] = a, box[turn][w][1] = b;
+  // this warp's two numbers to all warps; lane i gets the i-th warp's
+  __device__ __forceinline__ uint2 pass_round(uint32_t a, uint32_t b) {
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) box[turn][w][0] = a, box[turn][w][1] = b;
     named_sync(bar, warps * 32);
-    int x = 0, y = 0;
-    for (int i = 0; i < warps; ++i) {
-      if (i == w) a_before = x, b_before = y;
-      x += box[turn][i][0];
-      y += box[turn][i][1];
-    }
-    a = x;
-    b = y;
+    const uint2 x = lane < warps ? make_uint2(box[turn][lane][0], box[turn][lane][1]) : make_uint2(0, 0);
     turn ^= 1;
+    return x;
   }
 };
+template <int LG>
 __device__ __forceinline__ void choose(const uint32_t *keys, int P, int first, int last, int n_sel, int *sel, Choice &ch) {
+  constexpr int kOwn = 1 << LG, kBlock = 32 * kOwn;  // keys that a lane, a warp holds in registers
   const int lane = threadIdx.x & 31, need = n_sel - first - last;
-  const int chunks = (P + 127) / 128, per = (chunks + ch.warps - 1) / ch.warps;
-  const int c0 = min(ch.w * per, chunks), c1 = min(c0 + per, chunks);
-  auto at = [&](int c) { return *reinterpret_cast<const uint4 *>(keys + c * 128 + lane * 4); };
+  const int blocks = (P + kBlock - 1) / kBlock, per = (blocks + ch.warps - 1) / ch.warps;
+  const int c0 = min(ch.w * per, blocks), c1 = min(c0 + per, blocks);
   for (int i = ch.w * 32 + lane; i < first + last; i += ch.warps * 32) {
     const int x = i < first ? i : n_sel - last + i - first;
     sel[x] = i < first ? i : P - last + i - first;
   }
-  uint32_t cut = 1;
-  int dummy = 0, b0, b1;
-  if (need > 0) {
-    // bits that all candidates have in common need no search
-    uint32_t any = 0, all = ~0u;
-    for (int c = c0; c < c1; ++c) {
-      const uint4 k = at(c);
-      for (const uint32_t x : {k.x, k.y, k.z, k.w})
-        if (x) any |= x, all &= x;
+  if (need == 0) return;
+  uint32_t k[kOwn];
+  auto load = [&](int c) {
+#pragma unroll
+    for (int i = 0; i < kOwn / 4; ++i) {
+      const uint4 x = c < c1 ? *reinterpret_cast<const uint4 *>(keys + (long long)c * kBlock + i * 128 + lane * 4)
+                             : make_uint4(0, 0, 0, 0);
+      k[4 * i] = x.x, k[4 * i + 1] = x.y, k[4 * i + 2] = x.z, k[4 * i + 3] = x.w;
     }
-    any = __reduce_or_sync(kFull, any);
-    all = __reduce_and_sync(kFull, all);
-    if (ch.warps > 1) {
-      if (lane == 0) ch.box[ch.turn][ch.w][0] = any, ch.box[ch.turn][ch.w][1] = all;
-      named_sync(ch.bar, ch.warps * 32);
-      for (int i = 0; i < ch.warps; ++i) any |= ch.box[ch.turn][i][0], all &= ch.box[ch.turn][i][1];
-      ch.turn ^= 1;
-    }
-    const uint32_t differ = any ^ all;
-    int bit = 31 - __clz(differ);  // (-1: all the same)
-    cut = bit < 0 ? all : all & ~((2u << bit) - 1u);
-    for (; bit >= 0; --bit) {
-      const uint32_t next = cut | 1u << bit;
-      int n = 0;
+  };
+  const bool held = c1 - c0 <= 1;
+  // f over all of this warp's keys, a block at a time
+  auto each = [&](auto f) {
+    if (held) {
+      f(c0);
+    } else {
       for (int c = c0; c < c1; ++c) {
-        const uint4 k = at(c);
-        n += (k.x >= next) + (k.y >= next) + (k.z >= next) + (k.w >= next);
+        load(c);
+        f(c);
       }
-      dummy = 0;
-      ch.sums(n, dummy, b0, b1);
-      if (n >= need) cut = next;
-      if (n == need) break;
     }
+  };
+  if (held) load(c0);
+  // bits that all candidates have in common need no search
+  uint32_t any = 0, all = ~0u;
+  each([&](int) {
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+      any |= k[i];
+      all &= k[i] ? k[i] : ~0u;
+    }
+  });
+  any = __reduce_or_sync(kFull, any);
+  all = __reduce_and_sync(kFull, all);
+  if (ch.warps > 1) {
+    const uint2 x = ch.pass_round(any, ~all);
+    any = __reduce_or_sync(kFull, x.x);
+    all = ~__reduce_or_sync(kFull, x.y);
+  }
+  int bit = 31 - __clz(any ^ all);  // (-1: all the same)
+  uint32_t cut = bit < 0 ? all : all & ~((2u << bit) - 1u);
+  for (; bit >= 0; --bit) {
+    const uint32_t next = cut | 1u << bit;
+    uint32_t part[4] = {0, 0, 0, 0};
+    each([&](int) {
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) part[i & 3] += k[i] >= next;
+    });
+    uint32_t n = __reduce_add_sync(kFull, (part[0] + part[1]) + (part[2] + part[3]));
+    if (ch.warps > 1) n = __reduce_add_sync(kFull, ch.pass_round(n, 0).x);
+    if ((int)n >= need) cut = next;
+    if ((int)n == need) break;
   }
   // those above the cut, and of those at it the first ones
-  int above = 0, equal = 0, above_before, equal_before;
-  for (int c = c0; c < c1; ++c) {
-    const uint4 k = at(c);
-    above += (k.x > cut) + (k.y > cut) + (k.z > cut) + (k.w > cut);
-    equal += (k.x == cut) + (k.y == cut) + (k.z == cut) + (k.w == cut);
+  uint32_t above = 0, equal = 0;
+  each([&](int) {
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) above += k[i] > cut, equal += k[i] == cut;
+  });
+  uint32_t before = 0, tied = 0, all_above = __reduce_add_sync(kFull, above);
+  if (ch.warps > 1) {
+    const uint2 x = ch.pass_round(all_above, __reduce_add_sync(kFull, equal));
+    all_above = __reduce_add_sync(kFull, x.x);
+    before = __reduce_add_sync(kFull, lane < ch.w ? x.x : 0);
+    tied = __reduce_add_sync(kFull, lane < ch.w ? x.y : 0);
   }
-  ch.sums(above, equal, above_before, equal_before);
-  if (need <= 0) return;
-  const int ties = need - above;
-  const uint32_t below = (1u << lane) - 1u;
-  int out = first + above_before + min(equal_before, ties), tied = equal_before;
-  for (int c = c0; c < c1; ++c) {
-    const uint4 k4 = at(c);
-    const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
-    uint32_t eq[4], take[4];
-    int eq_mine = tied, eq_all = 0;
+  const int ties = need - (int)all_above;
+  each([&](int c) {
+    if (!held) {
+      above = equal = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      eq[e] = __ballot_sync(kFull, k[e] == cut);
-      eq_mine += __popc(eq[e] & below);
-      eq_all += __popc(eq[e]);
+      for (int i = 0; i < kOwn; ++i) above += k[i] > cut, equal += k[i] == cut;
     }
+    uint32_t a = above, e = equal;  // up to and with this lane
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const bool is = k[e] == cut;
-      take[e] = __ballot_sync(kFull, k[e] > cut || (is && eq_mine < ties));
-      eq_mine += is;
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(kFull, a, o), y = __shfl_up_sync(kFull, e, o);
+      if (lane >= o) a += x, e += y;
     }
-    int to = out;
+    const uint32_t sum_a = __shfl_sync(kFull, a, 31), sum_e = __shfl_sync(kFull, e, 31);
+    int eq = (int)(tied + e - equal), out = first + (int)(before + a - above) + min(eq, ties);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) to += __popc(take[e] & below);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (take[e] >> lane & 1u) sel[to++] = c * 128 + lane * 4 + e;
-      out += __popc(take[e]);
+    for (int i = 0; i < kOwn; ++i) {
+      const bool is = k[i] == cut;
+      if (k[i] > cut || (is && eq < ties)) sel[out++] = c * kBlock + lane * kOwn + i;
+      eq += is;
     }
-    tied += eq_all;
-  }
+    before += sum_a;
+    tied += sum_e;
+  });
 }
 
-template <int D>
-__global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectParams p, const SelectPlan plan) {
+template <int D, bool MANY>
+__global__ void __launch_bounds__(32 * kWarps<MANY>, MANY ? 2 : 4) select_kernel(const SelectParams p, const SelectPlan plan) {
+  constexpr int kThreads = 32 * kWarps<MANY>;
   constexpr int kChunks = D / 32, kSteps = D / 8;  // 64-byte chunks of a page's 2 D codes, steps of 16 of them
   extern __shared__ __align__(16) uint32_t s_dyn[];
   __shared__ uint32_t s_top[kSelectGroups * 8];
   __shared__ uint32_t s_box[kSelectWarps][2][kSelectWarps][2];
-  __shared__ int s_max[kSelectWarps];
-  uint2 *s_q = reinterpret_cast<uint2 *>(s_dyn);  // [group][step][lane]: the product's second operand
-  uint32_t *s_keys = s_dyn + plan.groups * kSteps * 64;  // [slot][page]
+  __shared__ int s_max[kWarps<MANY>];
+  // the product's second operand [group][pair of steps][lane][step], keys
+  uint2 *s_q = reinterpret_cast<uint2 *>(s_dyn);
+  uint32_t *s_keys = reinterpret_cast<uint32_t *>(s_q + plan.groups * kSteps * 32);
   pdl_trigger();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quad = lane & 3;
-  const int cs = plan.cluster, rank = (int)cluster_rank(), h = blockIdx.x / cs, b = blockIdx.y;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quad = lane & 3, r0 = lane >> 2;
+  const int cs = plan.cluster, rank = (int)cluster_rank(), h = blockIdx.x >> plan.shift, b = blockIdx.y;
   const int G = p.Hq / p.Hkv, gp = plan.gp;
   pdl_wait();
   // the sequence, its offsets within their bounds
+  const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), raw = __ldg(p.ctx + b);
   int top = 0;
-  for (int i = threadIdx.x; i <= b; i += kSelectThreads) top = max(top, min(max(__ldg(p.cu + i), 0), p.N));
+  for (int i = threadIdx.x; i <= b; i += kThreads) top = max(top, min(max(__ldg(p.cu + i), 0), p.N));
   top = __reduce_max_sync(kFull, top);
   if (lane == 0) s_max[warp] = top;
   __syncthreads();
   int a0 = 0;
 #pragma unroll
-  for (int w = 0; w < kSelectWarps; ++w) a0 = max(a0, s_max[w]);
-  const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), a1 = max(min(max(c1, 0), p.N), a0);
-  const int n = min(a1 - a0, kAttnMaxNodes), raw = __ldg(p.ctx + b), ctx = min(max(raw, 0), p.table_cols * p.page_size);
+  for (int w = 0; w < kWarps<MANY>; ++w) a0 = max(a0, s_max[w]);
+  const int a1 = max(min(max(c1, 0), p.N), a0);
+  const int n = min(a1 - a0, kAttnMaxNodes), ctx = min(max(raw, 0), p.table_cols * p.page_size);
   if (blockIdx.x == 0 && threadIdx.x == 0 && p.status && (c0 != a0 || c1 != a1 || a1 - a0 > kAttnMaxNodes || raw != ctx))
     atomicOr(p.status, kBadIndex);
   const int P = (ctx + p.page_size - 1) / p.page_size;
@@ -360,190 +387,283 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectP
   if (n == 0) return;
   if (P <= p.n_sel) {  // (the whole cluster)
     for (int node = rank; node < n; node += cs)
-      for (int i = threadIdx.x; i < p.n_sel; i += kSelectThreads) row_of(node)[i] = i < P ? i : -1;
+      for (int i = threadIdx.x; i < p.n_sel; i += kThreads) row_of(node)[i] = i < P ? i : -1;
     return;
   }
   const int *table = p.table + (long long)b * p.ld_table;
   const int8_t *codes = p.index.codes + h * p.index.codes_head;
   const uint8_t *exps = p.index.exps + h;
-  const int tiles = (P + 127) / 128 * 8, stride = cs * kSelectWarps;
+  const int lg = lane_shift(P), tiles = (P + 15) / 16, stride = cs * kWarps<MANY>;
+  // this lane's two pages of a tile
+  auto candidate = [&](int t, int i) {
+    const int j = t * 16 + r0 + 8 * i;
+    return j >= p.first && j < P - p.last;
+  };
+  auto page_ids = [&](int t) {
+    return make_int2(candidate(t, 0) ? __ldg(table + t * 16 + r0) : 0, candidate(t, 1) ? __ldg(table + t * 16 + r0 + 8) : 0);
+  };
+  auto in_index = [&](int id) { return (uint32_t)id < (uint32_t)p.index.pages; };
+  // where the codes of a page begin for this lane (page 0's in place of one outside)
+  auto codes_at = [&](int id) {
+    return reinterpret_cast<const uint4 *>(codes + (in_index(id) ? id : 0) * p.index.codes_page + quad * 16);
+  };
+  auto code_of = [&](int id) { return (int)__ldg(exps + (in_index(id) ? id : 0) * p.index.exps_page); };
   // nodes of a pass: as many as have a slot and columns
-  const int pass = min(plan.slots * cs, plan.groups * 8 / gp);
+  auto node_of = [&](int c) { return c * plan.gp_inv >> 16; };
+  const int pass = min(plan.slots * cs, node_of(plan.groups * 8));
   for (int n0 = 0; n0 < n; n0 += pass) {
     const int nodes = min(pass, n - n0), columns = nodes * gp, groups = (columns + 7) / 8;
-    // q in whole numbers
-    for (int i = threadIdx.x; i < nodes; i += kSelectThreads) s_top[i] = 0;
-    __syncthreads();
-    auto load_q = [&](int c, int &node) {  // four channels of a column
-      node = c / gp;
-      const int g = c - node * gp, head = h * G + (g < G ? g : 0);
-      uint2 x = make_uint2(0, 0);
-      if (lane * 4 < D && node < nodes)
-        x = *reinterpret_cast<const uint2 *>(p.q.ptr + (long long)(a0 + n0 + node) * p.q.tok + head * p.q.head + lane * 4);
-      return x;
+    // (the first pages come while q is made ready)
+    int tile = rank * kWarps<MANY> + warp, code[2] = {0, 0};
+    int2 ids = make_int2(0, 0);
+    uint4 w[2][kChunks];
+    auto load_tile = [&]() {
+      const uint4 *from[2] = {codes_at(ids.x), codes_at(ids.y)};
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) w[i][k] = __ldg(from[i] + k * 4);
+      code[0] = code_of(ids.x);
+      code[1] = code_of(ids.y);
     };
-    for (int c = warp; c < columns; c += kSelectWarps) {
-      int node;
-      const uint2 x = load_q(c, node);
-      uint32_t m = max(max(x.x & 0x7FFFu, x.x >> 16 & 0x7FFFu), max(x.y & 0x7FFFu, x.y >> 16 & 0x7FFFu));
-      m = __reduce_max_sync(kFull, m);
-      if (lane == 0) atomicMax(&s_top[node], m);
+    if (tile < tiles) {
+      ids = page_ids(tile);
+      load_tile();
+    }
+    int2 next_ids = tile + stride < tiles ? page_ids(tile + stride) : make_int2(0, 0);
+    // q in whole numbers
+    for (int i = threadIdx.x; i < kSelectGroups * 8; i += kThreads) s_top[i] = 0;
+    const int mine = (nodes - rank + cs - 1) >> plan.shift;  // nodes that this block chooses for
+    if (!plan.spill) {  // (keys past the last page)
+      const int block = 32 << lg, end = (P + block - 1) / block * block;
+      for (int s = 0; s < mine; ++s)
+        for (int j = tiles * 16 + threadIdx.x; j < end; j += kThreads) s_keys[s * plan.cols + key_at(j, lg)] = 0;
+    } else {
+      const int block = 32 << lg, end = (P + block - 1) / block * block;
+      for (int s = 0; s < mine; ++s)
+        for (int j = tiles * 16 + threadIdx.x; j < end; j += kThreads)
+          reinterpret_cast<uint32_t *>(p.ws)[((long long)(a0 + n0 + s * cs + rank) * p.Hkv + h) * plan.cols + key_at(j, lg)] = 0;
     }
     __syncthreads();
-    for (int c = warp; c < groups * 8; c += kSelectWarps) {
-      int node;
-      const uint2 x = load_q(c, node);
-      const uint32_t m = node < nodes ? s_top[node] : 0;
-      const float down = m < 0x7F80u ? scale_down(exponent_of(__uint_as_float(m << 16))) : 0.0f;
-      const uint32_t w[4] = {x.x << 16, x.x & 0xFFFF0000u, x.y << 16, x.y & 0xFFFF0000u};
-      uint32_t up[2] = {0, 0}, lo[2] = {0, 0};  // fp16 pairs of max(x, 0), min(x, 0)
-      if (m < 0x7F80u) {
-        float v[4];
+    auto load_q = [&](int c) {  // four channels of a column
+      const int node = node_of(c), g = c - node * gp, head = h * G + (g < G ? g : 0);
+      return lane * 4 < D && c < columns
+                 ? __ldg(reinterpret_cast<const uint2 *>(p.q.ptr + (long long)(a0 + n0 + node) * p.q.tok + head * p.q.head +
+                                                         lane * 4))
+                 : make_uint2(0, 0);
+    };
+    constexpr int kAtOnce = 8;  // columns of a warp in flight
+    for (int c = warp; c < columns; c += kWarps<MANY> * kAtOnce) {
+      uint2 x[kAtOnce];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = rintf(__uint_as_float(w[i]) * down);
+      for (int i = 0; i < kAtOnce; ++i) x[i] = load_q(c + i * kWarps<MANY>);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(up[i]) : "f"(fmaxf(v[2 * i + 1], 0.0f)), "f"(fmaxf(v[2 * i], 0.0f)));
-          asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo[i]) : "f"(fminf(v[2 * i + 1], 0.0f)), "f"(fminf(v[2 * i], 0.0f)));
-        }
+      for (int i = 0; i < kAtOnce; ++i) {
+        if (c + i * kWarps<MANY> >= columns) break;
+        uint32_t m = max(max(x[i].x & 0x7FFFu, x[i].x >> 16 & 0x7FFFu), max(x[i].y & 0x7FFFu, x[i].y >> 16 & 0x7FFFu));
+        m = __reduce_max_sync(kFull, m);
+        if (lane == 0) atomicMax(&s_top[node_of(c + i * kWarps<MANY>)], m);
       }
-      if (lane * 4 < D) {
-        auto put = [&](int byte, uint32_t h01, uint32_t h23) {  // code positions byte .. byte + 3
-          const int step = byte / 64 * 4 + byte % 16 / 4, to = (c & 7) * 4 + byte % 64 / 16;
-          s_q[((c >> 3) * kSteps + step) * 32 + to] = make_uint2(h01, h23);
-        };
-        put(lane * 4, up[0], up[1]);
-        put(D + lane * 4, lo[0], lo[1]);
+    }
+    __syncthreads();
+    for (int cc = warp; cc < groups * 8; cc += kWarps<MANY> * kAtOnce) {
+      uint2 xs[kAtOnce];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) xs[i] = load_q(cc + i * kWarps<MANY>);
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int c = cc + i * kWarps<MANY>;
+        if (c >= groups * 8) break;
+        const uint2 x = xs[i];
+        const uint32_t m = c < columns ? s_top[node_of(c)] : 0;
+        const float down = m < 0x7F80u ? scale_down(exponent_of(__uint_as_float(m << 16))) : 0.0f;
+        const uint32_t w[4] = {x.x << 16, x.x & 0xFFFF0000u, x.y << 16, x.y & 0xFFFF0000u};
+        uint32_t up[2] = {0, 0}, lo[2] = {0, 0};  // fp16 pairs of max(x, 0), min(x, 0)
+        if (m < 0x7F80u) {
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = rintf(__uint_as_float(w[e]) * down);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(up[e]) : "f"(fmaxf(v[2 * e + 1], 0.0f)), "f"(fmaxf(v[2 * e], 0.0f)));
+            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo[e]) : "f"(fminf(v[2 * e + 1], 0.0f)), "f"(fminf(v[2 * e], 0.0f)));
+          }
+        }
+        if (lane * 4 < D) {
+          // code positions byte .. byte + 3: word byte % 16 / 4 of what a lane reads of a chunk
+          auto put = [&](int byte, const uint32_t(&v)[2]) {
+            const int step = byte / 64 * 4 + byte % 16 / 4, to = (c & 7) * 4 + byte % 64 / 16;
+            s_q[((c >> 3) * (kSteps / 2) + step / 2) * 64 + to * 2 + step % 2] = make_uint2(v[0], v[1]);
+          };
+          put(lane * 4, up);
+          put(D + lane * 4, lo);
+        }
       }
     }
     __syncthreads();
     // scores
-    auto page_at = [&](int tile, int r) {  // -2: no candidate, -1: outside the index
-      const int j = tile * 16 + r;
-      if (tile >= tiles || j < p.first || j >= P - p.last) return -2;
-      const int pg = __ldg(table + j);
-      return (uint32_t)pg < (uint32_t)p.index.pages ? pg : -1;
-    };
-    const int r0 = lane >> 2;
-    int tile = rank * kSelectWarps + warp;
-    int pg[2] = {page_at(tile, r0), page_at(tile, r0 + 8)};
+    const uint4 *s_b = reinterpret_cast<const uint4 *>(s_q) + lane;  // two steps
     for (; tile < tiles; tile += stride) {
-      uint4 x[2][kChunks];
-      int code[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        code[i] = 0;
-        if (pg[i] >= 0) code[i] = __ldg(exps + pg[i] * p.index.exps_page);
-#pragma unroll
-        for (int k = 0; k < kChunks; ++k)
-          x[i][k] = pg[i] >= 0 ? __ldg(reinterpret_cast<const uint4 *>(codes + pg[i] * p.index.codes_page + k * 64 + quad * 16))
-                               : make_uint4(0, 0, 0, 0);
-      }
-      if (p.status && (pg[0] == -1 || pg[1] == -1)) atomicOr(p.status, kBadIndex);
-      const bool cand[2] = {pg[0] != -2, pg[1] != -2}, in[2] = {pg[0] >= 0, pg[1] >= 0};
-      pg[0] = page_at(tile + stride, r0);
-      pg[1] = page_at(tile + stride, r0 + 8);
-      uint32_t a[kSteps][4];
-#pragma unroll
-      for (int k = 0; k < kChunks; ++k) {
-        const uint32_t w0[4] = {x[0][k].x, x[0][k].y, x[0][k].z, x[0][k].w};
-        const uint32_t w1[4] = {x[1][k].x, x[1][k].y, x[1][k].z, x[1][k].w};
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          bytes_to_half(w0[w], a[k * 4 + w][0], a[k * 4 + w][2]);
-          bytes_to_half(w1[w], a[k * 4 + w][1], a[k * 4 + w][3]);
-        }
-      }
-      // 2^(code - 127 - 20): no score overflows
-      const float up[2] = {__uint_as_float((uint32_t)max(code[0] - 20, 1) << 23),
-                           __uint_as_float((uint32_t)max(code[1] - 20, 1) << 23)};
-      auto put = [&](int node, int i, float s) {
+      const bool cand[2] = {candidate(tile, 0), candidate(tile, 1)}, in[2] = {in_index(ids.x), in_index(ids.y)};
+      const int code_now[2] = {code[0], code[1]};
+      if (p.status && ((cand[0] && !in[0]) || (cand[1] && !in[1]))) atomicOr(p.status, kBadIndex);
+      // a score, as its key, to the block that chooses for the node
+      auto put = [&](int node, int i, float sum) {
         if (node >= nodes) return;
-        const uint32_t key = !cand[i] ? 0u
-                             : !in[i] ? order_key(0.0f)
-                             : code[i] == 255 ? order_key(INFINITY)
-                                              : order_key(s * up[i] + 0.0f);  // (no zero below another one)
-        const int j = tile * 16 + r0 + 8 * i;
+        // 2^(code - 127 - 20): no score overflows; (+ 0: no zero below another one)
+        const float up = __uint_as_float((uint32_t)max(code_now[i] - 20, 1) << 23);
+        const uint32_t key = !cand[i]              ? 0u
+                             : !in[i]              ? order_key(0.0f)
+                             : code_now[i] == 255  ? order_key(INFINITY)
+                                                   : order_key(sum * up + 0.0f);
+        const int j = key_at(tile * 16 + r0 + 8 * i, lg);
         if (plan.spill)
           reinterpret_cast<uint32_t *>(p.ws)[((long long)(a0 + n0 + node) * p.Hkv + h) * plan.cols + j] = key;
         else
-          st_cluster(smem_addr(s_keys + (node / cs) * plan.cols + j), node % cs, key);
+          st_cluster(smem_addr(s_keys + (node >> plan.shift) * plan.cols + j), node & (cs - 1), key);
       };
-      float run[2] = {-INFINITY, -INFINITY};
-      for (int g = 0; g < groups; ++g) {
-        float c[2][4] = {};
+      // the largest of a node's columns, then its score
+      float run[2];
+      int node = 0, in_node = 0;  // of the next group of columns
+      auto finish = [&](const float (&v)[4][4]) {
+        float s[4];
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-          const uint2 q = s_q[(g * kSteps + s) * 32 + lane];
-          mma_f16(c[s & 1], a[s], q.x, q.y);
-        }
-        const float v[4] = {c[0][0] + c[1][0], c[0][1] + c[1][1], c[0][2] + c[1][2], c[0][3] + c[1][3]};
+        for (int i = 0; i < 4; ++i) s[i] = (v[0][i] + v[1][i]) + (v[2][i] + v[3][i]);
         if (gp == 1) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) put(g * 8 + quad * 2 + (i & 1), i >> 1, v[i]);
-          continue;
+          for (int i = 0; i < 4; ++i) put(node + quad * 2 + (i & 1), i >> 1, s[i]);
+          node += 8;
+          return;
         }
+        float m[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float m = fmaxf(v[2 * i], v[2 * i + 1]);
-          if (gp >= 4) m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
-          if (gp >= 8) m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
-          if (gp <= 4) {
-            if (quad % (gp / 2) == 0) put((g * 8 + quad * 2) / gp, i, m);
-          } else {
-            run[i] = fmaxf(run[i], m);
-            if ((g + 1) * 8 % gp == 0) {
-              if (quad == 0) put(g * 8 / gp, i, run[i]);
-              run[i] = -INFINITY;
-            }
+          m[i] = fmaxf(s[2 * i], s[2 * i + 1]);
+          if (gp >= 4) m[i] = fmaxf(m[i], __shfl_xor_sync(kFull, m[i], 1));
+          if (gp >= 8) m[i] = fmaxf(m[i], __shfl_xor_sync(kFull, m[i], 2));
+        }
+        if (gp <= 4) {
+          const bool four = gp == 4;
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (!four || quad % 2 == 0) put(node + (four ? quad / 2 : quad), i, m[i]);
+          node += four ? 2 : 4;
+          return;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) run[i] = in_node == 0 ? m[i] : fmaxf(run[i], m[i]);
+        in_node += 8;
+        if (in_node < gp) return;
+        if (quad == 0) put(node, 0, run[0]);
+        if (quad == 1) put(node, 1, run[1]);
+        in_node = 0;
+        ++node;
+      };
+      const bool more = tile + stride < tiles;
+      if constexpr (!MANY) {
+        // codes converted as they are multiplied, the next tile's in their place
+        const uint4 *from[2] = {codes_at(next_ids.x), codes_at(next_ids.y)};
+        float v[4][4] = {};
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k) {
+          const uint32_t w0[4] = {w[0][k].x, w[0][k].y, w[0][k].z, w[0][k].w};
+          const uint32_t w1[4] = {w[1][k].x, w[1][k].y, w[1][k].z, w[1][k].w};
+          const uint4 q[2] = {s_b[k * 64], s_b[k * 64 + 32]};
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            uint32_t a[4];
+            bytes_to_half(w0[s], a[0], a[2]);
+            bytes_to_half(w1[s], a[1], a[3]);
+            mma_f16(v[s], a[0], a[1], a[2], a[3], s & 1 ? q[s / 2].z : q[s / 2].x, s & 1 ? q[s / 2].w : q[s / 2].y);
+          }
+          if (more) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) w[i][k] = __ldg(from[i] + k * 4);
           }
         }
+        if (more) code[0] = code_of(next_ids.x), code[1] = code_of(next_ids.y);
+        finish(v);
+      } else {
+        // codes converted once for all groups
+        uint32_t a[kSteps][4];
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k) {
+          const uint32_t w0[4] = {w[0][k].x, w[0][k].y, w[0][k].z, w[0][k].w};
+          const uint32_t w1[4] = {w[1][k].x, w[1][k].y, w[1][k].z, w[1][k].w};
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            bytes_to_half(w0[s], a[k * 4 + s][0], a[k * 4 + s][2]);
+            bytes_to_half(w1[s], a[k * 4 + s][1], a[k * 4 + s][3]);
+          }
+        }
+        for (int g = 0; g < groups; ++g) {
+          float v[4][4] = {};
+#pragma unroll
+          for (int s = 0; s < kSteps; s += 2) {
+            const uint4 q = s_b[(g * (kSteps / 2) + s / 2) * 32];
+            mma_f16(v[s & 2], a[s][0], a[s][1], a[s][2], a[s][3], q.x, q.y);
+            mma_f16(v[(s & 2) + 1], a[s + 1][0], a[s + 1][1], a[s + 1][2], a[s + 1][3], q.z, q.w);
+          }
+          finish(v);
+        }
       }
+      ids = next_ids;
+      if (MANY && more) load_tile();
+      if (tile + 2 * stride < tiles) next_ids = page_ids(tile + 2 * stride);
     }
     cluster_sync();
-    // the choice: this block's nodes, some warps each
-    const int mine = (nodes - rank + cs - 1) / cs;
-    int wpn = kSelectWarps;
-    while (wpn > 1 && mine * wpn > kSelectWarps) wpn >>= 1;
+    // The choice: this block's nodes, some warps each -- as few as hold the keys in
+    // registers, since their exchanges cost more than the counting.
+    int wpn = 1;
+    while (wpn < kWarps<MANY> && wpn * (32 << lg) < P) wpn <<= 1;
+    while (wpn > 1 && mine * wpn > kWarps<MANY>) wpn >>= 1;
     const int team = warp / wpn;
     Choice ch = {s_box[team], warp - team * wpn, wpn, 1 + team, 0};
-    for (int slot = team; slot < mine; slot += kSelectWarps / wpn) {
+    for (int slot = team; slot < mine; slot += kWarps<MANY> / wpn) {
       const int node = slot * cs + rank;
       const uint32_t *keys = plan.spill ? reinterpret_cast<const uint32_t *>(p.ws) +
                                               ((long long)(a0 + n0 + node) * p.Hkv + h) * plan.cols
                                         : s_keys + slot * plan.cols;
-      choose(keys, P, p.first, p.last, p.n_sel, row_of(n0 + node), ch);
+      if (lg == 3) choose<3>(keys, P, p.first, p.last, p.n_sel, row_of(n0 + node), ch);
+      else choose<5>(keys, P, p.first, p.last, p.n_sel, row_of(n0 + node), ch);
     }
     if (n0 + pass < n) cluster_sync();  // (before the keys are written again)
   }
+}
+
+int select_cols(int table_cols) {
+  const int block = 32 << lane_shift(table_cols);
+  return (table_cols + block - 1) / block * block;
 }
 
 SelectPlan plan_select(const SelectParams &p, int sm_count) {
   SelectPlan s;
   const int G = p.Hq / p.Hkv;
   s.gp = G <= 2 ? G : G <= 4 ? 4 : (G + 7) / 8 * 8;
-  s.groups = s.gp / 8 > kSelectGroups ? s.gp / 8 : kSelectGroups;
-  s.cols = (p.table_cols + 127) / 128 * 128;
+  // columns for as many nodes as a sequence has on average
+  const long long columns = ((long long)p.N + p.B - 1) / p.B * s.gp;
+  s.gp_inv = (65536 + s.gp - 1) / s.gp;
+  s.groups = columns < kSelectGroups * 8 ? (int)((columns + 7) / 8) : kSelectGroups;
+  if (s.groups < s.gp / 8) s.groups = s.gp / 8;
+  s.cols = select_cols(p.table_cols);
   s.spill = s.cols > kSelectMostKeys;
   // blocks enough for every SM, as far as there are pages for their warps
   s.cluster = 1;
+  s.shift = 0;
   while (s.cluster < kSelectMostCluster && (long long)p.B * p.Hkv * s.cluster < 2LL * sm_count &&
-         s.cluster * 16 * kSelectWarps < s.cols)
-    s.cluster *= 2;
-  s.slots = s.spill || s.cols == 0 ? kSelectWarps : kSelectKeys / s.cols;
-  s.slots = s.slots < 1 ? 1 : s.slots > kSelectWarps ? kSelectWarps : s.slots;
-  // (as many nodes as have columns)
-  const int most = (s.groups * 8 / s.gp + s.cluster - 1) / s.cluster;
-  if (s.slots > most) s.slots = most;
+         s.cluster * 16 * (s.groups > 1 ? kWarps<true> : kWarps<false>) < p.table_cols)
+    s.cluster *= 2, ++s.shift;
+  const int most = (s.groups * 8 / s.gp + s.cluster - 1) / s.cluster;  // as many nodes as have columns
+  s.slots = s.spill || s.cols == 0 ? most : kSelectKeys / s.cols;
+  s.slots = s.slots < 1 ? 1 : s.slots > most ? most : s.slots;
   return s;
 }
 
-template <int D>
-cudaError_t launch_select(const SelectParams &p, int sm_count, cudaStream_t stream) {
-  auto kern = select_kernel<D>;
+template <int D, bool MANY>
+cudaError_t launch_select(const SelectParams &p, const SelectPlan &plan, cudaStream_t stream) {
+  auto kern = select_kernel<D, MANY>;
   constexpr int kMost = 16 * (D / 8) * 256 + kSelectMostKeys * 4;  // 128 heads of a kv head, and the most keys
-  static_assert(kMost <= 220 * 1024, "shared memory");
-  const SelectPlan plan = plan_select(p, sm_count);
+  static_assert(kMost <= 225 * 1024, "shared memory");
   const size_t smem = (size_t)plan.groups * (D / 8) * 256 + (plan.spill ? 0 : (size_t)plan.slots * plan.cols * 4);
   static DeviceOnce once;
   int dev = -1;
@@ -555,7 +675,7 @@ cudaError_t launch_select(const SelectParams &p, int sm_count, cudaStream_t stre
     once.set(dev);
   }
   cudaLaunchConfig_t cfg =
-      pdl_config(dim3((unsigned)(plan.cluster * p.Hkv), (unsigned)p.B), dim3(kSelectThreads), smem, stream);
+      pdl_config(dim3((unsigned)(plan.cluster * p.Hkv), (unsigned)p.B), dim3(32 * kWarps<MANY>), smem, stream);
   cudaLaunchAttribute attr[2];
   attach_pdl(cfg, attr);
   attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
@@ -575,11 +695,14 @@ cudaError_t launch_kv_index(const IndexParams &p, int sm_count, cudaStream_t str
 }
 
 cudaError_t launch_attn_select(const SelectParams &p, int sm_count, cudaStream_t stream) {
-  return p.D == 64 ? launch_select<64>(p, sm_count, stream) : launch_select<128>(p, sm_count, stream);
+  const SelectPlan plan = plan_select(p, sm_count);
+  if (plan.groups > 1)
+    return p.D == 64 ? launch_select<64, true>(p, plan, stream) : launch_select<128, true>(p, plan, stream);
+  return p.D == 64 ? launch_select<64, false>(p, plan, stream) : launch_select<128, false>(p, plan, stream);
 }
 
 size_t attn_select_ws_bytes(long long N, int Hkv, int table_cols) {
-  const long long cols = ((long long)table_cols + 127) / 128 * 128;
+  const long long cols = select_cols(table_cols);
   return cols > kSelectMostKeys ? (size_t)(N * Hkv * cols * 4) : 256;
 }
 
