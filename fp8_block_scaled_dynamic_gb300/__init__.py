@@ -452,6 +452,5 @@ def mxg_query_status(dev_status: torch.Tensor | None, stream=None) -> int:
 # ---------------------------------------------------------------- attention
 from . import attention  # noqa: E402  (it uses the helpers above)
 from .attention import (KVCache, PageIndex, attn_prompt, attn_select, attn_shared,  # noqa: E402,F401
-                        attn_sparse, attn_tree, kv_append, kv_index, mxg_attn_select_workspace_bytes,
-                        mxg_attn_shared_workspace_bytes, mxg_attn_sparse_workspace_bytes,
+                        attn_sparse, attn_tree, kv_append, kv_index, mxg_attn_shared_workspace_bytes, mxg_attn_sparse_workspace_bytes,
                         mxg_attn_tree_workspace_bytes, qk_norm_rope)

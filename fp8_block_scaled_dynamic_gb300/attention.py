@@ -61,9 +61,7 @@ def bind(L: ctypes.CDLL):
     L.attn_shared.restype = i
     L.kv_index.argtypes = [C, i, i, X, vp, i, i, i, vp, vp, vp, vp]
     L.kv_index.restype = i
-    L.mxg_attn_select_workspace_bytes.argtypes = [i, i, i]
-    L.mxg_attn_select_workspace_bytes.restype = sz
-    L.attn_select.argtypes = [H, vp, i, i, X, i, vp, i, i, vp, i, i, i, i, i, i, vp, O, vp]
+    L.attn_select.argtypes = [H, vp, i, i, X, i, vp, i, i, vp, i, i, i, i, i, i, vp, vp, vp]
     L.attn_select.restype = i
     L.mxg_attn_sparse_workspace_bytes.argtypes = [i, i, i, i]
     L.mxg_attn_sparse_workspace_bytes.restype = sz
@@ -225,20 +223,15 @@ def kv_index(cache: KVCache, index: PageIndex, block_table: torch.Tensor, ctx_ol
     return index
 
 
-def mxg_attn_select_workspace_bytes(N: int, Hkv: int, table_cols: int) -> int:
-    """Workspace of attn_select."""
-    return int(lib().mxg_attn_select_workspace_bytes(N, Hkv, table_cols))
-
-
 def attn_select(q: torch.Tensor, cu_nodes: torch.Tensor, index: PageIndex, block_table: torch.Tensor,
-                ctx_len: torch.Tensor, n_sel: int, *, first: int = 1, last: int = 1, out=None, ws=None, dev_status=None,
+                ctx_len: torch.Tensor, n_sel: int, *, first: int = 1, last: int = 1, out=None, dev_status=None,
                 stream=None) -> torch.Tensor:
     """The pages each node's query heads attend to, a kv head each: the first
     `first` and last `last` logical pages of the sequence and those whose bounds
     (one layer: index.layer(i)) promise the largest scores, n_sel in all.
     Returns (N, Hkv, n_sel) int32, ascending, -1 past the last."""
     return (_mod or _load()).attn_select(q, cu_nodes, index.codes, index.exps, index.page_size, block_table, ctx_len,
-                                         n_sel, first, last, out, dev_status, ws, stream)
+                                         n_sel, first, last, out, dev_status, stream)
 
 
 def mxg_attn_sparse_workspace_bytes(N: int, Hkv: int, n_sel: int, D: int) -> int:

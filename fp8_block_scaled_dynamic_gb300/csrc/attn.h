@@ -105,13 +105,13 @@ struct SelectParams {
   PageIndex index;
   const int *cu, *table, *ctx;
   int *sel, *status;
-  float *ws;  // scores
   int B, N, Hq, Hkv, D, page_size, ld_table, table_cols, n_sel, first, last;
 };
 
 constexpr int kAttnMaxSeqs = 4096;
 constexpr int kAttnMaxNodes = 64;
 constexpr int kAttnMaxSelect = 512;
+constexpr int kAttnMaxScored = 1 << 15;  // columns of attn_select's block table (a node's keys in shared memory)
 constexpr int kAttnMaxListed = 1 << 19;  // columns of attn_sparse's block table (a bit each in shared memory)
 
 cudaError_t launch_qk_norm_rope(const RopeParams &p, bool interleaved, int sm_count, cudaStream_t stream);
@@ -125,6 +125,5 @@ cudaError_t launch_attn_sparse(const SparseParams &p, int sm_count, cudaStream_t
 size_t attn_sparse_ws_bytes(long long N, int Hkv, int n_sel, int D, int sm_count);
 cudaError_t launch_kv_index(const IndexParams &p, int sm_count, cudaStream_t stream);
 cudaError_t launch_attn_select(const SelectParams &p, int sm_count, cudaStream_t stream);
-size_t attn_select_ws_bytes(long long N, int Hkv, int table_cols);
 
 }  // namespace mxg

@@ -118,6 +118,7 @@ mxg_status check_index(const mxg_page_index *x) {
       x->codes_head < 0 || x->exps_layer < 0 || x->exps_page < 0)
     return MXG_ERR_INVALID_ARG;
   if (!aligned(x->codes, 16) || !bytes_ok(x->codes_layer) || !bytes_ok(x->codes_page) || !bytes_ok(x->codes_head) ||
+      x->codes_page > INT32_MAX || x->exps_page > INT32_MAX ||
       x->exps_layer >= (1LL << 38) || x->exps_page >= (1LL << 38))
     return MXG_ERR_MISALIGNED;
   return MXG_OK;
@@ -363,22 +364,16 @@ mxg_status kv_index(const mxg_kv_cache *cache, int Hkv, int D, const mxg_page_in
   return e == cudaSuccess ? MXG_OK : MXG_ERR_CUDA;
 }
 
-size_t mxg_attn_select_workspace_bytes(int N, int Hkv, int table_cols) {
-  if (N < 0 || Hkv < 1 || table_cols < 0) return 0;
-  return mxg::attn_select_ws_bytes(N, Hkv, table_cols);
-}
-
 mxg_status attn_select(const mxg_heads *q, const int *cu_nodes, int B, int N, const mxg_page_index *index,
                        int page_size, const int *block_table, int ld_table, int table_cols, const int *ctx_len, int Hq,
-                       int Hkv, int D, int n_sel, int first, int last, int *sel, const mxg_attn_opts *opts,
+                       int Hkv, int D, int n_sel, int first, int last, int *sel, int *dev_status,
                        mxg_stream_t stream) {
   if (!cu_nodes || B < 1 || N < 0 || Hq < 1 || Hkv < 1 || !ctx_len || table_cols < 0 || ld_table < table_cols ||
       (table_cols > 0 && !block_table) || (N > 0 && !sel) || first < 0 || last < 1 || n_sel < 1 || first > n_sel ||
       last > n_sel - first || page_size < 1)
     return MXG_ERR_INVALID_ARG;
-  if (opts && opts->debug_stall != 0) return MXG_ERR_INVALID_ARG;
   if ((D != 64 && D != 128) || Hq % Hkv != 0 || Hq / Hkv > 128 || B > mxg::kAttnMaxSeqs ||
-      n_sel > mxg::kAttnMaxSelect ||
+      n_sel > mxg::kAttnMaxSelect || table_cols > mxg::kAttnMaxScored || (long long)Hkv * 8 > 0x7fffffffLL ||
       (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128 && page_size != 256) ||
       (long long)table_cols * page_size > 0x7fffff00LL || (long long)N * Hkv > 0x7fffffffLL)
     return MXG_ERR_UNSUPPORTED_SHAPE;
@@ -386,11 +381,10 @@ mxg_status attn_select(const mxg_heads *q, const int *cu_nodes, int B, int N, co
   if ((st = check_index(index)) != MXG_OK) return st;
   if (N > 0 && (st = check_heads(q)) != MXG_OK) return st;
   if (!aligned(cu_nodes, 4) || !aligned(block_table, 4) || !aligned(ctx_len, 4) || !aligned(sel, 4) ||
-      (opts && opts->dev_status && !aligned(opts->dev_status, 4)))
+      !aligned(dev_status, 4))
     return MXG_ERR_MISALIGNED;
   int sm = 0;
   if ((st = device_sms(&sm)) != MXG_OK) return st;
-  if ((st = check_ws(opts, mxg::attn_select_ws_bytes(N, Hkv, table_cols))) != MXG_OK) return st;
   if (N == 0) return MXG_OK;
   mxg::SelectParams p = {};
   p.q = heads(q);
@@ -399,8 +393,7 @@ mxg_status attn_select(const mxg_heads *q, const int *cu_nodes, int B, int N, co
   p.table = block_table;
   p.ctx = ctx_len;
   p.sel = sel;
-  p.status = opts->dev_status;
-  p.ws = static_cast<float *>(opts->workspace);
+  p.status = dev_status;
   p.B = B;
   p.N = N;
   p.Hq = Hq;

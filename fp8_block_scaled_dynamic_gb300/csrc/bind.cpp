@@ -382,11 +382,11 @@ PyObject *py_index(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
-// (q, cu_nodes, codes, exps, page_size, block_table, ctx_len, n_sel, first, last, out, dev_status, ws, stream)
+// (q, cu_nodes, codes, exps, page_size, block_table, ctx_len, n_sel, first, last, out, dev_status, stream)
 PyObject *py_select(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded([&]() -> PyObject * {
-    count(n, 14);
-    const Stream stream(a[13]);
+    count(n, 13);
+    const Stream stream(a[12]);
     const at::Tensor &q = heads_of(a[0], "q");
     if (!THPVariable_Check(a[2])) bad("an index holds two tensors");
     const at::Tensor &codes = THPVariable_Unpack(a[2]);
@@ -404,19 +404,11 @@ PyObject *py_select(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                         : at::empty({N, Hkv, (int64_t)n_sel}, q.options().dtype(at::kInt));
     need(sel.size(0) == N && sel.size(1) == Hkv && sel.size(2) == n_sel && sel.is_contiguous(),
          "out must be contiguous (N, Hkv, n_sel)");
-    const at::Tensor ws =
-        given(a[12]) ? tensor(a[12], "ws", at::kByte, 1)
-                     : at::empty({(int64_t)mxg_attn_select_workspace_bytes(as_int(N, "nodes"), as_int(Hkv, "heads"), t.cols)},
-                                 q.options().dtype(at::kByte));
-    mxg_attn_opts o = {};
-    o.workspace = ptr(ws);
-    o.ws_bytes = (size_t)ws.numel();
-    o.dev_status = status_word(a[11]);
     const mxg_heads qh = heads(q);
     check("attn_select", attn_select(&qh, cu, as_int(B, "sequences"), as_int(N, "nodes"), &x, (int)page, t.p, t.ld, t.cols,
                                      static_cast<int *>(ptr(ctx)), as_int(Hq, "heads"), as_int(Hkv, "heads"),
                                      as_int(D, "channels"), (int)n_sel, (int)first, (int)last,
-                                     static_cast<int *>(ptr(sel)), &o, stream.handle()));
+                                     static_cast<int *>(ptr(sel)), status_word(a[11]), stream.handle()));
     return THPVariable_Wrap(sel);
   });
 }

@@ -167,9 +167,8 @@ __global__ void __launch_bounds__(kIndexThreads) index_kernel(const IndexParams 
 // exactly (the 8-bit form of the instruction, without the codes' conversion, is far
 // slower on this part: a batch of 64 x 1024 pages 102 us where this one took 72).  A
 // page's codes are kept in the order in which the product wants them: which 16 of the
-// 2 D positions a step takes does not matter as long as both operands agree.  With one
-// group a tile's registers are filled again for the next tile as they are used; with
-// several (MANY) its codes are converted once.  A score goes, as a 32-bit key of the
+// 2 D positions a step takes does not matter as long as both operands agree.  A tile's
+// registers are filled again for the next one as they are used.  A score goes, as a 32-bit key of the
 // same order, to the shared memory of the block that chooses for its node; there the
 // warps of a node find the key of the last page that is taken, bit by bit from the top,
 // and write the pages out in order.
@@ -178,7 +177,6 @@ template <bool MANY>
 constexpr int kWarps = MANY ? 8 : 4;
 constexpr int kSelectGroups = 8;            // most groups of eight columns (query heads) in a pass, or one node's
 constexpr int kSelectKeys = 12 * 1024;      // most keys of a block in shared memory, where one node's are no more
-constexpr int kSelectMostKeys = 32 * 1024;  // beyond that they are in the workspace
 constexpr int kSelectMostCluster = 8;
 
 struct SelectPlan {
@@ -189,7 +187,6 @@ struct SelectPlan {
   int gp;       // columns of a node: Hq / Hkv rounded up to 1, 2, 4 or a multiple of 8
   int gp_inv;   // 2^16 / gp, rounded up: c / gp = c * gp_inv >> 16 for the columns of a pass (a division took 25 instructions)
   int groups;   // of eight columns in a pass
-  bool spill;   // keys in the workspace
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -198,6 +195,13 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 // Four signed bytes as fp16: 0x6400 + (x + 128) is 1152 + x.
 __device__ __forceinline__ void bytes_to_half(uint32_t w, uint32_t &h01, uint32_t &h23) {
@@ -250,8 +254,10 @@ struct Choice {
     return x;
   }
 };
+// (Out of line, as prepare_q is: inlined, its registers made the score loop spill,
+// a batch of 64 x 1024 pages 50 us instead of 35.)
 template <int LG>
-__device__ __forceinline__ void choose(const uint32_t *keys, int P, int first, int last, int n_sel, int *sel, Choice &ch) {
+__device__ __forceinline__ void choose(const uint32_t *keys, int P, int first, int last, int n_sel, int *sel, Choice ch) {
   constexpr int kOwn = 1 << LG, kBlock = 32 * kOwn;  // keys that a lane, a warp holds in registers
   const int lane = threadIdx.x & 31, need = n_sel - first - last;
   const int blocks = (P + kBlock - 1) / kBlock, per = (blocks + ch.warps - 1) / ch.warps;
@@ -352,12 +358,75 @@ __device__ __forceinline__ void choose(const uint32_t *keys, int P, int first, i
   });
 }
 
+// The product's second operand of a pass: the nodes' q in whole numbers, as fp16
+// pairs of max(x, 0) and of min(x, 0).
+template <int D, int WARPS>
+__device__ __forceinline__ void prepare_q(const uint16_t *q, long long tok, long long head, int nodes, int G, int gp, uint2 *s_q) {
+  constexpr int kSteps = D / 8;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+      // A node's columns are some warps', which all look for its largest value.  (x in
+      // units of 2^e is exact; + 1.5 2^23 rounds it to a whole number, ties to even.)
+      int team = 1;
+      while (team < WARPS && nodes * team * 2 <= WARPS) team <<= 1;
+      const int part = warp & (team - 1);
+      constexpr int kAtOnce = 8;  // columns in flight
+      for (int node = warp / team; node < nodes; node += WARPS / team) {
+        const uint16_t *row = q + node * tok + lane * 4;
+        auto load_q = [&](int g) {  // four channels of a head; the first one's in place of those past the last
+          return lane * 4 < D ? __ldg(reinterpret_cast<const uint2 *>(row + (g < G ? g : 0) * head)) : make_uint2(0, 0);
+        };
+        uint32_t m = 0;
+        uint2 x[kAtOnce];
+        for (int g = 0; g < gp; g += kAtOnce) {
+#pragma unroll
+          for (int i = 0; i < kAtOnce; ++i) x[i] = load_q(g + i);
+#pragma unroll
+          for (int i = 0; i < kAtOnce; ++i)
+            m = max(m, max(max(x[i].x & 0x7FFFu, x[i].x >> 16 & 0x7FFFu), max(x[i].y & 0x7FFFu, x[i].y >> 16 & 0x7FFFu)));
+        }
+        m = __reduce_max_sync(kFull, m);
+        const bool fine = m < 0x7F80u;
+        const float down = fine ? scale_down(exponent_of(__uint_as_float(m << 16))) : 0.0f;
+        for (int g = 0; g < gp; g += kAtOnce) {
+          if (gp > kAtOnce) {
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) x[i] = load_q(g + i);
+          }
+#pragma unroll
+          for (int i = 0; i < kAtOnce; ++i) {
+            if (g + i >= gp || (i & (team - 1)) != part) continue;
+            const int c = node * gp + g + i;
+            uint2 v = fine ? x[i] : make_uint2(0, 0);
+            const uint32_t e[4] = {v.x << 16, v.x & 0xFFFF0000u, v.y << 16, v.y & 0xFFFF0000u};
+            float f[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) f[k] = __fmaf_rn(__uint_as_float(e[k]), down, 12582912.0f) - 12582912.0f;
+            uint32_t w[2], up[2], lo[2];  // fp16 pairs of x, max(x, 0), min(x, 0)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[k]) : "f"(f[2 * k + 1]), "f"(f[2 * k]));
+              asm("max.f16x2 %0, %1, %2;" : "=r"(up[k]) : "r"(w[k]), "r"(0u));
+              asm("min.f16x2 %0, %1, %2;" : "=r"(lo[k]) : "r"(w[k]), "r"(0u));
+            }
+            if (lane * 4 < D) {
+              // code positions byte .. byte + 3: word byte % 16 / 4 of what a lane reads of a chunk
+              auto put = [&](int byte, const uint32_t(&y)[2]) {
+                const int step = byte / 64 * 4 + byte % 16 / 4, to = (c & 7) * 4 + byte % 64 / 16;
+                s_q[((c >> 3) * (kSteps / 2) + step / 2) * 64 + to * 2 + step % 2] = make_uint2(y[0], y[1]);
+              };
+              put(lane * 4, up);
+              put(D + lane * 4, lo);
+            }
+          }
+        }
+      }
+}
+
 template <int D, bool MANY>
 __global__ void __launch_bounds__(32 * kWarps<MANY>, MANY ? 2 : 4) select_kernel(const SelectParams p, const SelectPlan plan) {
   constexpr int kThreads = 32 * kWarps<MANY>;
   constexpr int kChunks = D / 32, kSteps = D / 8;  // 64-byte chunks of a page's 2 D codes, steps of 16 of them
   extern __shared__ __align__(16) uint32_t s_dyn[];
-  __shared__ uint32_t s_top[kSelectGroups * 8];
   __shared__ uint32_t s_box[kSelectWarps][2][kSelectWarps][2];
   __shared__ int s_max[kWarps<MANY>];
   // the product's second operand [group][pair of steps][lane][step], keys
@@ -394,141 +463,95 @@ __global__ void __launch_bounds__(32 * kWarps<MANY>, MANY ? 2 : 4) select_kernel
   const int8_t *codes = p.index.codes + h * p.index.codes_head;
   const uint8_t *exps = p.index.exps + h;
   const int lg = lane_shift(P), tiles = (P + 15) / 16, stride = cs * kWarps<MANY>;
-  // this lane's two pages of a tile
-  auto candidate = [&](int t, int i) {
-    const int j = t * 16 + r0 + 8 * i;
-    return j >= p.first && j < P - p.last;
+  // This lane's two pages of a tile: their numbers (0 in place of one outside the
+  // index), and for each whether it is a candidate (1) in the index (2).
+  const uint32_t codes_page = (uint32_t)p.index.codes_page, exps_page = (uint32_t)p.index.exps_page;
+  struct Pages {
+    uint32_t id[2], kind[2];
   };
-  auto page_ids = [&](int t) {
-    return make_int2(candidate(t, 0) ? __ldg(table + t * 16 + r0) : 0, candidate(t, 1) ? __ldg(table + t * 16 + r0 + 8) : 0);
+  bool outside = false;
+  auto pages_of = [&](int t) {
+    Pages x;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int j = t * 16 + r0 + 8 * i;
+      const bool cand = j >= p.first && j < P - p.last;
+      x.id[i] = cand ? (uint32_t)__ldg(table + j) : 0u;
+      x.kind[i] = cand;
+    }
+    return x;
   };
-  auto in_index = [&](int id) { return (uint32_t)id < (uint32_t)p.index.pages; };
-  // where the codes of a page begin for this lane (page 0's in place of one outside)
-  auto codes_at = [&](int id) {
-    return reinterpret_cast<const uint4 *>(codes + (in_index(id) ? id : 0) * p.index.codes_page + quad * 16);
+  auto within = [&](Pages &x) {  // (once the numbers are there)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const bool in = x.id[i] < (uint32_t)p.index.pages;
+      outside |= !in;
+      x.id[i] = in ? x.id[i] : 0u;
+      x.kind[i] |= in ? 2u : 0u;
+    }
   };
-  auto code_of = [&](int id) { return (int)__ldg(exps + (in_index(id) ? id : 0) * p.index.exps_page); };
+  // where the codes of a page begin for this lane
+  auto codes_at = [&](uint32_t id) {
+    return reinterpret_cast<const uint4 *>(codes + (unsigned long long)id * codes_page + quad * 16);
+  };
+  auto code_of = [&](uint32_t id) { return (int)__ldg(exps + (unsigned long long)id * exps_page); };
   // nodes of a pass: as many as have a slot and columns
   auto node_of = [&](int c) { return c * plan.gp_inv >> 16; };
   const int pass = min(plan.slots * cs, node_of(plan.groups * 8));
   for (int n0 = 0; n0 < n; n0 += pass) {
-    const int nodes = min(pass, n - n0), columns = nodes * gp, groups = (columns + 7) / 8;
-    // (the first pages come while q is made ready)
+    const int nodes = min(pass, n - n0), groups = (nodes * gp + 7) / 8;
+    // (the first pages come into L2 while q is made ready)
     int tile = rank * kWarps<MANY> + warp, code[2] = {0, 0};
-    int2 ids = make_int2(0, 0);
+    Pages now = {}, next = {};
     uint4 w[2][kChunks];
-    auto load_tile = [&]() {
-      const uint4 *from[2] = {codes_at(ids.x), codes_at(ids.y)};
+    auto load_tile = [&](const Pages &x) {
+      const uint4 *from[2] = {codes_at(x.id[0]), codes_at(x.id[1])};
 #pragma unroll
       for (int k = 0; k < kChunks; ++k)
 #pragma unroll
         for (int i = 0; i < 2; ++i) w[i][k] = __ldg(from[i] + k * 4);
-      code[0] = code_of(ids.x);
-      code[1] = code_of(ids.y);
+      code[0] = code_of(x.id[0]);
+      code[1] = code_of(x.id[1]);
     };
     if (tile < tiles) {
-      ids = page_ids(tile);
-      load_tile();
+      now = pages_of(tile);
+      if (tile + stride < tiles) next = pages_of(tile + stride);
+      within(now);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (quad < kChunks / 2 + 1) prefetch_l2(codes_at(now.id[i]) - quad + quad * (kChunks > 2 ? 8 : 4));
     }
-    int2 next_ids = tile + stride < tiles ? page_ids(tile + stride) : make_int2(0, 0);
     // q in whole numbers
-    for (int i = threadIdx.x; i < kSelectGroups * 8; i += kThreads) s_top[i] = 0;
     const int mine = (nodes - rank + cs - 1) >> plan.shift;  // nodes that this block chooses for
-    if (!plan.spill) {  // (keys past the last page)
-      const int block = 32 << lg, end = (P + block - 1) / block * block;
-      for (int s = 0; s < mine; ++s)
-        for (int j = tiles * 16 + threadIdx.x; j < end; j += kThreads) s_keys[s * plan.cols + key_at(j, lg)] = 0;
-    } else {
-      const int block = 32 << lg, end = (P + block - 1) / block * block;
-      for (int s = 0; s < mine; ++s)
-        for (int j = tiles * 16 + threadIdx.x; j < end; j += kThreads)
-          reinterpret_cast<uint32_t *>(p.ws)[((long long)(a0 + n0 + s * cs + rank) * p.Hkv + h) * plan.cols + key_at(j, lg)] = 0;
-    }
-    __syncthreads();
-    auto load_q = [&](int c) {  // four channels of a column
-      const int node = node_of(c), g = c - node * gp, head = h * G + (g < G ? g : 0);
-      return lane * 4 < D && c < columns
-                 ? __ldg(reinterpret_cast<const uint2 *>(p.q.ptr + (long long)(a0 + n0 + node) * p.q.tok + head * p.q.head +
-                                                         lane * 4))
-                 : make_uint2(0, 0);
-    };
-    constexpr int kAtOnce = 8;  // columns of a warp in flight
-    for (int c = warp; c < columns; c += kWarps<MANY> * kAtOnce) {
-      uint2 x[kAtOnce];
-#pragma unroll
-      for (int i = 0; i < kAtOnce; ++i) x[i] = load_q(c + i * kWarps<MANY>);
-#pragma unroll
-      for (int i = 0; i < kAtOnce; ++i) {
-        if (c + i * kWarps<MANY> >= columns) break;
-        uint32_t m = max(max(x[i].x & 0x7FFFu, x[i].x >> 16 & 0x7FFFu), max(x[i].y & 0x7FFFu, x[i].y >> 16 & 0x7FFFu));
-        m = __reduce_max_sync(kFull, m);
-        if (lane == 0) atomicMax(&s_top[node_of(c + i * kWarps<MANY>)], m);
-      }
-    }
-    __syncthreads();
-    for (int cc = warp; cc < groups * 8; cc += kWarps<MANY> * kAtOnce) {
-      uint2 xs[kAtOnce];
-#pragma unroll
-      for (int i = 0; i < kAtOnce; ++i) xs[i] = load_q(cc + i * kWarps<MANY>);
-#pragma unroll
-      for (int i = 0; i < kAtOnce; ++i) {
-        const int c = cc + i * kWarps<MANY>;
-        if (c >= groups * 8) break;
-        const uint2 x = xs[i];
-        const uint32_t m = c < columns ? s_top[node_of(c)] : 0;
-        const float down = m < 0x7F80u ? scale_down(exponent_of(__uint_as_float(m << 16))) : 0.0f;
-        const uint32_t w[4] = {x.x << 16, x.x & 0xFFFF0000u, x.y << 16, x.y & 0xFFFF0000u};
-        uint32_t up[2] = {0, 0}, lo[2] = {0, 0};  // fp16 pairs of max(x, 0), min(x, 0)
-        if (m < 0x7F80u) {
-          float v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = rintf(__uint_as_float(w[e]) * down);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(up[e]) : "f"(fmaxf(v[2 * e + 1], 0.0f)), "f"(fmaxf(v[2 * e], 0.0f)));
-            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo[e]) : "f"(fminf(v[2 * e + 1], 0.0f)), "f"(fminf(v[2 * e], 0.0f)));
-          }
-        }
-        if (lane * 4 < D) {
-          // code positions byte .. byte + 3: word byte % 16 / 4 of what a lane reads of a chunk
-          auto put = [&](int byte, const uint32_t(&v)[2]) {
-            const int step = byte / 64 * 4 + byte % 16 / 4, to = (c & 7) * 4 + byte % 64 / 16;
-            s_q[((c >> 3) * (kSteps / 2) + step / 2) * 64 + to * 2 + step % 2] = make_uint2(v[0], v[1]);
-          };
-          put(lane * 4, up);
-          put(D + lane * 4, lo);
-        }
-      }
-    }
+    const int block = 32 << lg, end = (P + block - 1) / block * block;
+    for (int i = 0; i < mine; ++i)  // (keys past the last page)
+      for (int j = tiles * 16 + threadIdx.x; j < end; j += kThreads) s_keys[i * plan.cols + key_at(j, lg)] = 0;
+    prepare_q<D, kWarps<MANY>>(p.q.ptr + (long long)(a0 + n0) * p.q.tok + (long long)(h * G) * p.q.head, p.q.tok, p.q.head,
+                               nodes, G, gp, s_q);
     __syncthreads();
     // scores
+    if (tile < tiles) load_tile(now);
     const uint4 *s_b = reinterpret_cast<const uint4 *>(s_q) + lane;  // two steps
     for (; tile < tiles; tile += stride) {
-      const bool cand[2] = {candidate(tile, 0), candidate(tile, 1)}, in[2] = {in_index(ids.x), in_index(ids.y)};
       const int code_now[2] = {code[0], code[1]};
-      if (p.status && ((cand[0] && !in[0]) || (cand[1] && !in[1]))) atomicOr(p.status, kBadIndex);
+      const uint32_t kind_now[2] = {now.kind[0], now.kind[1]};
       // a score, as its key, to the block that chooses for the node
-      auto put = [&](int node, int i, float sum) {
+      const uint32_t at = key_at(tile * 16 + r0, lg), at8 = lg == 3 ? 4 : 256;  // (eight pages on)
+      auto put = [&](int node, bool second, float sum) {
         if (node >= nodes) return;
+        const int code = second ? code_now[1] : code_now[0];
+        const uint32_t kind = second ? kind_now[1] : kind_now[0], j = at + (second ? at8 : 0u);
         // 2^(code - 127 - 20): no score overflows; (+ 0: no zero below another one)
-        const float up = __uint_as_float((uint32_t)max(code_now[i] - 20, 1) << 23);
-        const uint32_t key = !cand[i]              ? 0u
-                             : !in[i]              ? order_key(0.0f)
-                             : code_now[i] == 255  ? order_key(INFINITY)
-                                                   : order_key(sum * up + 0.0f);
-        const int j = key_at(tile * 16 + r0 + 8 * i, lg);
-        if (plan.spill)
-          reinterpret_cast<uint32_t *>(p.ws)[((long long)(a0 + n0 + node) * p.Hkv + h) * plan.cols + j] = key;
-        else
-          st_cluster(smem_addr(s_keys + (node >> plan.shift) * plan.cols + j), node & (cs - 1), key);
+        float score = fmaf(sum, __uint_as_float((uint32_t)max(code - 20, 1) << 23), 0.0f);
+        if (code == 255) score = INFINITY;
+        if (kind < 2) score = 0.0f;
+        const uint32_t key = kind & 1 ? order_key(score) : 0u;
+        st_cluster(smem_addr(s_keys + (node >> plan.shift) * plan.cols + j), node & (cs - 1), key);
       };
       // the largest of a node's columns, then its score
       float run[2];
       int node = 0, in_node = 0;  // of the next group of columns
-      auto finish = [&](const float (&v)[4][4]) {
-        float s[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] = (v[0][i] + v[1][i]) + (v[2][i] + v[3][i]);
+      auto finish = [&](const float (&s)[4]) {
         if (gp == 1) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) put(node + quad * 2 + (i & 1), i >> 1, s[i]);
@@ -542,28 +565,36 @@ __global__ void __launch_bounds__(32 * kWarps<MANY>, MANY ? 2 : 4) select_kernel
           if (gp >= 4) m[i] = fmaxf(m[i], __shfl_xor_sync(kFull, m[i], 1));
           if (gp >= 8) m[i] = fmaxf(m[i], __shfl_xor_sync(kFull, m[i], 2));
         }
-        if (gp <= 4) {
-          const bool four = gp == 4;
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (!four || quad % 2 == 0) put(node + (four ? quad / 2 : quad), i, m[i]);
-          node += four ? 2 : 4;
+        if (gp == 2) {
+          put(node + quad, false, m[0]);
+          put(node + quad, true, m[1]);
+          node += 4;
           return;
         }
+        // (a quad's lanes hold the same: one writes the first page's, one the second's)
+        if (gp == 4) {
+          put(node + (quad >> 1), quad & 1, quad & 1 ? m[1] : m[0]);
+          node += 2;
+          return;
+        }
+        if (MANY) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) run[i] = in_node == 0 ? m[i] : fmaxf(run[i], m[i]);
-        in_node += 8;
-        if (in_node < gp) return;
-        if (quad == 0) put(node, 0, run[0]);
-        if (quad == 1) put(node, 1, run[1]);
-        in_node = 0;
+          for (int i = 0; i < 2; ++i) run[i] = in_node == 0 ? m[i] : fmaxf(run[i], m[i]);
+          in_node += 8;
+          if (in_node < gp) return;
+          in_node = 0;
+          m[0] = run[0], m[1] = run[1];
+        }
+        if (quad < 2) put(node, quad, quad ? m[1] : m[0]);
         ++node;
       };
       const bool more = tile + stride < tiles;
+      within(next);
+      const uint4 *from[2] = {codes_at(next.id[0]), codes_at(next.id[1])};
+      // codes converted as they are multiplied, the next tile's in their place: with
+      // one group of columns in four sums, else for up to eight groups at once
       if constexpr (!MANY) {
-        // codes converted as they are multiplied, the next tile's in their place
-        const uint4 *from[2] = {codes_at(next_ids.x), codes_at(next_ids.y)};
-        float v[4][4] = {};
+        float v[4][4];
 #pragma unroll
         for (int k = 0; k < kChunks; ++k) {
           const uint32_t w0[4] = {w[0][k].x, w[0][k].y, w[0][k].z, w[0][k].w};
@@ -574,56 +605,72 @@ __global__ void __launch_bounds__(32 * kWarps<MANY>, MANY ? 2 : 4) select_kernel
             uint32_t a[4];
             bytes_to_half(w0[s], a[0], a[2]);
             bytes_to_half(w1[s], a[1], a[3]);
-            mma_f16(v[s], a[0], a[1], a[2], a[3], s & 1 ? q[s / 2].z : q[s / 2].x, s & 1 ? q[s / 2].w : q[s / 2].y);
+            const uint32_t b0 = s & 1 ? q[s / 2].z : q[s / 2].x, b1 = s & 1 ? q[s / 2].w : q[s / 2].y;
+            if (k == 0) mma_f16_first(v[s], a[0], a[1], a[2], a[3], b0, b1);
+            else mma_f16(v[s], a[0], a[1], a[2], a[3], b0, b1);
           }
           if (more) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) w[i][k] = __ldg(from[i] + k * 4);
           }
         }
-        if (more) code[0] = code_of(next_ids.x), code[1] = code_of(next_ids.y);
-        finish(v);
+        float sum[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[i] = (v[0][i] + v[1][i]) + (v[2][i] + v[3][i]);
+        finish(sum);
       } else {
-        // codes converted once for all groups
-        uint32_t a[kSteps][4];
+        for (int g0 = 0; g0 < groups; g0 += kSelectGroups) {
+          float v[kSelectGroups][4];
 #pragma unroll
-        for (int k = 0; k < kChunks; ++k) {
-          const uint32_t w0[4] = {w[0][k].x, w[0][k].y, w[0][k].z, w[0][k].w};
-          const uint32_t w1[4] = {w[1][k].x, w[1][k].y, w[1][k].z, w[1][k].w};
+          for (int k = 0; k < kChunks; ++k) {
+            const uint32_t w0[4] = {w[0][k].x, w[0][k].y, w[0][k].z, w[0][k].w};
+            const uint32_t w1[4] = {w[1][k].x, w[1][k].y, w[1][k].z, w[1][k].w};
+            uint32_t a[4][4];
 #pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            bytes_to_half(w0[s], a[k * 4 + s][0], a[k * 4 + s][2]);
-            bytes_to_half(w1[s], a[k * 4 + s][1], a[k * 4 + s][3]);
+            for (int s = 0; s < 4; ++s) {
+              bytes_to_half(w0[s], a[s][0], a[s][2]);
+              bytes_to_half(w1[s], a[s][1], a[s][3]);
+            }
+            if (more && g0 + kSelectGroups >= groups) {
+#pragma unroll
+              for (int i = 0; i < 2; ++i) w[i][k] = __ldg(from[i] + k * 4);
+            }
+#pragma unroll
+            for (int g = 0; g < kSelectGroups; ++g) {
+              if (g0 + g >= groups) break;
+#pragma unroll
+              for (int s = 0; s < 4; s += 2) {
+                const uint4 q = s_b[((g0 + g) * (kSteps / 2) + k * 2 + s / 2) * 32];
+                if (k == 0 && s == 0) mma_f16_first(v[g], a[s][0], a[s][1], a[s][2], a[s][3], q.x, q.y);
+                else mma_f16(v[g], a[s][0], a[s][1], a[s][2], a[s][3], q.x, q.y);
+                mma_f16(v[g], a[s + 1][0], a[s + 1][1], a[s + 1][2], a[s + 1][3], q.z, q.w);
+              }
+            }
+            asm volatile("" ::: "memory");  // (one chunk's operands at a time in registers)
           }
-        }
-        for (int g = 0; g < groups; ++g) {
-          float v[4][4] = {};
 #pragma unroll
-          for (int s = 0; s < kSteps; s += 2) {
-            const uint4 q = s_b[(g * (kSteps / 2) + s / 2) * 32];
-            mma_f16(v[s & 2], a[s][0], a[s][1], a[s][2], a[s][3], q.x, q.y);
-            mma_f16(v[(s & 2) + 1], a[s + 1][0], a[s + 1][1], a[s + 1][2], a[s + 1][3], q.z, q.w);
+          for (int g = 0; g < kSelectGroups; ++g) {
+            if (g0 + g >= groups) break;
+            finish(v[g]);
           }
-          finish(v);
         }
       }
-      ids = next_ids;
-      if (MANY && more) load_tile();
-      if (tile + 2 * stride < tiles) next_ids = page_ids(tile + 2 * stride);
+      if (more) code[0] = code_of(next.id[0]), code[1] = code_of(next.id[1]);
+      now = next;
+      if (tile + 2 * stride < tiles) next = pages_of(tile + 2 * stride);
     }
+    if (outside && p.status) atomicOr(p.status, kBadIndex);
     cluster_sync();
     // The choice: this block's nodes, some warps each -- as few as hold the keys in
     // registers, since their exchanges cost more than the counting.
     int wpn = 1;
     while (wpn < kWarps<MANY> && wpn * (32 << lg) < P) wpn <<= 1;
     while (wpn > 1 && mine * wpn > kWarps<MANY>) wpn >>= 1;
-    const int team = warp / wpn;
-    Choice ch = {s_box[team], warp - team * wpn, wpn, 1 + team, 0};
-    for (int slot = team; slot < mine; slot += kWarps<MANY> / wpn) {
+    const int crew = warp / wpn;
+    Choice ch = {s_box[crew], warp - crew * wpn, wpn, 1 + crew, 0};
+    for (int slot = crew; slot < mine; slot += kWarps<MANY> / wpn) {
       const int node = slot * cs + rank;
-      const uint32_t *keys = plan.spill ? reinterpret_cast<const uint32_t *>(p.ws) +
-                                              ((long long)(a0 + n0 + node) * p.Hkv + h) * plan.cols
-                                        : s_keys + slot * plan.cols;
+      const uint32_t *keys = s_keys + slot * plan.cols;
       if (lg == 3) choose<3>(keys, P, p.first, p.last, p.n_sel, row_of(n0 + node), ch);
       else choose<5>(keys, P, p.first, p.last, p.n_sel, row_of(n0 + node), ch);
     }
@@ -646,7 +693,6 @@ SelectPlan plan_select(const SelectParams &p, int sm_count) {
   s.groups = columns < kSelectGroups * 8 ? (int)((columns + 7) / 8) : kSelectGroups;
   if (s.groups < s.gp / 8) s.groups = s.gp / 8;
   s.cols = select_cols(p.table_cols);
-  s.spill = s.cols > kSelectMostKeys;
   // blocks enough for every SM, as far as there are pages for their warps
   s.cluster = 1;
   s.shift = 0;
@@ -654,7 +700,7 @@ SelectPlan plan_select(const SelectParams &p, int sm_count) {
          s.cluster * 16 * (s.groups > 1 ? kWarps<true> : kWarps<false>) < p.table_cols)
     s.cluster *= 2, ++s.shift;
   const int most = (s.groups * 8 / s.gp + s.cluster - 1) / s.cluster;  // as many nodes as have columns
-  s.slots = s.spill || s.cols == 0 ? most : kSelectKeys / s.cols;
+  s.slots = s.cols == 0 ? most : kSelectKeys / s.cols;
   s.slots = s.slots < 1 ? 1 : s.slots > most ? most : s.slots;
   return s;
 }
@@ -662,9 +708,9 @@ SelectPlan plan_select(const SelectParams &p, int sm_count) {
 template <int D, bool MANY>
 cudaError_t launch_select(const SelectParams &p, const SelectPlan &plan, cudaStream_t stream) {
   auto kern = select_kernel<D, MANY>;
-  constexpr int kMost = 16 * (D / 8) * 256 + kSelectMostKeys * 4;  // 128 heads of a kv head, and the most keys
+  constexpr int kMost = 16 * (D / 8) * 256 + kAttnMaxScored * 4;  // 128 heads of a kv head, and the most keys
   static_assert(kMost <= 225 * 1024, "shared memory");
-  const size_t smem = (size_t)plan.groups * (D / 8) * 256 + (plan.spill ? 0 : (size_t)plan.slots * plan.cols * 4);
+  const size_t smem = (size_t)plan.groups * (D / 8) * 256 + (size_t)plan.slots * plan.cols * 4;
   static DeviceOnce once;
   int dev = -1;
   cudaError_t e = cudaGetDevice(&dev);
@@ -699,11 +745,6 @@ cudaError_t launch_attn_select(const SelectParams &p, int sm_count, cudaStream_t
   if (plan.groups > 1)
     return p.D == 64 ? launch_select<64, true>(p, plan, stream) : launch_select<128, true>(p, plan, stream);
   return p.D == 64 ? launch_select<64, false>(p, plan, stream) : launch_select<128, false>(p, plan, stream);
-}
-
-size_t attn_select_ws_bytes(long long N, int Hkv, int table_cols) {
-  const long long cols = select_cols(table_cols);
-  return cols > kSelectMostKeys ? (size_t)(N * Hkv * cols * 4) : 256;
 }
 
 }  // namespace mxg

@@ -74,7 +74,7 @@ typedef struct {
 /* Bounds of the keys of a paged cache's full pages, by physical page: of (layer
  * l, page p, head h) two rows of D codes -- the upper bounds, then the lower --
  * at codes + l * codes_layer + p * codes_page + h * codes_head (strides in
- * bytes, multiples of 16) and the power of two that they count, as an E8M0 code,
+ * bytes, multiples of 16; those of pages below 2^31) and the power of two that they count, as an E8M0 code,
  * at exps + l * exps_layer + p * exps_page + h. */
 typedef struct {
     int8_t *codes;
@@ -84,7 +84,7 @@ typedef struct {
 } mxg_page_index;
 
 typedef struct {
-    void *workspace;     /* attn_tree, attn_shared, attn_select, attn_sparse: device scratch of >=
+    void *workspace;     /* attn_tree, attn_shared, attn_sparse: device scratch of >=
                             mxg_<name>_workspace_bytes(), 256-byte aligned; its contents on
                             entry do not matter.  Calls that overlap on the GPU need separate
                             workspaces. */
@@ -239,14 +239,14 @@ mxg_status kv_index(const mxg_kv_cache *cache, int Hkv, int D, const mxg_page_in
  * nodes past cu_nodes[B] are not written.  The last page, which may not be full, is
  * always selected and needs no bounds: 1 <= last, 0 <= first, first + last <= n_sel
  * <= MXG_ATTN_MAX_SELECT.
- * D in {64, 128}, Hq % Hkv == 0, Hq / Hkv <= 128, B <= MXG_ATTN_MAX_SEQS.
+ * D in {64, 128}, Hq % Hkv == 0, Hq / Hkv <= 128, B <= MXG_ATTN_MAX_SEQS,
+ * table_cols <= 32768.
  * Out of range: offsets, nodes and ctx_len are clamped as for attn_tree; a page
  * whose number is outside [0, index->pages) has the score zero. */
-size_t mxg_attn_select_workspace_bytes(int N, int Hkv, int table_cols);
 mxg_status attn_select(const mxg_heads *q, const int *cu_nodes, int B, int N,
                        const mxg_page_index *index, int page_size, const int *block_table,
                        int ld_table, int table_cols, const int *ctx_len, int Hq, int Hkv, int D,
-                       int n_sel, int first, int last, int *sel, const mxg_attn_opts *opts,
+                       int n_sel, int first, int last, int *sel, int *dev_status,
                        mxg_stream_t stream);
 
 /* attn_tree where node i and the query heads of kv head h see, of the sequence's

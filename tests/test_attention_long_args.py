@@ -44,7 +44,7 @@ def test_sparse_refusals(kw, want):
 
 
 SELECT = dict(q=H(), cu=P, B=2, N=10, index=X(), page=64, table=P, ld=8, cols=8, ctx=P, Hq=8, Hkv=2, D=128, n_sel=4, first=1, last=1,
-              sel=P, opts=AttnOpts(P, 1 << 40), stream=None)
+              sel=P, status=None, stream=None)
 
 
 @pytest.mark.parametrize("kw,want", [
@@ -52,10 +52,11 @@ SELECT = dict(q=H(), cu=P, B=2, N=10, index=X(), page=64, table=P, ld=8, cols=8,
     (dict(cols=9), 1), (dict(n_sel=0), 1), (dict(first=-1), 1), (dict(last=0), 1), (dict(first=4), 1), (dict(last=4), 1), (dict(last=2147483647), 1),
     (dict(page=0), 1), (dict(page=24), 2), (dict(n_sel=513), 2), (dict(D=96), 2), (dict(Hkv=3), 2), (dict(Hq=258), 2), (dict(B=4097), 2),
     (dict(q=None), 1), (dict(q=H(tok=4)), 3), (dict(sel=P + 2), 3), (dict(cu=P + 2), 3), (dict(ctx=P + 1), 3),
-    (dict(opts=AttnOpts(P, 1 << 40, debug_stall=1)), 1), (dict(opts=AttnOpts(P, 1 << 40, P + 1)), 3),
+    (dict(status=P + 1), 3), (dict(cols=32769, ld=32769), 2),
     (dict(index=X(codes=None)), 1), (dict(index=X(exps=None)), 1), (dict(index=X(pages=0)), 1), (dict(index=X(layers=0)), 1),
     (dict(index=X(codes=P + 8)), 3), (dict(index=X(codes_page=8)), 3), (dict(index=X(codes_head=-16)), 1), (dict(index=X(exps_page=-1)), 1),
-    (dict(index=X(codes_head=1 << 39)), 3), (dict(cols=1 << 27, ld=1 << 27), 2),
+    (dict(index=X(codes_head=1 << 39)), 3), (dict(index=X(codes_page=1 << 31)), 3), (dict(index=X(exps_page=1 << 31)), 3),
+    (dict(cols=1 << 27, ld=1 << 27), 2),
 ])
 def test_select_refusals(kw, want):
     assert mx.lib().attn_select(*{**SELECT, **kw}.values()) == want
@@ -76,7 +77,5 @@ def test_index_refusals(kw, want):
 
 def test_workspace_sizes_of_nothing():
     L = mx.lib()
-    assert L.mxg_attn_select_workspace_bytes(-1, 1, 4) == 0 and L.mxg_attn_select_workspace_bytes(1, 0, 4) == 0
-    assert L.mxg_attn_select_workspace_bytes(3, 2, 0) > 0
     assert L.mxg_attn_shared_workspace_bytes(4, 8, 96) == 0 and L.mxg_attn_shared_workspace_bytes(-1, 8, 128) == 0
     assert L.mxg_attn_sparse_workspace_bytes(4, 2, 0, 128) == 0 and L.mxg_attn_sparse_workspace_bytes(4, 2, 4, 32) == 0
