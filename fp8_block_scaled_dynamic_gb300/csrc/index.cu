@@ -233,7 +233,7 @@ __device__ __forceinline__ void named_sync(int id, int threads) {
 }
 // Keys are kept in blocks of 32 lanes x 2^lg: a lane's are consecutive pages, four
 // of them side by side, so that it reads its own ones 16 bytes at a time.
-__host__ __device__ __forceinline__ int lane_shift(int pages) { return pages <= 256 ? 3 : 5; }
+__host__ __device__ __forceinline__ int lane_shift(int pages) { return pages <= 256 ? 3 : 4; }
 __device__ __forceinline__ int key_at(int j, int lg) {
   const int in = j & ((1 << lg) - 1), lane = (j >> lg) & 31;
   return (j & ~((32 << lg) - 1)) + (in >> 2) * 128 + lane * 4 + (in & 3);
@@ -369,7 +369,7 @@ __device__ __forceinline__ void prepare_q(const uint16_t *q, long long tok, long
       int team = 1;
       while (team < WARPS && nodes * team * 2 <= WARPS) team <<= 1;
       const int part = warp & (team - 1);
-      constexpr int kAtOnce = 8;  // columns in flight
+      constexpr int kAtOnce = WARPS == 8 ? 8 : 4;  // columns in flight (8 of them made the one-group kernel spill)
       for (int node = warp / team; node < nodes; node += WARPS / team) {
         const uint16_t *row = q + node * tok + lane * 4;
         auto load_q = [&](int g) {  // four channels of a head; the first one's in place of those past the last
@@ -423,7 +423,7 @@ __device__ __forceinline__ void prepare_q(const uint16_t *q, long long tok, long
 }
 
 template <int D, bool MANY>
-__global__ void __launch_bounds__(32 * kWarps<MANY>, MANY ? 2 : 4) select_kernel(const SelectParams p, const SelectPlan plan) {
+__global__ void __launch_bounds__(32 * kWarps<MANY>, MANY ? 1 : 4) select_kernel(const SelectParams p, const SelectPlan plan) {
   constexpr int kThreads = 32 * kWarps<MANY>;
   constexpr int kChunks = D / 32, kSteps = D / 8;  // 64-byte chunks of a page's 2 D codes, steps of 16 of them
   extern __shared__ __align__(16) uint32_t s_dyn[];
@@ -459,67 +459,21 @@ __global__ void __launch_bounds__(32 * kWarps<MANY>, MANY ? 2 : 4) select_kernel
       for (int i = threadIdx.x; i < p.n_sel; i += kThreads) row_of(node)[i] = i < P ? i : -1;
     return;
   }
-  const int *table = p.table + (long long)b * p.ld_table;
-  const int8_t *codes = p.index.codes + h * p.index.codes_head;
-  const uint8_t *exps = p.index.exps + h;
   const int lg = lane_shift(P), tiles = (P + 15) / 16, stride = cs * kWarps<MANY>;
-  // This lane's two pages of a tile: their numbers (0 in place of one outside the
-  // index), and for each whether it is a candidate (1) in the index (2).
-  const uint32_t codes_page = (uint32_t)p.index.codes_page, exps_page = (uint32_t)p.index.exps_page;
-  struct Pages {
-    uint32_t id[2], kind[2];
-  };
-  bool outside = false;
-  auto pages_of = [&](int t) {
-    Pages x;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int j = t * 16 + r0 + 8 * i;
-      const bool cand = j >= p.first && j < P - p.last;
-      x.id[i] = cand ? (uint32_t)__ldg(table + j) : 0u;
-      x.kind[i] = cand;
-    }
-    return x;
-  };
-  auto within = [&](Pages &x) {  // (once the numbers are there)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const bool in = x.id[i] < (uint32_t)p.index.pages;
-      outside |= !in;
-      x.id[i] = in ? x.id[i] : 0u;
-      x.kind[i] |= in ? 2u : 0u;
-    }
-  };
-  // where the codes of a page begin for this lane
-  auto codes_at = [&](uint32_t id) {
-    return reinterpret_cast<const uint4 *>(codes + (unsigned long long)id * codes_page + quad * 16);
-  };
-  auto code_of = [&](uint32_t id) { return (int)__ldg(exps + (unsigned long long)id * exps_page); };
   // nodes of a pass: as many as have a slot and columns
   auto node_of = [&](int c) { return c * plan.gp_inv >> 16; };
   const int pass = min(plan.slots * cs, node_of(plan.groups * 8));
   for (int n0 = 0; n0 < n; n0 += pass) {
     const int nodes = min(pass, n - n0), groups = (nodes * gp + 7) / 8;
-    // (the first pages come into L2 while q is made ready)
-    int tile = rank * kWarps<MANY> + warp, code[2] = {0, 0};
-    Pages now = {}, next = {};
-    uint4 w[2][kChunks];
-    auto load_tile = [&](const Pages &x) {
-      const uint4 *from[2] = {codes_at(x.id[0]), codes_at(x.id[1])};
-#pragma unroll
-      for (int k = 0; k < kChunks; ++k)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) w[i][k] = __ldg(from[i] + k * 4);
-      code[0] = code_of(x.id[0]);
-      code[1] = code_of(x.id[1]);
-    };
-    if (tile < tiles) {
-      now = pages_of(tile);
-      if (tile + stride < tiles) next = pages_of(tile + stride);
-      within(now);
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (quad < kChunks / 2 + 1) prefetch_l2(codes_at(now.id[i]) - quad + quad * (kChunks > 2 ? 8 : 4));
+    int tile = rank * kWarps<MANY> + warp;
+    if (tile < tiles) {  // the first pages come into L2 while q is made ready
+      constexpr int kLines = 2 * D / 128;
+      const int j = tile * 16 + lane / 2, line = lane % 2;
+      if (j >= p.first && j < P - p.last && line < kLines) {
+        const uint32_t id = (uint32_t)__ldg(p.table + (long long)b * p.ld_table + j);
+        if (id < (uint32_t)p.index.pages)
+          prefetch_l2(p.index.codes + h * p.index.codes_head + id * p.index.codes_page + line * 128);
+      }
     }
     // q in whole numbers
     const int mine = (nodes - rank + cs - 1) >> plan.shift;  // nodes that this block chooses for
@@ -530,7 +484,60 @@ __global__ void __launch_bounds__(32 * kWarps<MANY>, MANY ? 2 : 4) select_kernel
                                nodes, G, gp, s_q);
     __syncthreads();
     // scores
-    if (tile < tiles) load_tile(now);
+    // (what follows is worked out anew in each pass: held through the other phases, it
+    // made this one spill: a batch of 64 x 1024 pages 45 us instead of 33)
+    int anew = 0;
+    asm volatile("" : "+r"(anew));
+    const int *table = p.table + (long long)(b + anew) * p.ld_table;
+    const int8_t *codes = p.index.codes + (h + anew) * p.index.codes_head + quad * 16;
+    const uint8_t *exps = p.index.exps + (h + anew);
+    // This lane's two pages of a tile: their numbers (0 in place of one outside the
+    // index), and for each whether it is a candidate (1) in the index (2).
+    const uint32_t codes_page = (uint32_t)p.index.codes_page + anew, exps_page = (uint32_t)p.index.exps_page + anew;
+    struct Pages {
+      uint32_t id[2], kind[2];
+    };
+    bool outside = false;
+    auto pages_of = [&](int t) {
+      Pages x;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int j = t * 16 + r0 + 8 * i;
+        const bool cand = j >= p.first && j < P - p.last;
+        x.id[i] = cand ? (uint32_t)__ldg(table + j) : 0u;
+        x.kind[i] = cand;
+      }
+      return x;
+    };
+    auto within = [&](Pages &x) {  // (once the numbers are there)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const bool in = x.id[i] < (uint32_t)p.index.pages;
+        outside |= !in;
+        x.id[i] = in ? x.id[i] : 0u;
+        x.kind[i] |= in ? 2u : 0u;
+      }
+    };
+    // where the codes of a page begin for this lane
+    auto codes_at = [&](uint32_t id) {
+      return reinterpret_cast<const uint4 *>(codes + (unsigned long long)id * codes_page);
+    };
+    auto code_of = [&](uint32_t id) { return (int)__ldg(exps + (unsigned long long)id * exps_page); };
+    int code[2] = {0, 0};
+    Pages now = {}, next = {};
+    uint4 w[2][kChunks];
+    if (tile < tiles) {
+      now = pages_of(tile);
+      if (tile + stride < tiles) next = pages_of(tile + stride);
+      within(now);
+      const uint4 *from[2] = {codes_at(now.id[0]), codes_at(now.id[1])};
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) w[i][k] = __ldg(from[i] + k * 4);
+      code[0] = code_of(now.id[0]);
+      code[1] = code_of(now.id[1]);
+    }
     const uint4 *s_b = reinterpret_cast<const uint4 *>(s_q) + lane;  // two steps
     for (; tile < tiles; tile += stride) {
       const int code_now[2] = {code[0], code[1]};
@@ -672,7 +679,7 @@ __global__ void __launch_bounds__(32 * kWarps<MANY>, MANY ? 2 : 4) select_kernel
       const int node = slot * cs + rank;
       const uint32_t *keys = s_keys + slot * plan.cols;
       if (lg == 3) choose<3>(keys, P, p.first, p.last, p.n_sel, row_of(n0 + node), ch);
-      else choose<5>(keys, P, p.first, p.last, p.n_sel, row_of(n0 + node), ch);
+      else choose<4>(keys, P, p.first, p.last, p.n_sel, row_of(n0 + node), ch);
     }
     if (n0 + pass < n) cluster_sync();  // (before the keys are written again)
   }
