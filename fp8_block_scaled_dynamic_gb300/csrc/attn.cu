@@ -10,7 +10,9 @@ cudaError_t launch_attn_prompt(const AttnParams &p, int sm_count, cudaStream_t s
 cudaError_t launch_attn_tree(const AttnParams &tree, int sm_count, cudaStream_t stream) {
   AttnParams p = tree;
   p.slots = kJoinFloats;
-  return p.D == 64 ? launch_t<64, kTree>(p, sm_count, stream) : launch_t<128, kTree>(p, sm_count, stream);
+  const cudaError_t e = p.D == 64 ? launch_t<64, kTree>(p, sm_count, stream) : launch_t<128, kTree>(p, sm_count, stream);
+  if (e != cudaSuccess) return e;
+  return p.D == 64 ? launch_join<64, kTree>(p, sm_count, stream) : launch_join<128, kTree>(p, sm_count, stream);
 }
 size_t attn_tree_ws_bytes(int D, int sm_count) {
   const long long f = D == 64 ? Cfg<64, kTree>::kSlotFloats : Cfg<128, kTree>::kSlotFloats;

@@ -55,6 +55,7 @@ struct Plan {
   const unsigned long long *names;  // sparse: the nodes that name a page, a bit each
   const int *info;                  // shared: of each node, how its parts are joined
   float *rows, *stats;              // shared: parts of whole rows (prefix, own): sums, references and weights
+  float *part_ws[2];                // shared: the two launches' items and slots
 };
 
 struct AttnParams {

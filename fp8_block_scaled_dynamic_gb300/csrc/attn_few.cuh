@@ -1,0 +1,665 @@
+// attn_few.cuh -- attention of few rows a sequence and kv head over a plan's
+// records: decoding and small trees, where attn_kernel.cuh's tiles would be mostly
+// empty.
+//
+// The same sums with the operands exchanged, so that keys and channels, not rows,
+// fill the tensor core's 128 lanes:
+//   S^T (keys x rows)     = K (128 keys x D) . Q^T (D x NR rows)
+//   O^T (channels x rows) += V^T (channels x 128 keys) . P^T (128 keys x NR rows)
+// A softmax thread is a key of the tile (its NR scores), at the end a channel (NR
+// results).  A row's exponentials are spread over 128 threads: a tile of 8 rows
+// takes a warp 0.3 us of instructions where a thread a row took 1.6, and so an item of
+// a few tiles, whose parts follow one another, a third of the time.
+//
+// One pass with a reference a row, as there: it is the first tile's maximum and is
+// moved only when a score is past it by 2^8 (one vote a tile; the maxima themselves
+// are taken when it is).  Weights are rounded to bf16 and summed as rounded, so that
+// what one key's rounding adds above it also adds below.
+//
+// Rows see different keys: a key has a word of the rows that see it (mask words for
+// nodes, a page's word for lists).  A key that no row sees has its v set to zero in
+// shared memory.  A NaN or an infinity in the v of a key that some rows see makes an
+// accumulator that is not finite; such a row is summed again, key by key, from what it
+// sees.
+//
+// Warps: 0-3 softmax, 4 the MMAs, 5 the loads, 6 the items.
+// TMEM columns: two buffers of scores, two of results (of items in turn), 64 each.
+#pragma once
+#include "attn_kernel.cuh"
+
+namespace mxg {
+namespace {
+
+constexpr int kFewThreads = 224;
+constexpr int kFewHead = 6 * 1024;  // bytes of shared memory before the tiles
+
+template <int D, int NR>
+struct FewCfg {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kTile = kKeys * D * 2;
+  static constexpr int kQ = NR * 128 * kHalves;  // a q tile: NR rows of 128 bytes for each 64 channels
+  static constexpr int kP = NR * 256;            // weights: NR rows of 128 bytes for each 64 keys
+  static constexpr int kEnd = 16 * 1024;         // (with D = 64 the lanes past the channels read on behind a v tile)
+  static constexpr int kFit = (227 * 1024 - kFewHead - 2 * kQ - (2 * kP < kEnd ? kEnd : 2 * kP)) / kTile;
+  static constexpr int kSlots = kFit < 12 ? kFit : 12;
+  static constexpr int kSmem = kFewHead + kSlots * kTile + 2 * kQ + (2 * kP < kEnd ? kEnd : 2 * kP);
+  static_assert(kSlots >= 4 && kQ % 1024 == 0 && kP % 1024 == 0, "shared memory");
+};
+
+constexpr int kFewReaders = 6;  // warps 0 to 5
+
+template <int D, int NR, int MODE>
+struct FewSmem {
+  using C = FewCfg<D, NR>;
+  uint64_t kv_full[C::kSlots], kv_empty[C::kSlots], q_full[2], q_empty[2], s_full[2], p_ready[2], pv_done[2];
+  uint64_t o_free[2], item_full[2], item_free[2], mma_done, stall;
+  unsigned long long sees[kAttnMaxNodes];  // of a node as a key: the rows that see it
+  unsigned long long seen[4];              // of a warp's keys: the rows that see one
+  // of a row: its reference m, -m in units of the exponent (infinite: none yet), four warps' maxima or sums
+  alignas(16) float ref[NR], neg[NR], part[4][NR];
+  uint32_t bad[2];  // rows whose accumulator is not finite
+  uint32_t tmem;
+  int abort_flag;
+  Item<MODE> items[2];
+  Prefix pre;
+};
+
+// D fp32, A (N-major or not) and B K-major.
+__host__ __device__ constexpr uint32_t idesc_few(int n, bool a_mn) {
+  return idesc_bf16(128, n, false) | ((a_mn ? 1u : 0u) << 15);
+}
+
+__device__ __forceinline__ bool any_of_four(bool x) {  // of the softmax warps' threads
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void sync_four() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void st_shared_u16(uint32_t to, uint32_t v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"((uint16_t)v) : "memory");
+}
+template <int NR>
+__device__ __forceinline__ void tmem_ld_rows(uint32_t at, uint32_t (&r)[NR]) {
+  if constexpr (NR == 16) {
+    tmem_ld16(at, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < NR / 32; ++i) tmem_ld32(at + i * 32, reinterpret_cast<uint32_t(&)[32]>(r[i * 32]));
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < NR / 32; ++i) tmem_landed(reinterpret_cast<uint32_t(&)[32]>(r[i * 32]));
+  }
+}
+
+// A row of a part summed again by a warp, key by key: lane i has channels i, i + 32,
+// ... of the result.
+template <int D, int MODE>
+__device__ __noinline__ void few_again(const AttnParams &p, const Item<MODE> it, int row, float ref, uint16_t *out,
+                                       float *part, float scale_by) {
+  constexpr int V = D / 32;
+  constexpr unsigned kFull = 0xFFFFFFFFu;
+  const int lane = threadIdx.x & 31, G = p.Hq / p.Hkv, node = row / G, shift = 31 - __clz(p.cache.page_size);
+  const int tok = it.r0 + node, head = it.hk * G + row - node * G;
+  const float c = p.scale * kLog2e;
+  auto value = [](uint32_t x) { return __uint_as_float(x << 16); };
+  float q[V], y[V] = {};
+#pragma unroll
+  for (int i = 0; i < V; ++i) q[i] = value(p.q.ptr[(long long)(it.a0 + tok) * p.q.tok + head * p.q.head + i * 32 + lane]);
+  auto take = [&](const uint16_t *k, const uint16_t *v) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) s = fmaf(q[i], value(k[i * 32 + lane]), s);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+    const float w = __uint_as_float(pack_bf16x2(0.0f, ex2(fmaf(s, c, ref))) & 0xFFFF0000u);
+#pragma unroll
+    for (int i = 0; i < V; ++i) y[i] = fmaf(w, value(v[i * 32 + lane]), y[i]);
+  };
+  const long long list = list_of(it);
+  const int *pages = MODE == kSparse ? p.plan.list : p.table;
+  for (int t = it.t0 * kKeys; t < min(it.ctx, it.t1 * kKeys); ++t) {
+    const int page = pages[list + (t >> shift)];
+    if ((uint32_t)page >= (uint32_t)p.cache.pages) continue;  // (values of zero)
+    if (MODE == kSparse && (flags_of(it) & kLists) && !(p.plan.names[list + (t >> shift)] >> tok & 1ull)) continue;
+    const long long at = page * p.cache.page + (t & (p.cache.page_size - 1)) * p.cache.slot + it.hk * p.cache.head;
+    take(p.cache.k + at, p.cache.v + at);
+  }
+  if (it.t1 > it.nct) {
+    unsigned long long word = p.mask[it.a0 + tok] & (it.n >= 64 ? ~0ull : (1ull << it.n) - 1ull);
+    for (; word; word &= word - 1) {
+      const long long i = it.a0 + __ffsll(word) - 1;
+      take(p.k.ptr + i * p.k.tok + it.hk * p.k.head, p.v.ptr + i * p.v.tok + it.hk * p.v.head);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    if (part) part[i * 32 + lane] = y[i];
+    else out[i * 32 + lane] = (uint16_t)pack_bf16x2(y[i] * scale_by, 0.0f);
+  }
+}
+
+template <int D, int NR, int MODE>
+__global__ void __launch_bounds__(kFewThreads, 1)
+    attn_few_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKC,
+                    const __grid_constant__ CUtensorMap tmVC, const __grid_constant__ AttnParams p) {
+  using C = FewCfg<D, NR>;
+  constexpr int S = C::kSlots;
+  constexpr unsigned kFull = 0xFFFFFFFFu;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  static_assert(sizeof(FewSmem<D, NR, MODE>) <= kFewHead, "shared memory head");
+  FewSmem<D, NR, MODE> &sm = *reinterpret_cast<FewSmem<D, NR, MODE> *>(smem_raw);
+  const uint32_t base = smem_addr(smem_raw);
+  if (base & 1023u) {  // the swizzled tiles need it (uniform over the grid)
+    if (threadIdx.x == 0) {
+      pdl_wait();
+      reinterpret_cast<JoinItem *>(p.ws)[blockIdx.x].rows = 0;
+      if (p.status) atomicOr(p.status, kSmemLayout);
+    }
+    return;
+  }
+  const uint32_t kv_smem = base + kFewHead, q_smem = kv_smem + S * C::kTile, p_smem = q_smem + 2 * C::kQ;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = p.Hq / p.Hkv, TQ = NR / G;  // (the host sees to G <= NR)
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(smem_addr(&sm.kv_full[i]), 1);
+      mbar_init(smem_addr(&sm.kv_empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&sm.q_full[i]), 1);
+      mbar_init(smem_addr(&sm.q_empty[i]), 1);
+      mbar_init(smem_addr(&sm.s_full[i]), 1);
+      mbar_init(smem_addr(&sm.p_ready[i]), 4);
+      mbar_init(smem_addr(&sm.pv_done[i]), 1);
+      mbar_init(smem_addr(&sm.o_free[i]), 4);
+      mbar_init(smem_addr(&sm.item_full[i]), 1);
+      mbar_init(smem_addr(&sm.item_free[i]), kFewReaders);
+    }
+    mbar_init(smem_addr(&sm.mma_done), 1);
+    mbar_init(smem_addr(&sm.stall), 1);
+    sm.abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 4) {
+    tmem_alloc(smem_addr(&sm.tmem), 256);
+    tmem_relinquish();
+  }
+  if (warp == 5 && lane == 0) {
+    prefetch_tmap(&tmQ);
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
+    prefetch_tmap(&tmKC);
+    prefetch_tmap(&tmVC);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&sm.tmem);
+  const WaitCtl ctl{&sm.abort_flag, p.status, p.timeout_ns};
+  pdl_wait();
+  Item<MODE> it;
+  auto next_item = [&](int k) {
+    if (!warp_wait(&sm.item_full[k & 1], (k >> 1) & 1, ctl)) return false;
+    it = sm.items[k & 1];
+    return it.t1 > it.t0;
+  };
+  auto done_item = [&](int k) { warp_arrive(&sm.item_free[k & 1], lane); };
+
+  if (warp == 5) {
+    // --------------------------------------------------------------- loads
+    uint32_t n = 0, nq = 0, slot = 0, turn = 0;
+    bool ok = true;
+    const bool el = elect_one();
+    const uint32_t kvb = uniform(kv_smem), full0 = uniform(smem_addr(&sm.kv_full[0])), qb = uniform(q_smem);
+    const int page_shift = 31 - __clz(p.cache.page_size), box_shift = min(page_shift, 7);
+    for (int k = 0; ok && next_item(k); ++k) {
+      const int t0 = (int)uniform(it.t0), t1 = (int)uniform(it.t1), nct = (int)uniform(it.nct);
+      const int hk = (int)uniform(it.hk), a0 = (int)uniform(it.a0), ctx = (int)uniform(it.ctx);
+      const int *row = (MODE == kSparse ? p.plan.list : p.table) + list_of(it);
+      // lane b: the page of box b (a page of up to 128 keys) of tile j
+      auto page_of = [&](int j) {
+        const int key = (j << 7) + (lane << box_shift);
+        if (j >= nct || j >= t1 || (lane << box_shift) >= kKeys || key >= ctx) return 0;
+        return __ldg(row + (key >> page_shift));
+      };
+      auto load_kv = [&](int j, bool is_v, int pg) {
+        if (!warp_wait_far(&sm.kv_empty[slot], turn ^ 1, ctl)) return false;  // (free at first)
+        const uint32_t us = uniform(slot), bar = full0 + 8 * us, dst = kvb + us * C::kTile;
+        if (j < nct) {
+          const int boxes = (min(kKeys, ctx - (j << 7)) + (1 << box_shift) - 1) >> box_shift;
+          if ((uint32_t)pg >= (uint32_t)p.cache.pages) {
+            pg = p.cache.pages;  // out of the map's bounds: zeros
+            if (p.status) atomicOr(p.status, kBadIndex);
+          }
+          int page[8];
+#pragma unroll
+          for (int b = 0; b < 8; ++b) page[b] = (int)__shfl_sync(kFull, pg, b);
+          if (el) {
+            mbar_arrive_expect_tx(bar, (uint32_t)boxes << (box_shift + 7) << (C::kHalves - 1));
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+              if (b >= boxes) break;
+#pragma unroll
+              for (int h = 0; h < C::kHalves; ++h)
+                tma_load_4d(dst + h * 16384 + (b << box_shift) * 128, is_v ? &tmVC : &tmKC, h * 64, hk,
+                            (j << 7) & ((1 << page_shift) - 1), page[b], bar);
+            }
+          }
+        } else if (el) {
+          mbar_arrive_expect_tx(bar, (uint32_t)(kAttnMaxNodes * 128 * C::kHalves));
+#pragma unroll
+          for (int h = 0; h < C::kHalves; ++h) tma_load_3d(dst + h * 16384, is_v ? &tmV : &tmK, h * 64, hk, a0, bar);
+        }
+        __syncwarp();
+        ++n;
+        if (++slot == S) slot = 0, turn ^= 1;
+        return true;
+      };
+      int pg[4];  // this lane's pages of tiles j .. j + 3
+#pragma unroll
+      for (int x = 0; x < 3; ++x) pg[x] = page_of(t0 + x);
+      // q (the q tiles in turn)
+      if (nq >= 2) ok = warp_wait_far(&sm.q_empty[nq & 1], ((nq >> 1) - 1) & 1, ctl);
+      if (!ok) break;
+      if (el) {
+        const uint32_t bar = smem_addr(&sm.q_full[nq & 1]);
+        mbar_arrive_expect_tx(bar, (uint32_t)(TQ * G * 128 * C::kHalves));
+#pragma unroll
+        for (int h = 0; h < C::kHalves; ++h)
+          tma_load_3d(qb + (nq & 1) * C::kQ + h * NR * 128, &tmQ, h * 64, hk * G, a0 + (int)it.r0, bar);
+      }
+      __syncwarp();
+      ++nq;
+      ok = load_kv(t0, false, pg[0]);
+      if (ok && t0 + 1 < t1) ok = load_kv(t0 + 1, false, pg[1]);
+      for (int j = t0; ok && j < t1; ++j) {  // (k two tiles ahead of v)
+        pg[3] = page_of(j + 3);
+        ok = load_kv(j, true, pg[0]);
+        if (ok && j + 2 < t1) ok = load_kv(j + 2, false, pg[2]);
+#pragma unroll
+        for (int x = 0; x < 3; ++x) pg[x] = pg[x + 1];
+      }
+      done_item(k);
+    }
+    // nothing may land in shared memory once the CTA is gone (a timeout)
+    for (uint32_t k = n > S ? n - S : 0; k < n; ++k) drain(&sm.kv_full[k % S], (k / S) & 1, p.timeout_ns);
+    for (uint32_t k = nq > 2 ? nq - 2 : 0; k < nq; ++k) drain(&sm.q_full[k & 1], (k >> 1) & 1, p.timeout_ns);
+  } else if (warp == 4) {
+    // ---------------------------------------------------------------- MMAs
+    const bool el = elect_one();
+    const uint32_t tm = uniform(tmem), qb = uniform(q_smem), kb = uniform(kv_smem), pb = uniform(p_smem);
+    constexpr uint32_t kIdQK = idesc_few(NR, false), kIdPV = idesc_few(NR, true);
+    uint32_t rn = 0, tile = 0;  // tiles of the ring, tiles of keys so far
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return lane_wait(bar, parity, ctl); };
+    auto ring = [&](uint32_t k) { return wait(&sm.kv_full[k % S], (k / S) & 1); };
+    auto all_ok = [&](bool x) { return __all_sync(kFull, x) != 0; };
+    // scores of tile number t of all (buffer t & 1); its k is ring tile r
+    auto qk = [&](uint32_t t, uint64_t kd, uint64_t qd, uint32_t r) {
+      tc_fence_after();
+#pragma unroll
+      for (int h = 0; h < C::kHalves; ++h)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          mma_bf16_ss(tm + (t & 1) * 64, kd + h * 1024 + x * 2, qd + h * (NR * 8) + x * 2, kIdQK, (h | x) != 0);
+      tc_commit(smem_addr(&sm.s_full[t & 1]));
+      tc_commit(smem_addr(&sm.kv_empty[r % S]));
+    };
+    auto kdesc = [&](uint32_t r) { return sdesc_kmajor_sw128(kb + uniform(r % S) * C::kTile); };
+    auto vdesc = [&](uint32_t r) { return sdesc_mnmajor_sw128(kb + uniform(r % S) * C::kTile, 16384); };
+    for (int k = 0; ok && next_item(k); ++k) {
+      const int nt = (int)uniform(it.t1 - it.t0);
+      done_item(k);
+      const uint64_t qd = sdesc_kmajor_sw128(qb + uniform(k & 1) * C::kQ);
+      const uint32_t o = tm + 128 + (k & 1) * 64;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (!ok || s >= nt) continue;
+        const uint64_t kd = kdesc(rn);
+        if (el) {
+          // (the weights of two tiles back are there: their scores have been read)
+          const uint32_t t = tile + s;
+          ok = ring(rn) && (s > 0 || wait(&sm.q_full[k & 1], (k >> 1) & 1));
+          if (ok) qk(t, kd, qd, rn);
+        }
+        ok = all_ok(ok);
+        ++rn;
+      }
+      for (int i = 0; ok && i < nt; ++i) {
+        const bool more = i + 2 < nt;
+        const uint64_t vd = vdesc(rn), kd = kdesc(rn + 1);
+        const uint32_t t = tile + i;
+        if (el) {
+          const uint64_t pd = sdesc_kmajor_sw128(pb + (t & 1) * C::kP);
+          ok = ring(rn) && (i > 0 || k < 2 || wait(&sm.o_free[k & 1], ((k >> 1) - 1) & 1)) &&
+               wait(&sm.p_ready[t & 1], (t >> 1) & 1);
+          if (ok) {
+            tc_fence_after();
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              mma_bf16_ss(o, vd + x * 128, pd + (x >> 2) * (NR * 8) + (x & 3) * 2, kIdPV, i > 0 || x > 0);
+            tc_commit(smem_addr(&sm.pv_done[t & 1]));
+            tc_commit(smem_addr(&sm.kv_empty[rn % S]));
+            if (i + 1 == nt) tc_commit(smem_addr(&sm.q_empty[k & 1]));
+          }
+          if (ok && more) {
+            ok = ring(rn + 1);
+            if (ok) qk(t + 2, kd, qd, rn + 1);
+          }
+        }
+        ok = all_ok(ok);
+        rn += more ? 2 : 1;
+      }
+      tile += nt;
+    }
+    // every MMA has completed before the CTA leaves its shared memory and TMEM
+    if (el) {
+      tc_commit(smem_addr(&sm.mma_done));
+      drain(&sm.mma_done, 0, p.timeout_ns);
+    }
+    __syncwarp();
+  } else if (warp == 6) {
+    // --------------------------------------------------------------- items
+    const bool few = seqs<MODE>(p) <= 32;
+    Small<MODE> small;
+    if (few) small.read(p, TQ, lane, false);
+    else fill_prefix<MODE>(p, sm.pre, TQ, lane, false);
+    if (few) small.number(p, lane);
+    Walk<MODE> walk(few ? small.total : sm.pre.units[kBlocks], TQ);
+    Found found;
+    bool going_on = false;
+    if (few) walk.choose_chunk(small);
+    for (int k = 0;; ++k) {
+      Item<MODE> w;
+      int last = 0;  // the last CTA that has a part of the row group
+      if (walk.chunk > 0 && k == 0) {
+        last = walk.one_chunk(p, small, TQ, w);
+      } else {
+        walk.next(p, TQ, w, [&](int &u, int &b) {
+          return few ? small.find(u, b) : find_seq<MODE>(p, sm.pre, TQ, u, b, found);
+        });
+        if (w.t1 > w.t0 && w.part == 1)
+          last = share_owner(share_begin(blockIdx.x + 1, walk.q, walk.r) + w.nct + (flags_of(w) & kHasNodes) - 1 - w.t1,
+                             walk.q, walk.r);
+      }
+      if (k >= 2 && !warp_wait_far(&sm.item_free[k & 1], ((k >> 1) - 1) & 1, ctl)) break;
+      if (lane == 0) sm.items[k & 1] = w;
+      warp_arrive(&sm.item_full[k & 1], lane);
+      if (w.t1 == w.t0) break;
+      if (w.part == 1) {
+        going_on = true;
+        if (lane == 0) {
+          JoinItem j;
+          j.rows0 = j.rows = w.cnt[0] * G;
+          j.tok = w.a0 + w.r0;
+          j.cnt0 = w.cnt[0];
+          j.head = w.hk * G;
+          j.last = last;
+          j.word = w.n;
+          j.ctx = w.ctx;
+          reinterpret_cast<JoinItem *>(p.ws)[blockIdx.x] = j;
+        }
+      }
+    }
+    if (!going_on && lane == 0) reinterpret_cast<JoinItem *>(p.ws)[blockIdx.x].rows = 0;
+  } else {
+    // ------------------------------------------------------------- softmax
+    // (A wait that runs out lets a warp go on without what it waited for, to the
+    // next common barrier: the four warps leave together.)
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    const int key = warp * 32 + lane;  // of a tile; at the end the channel
+    const float c = p.scale * kLog2e;
+    const int page_shift = 31 - __clz(p.cache.page_size);
+    uint32_t tile = 0, rn = 0;
+    bool ok = true;
+    if (p.debug_stall) ok = warp_wait(&sm.stall, 0, ctl);
+    for (int k = 0;; ++k) {
+      const bool there = ok && next_item(k);
+      if (any_of_four(!there)) break;
+      const int nt = it.t1 - it.t0, rows = it.cnt[0] * G;
+      const unsigned long long mine = rows >= 64 ? ~0ull : (1ull << rows) - 1ull;  // the item's rows
+      const unsigned long long group = G >= 64 ? ~0ull : (1ull << G) - 1ull;
+      const bool lists = MODE == kSparse && (flags_of(it) & kLists);
+      // the rows of the nodes in a word
+      auto rows_of = [&](unsigned long long nodes) {
+        unsigned long long r = 0;
+        nodes >>= it.r0;
+        for (int i = 0; i < it.cnt[0]; ++i)
+          if (nodes >> i & 1ull) r |= group << (i * G);
+        return r;
+      };
+      unsigned long long who = 0;  // lists: the nodes that name this key's page, of the next tile
+      auto names_of = [&](int j) {
+        const int t = j * kKeys + key;
+        if (lists && j < it.nct && t < it.ctx) who = __ldg(p.plan.names + list_of(it) + (t >> page_shift));
+      };
+      names_of(it.t0);
+      if (it.t1 > it.nct && key < kAttnMaxNodes) {
+        // of this node as a key: the rows that see it
+        unsigned long long r = 0;
+        if (key < it.n)
+          for (int i = 0; i < it.cnt[0]; ++i)
+            if (__ldg(p.mask + it.a0 + it.r0 + i) >> key & 1ull) r |= group << (i * G);
+        sm.sees[key] = r;
+      }
+      float l[NR];
+#pragma unroll
+      for (int r = 0; r < NR; ++r) l[r] = 0.0f;
+      if (key < NR) sm.ref[key] = -INFINITY, sm.neg[key] = INFINITY;
+      if (key < 2) sm.bad[key] = 0;
+      unsigned long long saw = 0;
+      sync_four();
+      for (int i = 0; i < nt; ++i) {
+        const int j = it.t0 + i;
+        const uint32_t t = tile + i, sb = t & 1, ph = (t >> 1) & 1;
+        const uint32_t v_at = rn + (nt > 1 ? 2 : 1) + i + min(i, max(nt - 2, 0));  // the v tile's place in the ring
+        unsigned long long see;
+        if (j >= it.nct) see = key < kAttnMaxNodes ? sm.sees[key] : 0ull;
+        else if (j * kKeys + key >= it.ctx) see = 0ull;
+        else see = lists ? rows_of(who) : mine;
+        names_of(j + 1);
+        saw |= see;
+        if (!warp_wait(&sm.s_full[sb], ph, ctl)) ok = false;
+        tc_fence_after();
+        uint32_t s[NR];
+        tmem_ld_rows<NR>(tmem + lanes + sb * 64, s);
+        if (see != ~0ull) {
+#pragma unroll
+          for (int r = 0; r < NR; ++r)
+            if (!((r < 32 ? (uint32_t)see >> (r & 31) : (uint32_t)(see >> 32) >> (r & 31)) & 1u)) s[r] = 0xFF800000u;
+        }
+        // is a score past its row's reference?  (no reference yet: any is)
+        bool past = false;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) past |= fmaf(__uint_as_float(s[r]), c, sm.neg[r]) > kFallBehind;
+        if (any_of_four(past)) {
+          // the rows' maxima: this warp's keys, then all
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            float m = __uint_as_float(s[r]);
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, x));
+            if (lane == (r & 31)) sm.part[warp][r] = m;
+          }
+          sync_four();
+          // a first maximum is the reference; later ones move it, the sums and the accumulator
+          const uint32_t prev = t - 1;
+          if (i > 0) {
+            if (!warp_wait(&sm.pv_done[prev & 1], (prev >> 1) & 1, ctl)) ok = false;
+            tc_fence_after();
+            uint32_t o[NR];
+            const uint32_t at = tmem + lanes + 128 + (k & 1) * 64;
+            tmem_ld_rows<NR>(at, o);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+              const float old = sm.ref[r];
+              const float top = fmaxf(fmaxf(sm.part[0][r], sm.part[1][r]), fmaxf(sm.part[2][r], sm.part[3][r]));
+              const float f = top > old ? (old == -INFINITY ? 0.0f : ex2((old - top) * c)) : 1.0f;
+              l[r] *= f;
+              // (an accumulator without a reference yet is zero, or what an unseen NaN made of it)
+              o[r] = __float_as_uint(__uint_as_float(o[r]) * f);
+            }
+#pragma unroll
+            for (int x = 0; x < NR / 16; ++x) tmem_st16(at + x * 16, o + x * 16);
+            tmem_st_wait();
+            tc_fence_before();
+          }
+          sync_four();
+          if (key < NR) {
+            const float m =
+                fmaxf(sm.ref[key], fmaxf(fmaxf(sm.part[0][key], sm.part[1][key]), fmaxf(sm.part[2][key], sm.part[3][key])));
+            sm.ref[key] = m;
+            sm.neg[key] = -m * c;
+          }
+          sync_four();
+        }
+        // weights, rounded to bf16, for the product (the tile before the last has been multiplied by now:
+        // its scores' buffer is in use again) and as sums
+        const uint32_t to = p_smem + sb * C::kP + (key >> 6) * (NR * 128) + (key & 7) * 2, unit = (key >> 3) & 7;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          const float neg = sm.neg[r];
+          const uint32_t w = pack_bf16x2(ex2(fmaf(__uint_as_float(s[r]), c, neg == INFINITY ? 0.0f : neg)), 0.0f);
+          l[r] += __uint_as_float(w << 16);
+          st_shared_u16(to + r * 128 + ((unit ^ (r & 7)) << 4), w);
+        }
+        if (see == 0ull) {
+          // no row sees this key: its v is made zero
+          if (!mbar_wait_quick(smem_addr(&sm.kv_full[v_at % S]), (v_at / S) & 1, ctl)) ok = false;
+          const uint32_t v = kv_smem + (v_at % S) * C::kTile + key * 128;
+#pragma unroll
+          for (int h = 0; h < C::kHalves; ++h)
+#pragma unroll
+            for (int x = 0; x < 8; ++x) st_shared_v4(v + h * 16384 + ((x + lane) & 7) * 16, 0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        warp_arrive(&sm.p_ready[sb], lane);
+      }
+      ok = __all_sync(kFull, ok);
+      // sums over the keys, rows seen
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        float x = l[r];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
+        if (lane == (r & 31)) sm.part[warp][r] = x;
+      }
+      const uint32_t saw_lo = __reduce_or_sync(kFull, (uint32_t)saw), saw_hi = __reduce_or_sync(kFull, (uint32_t)(saw >> 32));
+      if (lane == 0) sm.seen[warp] = (unsigned long long)saw_hi << 32 | saw_lo;
+      const uint32_t lastt = tile + nt - 1;
+      if (!warp_wait(&sm.pv_done[lastt & 1], (lastt >> 1) & 1, ctl)) ok = false;
+      tc_fence_after();
+      uint32_t o[NR];
+      tmem_ld_rows<NR>(tmem + lanes + 128 + (k & 1) * 64, o);
+      tc_fence_before();
+      warp_arrive(&sm.o_free[k & 1], lane);
+      if (key < D) {
+        uint32_t bad[2] = {0, 0};
+#pragma unroll
+        for (int r = 0; r < NR; ++r) bad[r / 32] |= (o[r] & 0x7F800000u) == 0x7F800000u ? 1u << (r & 31) : 0u;
+        bad[0] &= (uint32_t)mine;
+        bad[1] &= (uint32_t)(mine >> 32);
+        if (bad[0]) atomicOr(&sm.bad[0], bad[0]);
+        if (bad[1]) atomicOr(&sm.bad[1], bad[1]);
+      }
+      sync_four();
+      const unsigned long long seen = sm.seen[0] | sm.seen[1] | sm.seen[2] | sm.seen[3];
+      const unsigned long long bad = (unsigned long long)sm.bad[1] << 32 | sm.bad[0];
+      // the rows of this item, in memory: of nodes, a head each
+      const float *slot_m = nullptr;
+      float *slot = nullptr;
+      if (it.part == 0 || it.part == 1) {
+        slot = p.ws + p.slots + ((long long)blockIdx.x * 2 + it.part) * Cfg<D, MODE>::kSlotFloats;
+        slot_m = slot + D * kRowsT;
+      }
+      const long long row0 = (long long)(it.a0 + it.r0) * p.Hq + it.hk * G;  // shared: first row's place
+      const long long kind = MODE == kShared ? (long long)(flags_of(it) & kHasNodes) * p.T * p.Hq : 0;
+      int node = 0, head = 0;
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        if (r >= rows) break;
+        const float total = (sm.part[0][r] + sm.part[1][r]) + (sm.part[2][r] + sm.part[3][r]), m = sm.ref[r];
+        const bool any = seen >> r & 1ull;
+        const long long at = row0 + (long long)node * p.Hq + head;
+        if (it.part < 0) {
+          if (key < D) {
+            const float y = __uint_as_float(o[r]) * (1.0f / total);
+            p.out.ptr[(long long)(it.a0 + it.r0 + node) * p.out.tok + (it.hk * G + head) * p.out.head + key] =
+                any ? (uint16_t)pack_bf16x2(y, 0.0f) : (uint16_t)0;
+          }
+        } else {
+          float *to = it.part == 2 ? p.plan.rows + (kind + at) * D : slot + r * D;
+          float *stat = it.part == 2 ? p.plan.stats + (kind + at) * 2 : const_cast<float *>(slot_m) + r;
+          if (key < D) to[key] = __uint_as_float(o[r]);
+          if (key == (r & 127)) {
+            // (a sum of 0 says that the row sees nothing of the part)
+            stat[0] = m;
+            stat[it.part == 2 ? 1 : kRowsT] = !any ? 0.0f : m == -INFINITY ? 1.0f : total;
+          }
+        }
+        if (++head == G) head = 0, ++node;
+      }
+      // rows to be summed again, after what was stored of them: a warp each
+      if (bad) {
+        sync_four();
+        for (int r = warp; r < rows; r += 4) {
+          if (!(bad >> r & 1ull)) continue;
+          const int nd = r / G, hd = r - nd * G;
+          const float total = (sm.part[0][r] + sm.part[1][r]) + (sm.part[2][r] + sm.part[3][r]), m = sm.ref[r];
+          const long long at = row0 + (long long)nd * p.Hq + hd;
+          uint16_t *out = p.out.ptr + (long long)(it.a0 + it.r0 + nd) * p.out.tok + (it.hk * G + hd) * p.out.head;
+          float *part = it.part < 0 ? nullptr : it.part == 2 ? p.plan.rows + (kind + at) * D : slot + r * D;
+          if (it.part >= 0 || (seen >> r & 1ull))
+            few_again<D, MODE>(p, it, r, m == -INFINITY ? 0.0f : -m * c, out, part, 1.0f / total);
+        }
+      }
+      tile += nt;
+      rn += 2 * nt;
+      done_item(k);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 4) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
+  }
+}
+
+template <int D, int NR, int MODE>
+cudaError_t launch_few(const AttnParams &p, int sm_count, cudaStream_t stream) {
+  using C = FewCfg<D, NR>;
+  auto kern = attn_few_kernel<D, NR, MODE>;
+  static DeviceOnce once;
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!once.done(dev)) {
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem)) != cudaSuccess) return e;
+    once.set(dev);
+  }
+  const int G = p.Hq / p.Hkv, TQ = NR / G;
+  CUtensorMap q, k, v, kc, vc;
+  if (!heads_map(&q, p.q, p.Hq, p.T, D, G, TQ) || !heads_map(&k, p.k, p.Hkv, p.T, D, 1, kAttnMaxNodes) ||
+      !heads_map(&v, p.v, p.Hkv, p.T, D, 1, kAttnMaxNodes) || !cache_maps(&kc, &vc, p))
+    return cudaErrorInvalidValue;
+  const int ctas = sm_count < kMaxCtas ? sm_count : kMaxCtas;
+  cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)ctas), dim3(kFewThreads), C::kSmem, stream);
+  cudaLaunchAttribute attr[1];
+  attach_pdl(cfg, attr);
+  return cudaLaunchKernelEx(&cfg, kern, q, k, v, kc, vc, p);
+}
+
+}  // namespace
+}  // namespace mxg

@@ -332,7 +332,7 @@ struct JoinItem {
   int head;         // first query head
   int last;         // last CTA that holds a part
   int word;         // bits of a mask word that count
-  int ctx;          // cached tokens; shared: 0 = a prefix, 1 = a sequence's own
+  int ctx;          // cached tokens
 };
 
 static_assert(sizeof(JoinItem) == 32, "workspace header");
@@ -1144,7 +1144,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             j.head = w.hk * G;
             j.last = last;
             j.word = w.n;
-            j.ctx = MODE == kShared ? flags_of(w) & kHasNodes : w.ctx;
+            j.ctx = w.ctx;
             reinterpret_cast<JoinItem *>(p.ws)[blockIdx.x] = j;
           }
         }
@@ -1640,43 +1640,49 @@ __global__ void __launch_bounds__(32 * kJoinWarps, kJoinBlocksSm) attn_join_kern
 // The same for groups that share a prefix: a warp takes a row of the call, whose
 // parts are those of its group's prefix, in the order of the keys, and those of
 // its sequence's own keys.  Either is one part in the row's own place, or the
-// slots of the CTAs that shared it: the items that went on are in the order of
-// (prefix or own, first node, kv head), so the row's is found by bisection.
+// slots of the CTAs that shared it.  Prefixes and own keys were two launches, each
+// with its list of items that went on and its slots; a list is in the order of (first
+// node, kv head), so the row's item is found by bisection.
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps, kJoinBlocksSm) attn_join_rows_kernel(const AttnParams p, int ctas) {
   using C = Cfg<D, kShared>;
   constexpr int V = D / 32;
   constexpr unsigned kFull = 0xFFFFFFFFu;
-  __shared__ JoinItem s_item[kMaxCtas];
-  __shared__ unsigned long long s_key[kMaxCtas];
-  __shared__ int s_cta[kMaxCtas], s_warp[kJoinWarps];
+  __shared__ JoinItem s_item[2][kMaxCtas];
+  __shared__ unsigned long long s_key[2][kMaxCtas];
+  __shared__ int s_cta[2][kMaxCtas], s_warp[2][kJoinWarps];
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.Hq / p.Hkv;
   const float c = p.scale * kLog2e;
-  s_key[threadIdx.x] = ~0ull;
+  s_key[0][threadIdx.x] = s_key[1][threadIdx.x] = ~0ull;
   pdl_wait();
-  JoinItem mine = {};
-  if ((int)threadIdx.x < ctas) mine = reinterpret_cast<const JoinItem *>(p.ws)[threadIdx.x];
-  const unsigned has = __ballot_sync(kFull, mine.rows > 0);
-  if (lane == 0) s_warp[warp] = __popc(has);
-  __syncthreads();
-  auto key_of = [&](int kind, int node, int hk) {
-    return ((unsigned long long)kind << 55) | ((unsigned long long)(uint32_t)node << 24) | (unsigned long long)hk;
-  };
-  if (mine.rows > 0) {
-    int at = __popc(has & ((1u << lane) - 1u));
-    for (int w = 0; w < warp; ++w) at += s_warp[w];
-    s_item[at] = mine;
-    s_cta[at] = threadIdx.x;
-    s_key[at] = key_of(mine.ctx, mine.tok, mine.head / G);
+  JoinItem mine[2] = {};
+  unsigned has[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if ((int)threadIdx.x < ctas && p.plan.part_ws[i])
+      mine[i] = reinterpret_cast<const JoinItem *>(p.plan.part_ws[i])[threadIdx.x];
+    has[i] = __ballot_sync(kFull, mine[i].rows > 0);
+    if (lane == 0) s_warp[i][warp] = __popc(has[i]);
   }
   __syncthreads();
-  auto last_at = [&](unsigned long long key) {  // the last item whose key is not above this one, or -1
+  auto key_of = [&](int node, int hk) { return ((unsigned long long)(uint32_t)node << 24) | (unsigned long long)hk; };
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (mine[i].rows > 0) {
+      int at = __popc(has[i] & ((1u << lane) - 1u));
+      for (int w = 0; w < warp; ++w) at += s_warp[i][w];
+      s_item[i][at] = mine[i];
+      s_cta[i][at] = threadIdx.x;
+      s_key[i][at] = key_of(mine[i].tok, mine[i].head / G);
+    }
+  __syncthreads();
+  auto last_at = [&](int list, unsigned long long key) {  // the last item whose key is not above this one, or -1
     int i = -1;
 #pragma unroll
     for (int o = kMaxCtas / 2; o > 0; o >>= 1)
-      if (s_key[i + o] <= key) i += o;
+      if (s_key[list][i + o] <= key) i += o;
     return i;
   };
   const long long total = (long long)p.T * p.Hq;
@@ -1690,15 +1696,16 @@ __global__ void __launch_bounds__(32 * kJoinWarps, kJoinBlocksSm) attn_join_rows
     for (int kind = 0; kind < 2; ++kind) {
       if (kind >= 1 - info) {
         // the first node of the last row group that begins at or before this one, then its item of this kv head
-        int i = last_at(key_of(kind, node, (1 << 24) - 1));
-        if (i >= 0) i = last_at(key_of(kind, s_item[i].tok, hk));
+        int i = last_at(kind, key_of(node, (1 << 24) - 1));
+        if (i >= 0) i = last_at(kind, key_of(s_item[kind][i].tok, hk));
         if (i >= 0) {
-          const JoinItem it = s_item[i];
+          const JoinItem it = s_item[kind][i];
           const int d = node - it.tok, tile = d >= it.cnt0;
-          if (it.ctx == kind && it.head == hk * G && d >= 0 && d * G < it.rows) {
+          if (it.head == hk * G && d >= 0 && d * G < it.rows) {
             row[kind] = (d - tile * it.cnt0) * G + head - it.head;
-            parts[kind] = it.last - s_cta[i] + 1;
-            base[kind] = p.ws + p.slots + ((long long)s_cta[i] * 2 + 1) * C::kSlotFloats + tile * (kRowsT * (D + 2));
+            parts[kind] = it.last - s_cta[kind][i] + 1;
+            base[kind] = p.plan.part_ws[kind] + p.slots + ((long long)s_cta[kind][i] * 2 + 1) * C::kSlotFloats +
+                         tile * (kRowsT * (D + 2));
           }
         }
       }
@@ -1762,6 +1769,25 @@ bool heads_map(CUtensorMap *m, const Heads &h, int heads, int T, int D, int box_
   return make_map(m, h.ptr, 3, dims, st, box);
 }
 
+bool cache_maps(CUtensorMap *k, CUtensorMap *v, const AttnParams &p) {
+  const cuuint64_t dims[4] = {(cuuint64_t)p.D, (cuuint64_t)p.Hkv, (cuuint64_t)p.cache.page_size, (cuuint64_t)p.cache.pages};
+  const long long st[3] = {p.cache.head, p.cache.slot, p.cache.page};
+  const cuuint32_t box[4] = {64, 1, (cuuint32_t)(p.cache.page_size < kKeys ? p.cache.page_size : kKeys), 1};
+  return make_map(k, p.cache.k, 4, dims, st, box) && make_map(v, p.cache.v, 4, dims, st, box);
+}
+
+// The grid of a paged kernel: what a part's slot is numbered by.
+int paged_ctas(int sm_count) { return sm_count < kMaxCtas ? sm_count : kMaxCtas; }
+
+template <int D, int MODE>
+cudaError_t launch_join(const AttnParams &p, int sm_count, cudaStream_t stream) {
+  cudaLaunchConfig_t jc = pdl_config(dim3((unsigned)(kJoinBlocksSm * sm_count)), dim3(32 * kJoinWarps), 0, stream);
+  cudaLaunchAttribute attr[1];
+  attach_pdl(jc, attr);
+  if constexpr (MODE == kShared) return cudaLaunchKernelEx(&jc, attn_join_rows_kernel<D>, p, paged_ctas(sm_count));
+  else return cudaLaunchKernelEx(&jc, attn_join_kernel<D, MODE>, p, paged_ctas(sm_count));
+}
+
 template <int D, int MODE>
 cudaError_t launch_t(const AttnParams &p, int sm_count, cudaStream_t stream) {
   using C = Cfg<D, MODE>;
@@ -1788,14 +1814,9 @@ cudaError_t launch_t(const AttnParams &p, int sm_count, cudaStream_t stream) {
   if (!heads_map(&q, p.q, p.Hq, p.T, D, G, TQ) || !heads_map(&k, p.k, p.Hkv, p.T, D, 1, rows) ||
       !heads_map(&v, p.v, p.Hkv, p.T, D, 1, rows))
     return cudaErrorInvalidValue;
-  long long ctas = sm_count < kMaxCtas ? sm_count : kMaxCtas;
+  long long ctas = paged_ctas(sm_count);
   if (TREE) {
-    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)p.Hkv, (cuuint64_t)p.cache.page_size,
-                                (cuuint64_t)p.cache.pages};
-    const long long st[3] = {p.cache.head, p.cache.slot, p.cache.page};
-    const cuuint32_t box[4] = {64, 1, (cuuint32_t)(p.cache.page_size < kKeys ? p.cache.page_size : kKeys), 1};
-    if (!make_map(&kc, p.cache.k, 4, dims, st, box) || !make_map(&vc, p.cache.v, 4, dims, st, box))
-      return cudaErrorInvalidValue;
+    if (!cache_maps(&kc, &vc, p)) return cudaErrorInvalidValue;
   } else {
     // no more than there can be row groups (each sequence rounds up)
     const long long items = ((long long)p.T / TQ + p.B) * p.Hkv;
@@ -1804,15 +1825,7 @@ cudaError_t launch_t(const AttnParams &p, int sm_count, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)ctas), dim3(kThreads), C::kSmem, stream);
   cudaLaunchAttribute attr[1];
   attach_pdl(cfg, attr);
-  e = cudaLaunchKernelEx(&cfg, kern, q, k, v, kc, vc, p);
-  if constexpr (TREE) {
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t jc = pdl_config(dim3((unsigned)(kJoinBlocksSm * sm_count)), dim3(32 * kJoinWarps), 0, stream);
-    attach_pdl(jc, attr);
-    if constexpr (MODE == kShared) e = cudaLaunchKernelEx(&jc, attn_join_rows_kernel<D>, p, (int)ctas);
-    else e = cudaLaunchKernelEx(&jc, attn_join_kernel<D, MODE>, p, (int)ctas);
-  }
-  return e;
+  return cudaLaunchKernelEx(&cfg, kern, q, k, v, kc, vc, p);
 }
 
 }  // namespace

@@ -11,6 +11,7 @@
 //   its nodes names, in order, with a word a page that says which nodes do.  A page
 //   is then loaded once for all of them; the scores of those that do not name it are
 //   taken out by the word.
+#include "attn_few.cuh"
 #include "attn_kernel.cuh"
 
 namespace mxg {
@@ -220,28 +221,63 @@ size_t slots_bytes(int D, int sm_count) {
   return (size_t)(2 * f * (sm_count < kMaxCtas ? sm_count : kMaxCtas)) * sizeof(float);
 }
 
-// Byte offsets; the items that attn_join_kernel reads come first.
+// Byte offsets; a launch's items, which the join reads, come first, then its slots.
 struct SharedWs {
-  size_t rec, info, slots, rows, stats, end;
+  size_t slots, second, rec, info, rows, stats, end;
   SharedWs(long long N, int Hq, int D, int sm_count) {
-    rec = kJoinFloats * sizeof(float);
+    slots = kJoinFloats * sizeof(float);
+    second = slots + slots_bytes(D, sm_count);
+    rec = 2 * second;
     info = rec + 2 * kAttnMaxSeqs * sizeof(PlanRec);
-    slots = round256(info + N * sizeof(int));
-    rows = slots + slots_bytes(D, sm_count);
+    rows = round256(info + N * sizeof(int));
     stats = rows + (size_t)(2 * N * Hq) * D * sizeof(float);
     end = round256(stats + (size_t)(2 * N * Hq) * 2 * sizeof(float));
   }
 };
 struct SparseWs {
-  size_t rec, slots, names, list, end;
+  size_t slots, rec, names, list, end;
   SparseWs(long long N, int Hkv, int n_sel, int D, int sm_count) {
-    rec = kJoinFloats * sizeof(float);
-    slots = rec + (size_t)kAttnMaxSeqs * Hkv * sizeof(PlanRec);
-    names = slots + slots_bytes(D, sm_count);
+    slots = kJoinFloats * sizeof(float);
+    rec = slots + slots_bytes(D, sm_count);
+    names = rec + (size_t)kAttnMaxSeqs * Hkv * sizeof(PlanRec);
     list = names + (size_t)(N * Hkv) * n_sel * sizeof(unsigned long long);
     end = round256(list + (size_t)(N * Hkv) * n_sel * sizeof(int));
   }
 };
+
+// Sequences' rows of a kv head: where an average sequence's fit, the kernel of few
+// rows, with as many as it needs; else the one of full tiles.
+template <int D, int MODE>
+cudaError_t launch_rows(const AttnParams &p, int sm_count, cudaStream_t stream) {
+  const int G = p.Hq / p.Hkv;
+  const long long rows = ((long long)p.T + p.B - 1) / p.B * G;
+  if (rows <= 16) return launch_few<D, 16, MODE>(p, sm_count, stream);
+  if (rows <= 32) return launch_few<D, 32, MODE>(p, sm_count, stream);
+  if (rows <= 64) return launch_few<D, 64, MODE>(p, sm_count, stream);
+  return launch_t<D, MODE>(p, sm_count, stream);
+}
+
+template <int D>
+cudaError_t launch_shared(const SharedParams &p, AttnParams a, PlanRec *rec, int sm_count, cudaStream_t stream) {
+  cudaError_t e = cudaSuccess;
+  if (p.n_groups > 0) {
+    a.ws = a.plan.part_ws[0];
+    a.plan.rec = rec;
+    a.plan.n = p.n_groups;
+    if ((e = launch_t<D, kShared>(a, sm_count, stream)) != cudaSuccess) return e;
+  }
+  a.ws = a.plan.part_ws[1];
+  a.plan.rec = rec + p.n_groups;
+  a.plan.n = a.B;
+  if ((e = launch_rows<D, kShared>(a, sm_count, stream)) != cudaSuccess) return e;
+  return launch_join<D, kShared>(a, sm_count, stream);
+}
+
+template <int D>
+cudaError_t launch_sparse(const AttnParams &a, int sm_count, cudaStream_t stream) {
+  const cudaError_t e = launch_rows<D, kSparse>(a, sm_count, stream);
+  return e == cudaSuccess ? launch_join<D, kSparse>(a, sm_count, stream) : e;
+}
 
 }  // namespace
 
@@ -250,10 +286,10 @@ size_t attn_sparse_ws_bytes(long long N, int Hkv, int n_sel, int D, int sm_count
   return SparseWs(N, Hkv, n_sel, D, sm_count).end;
 }
 
-cudaError_t launch_attn_shared(const SharedParams &shared, int sm_count, cudaStream_t stream) {
-  SharedParams p = shared;
-  const SharedWs ws(p.a.T, p.a.Hq, p.a.D, sm_count);
-  char *w = reinterpret_cast<char *>(p.a.ws);
+cudaError_t launch_attn_shared(const SharedParams &p, int sm_count, cudaStream_t stream) {
+  AttnParams a = p.a;
+  const SharedWs ws(a.T, a.Hq, a.D, sm_count);
+  char *w = reinterpret_cast<char *>(a.ws);
   PlanRec *rec = reinterpret_cast<PlanRec *>(w + ws.rec);
   int *info = reinterpret_cast<int *>(w + ws.info);
   cudaLaunchConfig_t cfg = pdl_config(dim3(1), dim3(kPlanThreads), 0, stream);
@@ -261,19 +297,19 @@ cudaError_t launch_attn_shared(const SharedParams &shared, int sm_count, cudaStr
   attach_pdl(cfg, attr);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, shared_plan_kernel, p, rec, info);
   if (e != cudaSuccess) return e;
-  p.a.slots = (long long)(ws.slots / sizeof(float));
-  p.a.plan.rec = rec;
-  p.a.plan.n = p.n_groups + p.a.B;
-  p.a.plan.info = info;
-  p.a.plan.rows = reinterpret_cast<float *>(w + ws.rows);
-  p.a.plan.stats = reinterpret_cast<float *>(w + ws.stats);
-  return p.a.D == 64 ? launch_t<64, kShared>(p.a, sm_count, stream) : launch_t<128, kShared>(p.a, sm_count, stream);
+  a.slots = kJoinFloats;
+  a.plan.info = info;
+  a.plan.rows = reinterpret_cast<float *>(w + ws.rows);
+  a.plan.stats = reinterpret_cast<float *>(w + ws.stats);
+  a.plan.part_ws[0] = p.n_groups > 0 ? reinterpret_cast<float *>(w) : nullptr;
+  a.plan.part_ws[1] = reinterpret_cast<float *>(w + ws.second);
+  return a.D == 64 ? launch_shared<64>(p, a, rec, sm_count, stream) : launch_shared<128>(p, a, rec, sm_count, stream);
 }
 
-cudaError_t launch_attn_sparse(const SparseParams &sparse, int sm_count, cudaStream_t stream) {
-  SparseParams p = sparse;
-  const SparseWs ws(p.a.T, p.a.Hkv, p.n_sel, p.a.D, sm_count);
-  char *w = reinterpret_cast<char *>(p.a.ws);
+cudaError_t launch_attn_sparse(const SparseParams &p, int sm_count, cudaStream_t stream) {
+  AttnParams a = p.a;
+  const SparseWs ws(a.T, a.Hkv, p.n_sel, a.D, sm_count);
+  char *w = reinterpret_cast<char *>(a.ws);
   PlanRec *rec = reinterpret_cast<PlanRec *>(w + ws.rec);
   int *list = reinterpret_cast<int *>(w + ws.list);
   unsigned long long *names = reinterpret_cast<unsigned long long *>(w + ws.names);
@@ -286,18 +322,18 @@ cudaError_t launch_attn_sparse(const SparseParams &sparse, int sm_count, cudaStr
     if (e != cudaSuccess) return e;
     once.set(dev);
   }
-  const size_t smem = (size_t)((p.a.table_cols + 31) / 32) * 2 * sizeof(uint32_t);
-  cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)p.a.Hkv, (unsigned)p.a.B), dim3(kListThreads), smem, stream);
+  const size_t smem = (size_t)((a.table_cols + 31) / 32) * 2 * sizeof(uint32_t);
+  cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)a.Hkv, (unsigned)a.B), dim3(kListThreads), smem, stream);
   cudaLaunchAttribute attr[1];
   attach_pdl(cfg, attr);
   e = cudaLaunchKernelEx(&cfg, sparse_plan_kernel, p, rec, list, names);
   if (e != cudaSuccess) return e;
-  p.a.slots = (long long)(ws.slots / sizeof(float));
-  p.a.plan.rec = rec;
-  p.a.plan.n = p.a.B * p.a.Hkv;
-  p.a.plan.list = list;
-  p.a.plan.names = names;
-  return p.a.D == 64 ? launch_t<64, kSparse>(p.a, sm_count, stream) : launch_t<128, kSparse>(p.a, sm_count, stream);
+  a.slots = kJoinFloats;
+  a.plan.rec = rec;
+  a.plan.n = a.B * a.Hkv;
+  a.plan.list = list;
+  a.plan.names = names;
+  return a.D == 64 ? launch_sparse<64>(a, sm_count, stream) : launch_sparse<128>(a, sm_count, stream);
 }
 
 }  // namespace mxg
