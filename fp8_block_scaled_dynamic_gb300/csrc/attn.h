@@ -51,6 +51,7 @@ static_assert(sizeof(PlanRec) == 32, "read as two 16-byte words");
 struct Plan {
   const PlanRec *rec;
   int n;                            // records
+  const int *units;                 // of each record, zeros behind the last one (PlanUnits)
   const int *list;                  // sparse: page numbers
   const unsigned long long *names;  // sparse: the nodes that name a page, a bit each
   const int *info;                  // shared: of each node, how its parts are joined

@@ -53,15 +53,13 @@ struct FewSmem {
   using C = FewCfg<D, NR>;
   uint64_t kv_full[C::kSlots], kv_empty[C::kSlots], q_full[2], q_empty[2], s_full[2], p_ready[2], pv_done[2];
   uint64_t o_free[2], item_full[2], item_free[2], mma_done, stall;
-  unsigned long long sees[kAttnMaxNodes];  // of a node as a key: the rows that see it
-  unsigned long long seen[4];              // of a warp's keys: the rows that see one
-  // of a row: its reference m, -m in units of the exponent (infinite: none yet), four warps' maxima or sums
-  alignas(16) float ref[NR], neg[NR], part[4][NR];
+  unsigned long long seen[4];  // of a warp's keys: the rows that see one
+  // of a row: its reference m, -m in units of the exponent (infinite: none yet), a factor or at the end its sum
+  alignas(16) float ref[NR], neg[NR], fac[NR];
   uint32_t bad[2];  // rows whose accumulator is not finite
   uint32_t tmem;
   int abort_flag;
   Item<MODE> items[2];
-  Prefix pre;
 };
 
 // D fp32, A (N-major or not) and B K-major.
@@ -98,29 +96,30 @@ __device__ __forceinline__ void tmem_ld_rows(uint32_t at, uint32_t (&r)[NR]) {
   }
 }
 
-// A row of a part summed again by a warp, key by key: lane i has channels i, i + 32,
-// ... of the result.
+// A row of a part summed again by a warp, key by key; tmp: room for the row.
 template <int D, int MODE>
-__device__ __noinline__ void few_again(const AttnParams &p, const Item<MODE> it, int row, float ref, uint16_t *out,
-                                       float *part, float scale_by) {
-  constexpr int V = D / 32;
+__device__ __noinline__ void few_again(const AttnParams &p, const Item<MODE> it, int row, float ref, float *tmp, float *y) {
+  constexpr int V = D / 32;  // channels a lane, one after another
   constexpr unsigned kFull = 0xFFFFFFFFu;
   const int lane = threadIdx.x & 31, G = p.Hq / p.Hkv, node = row / G, shift = 31 - __clz(p.cache.page_size);
   const int tok = it.r0 + node, head = it.hk * G + row - node * G;
   const float c = p.scale * kLog2e;
   auto value = [](uint32_t x) { return __uint_as_float(x << 16); };
-  float q[V], y[V] = {};
+  float q[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) q[i] = value(p.q.ptr[(long long)(it.a0 + tok) * p.q.tok + head * p.q.head + i * 32 + lane]);
+  for (int i = 0; i < V; ++i) {
+    q[i] = value(p.q.ptr[(long long)(it.a0 + tok) * p.q.tok + head * p.q.head + lane * V + i]);
+    tmp[lane * V + i] = 0.0f;
+  }
   auto take = [&](const uint16_t *k, const uint16_t *v) {
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) s = fmaf(q[i], value(k[i * 32 + lane]), s);
+    for (int i = 0; i < V; ++i) s = fmaf(q[i], value(k[lane * V + i]), s);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
     const float w = __uint_as_float(pack_bf16x2(0.0f, ex2(fmaf(s, c, ref))) & 0xFFFF0000u);
 #pragma unroll
-    for (int i = 0; i < V; ++i) y[i] = fmaf(w, value(v[i * 32 + lane]), y[i]);
+    for (int i = 0; i < V; ++i) tmp[lane * V + i] = fmaf(w, value(v[lane * V + i]), tmp[lane * V + i]);
   };
   const long long list = list_of(it);
   const int *pages = MODE == kSparse ? p.plan.list : p.table;
@@ -139,10 +138,7 @@ __device__ __noinline__ void few_again(const AttnParams &p, const Item<MODE> it,
     }
   }
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    if (part) part[i * 32 + lane] = y[i];
-    else out[i * 32 + lane] = (uint16_t)pack_bf16x2(y[i] * scale_by, 0.0f);
-  }
+  for (int i = 0; i < V; ++i) y[i] = tmp[lane * V + i];
 }
 
 template <int D, int NR, int MODE>
@@ -371,11 +367,14 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     // --------------------------------------------------------------- items
     const bool few = seqs<MODE>(p) <= 32;
     Small<MODE> small;
-    if (few) small.read(p, TQ, lane, false);
-    else fill_prefix<MODE>(p, sm.pre, TQ, lane, false);
-    if (few) small.number(p, lane);
-    Walk<MODE> walk(few ? small.total : sm.pre.units[kBlocks], TQ);
-    Found found;
+    PlanUnits<MODE> units;
+    if (few) {
+      small.read(p, TQ, lane, false);
+      small.number(p, lane);
+    } else {
+      units.read(p, lane);
+    }
+    Walk<MODE> walk(few ? small.total : units.total, TQ);
     bool going_on = false;
     if (few) walk.choose_chunk(small);
     for (int k = 0;; ++k) {
@@ -384,9 +383,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       if (walk.chunk > 0 && k == 0) {
         last = walk.one_chunk(p, small, TQ, w);
       } else {
-        walk.next(p, TQ, w, [&](int &u, int &b) {
-          return few ? small.find(u, b) : find_seq<MODE>(p, sm.pre, TQ, u, b, found);
-        });
+        walk.next(p, TQ, w, [&](int &u, int &b) { return few ? small.find(u, b) : units.find(p, TQ, u, b); });
         if (w.t1 > w.t0 && w.part == 1)
           last = share_owner(share_begin(blockIdx.x + 1, walk.q, walk.r) + w.nct + (flags_of(w) & kHasNodes) - 1 - w.t1,
                              walk.q, walk.r);
@@ -419,111 +416,116 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     const int key = warp * 32 + lane;  // of a tile; at the end the channel
     const float c = p.scale * kLog2e;
     const int page_shift = 31 - __clz(p.cache.page_size);
+    // The weights' tiles are also where values are turned from a thread a key (or
+    // channel) to a warp a row: when no product reads them.
+    float *const turn = reinterpret_cast<float *>(smem_raw + (p_smem - base));  // [row][128]
     uint32_t tile = 0, rn = 0;
     bool ok = true;
     if (p.debug_stall) ok = warp_wait(&sm.stall, 0, ctl);
     for (int k = 0;; ++k) {
       const bool there = ok && next_item(k);
       if (any_of_four(!there)) break;
-      const int nt = it.t1 - it.t0, rows = it.cnt[0] * G;
+      const int nt = it.t1 - it.t0, cnt = it.cnt[0], rows = cnt * G;
       const unsigned long long mine = rows >= 64 ? ~0ull : (1ull << rows) - 1ull;  // the item's rows
       const unsigned long long group = G >= 64 ? ~0ull : (1ull << G) - 1ull;
       const bool lists = MODE == kSparse && (flags_of(it) & kLists);
-      // the rows of the nodes in a word
-      auto rows_of = [&](unsigned long long nodes) {
-        unsigned long long r = 0;
-        nodes >>= it.r0;
-        for (int i = 0; i < it.cnt[0]; ++i)
-          if (nodes >> i & 1ull) r |= group << (i * G);
-        return r;
-      };
-      unsigned long long who = 0;  // lists: the nodes that name this key's page, of the next tile
+      // lists: the nodes that name this key's page, of the next tile
+      unsigned long long who = 0;
       auto names_of = [&](int j) {
         const int t = j * kKeys + key;
         if (lists && j < it.nct && t < it.ctx) who = __ldg(p.plan.names + list_of(it) + (t >> page_shift));
       };
       names_of(it.t0);
-      if (it.t1 > it.nct && key < kAttnMaxNodes) {
-        // of this node as a key: the rows that see it
-        unsigned long long r = 0;
-        if (key < it.n)
-          for (int i = 0; i < it.cnt[0]; ++i)
-            if (__ldg(p.mask + it.a0 + it.r0 + i) >> key & 1ull) r |= group << (i * G);
-        sm.sees[key] = r;
+      unsigned long long word[2] = {0, 0};  // mask words of nodes lane and lane + 32 of the item
+      if (it.t1 > it.nct) {
+        if (lane < cnt) word[0] = __ldg(p.mask + it.a0 + it.r0 + lane);
+        if (NR > 32 && lane + 32 < cnt) word[1] = __ldg(p.mask + it.a0 + it.r0 + lane + 32);
       }
+      // the rows that see this key of tile j
+      auto rows_that_see = [&](int j) {
+        unsigned long long r = 0;
+        if (j >= it.nct) {
+          for (int i = 0; i < cnt; ++i) {
+            const unsigned long long w = __shfl_sync(kFull, i < 32 ? word[0] : word[1], i & 31);
+            if (key < it.n && (w >> (key & 63) & 1ull)) r |= group << (i * G);
+          }
+        } else if (j * kKeys + key < it.ctx) {
+          if (!lists) return mine;
+          const unsigned long long w = who >> it.r0;
+          for (int i = 0; i < cnt; ++i)
+            if (w >> i & 1ull) r |= group << (i * G);
+        }
+        return r;
+      };
       float l[NR];
 #pragma unroll
       for (int r = 0; r < NR; ++r) l[r] = 0.0f;
-      if (key < NR) sm.ref[key] = -INFINITY, sm.neg[key] = INFINITY;
       if (key < 2) sm.bad[key] = 0;
       unsigned long long saw = 0;
-      sync_four();
       for (int i = 0; i < nt; ++i) {
         const int j = it.t0 + i;
         const uint32_t t = tile + i, sb = t & 1, ph = (t >> 1) & 1;
         const uint32_t v_at = rn + (nt > 1 ? 2 : 1) + i + min(i, max(nt - 2, 0));  // the v tile's place in the ring
-        unsigned long long see;
-        if (j >= it.nct) see = key < kAttnMaxNodes ? sm.sees[key] : 0ull;
-        else if (j * kKeys + key >= it.ctx) see = 0ull;
-        else see = lists ? rows_of(who) : mine;
+        const unsigned long long see = rows_that_see(j);
         names_of(j + 1);
         saw |= see;
         if (!warp_wait(&sm.s_full[sb], ph, ctl)) ok = false;
         tc_fence_after();
         uint32_t s[NR];
         tmem_ld_rows<NR>(tmem + lanes + sb * 64, s);
-        if (see != ~0ull) {
+        const uint32_t see2[2] = {(uint32_t)see, (uint32_t)(see >> 32)};
 #pragma unroll
-          for (int r = 0; r < NR; ++r)
-            if (!((r < 32 ? (uint32_t)see >> (r & 31) : (uint32_t)(see >> 32) >> (r & 31)) & 1u)) s[r] = 0xFF800000u;
-        }
+        for (int r = 0; r < NR; ++r)
+          if (!(see2[r / 32] >> (r & 31) & 1u)) s[r] = 0xFF800000u;
         // is a score past its row's reference?  (no reference yet: any is)
-        bool past = false;
+        bool past = true;
+        if (i > 0) {
+          float most = -INFINITY;
 #pragma unroll
-        for (int r = 0; r < NR; ++r) past |= fmaf(__uint_as_float(s[r]), c, sm.neg[r]) > kFallBehind;
-        if (any_of_four(past)) {
-          // the rows' maxima: this warp's keys, then all
+          for (int r = 0; r < NR; ++r) most = fmaxf(most, fmaf(__uint_as_float(s[r]), c, sm.neg[r]));
+          past = any_of_four(most > kFallBehind);
+        }
+        if (past) {
+          const uint32_t prev = t - 1;
+          if (i > 0 && !warp_wait(&sm.pv_done[prev & 1], (prev >> 1) & 1, ctl)) ok = false;
+          // the rows' maxima, a warp a row; a first one is the reference, a later one moves it
 #pragma unroll
-          for (int r = 0; r < NR; ++r) {
-            float m = __uint_as_float(s[r]);
+          for (int r = 0; r < NR; ++r) turn[r * 128 + key] = __uint_as_float(s[r]);
+          sync_four();
+#pragma unroll 1
+          for (int r = warp; r < NR; r += 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(turn + r * 128 + lane * 4);
+            float top = fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w));
 #pragma unroll
-            for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, x));
-            if (lane == (r & 31)) sm.part[warp][r] = m;
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+            if (lane == 0) {
+              const float old = i > 0 ? sm.ref[r] : -INFINITY, m = fmaxf(old, top);
+              sm.fac[r] = m == old ? 1.0f : old == -INFINITY ? 0.0f : ex2((old - m) * c);
+              sm.ref[r] = m;
+              sm.neg[r] = -m * c;  // (infinite: none yet)
+            }
           }
           sync_four();
-          // a first maximum is the reference; later ones move it, the sums and the accumulator
-          const uint32_t prev = t - 1;
           if (i > 0) {
-            if (!warp_wait(&sm.pv_done[prev & 1], (prev >> 1) & 1, ctl)) ok = false;
             tc_fence_after();
-            uint32_t o[NR];
             const uint32_t at = tmem + lanes + 128 + (k & 1) * 64;
-            tmem_ld_rows<NR>(at, o);
+#pragma unroll 1
+            for (int x = 0; x < NR; x += 16) {
+              uint32_t o[16];
+              tmem_ld16(at + x, o);
+              tmem_ld_wait();
 #pragma unroll
-            for (int r = 0; r < NR; ++r) {
-              const float old = sm.ref[r];
-              const float top = fmaxf(fmaxf(sm.part[0][r], sm.part[1][r]), fmaxf(sm.part[2][r], sm.part[3][r]));
-              const float f = top > old ? (old == -INFINITY ? 0.0f : ex2((old - top) * c)) : 1.0f;
-              l[r] *= f;
-              // (an accumulator without a reference yet is zero, or what an unseen NaN made of it)
-              o[r] = __float_as_uint(__uint_as_float(o[r]) * f);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * sm.fac[x + e]);
+              tmem_st16(at + x, o);
             }
-#pragma unroll
-            for (int x = 0; x < NR / 16; ++x) tmem_st16(at + x * 16, o + x * 16);
             tmem_st_wait();
             tc_fence_before();
+#pragma unroll
+            for (int r = 0; r < NR; ++r) l[r] *= sm.fac[r];
           }
-          sync_four();
-          if (key < NR) {
-            const float m =
-                fmaxf(sm.ref[key], fmaxf(fmaxf(sm.part[0][key], sm.part[1][key]), fmaxf(sm.part[2][key], sm.part[3][key])));
-            sm.ref[key] = m;
-            sm.neg[key] = -m * c;
-          }
-          sync_four();
         }
-        // weights, rounded to bf16, for the product (the tile before the last has been multiplied by now:
-        // its scores' buffer is in use again) and as sums
+        // Weights, rounded to bf16, for the product and as sums.  (The tile that had
+        // these two buffers before has been multiplied: the scores came after it.)
         const uint32_t to = p_smem + sb * C::kP + (key >> 6) * (NR * 128) + (key & 7) * 2, unit = (key >> 3) & 7;
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
@@ -546,81 +548,76 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         warp_arrive(&sm.p_ready[sb], lane);
       }
       ok = __all_sync(kFull, ok);
-      // sums over the keys, rows seen
-#pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        float x = l[r];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
-        if (lane == (r & 31)) sm.part[warp][r] = x;
-      }
-      const uint32_t saw_lo = __reduce_or_sync(kFull, (uint32_t)saw), saw_hi = __reduce_or_sync(kFull, (uint32_t)(saw >> 32));
-      if (lane == 0) sm.seen[warp] = (unsigned long long)saw_hi << 32 | saw_lo;
       const uint32_t lastt = tile + nt - 1;
       if (!warp_wait(&sm.pv_done[lastt & 1], (lastt >> 1) & 1, ctl)) ok = false;
       tc_fence_after();
-      uint32_t o[NR];
-      tmem_ld_rows<NR>(tmem + lanes + 128 + (k & 1) * 64, o);
-      tc_fence_before();
-      warp_arrive(&sm.o_free[k & 1], lane);
-      if (key < D) {
-        uint32_t bad[2] = {0, 0};
+      // the rows' sums over the keys, a warp a row
+      const uint32_t saw_lo = __reduce_or_sync(kFull, (uint32_t)saw), saw_hi = __reduce_or_sync(kFull, (uint32_t)(saw >> 32));
+      if (lane == 0) sm.seen[warp] = (unsigned long long)saw_hi << 32 | saw_lo;
 #pragma unroll
-        for (int r = 0; r < NR; ++r) bad[r / 32] |= (o[r] & 0x7F800000u) == 0x7F800000u ? 1u << (r & 31) : 0u;
-        bad[0] &= (uint32_t)mine;
-        bad[1] &= (uint32_t)(mine >> 32);
-        if (bad[0]) atomicOr(&sm.bad[0], bad[0]);
-        if (bad[1]) atomicOr(&sm.bad[1], bad[1]);
-      }
+      for (int r = 0; r < NR; ++r) turn[r * 128 + key] = l[r];
       sync_four();
       const unsigned long long seen = sm.seen[0] | sm.seen[1] | sm.seen[2] | sm.seen[3];
-      const unsigned long long bad = (unsigned long long)sm.bad[1] << 32 | sm.bad[0];
-      // the rows of this item, in memory: of nodes, a head each
-      const float *slot_m = nullptr;
-      float *slot = nullptr;
-      if (it.part == 0 || it.part == 1) {
-        slot = p.ws + p.slots + ((long long)blockIdx.x * 2 + it.part) * Cfg<D, MODE>::kSlotFloats;
-        slot_m = slot + D * kRowsT;
-      }
-      const long long row0 = (long long)(it.a0 + it.r0) * p.Hq + it.hk * G;  // shared: first row's place
-      const long long kind = MODE == kShared ? (long long)(flags_of(it) & kHasNodes) * p.T * p.Hq : 0;
-      int node = 0, head = 0;
+#pragma unroll 1
+      for (int r = warp; r < rows; r += 4) {
+        const float4 x = *reinterpret_cast<const float4 *>(turn + r * 128 + lane * 4);
+        float sum = (x.x + x.y) + (x.z + x.w);
 #pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        if (r >= rows) break;
-        const float total = (sm.part[0][r] + sm.part[1][r]) + (sm.part[2][r] + sm.part[3][r]), m = sm.ref[r];
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+        if (lane == 0) sm.fac[r] = sum;
+      }
+      sync_four();
+      // results turned the same way
+      const uint32_t at = tmem + lanes + 128 + (k & 1) * 64;
+#pragma unroll 1
+      for (int x = 0; x < rows; x += 16) {
+        uint32_t o[16];
+        tmem_ld16(at + x, o);
+        tmem_ld_wait();
+        uint32_t bad = 0;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          turn[(x + e) * 128 + key] = __uint_as_float(o[e]);
+          bad |= (o[e] & 0x7F800000u) == 0x7F800000u ? 1u << e : 0u;
+        }
+        bad = key < D ? (bad << (x & 31)) & (uint32_t)(mine >> (x & 32)) : 0u;
+        if (bad) atomicOr(&sm.bad[x >> 5], bad);
+      }
+      tc_fence_before();
+      warp_arrive(&sm.o_free[k & 1], lane);
+      sync_four();
+      const unsigned long long bad = (unsigned long long)sm.bad[1] << 32 | sm.bad[0];
+      // rows in memory, a warp a row: results, or parts in the CTA's slot or the rows' own places
+      float *const slot = p.ws + p.slots + ((long long)blockIdx.x * 2 + (it.part & 1)) * Cfg<D, MODE>::kSlotFloats;
+      const long long kind = MODE == kShared ? (long long)(flags_of(it) & kHasNodes) * p.T * p.Hq : 0;
+#pragma unroll 1
+      for (int r = warp; r < rows; r += 4) {
+        constexpr int V = D / 32;
+        const int nd = r / G, hd = it.hk * G + r - nd * G, node = it.a0 + it.r0 + nd;
+        const float total = sm.fac[r], m = sm.ref[r];
         const bool any = seen >> r & 1ull;
-        const long long at = row0 + (long long)node * p.Hq + head;
+        float y[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) y[e] = turn[r * 128 + lane * V + e];
+        if (bad >> r & 1ull)  // what another row's NaN has spoilt is summed again
+          few_again<D, MODE>(p, it, r, m == -INFINITY ? 0.0f : -m * c, turn + r * 128, y);
         if (it.part < 0) {
-          if (key < D) {
-            const float y = __uint_as_float(o[r]) * (1.0f / total);
-            p.out.ptr[(long long)(it.a0 + it.r0 + node) * p.out.tok + (it.hk * G + head) * p.out.head + key] =
-                any ? (uint16_t)pack_bf16x2(y, 0.0f) : (uint16_t)0;
-          }
+          const float inv = 1.0f / total;
+          uint16_t *out = p.out.ptr + (long long)node * p.out.tok + hd * p.out.head + lane * V;
+#pragma unroll
+          for (int e = 0; e < V; e += 2)
+            reinterpret_cast<uint32_t *>(out)[e / 2] = any ? pack_bf16x2(y[e] * inv, y[e + 1] * inv) : 0u;
         } else {
-          float *to = it.part == 2 ? p.plan.rows + (kind + at) * D : slot + r * D;
-          float *stat = it.part == 2 ? p.plan.stats + (kind + at) * 2 : const_cast<float *>(slot_m) + r;
-          if (key < D) to[key] = __uint_as_float(o[r]);
-          if (key == (r & 127)) {
+          const long long own = kind + (long long)node * p.Hq + hd;
+          float *to = it.part == 2 ? p.plan.rows + own * D : slot + r * D;
+          float *stat = it.part == 2 ? p.plan.stats + own * 2 : slot + D * kRowsT + r;
+#pragma unroll
+          for (int e = 0; e < V; ++e) to[lane * V + e] = y[e];
+          if (lane == 0) {
             // (a sum of 0 says that the row sees nothing of the part)
             stat[0] = m;
             stat[it.part == 2 ? 1 : kRowsT] = !any ? 0.0f : m == -INFINITY ? 1.0f : total;
           }
-        }
-        if (++head == G) head = 0, ++node;
-      }
-      // rows to be summed again, after what was stored of them: a warp each
-      if (bad) {
-        sync_four();
-        for (int r = warp; r < rows; r += 4) {
-          if (!(bad >> r & 1ull)) continue;
-          const int nd = r / G, hd = r - nd * G;
-          const float total = (sm.part[0][r] + sm.part[1][r]) + (sm.part[2][r] + sm.part[3][r]), m = sm.ref[r];
-          const long long at = row0 + (long long)nd * p.Hq + hd;
-          uint16_t *out = p.out.ptr + (long long)(it.a0 + it.r0 + nd) * p.out.tok + (it.hk * G + hd) * p.out.head;
-          float *part = it.part < 0 ? nullptr : it.part == 2 ? p.plan.rows + (kind + at) * D : slot + r * D;
-          if (it.part >= 0 || (seen >> r & 1ull))
-            few_again<D, MODE>(p, it, r, m == -INFINITY ? 0.0f : -m * c, out, part, 1.0f / total);
         }
       }
       tile += nt;

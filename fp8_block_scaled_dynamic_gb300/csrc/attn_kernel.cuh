@@ -286,6 +286,51 @@ __device__ __forceinline__ Seq find_seq(const AttnParams &p, const Prefix &pre, 
   return s;
 }
 
+// The records of a plan by their units, of which the plan kernel has left a list:
+// a lane adds up `per` of them, zeros behind the last one.  (Worked out from the
+// records themselves, 256 of them took a CTA 4 us before its first load.)
+__host__ __device__ __forceinline__ int units_per_lane(int records) { return ((records + 31) / 32 + 3) / 4 * 4; }
+template <int MODE>
+struct PlanUnits {
+  int before, sum, total;  // of this lane's records
+  int b = -1, base = 0, units = 0;  // the record found last
+  __device__ __forceinline__ void read(const AttnParams &p, int lane) {
+    const int per = units_per_lane(p.plan.n);
+    const int4 *at = reinterpret_cast<const int4 *>(p.plan.units + lane * per);
+    sum = 0;
+#pragma unroll 4
+    for (int i = 0; i < per / 4; ++i) {
+      const int4 x = __ldg(at + i);
+      sum += (x.x + x.y) + (x.z + x.w);
+    }
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    before = incl - sum;
+    total = __shfl_sync(0xFFFFFFFFu, incl, 31);
+  }
+  // the record of unit u (u < total), and u's number in it
+  __device__ __forceinline__ Seq find(const AttnParams &p, int tq2, int &u, int &of) {
+    if (b < 0 || u < base) {
+      const int lane = __ffs(__ballot_sync(0xFFFFFFFFu, u >= before && u < before + sum)) - 1;
+      base = __shfl_sync(0xFFFFFFFFu, before, lane);
+      b = lane * units_per_lane(p.plan.n);
+      units = __ldg(p.plan.units + b);
+    }
+    while (u >= base + units) {
+      base += units;
+      units = __ldg(p.plan.units + ++b);
+    }
+    of = b;
+    u -= base;
+    int running = 0;
+    return seq_of<MODE>(p, raw_seq<MODE>(p, b), tq2, running, nullptr);
+  }
+};
+
 struct PlainItem {
   int b, hk;
   int a0, n;   // the sequence's first token (node) and count
@@ -1099,11 +1144,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // -------------------------------------------------------------- items
       const bool few = seqs<MODE>(p) <= 32;
       Small<MODE> small;
+      PlanUnits<MODE> planned_units;
       if (few) small.read(p, 2 * TQ, lane, blockIdx.x == 0);
+      else if constexpr (planned(MODE)) planned_units.read(p, lane);
       else fill_prefix<MODE>(p, sm.pre, 2 * TQ, lane, blockIdx.x == 0);
       const int span = !TREE && few ? small.choose_span(p, TQ, lane) : 2 * TQ;
       if (few) small.number(p, lane);
-      Walk<MODE> walk(few ? small.total : sm.pre.units[kBlocks], span);
+      Walk<MODE> walk(few ? small.total : planned(MODE) ? planned_units.total : sm.pre.units[kBlocks], span);
       Found found;
       bool going_on = false;
       if constexpr (TREE) {
@@ -1117,7 +1164,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             last = walk.one_chunk(p, small, TQ, w);
           } else {
             walk.next(p, TQ, w, [&](int &u, int &b) {
-              return few ? small.find(u, b) : find_seq<MODE>(p, sm.pre, 2 * TQ, u, b, found);
+              if (few) return small.find(u, b);
+              if constexpr (planned(MODE)) return planned_units.find(p, 2 * TQ, u, b);
+              else return find_seq<MODE>(p, sm.pre, 2 * TQ, u, b, found);
             });
             if (w.t1 > w.t0 && w.part == 1)
               last = share_owner(share_begin(blockIdx.x + 1, walk.q, walk.r) + w.nct + (flags_of(w) & kHasNodes) - 1 - w.t1,

@@ -55,14 +55,27 @@ constexpr int kPlanThreads = 1024;
 constexpr int kPlanOwn = kAttnMaxSeqs / kPlanThreads;  // sequences (groups) of a thread, one after another
 
 // One block: the sequences' nodes and contexts, the groups' sequences and
-// prefixes, all within their bounds, as records.
-__global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedParams p, PlanRec *rec, int *info) {
+// prefixes, all within their bounds, as records and their units (key tiles of row
+// groups of span[0] nodes of a group, span[1] of a sequence).
+struct SharedLists {
+  PlanRec *rec;
+  int *info, *units[2], span[2];
+};
+__global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedParams p, const SharedLists to) {
   __shared__ int s_a0[kAttnMaxSeqs + 1], s_len[kAttnMaxSeqs], s_warp[kPlanThreads / 32];
   __shared__ uint16_t s_g[kAttnMaxSeqs + 1];
   pdl_trigger();
   pdl_wait();
   const AttnParams &a = p.a;
-  const int B = a.B, page = a.cache.page_size, limit = a.table_cols * page, tid = threadIdx.x;
+  const int B = a.B, page = a.cache.page_size, limit = a.table_cols * page, tid = threadIdx.x, ng = p.n_groups;
+  // (what is read one after another below is on its way at once)
+  if (tid * 32 <= B) {
+    prefetch_l1(a.cu + tid * 32);
+    if (tid * 32 < B) prefetch_l1(a.ctx + tid * 32);
+    if (ng > 0 && tid * 32 <= ng) prefetch_l1(p.groups + tid * 32);
+    if (tid * 32 < ng) prefetch_l1(p.prefix + tid * 32);
+  }
+  PlanRec *rec = to.rec;
   bool bad = false;
   // offsets never fall: a thread's own ones, then what comes before them
   auto clamp_offsets = [&](const int *at, int n, int most, auto put) {
@@ -78,7 +91,6 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     }
   };
   clamp_offsets(a.cu, B + 1, a.T, [&](int b, int x) { s_a0[b] = x; });
-  const int ng = p.n_groups;
   if (ng > 0) clamp_offsets(p.groups, ng + 1, B, [&](int g, int x) { s_g[g] = (uint16_t)x; });
   for (int g = tid; g < ng; g += kPlanThreads) s_len[g] = limit;
   __syncthreads();
@@ -119,7 +131,9 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     r.list = (long long)g0 * a.ld_table;
     r.flags = kJoined;
     rec[g] = r;
+    to.units[0][g] = (r.n + to.span[0] - 1) / to.span[0] * a.Hkv * ((len + kKeys - 1) / kKeys);
   }
+  for (int g = ng + tid; g < 32 * units_per_lane(ng); g += kPlanThreads) to.units[0][g] = 0;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kPlanOwn; ++i) {
@@ -134,10 +148,12 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     r.list = (long long)b * a.ld_table + len / page;
     r.flags = kHasNodes | (len > 0 ? kJoined : 0);
     rec[ng + b] = r;
-    for (int x = a0; x < a1; ++x) info[x] = x - a0 < kAttnMaxNodes ? len > 0 : -1;
+    to.units[1][b] = (r.n + to.span[1] - 1) / to.span[1] * a.Hkv * ((r.ctx + kKeys - 1) / kKeys + 1);
+    for (int x = a0; x < a1; ++x) to.info[x] = x - a0 < kAttnMaxNodes ? len > 0 : -1;
   }
-  for (int x = tid; x < s_a0[0]; x += kPlanThreads) info[x] = -1;
-  for (int x = s_a0[B] + tid; x < a.T; x += kPlanThreads) info[x] = -1;
+  for (int b = B + tid; b < 32 * units_per_lane(B); b += kPlanThreads) to.units[1][b] = 0;
+  for (int x = tid; x < s_a0[0]; x += kPlanThreads) to.info[x] = -1;
+  for (int x = s_a0[B] + tid; x < a.T; x += kPlanThreads) to.info[x] = -1;
   if (bad && a.status) atomicOr(a.status, kBadIndex);
 }
 
@@ -147,20 +163,28 @@ constexpr int kListThreads = 128;
 // A block a sequence and kv head: the pages that any of its nodes names, in
 // order (a bit a logical page in shared memory, a page's place is the number of bits
 // below its own), and for several nodes the word of those that name it.
-__global__ void __launch_bounds__(kListThreads) sparse_plan_kernel(const SparseParams p, PlanRec *rec, int *list,
-                                                                   unsigned long long *names) {
+struct SparseLists {
+  PlanRec *rec;
+  int *list, *units, span;
+  unsigned long long *names;
+};
+__global__ void __launch_bounds__(kListThreads) sparse_plan_kernel(const SparseParams p, const SparseLists to) {
   extern __shared__ uint32_t s_bits[];  // words of bits, then the number of bits before each
   __shared__ int s_warp[kListThreads / 32];
   pdl_trigger();
   const AttnParams &a = p.a;
   const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, page = a.cache.page_size;
+  int *list = to.list;
+  unsigned long long *names = to.names;
   pdl_wait();
+  if (tid * 32 < a.table_cols) prefetch_l1(a.table + (long long)b * a.ld_table + tid * 32);  // (read at the end)
+  const int c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1), raw = __ldg(a.ctx + b);
   int top = 0;
   for (int i = tid; i <= b; i += kListThreads) top = max(top, min(max(__ldg(a.cu + i), 0), a.T));
   int a0;
   scan_block<kListThreads>(top, 0, s_warp, Max(), &a0);
-  const int c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1), a1 = max(min(max(c1, 0), a.T), a0);
-  const int n = min(a1 - a0, kAttnMaxNodes), raw = __ldg(a.ctx + b), ctx = min(max(raw, 0), a.table_cols * page);
+  const int a1 = max(min(max(c1, 0), a.T), a0);
+  const int n = min(a1 - a0, kAttnMaxNodes), ctx = min(max(raw, 0), a.table_cols * page);
   bool bad = h == 0 && (c0 != a0 || c1 != a1 || a1 - a0 > kAttnMaxNodes || raw != ctx);
   const int P = (ctx + page - 1) / page, W = (P + 31) / 32, total = n * p.n_sel;
   uint32_t *s_before = s_bits + W;
@@ -209,7 +233,12 @@ __global__ void __launch_bounds__(kListThreads) sparse_plan_kernel(const SparseP
     r.hk = h;
     r.list = base;
     r.flags = kHasNodes | (n > 1 ? kLists : 0);
-    rec[b * a.Hkv + h] = r;
+    to.rec[b * a.Hkv + h] = r;
+    to.units[b * a.Hkv + h] = (n + to.span - 1) / to.span * ((r.ctx + kKeys - 1) / kKeys + 1);
+  }
+  if (b == (int)gridDim.y - 1 && h == (int)gridDim.x - 1) {
+    const int V = a.B * a.Hkv;
+    for (int i = V + tid; i < 32 * units_per_lane(V); i += kListThreads) to.units[i] = 0;
   }
   if (bad && a.status) atomicOr(a.status, kBadIndex);
 }
@@ -223,51 +252,61 @@ size_t slots_bytes(int D, int sm_count) {
 
 // Byte offsets; a launch's items, which the join reads, come first, then its slots.
 struct SharedWs {
-  size_t slots, second, rec, info, rows, stats, end;
+  size_t slots, second, rec, units, info, rows, stats, end;
   SharedWs(long long N, int Hq, int D, int sm_count) {
     slots = kJoinFloats * sizeof(float);
     second = slots + slots_bytes(D, sm_count);
     rec = 2 * second;
-    info = rec + 2 * kAttnMaxSeqs * sizeof(PlanRec);
+    units = rec + 2 * kAttnMaxSeqs * sizeof(PlanRec);
+    info = units + 2 * (kAttnMaxSeqs + 128) * sizeof(int);
     rows = round256(info + N * sizeof(int));
     stats = rows + (size_t)(2 * N * Hq) * D * sizeof(float);
     end = round256(stats + (size_t)(2 * N * Hq) * 2 * sizeof(float));
   }
 };
 struct SparseWs {
-  size_t slots, rec, names, list, end;
+  size_t slots, rec, units, names, list, end;
   SparseWs(long long N, int Hkv, int n_sel, int D, int sm_count) {
     slots = kJoinFloats * sizeof(float);
     rec = slots + slots_bytes(D, sm_count);
-    names = rec + (size_t)kAttnMaxSeqs * Hkv * sizeof(PlanRec);
+    units = rec + (size_t)kAttnMaxSeqs * Hkv * sizeof(PlanRec);
+    names = units + ((size_t)kAttnMaxSeqs * Hkv + 128) * sizeof(int);
     list = names + (size_t)(N * Hkv) * n_sel * sizeof(unsigned long long);
     end = round256(list + (size_t)(N * Hkv) * n_sel * sizeof(int));
   }
 };
 
 // Sequences' rows of a kv head: where an average sequence's fit, the kernel of few
-// rows, with as many as it needs; else the one of full tiles.
+// rows (16, 32 or 64 of them), else the one of full tiles (0).
+int few_rows(const AttnParams &p) {
+  const long long rows = ((long long)p.T + p.B - 1) / p.B * (p.Hq / p.Hkv);
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 0;
+}
+int span_of(const AttnParams &p, int rows) { return (rows ? rows : 2 * kRowsT) / (p.Hq / p.Hkv); }
+
 template <int D, int MODE>
 cudaError_t launch_rows(const AttnParams &p, int sm_count, cudaStream_t stream) {
-  const int G = p.Hq / p.Hkv;
-  const long long rows = ((long long)p.T + p.B - 1) / p.B * G;
-  if (rows <= 16) return launch_few<D, 16, MODE>(p, sm_count, stream);
-  if (rows <= 32) return launch_few<D, 32, MODE>(p, sm_count, stream);
-  if (rows <= 64) return launch_few<D, 64, MODE>(p, sm_count, stream);
+  switch (few_rows(p)) {
+    case 16: return launch_few<D, 16, MODE>(p, sm_count, stream);
+    case 32: return launch_few<D, 32, MODE>(p, sm_count, stream);
+    case 64: return launch_few<D, 64, MODE>(p, sm_count, stream);
+  }
   return launch_t<D, MODE>(p, sm_count, stream);
 }
 
 template <int D>
-cudaError_t launch_shared(const SharedParams &p, AttnParams a, PlanRec *rec, int sm_count, cudaStream_t stream) {
+cudaError_t launch_shared(const SharedParams &p, AttnParams a, const SharedLists &to, int sm_count, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   if (p.n_groups > 0) {
     a.ws = a.plan.part_ws[0];
-    a.plan.rec = rec;
+    a.plan.rec = to.rec;
+    a.plan.units = to.units[0];
     a.plan.n = p.n_groups;
     if ((e = launch_t<D, kShared>(a, sm_count, stream)) != cudaSuccess) return e;
   }
   a.ws = a.plan.part_ws[1];
-  a.plan.rec = rec + p.n_groups;
+  a.plan.rec = to.rec + p.n_groups;
+  a.plan.units = to.units[1];
   a.plan.n = a.B;
   if ((e = launch_rows<D, kShared>(a, sm_count, stream)) != cudaSuccess) return e;
   return launch_join<D, kShared>(a, sm_count, stream);
@@ -290,29 +329,37 @@ cudaError_t launch_attn_shared(const SharedParams &p, int sm_count, cudaStream_t
   AttnParams a = p.a;
   const SharedWs ws(a.T, a.Hq, a.D, sm_count);
   char *w = reinterpret_cast<char *>(a.ws);
-  PlanRec *rec = reinterpret_cast<PlanRec *>(w + ws.rec);
-  int *info = reinterpret_cast<int *>(w + ws.info);
+  SharedLists to = {};
+  to.rec = reinterpret_cast<PlanRec *>(w + ws.rec);
+  to.info = reinterpret_cast<int *>(w + ws.info);
+  to.units[0] = reinterpret_cast<int *>(w + ws.units);
+  to.units[1] = to.units[0] + kAttnMaxSeqs + 128;
+  to.span[0] = span_of(a, 0);
+  to.span[1] = span_of(a, few_rows(a));
   cudaLaunchConfig_t cfg = pdl_config(dim3(1), dim3(kPlanThreads), 0, stream);
   cudaLaunchAttribute attr[1];
   attach_pdl(cfg, attr);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, shared_plan_kernel, p, rec, info);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, shared_plan_kernel, p, to);
   if (e != cudaSuccess) return e;
   a.slots = kJoinFloats;
-  a.plan.info = info;
+  a.plan.info = to.info;
   a.plan.rows = reinterpret_cast<float *>(w + ws.rows);
   a.plan.stats = reinterpret_cast<float *>(w + ws.stats);
   a.plan.part_ws[0] = p.n_groups > 0 ? reinterpret_cast<float *>(w) : nullptr;
   a.plan.part_ws[1] = reinterpret_cast<float *>(w + ws.second);
-  return a.D == 64 ? launch_shared<64>(p, a, rec, sm_count, stream) : launch_shared<128>(p, a, rec, sm_count, stream);
+  return a.D == 64 ? launch_shared<64>(p, a, to, sm_count, stream) : launch_shared<128>(p, a, to, sm_count, stream);
 }
 
 cudaError_t launch_attn_sparse(const SparseParams &p, int sm_count, cudaStream_t stream) {
   AttnParams a = p.a;
   const SparseWs ws(a.T, a.Hkv, p.n_sel, a.D, sm_count);
   char *w = reinterpret_cast<char *>(a.ws);
-  PlanRec *rec = reinterpret_cast<PlanRec *>(w + ws.rec);
-  int *list = reinterpret_cast<int *>(w + ws.list);
-  unsigned long long *names = reinterpret_cast<unsigned long long *>(w + ws.names);
+  SparseLists to = {};
+  to.rec = reinterpret_cast<PlanRec *>(w + ws.rec);
+  to.list = reinterpret_cast<int *>(w + ws.list);
+  to.units = reinterpret_cast<int *>(w + ws.units);
+  to.names = reinterpret_cast<unsigned long long *>(w + ws.names);
+  to.span = span_of(a, few_rows(a));
   static DeviceOnce once;
   int dev = -1;
   cudaError_t e = cudaGetDevice(&dev);
@@ -326,13 +373,14 @@ cudaError_t launch_attn_sparse(const SparseParams &p, int sm_count, cudaStream_t
   cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)a.Hkv, (unsigned)a.B), dim3(kListThreads), smem, stream);
   cudaLaunchAttribute attr[1];
   attach_pdl(cfg, attr);
-  e = cudaLaunchKernelEx(&cfg, sparse_plan_kernel, p, rec, list, names);
+  e = cudaLaunchKernelEx(&cfg, sparse_plan_kernel, p, to);
   if (e != cudaSuccess) return e;
   a.slots = kJoinFloats;
-  a.plan.rec = rec;
+  a.plan.rec = to.rec;
+  a.plan.units = to.units;
   a.plan.n = a.B * a.Hkv;
-  a.plan.list = list;
-  a.plan.names = names;
+  a.plan.list = to.list;
+  a.plan.names = to.names;
   return a.D == 64 ? launch_sparse<64>(a, sm_count, stream) : launch_sparse<128>(a, sm_count, stream);
 }
 
