@@ -22,7 +22,8 @@
 // accumulator that is not finite; such a row is summed again, key by key, from what it
 // sees.
 //
-// Warps: 0-3 softmax, 4 the MMAs, 5 the loads, 6 the items.
+// Warps: four of softmax for each 16 rows (a thread with 64 rows had 24 KB of code a
+// tile, whose fetching took 3.4 us), then one each for MMAs, loads and items.
 // TMEM columns: two buffers of scores, two of results (of items in turn), 64 each.
 #pragma once
 #include "attn_kernel.cuh"
@@ -30,7 +31,7 @@
 namespace mxg {
 namespace {
 
-constexpr int kFewThreads = 224;
+constexpr int kFewRows = 16;  // rows of a softmax thread
 constexpr int kFewHead = 6 * 1024;  // bytes of shared memory before the tiles
 
 template <int D, int NR>
@@ -38,25 +39,26 @@ struct FewCfg {
   static constexpr int kHalves = D / 64;
   static constexpr int kTile = kKeys * D * 2;
   static constexpr int kQ = NR * 128 * kHalves;  // a q tile: NR rows of 128 bytes for each 64 channels
-  static constexpr int kP = NR * 256;            // weights: NR rows of 128 bytes for each 64 keys
+  static constexpr int kGroups = NR / kFewRows;  // of four softmax warps
+  static constexpr int kThreads = 128 * kGroups + 96;
+  static constexpr int kP = kFewRows * 256;      // weights of a group: its rows of 128 bytes for each 64 keys
+  static constexpr int kW = 2 * kGroups * kP;    // two buffers of them a group
   static constexpr int kEnd = 16 * 1024;         // (with D = 64 the lanes past the channels read on behind a v tile)
-  static constexpr int kFit = (227 * 1024 - kFewHead - 2 * kQ - (2 * kP < kEnd ? kEnd : 2 * kP)) / kTile;
+  static constexpr int kFit = (227 * 1024 - kFewHead - 2 * kQ - (kW < kEnd ? kEnd : kW)) / kTile;
   static constexpr int kSlots = kFit < 12 ? kFit : 12;
-  static constexpr int kSmem = kFewHead + kSlots * kTile + 2 * kQ + (2 * kP < kEnd ? kEnd : 2 * kP);
+  static constexpr int kSmem = kFewHead + kSlots * kTile + 2 * kQ + (kW < kEnd ? kEnd : kW);
   static_assert(kSlots >= 4 && kQ % 1024 == 0 && kP % 1024 == 0, "shared memory");
 };
-
-constexpr int kFewReaders = 6;  // warps 0 to 5
 
 template <int D, int NR, int MODE>
 struct FewSmem {
   using C = FewCfg<D, NR>;
   uint64_t kv_full[C::kSlots], kv_empty[C::kSlots], q_full[2], q_empty[2], s_full[2], p_ready[2], pv_done[2];
   uint64_t o_free[2], item_full[2], item_free[2], mma_done, stall;
-  unsigned long long seen[4];  // of a warp's keys: the rows that see one
   // of a row: its reference m, -m in units of the exponent (infinite: none yet), a factor or at the end its sum
   alignas(16) float ref[NR], neg[NR], fac[NR];
-  uint32_t bad[2];  // rows whose accumulator is not finite
+  uint32_t seen[C::kGroups][4];  // of a warp's keys: the rows of its group that see one
+  uint32_t bad[C::kGroups];      // rows whose accumulator is not finite
   uint32_t tmem;
   int abort_flag;
   Item<MODE> items[2];
@@ -67,33 +69,25 @@ __host__ __device__ constexpr uint32_t idesc_few(int n, bool a_mn) {
   return idesc_bf16(128, n, false) | ((a_mn ? 1u : 0u) << 15);
 }
 
-__device__ __forceinline__ bool any_of_four(bool x) {  // of the softmax warps' threads
+// Common barriers of a group's four warps.
+__device__ __forceinline__ bool any_of_four(int group, bool x) {
   uint32_t r;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbarrier.cta.red.or.pred q, %1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)x)
+      : "r"(1 + group), "r"((uint32_t)x)
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void sync_four() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void sync_four(int group) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + group) : "memory"); }
 __device__ __forceinline__ void st_shared_u16(uint32_t to, uint32_t v) {
   asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"((uint16_t)v) : "memory");
 }
-template <int NR>
-__device__ __forceinline__ void tmem_ld_rows(uint32_t at, uint32_t (&r)[NR]) {
-  if constexpr (NR == 16) {
-    tmem_ld16(at, r);
-    tmem_ld_wait();
+__device__ __forceinline__ void tmem_ld_rows(uint32_t at, uint32_t (&r)[kFewRows]) {
+  tmem_ld16(at, r);
+  tmem_ld_wait();
 #pragma unroll
-    for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));
-  } else {
-#pragma unroll
-    for (int i = 0; i < NR / 32; ++i) tmem_ld32(at + i * 32, reinterpret_cast<uint32_t(&)[32]>(r[i * 32]));
-    tmem_ld_wait();
-#pragma unroll
-    for (int i = 0; i < NR / 32; ++i) tmem_landed(reinterpret_cast<uint32_t(&)[32]>(r[i * 32]));
-  }
+  for (int i = 0; i < kFewRows; ++i) asm volatile("" : "+r"(r[i]));
 }
 
 // A row of a part summed again by a warp, key by key; tmp: room for the row.
@@ -142,12 +136,12 @@ __device__ __noinline__ void few_again(const AttnParams &p, const Item<MODE> it,
 }
 
 template <int D, int NR, int MODE>
-__global__ void __launch_bounds__(kFewThreads, 1)
+__global__ void __launch_bounds__(FewCfg<D, NR>::kThreads, 1)
     attn_few_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKC,
                     const __grid_constant__ CUtensorMap tmVC, const __grid_constant__ AttnParams p) {
   using C = FewCfg<D, NR>;
-  constexpr int S = C::kSlots;
+  constexpr int S = C::kSlots, kSoft = 4 * C::kGroups;  // softmax warps
   constexpr unsigned kFull = 0xFFFFFFFFu;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   static_assert(sizeof(FewSmem<D, NR, MODE>) <= kFewHead, "shared memory head");
@@ -174,22 +168,22 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       mbar_init(smem_addr(&sm.q_full[i]), 1);
       mbar_init(smem_addr(&sm.q_empty[i]), 1);
       mbar_init(smem_addr(&sm.s_full[i]), 1);
-      mbar_init(smem_addr(&sm.p_ready[i]), 4);
+      mbar_init(smem_addr(&sm.p_ready[i]), kSoft);
       mbar_init(smem_addr(&sm.pv_done[i]), 1);
-      mbar_init(smem_addr(&sm.o_free[i]), 4);
+      mbar_init(smem_addr(&sm.o_free[i]), kSoft);
       mbar_init(smem_addr(&sm.item_full[i]), 1);
-      mbar_init(smem_addr(&sm.item_free[i]), kFewReaders);
+      mbar_init(smem_addr(&sm.item_free[i]), kSoft + 2);
     }
     mbar_init(smem_addr(&sm.mma_done), 1);
     mbar_init(smem_addr(&sm.stall), 1);
     sm.abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 4) {
+  if (warp == kSoft) {
     tmem_alloc(smem_addr(&sm.tmem), 256);
     tmem_relinquish();
   }
-  if (warp == 5 && lane == 0) {
+  if (warp == kSoft + 1 && lane == 0) {
     prefetch_tmap(&tmQ);
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
@@ -210,7 +204,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   };
   auto done_item = [&](int k) { warp_arrive(&sm.item_free[k & 1], lane); };
 
-  if (warp == 5) {
+  if (warp == kSoft + 1) {
     // --------------------------------------------------------------- loads
     uint32_t n = 0, nq = 0, slot = 0, turn = 0;
     bool ok = true;
@@ -289,11 +283,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     // nothing may land in shared memory once the CTA is gone (a timeout)
     for (uint32_t k = n > S ? n - S : 0; k < n; ++k) drain(&sm.kv_full[k % S], (k / S) & 1, p.timeout_ns);
     for (uint32_t k = nq > 2 ? nq - 2 : 0; k < nq; ++k) drain(&sm.q_full[k & 1], (k >> 1) & 1, p.timeout_ns);
-  } else if (warp == 4) {
+  } else if (warp == kSoft) {
     // ---------------------------------------------------------------- MMAs
     const bool el = elect_one();
     const uint32_t tm = uniform(tmem), qb = uniform(q_smem), kb = uniform(kv_smem), pb = uniform(p_smem);
-    constexpr uint32_t kIdQK = idesc_few(NR, false), kIdPV = idesc_few(NR, true);
+    constexpr uint32_t kIdQK = idesc_few(NR, false), kIdPV = idesc_few(kFewRows, true);
     uint32_t rn = 0, tile = 0;  // tiles of the ring, tiles of keys so far
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t parity) { return lane_wait(bar, parity, ctl); };
@@ -335,14 +329,17 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         const uint64_t vd = vdesc(rn), kd = kdesc(rn + 1);
         const uint32_t t = tile + i;
         if (el) {
-          const uint64_t pd = sdesc_kmajor_sw128(pb + (t & 1) * C::kP);
+          const uint64_t pd = sdesc_kmajor_sw128(pb + (t & 1) * C::kP);  // the first group's
           ok = ring(rn) && (i > 0 || k < 2 || wait(&sm.o_free[k & 1], ((k >> 1) - 1) & 1)) &&
                wait(&sm.p_ready[t & 1], (t >> 1) & 1);
           if (ok) {
             tc_fence_after();
 #pragma unroll
             for (int x = 0; x < 8; ++x)
-              mma_bf16_ss(o, vd + x * 128, pd + (x >> 2) * (NR * 8) + (x & 3) * 2, kIdPV, i > 0 || x > 0);
+#pragma unroll
+              for (int g = 0; g < C::kGroups; ++g)
+                mma_bf16_ss(o + g * kFewRows, vd + x * 128, pd + g * (2 * C::kP / 16) + (x >> 2) * (kFewRows * 8) + (x & 3) * 2,
+                            kIdPV, i > 0 || x > 0);
             tc_commit(smem_addr(&sm.pv_done[t & 1]));
             tc_commit(smem_addr(&sm.kv_empty[rn % S]));
             if (i + 1 == nt) tc_commit(smem_addr(&sm.q_empty[k & 1]));
@@ -363,7 +360,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       drain(&sm.mma_done, 0, p.timeout_ns);
     }
     __syncwarp();
-  } else if (warp == 6) {
+  } else if (warp == kSoft + 2) {
     // --------------------------------------------------------------- items
     const bool few = seqs<MODE>(p) <= 32;
     Small<MODE> small;
@@ -411,23 +408,28 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   } else {
     // ------------------------------------------------------------- softmax
     // (A wait that runs out lets a warp go on without what it waited for, to the
-    // next common barrier: the four warps leave together.)
-    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-    const int key = warp * 32 + lane;  // of a tile; at the end the channel
+    // next common barrier: a group's four warps leave together.)
+    constexpr int R = kFewRows;
+    const int grp = warp >> 2, wi = warp & 3, first = grp * R;  // the group's first row
+    const uint32_t lanes = (uint32_t)(wi * 32) << 16;
+    const int key = wi * 32 + lane;  // of a tile; at the end the channel
     const float c = p.scale * kLog2e;
     const int page_shift = 31 - __clz(p.cache.page_size);
-    // The weights' tiles are also where values are turned from a thread a key (or
-    // channel) to a warp a row: when no product reads them.
-    float *const turn = reinterpret_cast<float *>(smem_raw + (p_smem - base));  // [row][128]
+    // A group's weights' tiles are also where its values are turned from a thread a
+    // key (or channel) to a warp a row: when no product reads them.
+    const uint32_t p_mine = p_smem + grp * 2 * C::kP;
+    float *const turn = reinterpret_cast<float *>(smem_raw + (p_mine - base));  // [row][128]
+    float *const ref = sm.ref + first, *const neg = sm.neg + first, *const fac = sm.fac + first;
     uint32_t tile = 0, rn = 0;
     bool ok = true;
     if (p.debug_stall) ok = warp_wait(&sm.stall, 0, ctl);
     for (int k = 0;; ++k) {
       const bool there = ok && next_item(k);
-      if (any_of_four(!there)) break;
-      const int nt = it.t1 - it.t0, cnt = it.cnt[0], rows = cnt * G;
-      const unsigned long long mine = rows >= 64 ? ~0ull : (1ull << rows) - 1ull;  // the item's rows
+      if (any_of_four(grp, !there)) break;
+      const int nt = it.t1 - it.t0, cnt = it.cnt[0], rows = min(max(cnt * G - first, 0), R);  // this group's rows
+      const unsigned long long all = cnt * G >= 64 ? ~0ull : (1ull << cnt * G) - 1ull;
       const unsigned long long group = G >= 64 ? ~0ull : (1ull << G) - 1ull;
+      const uint32_t mine = (1u << rows) - 1u;
       const bool lists = MODE == kSparse && (flags_of(it) & kLists);
       // lists: the nodes that name this key's page, of the next tile
       unsigned long long who = 0;
@@ -450,92 +452,90 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             if (key < it.n && (w >> (key & 63) & 1ull)) r |= group << (i * G);
           }
         } else if (j * kKeys + key < it.ctx) {
-          if (!lists) return mine;
+          if (!lists) return all;
           const unsigned long long w = who >> it.r0;
           for (int i = 0; i < cnt; ++i)
             if (w >> i & 1ull) r |= group << (i * G);
         }
         return r;
       };
-      float l[NR];
+      float l[R];
 #pragma unroll
-      for (int r = 0; r < NR; ++r) l[r] = 0.0f;
-      if (key < 2) sm.bad[key] = 0;
-      unsigned long long saw = 0;
+      for (int r = 0; r < R; ++r) l[r] = 0.0f;
+      if (key == 0) sm.bad[grp] = 0;
+      uint32_t saw = 0;
       for (int i = 0; i < nt; ++i) {
         const int j = it.t0 + i;
         const uint32_t t = tile + i, sb = t & 1, ph = (t >> 1) & 1;
-        const uint32_t v_at = rn + (nt > 1 ? 2 : 1) + i + min(i, max(nt - 2, 0));  // the v tile's place in the ring
-        const unsigned long long see = rows_that_see(j);
+        const unsigned long long every = rows_that_see(j);
+        const uint32_t see = (uint32_t)(every >> first) & 0xFFFFu;
         names_of(j + 1);
         saw |= see;
         if (!warp_wait(&sm.s_full[sb], ph, ctl)) ok = false;
         tc_fence_after();
-        uint32_t s[NR];
-        tmem_ld_rows<NR>(tmem + lanes + sb * 64, s);
-        const uint32_t see2[2] = {(uint32_t)see, (uint32_t)(see >> 32)};
+        uint32_t s[R];
+        tmem_ld_rows(tmem + lanes + sb * 64 + first, s);
 #pragma unroll
-        for (int r = 0; r < NR; ++r)
-          if (!(see2[r / 32] >> (r & 31) & 1u)) s[r] = 0xFF800000u;
+        for (int r = 0; r < R; ++r)
+          if (!(see >> r & 1u)) s[r] = 0xFF800000u;
         // is a score past its row's reference?  (no reference yet: any is)
         bool past = true;
         if (i > 0) {
           float most = -INFINITY;
 #pragma unroll
-          for (int r = 0; r < NR; ++r) most = fmaxf(most, fmaf(__uint_as_float(s[r]), c, sm.neg[r]));
-          past = any_of_four(most > kFallBehind);
+          for (int r = 0; r < R; ++r) most = fmaxf(most, fmaf(__uint_as_float(s[r]), c, neg[r]));
+          past = any_of_four(grp, most > kFallBehind);
         }
         if (past) {
           const uint32_t prev = t - 1;
           if (i > 0 && !warp_wait(&sm.pv_done[prev & 1], (prev >> 1) & 1, ctl)) ok = false;
           // the rows' maxima, a warp a row; a first one is the reference, a later one moves it
 #pragma unroll
-          for (int r = 0; r < NR; ++r) turn[r * 128 + key] = __uint_as_float(s[r]);
-          sync_four();
-#pragma unroll 1
-          for (int r = warp; r < NR; r += 4) {
+          for (int r = 0; r < R; ++r) turn[r * 128 + key] = __uint_as_float(s[r]);
+          sync_four(grp);
+#pragma unroll
+          for (int r = wi; r < R; r += 4) {
             const float4 x = *reinterpret_cast<const float4 *>(turn + r * 128 + lane * 4);
             float top = fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w));
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
             if (lane == 0) {
-              const float old = i > 0 ? sm.ref[r] : -INFINITY, m = fmaxf(old, top);
-              sm.fac[r] = m == old ? 1.0f : old == -INFINITY ? 0.0f : ex2((old - m) * c);
-              sm.ref[r] = m;
-              sm.neg[r] = -m * c;  // (infinite: none yet)
+              const float old = i > 0 ? ref[r] : -INFINITY, m = fmaxf(old, top);
+              fac[r] = m == old ? 1.0f : old == -INFINITY ? 0.0f : ex2((old - m) * c);
+              ref[r] = m;
+              neg[r] = -m * c;  // (infinite: none yet)
             }
           }
-          sync_four();
+          sync_four(grp);
           if (i > 0) {
             tc_fence_after();
-            const uint32_t at = tmem + lanes + 128 + (k & 1) * 64;
-#pragma unroll 1
-            for (int x = 0; x < NR; x += 16) {
-              uint32_t o[16];
-              tmem_ld16(at + x, o);
-              tmem_ld_wait();
+            const uint32_t at = tmem + lanes + 128 + (k & 1) * 64 + first;
+            uint32_t o[R];
+            tmem_ld_rows(at, o);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * sm.fac[x + e]);
-              tmem_st16(at + x, o);
+            for (int r = 0; r < R; ++r) {
+              const float f = fac[r];
+              l[r] *= f;
+              o[r] = __float_as_uint(__uint_as_float(o[r]) * f);
             }
+            tmem_st16(at, o);
             tmem_st_wait();
             tc_fence_before();
-#pragma unroll
-            for (int r = 0; r < NR; ++r) l[r] *= sm.fac[r];
           }
         }
         // Weights, rounded to bf16, for the product and as sums.  (The tile that had
         // these two buffers before has been multiplied: the scores came after it.)
-        const uint32_t to = p_smem + sb * C::kP + (key >> 6) * (NR * 128) + (key & 7) * 2, unit = (key >> 3) & 7;
+        const uint32_t to = p_mine + sb * C::kP + (key >> 6) * (R * 128) + (key & 7) * 2, unit = (key >> 3) & 7;
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          const float neg = sm.neg[r];
-          const uint32_t w = pack_bf16x2(ex2(fmaf(__uint_as_float(s[r]), c, neg == INFINITY ? 0.0f : neg)), 0.0f);
+        for (int r = 0; r < R; ++r) {
+          const float n = neg[r];
+          const uint32_t w = pack_bf16x2(ex2(fmaf(__uint_as_float(s[r]), c, n == INFINITY ? 0.0f : n)), 0.0f);
           l[r] += __uint_as_float(w << 16);
           st_shared_u16(to + r * 128 + ((unit ^ (r & 7)) << 4), w);
         }
-        if (see == 0ull) {
+        if (grp == 0 && every == 0ull) {
           // no row sees this key: its v is made zero
+          const uint32_t v_at = rn + (nt > 1 ? 2 : 1) + i + min(i, max(nt - 2, 0));  // the v tile's place in the ring
           if (!mbar_wait_quick(smem_addr(&sm.kv_full[v_at % S]), (v_at / S) & 1, ctl)) ok = false;
           const uint32_t v = kv_smem + (v_at % S) * C::kTile + key * 128;
 #pragma unroll
@@ -552,55 +552,49 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       if (!warp_wait(&sm.pv_done[lastt & 1], (lastt >> 1) & 1, ctl)) ok = false;
       tc_fence_after();
       // the rows' sums over the keys, a warp a row
-      const uint32_t saw_lo = __reduce_or_sync(kFull, (uint32_t)saw), saw_hi = __reduce_or_sync(kFull, (uint32_t)(saw >> 32));
-      if (lane == 0) sm.seen[warp] = (unsigned long long)saw_hi << 32 | saw_lo;
+      saw = __reduce_or_sync(kFull, saw);
+      if (lane == 0) sm.seen[grp][wi] = saw;
 #pragma unroll
-      for (int r = 0; r < NR; ++r) turn[r * 128 + key] = l[r];
-      sync_four();
-      const unsigned long long seen = sm.seen[0] | sm.seen[1] | sm.seen[2] | sm.seen[3];
-#pragma unroll 1
-      for (int r = warp; r < rows; r += 4) {
+      for (int r = 0; r < R; ++r) turn[r * 128 + key] = l[r];
+      uint32_t o[R];
+      tmem_ld_rows(tmem + lanes + 128 + (k & 1) * 64 + first, o);
+      tc_fence_before();
+      warp_arrive(&sm.o_free[k & 1], lane);
+      uint32_t bad = 0;
+#pragma unroll
+      for (int r = 0; r < R; ++r) bad |= (o[r] & 0x7F800000u) == 0x7F800000u ? 1u << r : 0u;
+      bad = key < D ? bad & mine : 0u;
+      if (bad) atomicOr(&sm.bad[grp], bad);
+      sync_four(grp);
+      const uint32_t seen = sm.seen[grp][0] | sm.seen[grp][1] | sm.seen[grp][2] | sm.seen[grp][3];
+      bad = sm.bad[grp];
+#pragma unroll
+      for (int r = wi; r < R; r += 4) {
         const float4 x = *reinterpret_cast<const float4 *>(turn + r * 128 + lane * 4);
         float sum = (x.x + x.y) + (x.z + x.w);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-        if (lane == 0) sm.fac[r] = sum;
+        for (int o2 = 16; o2 > 0; o2 >>= 1) sum += __shfl_xor_sync(kFull, sum, o2);
+        if (lane == 0) fac[r] = sum;
       }
-      sync_four();
+      sync_four(grp);
       // results turned the same way
-      const uint32_t at = tmem + lanes + 128 + (k & 1) * 64;
-#pragma unroll 1
-      for (int x = 0; x < rows; x += 16) {
-        uint32_t o[16];
-        tmem_ld16(at + x, o);
-        tmem_ld_wait();
-        uint32_t bad = 0;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          turn[(x + e) * 128 + key] = __uint_as_float(o[e]);
-          bad |= (o[e] & 0x7F800000u) == 0x7F800000u ? 1u << e : 0u;
-        }
-        bad = key < D ? (bad << (x & 31)) & (uint32_t)(mine >> (x & 32)) : 0u;
-        if (bad) atomicOr(&sm.bad[x >> 5], bad);
-      }
-      tc_fence_before();
-      warp_arrive(&sm.o_free[k & 1], lane);
-      sync_four();
-      const unsigned long long bad = (unsigned long long)sm.bad[1] << 32 | sm.bad[0];
+      for (int r = 0; r < R; ++r) turn[r * 128 + key] = __uint_as_float(o[r]);
+      sync_four(grp);
       // rows in memory, a warp a row: results, or parts in the CTA's slot or the rows' own places
       float *const slot = p.ws + p.slots + ((long long)blockIdx.x * 2 + (it.part & 1)) * Cfg<D, MODE>::kSlotFloats;
       const long long kind = MODE == kShared ? (long long)(flags_of(it) & kHasNodes) * p.T * p.Hq : 0;
 #pragma unroll 1
-      for (int r = warp; r < rows; r += 4) {
+      for (int r = wi; r < rows; r += 4) {
         constexpr int V = D / 32;
-        const int nd = r / G, hd = it.hk * G + r - nd * G, node = it.a0 + it.r0 + nd;
-        const float total = sm.fac[r], m = sm.ref[r];
-        const bool any = seen >> r & 1ull;
+        const int row = first + r, nd = row / G, hd = it.hk * G + row - nd * G, node = it.a0 + it.r0 + nd;
+        const float total = fac[r], m = ref[r];
+        const bool any = seen >> r & 1u;
         float y[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) y[e] = turn[r * 128 + lane * V + e];
-        if (bad >> r & 1ull)  // what another row's NaN has spoilt is summed again
-          few_again<D, MODE>(p, it, r, m == -INFINITY ? 0.0f : -m * c, turn + r * 128, y);
+        if (bad >> r & 1u)  // what another row's NaN has spoilt is summed again
+          few_again<D, MODE>(p, it, row, m == -INFINITY ? 0.0f : -m * c, turn + r * 128, y);
         if (it.part < 0) {
           const float inv = 1.0f / total;
           uint16_t *out = p.out.ptr + (long long)node * p.out.tok + hd * p.out.head + lane * V;
@@ -609,8 +603,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             reinterpret_cast<uint32_t *>(out)[e / 2] = any ? pack_bf16x2(y[e] * inv, y[e + 1] * inv) : 0u;
         } else {
           const long long own = kind + (long long)node * p.Hq + hd;
-          float *to = it.part == 2 ? p.plan.rows + own * D : slot + r * D;
-          float *stat = it.part == 2 ? p.plan.stats + own * 2 : slot + D * kRowsT + r;
+          float *to = it.part == 2 ? p.plan.rows + own * D : slot + row * D;
+          float *stat = it.part == 2 ? p.plan.stats + own * 2 : slot + D * kRowsT + row;
 #pragma unroll
           for (int e = 0; e < V; ++e) to[lane * V + e] = y[e];
           if (lane == 0) {
@@ -628,7 +622,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 4) {
+  if (warp == kSoft) {
     tc_fence_after();
     tmem_dealloc(tmem, 256);
   }
@@ -652,7 +646,7 @@ cudaError_t launch_few(const AttnParams &p, int sm_count, cudaStream_t stream) {
       !heads_map(&v, p.v, p.Hkv, p.T, D, 1, kAttnMaxNodes) || !cache_maps(&kc, &vc, p))
     return cudaErrorInvalidValue;
   const int ctas = sm_count < kMaxCtas ? sm_count : kMaxCtas;
-  cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)ctas), dim3(kFewThreads), C::kSmem, stream);
+  cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)ctas), dim3(C::kThreads), C::kSmem, stream);
   cudaLaunchAttribute attr[1];
   attach_pdl(cfg, attr);
   return cudaLaunchKernelEx(&cfg, kern, q, k, v, kc, vc, p);
