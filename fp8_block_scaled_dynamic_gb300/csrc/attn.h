@@ -57,6 +57,7 @@ struct Plan {
   const int *info;                  // shared: of each node, how its parts are joined
   float *rows, *stats;              // shared: parts of whole rows (prefix, own): sums, references and weights
   float *part_ws[2];                // shared: the two launches' items and slots
+  bool beside;                      // shared: the launch may run beside the one before it
 };
 
 struct AttnParams {

@@ -11,10 +11,12 @@
 // takes a warp 0.3 us of instructions where a thread a row took 1.6, and so an item of
 // a few tiles, whose parts follow one another, a third of the time.
 //
-// One pass with a reference a row, as there: it is the first tile's maximum and is
-// moved only when a score is past it by 2^8 (one vote a tile; the maxima themselves
-// are taken when it is).  Weights are rounded to bf16 and summed as rounded, so that
-// what one key's rounding adds above it also adds below.
+// One pass with a reference a row, as there.  It need not be near the maximum: weights
+// have fp32's and bf16's range of exponents, and a reference that some key of the row
+// has is never above it.  So the first key's score serves where all rows see it (else
+// the first tile's maximum, 0.9 us more), and it is moved to the maximum only when a
+// weight is past 2^60 (one vote a tile).  Weights are rounded to bf16 and summed as
+// rounded, so that what one key's rounding adds above it also adds below.
 //
 // Rows see different keys: a key has a word of the rows that see it (mask words for
 // nodes, a page's word for lists).  A key that no row sees has its v set to zero in
@@ -50,13 +52,16 @@ struct FewCfg {
   static_assert(kSlots >= 4 && kQ % 1024 == 0 && kP % 1024 == 0, "shared memory");
 };
 
+constexpr float kFewPast = 0x1p60f;  // a weight above this moves the reference
+
 template <int D, int NR, int MODE>
 struct FewSmem {
   using C = FewCfg<D, NR>;
   uint64_t kv_full[C::kSlots], kv_empty[C::kSlots], q_full[2], q_empty[2], s_full[2], p_ready[2], pv_done[2];
   uint64_t o_free[2], item_full[2], item_free[2], mma_done, stall;
-  // of a row: its reference m, -m in units of the exponent (infinite: none yet), a factor or at the end its sum
+  // of a row: its reference m, -m in units of the exponent (infinite: none yet), what the sums are scaled by
   alignas(16) float ref[NR], neg[NR], fac[NR];
+  float part[C::kGroups][4][kFewRows];  // of a group's warps: the rows' maxima or sums over their keys
   uint32_t seen[C::kGroups][4];  // of a warp's keys: the rows of its group that see one
   uint32_t bad[C::kGroups];      // rows whose accumulator is not finite
   uint32_t tmem;
@@ -88,6 +93,22 @@ __device__ __forceinline__ void tmem_ld_rows(uint32_t at, uint32_t (&r)[kFewRows
   tmem_ld_wait();
 #pragma unroll
   for (int i = 0; i < kFewRows; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// The lanes' values of 16 rows joined by op over a warp: lane i gets row few_row(i).
+__device__ __forceinline__ int few_row(int lane) {
+  return (lane >> 4 & 1) * 8 + (lane >> 3 & 1) * 4 + (lane >> 2 & 1) * 2 + (lane >> 1 & 1);
+}
+template <class Op>
+__device__ __forceinline__ float over_lanes(float (&v)[kFewRows], int lane, Op op) {
+#pragma unroll
+  for (int half = 8, bit = 16; half > 0; half >>= 1, bit >>= 1)
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float keep = lane & bit ? v[i + half] : v[i], send = lane & bit ? v[i] : v[i + half];
+      v[i] = op(keep, __shfl_xor_sync(0xFFFFFFFFu, send, bit));
+    }
+  return op(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], 1));
 }
 
 // A row of a part summed again by a warp, key by key; tmp: room for the row.
@@ -159,6 +180,10 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.Hq / p.Hkv, TQ = NR / G;  // (the host sees to G <= NR)
   pdl_trigger();
+  // (attn_shared: the launch before this one, which has not waited for anything else
+  // when it lets this one start, works on the prefixes: what this one reads is older,
+  // so it waits at its end, for the join's sake)
+  const bool late = MODE == kShared && p.plan.beside;
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
       mbar_init(smem_addr(&sm.kv_full[i]), 1);
@@ -195,7 +220,7 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&sm.tmem);
   const WaitCtl ctl{&sm.abort_flag, p.status, p.timeout_ns};
-  pdl_wait();
+  if (!late) pdl_wait();
   Item<MODE> it;
   auto next_item = [&](int k) {
     if (!warp_wait(&sm.item_full[k & 1], (k >> 1) & 1, ctl)) return false;
@@ -427,7 +452,6 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::kThreads, 1)
       const bool there = ok && next_item(k);
       if (any_of_four(grp, !there)) break;
       const int nt = it.t1 - it.t0, cnt = it.cnt[0], rows = min(max(cnt * G - first, 0), R);  // this group's rows
-      const unsigned long long all = cnt * G >= 64 ? ~0ull : (1ull << cnt * G) - 1ull;
       const unsigned long long group = G >= 64 ? ~0ull : (1ull << G) - 1ull;
       const uint32_t mine = (1u << rows) - 1u;
       const bool lists = MODE == kSparse && (flags_of(it) & kLists);
@@ -443,21 +467,34 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::kThreads, 1)
         if (lane < cnt) word[0] = __ldg(p.mask + it.a0 + it.r0 + lane);
         if (NR > 32 && lane + 32 < cnt) word[1] = __ldg(p.mask + it.a0 + it.r0 + lane + 32);
       }
-      // the rows that see this key of tile j
-      auto rows_that_see = [&](int j) {
-        unsigned long long r = 0;
+      unsigned long long words = word[0] | word[1];  // of all the item's nodes
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) words |= __shfl_xor_sync(kFull, words, x);
+      // The group's rows that see this key of tile j, and whether any row of the item
+      // does: rows of nodes n0 ... are G bits each, the first of them cut off.
+      const int n0 = first / G, cut = first - n0 * G, n1 = min((first + R - 1) / G + 1, cnt);
+      auto rows_that_see = [&](int j, bool &some) {
+        uint32_t r = 0;
+        some = false;
+        auto add = [&](int i, bool sees) {
+          const int at = (i - n0) * G - cut;  // (a node has at most 64 rows, and the first may begin below)
+          const unsigned long long bits = at >= 0 ? group << at : group >> -at;
+          r |= sees ? (uint32_t)bits & 0xFFFFu : 0u;
+        };
         if (j >= it.nct) {
-          for (int i = 0; i < cnt; ++i) {
+          some = key < it.n && (words >> (key & 63) & 1ull);
+          for (int i = n0; i < n1; ++i) {
             const unsigned long long w = __shfl_sync(kFull, i < 32 ? word[0] : word[1], i & 31);
-            if (key < it.n && (w >> (key & 63) & 1ull)) r |= group << (i * G);
+            add(i, key < it.n && (w >> (key & 63) & 1ull));
           }
         } else if (j * kKeys + key < it.ctx) {
-          if (!lists) return all;
+          some = true;
+          if (!lists) return mine;
           const unsigned long long w = who >> it.r0;
-          for (int i = 0; i < cnt; ++i)
-            if (w >> i & 1ull) r |= group << (i * G);
+          some = (w & (cnt >= 64 ? ~0ull : (1ull << cnt) - 1ull)) != 0ull;
+          for (int i = n0; i < n1; ++i) add(i, w >> i & 1ull);
         }
-        return r;
+        return r & mine;
       };
       float l[R];
 #pragma unroll
@@ -467,8 +504,8 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::kThreads, 1)
       for (int i = 0; i < nt; ++i) {
         const int j = it.t0 + i;
         const uint32_t t = tile + i, sb = t & 1, ph = (t >> 1) & 1;
-        const unsigned long long every = rows_that_see(j);
-        const uint32_t see = (uint32_t)(every >> first) & 0xFFFFu;
+        bool some;
+        const uint32_t see = rows_that_see(j, some);
         names_of(j + 1);
         saw |= see;
         if (!warp_wait(&sm.s_full[sb], ph, ctl)) ok = false;
@@ -478,33 +515,48 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::kThreads, 1)
 #pragma unroll
         for (int r = 0; r < R; ++r)
           if (!(see >> r & 1u)) s[r] = 0xFF800000u;
-        // is a score past its row's reference?  (no reference yet: any is)
-        bool past = true;
-        if (i > 0) {
-          float most = -INFINITY;
+        bool past = false;
+        if (i == 0) {
+          if (!lists && it.nct > it.t0) {
+            // all rows see the tile's first key
+            if (key == 0) {
 #pragma unroll
-          for (int r = 0; r < R; ++r) most = fmaxf(most, fmaf(__uint_as_float(s[r]), c, neg[r]));
-          past = any_of_four(grp, most > kFallBehind);
+              for (int r = 0; r < R; ++r) ref[r] = __uint_as_float(s[r]), neg[r] = -__uint_as_float(s[r]) * c;
+            }
+            sync_four(grp);
+          } else {
+            past = true;
+          }
         }
+        uint32_t w[R];  // weights, rounded to bf16
+        const auto weigh = [&]() {
+          float most = 0.0f;
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const float n = neg[r], x = ex2(fmaf(__uint_as_float(s[r]), c, n == INFINITY ? 0.0f : n));
+            most = fmaxf(most, n == INFINITY && s[r] != 0xFF800000u ? INFINITY : x);
+            w[r] = pack_bf16x2(x, 0.0f);
+          }
+          return most > kFewPast;
+        };
+        if (!past) past = any_of_four(grp, weigh());
         if (past) {
           const uint32_t prev = t - 1;
           if (i > 0 && !warp_wait(&sm.pv_done[prev & 1], (prev >> 1) & 1, ctl)) ok = false;
-          // the rows' maxima, a warp a row; a first one is the reference, a later one moves it
+          // the rows' maxima: a first one is the reference, a later one moves it
+          float x[R];
 #pragma unroll
-          for (int r = 0; r < R; ++r) turn[r * 128 + key] = __uint_as_float(s[r]);
+          for (int r = 0; r < R; ++r) x[r] = __uint_as_float(s[r]);
+          const float top = over_lanes(x, lane, [](float a, float b) { return fmaxf(a, b); });
+          if (!(lane & 1)) sm.part[grp][wi][few_row(lane)] = top;
           sync_four(grp);
-#pragma unroll
-          for (int r = wi; r < R; r += 4) {
-            const float4 x = *reinterpret_cast<const float4 *>(turn + r * 128 + lane * 4);
-            float top = fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w));
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-            if (lane == 0) {
-              const float old = i > 0 ? ref[r] : -INFINITY, m = fmaxf(old, top);
-              fac[r] = m == old ? 1.0f : old == -INFINITY ? 0.0f : ex2((old - m) * c);
-              ref[r] = m;
-              neg[r] = -m * c;  // (infinite: none yet)
-            }
+          if (key < R) {
+            const float(&m4)[4][R] = sm.part[grp];
+            const float old = i > 0 ? ref[key] : -INFINITY;
+            const float m = fmaxf(fmaxf(old, fmaxf(m4[0][key], m4[1][key])), fmaxf(m4[2][key], m4[3][key]));
+            fac[key] = m == old ? 1.0f : old == -INFINITY ? 0.0f : ex2((old - m) * c);
+            ref[key] = m;
+            neg[key] = -m * c;
           }
           sync_four(grp);
           if (i > 0) {
@@ -522,18 +574,17 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::kThreads, 1)
             tmem_st_wait();
             tc_fence_before();
           }
+          weigh();
         }
-        // Weights, rounded to bf16, for the product and as sums.  (The tile that had
-        // these two buffers before has been multiplied: the scores came after it.)
+        // For the product and as sums.  (The tile that had these two buffers before has
+        // been multiplied: the scores came after it.)
         const uint32_t to = p_mine + sb * C::kP + (key >> 6) * (R * 128) + (key & 7) * 2, unit = (key >> 3) & 7;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          const float n = neg[r];
-          const uint32_t w = pack_bf16x2(ex2(fmaf(__uint_as_float(s[r]), c, n == INFINITY ? 0.0f : n)), 0.0f);
-          l[r] += __uint_as_float(w << 16);
-          st_shared_u16(to + r * 128 + ((unit ^ (r & 7)) << 4), w);
+          l[r] += __uint_as_float(w[r] << 16);
+          st_shared_u16(to + r * 128 + ((unit ^ (r & 7)) << 4), w[r]);
         }
-        if (grp == 0 && every == 0ull) {
+        if (grp == 0 && !some) {
           // no row sees this key: its v is made zero
           const uint32_t v_at = rn + (nt > 1 ? 2 : 1) + i + min(i, max(nt - 2, 0));  // the v tile's place in the ring
           if (!mbar_wait_quick(smem_addr(&sm.kv_full[v_at % S]), (v_at / S) & 1, ctl)) ok = false;
@@ -551,36 +602,26 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::kThreads, 1)
       const uint32_t lastt = tile + nt - 1;
       if (!warp_wait(&sm.pv_done[lastt & 1], (lastt >> 1) & 1, ctl)) ok = false;
       tc_fence_after();
-      // the rows' sums over the keys, a warp a row
+      // the rows' sums over the keys; results turned to a warp a row
+      const float sum = over_lanes(l, lane, [](float a, float b) { return a + b; });
+      if (!(lane & 1)) sm.part[grp][wi][few_row(lane)] = sum;
       saw = __reduce_or_sync(kFull, saw);
       if (lane == 0) sm.seen[grp][wi] = saw;
-#pragma unroll
-      for (int r = 0; r < R; ++r) turn[r * 128 + key] = l[r];
       uint32_t o[R];
       tmem_ld_rows(tmem + lanes + 128 + (k & 1) * 64 + first, o);
       tc_fence_before();
       warp_arrive(&sm.o_free[k & 1], lane);
       uint32_t bad = 0;
 #pragma unroll
-      for (int r = 0; r < R; ++r) bad |= (o[r] & 0x7F800000u) == 0x7F800000u ? 1u << r : 0u;
+      for (int r = 0; r < R; ++r) {
+        turn[r * 128 + key] = __uint_as_float(o[r]);
+        bad |= (o[r] & 0x7F800000u) == 0x7F800000u ? 1u << r : 0u;
+      }
       bad = key < D ? bad & mine : 0u;
       if (bad) atomicOr(&sm.bad[grp], bad);
       sync_four(grp);
       const uint32_t seen = sm.seen[grp][0] | sm.seen[grp][1] | sm.seen[grp][2] | sm.seen[grp][3];
       bad = sm.bad[grp];
-#pragma unroll
-      for (int r = wi; r < R; r += 4) {
-        const float4 x = *reinterpret_cast<const float4 *>(turn + r * 128 + lane * 4);
-        float sum = (x.x + x.y) + (x.z + x.w);
-#pragma unroll
-        for (int o2 = 16; o2 > 0; o2 >>= 1) sum += __shfl_xor_sync(kFull, sum, o2);
-        if (lane == 0) fac[r] = sum;
-      }
-      sync_four(grp);
-      // results turned the same way
-#pragma unroll
-      for (int r = 0; r < R; ++r) turn[r * 128 + key] = __uint_as_float(o[r]);
-      sync_four(grp);
       // rows in memory, a warp a row: results, or parts in the CTA's slot or the rows' own places
       float *const slot = p.ws + p.slots + ((long long)blockIdx.x * 2 + (it.part & 1)) * Cfg<D, MODE>::kSlotFloats;
       const long long kind = MODE == kShared ? (long long)(flags_of(it) & kHasNodes) * p.T * p.Hq : 0;
@@ -588,7 +629,8 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::kThreads, 1)
       for (int r = wi; r < rows; r += 4) {
         constexpr int V = D / 32;
         const int row = first + r, nd = row / G, hd = it.hk * G + row - nd * G, node = it.a0 + it.r0 + nd;
-        const float total = fac[r], m = ref[r];
+        const float(&p4)[4][R] = sm.part[grp];
+        const float total = (p4[0][r] + p4[1][r]) + (p4[2][r] + p4[3][r]), m = ref[r];
         const bool any = seen >> r & 1u;
         float y[V];
 #pragma unroll
@@ -620,6 +662,7 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::kThreads, 1)
     }
   }
 
+  if (late) pdl_wait();
   tc_fence_before();
   __syncthreads();
   if (warp == kSoft) {

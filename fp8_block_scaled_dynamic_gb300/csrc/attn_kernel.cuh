@@ -747,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t q_smem = base + kHead, kv_smem = q_smem + 2 * C::kTile;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.Hq / p.Hkv, TQ = kRowsT / G;
-  pdl_trigger();
+  if (MODE != kShared) pdl_trigger();
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -794,6 +794,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&sm.tmem);
   const WaitCtl ctl{&sm.abort_flag, p.status, p.timeout_ns};
   pdl_wait();
+  if (MODE == kShared) pdl_trigger();  // (the plan is there for whoever starts now)
   Item<MODE> it;
   // item k of the CTA; false when there is none (or a wait ran out)
   auto next_item = [&](int k) {
@@ -1527,7 +1528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // rows of all of them over the grid's warps (a block an item and 8 rows, most
 // of them empty, took 6.5 us for a verify step); the references and sums of 32
 // parts come in one load a lane, the parts themselves 8 in flight.
-constexpr int kJoinWarps = 8, kJoinBlocksSm = 2;
+constexpr int kJoinWarps = 8, kJoinBlocksSm = 2, kJoinRowsBlocksSm = 3;
 // Up to eight parts of a row at once (zeros for those past n), V values a
 // lane.  One statement: left to itself, the compiler put each part's sums
 // before the next part's load, eight round trips to L2 instead of one.
@@ -1693,7 +1694,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, kJoinBlocksSm) attn_join_kern
 // with its list of items that went on and its slots; a list is in the order of (first
 // node, kv head), so the row's item is found by bisection.
 template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps, kJoinBlocksSm) attn_join_rows_kernel(const AttnParams p, int ctas) {
+__global__ void __launch_bounds__(32 * kJoinWarps, kJoinRowsBlocksSm) attn_join_rows_kernel(const AttnParams p, int ctas) {
   using C = Cfg<D, kShared>;
   constexpr int V = D / 32;
   constexpr unsigned kFull = 0xFFFFFFFFu;
@@ -1830,7 +1831,8 @@ int paged_ctas(int sm_count) { return sm_count < kMaxCtas ? sm_count : kMaxCtas;
 
 template <int D, int MODE>
 cudaError_t launch_join(const AttnParams &p, int sm_count, cudaStream_t stream) {
-  cudaLaunchConfig_t jc = pdl_config(dim3((unsigned)(kJoinBlocksSm * sm_count)), dim3(32 * kJoinWarps), 0, stream);
+  const int per_sm = MODE == kShared ? kJoinRowsBlocksSm : kJoinBlocksSm;
+  cudaLaunchConfig_t jc = pdl_config(dim3((unsigned)(per_sm * sm_count)), dim3(32 * kJoinWarps), 0, stream);
   cudaLaunchAttribute attr[1];
   attach_pdl(jc, attr);
   if constexpr (MODE == kShared) return cudaLaunchKernelEx(&jc, attn_join_rows_kernel<D>, p, paged_ctas(sm_count));

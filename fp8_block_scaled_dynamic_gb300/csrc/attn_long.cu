@@ -20,9 +20,9 @@ namespace {
 constexpr unsigned kFull = 0xFFFFFFFFu;
 
 // Exclusive sum (or running maximum) over the block's threads of one value each.
-template <int THREADS, class Op>
+template <class Op>
 __device__ __forceinline__ int scan_block(int x, int none, int *s_warp, Op op, int *total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   int incl = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -35,8 +35,7 @@ __device__ __forceinline__ int scan_block(int x, int none, int *s_warp, Op op, i
   if (lane == 0) excl = none;
   __syncthreads();
   int all = none;
-#pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) {
+  for (int w = 0; w < warps; ++w) {
     if (w < warp) excl = op(excl, s_warp[w]);
     all = op(all, s_warp[w]);
   }
@@ -51,8 +50,8 @@ struct Sum {
 };
 
 // ------------------------------------------------------------------ shared
-constexpr int kPlanThreads = 1024;
-constexpr int kPlanOwn = kAttnMaxSeqs / kPlanThreads;  // sequences (groups) of a thread, one after another
+constexpr int kPlanThreads = 1024;  // at most: a thread a sequence, where there are as many
+constexpr int kPlanOwn = kAttnMaxSeqs / kPlanThreads;
 
 // One block: the sequences' nodes and contexts, the groups' sequences and
 // prefixes, all within their bounds, as records and their units (key tiles of row
@@ -67,6 +66,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
   pdl_trigger();
   pdl_wait();
   const AttnParams &a = p.a;
+  const int threads = blockDim.x;
   const int B = a.B, page = a.cache.page_size, limit = a.table_cols * page, tid = threadIdx.x, ng = p.n_groups;
   // (what is read one after another below is on its way at once)
   if (tid * 32 <= B) {
@@ -79,10 +79,10 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
   bool bad = false;
   // offsets never fall: a thread's own ones, then what comes before them
   auto clamp_offsets = [&](const int *at, int n, int most, auto put) {
-    const int per = (n + kPlanThreads - 1) / kPlanThreads, b0 = min(tid * per, n), b1 = min(b0 + per, n);
+    const int per = (n + threads - 1) / threads, b0 = min(tid * per, n), b1 = min(b0 + per, n);
     int top = 0;
     for (int b = b0; b < b1; ++b) top = max(top, min(max(__ldg(at + b), 0), most));
-    int running = scan_block<kPlanThreads>(top, 0, s_warp, Max(), nullptr);
+    int running = scan_block(top, 0, s_warp, Max(), nullptr);
     for (int b = b0; b < b1; ++b) {
       const int raw = __ldg(at + b);
       running = max(running, min(max(raw, 0), most));
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
   };
   clamp_offsets(a.cu, B + 1, a.T, [&](int b, int x) { s_a0[b] = x; });
   if (ng > 0) clamp_offsets(p.groups, ng + 1, B, [&](int g, int x) { s_g[g] = (uint16_t)x; });
-  for (int g = tid; g < ng; g += kPlanThreads) s_len[g] = limit;
+  for (int g = tid; g < ng; g += threads) s_len[g] = limit;
   __syncthreads();
   // a sequence's group, or -1: the last group that begins at or before it and is not empty
   auto group_of = [&](int b) {
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
   int ctx[kPlanOwn], of[kPlanOwn];
 #pragma unroll
   for (int i = 0; i < kPlanOwn; ++i) {
-    const int b = tid + i * kPlanThreads;
+    const int b = tid + i * threads;
     of[i] = -1;
     if (b >= B) continue;
     const int raw = __ldg(a.ctx + b);
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     if (of[i] >= 0) atomicMin(&s_len[of[i]], ctx[i]);
   }
   __syncthreads();
-  for (int g = tid; g < ng; g += kPlanThreads) {
+  for (int g = tid; g < ng; g += threads) {
     const int g0 = s_g[g], g1 = s_g[g + 1], raw = __ldg(p.prefix + g);
     const int len = g1 > g0 ? min(max(raw, 0), s_len[g]) / page * page : 0;
     bad |= g1 > g0 && raw != len;
@@ -133,11 +133,11 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     rec[g] = r;
     to.units[0][g] = (r.n + to.span[0] - 1) / to.span[0] * a.Hkv * ((len + kKeys - 1) / kKeys);
   }
-  for (int g = ng + tid; g < 32 * units_per_lane(ng); g += kPlanThreads) to.units[0][g] = 0;
+  for (int g = ng + tid; g < 32 * units_per_lane(ng); g += threads) to.units[0][g] = 0;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kPlanOwn; ++i) {
-    const int b = tid + i * kPlanThreads;
+    const int b = tid + i * threads;
     if (b >= B) continue;
     const int len = of[i] >= 0 ? s_len[of[i]] : 0, a0 = s_a0[b], a1 = s_a0[b + 1];
     PlanRec r = {};
@@ -151,9 +151,9 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     to.units[1][b] = (r.n + to.span[1] - 1) / to.span[1] * a.Hkv * ((r.ctx + kKeys - 1) / kKeys + 1);
     for (int x = a0; x < a1; ++x) to.info[x] = x - a0 < kAttnMaxNodes ? len > 0 : -1;
   }
-  for (int b = B + tid; b < 32 * units_per_lane(B); b += kPlanThreads) to.units[1][b] = 0;
-  for (int x = tid; x < s_a0[0]; x += kPlanThreads) to.info[x] = -1;
-  for (int x = s_a0[B] + tid; x < a.T; x += kPlanThreads) to.info[x] = -1;
+  for (int b = B + tid; b < 32 * units_per_lane(B); b += threads) to.units[1][b] = 0;
+  for (int x = tid; x < s_a0[0]; x += threads) to.info[x] = -1;
+  for (int x = s_a0[B] + tid; x < a.T; x += threads) to.info[x] = -1;
   if (bad && a.status) atomicOr(a.status, kBadIndex);
 }
 
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kListThreads) sparse_plan_kernel(const SparseP
   int top = 0;
   for (int i = tid; i <= b; i += kListThreads) top = max(top, min(max(__ldg(a.cu + i), 0), a.T));
   int a0;
-  scan_block<kListThreads>(top, 0, s_warp, Max(), &a0);
+  scan_block(top, 0, s_warp, Max(), &a0);
   const int a1 = max(min(max(c1, 0), a.T), a0);
   const int n = min(a1 - a0, kAttnMaxNodes), ctx = min(max(raw, 0), a.table_cols * page);
   bool bad = h == 0 && (c0 != a0 || c1 != a1 || a1 - a0 > kAttnMaxNodes || raw != ctx);
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kListThreads) sparse_plan_kernel(const SparseP
   const int per = (W + kListThreads - 1) / kListThreads, w0 = min(tid * per, W), w1 = min(w0 + per, W);
   int sum = 0, count;
   for (int i = w0; i < w1; ++i) sum += __popc(s_bits[i]);
-  int at = scan_block<kListThreads>(sum, 0, s_warp, Sum(), &count);
+  int at = scan_block(sum, 0, s_warp, Sum(), &count);
   const long long base = ((long long)a0 * a.Hkv + (long long)h * n) * p.n_sel;
   for (int i = w0; i < w1; ++i) {
     s_before[i] = at;
@@ -308,6 +308,7 @@ cudaError_t launch_shared(const SharedParams &p, AttnParams a, const SharedLists
   a.plan.rec = to.rec + p.n_groups;
   a.plan.units = to.units[1];
   a.plan.n = a.B;
+  a.plan.beside = p.n_groups > 0;
   if ((e = launch_rows<D, kShared>(a, sm_count, stream)) != cudaSuccess) return e;
   return launch_join<D, kShared>(a, sm_count, stream);
 }
@@ -336,7 +337,8 @@ cudaError_t launch_attn_shared(const SharedParams &p, int sm_count, cudaStream_t
   to.units[1] = to.units[0] + kAttnMaxSeqs + 128;
   to.span[0] = span_of(a, 0);
   to.span[1] = span_of(a, few_rows(a));
-  cudaLaunchConfig_t cfg = pdl_config(dim3(1), dim3(kPlanThreads), 0, stream);
+  const int threads = a.B < 128 ? 128 : a.B < kPlanThreads ? (a.B + 31) / 32 * 32 : kPlanThreads;
+  cudaLaunchConfig_t cfg = pdl_config(dim3(1), dim3((unsigned)threads), 0, stream);
   cudaLaunchAttribute attr[1];
   attach_pdl(cfg, attr);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, shared_plan_kernel, p, to);

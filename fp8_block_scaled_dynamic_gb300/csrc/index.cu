@@ -11,6 +11,7 @@
 #include <cuda_runtime.h>
 #include <climits>
 #include <cstdint>
+#include <type_traits>
 
 #include "attn.h"
 #include "attn_ptx.cuh"
@@ -57,19 +58,27 @@ __device__ __forceinline__ void bound_page(const IndexParams &p, int layer, int 
   uint32_t hi[4], lo[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) hi[i] = 0xFF80FF80u, lo[i] = 0x7F807F80u;  // -inf, +inf
-  const int steps = p.cache.page_size / R;  // (a multiple of 4)
-  for (int t = 0; t < steps; t += 4) {
-    uint4 x[4];
+  // kAhead loads of a lane in flight (a step's few pages are a chain of them: with
+  // four, 6.4 us)
+  auto take = [&](auto ahead, int t) {
+    constexpr int kAhead = decltype(ahead)::value;
+    uint4 x[kAhead];
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
+    for (int u = 0; u < kAhead; ++u)
       x[u] = __ldg(reinterpret_cast<const uint4 *>(k + (long long)((t + u) * R + sub) * p.cache.slot));
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < kAhead; ++u) {
       hi[0] = max2(hi[0], x[u].x), lo[0] = min2(lo[0], x[u].x);
       hi[1] = max2(hi[1], x[u].y), lo[1] = min2(lo[1], x[u].y);
       hi[2] = max2(hi[2], x[u].z), lo[2] = min2(lo[2], x[u].z);
       hi[3] = max2(hi[3], x[u].w), lo[3] = min2(lo[3], x[u].w);
     }
+  };
+  const int steps = p.cache.page_size / R;  // (a power of two, at least 4)
+  if (steps >= 16) {
+    for (int t = 0; t < steps; t += 16) take(std::integral_constant<int, 16>(), t);
+  } else {
+    for (int t = 0; t < steps; t += 4) take(std::integral_constant<int, 4>(), t);
   }
 #pragma unroll
   for (int o = 16; o >= L; o >>= 1)
@@ -110,7 +119,7 @@ __device__ __forceinline__ void bound_page(const IndexParams &p, int layer, int 
 // the grid take pages, a kv head each: the heads of a page next to one another, so
 // that a block reads whole tokens.
 template <int D>
-__global__ void __launch_bounds__(kIndexThreads) index_kernel(const IndexParams p) {
+__global__ void __launch_bounds__(kIndexThreads, 2) index_kernel(const IndexParams p) {
   __shared__ int s_end[kAttnMaxSeqs], s_warp[kIndexThreads / 32];
   pdl_trigger();
   pdl_wait();
@@ -213,14 +222,6 @@ __device__ __forceinline__ void bytes_to_half(uint32_t w, uint32_t &h01, uint32_
 __device__ __forceinline__ uint32_t order_key(float x) {
   const uint32_t b = __float_as_uint(x);
   return b & 0x80000000u ? ~b : b | 0x80000000u;
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void st_cluster(uint32_t saddr, uint32_t rank, uint32_t v) {
   asm volatile(
@@ -741,7 +742,7 @@ cudaError_t launch_select(const SelectParams &p, const SelectPlan &plan, cudaStr
 }  // namespace
 
 cudaError_t launch_kv_index(const IndexParams &p, int sm_count, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)(4 * sm_count)), dim3(kIndexThreads), 0, stream);
+  cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)(2 * sm_count)), dim3(kIndexThreads), 0, stream);
   cudaLaunchAttribute attr[1];
   attach_pdl(cfg, attr);
   return p.D == 64 ? cudaLaunchKernelEx(&cfg, index_kernel<64>, p) : cudaLaunchKernelEx(&cfg, index_kernel<128>, p);
