@@ -58,6 +58,7 @@ struct Plan {
   float *rows, *stats;              // shared: parts of whole rows (prefix, own): sums, references and weights
   float *part_ws[2];                // shared: the two launches' items and slots
   bool beside;                      // shared: the launch may run beside the one before it
+  const int *ctas;                  // shared: the launch's CTAs that have a share of its work
 };
 
 struct AttnParams {

@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::kThreads, 1)
     } else {
       units.read(p, lane);
     }
-    Walk<MODE> walk(few ? small.total : units.total, TQ);
+    Walk<MODE> walk(few ? small.total : units.total, TQ, p.plan.ctas ? __ldg(p.plan.ctas) : (int)gridDim.x);
     bool going_on = false;
     if (few) walk.choose_chunk(small);
     for (int k = 0;; ++k) {
@@ -501,6 +501,7 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::kThreads, 1)
       for (int r = 0; r < R; ++r) l[r] = 0.0f;
       if (key == 0) sm.bad[grp] = 0;
       uint32_t saw = 0;
+      bool open = true;
       for (int i = 0; i < nt; ++i) {
         const int j = it.t0 + i;
         const uint32_t t = tile + i, sb = t & 1, ph = (t >> 1) & 1;
@@ -516,26 +517,50 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::kThreads, 1)
         for (int r = 0; r < R; ++r)
           if (!(see >> r & 1u)) s[r] = 0xFF800000u;
         bool past = false;
+        // a row without a reference yet has an infinite `neg` (rows past the last one: 0)
+        const auto open_rows = [&]() {
+          bool x = false;
+#pragma unroll
+          for (int r = 0; r < R; ++r) x |= neg[r] == INFINITY;
+          return x;
+        };
         if (i == 0) {
           if (!lists && it.nct > it.t0) {
             // all rows see the tile's first key
             if (key == 0) {
 #pragma unroll
-              for (int r = 0; r < R; ++r) ref[r] = __uint_as_float(s[r]), neg[r] = -__uint_as_float(s[r]) * c;
+              for (int r = 0; r < R; ++r)
+                ref[r] = __uint_as_float(s[r]), neg[r] = r < rows ? -__uint_as_float(s[r]) * c : 0.0f;
             }
             sync_four(grp);
+            open = open_rows();
           } else {
             past = true;
           }
         }
-        uint32_t w[R];  // weights, rounded to bf16
+        uint32_t w[R / 2];  // weights, rounded to bf16, of two rows each
         const auto weigh = [&]() {
           float most = 0.0f;
+          if (!open) {
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const float n = neg[r], x = ex2(fmaf(__uint_as_float(s[r]), c, n == INFINITY ? 0.0f : n));
-            most = fmaxf(most, n == INFINITY && s[r] != 0xFF800000u ? INFINITY : x);
-            w[r] = pack_bf16x2(x, 0.0f);
+            for (int r = 0; r < R; r += 2) {
+              const float x = ex2(fmaf(__uint_as_float(s[r]), c, neg[r]));
+              const float y = ex2(fmaf(__uint_as_float(s[r + 1]), c, neg[r + 1]));
+              most = fmaxf(most, fmaxf(x, y));
+              w[r / 2] = pack_bf16x2(x, y);
+            }
+          } else {
+#pragma unroll
+            for (int r = 0; r < R; r += 2) {
+              float x[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float n = neg[r + e];
+                x[e] = ex2(fmaf(__uint_as_float(s[r + e]), c, n == INFINITY ? 0.0f : n));
+                most = fmaxf(most, n == INFINITY && s[r + e] != 0xFF800000u ? INFINITY : x[e]);
+              }
+              w[r / 2] = pack_bf16x2(x[0], x[1]);
+            }
           }
           return most > kFewPast;
         };
@@ -556,9 +581,10 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::kThreads, 1)
             const float m = fmaxf(fmaxf(old, fmaxf(m4[0][key], m4[1][key])), fmaxf(m4[2][key], m4[3][key]));
             fac[key] = m == old ? 1.0f : old == -INFINITY ? 0.0f : ex2((old - m) * c);
             ref[key] = m;
-            neg[key] = -m * c;
+            neg[key] = key < rows ? -m * c : 0.0f;
           }
           sync_four(grp);
+          open = open_rows();
           if (i > 0) {
             tc_fence_after();
             const uint32_t at = tmem + lanes + 128 + (k & 1) * 64 + first;
@@ -580,9 +606,12 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::kThreads, 1)
         // been multiplied: the scores came after it.)
         const uint32_t to = p_mine + sb * C::kP + (key >> 6) * (R * 128) + (key & 7) * 2, unit = (key >> 3) & 7;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          l[r] += __uint_as_float(w[r] << 16);
-          st_shared_u16(to + r * 128 + ((unit ^ (r & 7)) << 4), w[r]);
+        for (int r = 0; r < R; r += 2) {
+          const uint32_t x = w[r / 2];
+          l[r] += __uint_as_float(x << 16);
+          l[r + 1] += __uint_as_float(x & 0xFFFF0000u);
+          st_shared_u16(to + r * 128 + ((unit ^ (r & 7)) << 4), x);
+          st_shared_u16(to + (r + 1) * 128 + ((unit ^ ((r + 1) & 7)) << 4), x >> 16);
         }
         if (grp == 0 && !some) {
           // no row sees this key: its v is made zero

@@ -492,12 +492,13 @@ struct Walk {
   int cur, end, q, r;  // tree: this CTA's units, the shares; prompt: the round, the number of items
   int chunk;           // tree: most key tiles of a chunk, 0: equal ranges
   int span;            // tokens (nodes) of a row group
-  __device__ __forceinline__ Walk(int U, int span) : chunk(0), span(span) {
+  int ctas;            // that share the work
+  __device__ __forceinline__ Walk(int U, int span, int ctas) : chunk(0), span(span), ctas(ctas) {
     if (paged(MODE)) {
-      q = U / (int)gridDim.x;
-      r = U - q * (int)gridDim.x;
+      q = U / ctas;
+      r = U - q * ctas;
       cur = share_begin(blockIdx.x, q, r);
-      end = share_begin(blockIdx.x + 1, q, r);
+      end = (int)blockIdx.x < ctas ? share_begin(blockIdx.x + 1, q, r) : cur;
     } else {
       cur = 0;
       end = U;
@@ -514,7 +515,7 @@ struct Walk {
       chunks[i] = __reduce_add_sync(0xFFFFFFFFu, b.s.rows * div_small(b.s.per + least + i - 1, least + i));
 #pragma unroll
     for (int i = 2; i >= 0; --i)
-      if (chunks[i] <= (int)gridDim.x) chunk = least + i;
+      if (chunks[i] <= ctas) chunk = least + i;
   }
   // this CTA's only item, a chunk; returns the last CTA of the row group's chunks
   __device__ __forceinline__ int one_chunk(const AttnParams &p, const Small<MODE> &b, int tq, Item<MODE> &it) {
@@ -1151,7 +1152,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       else fill_prefix<MODE>(p, sm.pre, 2 * TQ, lane, blockIdx.x == 0);
       const int span = !TREE && few ? small.choose_span(p, TQ, lane) : 2 * TQ;
       if (few) small.number(p, lane);
-      Walk<MODE> walk(few ? small.total : planned(MODE) ? planned_units.total : sm.pre.units[kBlocks], span);
+      int ctas = gridDim.x;
+      if constexpr (MODE == kShared) ctas = __ldg(p.plan.ctas);
+      Walk<MODE> walk(few ? small.total : planned(MODE) ? planned_units.total : sm.pre.units[kBlocks], span, ctas);
       Found found;
       bool going_on = false;
       if constexpr (TREE) {

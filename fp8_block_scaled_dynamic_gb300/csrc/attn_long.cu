@@ -56,9 +56,12 @@ constexpr int kPlanOwn = kAttnMaxSeqs / kPlanThreads;
 // One block: the sequences' nodes and contexts, the groups' sequences and
 // prefixes, all within their bounds, as records and their units (key tiles of row
 // groups of span[0] nodes of a group, span[1] of a sequence).
+constexpr float kShortWork = 20.0f;  // us of every CTA
 struct SharedLists {
   PlanRec *rec;
   int *info, *units[2], span[2];
+  int *ctas;       // of the two launches, that share their work
+  int most;        // CTAs of a launch
 };
 __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedParams p, const SharedLists to) {
   __shared__ int s_a0[kAttnMaxSeqs + 1], s_len[kAttnMaxSeqs], s_warp[kPlanThreads / 32];
@@ -154,6 +157,42 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
   for (int b = B + tid; b < 32 * units_per_lane(B); b += threads) to.units[1][b] = 0;
   for (int x = tid; x < s_a0[0]; x += threads) to.info[x] = -1;
   for (int x = s_a0[B] + tid; x < a.T; x += threads) to.info[x] = -1;
+  // Estimated times, us of one CTA: a prefix's key tile (two row tiles) takes 2.0 and
+  // its row group 5, a sequence's 1.0 and 3.  Where both are short, the two launches
+  // share the SMs and run beside one another (8 requests of 8 nodes behind 1024 tokens
+  // 37 us, 42 one after the other); else each has all of them, since the keys of the
+  // one held up the other's (64 requests behind 16384 tokens 103 us, 94 one after the
+  // other).
+  if (ng > 0) {
+    float work[2] = {0.0f, 0.0f};
+    for (int g = tid; g < ng; g += threads) {
+      const int n = s_a0[s_g[g + 1]] - s_a0[s_g[g]];
+      work[0] += 2.0f * (float)to.units[0][g] + (s_len[g] > 0 ? 5.0f : 0.0f) * (float)((n + to.span[0] - 1) / to.span[0] * a.Hkv);
+    }
+    for (int b = tid; b < B; b += threads) {
+      const int n = min(s_a0[b + 1] - s_a0[b], kAttnMaxNodes);
+      work[1] += (float)to.units[1][b] + 3.0f * (float)((n + to.span[1] - 1) / to.span[1] * a.Hkv);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) work[i] += __shfl_xor_sync(kFull, work[i], o);
+      __syncthreads();
+      if ((tid & 31) == 0) reinterpret_cast<float *>(s_warp)[tid >> 5] = work[i];
+      __syncthreads();
+      work[i] = 0.0f;
+      for (int w = 0; w < threads / 32; ++w) work[i] += reinterpret_cast<float *>(s_warp)[w];
+    }
+    if (tid == 0) {
+      const int first = (int)((float)to.most * work[0] / (work[0] + work[1]) + 0.5f);
+      const int x = max(min(first, to.most - 1), 1);
+      const bool both = work[0] + work[1] < kShortWork * (float)to.most;
+      to.ctas[0] = both ? x : to.most;
+      to.ctas[1] = both ? max(to.most - x, 1) : to.most;
+    }
+  } else if (tid == 0) {
+    to.ctas[0] = to.ctas[1] = to.most;
+  }
   if (bad && a.status) atomicOr(a.status, kBadIndex);
 }
 
@@ -252,13 +291,14 @@ size_t slots_bytes(int D, int sm_count) {
 
 // Byte offsets; a launch's items, which the join reads, come first, then its slots.
 struct SharedWs {
-  size_t slots, second, rec, units, info, rows, stats, end;
+  size_t slots, second, rec, units, ctas, info, rows, stats, end;
   SharedWs(long long N, int Hq, int D, int sm_count) {
     slots = kJoinFloats * sizeof(float);
     second = slots + slots_bytes(D, sm_count);
     rec = 2 * second;
     units = rec + 2 * kAttnMaxSeqs * sizeof(PlanRec);
-    info = units + 2 * (kAttnMaxSeqs + 128) * sizeof(int);
+    ctas = units + 2 * (kAttnMaxSeqs + 128) * sizeof(int);
+    info = ctas + 16;
     rows = round256(info + N * sizeof(int));
     stats = rows + (size_t)(2 * N * Hq) * D * sizeof(float);
     end = round256(stats + (size_t)(2 * N * Hq) * 2 * sizeof(float));
@@ -301,6 +341,7 @@ cudaError_t launch_shared(const SharedParams &p, AttnParams a, const SharedLists
     a.ws = a.plan.part_ws[0];
     a.plan.rec = to.rec;
     a.plan.units = to.units[0];
+    a.plan.ctas = to.ctas;
     a.plan.n = p.n_groups;
     if ((e = launch_t<D, kShared>(a, sm_count, stream)) != cudaSuccess) return e;
   }
@@ -308,6 +349,7 @@ cudaError_t launch_shared(const SharedParams &p, AttnParams a, const SharedLists
   a.plan.rec = to.rec + p.n_groups;
   a.plan.units = to.units[1];
   a.plan.n = a.B;
+  a.plan.ctas = to.ctas + 1;
   a.plan.beside = p.n_groups > 0;
   if ((e = launch_rows<D, kShared>(a, sm_count, stream)) != cudaSuccess) return e;
   return launch_join<D, kShared>(a, sm_count, stream);
@@ -335,6 +377,8 @@ cudaError_t launch_attn_shared(const SharedParams &p, int sm_count, cudaStream_t
   to.info = reinterpret_cast<int *>(w + ws.info);
   to.units[0] = reinterpret_cast<int *>(w + ws.units);
   to.units[1] = to.units[0] + kAttnMaxSeqs + 128;
+  to.ctas = reinterpret_cast<int *>(w + ws.ctas);
+  to.most = paged_ctas(sm_count);
   to.span[0] = span_of(a, 0);
   to.span[1] = span_of(a, few_rows(a));
   const int threads = a.B < 128 ? 128 : a.B < kPlanThreads ? (a.B + 31) / 32 * 32 : kPlanThreads;
