@@ -175,3 +175,15 @@ def test_same_result_each_time_and_on_a_stream():
     out = c.run(stream=s)
     s.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("nodes,scale", [([1, 1], 3.0), ([8, 5], 3.0), ([20, 64], 3.0), ([1, 1], 60.0), ([8, 3], 60.0)])
+def test_scores_far_apart(nodes, scale):
+    """Scores that differ by hundreds, in the prefix, in the own tokens and in the nodes."""
+    c = Case([2], [512], [300, 40], nodes, 8, 2, 128, 64, seed=21)
+    c.scale = scale
+    for i, t in enumerate([0, 200, 511, 512, 700, 811]):
+        page = int(c.tab[0, t // 64])
+        c.kc[page, t % 64, i % 2] = c.q[0, (i % 2) * 4 + i % 4] * (0.5 if i % 2 else 2.0)
+    c.k[nodes[0] - 1, 0] = c.q[nodes[0] - 1, 3] * 3
+    c.check(c.run(scale=scale), f"{nodes} {scale}")

@@ -161,3 +161,32 @@ def test_same_result_each_time_and_on_a_stream():
     out = c.run(stream=s)
     s.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("nodes,scale", [([1, 1], 3.0), ([2, 1], 3.0), ([8, 5], 3.0), ([16, 3], 3.0), ([1, 1], 60.0), ([8, 3], 60.0)])
+def test_scores_far_apart(nodes, scale):
+    """Scores that differ by hundreds, the largest where they may: the reference has to be moved."""
+    c = Case([900, 333], nodes, 8, 2, 128, 64, 9, seed=17)
+    c.scale = scale
+    for i, t in enumerate([0, 5, 64 * 3, 64 * 7 + 1, 899]):  # a key along a query each
+        page = int(c.tab[0, t // 64])
+        c.kc[page, t % 64, i % 2] = c.q[0, (i % 2) * 4 + i % 4] * (0.5 if i % 2 else 2.0)
+    c.check(c.run(scale=scale), f"{nodes} {scale}")
+
+
+@pytest.mark.parametrize("n", [1, 3, 8])
+def test_first_key_that_counts_for_nothing(n):
+    """A first key whose score is -infinity in 32 bits, or NaN, or infinite."""
+    c = Case([300, 300], [n, n], 8, 2, 128, 64, 5, seed=19)
+    for b in range(2):
+        page = int(c.tab[b, 0])
+        c.kc[page, 0, 0] = -c.q[b * n, 1].sign() * 3e38
+    c.kc[int(c.tab[1, 0]), 0, 1] = float("nan")
+    out = c.run()
+    # the row that the key was made against has only negative products, a score of -infinity in 32 bits, and does without
+    # it; the others' products of either sign overflow 32 bits, and what comes of infinity - infinity is theirs
+    assert bool(torch.isfinite(out[0, 1].float()).all()) and bool(torch.isfinite(out[n, 1].float()).all())
+    assert bool(torch.isnan(out[n:, 4:]).all())
+    c.kc[:, 0, 0] = 0
+    c.kc[int(c.tab[1, 0]), 0, 1] = 0
+    c.check(c.run(), "after")
