@@ -255,8 +255,6 @@ struct Choice {
     return x;
   }
 };
-// (Out of line, as prepare_q is: inlined, its registers made the score loop spill,
-// a batch of 64 x 1024 pages 50 us instead of 35.)
 template <int LG>
 __device__ __forceinline__ void choose(const uint32_t *keys, int P, int first, int last, int n_sel, int *sel, Choice ch) {
   constexpr int kOwn = 1 << LG, kBlock = 32 * kOwn;  // keys that a lane, a warp holds in registers
@@ -365,62 +363,62 @@ template <int D, int WARPS>
 __device__ __forceinline__ void prepare_q(const uint16_t *q, long long tok, long long head, int nodes, int G, int gp, uint2 *s_q) {
   constexpr int kSteps = D / 8;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-      // A node's columns are some warps', which all look for its largest value.  (x in
-      // units of 2^e is exact; + 1.5 2^23 rounds it to a whole number, ties to even.)
-      int team = 1;
-      while (team < WARPS && nodes * team * 2 <= WARPS) team <<= 1;
-      const int part = warp & (team - 1);
-      constexpr int kAtOnce = WARPS == 8 ? 8 : 4;  // columns in flight (8 of them made the one-group kernel spill)
-      for (int node = warp / team; node < nodes; node += WARPS / team) {
-        const uint16_t *row = q + node * tok + lane * 4;
-        auto load_q = [&](int g) {  // four channels of a head; the first one's in place of those past the last
-          return lane * 4 < D ? __ldg(reinterpret_cast<const uint2 *>(row + (g < G ? g : 0) * head)) : make_uint2(0, 0);
-        };
-        uint32_t m = 0;
-        uint2 x[kAtOnce];
-        for (int g = 0; g < gp; g += kAtOnce) {
+  // A node's columns are some warps', which all look for its largest value.  (x in
+  // units of 2^e is exact; + 1.5 2^23 rounds it to a whole number, ties to even.)
+  int team = 1;
+  while (team < WARPS && nodes * team * 2 <= WARPS) team <<= 1;
+  const int part = warp & (team - 1);
+  constexpr int kAtOnce = WARPS == 8 ? 8 : 4;  // columns in flight (8 of them made the one-group kernel spill)
+  for (int node = warp / team; node < nodes; node += WARPS / team) {
+    const uint16_t *row = q + node * tok + lane * 4;
+    auto load_q = [&](int g) {  // four channels of a head; the first one's in place of those past the last
+      return lane * 4 < D ? __ldg(reinterpret_cast<const uint2 *>(row + (g < G ? g : 0) * head)) : make_uint2(0, 0);
+    };
+    uint32_t m = 0;
+    uint2 x[kAtOnce];
+    for (int g = 0; g < gp; g += kAtOnce) {
 #pragma unroll
-          for (int i = 0; i < kAtOnce; ++i) x[i] = load_q(g + i);
+      for (int i = 0; i < kAtOnce; ++i) x[i] = load_q(g + i);
 #pragma unroll
-          for (int i = 0; i < kAtOnce; ++i)
-            m = max(m, max(max(x[i].x & 0x7FFFu, x[i].x >> 16 & 0x7FFFu), max(x[i].y & 0x7FFFu, x[i].y >> 16 & 0x7FFFu)));
+      for (int i = 0; i < kAtOnce; ++i)
+        m = max(m, max(max(x[i].x & 0x7FFFu, x[i].x >> 16 & 0x7FFFu), max(x[i].y & 0x7FFFu, x[i].y >> 16 & 0x7FFFu)));
+    }
+    m = __reduce_max_sync(kFull, m);
+    const bool fine = m < 0x7F80u;
+    const float down = fine ? scale_down(exponent_of(__uint_as_float(m << 16))) : 0.0f;
+    for (int g = 0; g < gp; g += kAtOnce) {
+      if (gp > kAtOnce) {
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) x[i] = load_q(g + i);
+      }
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        if (g + i >= gp || (i & (team - 1)) != part) continue;
+        const int c = node * gp + g + i;
+        uint2 v = fine ? x[i] : make_uint2(0, 0);
+        const uint32_t e[4] = {v.x << 16, v.x & 0xFFFF0000u, v.y << 16, v.y & 0xFFFF0000u};
+        float f[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) f[k] = __fmaf_rn(__uint_as_float(e[k]), down, 12582912.0f) - 12582912.0f;
+        uint32_t w[2], up[2], lo[2];  // fp16 pairs of x, max(x, 0), min(x, 0)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[k]) : "f"(f[2 * k + 1]), "f"(f[2 * k]));
+          asm("max.f16x2 %0, %1, %2;" : "=r"(up[k]) : "r"(w[k]), "r"(0u));
+          asm("min.f16x2 %0, %1, %2;" : "=r"(lo[k]) : "r"(w[k]), "r"(0u));
         }
-        m = __reduce_max_sync(kFull, m);
-        const bool fine = m < 0x7F80u;
-        const float down = fine ? scale_down(exponent_of(__uint_as_float(m << 16))) : 0.0f;
-        for (int g = 0; g < gp; g += kAtOnce) {
-          if (gp > kAtOnce) {
-#pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) x[i] = load_q(g + i);
-          }
-#pragma unroll
-          for (int i = 0; i < kAtOnce; ++i) {
-            if (g + i >= gp || (i & (team - 1)) != part) continue;
-            const int c = node * gp + g + i;
-            uint2 v = fine ? x[i] : make_uint2(0, 0);
-            const uint32_t e[4] = {v.x << 16, v.x & 0xFFFF0000u, v.y << 16, v.y & 0xFFFF0000u};
-            float f[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) f[k] = __fmaf_rn(__uint_as_float(e[k]), down, 12582912.0f) - 12582912.0f;
-            uint32_t w[2], up[2], lo[2];  // fp16 pairs of x, max(x, 0), min(x, 0)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[k]) : "f"(f[2 * k + 1]), "f"(f[2 * k]));
-              asm("max.f16x2 %0, %1, %2;" : "=r"(up[k]) : "r"(w[k]), "r"(0u));
-              asm("min.f16x2 %0, %1, %2;" : "=r"(lo[k]) : "r"(w[k]), "r"(0u));
-            }
-            if (lane * 4 < D) {
-              // code positions byte .. byte + 3: word byte % 16 / 4 of what a lane reads of a chunk
-              auto put = [&](int byte, const uint32_t(&y)[2]) {
-                const int step = byte / 64 * 4 + byte % 16 / 4, to = (c & 7) * 4 + byte % 64 / 16;
-                s_q[((c >> 3) * (kSteps / 2) + step / 2) * 64 + to * 2 + step % 2] = make_uint2(y[0], y[1]);
-              };
-              put(lane * 4, up);
-              put(D + lane * 4, lo);
-            }
-          }
+        if (lane * 4 < D) {
+          // code positions byte .. byte + 3: word byte % 16 / 4 of what a lane reads of a chunk
+          auto put = [&](int byte, const uint32_t(&y)[2]) {
+            const int step = byte / 64 * 4 + byte % 16 / 4, to = (c & 7) * 4 + byte % 64 / 16;
+            s_q[((c >> 3) * (kSteps / 2) + step / 2) * 64 + to * 2 + step % 2] = make_uint2(y[0], y[1]);
+          };
+          put(lane * 4, up);
+          put(D + lane * 4, lo);
         }
       }
+    }
+  }
 }
 
 template <int D, bool MANY>
@@ -460,6 +458,7 @@ __global__ void __launch_bounds__(32 * kWarps<MANY>, MANY ? 1 : 4) select_kernel
       for (int i = threadIdx.x; i < p.n_sel; i += kThreads) row_of(node)[i] = i < P ? i : -1;
     return;
   }
+  cluster_begun();
   const int lg = lane_shift(P), tiles = (P + 15) / 16, stride = cs * kWarps<MANY>;
   // nodes of a pass: as many as have a slot and columns
   auto node_of = [&](int c) { return c * plan.gp_inv >> 16; };
@@ -484,6 +483,7 @@ __global__ void __launch_bounds__(32 * kWarps<MANY>, MANY ? 1 : 4) select_kernel
     prepare_q<D, kWarps<MANY>>(p.q.ptr + (long long)(a0 + n0) * p.q.tok + (long long)(h * G) * p.q.head, p.q.tok, p.q.head,
                                nodes, G, gp, s_q);
     __syncthreads();
+    if (n0 == 0) cluster_all_begun();
     // scores
     // (what follows is worked out anew in each pass: held through the other phases, it
     // made this one spill: a batch of 64 x 1024 pages 45 us instead of 33)
