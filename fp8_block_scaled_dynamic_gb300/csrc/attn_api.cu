@@ -96,7 +96,9 @@ mxg_status check_paged(int N, const uint64_t *mask, const mxg_kv_cache *cache, c
 }
 
 // Row groups x kv heads x key tiles, numbered in 32 bits; starts: row groups that
-// begin anew, besides the full ones.
+// begin anew, besides the full ones.  (Two a sequence for attn_shared and
+// attn_sparse: a prefix's, or the smaller row groups of few rows, which hold an
+// average sequence's nodes: full ones are then no more than the sequences.)
 mxg_status check_units(int N, int Hq, int Hkv, long long starts, int table_cols, int page_size) {
   const int tq = 128 / (Hq / Hkv);
   const long long groups = N / (2 * tq) + starts;
@@ -431,9 +433,8 @@ mxg_status attn_sparse(const mxg_heads *q, const mxg_heads *k, const mxg_heads *
   if ((st = check_ws(opts, mxg::attn_sparse_ws_bytes(N, Hkv, n_sel, D, sm))) != MXG_OK) return st;
   // (a sequence's nodes name no more pages than there are, nor than all their lists hold)
   const long long named = (long long)mxg::kAttnMaxNodes * n_sel;
-  if ((st = check_units(N, Hq, Hkv, N < B ? N : B, named < table_cols ? (int)named : table_cols, cache->page_size)) !=
-      MXG_OK)
-    return st;
+  const int cols = named < table_cols ? (int)named : table_cols;
+  if ((st = check_units(N, Hq, Hkv, 2LL * (N < B ? N : B), cols, cache->page_size)) != MXG_OK) return st;
   if (N == 0) return MXG_OK;
   mxg::SparseParams p = {};
   p.a = attn_params(q, k, v, cu_nodes, B, N, Hq, Hkv, D, scale, out, opts);

@@ -15,7 +15,7 @@
 // have fp32's and bf16's range of exponents, and a reference that some key of the row
 // has is never above it.  So the first key's score serves where all rows see it (else
 // the first tile's maximum, 0.9 us more), and it is moved to the maximum only when a
-// weight is past 2^60 (one vote a tile).  Weights are rounded to bf16 and summed as
+// weight is past 2^30 (one vote a tile).  Weights are rounded to bf16 and summed as
 // rounded, so that what one key's rounding adds above it also adds below.
 //
 // Rows see different keys: a key has a word of the rows that see it (mask words for
@@ -52,7 +52,9 @@ struct FewCfg {
   static_assert(kSlots >= 4 && kQ % 1024 == 0 && kP % 1024 == 0, "shared memory");
 };
 
-constexpr float kFewPast = 0x1p60f;  // a weight above this moves the reference
+// A weight above this moves the reference (what a row adds up is at most so much
+// larger than with its maximum: values below 2^80 cannot take it past fp32's largest).
+constexpr float kFewPast = 0x1p30f;
 
 template <int D, int NR, int MODE>
 struct FewSmem {

@@ -209,10 +209,8 @@ __device__ __forceinline__ void fill_prefix(const AttnParams &p, Prefix &pre, in
   Raw first = {};  // (a small batch is read once)
   if (b0 < b1) first = raw_seq<MODE>(p, b0);
   int top = min(max(first.c0, 0), p.T);  // largest offset of this lane's sequences, then of those before
-  if constexpr (!planned(MODE)) {
 #pragma unroll 8
-    for (int b = b0 + 1; b < b1; ++b) top = max(top, min(max(__ldg(p.cu + b), 0), p.T));
-  }
+  for (int b = b0 + 1; b < b1; ++b) top = max(top, min(max(__ldg(p.cu + b), 0), p.T));
   int incl = top;
   for (int o = 1; o < 32; o <<= 1) {
     const int x = __shfl_up_sync(kFull, incl, o);

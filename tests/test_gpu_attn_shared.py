@@ -187,3 +187,15 @@ def test_scores_far_apart(nodes, scale):
         c.kc[page, t % 64, i % 2] = c.q[0, (i % 2) * 4 + i % 4] * (0.5 if i % 2 else 2.0)
     c.k[nodes[0] - 1, 0] = c.q[nodes[0] - 1, 3] * 3
     c.check(c.run(scale=scale), f"{nodes} {scale}")
+
+
+@pytest.mark.parametrize("nodes", [[1, 1], [4, 2], [8, 5], [40, 33]])
+def test_large_values(nodes):
+    """Values 2^76 times as large: the same bits with another exponent, whatever the reference of a row is."""
+    c = Case([2], [512], [300, 40], nodes, 8, 2, 128, 64, seed=24)
+    for b, t in ((0, 0), (0, 512), (1, 512)):  # first keys far below the others of their rows
+        c.kc[int(c.tab[b, t // 64]), 0] = -c.q[c.nodes[0] * b].view(2, 4, -1).float().mean(1).bfloat16()
+    want = c.run()
+    c.check(want, "as they are")
+    c.v, c.vc = c.v * 2.0**76, c.vc * 2.0**76
+    assert torch.equal(c.run(), want * 2.0**76)

@@ -190,3 +190,15 @@ def test_first_key_that_counts_for_nothing(n):
     c.kc[:, 0, 0] = 0
     c.kc[int(c.tab[1, 0]), 0, 1] = 0
     c.check(c.run(), "after")
+
+
+@pytest.mark.parametrize("nodes", [[1, 1], [4, 2], [8, 5], [40, 33]])
+def test_large_values(nodes):
+    """Values 2^76 times as large: the same bits with another exponent, whatever the reference of a row is."""
+    c = Case([900, 333], nodes, 8, 2, 128, 64, 9, seed=23)
+    for b in range(2):  # a first key far below the others of its rows
+        c.kc[int(c.tab[b, 0]), 0] = -c.q[c.nodes[0] * b].view(2, 4, -1).float().mean(1).bfloat16()
+    want = c.run()
+    c.check(want, "as they are")
+    c.v, c.vc = c.v * 2.0**76, c.vc * 2.0**76
+    assert torch.equal(c.run(), want * 2.0**76)
