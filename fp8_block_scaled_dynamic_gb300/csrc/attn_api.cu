@@ -342,6 +342,12 @@ mxg_status kv_index(const mxg_kv_cache *cache, int Hkv, int D, const mxg_page_in
   mxg_status st;
   if ((st = check_cache(cache)) != MXG_OK || (st = check_index(index)) != MXG_OK) return st;
   if (index->layers < cache->layers || index->pages < cache->pages) return MXG_ERR_INVALID_ARG;
+  // (entries are written: none over another)
+  const auto apart = [](int64_t stride, int n, int64_t bytes) { return n < 2 || stride >= bytes; };
+  if (!apart(index->codes_layer, index->layers, 2 * D) || !apart(index->codes_page, index->pages, 2 * D) ||
+      !apart(index->codes_head, Hkv, 2 * D) || !apart(index->exps_layer, index->layers, Hkv) ||
+      !apart(index->exps_page, index->pages, Hkv))
+    return MXG_ERR_UNSUPPORTED_SHAPE;
   // (pages of all sequences, numbered in 32 bits)
   if ((long long)table_cols * cache->page_size > 0x7fffff00LL || (long long)table_cols * B > 0x7fffffffLL)
     return MXG_ERR_UNSUPPORTED_SHAPE;

@@ -74,8 +74,8 @@ typedef struct {
 /* Bounds of the keys of a paged cache's full pages, by physical page: of (layer
  * l, page p, head h) two rows of D codes -- the upper bounds, then the lower --
  * at codes + l * codes_layer + p * codes_page + h * codes_head (strides in
- * bytes, multiples of 16; those of pages below 2^31) and the power of two that they count, as an E8M0 code,
- * at exps + l * exps_layer + p * exps_page + h. */
+ * bytes, multiples of 16; those of pages below 2^31) and the power of two that
+ * they count, as an E8M0 code, at exps + l * exps_layer + p * exps_page + h. */
 typedef struct {
     int8_t *codes;
     uint8_t *exps;
@@ -217,7 +217,8 @@ mxg_status attn_shared(const mxg_heads *q, const mxg_heads *k, const mxg_heads *
  * Sequences may share pages.  Other pages' entries are left as they were; v is
  * not read (cache->v must be given all the same).  index: as many layers as the
  * cache, entries for at least its pages.
- * D in {64, 128}, B <= MXG_ATTN_MAX_SEQS.
+ * D in {64, 128}, B <= MXG_ATTN_MAX_SEQS; entries of index apart from one another
+ * (strides of layers, pages and heads of at least 2 D codes and Hkv exponents).
  * Out of range: ctx_old and ctx_new are clamped to [0, table_cols * page_size], a
  * page outside [0, pages) is skipped. */
 mxg_status kv_index(const mxg_kv_cache *cache, int Hkv, int D, const mxg_page_index *index,

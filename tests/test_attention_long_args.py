@@ -70,6 +70,8 @@ INDEX = dict(cache=C(), Hkv=2, D=128, index=X(), table=P, B=2, ld=8, cols=8, old
     (dict(index=None), 1), (dict(D=96), 2), (dict(B=4097), 2), (dict(Hkv=65536), 2), (dict(index=X(pages=3)), 1), (dict(cache=C(layers=2)), 1),
     (dict(cache=C(page_size=20)), 2), (dict(cols=1 << 26, ld=1 << 26), 2), (dict(now=P + 2), 3), (dict(old=P + 1), 3), (dict(table=P + 2), 3),
     (dict(status=P + 2), 3), (dict(index=X(codes=P + 4)), 3), (dict(cols=1 << 24, ld=1 << 24, B=200), 2),
+    (dict(index=X(codes_page=0)), 2), (dict(index=X(codes_head=128)), 2), (dict(index=X(exps_page=1)), 2),
+    (dict(index=X(layers=2)), 2), (dict(index=X(layers=2, codes_layer=8192)), 2),
 ])
 def test_index_refusals(kw, want):
     assert mx.lib().kv_index(*{**INDEX, **kw}.values()) == want
