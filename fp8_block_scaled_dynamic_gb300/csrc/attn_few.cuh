@@ -113,9 +113,9 @@ __device__ __forceinline__ float over_lanes(float (&v)[kFewRows], int lane, Op o
   return op(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], 1));
 }
 
-// A row of a part summed again by a warp, key by key; tmp: room for the row.
+// A row of a part summed again by a warp, key by key, to tmp.
 template <int D, int MODE>
-__device__ __noinline__ void few_again(const AttnParams &p, const Item<MODE> it, int row, float ref, float *tmp, float *y) {
+__device__ __noinline__ void few_again(const AttnParams &p, const Item<MODE> &it, int row, float ref, float *tmp) {
   constexpr int V = D / 32;  // channels a lane, one after another
   constexpr unsigned kFull = 0xFFFFFFFFu;
   const int lane = threadIdx.x & 31, G = p.Hq / p.Hkv, node = row / G, shift = 31 - __clz(p.cache.page_size);
@@ -154,8 +154,6 @@ __device__ __noinline__ void few_again(const AttnParams &p, const Item<MODE> it,
       take(p.k.ptr + i * p.k.tok + it.hk * p.k.head, p.v.ptr + i * p.v.tok + it.hk * p.v.head);
     }
   }
-#pragma unroll
-  for (int i = 0; i < V; ++i) y[i] = tmp[lane * V + i];
 }
 
 template <int D, int NR, int MODE>
@@ -401,6 +399,7 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::kThreads, 1)
     Walk<MODE> walk(few ? small.total : units.total, TQ, p.plan.ctas ? __ldg(p.plan.ctas) : (int)gridDim.x);
     bool going_on = false;
     if (few) walk.choose_chunk(small);
+    else walk.choose_chunk(units);
     for (int k = 0;; ++k) {
       Item<MODE> w;
       int last = 0;  // the last CTA that has a part of the row group
@@ -409,8 +408,10 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::kThreads, 1)
       } else {
         walk.next(p, TQ, w, [&](int &u, int &b) { return few ? small.find(u, b) : units.find(p, TQ, u, b); });
         if (w.t1 > w.t0 && w.part == 1)
-          last = share_owner(share_begin(blockIdx.x + 1, walk.q, walk.r) + w.nct + (flags_of(w) & kHasNodes) - 1 - w.t1,
-                             walk.q, walk.r);
+          last = walk.last >= 0 ? walk.last
+                                : share_owner(share_begin(blockIdx.x + 1, walk.q, walk.r) + w.nct +
+                                                  (flags_of(w) & kHasNodes) - 1 - w.t1,
+                                              walk.q, walk.r);
       }
       if (k >= 2 && !warp_wait_far(&sm.item_free[k & 1], ((k >> 1) - 1) & 1, ctl)) break;
       if (lane == 0) sm.items[k & 1] = w;
@@ -450,25 +451,36 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::kThreads, 1)
     uint32_t tile = 0, rn = 0;
     bool ok = true;
     if (p.debug_stall) ok = warp_wait(&sm.stall, 0, ctl);
+    // What an item's first tile needs from memory: the words of the nodes that name this
+    // key's page (lists), the mask words of nodes lane and lane + 32.
+    struct Words {
+      unsigned long long who, word[2];
+    };
+    auto lists_of = [&](const Item<MODE> &x) { return MODE == kSparse && (flags_of(x) & kLists); };
+    auto names_of = [&](const Item<MODE> &x, int j, unsigned long long &who) {
+      const int t = j * kKeys + key;
+      if (lists_of(x) && j < x.nct && t < x.ctx) who = __ldg(p.plan.names + list_of(x) + (t >> page_shift));
+    };
+    auto words_of = [&](const Item<MODE> &x) {
+      Words y = {};
+      names_of(x, x.t0, y.who);
+      if (x.t1 > x.nct) {
+        if (lane < x.cnt[0]) y.word[0] = __ldg(p.mask + x.a0 + x.r0 + lane);
+        if (NR > 32 && lane + 32 < x.cnt[0]) y.word[1] = __ldg(p.mask + x.a0 + x.r0 + lane + 32);
+      }
+      return y;
+    };
+    bool there = ok && next_item(0);
+    Words ahead = {};
+    if (there) ahead = words_of(it);
     for (int k = 0;; ++k) {
-      const bool there = ok && next_item(k);
-      if (any_of_four(grp, !there)) break;
+      if (any_of_four(grp, !there || !ok)) break;
       const int nt = it.t1 - it.t0, cnt = it.cnt[0], rows = min(max(cnt * G - first, 0), R);  // this group's rows
       const unsigned long long group = G >= 64 ? ~0ull : (1ull << G) - 1ull;
       const uint32_t mine = (1u << rows) - 1u;
-      const bool lists = MODE == kSparse && (flags_of(it) & kLists);
-      // lists: the nodes that name this key's page, of the next tile
-      unsigned long long who = 0;
-      auto names_of = [&](int j) {
-        const int t = j * kKeys + key;
-        if (lists && j < it.nct && t < it.ctx) who = __ldg(p.plan.names + list_of(it) + (t >> page_shift));
-      };
-      names_of(it.t0);
-      unsigned long long word[2] = {0, 0};  // mask words of nodes lane and lane + 32 of the item
-      if (it.t1 > it.nct) {
-        if (lane < cnt) word[0] = __ldg(p.mask + it.a0 + it.r0 + lane);
-        if (NR > 32 && lane + 32 < cnt) word[1] = __ldg(p.mask + it.a0 + it.r0 + lane + 32);
-      }
+      const bool lists = lists_of(it);
+      unsigned long long who = ahead.who;  // (of the next tile)
+      const unsigned long long word[2] = {ahead.word[0], ahead.word[1]};
       unsigned long long words = word[0] | word[1];  // of all the item's nodes
 #pragma unroll
       for (int x = 16; x > 0; x >>= 1) words |= __shfl_xor_sync(kFull, words, x);
@@ -509,7 +521,7 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::kThreads, 1)
         const uint32_t t = tile + i, sb = t & 1, ph = (t >> 1) & 1;
         bool some;
         const uint32_t see = rows_that_see(j, some);
-        names_of(j + 1);
+        names_of(it, j + 1, who);
         saw |= see;
         if (!warp_wait(&sm.s_full[sb], ph, ctl)) ok = false;
         tc_fence_after();
@@ -630,14 +642,18 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::kThreads, 1)
         warp_arrive(&sm.p_ready[sb], lane);
       }
       ok = __all_sync(kFull, ok);
-      const uint32_t lastt = tile + nt - 1;
-      if (!warp_wait(&sm.pv_done[lastt & 1], (lastt >> 1) & 1, ctl)) ok = false;
-      tc_fence_after();
-      // the rows' sums over the keys; results turned to a warp a row
+      // while the last product runs: the next item and its words, the rows' sums over the keys
+      const Item<MODE> &cur = sm.items[k & 1];  // (this one: its place is not free yet)
+      there = ok && next_item(k + 1);
+      if (there) ahead = words_of(it);
       const float sum = over_lanes(l, lane, [](float a, float b) { return a + b; });
       if (!(lane & 1)) sm.part[grp][wi][few_row(lane)] = sum;
       saw = __reduce_or_sync(kFull, saw);
       if (lane == 0) sm.seen[grp][wi] = saw;
+      const uint32_t lastt = tile + nt - 1;
+      if (!warp_wait(&sm.pv_done[lastt & 1], (lastt >> 1) & 1, ctl)) ok = false;
+      tc_fence_after();
+      // results turned to a warp a row
       uint32_t o[R];
       tmem_ld_rows(tmem + lanes + 128 + (k & 1) * 64 + first, o);
       tc_fence_before();
@@ -652,38 +668,43 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::kThreads, 1)
       if (bad) atomicOr(&sm.bad[grp], bad);
       sync_four(grp);
       const uint32_t seen = sm.seen[grp][0] | sm.seen[grp][1] | sm.seen[grp][2] | sm.seen[grp][3];
+      const float(&p4)[4][R] = sm.part[grp];
       bad = sm.bad[grp];
-      // rows in memory, a warp a row: results, or parts in the CTA's slot or the rows' own places
-      float *const slot = p.ws + p.slots + ((long long)blockIdx.x * 2 + (it.part & 1)) * Cfg<D, MODE>::kSlotFloats;
-      const long long kind = MODE == kShared ? (long long)(flags_of(it) & kHasNodes) * p.T * p.Hq : 0;
+      if (bad) {  // what another row's NaN has spoilt is summed again
+#pragma unroll 1
+        for (int r = wi; r < rows; r += 4)
+          if (bad >> r & 1u)
+            few_again<D, MODE>(p, cur, first + r, ref[r] == -INFINITY ? 0.0f : -ref[r] * c, turn + r * 128);
+      }
+      // Rows in memory, a warp a row: results, or parts in the CTA's slot or the rows' own
+      // places.
+      constexpr int V = D / 32;
+      const int part = cur.part;
+      float *const slot = p.ws + p.slots + ((long long)blockIdx.x * 2 + (part & 1)) * Cfg<D, MODE>::kSlotFloats;
+      const long long kind = MODE == kShared ? (long long)(flags_of(cur) & kHasNodes) * p.T : 0;
 #pragma unroll 1
       for (int r = wi; r < rows; r += 4) {
-        constexpr int V = D / 32;
-        const int row = first + r, nd = row / G, hd = it.hk * G + row - nd * G, node = it.a0 + it.r0 + nd;
-        const float(&p4)[4][R] = sm.part[grp];
-        const float total = (p4[0][r] + p4[1][r]) + (p4[2][r] + p4[3][r]), m = ref[r];
+        const int row = first + r, nd = div_small(row, G);
+        const int node = cur.a0 + cur.r0 + nd, hd = cur.hk * G + row - nd * G;
+        const float m = ref[r], total = (p4[0][r] + p4[1][r]) + (p4[2][r] + p4[3][r]);
         const bool any = seen >> r & 1u;
-        float y[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) y[e] = turn[r * 128 + lane * V + e];
-        if (bad >> r & 1u)  // what another row's NaN has spoilt is summed again
-          few_again<D, MODE>(p, it, row, m == -INFINITY ? 0.0f : -m * c, turn + r * 128, y);
-        if (it.part < 0) {
+        const float *y = turn + r * 128 + lane * V;
+        if (part < 0) {
           const float inv = 1.0f / total;
           uint16_t *out = p.out.ptr + (long long)node * p.out.tok + hd * p.out.head + lane * V;
 #pragma unroll
           for (int e = 0; e < V; e += 2)
             reinterpret_cast<uint32_t *>(out)[e / 2] = any ? pack_bf16x2(y[e] * inv, y[e + 1] * inv) : 0u;
         } else {
-          const long long own = kind + (long long)node * p.Hq + hd;
-          float *to = it.part == 2 ? p.plan.rows + own * D : slot + row * D;
-          float *stat = it.part == 2 ? p.plan.stats + own * 2 : slot + D * kRowsT + row;
-#pragma unroll
-          for (int e = 0; e < V; ++e) to[lane * V + e] = y[e];
+          const long long own = (kind + node) * p.Hq + hd;
+          float *to = (part == 2 ? p.plan.rows + own * D : slot + row * D) + lane * V;
+          if constexpr (V == 4) *reinterpret_cast<float4 *>(to) = *reinterpret_cast<const float4 *>(y);
+          else *reinterpret_cast<float2 *>(to) = *reinterpret_cast<const float2 *>(y);
           if (lane == 0) {
             // (a sum of 0 says that the row sees nothing of the part)
+            float *stat = part == 2 ? p.plan.stats + own * 2 : slot + D * kRowsT + row;
             stat[0] = m;
-            stat[it.part == 2 ? 1 : kRowsT] = !any ? 0.0f : m == -INFINITY ? 1.0f : total;
+            stat[part == 2 ? 1 : kRowsT] = !any ? 0.0f : m == -INFINITY ? 1.0f : total;
           }
         }
       }

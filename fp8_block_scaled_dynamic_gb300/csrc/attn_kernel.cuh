@@ -288,19 +288,28 @@ __device__ __forceinline__ Seq find_seq(const AttnParams &p, const Prefix &pre, 
 // a lane adds up `per` of them, zeros behind the last one.  (Worked out from the
 // records themselves, 256 of them took a CTA 4 us before its first load.)
 __host__ __device__ __forceinline__ int units_per_lane(int records) { return ((records + 31) / 32 + 3) / 4 * 4; }
+constexpr uint32_t kStrips = 0x80000000u;  // bit of a record's units: not one strip (row group of a kv head), but several
 template <int MODE>
 struct PlanUnits {
   int before, sum, total;  // of this lane's records
+  int4 own;                // its records' units, if there are four a lane, and whether that is so and each is a strip
+  bool alone;
   int b = -1, base = 0, units = 0;  // the record found last
   __device__ __forceinline__ void read(const AttnParams &p, int lane) {
     const int per = units_per_lane(p.plan.n);
     const int4 *at = reinterpret_cast<const int4 *>(p.plan.units + lane * per);
     sum = 0;
+    uint32_t some = 0;
+    int4 x;
 #pragma unroll 4
     for (int i = 0; i < per / 4; ++i) {
-      const int4 x = __ldg(at + i);
+      x = __ldg(at + i);
+      some |= (uint32_t)(x.x | x.y | x.z | x.w);
+      x.x &= ~kStrips, x.y &= ~kStrips, x.z &= ~kStrips, x.w &= ~kStrips;
       sum += (x.x + x.y) + (x.z + x.w);
     }
+    own = x;
+    alone = !__any_sync(0xFFFFFFFFu, some & kStrips) && per == 4;
     int incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -316,11 +325,11 @@ struct PlanUnits {
       const int lane = __ffs(__ballot_sync(0xFFFFFFFFu, u >= before && u < before + sum)) - 1;
       base = __shfl_sync(0xFFFFFFFFu, before, lane);
       b = lane * units_per_lane(p.plan.n);
-      units = __ldg(p.plan.units + b);
+      units = __ldg(p.plan.units + b) & ~kStrips;
     }
     while (u >= base + units) {
       base += units;
-      units = __ldg(p.plan.units + ++b);
+      units = __ldg(p.plan.units + ++b) & ~kStrips;
     }
     of = b;
     u -= base;
@@ -475,6 +484,54 @@ struct Small {
   }
 };
 
+// Strips (at most 128, a lane has the tiles of four and the units before them) cut
+// into chunks of at least `least` tiles, at most four more, such that all have a CTA:
+// this one's chunk as units x <= u < y, the CTA z of its strip's last chunk, and w = 0
+// if no such length is.  A second item costs a CTA of the kernel of few rows 3 to 6 us:
+// 64 strips of 19 tiles, two chunks each, 35.4 us instead of 36.5 as equal shares, 64
+// of 9 18.4 instead of 20.1.  (Out of line: most calls have no use for it, and fetching
+// its code cost them 0.7 us.)
+__device__ __noinline__ int4 chunk_of_strips(int4 own, int before, int least, int ctas) {
+  constexpr unsigned kFull = 0xFFFFFFFFu;
+  const int lane = threadIdx.x & 31, c = blockIdx.x;
+  const int tiles[4] = {own.x, own.y, own.z, own.w};
+  for (int chunk = least; chunk < least + 5; ++chunk) {
+    int pieces[4], mine = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mine += pieces[k] = div_small(tiles[k] + chunk - 1, chunk);
+    if (__reduce_add_sync(kFull, mine) > ctas) continue;
+    int at = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(kFull, at, o);
+      if (lane >= o) at += x;
+    }
+    at -= mine;
+    int4 r = make_int4(0, 0, 0, 1);
+    bool has = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = c - at, n = pieces[k];
+      if (i >= 0 && i < n) {
+        const int q = div_small(tiles[k], n), rest = tiles[k] - q * n;
+        has = true;
+        r.x = before + share_begin(i, q, rest);
+        r.y = before + share_begin(i + 1, q, rest);
+        r.z = at + n - 1;
+      }
+      at += n;
+      before += tiles[k];
+    }
+    const unsigned who = __ballot_sync(kFull, has);
+    const int from = who ? __ffs(who) - 1 : 0;  // (none: an empty range)
+    r.x = __shfl_sync(kFull, r.x, from);
+    r.y = __shfl_sync(kFull, r.y, from);
+    r.z = __shfl_sync(kFull, r.z, from);
+    return r;
+  }
+  return make_int4(0, 0, 0, 0);
+}
+
 // Walks the items of one CTA.
 // Prompt: row groups from the last number to the first, dealt over the CTAs there
 // and back.  A sequence's later row groups have more keys, so that within a long
@@ -489,9 +546,10 @@ template <int MODE>
 struct Walk {
   int cur, end, q, r;  // tree: this CTA's units, the shares; prompt: the round, the number of items
   int chunk;           // tree: most key tiles of a chunk, 0: equal ranges
+  int last;            // planned: the range is a chunk, and this the CTA of the strip's last one; -1: equal ranges
   int span;            // tokens (nodes) of a row group
   int ctas;            // that share the work
-  __device__ __forceinline__ Walk(int U, int span, int ctas) : chunk(0), span(span), ctas(ctas) {
+  __device__ __forceinline__ Walk(int U, int span, int ctas) : chunk(0), last(-1), span(span), ctas(ctas) {
     if (paged(MODE)) {
       q = U / ctas;
       r = U - q * ctas;
@@ -514,6 +572,13 @@ struct Walk {
 #pragma unroll
     for (int i = 2; i >= 0; --i)
       if (chunks[i] <= ctas) chunk = least + i;
+  }
+  // The same for a plan's records, where they are a strip each and four a lane: a chunk
+  // instead of the range.
+  __device__ __forceinline__ void choose_chunk(const PlanUnits<MODE> &b) {
+    if (q == 0 || !b.alone) return;
+    const int4 x = chunk_of_strips(b.own, b.before, q + (r > 0), ctas);
+    if (x.w) cur = x.x, end = x.y, last = x.z;
   }
   // this CTA's only item, a chunk; returns the last CTA of the row group's chunks
   __device__ __forceinline__ int one_chunk(const AttnParams &p, const Small<MODE> &b, int tq, Item<MODE> &it) {
@@ -1157,6 +1222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool going_on = false;
       if constexpr (TREE) {
         if (few) walk.choose_chunk(small);
+        else if constexpr (planned(MODE)) walk.choose_chunk(planned_units);
       }
       for (int k = 0;; ++k) {
         Item<MODE> w;
@@ -1171,8 +1237,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               else return find_seq<MODE>(p, sm.pre, 2 * TQ, u, b, found);
             });
             if (w.t1 > w.t0 && w.part == 1)
-              last = share_owner(share_begin(blockIdx.x + 1, walk.q, walk.r) + w.nct + (flags_of(w) & kHasNodes) - 1 - w.t1,
-                                 walk.q, walk.r);
+              last = planned(MODE) && walk.last >= 0
+                         ? walk.last
+                         : share_owner(share_begin(blockIdx.x + 1, walk.q, walk.r) + w.nct + (flags_of(w) & kHasNodes) - 1 - w.t1,
+                                       walk.q, walk.r);
           }
         } else {
           walk.next(p, TQ, w, [&](int &u, int &b) {

@@ -49,6 +49,11 @@ struct Sum {
   __device__ int operator()(int a, int b) const { return a + b; }
 };
 
+// A record's units (PlanUnits): strips, key tiles of each.
+__device__ __forceinline__ int units_of(int strips, int tiles) {
+  return (int)((uint32_t)(strips * tiles) | (strips > 1 ? kStrips : 0u));
+}
+
 // ------------------------------------------------------------------ shared
 constexpr int kPlanThreads = 1024;  // at most: a thread a sequence, where there are as many
 constexpr int kPlanOwn = kAttnMaxSeqs / kPlanThreads;
@@ -134,7 +139,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     r.list = (long long)g0 * a.ld_table;
     r.flags = kJoined;
     rec[g] = r;
-    to.units[0][g] = (r.n + to.span[0] - 1) / to.span[0] * a.Hkv * ((len + kKeys - 1) / kKeys);
+    to.units[0][g] = units_of((r.n + to.span[0] - 1) / to.span[0] * a.Hkv, (len + kKeys - 1) / kKeys);
   }
   for (int g = ng + tid; g < 32 * units_per_lane(ng); g += threads) to.units[0][g] = 0;
   __syncthreads();
@@ -151,7 +156,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     r.list = (long long)b * a.ld_table + len / page;
     r.flags = kHasNodes | (len > 0 ? kJoined : 0);
     rec[ng + b] = r;
-    to.units[1][b] = (r.n + to.span[1] - 1) / to.span[1] * a.Hkv * ((r.ctx + kKeys - 1) / kKeys + 1);
+    to.units[1][b] = units_of((r.n + to.span[1] - 1) / to.span[1] * a.Hkv, (r.ctx + kKeys - 1) / kKeys + 1);
     for (int x = a0; x < a1; ++x) to.info[x] = x - a0 < kAttnMaxNodes ? len > 0 : -1;
   }
   for (int b = B + tid; b < 32 * units_per_lane(B); b += threads) to.units[1][b] = 0;
@@ -167,11 +172,11 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     float work[2] = {0.0f, 0.0f};
     for (int g = tid; g < ng; g += threads) {
       const int n = s_a0[s_g[g + 1]] - s_a0[s_g[g]];
-      work[0] += 2.0f * (float)to.units[0][g] + (s_len[g] > 0 ? 5.0f : 0.0f) * (float)((n + to.span[0] - 1) / to.span[0] * a.Hkv);
+      work[0] += 2.0f * (float)(to.units[0][g] & ~kStrips) + (s_len[g] > 0 ? 5.0f : 0.0f) * (float)((n + to.span[0] - 1) / to.span[0] * a.Hkv);
     }
     for (int b = tid; b < B; b += threads) {
       const int n = min(s_a0[b + 1] - s_a0[b], kAttnMaxNodes);
-      work[1] += (float)to.units[1][b] + 3.0f * (float)((n + to.span[1] - 1) / to.span[1] * a.Hkv);
+      work[1] += (float)(to.units[1][b] & ~kStrips) + 3.0f * (float)((n + to.span[1] - 1) / to.span[1] * a.Hkv);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -216,7 +221,8 @@ __global__ void __launch_bounds__(kListThreads) sparse_plan_kernel(const SparseP
   int *list = to.list;
   unsigned long long *names = to.names;
   pdl_wait();
-  if (tid * 32 < a.table_cols) prefetch_l1(a.table + (long long)b * a.ld_table + tid * 32);  // (read at the end)
+  const int *table = a.table + (long long)b * a.ld_table;
+  if (tid * 32 < a.table_cols) prefetch_l1(table + tid * 32);  // (read at the end)
   const int c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1), raw = __ldg(a.ctx + b);
   int top = 0;
   for (int i = tid; i <= b; i += kListThreads) top = max(top, min(max(__ldg(a.cu + i), 0), a.T));
@@ -273,7 +279,7 @@ __global__ void __launch_bounds__(kListThreads) sparse_plan_kernel(const SparseP
     r.list = base;
     r.flags = kHasNodes | (n > 1 ? kLists : 0);
     to.rec[b * a.Hkv + h] = r;
-    to.units[b * a.Hkv + h] = (n + to.span - 1) / to.span * ((r.ctx + kKeys - 1) / kKeys + 1);
+    to.units[b * a.Hkv + h] = units_of((n + to.span - 1) / to.span, (r.ctx + kKeys - 1) / kKeys + 1);
   }
   if (b == (int)gridDim.y - 1 && h == (int)gridDim.x - 1) {
     const int V = a.B * a.Hkv;
