@@ -255,20 +255,21 @@ __global__ void __launch_bounds__(kListThreads) sparse_plan_kernel(const SparseP
   const long long base = ((long long)a0 * a.Hkv + (long long)h * n) * p.n_sel;
   for (int i = w0; i < w1; ++i) {
     s_before[i] = at;
-    for (uint32_t bits = s_bits[i]; bits; bits &= bits - 1) {
-      list[base + at] = __ldg(a.table + (long long)b * a.ld_table + i * 32 + __ffs(bits) - 1);
-      if (n > 1) names[base + at] = 0;
-      ++at;
+    at += __popc(s_bits[i]);
+  }
+  if (n > 1)
+    for (int i = tid; i < count; i += kListThreads) names[base + i] = 0;
+  __syncthreads();
+  // (several nodes name a page: they write the same number)
+  for (int e = tid; e < total; e += kListThreads) {
+    int node;
+    const int j = named(e, node);
+    if (j >= 0 && j < P) {
+      const long long x = base + s_before[j >> 5] + __popc(s_bits[j >> 5] & ((1u << (j & 31)) - 1u));
+      list[x] = __ldg(table + j);
+      if (n > 1) atomicOr(names + x, 1ull << node);
     }
   }
-  __syncthreads();
-  if (n > 1)
-    for (int e = tid; e < total; e += kListThreads) {
-      int node;
-      const int j = named(e, node);
-      if (j >= 0 && j < P)
-        atomicOr(names + base + s_before[j >> 5] + __popc(s_bits[j >> 5] & ((1u << (j & 31)) - 1u)), 1ull << node);
-    }
   if (tid == 0) {
     const bool has_last = P > 0 && (s_bits[(P - 1) >> 5] >> ((P - 1) & 31) & 1u);
     PlanRec r = {};
