@@ -126,9 +126,10 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     if (of[i] >= 0) atomicMin(&s_len[of[i]], ctx[i]);
   }
   __syncthreads();
+  float work[2] = {0.0f, 0.0f};  // us of one CTA, see below
   for (int g = tid; g < ng; g += threads) {
     const int g0 = s_g[g], g1 = s_g[g + 1], raw = __ldg(p.prefix + g);
-    const int len = g1 > g0 ? min(max(raw, 0), s_len[g]) / page * page : 0;
+    const int len = g1 > g0 ? min(max(raw, 0), s_len[g]) & -page : 0;  // (page: a power of two)
     bad |= g1 > g0 && raw != len;
     s_len[g] = len;
     PlanRec r = {};
@@ -139,7 +140,9 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     r.list = (long long)g0 * a.ld_table;
     r.flags = kJoined;
     rec[g] = r;
-    to.units[0][g] = units_of((r.n + to.span[0] - 1) / to.span[0] * a.Hkv, (len + kKeys - 1) / kKeys);
+    const int strips = div_small(r.n + to.span[0] - 1, to.span[0]) * a.Hkv, tiles = (len + kKeys - 1) / kKeys;
+    to.units[0][g] = units_of(strips, tiles);
+    work[0] += len > 0 ? (float)strips * (2.0f * (float)tiles + 5.0f) : 0.0f;
   }
   for (int g = ng + tid; g < 32 * units_per_lane(ng); g += threads) to.units[0][g] = 0;
   __syncthreads();
@@ -153,10 +156,12 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     r.n = min(a1 - a0, kAttnMaxNodes);
     r.ctx = ctx[i] - len;
     r.hk = -1;
-    r.list = (long long)b * a.ld_table + len / page;
+    r.list = (long long)b * a.ld_table + (len >> (31 - __clz(page)));
     r.flags = kHasNodes | (len > 0 ? kJoined : 0);
     rec[ng + b] = r;
-    to.units[1][b] = units_of((r.n + to.span[1] - 1) / to.span[1] * a.Hkv, (r.ctx + kKeys - 1) / kKeys + 1);
+    const int strips = div_small(r.n + to.span[1] - 1, to.span[1]) * a.Hkv, tiles = (r.ctx + kKeys - 1) / kKeys + 1;
+    to.units[1][b] = units_of(strips, tiles);
+    work[1] += (float)strips * (float)(tiles + 3);
     for (int x = a0; x < a1; ++x) to.info[x] = x - a0 < kAttnMaxNodes ? len > 0 : -1;
   }
   for (int b = B + tid; b < 32 * units_per_lane(B); b += threads) to.units[1][b] = 0;
@@ -169,26 +174,17 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
   // one held up the other's (64 requests behind 16384 tokens 103 us, 94 one after the
   // other).
   if (ng > 0) {
-    float work[2] = {0.0f, 0.0f};
-    for (int g = tid; g < ng; g += threads) {
-      const int n = s_a0[s_g[g + 1]] - s_a0[s_g[g]];
-      work[0] += 2.0f * (float)(to.units[0][g] & ~kStrips) + (s_len[g] > 0 ? 5.0f : 0.0f) * (float)((n + to.span[0] - 1) / to.span[0] * a.Hkv);
-    }
-    for (int b = tid; b < B; b += threads) {
-      const int n = min(s_a0[b + 1] - s_a0[b], kAttnMaxNodes);
-      work[1] += (float)(to.units[1][b] & ~kStrips) + 3.0f * (float)((n + to.span[1] - 1) / to.span[1] * a.Hkv);
-    }
+    float *const s_work = reinterpret_cast<float *>(s_len);  // (read for the last time before the barrier)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) work[i] += __shfl_xor_sync(kFull, work[i], o);
-      __syncthreads();
-      if ((tid & 31) == 0) reinterpret_cast<float *>(s_warp)[tid >> 5] = work[i];
-      __syncthreads();
-      work[i] = 0.0f;
-      for (int w = 0; w < threads / 32; ++w) work[i] += reinterpret_cast<float *>(s_warp)[w];
-    }
+    __syncthreads();
+    if ((tid & 31) == 0) s_work[tid >> 5] = work[0], s_work[32 + (tid >> 5)] = work[1];
+    __syncthreads();
     if (tid == 0) {
+      work[0] = work[1] = 0.0f;
+      for (int w = 0; w < threads / 32; ++w) work[0] += s_work[w], work[1] += s_work[32 + w];
       const int first = (int)((float)to.most * work[0] / (work[0] + work[1]) + 0.5f);
       const int x = max(min(first, to.most - 1), 1);
       const bool both = work[0] + work[1] < kShortWork * (float)to.most;
