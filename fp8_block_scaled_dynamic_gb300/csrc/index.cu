@@ -184,7 +184,8 @@ __global__ void __launch_bounds__(kIndexThreads, 2) index_kernel(const IndexPara
 constexpr int kSelectWarps = 8;  // most warps of a block
 template <bool MANY>
 constexpr int kWarps = MANY ? 8 : 4;
-constexpr int kSelectGroups = 8;            // most groups of eight columns (query heads) in a pass, or one node's
+constexpr int kSelectGroups = 8;            // groups of eight columns (query heads) that are multiplied at once
+constexpr int kSelectMost = 16;             // in a pass: one node's most
 constexpr int kSelectKeys = 12 * 1024;      // most keys of a block in shared memory, where one node's are no more
 constexpr int kSelectMostCluster = 8;
 
@@ -695,11 +696,12 @@ SelectPlan plan_select(const SelectParams &p, int sm_count) {
   SelectPlan s;
   const int G = p.Hq / p.Hkv;
   s.gp = G <= 2 ? G : G <= 4 ? 4 : (G + 7) / 8 * 8;
-  // columns for as many nodes as a sequence has on average
+  // A group where an average sequence's nodes fit in it, else as many as a pass may
+  // have: those that a sequence does not fill cost nothing, another pass 5 us.
   const long long columns = ((long long)p.N + p.B - 1) / p.B * s.gp;
   s.gp_inv = (65536 + s.gp - 1) / s.gp;
-  s.groups = columns < kSelectGroups * 8 ? (int)((columns + 7) / 8) : kSelectGroups;
-  if (s.groups < s.gp / 8) s.groups = s.gp / 8;
+  s.groups = columns <= 8 ? 1 : (kAttnMaxNodes * s.gp + 7) / 8;
+  if (s.groups > kSelectMost) s.groups = kSelectMost;
   s.cols = select_cols(p.table_cols);
   // blocks enough for every SM, as far as there are pages for their warps
   s.cluster = 1;
@@ -716,7 +718,7 @@ SelectPlan plan_select(const SelectParams &p, int sm_count) {
 template <int D, bool MANY>
 cudaError_t launch_select(const SelectParams &p, const SelectPlan &plan, cudaStream_t stream) {
   auto kern = select_kernel<D, MANY>;
-  constexpr int kMost = 16 * (D / 8) * 256 + kAttnMaxScored * 4;  // 128 heads of a kv head, and the most keys
+  constexpr int kMost = kSelectMost * (D / 8) * 256 + kAttnMaxScored * 4;  // with the most keys
   static_assert(kMost <= 225 * 1024, "shared memory");
   const size_t smem = (size_t)plan.groups * (D / 8) * 256 + (size_t)plan.slots * plan.cols * 4;
   static DeviceOnce once;
