@@ -61,12 +61,13 @@ constexpr int kPlanOwn = kAttnMaxSeqs / kPlanThreads;
 // One block: the sequences' nodes and contexts, the groups' sequences and
 // prefixes, all within their bounds, as records and their units (key tiles of row
 // groups of span[0] nodes of a group, span[1] of a sequence).
-constexpr float kShortWork = 20.0f;  // us of every CTA
+constexpr float kShortWork = 30.0f;  // us of every CTA
 struct SharedLists {
   PlanRec *rec;
   int *info, *units[2], span[2];
   int *ctas;       // of the two launches, that share their work
   int most;        // CTAs of a launch
+  float tile, strip;  // us of one CTA for a sequence's key tile, for its row group
 };
 __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedParams p, const SharedLists to) {
   __shared__ int s_a0[kAttnMaxSeqs + 1], s_len[kAttnMaxSeqs], s_warp[kPlanThreads / 32];
@@ -161,18 +162,18 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     rec[ng + b] = r;
     const int strips = div_small(r.n + to.span[1] - 1, to.span[1]) * a.Hkv, tiles = (r.ctx + kKeys - 1) / kKeys + 1;
     to.units[1][b] = units_of(strips, tiles);
-    work[1] += (float)strips * (float)(tiles + 3);
+    work[1] += (float)strips * (to.tile * (float)tiles + to.strip);
     for (int x = a0; x < a1; ++x) to.info[x] = x - a0 < kAttnMaxNodes ? len > 0 : -1;
   }
   for (int b = B + tid; b < 32 * units_per_lane(B); b += threads) to.units[1][b] = 0;
   for (int x = tid; x < s_a0[0]; x += threads) to.info[x] = -1;
   for (int x = s_a0[B] + tid; x < a.T; x += threads) to.info[x] = -1;
-  // Estimated times, us of one CTA: a prefix's key tile (two row tiles) takes 2.0 and
-  // its row group 5, a sequence's 1.0 and 3.  Where both are short, the two launches
-  // share the SMs and run beside one another (8 requests of 8 nodes behind 1024 tokens
-  // 37 us, 42 one after the other); else each has all of them, since the keys of the
-  // one held up the other's (64 requests behind 16384 tokens 103 us, 94 one after the
-  // other).
+  // Estimated times, us of one CTA: a key tile of full row tiles (a prefix's) takes 2.0
+  // and their row group 5, one of the kernel of few rows 1.0 and 3.  Where both launches
+  // are short, they share the SMs and run beside one another (8 requests of 8 nodes
+  // behind 1024 tokens 34 us, 42 one after the other; with 2000 tokens of their own
+  // behind 8192 62 and 69); else each has all of them, since the keys of the one held up
+  // the other's (64 requests behind 16384 tokens 105 us, 95 one after the other).
   if (ng > 0) {
     float *const s_work = reinterpret_cast<float *>(s_len);  // (read for the last time before the barrier)
 #pragma unroll
@@ -320,7 +321,9 @@ struct SparseWs {
 };
 
 // Sequences' rows of a kv head: where an average sequence's fit, the kernel of few
-// rows (16, 32 or 64 of them), else the one of full tiles (0).
+// rows (16, 32 or 64 of them), else the one of full tiles (0).  8 requests over 16
+// pages of 64, 8 heads a kv head: 1 node each 18.3 us, by full tiles 22.9; 4 nodes
+// 24.9 and 31.0; 8 nodes 34.7 and 37.7.
 int few_rows(const AttnParams &p) {
   const long long rows = ((long long)p.T + p.B - 1) / p.B * (p.Hq / p.Hkv);
   return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 0;
@@ -384,6 +387,8 @@ cudaError_t launch_attn_shared(const SharedParams &p, int sm_count, cudaStream_t
   to.most = paged_ctas(sm_count);
   to.span[0] = span_of(a, 0);
   to.span[1] = span_of(a, few_rows(a));
+  to.tile = few_rows(a) ? 1.0f : 2.0f;
+  to.strip = few_rows(a) ? 3.0f : 5.0f;
   const int threads = a.B < 128 ? 128 : a.B < kPlanThreads ? (a.B + 31) / 32 * 32 : kPlanThreads;
   cudaLaunchConfig_t cfg = pdl_config(dim3(1), dim3((unsigned)threads), 0, stream);
   cudaLaunchAttribute attr[1];

@@ -696,8 +696,9 @@ SelectPlan plan_select(const SelectParams &p, int sm_count) {
   SelectPlan s;
   const int G = p.Hq / p.Hkv;
   s.gp = G <= 2 ? G : G <= 4 ? 4 : (G + 7) / 8 * 8;
-  // A group where an average sequence's nodes fit in it, else as many as a pass may
-  // have: those that a sequence does not fill cost nothing, another pass 5 us.
+  // A group where an average sequence's nodes fit in it (a batch of 64 x 1024 pages 34
+  // us, with the kernel of several groups 73), else as many as a pass may have: those
+  // that a sequence does not fill cost nothing, another pass 4 us.
   const long long columns = ((long long)p.N + p.B - 1) / p.B * s.gp;
   s.gp_inv = (65536 + s.gp - 1) / s.gp;
   s.groups = columns <= 8 ? 1 : (kAttnMaxNodes * s.gp + 7) / 8;
