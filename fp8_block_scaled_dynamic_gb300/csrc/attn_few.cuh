@@ -27,6 +27,19 @@
 // Warps: four of softmax for each 16 rows (a thread with 64 rows had 24 KB of code a
 // tile, whose fetching took 3.4 us), then one each for MMAs, loads and items.
 // TMEM columns: two buffers of scores, two of results (of items in turn), 64 each.
+//
+// What bounds it, and what was measured (GB300; a copy runs at 6.8 TB/s): an item's
+// chain.  The first comes 2.3 us after the plan, its first scores 2 us later; a tile
+// follows the last after 0.6 (16 rows) to 1.4 us (64), where memory keeps up (64 KB a
+// tile and SM take 1.5 us); the last product, the results' turn and their way out 2 us.
+// - 32 requests over 32 pages of 64 each (64 / 8 heads of 128, 269 MB): 52 us, 5.1 TB/s
+//   in this kernel, 58 with plan and join.
+// - 8 trees of 8 nodes over 16 pages a node (74 MB in all): 34.5 us; one node a request:
+//   18.2.
+// Left out: a decoded token's own key added after its last part instead of a tile of its
+// own (64 requests 98 -> 106 us: the loads and the product are in the item's chain, the
+// tile is not); results of four rows unrolled (20.3 -> 21.2 us for short requests: more
+// code to fetch).
 #pragma once
 #include "attn_kernel.cuh"
 
