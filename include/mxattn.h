@@ -188,7 +188,10 @@ mxg_status kv_append(const mxg_heads *k, int64_t k_layer_stride, const mxg_heads
                      int Hkv, int D, int *ctx_out, int *dev_status, mxg_stream_t stream);
 
 /* attn_tree for sequences that share the beginning of their contexts by groups,
- * which is then read once for the group.  Group g is sequences cu_groups[g] ..
+ * which is then read once for the group: faster than attn_tree where many share
+ * much (64 sequences of a node: 67 us against 89 behind 1024 tokens, 93 against
+ * 388 behind 16384; 8 of them from 8192 tokens on), slower where few share little
+ * (8 trees of 8 nodes behind 1024 tokens 34 against 20).  Group g is sequences cu_groups[g] ..
  * cu_groups[g+1] - 1 (n_groups + 1 ints, cu_groups[0] = 0, non-decreasing,
  * cu_groups[n_groups] <= B; sequences past it share nothing); the first
  * prefix_len[g] cached tokens of each of them, a multiple of page_size, are read
