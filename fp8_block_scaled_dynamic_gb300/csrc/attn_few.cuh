@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::kThreads, 1)
           j.cnt0 = w.cnt[0];
           j.head = w.hk * G;
           j.last = last;
-          j.word = w.n;
+          j.word = MODE == kShared ? flags_of(w) & kHasNodes : w.n;
           j.ctx = w.ctx;
           reinterpret_cast<JoinItem *>(p.ws)[blockIdx.x] = j;
         }

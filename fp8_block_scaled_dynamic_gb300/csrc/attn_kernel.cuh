@@ -383,7 +383,7 @@ struct JoinItem {
   int tok, cnt0;    // first token of the rows, tokens of the first row tile
   int head;         // first query head
   int last;         // last CTA that holds a part
-  int word;         // bits of a mask word that count
+  int word;         // bits of a mask word that count; shared: 0 of a prefix, 1 of own keys
   int ctx;          // cached tokens
 };
 
@@ -1262,7 +1262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             j.cnt0 = w.cnt[0];
             j.head = w.hk * G;
             j.last = last;
-            j.word = w.n;
+            j.word = MODE == kShared ? flags_of(w) & kHasNodes : w.n;
             j.ctx = w.ctx;
             reinterpret_cast<JoinItem *>(p.ws)[blockIdx.x] = j;
           }
@@ -1760,8 +1760,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps, kJoinBlocksSm) attn_join_kern
 // parts are those of its group's prefix, in the order of the keys, and those of
 // its sequence's own keys.  Either is one part in the row's own place, or the
 // slots of the CTAs that shared it.  Prefixes and own keys were two launches, each
-// with its list of items that went on and its slots; a list is in the order of (first
-// node, kv head), so the row's item is found by bisection.
+// with its list of items that went on and its slots, or one with a list of both; of a
+// kind the list is in the order of (first node, kv head), so the row's item is found by
+// bisection.
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps, kJoinRowsBlocksSm) attn_join_rows_kernel(const AttnParams p, int ctas) {
   using C = Cfg<D, kShared>;
@@ -1782,6 +1783,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, kJoinRowsBlocksSm) attn_join_
   for (int i = 0; i < 2; ++i) {
     if ((int)threadIdx.x < ctas && p.plan.part_ws[i])
       mine[i] = reinterpret_cast<const JoinItem *>(p.plan.part_ws[i])[threadIdx.x];
+    if (mine[i].word != i) mine[i].rows = 0;  // (one list of both)
     has[i] = __ballot_sync(kFull, mine[i].rows > 0);
     if (lane == 0) s_warp[i][warp] = __popc(has[i]);
   }

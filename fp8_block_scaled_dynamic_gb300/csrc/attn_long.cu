@@ -73,7 +73,7 @@ struct SharedLists {
   int *info, *units[2], span[2];
   int *ctas;       // of the two launches, that share their work
   int most;        // CTAs of a launch
-  float tile, strip;  // us of one CTA for a sequence's key tile, for its row group
+  bool one;        // there is one launch, of all records
 };
 __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedParams p, const SharedLists to) {
   __shared__ int s_a0[kAttnMaxSeqs + 1], s_len[kAttnMaxSeqs], s_warp[kPlanThreads / 32];
@@ -151,7 +151,8 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     to.units[0][g] = units_of(strips, tiles);
     work[0] += len > 0 ? (float)strips * (2.0f * (float)tiles + 5.0f) : 0.0f;
   }
-  for (int g = ng + tid; g < 32 * units_per_lane(ng); g += threads) to.units[0][g] = 0;
+  if (!to.one)
+    for (int g = ng + tid; g < 32 * units_per_lane(ng); g += threads) to.units[0][g] = 0;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kPlanOwn; ++i) {
@@ -168,19 +169,19 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     rec[ng + b] = r;
     const int strips = div_small(r.n + to.span[1] - 1, to.span[1]) * a.Hkv, tiles = (r.ctx + kKeys - 1) / kKeys + 1;
     to.units[1][b] = units_of(strips, tiles);
-    work[1] += (float)strips * (to.tile * (float)tiles + to.strip);
+    work[1] += (float)strips * (float)(tiles + 3);
     for (int x = a0; x < a1; ++x) to.info[x] = x - a0 < kAttnMaxNodes ? len > 0 : -1;
   }
-  for (int b = B + tid; b < 32 * units_per_lane(B); b += threads) to.units[1][b] = 0;
+  const int before = to.one ? ng : 0;  // records of the list before the sequences'
+  for (int b = B + tid; b < 32 * units_per_lane(before + B) - before; b += threads) to.units[1][b] = 0;
   for (int x = tid; x < s_a0[0]; x += threads) to.info[x] = -1;
   for (int x = s_a0[B] + tid; x < a.T; x += threads) to.info[x] = -1;
-  // Estimated times, us of one CTA: a key tile of full row tiles (a prefix's) takes 2.0
-  // and their row group 5, one of the kernel of few rows 1.0 and 3.  Where both launches
-  // are short, they share the SMs and run beside one another (8 requests of 8 nodes
-  // behind 1024 tokens 34 us, 42 one after the other; with 2000 tokens of their own
-  // behind 8192 62 and 69); else each has all of them, since the keys of the one held up
-  // the other's (64 requests behind 16384 tokens 105 us, 95 one after the other).
-  if (ng > 0) {
+  // Two launches: estimated times, us of one CTA, are 2.0 for a prefix's key tile and 5
+  // for its row group, 1.0 and 3 for a sequence's.  Where both launches are short, they
+  // share the SMs and run beside one another (8 requests of 1 node behind 1024 tokens 27
+  // us, 32 one after the other); else each has all of them, since the keys of the one
+  // held up the other's (64 requests behind 16384 tokens 105 us, 95 one after the other).
+  if (ng > 0 && !to.one) {
     float *const s_work = reinterpret_cast<float *>(s_len);  // (read for the last time before the barrier)
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -327,28 +328,41 @@ struct SparseWs {
 };
 
 // Sequences' rows of a kv head: where an average sequence's fit, the kernel of few
-// rows (16, 32 or 64 of them), else the one of full tiles (0).  8 requests over 16
+// rows (16, 32 or, sparse, 64 of them), else the one of full tiles (0).  8 requests over 16
 // pages of 64, 8 heads a kv head: 1 node each 18.3 us, by full tiles 22.9; 4 nodes
 // 24.9 and 31.0; 8 nodes 34.7 and 37.7.
+template <int MODE>
 int few_rows(const AttnParams &p) {
   const long long rows = ((long long)p.T + p.B - 1) / p.B * (p.Hq / p.Hkv);
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 0;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 && MODE == kSparse ? 64 : 0;
 }
 int span_of(const AttnParams &p, int rows) { return (rows ? rows : 2 * kRowsT) / (p.Hq / p.Hkv); }
 
 template <int D, int MODE>
 cudaError_t launch_rows(const AttnParams &p, int sm_count, cudaStream_t stream) {
-  switch (few_rows(p)) {
+  switch (few_rows<MODE>(p)) {
     case 16: return launch_few<D, 16, MODE>(p, sm_count, stream);
     case 32: return launch_few<D, 32, MODE>(p, sm_count, stream);
-    case 64: return launch_few<D, 64, MODE>(p, sm_count, stream);
+    case 64:
+      if constexpr (MODE == kSparse) return launch_few<D, 64, MODE>(p, sm_count, stream);
   }
   return launch_t<D, MODE>(p, sm_count, stream);
 }
 
+// Prefixes by full tiles, and sequences beside or after them by the kernel of few rows
+// -- or all of it by full tiles in one launch.
 template <int D>
 cudaError_t launch_shared(const SharedParams &p, AttnParams a, const SharedLists &to, int sm_count, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
+  if (to.one) {
+    a.ws = a.plan.part_ws[1];
+    a.plan.rec = to.rec;
+    a.plan.units = to.units[0];
+    a.plan.ctas = to.ctas;
+    a.plan.n = p.n_groups + a.B;
+    if ((e = launch_t<D, kShared>(a, sm_count, stream)) != cudaSuccess) return e;
+    return launch_join<D, kShared>(a, sm_count, stream);
+  }
   if (p.n_groups > 0) {
     a.ws = a.plan.part_ws[0];
     a.plan.rec = to.rec;
@@ -388,13 +402,13 @@ cudaError_t launch_attn_shared(const SharedParams &p, int sm_count, cudaStream_t
   to.rec = reinterpret_cast<PlanRec *>(w + ws.rec);
   to.info = reinterpret_cast<int *>(w + ws.info);
   to.units[0] = reinterpret_cast<int *>(w + ws.units);
-  to.units[1] = to.units[0] + kAttnMaxSeqs + 128;
+  const int few = few_rows<kShared>(a);
+  to.one = few == 0;
+  to.units[1] = to.units[0] + (to.one ? p.n_groups : kAttnMaxSeqs + 128);
   to.ctas = reinterpret_cast<int *>(w + ws.ctas);
   to.most = paged_ctas(sm_count);
   to.span[0] = span_of(a, 0);
-  to.span[1] = span_of(a, few_rows(a));
-  to.tile = few_rows(a) ? 1.0f : 2.0f;
-  to.strip = few_rows(a) ? 3.0f : 5.0f;
+  to.span[1] = span_of(a, few);
   const int threads = a.B < 128 ? 128 : a.B < kPlanThreads ? (a.B + 31) / 32 * 32 : kPlanThreads;
   cudaLaunchConfig_t cfg = pdl_config(dim3(1), dim3((unsigned)threads), 0, stream);
   cudaLaunchAttribute attr[1];
@@ -405,8 +419,8 @@ cudaError_t launch_attn_shared(const SharedParams &p, int sm_count, cudaStream_t
   a.plan.info = to.info;
   a.plan.rows = reinterpret_cast<float *>(w + ws.rows);
   a.plan.stats = reinterpret_cast<float *>(w + ws.stats);
-  a.plan.part_ws[0] = p.n_groups > 0 ? reinterpret_cast<float *>(w) : nullptr;
   a.plan.part_ws[1] = reinterpret_cast<float *>(w + ws.second);
+  a.plan.part_ws[0] = to.one ? a.plan.part_ws[1] : p.n_groups > 0 ? reinterpret_cast<float *>(w) : nullptr;
   return a.D == 64 ? launch_shared<64>(p, a, to, sm_count, stream) : launch_shared<128>(p, a, to, sm_count, stream);
 }
 
@@ -419,7 +433,7 @@ cudaError_t launch_attn_sparse(const SparseParams &p, int sm_count, cudaStream_t
   to.list = reinterpret_cast<int *>(w + ws.list);
   to.units = reinterpret_cast<int *>(w + ws.units);
   to.names = reinterpret_cast<unsigned long long *>(w + ws.names);
-  to.span = span_of(a, few_rows(a));
+  to.span = span_of(a, few_rows<kSparse>(a));
   static DeviceOnce once;
   int dev = -1;
   cudaError_t e = cudaGetDevice(&dev);
