@@ -178,9 +178,10 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
   for (int x = s_a0[B] + tid; x < a.T; x += threads) to.info[x] = -1;
   // Two launches: estimated times, us of one CTA, are 2.0 for a prefix's key tile and 5
   // for its row group, 1.0 and 3 for a sequence's.  Where both launches are short, they
-  // share the SMs and run beside one another (8 requests of 1 node behind 1024 tokens 27
-  // us, 32 one after the other); else each has all of them, since the keys of the one
-  // held up the other's (64 requests behind 16384 tokens 105 us, 95 one after the other).
+  // share the SMs and run beside one another (8 requests of 1 node behind 1024 tokens, as
+  // two launches, 27 us, 32 one after the other); else each has all of them, since the
+  // keys of the one held up the other's (64 requests behind 16384 tokens 105 us, 95 one
+  // after the other).
   if (ng > 0 && !to.one) {
     float *const s_work = reinterpret_cast<float *>(s_len);  // (read for the last time before the barrier)
 #pragma unroll
@@ -331,8 +332,12 @@ struct SparseWs {
 // rows (16, 32 or, sparse, 64 of them), else the one of full tiles (0).  8 requests over 16
 // pages of 64, 8 heads a kv head: 1 node each 18.3 us, by full tiles 22.9; 4 nodes
 // 24.9 and 31.0; 8 nodes 34.7 and 37.7.
+// Shared: where sequences' strips are no more than the CTAs, full tiles too, since
+// prefixes are then in the same launch (8 requests of 1 node behind 1024 tokens 23.1 us,
+// by two launches 27.2; 16 25.5 and 32.3; but 32, 256 strips, behind 16384 76 and 66).
 template <int MODE>
-int few_rows(const AttnParams &p) {
+int few_rows(const AttnParams &p, int sm_count) {
+  if (MODE == kShared && p.B * p.Hkv <= paged_ctas(sm_count)) return 0;
   const long long rows = ((long long)p.T + p.B - 1) / p.B * (p.Hq / p.Hkv);
   return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 && MODE == kSparse ? 64 : 0;
 }
@@ -340,7 +345,7 @@ int span_of(const AttnParams &p, int rows) { return (rows ? rows : 2 * kRowsT) /
 
 template <int D, int MODE>
 cudaError_t launch_rows(const AttnParams &p, int sm_count, cudaStream_t stream) {
-  switch (few_rows<MODE>(p)) {
+  switch (few_rows<MODE>(p, sm_count)) {
     case 16: return launch_few<D, 16, MODE>(p, sm_count, stream);
     case 32: return launch_few<D, 32, MODE>(p, sm_count, stream);
     case 64:
@@ -402,7 +407,7 @@ cudaError_t launch_attn_shared(const SharedParams &p, int sm_count, cudaStream_t
   to.rec = reinterpret_cast<PlanRec *>(w + ws.rec);
   to.info = reinterpret_cast<int *>(w + ws.info);
   to.units[0] = reinterpret_cast<int *>(w + ws.units);
-  const int few = few_rows<kShared>(a);
+  const int few = few_rows<kShared>(a, sm_count);
   to.one = few == 0;
   to.units[1] = to.units[0] + (to.one ? p.n_groups : kAttnMaxSeqs + 128);
   to.ctas = reinterpret_cast<int *>(w + ws.ctas);
@@ -433,7 +438,7 @@ cudaError_t launch_attn_sparse(const SparseParams &p, int sm_count, cudaStream_t
   to.list = reinterpret_cast<int *>(w + ws.list);
   to.units = reinterpret_cast<int *>(w + ws.units);
   to.names = reinterpret_cast<unsigned long long *>(w + ws.names);
-  to.span = span_of(a, few_rows<kSparse>(a));
+  to.span = span_of(a, few_rows<kSparse>(a, sm_count));
   static DeviceOnce once;
   int dev = -1;
   cudaError_t e = cudaGetDevice(&dev);

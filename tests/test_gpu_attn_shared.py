@@ -199,3 +199,48 @@ def test_large_values(nodes):
     c.check(want, "as they are")
     c.v, c.vc = c.v * 2.0**76, c.vc * 2.0**76
     assert torch.equal(c.run(), want * 2.0**76)
+
+
+# more sequences x kv heads than SMs, few rows each: prefixes and sequences are launches of their own, beside one another
+# where both are short (all but the last)
+MANY = [
+    ([48], [512], [7 * i % 300 for i in range(48)], [1] * 48, 8, 4, 64),
+    ([20, 25], [1024, 160], [11 * i % 200 for i in range(50)], [i % 4 for i in range(50)], 16, 4, 32),
+    ([], [], [i * 5 % 400 for i in range(160)], [1 + i % 3 for i in range(160)], 8, 1, 16),
+    ([1, 30, 0, 2], [48, 2000, 16, 0], [3 * i % 170 for i in range(40)], [1 + (i == 7) * 63 for i in range(40)], 40, 8, 16),
+    ([48], [12288], [37 * i % 509 for i in range(48)], [1] * 48, 64, 8, 64),
+]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("i", range(len(MANY)))
+def test_many_sequences_of_few_rows(D, i):
+    groups, prefix, tails, nodes, Hq, Hkv, page = MANY[i]
+    c = Case(groups, prefix, tails, nodes, Hq, Hkv, D, page, seed=30 + i)
+    out = c.run()
+    c.check(out, MANY[i][:2])
+    assert torch.equal(c.run(), out)
+
+
+def test_many_sequences_scores_masks_and_values():
+    """The same launches: scores far apart, masks that leave nothing, NaN that nobody sees, large values."""
+    c = Case([30, 20], [256, 0], [13 * i % 300 for i in range(52)], [1 + i % 2 for i in range(52)], 8, 4, 128, 64, seed=40)
+    c.scale = 3.0
+    for i, t in enumerate([0, 100, 255, 256]):
+        c.kc[int(c.tab[0, t // 64]), t % 64, i % 4] = c.q[0, (i % 4) * 2] * (0.5 if i % 2 else 2.0)
+    c.mask[::3] = 0
+    c.check(c.run(scale=3.0), "far apart")
+    used = torch.zeros(c.kc.shape[0], dtype=torch.bool, device=dev())
+    tab = long_ref.shared_table(c.tab, c.groups, c.prefix, c.page)
+    for b, n in enumerate(c.ctx):
+        used[tab[b, :-(-n // c.page)].long()] = True
+    want = c.run(scale=3.0)
+    c.kc[~used], c.vc[~used] = float("nan"), float("inf")
+    for b, n in enumerate(c.ctx):
+        if n % c.page:
+            c.kc[int(tab[b, n // c.page]), n % c.page:] = float("nan")
+            c.vc[int(tab[b, n // c.page]), n % c.page:] = float("nan")
+    assert torch.equal(c.run(scale=3.0), want)
+    c.vc[used] = torch.nan_to_num(c.vc[used], nan=0.0) * 2.0**76
+    c.v = c.v * 2.0**76
+    assert torch.equal(c.run(scale=3.0), want * 2.0**76)
