@@ -189,14 +189,14 @@ mxg_status kv_append(const mxg_heads *k, int64_t k_layer_stride, const mxg_heads
 
 /* attn_tree for sequences that share the beginning of their contexts by groups,
  * which is then read once for the group: faster than attn_tree where many share
- * much (64 sequences of a node: 67 us against 89 behind 1024 tokens, 93 against
- * 388 behind 16384; 8 of them from 8192 tokens on), slower where few share little
- * (8 trees of 8 nodes behind 1024 tokens 34 against 20).  Group g is sequences cu_groups[g] ..
- * cu_groups[g+1] - 1 (n_groups + 1 ints, cu_groups[0] = 0, non-decreasing,
- * cu_groups[n_groups] <= B; sequences past it share nothing); the first
- * prefix_len[g] cached tokens of each of them, a multiple of page_size, are read
- * from the pages in the block table's row of the group's first sequence (where
- * the others name the same pages, the result is attn_tree's).  ctx_len counts
+ * much (64 sequences of a node: 68 us against 90 behind 1024 tokens, 93 against
+ * 388 behind 16384; 8 of them 26 against 37 behind 8192), slower where few share
+ * little (8 trees of 8 nodes behind 1024 tokens 31 against 20).  Group g is
+ * sequences cu_groups[g] .. cu_groups[g+1] - 1 (n_groups + 1 ints, cu_groups[0] =
+ * 0, non-decreasing, cu_groups[n_groups] <= B; sequences past it share nothing);
+ * the first prefix_len[g] cached tokens of each of them, a multiple of page_size,
+ * are read from the pages in the block table's row of the group's first sequence
+ * (where the others name the same pages, the result is attn_tree's).  ctx_len counts
  * them: it is at least prefix_len[g] throughout the group.  Everything else is as
  * for attn_tree.
  * n_groups <= B; n_groups 0: cu_groups and prefix_len may be NULL.
