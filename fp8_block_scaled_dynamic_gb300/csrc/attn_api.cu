@@ -320,7 +320,9 @@ mxg_status attn_shared(const mxg_heads *q, const mxg_heads *k, const mxg_heads *
   int sm = 0;
   if ((st = device_sms(&sm)) != MXG_OK) return st;
   if ((st = check_ws(opts, mxg::attn_shared_ws_bytes(N, Hq, D, sm))) != MXG_OK) return st;
-  if ((st = check_units(N, Hq, Hkv, 2LL * (N < B ? N : B), table_cols, cache->page_size)) != MXG_OK) return st;
+  // (prefixes' full row groups besides the sequences')
+  const long long starts = 2LL * (N < B ? N : B) + N / (256 / (Hq / Hkv));
+  if ((st = check_units(N, Hq, Hkv, starts, table_cols, cache->page_size)) != MXG_OK) return st;
   if (N == 0) return MXG_OK;
   mxg::SharedParams p = {};
   p.a = attn_params(q, k, v, cu_nodes, B, N, Hq, Hkv, D, scale, out, opts);
