@@ -207,6 +207,7 @@ struct SelectPlan {
   int gp;       // columns of a node: Hq / Hkv rounded up to 1, 2, 4 or a multiple of 8
   int gp_inv;   // 2^16 / gp, rounded up: c / gp = c * gp_inv >> 16 for the columns of a pass (a division took 25 instructions)
   int groups;   // of eight columns in a pass
+  int shares;   // clusters of a sequence and kv head, which take its passes in turn
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -465,16 +466,17 @@ __global__ void __launch_bounds__(32 * kWarps<MANY>, MANY ? 1 : 4) select_kernel
   auto row_of = [&](int node) { return p.sel + ((long long)(a0 + node) * p.Hkv + h) * p.n_sel; };
   if (n == 0) return;
   if (P <= p.n_sel) {  // (the whole cluster)
-    for (int node = rank; node < n; node += cs)
+    for (int node = rank + cs * blockIdx.z; node < n; node += cs * gridDim.z)
       for (int i = threadIdx.x; i < p.n_sel; i += kThreads) row_of(node)[i] = i < P ? i : -1;
     return;
   }
-  cluster_begun();
   const int lg = lane_shift(P), tiles = (P + 15) / 16, stride = cs * kWarps<MANY>;
   // nodes of a pass: as many as have a slot and columns
   auto node_of = [&](int c) { return c * plan.gp_inv >> 16; };
   const int pass = min(plan.slots * cs, node_of(plan.groups * 8));
-  for (int n0 = 0; n0 < n; n0 += pass) {
+  if (pass * (int)blockIdx.z >= n) return;  // (the whole cluster)
+  cluster_begun();
+  for (int n0 = pass * blockIdx.z; n0 < n; n0 += pass * gridDim.z) {
     const int nodes = min(pass, n - n0), groups = (nodes * gp + 7) / 8;
     int tile = rank * kWarps<MANY> + warp;
     if (tile < tiles) {  // the first pages come into L2 while q is made ready
@@ -494,7 +496,7 @@ __global__ void __launch_bounds__(32 * kWarps<MANY>, MANY ? 1 : 4) select_kernel
     prepare_q<D, kWarps<MANY>>(p.q.ptr + (long long)(a0 + n0) * p.q.tok + (long long)(h * G) * p.q.head, p.q.tok, p.q.head,
                                nodes, G, gp, s_q);
     __syncthreads();
-    if (n0 == 0) cluster_all_begun();
+    if (n0 == pass * (int)blockIdx.z) cluster_all_begun();
     // scores
     // (what follows is worked out anew in each pass: held through the other phases, it
     // made this one spill: a batch of 64 x 1024 pages 45 us instead of 33)
@@ -693,7 +695,7 @@ __global__ void __launch_bounds__(32 * kWarps<MANY>, MANY ? 1 : 4) select_kernel
       if (lg == 3) choose<3>(keys, P, p.first, p.last, p.n_sel, row_of(n0 + node), ch);
       else choose<4>(keys, P, p.first, p.last, p.n_sel, row_of(n0 + node), ch);
     }
-    if (n0 + pass < n) cluster_sync();  // (before the keys are written again)
+    if (n0 + pass * (int)gridDim.z < n) cluster_sync();  // (before the keys are written again)
   }
 }
 
@@ -707,12 +709,11 @@ SelectPlan plan_select(const SelectParams &p, int sm_count) {
   const int G = p.Hq / p.Hkv;
   s.gp = G <= 2 ? G : G <= 4 ? 4 : (G + 7) / 8 * 8;
   // A group where an average sequence's nodes fit in it (a batch of 64 x 1024 pages 34
-  // us, with the kernel of several groups 73), else as many as a pass may have: those
-  // that a sequence does not fill cost nothing, another pass 4 us.
+  // us, with the kernel of several groups 73), else eight.
   const long long columns = ((long long)p.N + p.B - 1) / p.B * s.gp;
   s.gp_inv = (65536 + s.gp - 1) / s.gp;
-  s.groups = columns <= 8 ? 1 : (kAttnMaxNodes * s.gp + 7) / 8;
-  if (s.groups > kSelectMost) s.groups = kSelectMost;
+  s.groups = columns <= 8 ? 1 : kSelectGroups;
+  if (s.groups < s.gp / 8) s.groups = s.gp / 8;
   s.cols = select_cols(p.table_cols);
   // blocks enough for every SM, as far as there are pages for their warps
   s.cluster = 1;
@@ -720,6 +721,17 @@ SelectPlan plan_select(const SelectParams &p, int sm_count) {
   while (s.cluster < kSelectMostCluster && (long long)p.B * p.Hkv * s.cluster < 2LL * sm_count &&
          s.cluster * 16 * (s.groups > 1 ? kWarps<true> : kWarps<false>) < p.table_cols)
     s.cluster *= 2, ++s.shift;
+  // A sequence's passes beside one another, as far as there are SMs; without room for
+  // two the most columns in a pass instead (those that a sequence does not fill cost
+  // nothing, another pass 4 us).
+  const long long room = 2LL * sm_count / ((long long)p.B * p.Hkv * s.cluster);
+  const int nodes = p.N < kAttnMaxNodes ? p.N : kAttnMaxNodes, pass = s.groups * 8 / s.gp, passes = (nodes + pass - 1) / pass;
+  s.shares = room < 2 ? 1 : room < passes ? (int)room : passes;
+  if (s.shares == 1 && s.groups > 1) {
+    s.groups = (nodes * s.gp + 7) / 8;
+    if (s.groups > kSelectMost) s.groups = kSelectMost;
+    if (s.groups < 2) s.groups = 2;  // (the kernel of several)
+  }
   const int most = (s.groups * 8 / s.gp + s.cluster - 1) / s.cluster;  // as many nodes as have columns
   s.slots = s.cols == 0 ? most : kSelectKeys / s.cols;
   s.slots = s.slots < 1 ? 1 : s.slots > most ? most : s.slots;
@@ -742,7 +754,7 @@ cudaError_t launch_select(const SelectParams &p, const SelectPlan &plan, cudaStr
     once.set(dev);
   }
   cudaLaunchConfig_t cfg =
-      pdl_config(dim3((unsigned)(plan.cluster * p.Hkv), (unsigned)p.B), dim3(32 * kWarps<MANY>), smem, stream);
+      pdl_config(dim3((unsigned)(plan.cluster * p.Hkv), (unsigned)p.B, (unsigned)plan.shares), dim3(32 * kWarps<MANY>), smem, stream);
   cudaLaunchAttribute attr[2];
   attach_pdl(cfg, attr);
   attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
