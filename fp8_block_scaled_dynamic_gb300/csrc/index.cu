@@ -14,7 +14,8 @@
 //   table, keys, one after another.
 // - attn_select is a chain of dependent steps: offsets, q, page numbers, codes,
 //   scores, two barriers and the choice's rounds: 11 us for one node of 64 / 8 heads
-//   over 2048 pages and for 8 trees of 8 nodes over 128 to 256.  A batch of 64 x 1024
+//   over 2048 pages and for 8 trees of 8 nodes over 128 to 256, 22 and 41 for 8 trees of
+//   16 and 32 nodes (passes of eight).  A batch of 64 x 1024
 //   pages reads 130 MB in 34 us, 3.9 TB/s: its blocks score, then choose, with nothing
 //   to load meanwhile, and only others on the SM cover that.
 #include <cuda_bf16.h>
@@ -721,10 +722,12 @@ SelectPlan plan_select(const SelectParams &p, int sm_count) {
   while (s.cluster < kSelectMostCluster && (long long)p.B * p.Hkv * s.cluster < 2LL * sm_count &&
          s.cluster * 16 * (s.groups > 1 ? kWarps<true> : kWarps<false>) < p.table_cols)
     s.cluster *= 2, ++s.shift;
-  // A sequence's passes beside one another, as far as there are SMs; without room for
-  // two the most columns in a pass instead (those that a sequence does not fill cost
-  // nothing, another pass 4 us).
-  const long long room = 2LL * sm_count / ((long long)p.B * p.Hkv * s.cluster);
+  // A sequence's passes beside one another, as far as there are SMs (to four times as
+  // many blocks, of which those past a sequence's nodes end at once: 8 trees of 1 to 64
+  // nodes 31.5 us, with twice as many 40.6, one after another 63); without room for two
+  // the most columns in a pass instead (those that a sequence does not fill cost nothing,
+  // another pass 4 us).
+  const long long room = 4LL * sm_count / ((long long)p.B * p.Hkv * s.cluster);
   const int nodes = p.N < kAttnMaxNodes ? p.N : kAttnMaxNodes, pass = s.groups * 8 / s.gp, passes = (nodes + pass - 1) / pass;
   s.shares = room < 2 ? 1 : room < passes ? (int)room : passes;
   if (s.shares == 1 && s.groups > 1) {

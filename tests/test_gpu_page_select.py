@@ -255,3 +255,13 @@ def test_select_strides_stream_and_repeats():
     out = c.run(21, last=2, stream=s)
     s.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(64, 8, 128), (10, 2, 64), (3, 1, 128), (24, 8, 64), (128, 1, 128), (4, 4, 64), (40, 4, 128)])
+def test_select_of_wide_trees(Hq, Hkv, D):
+    """Trees of up to 64 nodes beside single ones: several passes, one after another or beside one another, rows that need
+    no choice among them."""
+    ctx, nodes = [3339, 0, 760, 5134, 46, 12001, 330, 815], [64, 33, 1, 20, 30, 2, 1, 41]
+    for times in (1, 4):
+        c = Select(ctx * times, nodes * times, Hq, Hkv, D, 32, seed=Hq + times)
+        c.check(c.run(11, first=2, last=3), 11, f"{times}", 2, 3)
