@@ -158,3 +158,27 @@ def test_example():
     assert got.shape == want.shape
     off = float((got.double() - want.double()).norm() / want.double().norm())
     assert off < 2.0 ** -6, off
+
+
+def test_offsets_past_32_bits():
+    """The same keys in a cache of 5 GB, past 2^31 elements from its beginning: the same bits."""
+    page, hkv, d, far = 64, 8, 128, 40000
+    g = torch.Generator(device="cuda").manual_seed(50)
+    small = torch.randn(12, page, hkv, d, generator=g, device="cuda").bfloat16()
+    big = torch.empty(far + 12, page, hkv, d, dtype=torch.bfloat16, device="cuda")
+    big[far:] = small
+    q = torch.randn(3, 16, d, generator=g, device="cuda").bfloat16()
+    k, v = (torch.randn(3, hkv, d, generator=g, device="cuda").bfloat16() for _ in range(2))
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    cu, ctx, mask = ints([0, 1, 3]), ints([350, 300]), torch.tensor([1, 1, 3], device="cuda")
+    outs = []
+    for pages, base in ((small, 0), (big, far)):
+        tab = ints([[0, 1, 2, 3, 4, 5], [0, 1, 8, 9, 10, 11]]) + base
+        cache = mx.KVCache(pages, pages)
+        index = mx.kv_index(cache, mx.PageIndex.of(cache), tab, None, ctx)
+        sel = mx.attn_select(q, cu, index, tab, ctx, 4)
+        outs.append([index.codes[base:], index.exps[base:], sel,
+                     mx.attn_sparse(q, k, v, cu, mask, cache, tab, ctx, sel),
+                     mx.attn_shared(q, k, v, cu, mask, cache, tab, ctx, ints([0, 2]), ints([128]))])
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
