@@ -13,6 +13,8 @@ CASES = [
     (shared, ([2], [512], [300, 0, 500], [1, 1, 1], 16, 2, 128, 64)),
     (shared, ([2], [512], [300, 0, 500], [4, 8, 1], 16, 2, 64, 64)),
     (shared, ([3], [512], [300, 0, 500], [64, 40, 64], 16, 2, 128, 64)),
+    (shared, ([48], [512], [7 * i % 300 for i in range(48)], [1] * 48, 8, 4, 64, 64)),  # (two launches beside one another)
+    (shared, ([48], [512], [7 * i % 300 for i in range(48)], [3] * 48, 32, 4, 128, 64)),
     (sparse, ([3000, 0, 500], [1, 1, 1], 16, 2, 128, 64, 6)),
     (sparse, ([3000, 0, 500], [4, 8, 1], 16, 2, 64, 64, 6)),
     (sparse, ([3000, 0, 500], [64, 40, 64], 16, 2, 128, 64, 6)),
