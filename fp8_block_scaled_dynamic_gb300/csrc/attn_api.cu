@@ -314,14 +314,15 @@ mxg_status attn_shared(const mxg_heads *q, const mxg_heads *k, const mxg_heads *
   mxg_status st = check_attn(q, k, v, cu_nodes, B, N, Hq, Hkv, D, scale, out, opts);
   if (st != MXG_OK) return st;
   if (n_groups < 0 || n_groups > B || (n_groups > 0 && (!cu_groups || !prefix_len))) return MXG_ERR_INVALID_ARG;
-  if (N / (256 / (Hq / Hkv)) >= (1 << 22)) return MXG_ERR_UNSUPPORTED_SHAPE;  // (a group's row groups)
+  const int span = 2 * (128 / (Hq / Hkv));  // nodes of a row group
+  if (N / span >= (1 << 22)) return MXG_ERR_UNSUPPORTED_SHAPE;  // (a group's row groups)
   if ((st = check_paged(N, mask, cache, block_table, ld_table, table_cols, ctx_len, Hkv)) != MXG_OK) return st;
   if (!aligned(cu_groups, 4) || !aligned(prefix_len, 4)) return MXG_ERR_MISALIGNED;
   int sm = 0;
   if ((st = device_sms(&sm)) != MXG_OK) return st;
   if ((st = check_ws(opts, mxg::attn_shared_ws_bytes(N, Hq, D, sm))) != MXG_OK) return st;
   // (prefixes' full row groups besides the sequences')
-  const long long starts = 2LL * (N < B ? N : B) + N / (256 / (Hq / Hkv));
+  const long long starts = 2LL * (N < B ? N : B) + N / span;
   if ((st = check_units(N, Hq, Hkv, starts, table_cols, cache->page_size)) != MXG_OK) return st;
   if (N == 0) return MXG_OK;
   mxg::SharedParams p = {};

@@ -342,7 +342,12 @@ int few_rows(const AttnParams &p, int sm_count) {
   const long long rows = ((long long)p.T + p.B - 1) / p.B * (p.Hq / p.Hkv);
   return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 && MODE == kSparse ? 64 : 0;
 }
-int span_of(const AttnParams &p, int rows) { return (rows ? rows : 2 * kRowsT) / (p.Hq / p.Hkv); }
+// Nodes of a row group, as the kernels cut them: those of few rows' tile, or two row tiles
+// of whole nodes (12 heads a kv head: 2 * 10 nodes, not 256 / 12 = 21).
+int span_of(const AttnParams &p, int rows) {
+  const int G = p.Hq / p.Hkv;
+  return rows ? rows / G : 2 * (kRowsT / G);
+}
 
 template <int D, int MODE>
 cudaError_t launch_rows(const AttnParams &p, int sm_count, cudaStream_t stream) {
