@@ -757,22 +757,21 @@ __device__ __forceinline__ uint32_t finite2(uint32_t w) {
   return w;
 }
 
-// Half a row of a part, channels ch ..., key by key from what the row sees: its
-// accumulator held a NaN or an infinity, which may be another row's.
+// A row of a part, key by key from what the row sees: its accumulator held a NaN
+// or an infinity, which may be another row's.
 template <int D>
 __device__ __noinline__ void sum_again(const AttnParams &p, long long list, int t0, int t1, int nct, int ctx, int a0,
-                                       int tok, int hk, int head, int ch, unsigned long long word, float c, float m,
-                                       float *y) {
+                                       int tok, int hk, int head, unsigned long long word, float c, float m, float *y) {
   auto value = [](uint32_t x) { return __uint_as_float(x << 16); };
   const uint16_t *q = p.q.ptr + (long long)(a0 + tok) * p.q.tok + head * p.q.head;
   const float ref = m == -INFINITY ? 0.0f : -m * c;
   const int shift = 31 - __clz(p.cache.page_size);
-  for (int e = 0; e < D / 2; ++e) y[e] = 0.0f;
+  for (int e = 0; e < D; ++e) y[e] = 0.0f;
   auto take = [&](const uint16_t *k, const uint16_t *v) {
     float s = 0.0f;
     for (int d = 0; d < D; ++d) s = fmaf(value(q[d]), value(k[d]), s);
     const float w = __uint_as_float(pack_bf16x2(0.0f, ex2(fmaf(s, c, ref))) & 0xFFFF0000u);
-    for (int e = 0; e < D / 2; ++e) y[e] = fmaf(w, value(v[ch + e]), y[e]);
+    for (int e = 0; e < D; ++e) y[e] = fmaf(w, value(v[e]), y[e]);
   };
   for (int t = t0 * kKeys; t < min(ctx, t1 * kKeys); ++t) {
     const int page = p.plan.list[list + (t >> shift)];
@@ -1486,6 +1485,27 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 32 / kRowsStore; ++i) to[i] = __shfl_sync(0xFFFFFFFFu, row0, i * kRowsStore + sub);
         if (!warp_rows) warp_arrive(&sm.o_free[st], lane);
+        // A weight of zero times a NaN or an infinity of a page that other rows see: such a
+        // row is summed again, from what it sees, before any of it is stored (its q may be
+        // where the result goes).
+        bool again = false;
+        float y[MODE == kSparse ? D : 1];
+        if (lists && warp_rows) {
+          bool fine = true;
+#pragma unroll 1
+          for (int x = 0; x < D / 32; ++x) {
+            uint32_t o[32];
+            tmem_ld32(o_t + x * 32, o);
+            tmem_ld_wait();
+            tmem_landed(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) fine &= (o[e] & 0x7F800000u) != 0x7F800000u;
+          }
+          again = valid_row && !fine;
+          if (again)
+            sum_again<D>(p, list_of(it), it.t0, last, it.nct, it.ctx, it.a0, tok, it.hk, it.hk * G + rg, word, c, m, y);
+          __syncwarp();
+        }
 #pragma unroll 1
         for (int h = warp_rows ? 0 : 2; h < 2; ++h) {
           uint32_t o[D / 64][32];
@@ -1498,25 +1518,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();
             warp_arrive(&sm.o_free[st], lane);  // (the next item's products may begin)
           }
-          bool again = false;
-          if (lists) {
-            // A weight of zero times a NaN or an infinity of a page that other
-            // rows see: such a row is summed again, from what it sees.
-            bool fine = true;
+          if (again) {
 #pragma unroll
             for (int x = 0; x < D / 64; ++x)
 #pragma unroll
-              for (int e = 0; e < 32; ++e) fine &= (o[x][e] & 0x7F800000u) != 0x7F800000u;
-            again = valid_row && !fine;
-            if (again) {
-              float y[D / 2];
-              sum_again<D>(p, list_of(it), it.t0, last, it.nct, it.ctx, it.a0, tok, it.hk, it.hk * G + rg, h * (D / 2), word,
-                           c, m, y);
-#pragma unroll
-              for (int x = 0; x < D / 64; ++x)
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[x][e] = __float_as_uint(y[x * 32 + e]);
-            }
+              for (int e = 0; e < 32; ++e) o[x][e] = __float_as_uint(y[h * (D / 2) + x * 32 + e]);
           }
           if (anyp) {
             // what the guard has taken out of v rows, added by those who see them
