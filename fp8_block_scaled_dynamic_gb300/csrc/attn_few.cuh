@@ -110,65 +110,6 @@ __device__ __forceinline__ void tmem_ld_rows(uint32_t at, uint32_t (&r)[kFewRows
   for (int i = 0; i < kFewRows; ++i) asm volatile("" : "+r"(r[i]));
 }
 
-// The lanes' values of 16 rows joined by op over a warp: lane i gets row few_row(i).
-__device__ __forceinline__ int few_row(int lane) {
-  return (lane >> 4 & 1) * 8 + (lane >> 3 & 1) * 4 + (lane >> 2 & 1) * 2 + (lane >> 1 & 1);
-}
-template <class Op>
-__device__ __forceinline__ float over_lanes(float (&v)[kFewRows], int lane, Op op) {
-#pragma unroll
-  for (int half = 8, bit = 16; half > 0; half >>= 1, bit >>= 1)
-#pragma unroll
-    for (int i = 0; i < half; ++i) {
-      const float keep = lane & bit ? v[i + half] : v[i], send = lane & bit ? v[i] : v[i + half];
-      v[i] = op(keep, __shfl_xor_sync(0xFFFFFFFFu, send, bit));
-    }
-  return op(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], 1));
-}
-
-// A row of a part summed again by a warp, key by key, to tmp.
-template <int D, int MODE>
-__device__ __noinline__ void few_again(const AttnParams &p, const Item<MODE> &it, int row, float ref, float *tmp) {
-  constexpr int V = D / 32;  // channels a lane, one after another
-  constexpr unsigned kFull = 0xFFFFFFFFu;
-  const int lane = threadIdx.x & 31, G = p.Hq / p.Hkv, node = row / G, shift = 31 - __clz(p.cache.page_size);
-  const int tok = it.r0 + node, head = it.hk * G + row - node * G;
-  const float c = p.scale * kLog2e;
-  auto value = [](uint32_t x) { return __uint_as_float(x << 16); };
-  float q[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    q[i] = value(p.q.ptr[(long long)(it.a0 + tok) * p.q.tok + head * p.q.head + lane * V + i]);
-    tmp[lane * V + i] = 0.0f;
-  }
-  auto take = [&](const uint16_t *k, const uint16_t *v) {
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) s = fmaf(q[i], value(k[lane * V + i]), s);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
-    const float w = __uint_as_float(pack_bf16x2(0.0f, ex2(fmaf(s, c, ref))) & 0xFFFF0000u);
-#pragma unroll
-    for (int i = 0; i < V; ++i) tmp[lane * V + i] = fmaf(w, value(v[lane * V + i]), tmp[lane * V + i]);
-  };
-  const long long list = list_of(it);
-  const int *pages = MODE == kSparse ? p.plan.list : p.table;
-  for (int t = it.t0 * kKeys; t < min(it.ctx, it.t1 * kKeys); ++t) {
-    const int page = pages[list + (t >> shift)];
-    if ((uint32_t)page >= (uint32_t)p.cache.pages) continue;  // (values of zero)
-    if (MODE == kSparse && (flags_of(it) & kLists) && !(p.plan.names[list + (t >> shift)] >> tok & 1ull)) continue;
-    const long long at = page * p.cache.page + (t & (p.cache.page_size - 1)) * p.cache.slot + it.hk * p.cache.head;
-    take(p.cache.k + at, p.cache.v + at);
-  }
-  if (it.t1 > it.nct) {
-    unsigned long long word = p.mask[it.a0 + tok] & (it.n >= 64 ? ~0ull : (1ull << it.n) - 1ull);
-    for (; word; word &= word - 1) {
-      const long long i = it.a0 + __ffsll(word) - 1;
-      take(p.k.ptr + i * p.k.tok + it.hk * p.k.head, p.v.ptr + i * p.v.tok + it.hk * p.v.head);
-    }
-  }
-}
-
 template <int D, int NR, int MODE>
 __global__ void __launch_bounds__(FewCfg<D, NR>::kThreads, 1)
     attn_few_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -600,7 +541,7 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::kThreads, 1)
 #pragma unroll
           for (int r = 0; r < R; ++r) x[r] = __uint_as_float(s[r]);
           const float top = over_lanes(x, lane, [](float a, float b) { return fmaxf(a, b); });
-          if (!(lane & 1)) sm.part[grp][wi][few_row(lane)] = top;
+          if (!(lane & 1)) sm.part[grp][wi][lane >> 1] = top;
           sync_four(grp);
           if (key < R) {
             const float(&m4)[4][R] = sm.part[grp];
@@ -660,7 +601,7 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::kThreads, 1)
       there = ok && next_item(k + 1);
       if (there) ahead = words_of(it);
       const float sum = over_lanes(l, lane, [](float a, float b) { return a + b; });
-      if (!(lane & 1)) sm.part[grp][wi][few_row(lane)] = sum;
+      if (!(lane & 1)) sm.part[grp][wi][lane >> 1] = sum;
       saw = __reduce_or_sync(kFull, saw);
       if (lane == 0) sm.seen[grp][wi] = saw;
       const uint32_t lastt = tile + nt - 1;
@@ -684,10 +625,22 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::kThreads, 1)
       const float(&p4)[4][R] = sm.part[grp];
       bad = sm.bad[grp];
       if (bad) {  // what another row's NaN has spoilt is summed again
+        // (64 rows: a thread has 96 registers, and with more rows or keys at a time what the
+        // call saves of them costs every tile: 8 trees of 8 nodes 37 to 44 us, so 36)
+        constexpr int kAtOnce = NR == 64 ? 1 : 4, kLanes = 32 / kAtOnce;
 #pragma unroll 1
-        for (int r = wi; r < rows; r += 4)
-          if (bad >> r & 1u)
-            few_again<D, MODE>(p, cur, first + r, ref[r] == -INFINITY ? 0.0f : -ref[r] * c, turn + r * 128);
+        for (int r0 = wi; r0 < rows; r0 += 4 * kAtOnce) {
+          const int r = r0 + 4 * (lane / kLanes);
+          const bool is = r < rows && (bad >> r & 1u);
+          const float m = ref[min(r, R - 1)];
+          if (__any_sync(kFull, is))
+            sum_again<D, MODE, kAtOnce, NR == 64 ? 1 : 2>(p, cur, cur.r0, is ? first + r : -1, m == -INFINITY ? 0.0f : -m * c,
+                                                          turn + r0 * 128, 4 * 128);
+        }
+        // (read again, so that the call does not have to save them)
+        it = sm.items[(k + 1) & 1];
+        ahead = {};
+        if (there) ahead = words_of(it);
       }
       // Rows in memory, a warp a row: results, or parts in the CTA's slot or the rows' own
       // places.

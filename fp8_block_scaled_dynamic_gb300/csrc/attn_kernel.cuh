@@ -757,34 +757,160 @@ __device__ __forceinline__ uint32_t finite2(uint32_t w) {
   return w;
 }
 
-// A row of a part, key by key from what the row sees: its accumulator held a NaN
-// or an infinity, which may be another row's.
-template <int D>
-__device__ __noinline__ void sum_again(const AttnParams &p, long long list, int t0, int t1, int nct, int ctx, int a0,
-                                       int tok, int hk, int head, unsigned long long word, float c, float m, float *y) {
-  auto value = [](uint32_t x) { return __uint_as_float(x << 16); };
-  const uint16_t *q = p.q.ptr + (long long)(a0 + tok) * p.q.tok + head * p.q.head;
-  const float ref = m == -INFINITY ? 0.0f : -m * c;
-  const int shift = 31 - __clz(p.cache.page_size);
-  for (int e = 0; e < D; ++e) y[e] = 0.0f;
-  auto take = [&](const uint16_t *k, const uint16_t *v) {
-    float s = 0.0f;
-    for (int d = 0; d < D; ++d) s = fmaf(value(q[d]), value(k[d]), s);
-    const float w = __uint_as_float(pack_bf16x2(0.0f, ex2(fmaf(s, c, ref))) & 0xFFFF0000u);
-    for (int e = 0; e < D; ++e) y[e] = fmaf(w, value(v[e]), y[e]);
-  };
-  for (int t = t0 * kKeys; t < min(ctx, t1 * kKeys); ++t) {
-    const int page = p.plan.list[list + (t >> shift)];
-    // (a page outside the cache has values of zero)
-    if (!(p.plan.names[list + (t >> shift)] >> tok & 1ull) || (uint32_t)page >= (uint32_t)p.cache.pages) continue;
-    const long long at = page * p.cache.page + (t & (p.cache.page_size - 1)) * p.cache.slot + hk * p.cache.head;
-    take(p.cache.k + at, p.cache.v + at);
-  }
-  if (t1 > nct)
-    for (; word; word &= word - 1) {
-      const long long i = a0 + __ffsll(word) - 1;
-      take(p.k.ptr + i * p.k.tok + hk * p.k.head, p.v.ptr + i * p.v.tok + hk * p.v.head);
+// A row written by a warp, a lane V channels: the result (0 of a row that sees nothing), a part's sums.
+template <int V>
+__device__ __forceinline__ void store_row(uint16_t *out, const float (&o)[V], float inv, bool any, int lane) {
+#pragma unroll
+  for (int e = 0; e < V; e += 2)
+    reinterpret_cast<uint32_t *>(out + lane * V)[e / 2] = any ? pack_bf16x2(o[e] * inv, o[e + 1] * inv) : 0u;
+}
+template <int V>
+__device__ __forceinline__ void store_part(float *part, const float (&o)[V], int lane) {
+#pragma unroll
+  for (int e = 0; e < V; e += 2)
+    reinterpret_cast<float2 *>(part + lane * V)[e / 2] = make_float2(o[e], o[e + 1]);
+}
+
+// The lanes' values v[N] joined by op over a warp: lane i gets number i / (32 / N) of them.
+template <int N, class Op>
+__device__ __forceinline__ float over_lanes(float (&v)[N], int lane, Op op) {
+  int bit = 16;
+#pragma unroll
+  for (int half = N / 2; half > 0; half >>= 1, bit >>= 1)
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float keep = lane & bit ? v[i + half] : v[i], send = lane & bit ? v[i] : v[i + half];
+      v[i] = op(keep, __shfl_xor_sync(0xFFFFFFFFu, send, bit));
     }
+#pragma unroll
+  for (int rest = 16 / N; rest > 0; rest >>= 1) v[0] = op(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], rest));
+  return v[0];
+}
+
+// R rows of a part summed again by a warp, each from what it sees: their accumulators
+// held a NaN or an infinity, which may be another row's (a weight of zero times an
+// infinity is a NaN).  Lanes 32 / R * i ... give row i: its number in the row tile whose
+// first node is tok0 (-1: none) and `ref`, minus its reference in units of the exponent;
+// its sums go to to[i * stride ...].
+// U keys at a time, of the pages that one of the rows sees, of which a warp finds 32 at
+// once: their products with the rows' q are added up so that a lane has one row's and
+// key's.  Latency bounds it.  Other warps wait meanwhile, and may for a second: four rows
+// and keys at once take a warp with 32 rows 1.5 to 2 us a key (D = 128; 131072 keys, the
+// most that 512 pages hold, 0.25 s), one row and key at once 0.5 us a key and row.  (A
+// row's thread by itself took 16 us a key.)
+template <int D, int MODE, int R, int U>
+__device__ __noinline__ void sum_again(const AttnParams &p, const Item<MODE> &it, int tok0, int row, float ref, float *to,
+                                       int stride) {
+  constexpr int V = D / 32, L = 32 / R;  // channels of a lane, lanes of a row
+  constexpr unsigned kFull = 0xFFFFFFFFu;
+  const int lane = threadIdx.x & 31, shift = 31 - __clz(p.cache.page_size), G = p.Hq / p.Hkv;
+  const float c = p.scale * kLog2e;
+  struct Row {  // this lane's channels, as they are in memory
+    uint32_t w[V / 2];
+    __device__ __forceinline__ float operator[](int i) const {
+      return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+    }
+  };
+  auto load = [&](const uint16_t *x) {
+    Row r;
+    if constexpr (V == 4) {
+      const uint2 z = *reinterpret_cast<const uint2 *>(x + lane * V);
+      r.w[0] = z.x, r.w[1] = z.y;
+    } else {
+      r.w[0] = *reinterpret_cast<const uint32_t *>(x + lane * V);
+    }
+    return r;
+  };
+  const bool is = row >= 0;
+  const int nd = div_small(max(row, 0), G), tok = tok0 + nd;  // this lane's row's node in the sequence
+  const int my_key = lane % L / (L / U);
+  Row q[R];
+  float o[R][V] = {};
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int t = __shfl_sync(kFull, tok, L * i), h = __shfl_sync(kFull, max(row, 0) - nd * G, L * i);
+    q[i] = load(p.q.ptr + (long long)(it.a0 + t) * p.q.tok + (it.hk * G + h) * p.q.head);
+  }
+  // U keys, at k_of(u) and v_of(u); see: this lane's row sees this lane's key
+  auto take = [&](bool see, auto k_of, auto v_of) {
+    Row k[U], v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      k[u] = load(k_of(u));
+      v[u] = load(v_of(u));
+    }
+    float s[R * U];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float &x = s[U * i + u];
+        x = 0.0f;
+#pragma unroll
+        for (int d = 0; d < V; ++d) x = fmaf(q[i][d], k[u][d], x);
+      }
+    const float sum = over_lanes(s, lane, [](float a, float b) { return a + b; });
+    const uint32_t w = pack_bf16x2(0.0f, ex2(fmaf(sum, c, ref))) & 0xFFFF0000u;
+    const unsigned who = __ballot_sync(kFull, see && is);
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int from = L * i + L / U * u;
+        const float wu = __uint_as_float(__shfl_sync(kFull, w, from));
+        if (!(who >> from & 1u)) continue;  // (not even a zero times v)
+#pragma unroll
+        for (int d = 0; d < V; ++d) o[i][d] = fmaf(wu, v[u][d], o[i][d]);
+      }
+  };
+  // bits of the rows' nodes, or of their words
+  auto of_all = [&](unsigned long long x) {
+#pragma unroll
+    for (int i = L; i < 32; i <<= 1) x |= __shfl_xor_sync(kFull, x, i);
+    return x;
+  };
+  const unsigned long long toks = of_all(is ? 1ull << (tok & 63) : 0ull);
+  const long long list = list_of(it);
+  const int *pages = (MODE == kSparse ? p.plan.list : p.table) + list;
+  const bool lists = MODE == kSparse && (flags_of(it) & kLists);
+  const int begin = it.t0 * kKeys, end = min(it.ctx, it.t1 * kKeys), pe = (end + p.cache.page_size - 1) >> shift;
+  for (int p0 = begin >> shift; p0 < pe; p0 += 32) {
+    const int mine = p0 + lane;
+    unsigned long long names = 0;
+    if (mine < pe) names = lists ? p.plan.names[list + mine] : ~0ull;
+    const int id = (names & toks) ? pages[mine] : -1;
+    // (a page outside the cache is values of zero)
+    for (unsigned who = __ballot_sync(kFull, (uint32_t)id < (uint32_t)p.cache.pages); who; who &= who - 1) {
+      const int x = __ffs(who) - 1, page = __shfl_sync(kFull, id, x), first = (p0 + x) << shift;
+      const bool sees = __shfl_sync(kFull, names, x) >> (tok & 63) & 1ull;
+      const long long at = page * p.cache.page + it.hk * p.cache.head;
+      const uint16_t *const k0 = p.cache.k + at, *const v0 = p.cache.v + at;
+      const int n = min(end - first, p.cache.page_size);
+      for (int t = max(begin - first, 0); t < n; t += U)  // (past the last one: that one, which does not count)
+        take(sees && t + my_key < n, [&](int u) { return k0 + min(t + u, n - 1) * p.cache.slot; },
+             [&](int u) { return v0 + min(t + u, n - 1) * p.cache.slot; });
+    }
+  }
+  if (it.t1 > it.nct) {
+    unsigned long long word = 0;
+    if (is) word = p.mask[it.a0 + tok] & (it.n >= 64 ? ~0ull : (1ull << it.n) - 1ull);
+    for (unsigned long long rest = of_all(word); rest;) {
+      int node[U];
+      unsigned long long mine = 0;  // this lane's key's bit
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        node[u] = max(__ffsll((long long)rest) - 1, 0);  // (none left: the first one, which does not count)
+        if (u == my_key) mine = rest & (0ull - rest);
+        rest &= rest - 1ull;
+      }
+      take((word & mine) != 0ull, [&](int u) { return p.k.ptr + (long long)(it.a0 + node[u]) * p.k.tok + it.hk * p.k.head; },
+           [&](int u) { return p.v.ptr + (long long)(it.a0 + node[u]) * p.v.tok + it.hk * p.v.head; });
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+    if (__shfl_sync(kFull, row, L * i) >= 0) store_part(to + i * stride, o[i], lane);
+  __syncwarp();
 }
 
 template <int D, int MODE>
@@ -1480,16 +1606,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float inv = any ? 1.0f / l : 0.0f;
         uint16_t *out = p.out.ptr + (long long)(it.a0 + tok) * p.out.tok + (it.hk * G + rg) * p.out.head;
-        const unsigned long long row0 = valid_row ? reinterpret_cast<unsigned long long>(out) : 0ull;
-        unsigned long long to[32 / kRowsStore];  // the rows that this lane stores a unit of
-#pragma unroll
-        for (int i = 0; i < 32 / kRowsStore; ++i) to[i] = __shfl_sync(0xFFFFFFFFu, row0, i * kRowsStore + sub);
-        if (!warp_rows) warp_arrive(&sm.o_free[st], lane);
-        // A weight of zero times a NaN or an infinity of a page that other rows see: such a
-        // row is summed again, from what it sees, before any of it is stored (its q may be
-        // where the result goes).
-        bool again = false;
-        float y[MODE == kSparse ? D : 1];
+        // A weight of zero times a NaN or an infinity of a page that other rows see: such
+        // rows are summed again, from what they see, and written before the others (a row's q
+        // may be where its result goes).
+        unsigned redone = 0;
         if (lists && warp_rows) {
           bool fine = true;
 #pragma unroll 1
@@ -1501,11 +1621,40 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e) fine &= (o[e] & 0x7F800000u) != 0x7F800000u;
           }
-          again = valid_row && !fine;
-          if (again)
-            sum_again<D>(p, list_of(it), it.t0, last, it.nct, it.ctx, it.a0, tok, it.hk, it.hk * G + rg, word, c, m, y);
-          __syncwarp();
+          redone = __ballot_sync(0xFFFFFFFFu, valid_row && !fine);
+          float *const sums = reinterpret_cast<float *>(smem_raw + (stage - base));
+#pragma unroll 1
+          for (unsigned rest = redone; rest;) {
+            int r[4], mine = -1;  // lanes of four rows, of this lane's
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              r[i] = __ffs(rest) - 1;
+              rest &= rest - 1;
+              if (lane >> 3 == i) mine = r[i];
+            }
+            const float neg = __shfl_sync(0xFFFFFFFFu, m == -INFINITY ? 0.0f : -m * c, max(mine, 0));
+            sum_again<D, MODE, 4, 4>(p, sm.items[k & 1], it.r0 + st * TQ, mine < 0 ? -1 : (warp & 3) * 32 + mine, neg, sums, D);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (r[i] < 0) break;
+              auto of = [&](auto x) { return __shfl_sync(0xFFFFFFFFu, x, r[i]); };
+              float y[D / 32];
+#pragma unroll
+              for (int e = 0; e < D / 32; ++e) y[e] = sums[i * D + lane * (D / 32) + e];
+              const unsigned long long at = of(reinterpret_cast<unsigned long long>(part ? (void *)part : (void *)out));
+              const float by = of(inv);
+              if (part) store_part(reinterpret_cast<float *>(at), y, lane);
+              else store_row(reinterpret_cast<uint16_t *>(at), y, by, of((int)any), lane);
+            }
+            __syncwarp();
+          }
         }
+        const bool again = redone >> lane & 1u;
+        const unsigned long long row0 = valid_row && !again ? reinterpret_cast<unsigned long long>(out) : 0ull;
+        unsigned long long to[32 / kRowsStore];  // the rows that this lane stores a unit of
+#pragma unroll
+        for (int i = 0; i < 32 / kRowsStore; ++i) to[i] = __shfl_sync(0xFFFFFFFFu, row0, i * kRowsStore + sub);
+        if (!warp_rows) warp_arrive(&sm.o_free[st], lane);
 #pragma unroll 1
         for (int h = warp_rows ? 0 : 2; h < 2; ++h) {
           uint32_t o[D / 64][32];
@@ -1517,12 +1666,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (h == 1) {
             tc_fence_before();
             warp_arrive(&sm.o_free[st], lane);  // (the next item's products may begin)
-          }
-          if (again) {
-#pragma unroll
-            for (int x = 0; x < D / 64; ++x)
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[x][e] = __float_as_uint(y[h * (D / 2) + x * 32 + e]);
           }
           if (anyp) {
             // what the guard has taken out of v rows, added by those who see them
@@ -1551,7 +1694,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (part) {
             // (a part's rows are fp32, a whole line for every 32 values of a
             // thread, and often few: straight from the threads)
-            if (valid_row) {
+            if (valid_row && !again) {
 #pragma unroll
               for (int x = 0; x < D / 64; ++x)
 #pragma unroll
@@ -1698,11 +1841,7 @@ __device__ __forceinline__ Joined<V> join_parts(int parts, int lane, float c, At
 template <int V>
 __device__ __forceinline__ void store_joined(const AttnParams &p, const Joined<V> &r, bool any, int node, int head,
                                              int lane) {
-  const float inv = 1.0f / r.l;
-  uint16_t *out = p.out.ptr + (long long)node * p.out.tok + head * p.out.head + lane * V;
-#pragma unroll
-  for (int e = 0; e < V; e += 2)
-    reinterpret_cast<uint32_t *>(out)[e / 2] = any ? pack_bf16x2(r.o[e] * inv, r.o[e + 1] * inv) : 0u;
+  store_row(p.out.ptr + (long long)node * p.out.tok + head * p.out.head, r.o, 1.0f / r.l, any, lane);
 }
 
 template <int D, int MODE>

@@ -2,7 +2,8 @@
 import pytest
 import torch
 
-import long_ref
+import attn_ref
+import fp8_block_scaled_dynamic_gb300 as mx
 import test_gpu_attn_sparse as sparse
 
 pytestmark = pytest.mark.gpu
@@ -51,3 +52,34 @@ def test_values_that_some_see(D, B, nodes, Hq, Hkv):
         c.q = q.clone()
         assert torch.equal(c.run(out=c.q).view(torch.int16), want.view(torch.int16))
         c.q = q
+
+
+@pytest.mark.parametrize("nodes", [8, 9])
+def test_longest_lists(nodes):
+    """512 pages of 256, two strips a CTA, one value of the newest page: no wait runs out.  (The table's rows name the
+    same pages.)"""
+    page, n_sel, G, D = 256, 512, 8, 128
+    d = torch.device("cuda")
+    B = 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    g = torch.Generator(device=d).manual_seed(1)
+    rnd = lambda *s: torch.randn(*s, generator=g, device=d).bfloat16()  # noqa: E731
+    kc, vc, N = rnd(n_sel + 1, page, 1, D), rnd(n_sel + 1, page, 1, D), B * nodes
+    q, k, v = rnd(N, G, D), rnd(N, 1, D), rnd(N, 1, D)
+    table = torch.arange(n_sel + 1, dtype=torch.int32, device=d).expand(B, -1).contiguous()
+    ctx = torch.full((B,), (n_sel + 1) * page, dtype=torch.int32, device=d)
+    cu = torch.arange(0, N + 1, nodes, dtype=torch.int32, device=d)
+    sel = torch.arange(n_sel, dtype=torch.int32, device=d).expand(N, 1, -1).clone()
+    sel[::nodes, 0, -1] = n_sel  # each first node's
+    vc[n_sel, 3, 0, D - 1] = float("nan")
+    mask, status = torch.ones(N, dtype=torch.int64, device=d), torch.zeros(1, dtype=torch.int32, device=d)
+    out = mx.attn_sparse(q, k, v, cu, mask, mx.KVCache(kc, vc), table, ctx, sel, dev_status=status)
+    assert mx.mxg_query_status(status) == 0
+    nan = torch.zeros_like(out, dtype=torch.bool)
+    nan[::nodes, :, D - 1] = True
+    assert torch.equal(torch.isnan(out), nan)
+    for a in (0, N - nodes):  # the first sequence's rows, the last one's
+        for i in (a + 1, a + nodes - 1):
+            ks = torch.cat([kc[:n_sel].reshape(-1, D), k[a]]).double()
+            vs = torch.cat([vc[:n_sel].reshape(-1, D), v[a]]).double()
+            o, bound = attn_ref.rows(q[i].double(), ks, vs, torch.ones(G, len(ks), dtype=torch.bool, device=d), D ** -0.5)
+            attn_ref.assert_within(out[i], o, bound, f"node {i}")
