@@ -21,8 +21,8 @@
 // Rows see different keys: a key has a word of the rows that see it (mask words for
 // nodes, a page's word for lists).  A key that no row sees has its v set to zero in
 // shared memory.  A NaN or an infinity in the v of a key that some rows see makes an
-// accumulator that is not finite; such a row is summed again, key by key, from what it
-// sees.
+// accumulator that is not finite; such a row is summed again from what it sees, and so is
+// one whose values are too large for a reference so far below its maximum.
 //
 // Warps: four of softmax for each 16 rows (a thread with 64 rows had 24 KB of code a
 // tile, whose fetching took 3.4 us), then one each for MMAs, loads and items.
@@ -65,8 +65,8 @@ struct FewCfg {
   static_assert(kSlots >= 4 && kQ % 1024 == 0 && kP % 1024 == 0, "shared memory");
 };
 
-// A weight above this moves the reference (what a row adds up is at most so much
-// larger than with its maximum: values below 2^80 cannot take it past fp32's largest).
+// A weight above this moves the reference.  What a row adds up is at most so much larger
+// than with its maximum; where that makes it too large, the row is summed again.
 constexpr float kFewPast = 0x1p30f;
 
 template <int D, int NR, int MODE>
@@ -78,7 +78,7 @@ struct FewSmem {
   alignas(16) float ref[NR], neg[NR], fac[NR];
   float part[C::kGroups][4][kFewRows];  // of a group's warps: the rows' maxima or sums over their keys
   uint32_t seen[C::kGroups][4];  // of a warp's keys: the rows of its group that see one
-  uint32_t bad[C::kGroups];      // rows whose accumulator is not finite
+  uint32_t bad[C::kGroups];      // rows whose accumulator is not finite, or too large
   uint32_t tmem;
   int abort_flag;
   Item<MODE> items[2];
@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::kThreads, 1)
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         turn[r * 128 + key] = __uint_as_float(o[r]);
-        bad |= (o[r] & 0x7F800000u) == 0x7F800000u ? 1u << r : 0u;
+        bad |= too_large(o[r]) ? 1u << r : 0u;
       }
       bad = key < D ? bad & mine : 0u;
       if (bad) atomicOr(&sm.bad[grp], bad);
@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::kThreads, 1)
       const uint32_t seen = sm.seen[grp][0] | sm.seen[grp][1] | sm.seen[grp][2] | sm.seen[grp][3];
       const float(&p4)[4][R] = sm.part[grp];
       bad = sm.bad[grp];
-      if (bad) {  // what another row's NaN has spoilt is summed again
+      if (bad) {  // what another row's NaN has spoilt, or a low reference, is summed again
         // (64 rows: a thread has 96 registers, and with more rows or keys at a time what the
         // call saves of them costs every tile: 8 trees of 8 nodes 37 to 44 us, so 36)
         constexpr int kAtOnce = NR == 64 ? 1 : 4, kLanes = 32 / kAtOnce;
@@ -632,10 +632,15 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::kThreads, 1)
         for (int r0 = wi; r0 < rows; r0 += 4 * kAtOnce) {
           const int r = r0 + 4 * (lane / kLanes);
           const bool is = r < rows && (bad >> r & 1u);
-          const float m = ref[min(r, R - 1)];
-          if (__any_sync(kFull, is))
-            sum_again<D, MODE, kAtOnce, NR == 64 ? 1 : 2>(p, cur, cur.r0, is ? first + r : -1, m == -INFINITY ? 0.0f : -m * c,
-                                                          turn + r0 * 128, 4 * 128);
+          if (!__any_sync(kFull, is)) continue;
+          const float2 stat = sum_again<D, MODE, kAtOnce, NR == 64 ? 1 : 2>(p, cur, cur.r0, is ? first + r : -1,
+                                                                            turn + r0 * 128, 4 * 128);
+          if (is && lane % kLanes == 0) {
+            ref[r] = stat.x;
+            sm.part[grp][0][r] = stat.y;
+            sm.part[grp][1][r] = sm.part[grp][2][r] = sm.part[grp][3][r] = 0.0f;
+          }
+          __syncwarp();
         }
         // (read again, so that the call does not have to save them)
         it = sm.items[(k + 1) & 1];

@@ -787,11 +787,18 @@ __device__ __forceinline__ float over_lanes(float (&v)[N], int lane, Op op) {
   return v[0];
 }
 
+// A part's sums are taken for too large from here on.  Weights of up to 2^30 (few rows) or
+// 2^8 then keep them and, joined from all CTAs, their total below fp32's largest.
+constexpr uint32_t kTooLarge = 0x7A800000u;  // 2^118; NaN and infinities are above it
+__device__ __forceinline__ bool too_large(uint32_t x) { return (x & 0x7FFFFFFFu) >= kTooLarge; }
+__device__ const uint4 kNoKey[16] = {};  // of a page outside the cache
+
 // R rows of a part summed again by a warp, each from what it sees: their accumulators
 // held a NaN or an infinity, which may be another row's (a weight of zero times an
-// infinity is a NaN).  Lanes 32 / R * i ... give row i: its number in the row tile whose
-// first node is tok0 (-1: none) and `ref`, minus its reference in units of the exponent;
-// its sums go to to[i * stride ...].
+// infinity is a NaN), or were too large for their reference, which is the row's maximum
+// here.  Lanes 32 / R * i ... give row i, its number in the row tile whose first node is
+// tok0 (-1: none), and get its reference and sum of weights (as rounded); its sums go to
+// to[i * stride ...].
 // U keys at a time, of the pages that one of the rows sees, of which a warp finds 32 at
 // once: their products with the rows' q are added up so that a lane has one row's and
 // key's.  Latency bounds it.  Other warps wait meanwhile, and may for a second: four rows
@@ -799,8 +806,7 @@ __device__ __forceinline__ float over_lanes(float (&v)[N], int lane, Op op) {
 // most that 512 pages hold, 0.25 s), one row and key at once 0.5 us a key and row.  (A
 // row's thread by itself took 16 us a key.)
 template <int D, int MODE, int R, int U>
-__device__ __noinline__ void sum_again(const AttnParams &p, const Item<MODE> &it, int tok0, int row, float ref, float *to,
-                                       int stride) {
+__device__ __noinline__ float2 sum_again(const AttnParams &p, const Item<MODE> &it, int tok0, int row, float *to, int stride) {
   constexpr int V = D / 32, L = 32 / R;  // channels of a lane, lanes of a row
   constexpr unsigned kFull = 0xFFFFFFFFu;
   const int lane = threadIdx.x & 31, shift = 31 - __clz(p.cache.page_size), G = p.Hq / p.Hkv;
@@ -825,7 +831,7 @@ __device__ __noinline__ void sum_again(const AttnParams &p, const Item<MODE> &it
   const int nd = div_small(max(row, 0), G), tok = tok0 + nd;  // this lane's row's node in the sequence
   const int my_key = lane % L / (L / U);
   Row q[R];
-  float o[R][V] = {};
+  float o[R][V] = {}, m = -INFINITY, l = 0.0f;
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const int t = __shfl_sync(kFull, tok, L * i), h = __shfl_sync(kFull, max(row, 0) - nd * G, L * i);
@@ -850,8 +856,25 @@ __device__ __noinline__ void sum_again(const AttnParams &p, const Item<MODE> &it
         for (int d = 0; d < V; ++d) x = fmaf(q[i][d], k[u][d], x);
       }
     const float sum = over_lanes(s, lane, [](float a, float b) { return a + b; });
-    const uint32_t w = pack_bf16x2(0.0f, ex2(fmaf(sum, c, ref))) & 0xFFFF0000u;
     const unsigned who = __ballot_sync(kFull, see && is);
+    // the row's maximum: where it rises, the sums so far are scaled down
+    float top = see ? sum : -INFINITY;
+#pragma unroll
+    for (int x = L / U; x < L; x <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
+    const bool rises = top > m;
+    if (__any_sync(kFull, rises)) {
+      const float f = rises ? ex2((m - top) * c) : 1.0f;
+      m = fmaxf(m, top);
+      l *= f;
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const float fi = __shfl_sync(kFull, f, L * i);
+#pragma unroll
+        for (int d = 0; d < V; ++d) o[i][d] *= fi;
+      }
+    }
+    const uint32_t w = pack_bf16x2(0.0f, ex2(fmaf(sum, c, m == -INFINITY ? 0.0f : -m * c))) & 0xFFFF0000u;
+    if (see) l += __uint_as_float(w);
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
@@ -878,17 +901,18 @@ __device__ __noinline__ void sum_again(const AttnParams &p, const Item<MODE> &it
     const int mine = p0 + lane;
     unsigned long long names = 0;
     if (mine < pe) names = lists ? p.plan.names[list + mine] : ~0ull;
-    const int id = (names & toks) ? pages[mine] : -1;
-    // (a page outside the cache is values of zero)
-    for (unsigned who = __ballot_sync(kFull, (uint32_t)id < (uint32_t)p.cache.pages); who; who &= who - 1) {
+    const int id = (names & toks) ? pages[mine] : 0;
+    for (unsigned who = __ballot_sync(kFull, (names & toks) != 0ull); who; who &= who - 1) {
       const int x = __ffs(who) - 1, page = __shfl_sync(kFull, id, x), first = (p0 + x) << shift;
       const bool sees = __shfl_sync(kFull, names, x) >> (tok & 63) & 1ull;
-      const long long at = page * p.cache.page + it.hk * p.cache.head;
-      const uint16_t *const k0 = p.cache.k + at, *const v0 = p.cache.v + at;
+      const bool in = (uint32_t)page < (uint32_t)p.cache.pages;
+      const long long at = page * p.cache.page + it.hk * p.cache.head, slot = in ? p.cache.slot : 0;
+      const uint16_t *const none = reinterpret_cast<const uint16_t *>(kNoKey);
+      const uint16_t *const k0 = in ? p.cache.k + at : none, *const v0 = in ? p.cache.v + at : none;
       const int n = min(end - first, p.cache.page_size);
       for (int t = max(begin - first, 0); t < n; t += U)  // (past the last one: that one, which does not count)
-        take(sees && t + my_key < n, [&](int u) { return k0 + min(t + u, n - 1) * p.cache.slot; },
-             [&](int u) { return v0 + min(t + u, n - 1) * p.cache.slot; });
+        take(sees && t + my_key < n, [&](int u) { return k0 + min(t + u, n - 1) * slot; },
+             [&](int u) { return v0 + min(t + u, n - 1) * slot; });
     }
   }
   if (it.t1 > it.nct) {
@@ -911,6 +935,9 @@ __device__ __noinline__ void sum_again(const AttnParams &p, const Item<MODE> &it
   for (int i = 0; i < R; ++i)
     if (__shfl_sync(kFull, row, L * i) >= 0) store_part(to + i * stride, o[i], lane);
   __syncwarp();
+#pragma unroll
+  for (int x = L / U; x < L; x <<= 1) l += __shfl_xor_sync(kFull, l, x);
+  return make_float2(m, l);
 }
 
 template <int D, int MODE>
@@ -1619,7 +1646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld_wait();
             tmem_landed(o);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) fine &= (o[e] & 0x7F800000u) != 0x7F800000u;
+            for (int e = 0; e < 32; ++e) fine &= !too_large(o[e]);
           }
           redone = __ballot_sync(0xFFFFFFFFu, valid_row && !fine);
           float *const sums = reinterpret_cast<float *>(smem_raw + (stage - base));
@@ -1632,8 +1659,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               rest &= rest - 1;
               if (lane >> 3 == i) mine = r[i];
             }
-            const float neg = __shfl_sync(0xFFFFFFFFu, m == -INFINITY ? 0.0f : -m * c, max(mine, 0));
-            sum_again<D, MODE, 4, 4>(p, sm.items[k & 1], it.r0 + st * TQ, mine < 0 ? -1 : (warp & 3) * 32 + mine, neg, sums, D);
+            const float2 stat = sum_again<D, MODE, 4, 4>(p, sm.items[k & 1], it.r0 + st * TQ,
+                                                         mine < 0 ? -1 : (warp & 3) * 32 + mine, sums, D);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               if (r[i] < 0) break;
@@ -1642,9 +1669,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int e = 0; e < D / 32; ++e) y[e] = sums[i * D + lane * (D / 32) + e];
               const unsigned long long at = of(reinterpret_cast<unsigned long long>(part ? (void *)part : (void *)out));
-              const float by = of(inv);
+              const float li = __shfl_sync(0xFFFFFFFFu, stat.y, 8 * i), mi = __shfl_sync(0xFFFFFFFFu, stat.x, 8 * i);
+              if (lane == r[i]) m = mi, l = part && any && m == -INFINITY ? 1.0f : li;
               if (part) store_part(reinterpret_cast<float *>(at), y, lane);
-              else store_row(reinterpret_cast<uint16_t *>(at), y, by, of((int)any), lane);
+              else store_row(reinterpret_cast<uint16_t *>(at), y, 1.0f / li, of((int)any), lane);
             }
             __syncwarp();
           }

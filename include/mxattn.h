@@ -30,7 +30,8 @@
  * device waits bounded (mxg_attn_opts.timeout_ms); no memory allocated and no
  * pointer kept.  All tensors are bf16; norms, rotations, scores, softmax
  * statistics and accumulators are fp32, rounded to bf16 once at the end (the
- * softmax weights are rounded to bf16 before their product with v).  The bounds
+ * softmax weights are rounded to bf16 before their product with v).  A row's
+ * sums hold |v| times the number of keys that it sees below 2^119.  The bounds
  * and scores of kv_index and attn_select are whole numbers times powers of two,
  * computed without rounding: what is selected is the same on any machine.
  * These are inference operators: there are no gradients.
