@@ -1,9 +1,12 @@
 // attn_api.cu -- the C ABI declared in include/mxattn.h: argument and device
 // checks and launches.  Every host-detectable error is returned before
 // anything is launched.
+#include <algorithm>
+#include <array>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <utility>
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -124,6 +127,19 @@ mxg_status check_index(const mxg_page_index *x) {
       x->exps_layer >= (1LL << 38) || x->exps_page >= (1LL << 38))
     return MXG_ERR_MISALIGNED;
   return MXG_OK;
+}
+
+// Entries of `bytes` in three dimensions of (stride, number), apart from one another: each
+// dimension's stride spans the entries of those with smaller strides.
+bool apart(std::array<std::pair<int64_t, int>, 3> dims, int64_t bytes) {
+  std::sort(dims.begin(), dims.end());
+  __int128 span = bytes;
+  for (const auto &[stride, n] : dims) {
+    if (n < 2) continue;
+    if (stride < span) return false;
+    span += (__int128)stride * (n - 1);
+  }
+  return true;
 }
 
 mxg::PageIndex index_of(const mxg_page_index *x) {
@@ -346,10 +362,8 @@ mxg_status kv_index(const mxg_kv_cache *cache, int Hkv, int D, const mxg_page_in
   if ((st = check_cache(cache)) != MXG_OK || (st = check_index(index)) != MXG_OK) return st;
   if (index->layers < cache->layers || index->pages < cache->pages) return MXG_ERR_INVALID_ARG;
   // (entries are written: none over another)
-  const auto apart = [](int64_t stride, int n, int64_t bytes) { return n < 2 || stride >= bytes; };
-  if (!apart(index->codes_layer, index->layers, 2 * D) || !apart(index->codes_page, index->pages, 2 * D) ||
-      !apart(index->codes_head, Hkv, 2 * D) || !apart(index->exps_layer, index->layers, Hkv) ||
-      !apart(index->exps_page, index->pages, Hkv))
+  if (!apart({{{index->codes_layer, index->layers}, {index->codes_page, index->pages}, {index->codes_head, Hkv}}}, 2 * D) ||
+      !apart({{{index->exps_layer, index->layers}, {index->exps_page, index->pages}, {0, 1}}}, Hkv))
     return MXG_ERR_UNSUPPORTED_SHAPE;
   // (pages of all sequences, numbered in 32 bits)
   if ((long long)table_cols * cache->page_size > 0x7fffff00LL || (long long)table_cols * B > 0x7fffffffLL)

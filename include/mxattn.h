@@ -224,8 +224,9 @@ mxg_status attn_shared(const mxg_heads *q, const mxg_heads *k, const mxg_heads *
  * Sequences may share pages.  Other pages' entries are left as they were; v is
  * not read (cache->v must be given all the same).  index: as many layers as the
  * cache, entries for at least its pages.
- * D in {64, 128}, B <= MXG_ATTN_MAX_SEQS; entries of index apart from one another
- * (strides of layers, pages and heads of at least 2 D codes and Hkv exponents).
+ * D in {64, 128}, B <= MXG_ATTN_MAX_SEQS; entries of index (2 D codes; Hkv exponents)
+ * apart from one another: of layers, pages and heads, in any order, each stride at
+ * least as long as all entries of those with smaller strides.
  * Out of range: ctx_old and ctx_new are clamped to [0, table_cols * page_size], a
  * page outside [0, pages) is skipped. */
 mxg_status kv_index(const mxg_kv_cache *cache, int Hkv, int D, const mxg_page_index *index,
