@@ -264,8 +264,8 @@ mxg_status attn_select(const mxg_heads *q, const int *cu_nodes, int B, int N,
  * page is read once for all nodes of its sequence that name it.  Everything else
  * is as for attn_tree.
  * 1 <= n_sel <= MXG_ATTN_MAX_SELECT, table_cols <= 524288.
- * Out of range, besides attn_tree's: a logical page at or past the sequence's
- * last one names none. */
+ * Out of range, besides attn_tree's: a logical page past the sequence's last one
+ * (ceil(ctx_len / page_size) or more) names none. */
 size_t mxg_attn_sparse_workspace_bytes(int N, int Hkv, int n_sel, int D);
 mxg_status attn_sparse(const mxg_heads *q, const mxg_heads *k, const mxg_heads *v,
                        const int *cu_nodes, const uint64_t *mask, int B, int N,
