@@ -563,8 +563,9 @@ __global__ void __launch_bounds__(32 * kWarps<MANY>, MANY ? 1 : 4) select_kernel
         if (node >= nodes) return;
         const int code = second ? code_now[1] : code_now[0];
         const uint32_t kind = second ? kind_now[1] : kind_now[0], j = at + (second ? at8 : 0u);
-        // 2^(code - 127 - 20): no score overflows; (+ 0: no zero below another one)
-        float score = fmaf(sum, __uint_as_float((uint32_t)max(code - 20, 1) << 23), 0.0f);
+        // 2^(code - 127 - 20): no score overflows, and 2^-147 is still a number of fp32, as are
+        // its multiples; (+ 0: no zero below another one)
+        float score = fmaf(sum, __uint_as_float(code > 20 ? (uint32_t)(code - 20) << 23 : 4u << code), 0.0f);
         if (code == 255) score = INFINITY;
         if (kind < 2) score = 0.0f;
         const uint32_t key = kind & 1 ? order_key(score) : 0u;
