@@ -34,8 +34,8 @@
 // tile and SM take 1.5 us); the last product, the results' turn and their way out 2 us.
 // - 32 requests over 32 pages of 64 each (64 / 8 heads of 128, 269 MB): 52 us, 5.1 TB/s
 //   in this kernel, 58 with plan and join.
-// - 8 trees of 8 nodes over 16 pages a node (74 MB in all): 34.5 us; one node a request:
-//   18.2.
+// - 8 trees of 8 nodes over 16 pages a node (74 MB in all): 35.5 us; one node a request:
+//   18.6.
 // Left out: a decoded token's own key added after its last part instead of a tile of its
 // own (64 requests 98 -> 106 us: the loads and the product are in the item's chain, the
 // tile is not); results of four rows unrolled (20.3 -> 21.2 us for short requests: more

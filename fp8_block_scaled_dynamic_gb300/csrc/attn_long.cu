@@ -15,7 +15,7 @@
 // What bounds them (GB300): the chain of launches for short calls.  A plan takes 4 to 5
 // us, a join 4 to 5, a kernel's first item 5 to 8: one token behind 288 shared ones 19
 // us (attn_tree, which has no plan, 11), 8 x 8 nodes behind 1024 31.5, over selected
-// pages 34.  Long prefixes: full row tiles at 2.0 us a pair and key tile (64 requests
+// pages 35.5.  Long prefixes: full row tiles at 2.0 us a pair and key tile (64 requests
 // behind 16384 tokens, 64 / 8 heads of 128: 93 us, of which the prefix is 40, the own
 // keys 38).
 #include "attn_few.cuh"

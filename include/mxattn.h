@@ -93,9 +93,9 @@ typedef struct {
     int *dev_status;     /* optional device int; kernels OR MXG_DEV_* bits into it */
     uint32_t timeout_ms; /* limit of every device-side wait; 0 = 1000 ms.  The longest legitimate
                             one lasts as long as a CTA's keys: about 2 us for 128 of them.  Where
-                            attn_shared and attn_sparse meet a v that is not finite and that not
-                            every node sees, rows are summed again, for 2 us a key (0.25 s for the
-                            131072 keys of 512 pages of 256) */
+                            attn_shared and attn_sparse meet a v that is not finite, rows are
+                            summed again, for up to 2 us a key (0.25 s for the 131072 keys of 512
+                            pages of 256) */
     int debug_stall;     /* test hook: 1 makes the first wait of every CTA one that nothing
                             satisfies, so that the timeout path runs (no fault, no hang) */
 } mxg_attn_opts;
